@@ -19,12 +19,19 @@ missing or cannot be loaded, every call raises.
         the same with the maps around the recurrence (SiLU + L2 of q and k,
         sigmoid beta, sigmoid or softplus alpha, output RMSNorm) applied inside
         the kernels; flags are the FUSE_* constants
+    lr_qk_norm_rope / lr_fwd_window / lr_step_paged(...)
+        softmax attention with a sliding window and sinks, over whole sequences
+        and for single tokens over a paged cache, and the norm and rotation of
+        queries and keys before it (attention.py, ``include/lr_attn.h``)
 """
 from __future__ import annotations
 
 import ctypes
 import os
 
+from .attention import (ATTN_SYMBOLS, NO_WINDOW, lr_fwd_window, lr_qk_norm_rope, lr_step_paged,
+                        step_paged_workspace_size)
+from .attention import declare as _declare_attention
 from .build import LIB_PATH
 
 LINEAR, DECAY, DELTA, GATED_DELTA, DIAG_DECAY = 0, 1, 2, 3, 4
@@ -48,7 +55,8 @@ FUSE_ALPHA_SIGMOID_POW = 0x20
 STATIC_WORKSPACE_BYTES = 64 << 20   # LR_STATIC_WORKSPACE_BYTES
 STATUS = {0: "LR_OK", 1: "LR_ERR_NULL", 2: "LR_ERR_SHAPE", 3: "LR_ERR_DTYPE", 4: "LR_ERR_ALIGN",
           5: "LR_ERR_MODE", 6: "LR_ERR_UNSUPPORTED", 7: "LR_ERR_CUDA", 8: "LR_ERR_ALIAS",
-          9: "LR_ERR_TIMEOUT", 10: "LR_ERR_WORKSPACE", 11: "LR_ERR_TOO_LARGE", 12: "LR_ERR_FUSE"}
+          9: "LR_ERR_TIMEOUT", 10: "LR_ERR_WORKSPACE", 11: "LR_ERR_TOO_LARGE", 12: "LR_ERR_FUSE",
+          13: "LR_ERR_INDEX"}
 _USES_ALPHA = {LINEAR: False, DECAY: True, DELTA: False, GATED_DELTA: True, DIAG_DECAY: True}
 _USES_BETA = {LINEAR: False, DECAY: False, DELTA: True, GATED_DELTA: True, DIAG_DECAY: False}
 
@@ -123,6 +131,7 @@ def lib() -> ctypes.CDLL:
         L.lr_device_status.argtypes = []
         L.lr_debug_inject_scan_timeout.restype = i
         L.lr_debug_inject_scan_timeout.argtypes = [i]
+        _declare_attention(L)
         _lib = L
     return _lib
 

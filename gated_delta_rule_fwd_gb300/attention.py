@@ -1,0 +1,283 @@
+"""Softmax-attention operators of liblr: binding of ``include/lr_attn.h``.
+
+    lr_qk_norm_rope(q, k, positions, ...) -> (q_out, k_out)
+        RMS norm of every query and key head and the position rotation in one
+        pass, with an optional write of keys and values into a paged cache
+    lr_fwd_window(q, k, v, window=..., sinks=...) -> o
+        causal attention over whole sequences with a sliding window and sinks
+    lr_step_paged(q, k_cache, v_cache, table, lens, ...) -> o
+        the same attention for one new token per sequence over the cache
+
+Like the rest of the package this only marshals arguments; the functions are
+offered by the package itself.  Tensors may be on any device: the calls run
+there, on its current stream unless one is given.
+"""
+from __future__ import annotations
+
+import ctypes
+
+NO_WINDOW = (1 << 31) - 1   # a window that hides nothing
+QK_NORM = 0x1
+QK_INTERLEAVED = 0x2
+ATTN_SYMBOLS = ("lr_qk_norm_rope", "lr_fwd_window", "lr_step_paged", "lr_step_paged_workspace_size")
+
+
+class Strides(ctypes.Structure):
+    """lr_strides (include/lr_attn.h)."""
+    _fields_ = [("b", ctypes.c_longlong), ("h", ctypes.c_longlong), ("t", ctypes.c_longlong)]
+
+
+class Paged(ctypes.Structure):
+    """lr_paged (include/lr_attn.h)."""
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("table", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int), ("page", ctypes.c_int), ("max_pages", ctypes.c_int)]
+
+
+class QkMaps(ctypes.Structure):
+    """lr_qk_maps (include/lr_attn.h)."""
+    _fields_ = [("flags", ctypes.c_uint), ("q_weight", ctypes.c_void_p),
+                ("k_weight", ctypes.c_void_p), ("eps", ctypes.c_float), ("rot", ctypes.c_int),
+                ("inv_freq", ctypes.c_void_p)]
+
+
+def declare(L):
+    """Argument types of the attention entry points on a loaded library."""
+    vp, i, f, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
+    L.lr_qk_norm_rope.restype = i
+    L.lr_qk_norm_rope.argtypes = [vp, Strides, vp, Strides, vp, ctypes.POINTER(QkMaps), vp, vp, vp,
+                                  Strides, ctypes.POINTER(Paged)] + [i] * 6 + [vp]
+    L.lr_fwd_window.restype = i
+    L.lr_fwd_window.argtypes = ([vp, Strides] * 3 + [vp, vp, vp, Strides] + [i] * 8 + [f, i, vp])
+    L.lr_step_paged.restype = i
+    L.lr_step_paged.argtypes = ([vp, ctypes.POINTER(Paged), vp, vp] + [i] * 7 + [f, i, vp, sz, vp])
+    L.lr_step_paged_workspace_size.restype = sz
+    L.lr_step_paged_workspace_size.argtypes = [i] * 8
+
+
+def _base():
+    import gated_delta_rule_fwd_gb300 as base
+    return base
+
+
+def _strided(t, name, shape, dtype, device):
+    """Checks a [B, H, T, d] tensor with contiguous channels; its strides."""
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.stride(-1) != 1:
+        raise ValueError(f"{name} must have contiguous channels")
+    return Strides(t.stride(0), t.stride(1), t.stride(2))
+
+
+def _ints(t, name, shape, device):
+    import torch
+    if t is not None:
+        _base()._check(t, name, shape, torch.int32, device)
+
+
+def _paged(base, k_cache, v_cache, table, rows, d, dtype, dev):
+    """Checks the pools [P, Hk, page, d] and the table [rows, max_pages]."""
+    import torch
+    if k_cache.dim() != 4 or k_cache.shape[-1] != d:
+        raise ValueError(f"k_cache must have shape (pages, heads, page, {d}), got {tuple(k_cache.shape)}")
+    base._check(k_cache, "k_cache", k_cache.shape, dtype, dev)
+    base._check(v_cache, "v_cache", k_cache.shape, dtype, dev)
+    if table.dim() != 2:
+        raise ValueError(f"table must have shape ({rows}, pages of a sequence), got {tuple(table.shape)}")
+    base._check(table, "table", (rows, table.shape[1]), torch.int32, dev)
+    return Paged(k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), k_cache.shape[0],
+                 k_cache.shape[2], table.shape[1])
+
+
+def _on(stream, dev):
+    """Where a call allocates and launches: the given stream, or the device's
+    current one.  What is allocated inside belongs to that stream."""
+    import torch
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream must be on {dev}, got {stream.device}")
+    return torch.cuda.stream(stream)
+
+
+def _int32(x, name):
+    x = int(x)
+    if not -(1 << 31) <= x < (1 << 31):
+        raise ValueError(f"{name} does not fit 32 bits: {x}")
+    return x
+
+
+def lr_qk_norm_rope(q, k, positions=None, *, norm=True, q_weight=None, k_weight=None, eps=1e-6,
+                    inv_freq=None, interleaved=False, v=None, k_cache=None, v_cache=None,
+                    table=None, write_k=True, q_out=None, k_out=None, stream=None):
+    """Norm and rotation of queries and keys (``lr_qk_norm_rope`` in include/lr_attn.h).
+
+    q: [B,Hq,T,d]; k: [B,Hk,T,d] (float32 or bfloat16), any strides with
+    contiguous channels, e.g. transposed views of one projection;
+    positions: [B,T] int32 (negative: padding, left out) or None for 0..T-1;
+    q_weight, k_weight: [d] float32 or None; inv_freq: [rot/2] float64 radians
+    per position, or None for no rotation; ``interleaved`` rotates channels
+    (2i, 2i+1) instead of (i, i + rot/2).  With k_cache, v_cache
+    [pages,Hk,page,d], table [B,max_pages] int32 and v [B,Hk,T,d], the keys
+    and v are also written at their positions in the cache; then
+    ``write_k=False`` leaves out the contiguous keys.  Returns (q_out, k_out)
+    [B,H,T,d] contiguous (k_out None without ``write_k``)."""
+    import torch
+    base = _base()
+    dev = q.device
+    base._require_cuda(dev)
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q and k must have shape (B, heads, T, d)")
+    B, Hq, T, d = q.shape
+    Hk = k.shape[1]
+    dt = base._dtype_code(q)
+    qs = _strided(q, "q", (B, Hq, T, d), q.dtype, dev)
+    ks = _strided(k, "k", (B, Hk, T, d), q.dtype, dev)
+    _ints(positions, "positions", (B, T), dev)
+    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None:
+            base._check(t, n, (d,), torch.float32, dev)
+    rot = 0
+    if inv_freq is not None:
+        rot = 2 * inv_freq.numel()
+        base._check(inv_freq, "inv_freq", (rot // 2,), torch.float64, dev)
+    cache = vs = None
+    if k_cache is not None or v_cache is not None or table is not None or v is not None:
+        if k_cache is None or v_cache is None or table is None or v is None:
+            raise ValueError("a cache needs v, k_cache, v_cache and table together")
+        cache = _paged(base, k_cache, v_cache, table, B, d, q.dtype, dev)
+        if k_cache.shape[1] != Hk:
+            raise ValueError(f"k_cache must have {Hk} heads, got {k_cache.shape[1]}")
+        vs = _strided(v, "v", (B, Hk, T, d), q.dtype, dev)
+    elif not write_k:
+        raise ValueError("write_k=False needs a cache")
+    if q_out is not None:
+        base._check(q_out, "q_out", (B, Hq, T, d), q.dtype, dev)
+    if k_out is not None:
+        if not write_k:
+            raise ValueError("k_out given with write_k=False")
+        base._check(k_out, "k_out", (B, Hk, T, d), q.dtype, dev)
+    maps = QkMaps((QK_NORM if norm else 0) | (QK_INTERLEAVED if interleaved else 0),
+                  None if q_weight is None else q_weight.data_ptr(),
+                  None if k_weight is None else k_weight.data_ptr(), float(eps), rot,
+                  None if inv_freq is None else inv_freq.data_ptr())
+    with _on(stream, dev):
+        if q_out is None:
+            q_out = torch.empty((B, Hq, T, d), dtype=q.dtype, device=dev)
+        if k_out is None and write_k:
+            k_out = torch.empty((B, Hk, T, d), dtype=q.dtype, device=dev)
+        st = base.lib().lr_qk_norm_rope(
+            base._ptr(q), qs, base._ptr(k), ks, base._ptr(positions), ctypes.byref(maps),
+            base._ptr(q_out), base._ptr(k_out), base._ptr(v), vs or Strides(0, 0, 0),
+            None if cache is None else ctypes.byref(cache), B, T, Hq, Hk, d, dt,
+            base._stream_handle(stream, dev))
+    if st != 0:
+        raise base.LrError(st, "lr_qk_norm_rope")
+    return q_out, k_out
+
+
+def lr_fwd_window(q, k, v, *, window=None, sinks=0, q_len=None, k_len=None, scale=None, o=None,
+                  stream=None):
+    """Causal attention with a sliding window and sinks (``lr_fwd_window`` in
+    include/lr_attn.h).
+
+    q: [B,Hq,Tq,d]; k, v: [B,Hk,Tk,d] (float32 or bfloat16), any strides with
+    contiguous channels; Hq a multiple of Hk.  The queries are the last tokens
+    of the keys' sequence.  window: tokens a row sees, itself included (None:
+    all before it); sinks: first tokens that stay visible; q_len, k_len: [B]
+    int32 lengths of a padded batch or None; scale: default d**-0.5.  ``o``
+    may be strided too; rows behind q_len are left as they were (zeros when o
+    is made here).  Returns o: [B,Hq,Tq,d]."""
+    import torch
+    base = _base()
+    dev = q.device
+    base._require_cuda(dev)
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q, k and v must have shape (B, heads, T, d)")
+    B, Hq, Tq, d = q.shape
+    Hk, Tk = k.shape[1], k.shape[2]
+    dt = base._dtype_code(q)
+    qs = _strided(q, "q", (B, Hq, Tq, d), q.dtype, dev)
+    ks = _strided(k, "k", (B, Hk, Tk, d), q.dtype, dev)
+    vs = _strided(v, "v", (B, Hk, Tk, d), q.dtype, dev)
+    _ints(q_len, "q_len", (B,), dev)
+    _ints(k_len, "k_len", (B,), dev)
+    if o is not None:
+        _strided(o, "o", (B, Hq, Tq, d), q.dtype, dev)
+    window = NO_WINDOW if window is None else _int32(window, "window")
+    scale = d ** -0.5 if scale is None else float(scale)
+    with _on(stream, dev):
+        if o is None:
+            make = torch.empty if q_len is None else torch.zeros
+            o = make((B, Hq, Tq, d), dtype=q.dtype, device=dev)
+        st = base.lib().lr_fwd_window(
+            base._ptr(q), qs, base._ptr(k), ks, base._ptr(v), vs, base._ptr(q_len),
+            base._ptr(k_len), base._ptr(o), Strides(o.stride(0), o.stride(1), o.stride(2)), B, Hq, Hk, Tq, Tk, d, window,
+            _int32(sinks, "sinks"), scale, dt, base._stream_handle(stream, dev))
+    if st != 0:
+        raise base.LrError(st, "lr_fwd_window")
+    return o
+
+
+def step_paged_workspace_size(N, Hq, Hk, d, max_len, dtype, window=None, sinks=0) -> int:
+    """lr_step_paged_workspace_size for these sizes (dtype: torch dtype)."""
+    import torch
+    base = _base()
+    dt = base.F32 if dtype == torch.float32 else base.BF16
+    window = NO_WINDOW if window is None else _int32(window, "window")
+    return int(base.lib().lr_step_paged_workspace_size(N, Hq, Hk, d, _int32(max_len, "max_len"),
+                                                       window, _int32(sinks, "sinks"), dt))
+
+
+def lr_step_paged(q, k_cache, v_cache, table, lens, *, max_len=None, window=None, sinks=0,
+                  scale=None, o=None, workspace=None, stream=None):
+    """Attention of one new token per sequence over the paged cache
+    (``lr_step_paged`` in include/lr_attn.h).
+
+    q: [N,Hq,d]; k_cache, v_cache: [pages,Hk,page,d]; table: [N,max_pages]
+    int32; lens: [N] int32 tokens in the cache, this one included (0: a row of
+    zeros, negative: an unused slot, left as it was); max_len: bound on lens
+    (default: what the table can hold; a tight one is faster); window, sinks,
+    scale as for :func:`lr_fwd_window`.  ``workspace`` is a uint8 CUDA tensor
+    of at least ``step_paged_workspace_size(...)`` bytes, allocated here when
+    None.  Returns o: [N,Hq,d]."""
+    import torch
+    base = _base()
+    dev = q.device
+    base._require_cuda(dev)
+    if q.dim() != 3:
+        raise ValueError("q must have shape (N, heads, d)")
+    N, Hq, d = q.shape
+    dt = base._dtype_code(q)
+    base._check(q, "q", (N, Hq, d), q.dtype, dev)
+    cache = _paged(base, k_cache, v_cache, table, N, d, q.dtype, dev)
+    Hk = k_cache.shape[1]
+    if lens is None:
+        raise ValueError("lens is required")
+    _ints(lens, "lens", (N,), dev)
+    if o is not None:
+        base._check(o, "o", (N, Hq, d), q.dtype, dev)
+    holds = cache.page * cache.max_pages
+    max_len = holds if max_len is None else _int32(max_len, "max_len")
+    window = NO_WINDOW if window is None else _int32(window, "window")
+    sinks = _int32(sinks, "sinks")
+    scale = d ** -0.5 if scale is None else float(scale)
+    L = base.lib()
+    need = int(L.lr_step_paged_workspace_size(N, Hq, Hk, d, max_len, window, sinks, dt))
+    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+        raise ValueError(f"workspace must be contiguous and on {dev}")
+    with _on(stream, dev):
+        if o is None:
+            o = torch.empty((N, Hq, d), dtype=q.dtype, device=dev)
+        if workspace is None and need > 0:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        st = L.lr_step_paged(base._ptr(q), ctypes.byref(cache), base._ptr(lens), base._ptr(o), N,
+                             Hq, Hk, d, max_len, window, sinks, scale, dt, base._ptr(workspace),
+                             ws_bytes, base._stream_handle(stream, dev))
+    if st != 0:
+        raise base.LrError(st, "lr_step_paged")
+    return o

@@ -1,0 +1,85 @@
+// Declarations shared by the attention translation units of liblr (the
+// operators of include/lr_attn.h).
+#pragma once
+
+#include "lr_attn.h"
+#include "lr_internal.cuh"
+
+namespace lr {
+
+// Error word of the attention kernels: bits set by any of them, read and
+// cleared by lr_device_status.  Each translation unit has its own copy in its
+// module; attn_errors() collects them.
+constexpr unsigned kAttnIndex = 1u;    // a page or a length out of range
+constexpr unsigned kAttnTimeout = 2u;  // a bounded wait gave up
+
+// Keys that the query at position p sees: [0, s1) and [lo, hi), with
+// s1 <= lo (lo == 0 or s1 == 0 where one run covers all).
+struct SeenKeys {
+    int s1, lo, hi;
+};
+__host__ __device__ __forceinline__ SeenKeys seen_keys(int p, int klen, int window, int sinks) {
+    SeenKeys s;
+    s.hi = p + 1 < klen ? p + 1 : klen;
+    if (s.hi < 0) s.hi = 0;
+    const long long l = (long long)p - window + 1;
+    s.lo = l < 0 ? 0 : (int)l;
+    if (s.lo > s.hi) s.lo = s.hi;
+    s.s1 = sinks < s.lo ? sinks : s.lo;
+    return s;
+}
+
+// Lengths as the kernels use them; *bad when one was out of range.
+__device__ __forceinline__ int clamp_len(const int *len, int b, int most, bool *bad) {
+    if (!len) return most;
+    const int x = len[b];
+    if (x < 0 || x > most) *bad = true;
+    return x < 0 ? 0 : (x > most ? most : x);
+}
+
+struct QkMaps {
+    const float *qw, *kw;
+    const double *inv_freq;
+    float eps;
+    int rot;
+    unsigned flags;
+};
+
+// ------------------------------------------------------------------ launchers
+cudaError_t launch_qk_norm_rope(const void *q, lr_strides qs, const void *k, lr_strides ks,
+                                const int *positions, const QkMaps &maps, void *q_out, void *k_out,
+                                const void *v, lr_strides vs, const lr_paged *cache, int B, int T,
+                                int Hq, int Hk, int d, lr_dtype dt, cudaStream_t stream);
+
+struct WindowArgs {
+    const void *q, *k, *v;
+    void *o;
+    lr_strides qs, ks, vs, os;
+    const int *q_len, *k_len;
+    int B, Hq, Hk, Tq, Tk, window, sinks;
+    float scale;
+};
+// CUDA cores, fp32 (window_simt.cu).
+cudaError_t launch_window_simt(const WindowArgs &a, int d, lr_dtype dt, cudaStream_t stream);
+
+struct StepArgs {
+    const void *q, *k, *v;
+    void *o;
+    const int *table, *lens;
+    int N, Hq, Hk, max_len, window, sinks, num_pages, page_log2, max_pages;
+    float scale;
+};
+// How a step's keys are cut: chunks of `chunk` keys, at most `splits` of them.
+struct StepPlan {
+    int chunk, splits;
+};
+StepPlan step_plan(int N, int Hq, int Hk, int max_len, int window, int sinks, lr_dtype dt);
+size_t step_workspace_bytes(int N, int Hq, int d, const StepPlan &p);
+cudaError_t launch_step_paged(const StepArgs &a, int d, lr_dtype dt, void *ws, cudaStream_t stream);
+
+// Return and clear the error bits of each unit (-1: the device could not be read).
+int attn_errors_rope();
+int attn_errors_window_simt();
+int attn_errors_step();
+
+}  // namespace lr

@@ -3,6 +3,7 @@
 // launch, so an error status means nothing was enqueued.
 #include <atomic>
 
+#include "attn_internal.cuh"
 #include "lr_internal.cuh"
 
 namespace lr {
@@ -10,7 +11,7 @@ namespace lr {
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int kMaxSlots = 208;
+constexpr int kMaxSlots = 224;
 std::atomic<int> g_smem_bytes[kMaxDevices][kMaxSlots];
 
 bool supported_dim(int d) { return d == 32 || d == 64 || d == 128; }
@@ -129,6 +130,7 @@ const char *lr_status_string(lr_status s) {
     case LR_ERR_TIMEOUT: return "a kernel gave up a bounded wait; its outputs are incomplete";
     case LR_ERR_WORKSPACE: return "workspace is NULL or smaller than lr_fwd_chunked_workspace_size";
     case LR_ERR_TOO_LARGE: return "problem needs more scratch than the static workspace holds (LR_STATIC_WORKSPACE_BYTES)";
+    case LR_ERR_INDEX: return "a page or a length on the device is out of range";
     case LR_ERR_FUSE: return "invalid lr_fuse: unknown flag, both alpha maps, or a negative or non-finite norm_eps";
     }
     return "unknown status";
@@ -396,7 +398,13 @@ lr_status lr_device_status(void) {
     if (cudaDeviceSynchronize() != cudaSuccess) return LR_ERR_CUDA;
     const int e = read_and_clear_tc_error(), eg = read_and_clear_gd_tc_error();
     if (e < 0 || eg < 0) return LR_ERR_CUDA;
-    return (e || eg) ? LR_ERR_TIMEOUT : LR_OK;
+    unsigned attn = 0;
+    for (int a : {attn_errors_rope(), attn_errors_window_simt(), attn_errors_step()}) {
+        if (a < 0) return LR_ERR_CUDA;
+        attn |= (unsigned)a;
+    }
+    if (e || eg || (attn & kAttnTimeout)) return LR_ERR_TIMEOUT;
+    return (attn & kAttnIndex) ? LR_ERR_INDEX : LR_OK;
 }
 
 lr_status lr_debug_inject_scan_timeout(int on) {

@@ -58,8 +58,10 @@ typedef enum {
     LR_ERR_WORKSPACE = 10,  /* workspace NULL or smaller than lr_fwd_chunked_workspace_size */
     LR_ERR_TOO_LARGE = 11,  /* lr_fwd_chunked_noalloc: the problem needs more scratch
                                than LR_STATIC_WORKSPACE_BYTES */
-    LR_ERR_FUSE = 12        /* lr_fuse: unknown flag bits, two alpha maps at once,
+    LR_ERR_FUSE = 12,       /* lr_fuse: unknown flag bits, two alpha maps at once,
                                or norm_eps negative or not finite */
+    LR_ERR_INDEX = 13       /* a kernel of lr_attn.h met a page or a length on the device
+                               that is out of range (see lr_device_status) */
 } lr_status;
 
 /* Which row of the family (summary table of the first page). */
@@ -186,9 +188,10 @@ lr_status lr_step(const void *q, const void *k, const void *v,
  * Reports, then clears, the error word that kernels of this library set on
  * the current device when a bounded wait inside them gave up (a tensor-core
  * completion signal that never arrived); such a kernel stops early and its
- * outputs are incomplete.  Synchronises the current device first.
- * Returns LR_OK, LR_ERR_TIMEOUT, or LR_ERR_CUDA if the device cannot be
- * queried.
+ * outputs are incomplete.  Also reports and clears what the attention kernels
+ * (lr_attn.h) found out of range on the device.  Synchronises the current
+ * device first.  Returns LR_OK, LR_ERR_TIMEOUT, LR_ERR_INDEX, or LR_ERR_CUDA
+ * if the device cannot be queried.
  */
 lr_status lr_device_status(void);
 
