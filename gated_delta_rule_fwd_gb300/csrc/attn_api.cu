@@ -234,7 +234,9 @@ lr_status lr_fwd_window(const void *q, lr_strides qs, const void *k, lr_strides 
         if (overlap(so, i)) return LR_ERR_ALIAS;
     const WindowArgs a{q, k, v, o, qs, ks, vs, os, q_len, k_len, B, Hq, Hk, Tq, Tk, window, sinks,
                        scale};
-    return done(launch_window_simt(a, d, dt, stream));
+    if (Tk == 0) return done(launch_window_zero(a, d, dt, stream));
+    return done(dt == LR_DT_BF16 ? launch_window_tc(a, d, stream)
+                                 : launch_window_simt(a, d, stream));
 }
 
 size_t lr_step_paged_workspace_size(int N, int Hq, int Hk, int d, int max_len, int window,

@@ -1,4 +1,4 @@
-// lr_fwd_window on CUDA cores: one pass over the keys of a 64-row tile with
+// lr_fwd_window in fp32 on CUDA cores: one pass over the keys of a 64-row tile with
 // the running maximum and sum of the softmax.
 //
 // A CTA of 256 threads holds 64 query rows of one head.  For each tile of 64
@@ -186,19 +186,41 @@ cudaError_t launch(const WindowArgs &a, int slot, cudaStream_t stream) {
     return cudaGetLastError();
 }
 
-constexpr int kSlot = 208;  // ensure_smem_attr slots 208..213
+constexpr int kSlot = 208;  // ensure_smem_attr slots 208..210
+
+template <typename E>
+__global__ void window_zero_kernel(WindowArgs a, int units, long long n) {
+    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < n; i += gridDim.x * 256ll) {
+        const int u = (int)(i % units);
+        long long r = i / units;
+        const int t = (int)(r % a.Tq);
+        r /= a.Tq;
+        const int h = (int)(r % a.Hq), b = (int)(r / a.Hq);
+        bool bad = false;
+        const int ql = clamp_len(a.q_len, b, a.Tq, &bad);
+        clamp_len(a.k_len, b, a.Tk, &bad);
+        if (bad) atomicOr(&g_window_error, kAttnIndex);
+        if (t < ql)
+            *reinterpret_cast<uint4 *>(static_cast<E *>(a.o) + b * a.os.b + h * a.os.h + t * a.os.t +
+                                       u * (16 / (int)sizeof(E))) = make_uint4(0, 0, 0, 0);
+    }
+}
 
 }  // namespace
 
-cudaError_t launch_window_simt(const WindowArgs &a, int d, lr_dtype dt, cudaStream_t stream) {
-    if (dt == LR_DT_F32) {
-        if (d == 32) return launch<float, 32>(a, kSlot, stream);
-        if (d == 64) return launch<float, 64>(a, kSlot + 1, stream);
-        return launch<float, 128>(a, kSlot + 2, stream);
-    }
-    if (d == 32) return launch<__nv_bfloat16, 32>(a, kSlot + 3, stream);
-    if (d == 64) return launch<__nv_bfloat16, 64>(a, kSlot + 4, stream);
-    return launch<__nv_bfloat16, 128>(a, kSlot + 5, stream);
+cudaError_t launch_window_simt(const WindowArgs &a, int d, cudaStream_t stream) {
+    if (d == 32) return launch<float, 32>(a, kSlot, stream);
+    if (d == 64) return launch<float, 64>(a, kSlot + 1, stream);
+    return launch<float, 128>(a, kSlot + 2, stream);
+}
+
+cudaError_t launch_window_zero(const WindowArgs &a, int d, lr_dtype dt, cudaStream_t stream) {
+    const int units = d * (dt == LR_DT_F32 ? 4 : 2) / 16;  // 16-byte units of a row
+    const long long n = (long long)a.B * a.Hq * a.Tq * units;
+    const unsigned grid = (unsigned)((n + 255) / 256 < 4096 ? (n + 255) / 256 : 4096);
+    if (dt == LR_DT_F32) window_zero_kernel<float><<<grid, 256, 0, stream>>>(a, units, n);
+    else window_zero_kernel<__nv_bfloat16><<<grid, 256, 0, stream>>>(a, units, n);
+    return cudaGetLastError();
 }
 
 int attn_errors_window_simt() {

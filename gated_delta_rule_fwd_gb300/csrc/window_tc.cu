@@ -1,0 +1,531 @@
+// lr_fwd_window in bf16 on the tensor cores (tcgen05), one pass over the keys
+// with the running maximum and sum of the softmax.
+//
+// A CTA takes two 128-row query tiles that read the same keys: the same rows
+// of two heads that share a key head, or, where the heads of a group are odd
+// in number, consecutive rows of one head.  Per 128-key tile and query tile:
+//
+//     S = Q K^T        (tcgen05.mma, both operands in shared memory, S in TMEM)
+//     P = exp2(c S - m) row by row: one softmax thread per row reads its 128
+//                      scores, so maximum and sum need no exchange; P goes
+//                      back to TMEM in bf16, over the scores
+//     O += P V         (tcgen05.mma, P from TMEM, V from shared memory MN-major)
+//
+// The two query tiles alternate on the tensor pipe (P0 V, Q0 K', P1 V, Q1 K'),
+// so that one tile's softmax runs while the other's products do, and each key
+// tile is loaded once for 256 rows: at 1024 tensor cycles per 128 x 128 tile
+// (d = 128) the loads then need 32 bytes per cycle and SM, half of what a
+// single tile would.
+//
+// The maximum is raised only when a row's new one exceeds the one in use by a
+// factor of 2^8 (weights then stay below 2^8, exact in the sums' fp32 range);
+// only then O in TMEM is rescaled, by the softmax warp itself: the commit that
+// announced the scores also covers the tile's earlier products.
+//
+// Key tiles: the sinks' (before the window of every row), then the window's
+// from the first key that any row sees.  A tile that all rows of a query tile
+// see entirely skips the mask; one that none sees is skipped; a short one
+// takes fewer columns.  Masked weights are exact zeros, so only a non-finite
+// masked value row can disturb a result; rows whose output is not finite are
+// recomputed from the definition (attn_rows.cuh).
+//
+// Roles of the 320 threads: warps 0-3 softmax and output of query tile 0,
+// warps 4-7 of tile 1, warp 8 issues the products, warp 9 the TMA loads.
+// Every wait is bounded (lr_device_status).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "attn_internal.cuh"
+#include "attn_rows.cuh"
+#include "tc_common.cuh"
+
+namespace lr {
+namespace {
+
+using namespace tc;
+
+__device__ unsigned g_wtc_error = 0;
+
+constexpr int BM = 128, BN = 128;
+constexpr int NT = 320;
+
+template <int D>
+struct Layout {
+    static constexpr int KB = D > 64 ? 2 : 1;        // 64-column blocks of a tile
+    static constexpr int TILE = KB * 128 * 128;      // bytes of a 128-row tile
+    static constexpr int NS = D > 64 ? 5 : 8;        // key and value tiles in flight
+    static constexpr int Q = 0;
+    static constexpr int KV = 2 * TILE;
+    static constexpr int BAR = KV + NS * TILE;
+    static constexpr int BYTES = BAR + 256;
+    static constexpr int ALLOC = BYTES + 1024;
+};
+
+struct Barriers {
+    uint64_t qfull[2], sfull[2], pready[2], ofull[2], fin;
+    uint64_t full[8], empty[8];
+    uint32_t tmem;
+};
+
+constexpr uint32_t kS = 0, kO = 256;  // TMEM columns: S0, S1 (P over them), then O0, O1
+
+struct TcArgs {
+    WindowArgs w;
+    float c;          // |scale| log2 e, positive
+    unsigned negate;  // idesc bit: scores of -Q (scale < 0)
+    int pair_heads;   // the two query tiles are two heads, else consecutive rows
+    int tiles;        // row blocks of a head (pair) per batch
+};
+
+// D[tmem] (+)= A[tmem] * B[smem]
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
+                                            uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// 32 lanes x 16 consecutive 32-bit columns, written from registers.
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+// Tiled TMA load of a 4-D box (x innermost), completion counted on `bar`.
+__device__ __forceinline__ void tma_load_4d(void *dst, const void *map, int x, int y, int z, int w,
+                                            uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+// the lowest n bits (n clipped to 0..32)
+__device__ __forceinline__ uint32_t low_bits(int n) {
+    return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
+}
+
+// What a CTA works on; every role derives the same from its block index.
+struct Item {
+    int b, hk, head[2], i0[2];  // first row of each query tile
+    int rows[2], p0[2];         // valid rows, position of the first
+    int kl, sink_keys, sink_tiles, lo, hi, n;
+
+    __device__ __forceinline__ int key0(int it) const {
+        return it < sink_tiles ? it * BN : lo + (it - sink_tiles) * BN;
+    }
+    __device__ __forceinline__ int limit(int it) const { return it < sink_tiles ? sink_keys : hi; }
+    // columns that the tile needs, a multiple of 32
+    __device__ __forceinline__ int width(int it) const {
+        const int w = limit(it) - key0(it);
+        return w >= BN ? BN : (w + 31) & ~31;
+    }
+    // some row of query tile t may see some key
+    __device__ __forceinline__ bool active(int t, int it, const WindowArgs &a) const {
+        const int k0 = key0(it), ke = min(k0 + BN, limit(it));
+        return rows[t] > 0 && k0 <= p0[t] + rows[t] - 1 &&
+               ((long long)ke - 1 > (long long)p0[t] - a.window || k0 < a.sinks);
+    }
+    // every row sees every column of the tile's width
+    __device__ __forceinline__ bool whole(int t, int it, const WindowArgs &a) const {
+        const int k0 = key0(it), ke = k0 + width(it);
+        return ke <= limit(it) && ke - 1 <= p0[t] &&
+               ((long long)k0 > (long long)p0[t] + BM - 1 - a.window || ke <= a.sinks);
+    }
+    __device__ __forceinline__ int next(int t, int it, const WindowArgs &a) const {
+        while (it < n && !active(t, it, a)) ++it;
+        return it;
+    }
+};
+
+__device__ __forceinline__ Item make_item(const TcArgs &g, int block, bool *bad) {
+    const WindowArgs &a = g.w;
+    Item x;
+    const int groups = g.pair_heads ? a.Hq / 2 : a.Hq;
+    const int bh = block / g.tiles, tile = g.tiles - 1 - (block - bh * g.tiles);
+    x.b = bh / groups;
+    const int gh = bh - x.b * groups;
+    const int ql = clamp_len(a.q_len, x.b, a.Tq, bad);
+    x.kl = clamp_len(a.k_len, x.b, a.Tk, bad);
+    if (g.pair_heads) {
+        x.head[0] = 2 * gh, x.head[1] = 2 * gh + 1;
+        x.i0[0] = x.i0[1] = tile * BM;
+    } else {
+        x.head[0] = x.head[1] = gh;
+        x.i0[0] = tile * 2 * BM, x.i0[1] = x.i0[0] + BM;
+    }
+    x.hk = x.head[0] / (a.Hq / a.Hk);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        x.rows[t] = max(0, min(BM, ql - x.i0[t]));
+        x.p0[t] = x.kl - ql + x.i0[t];
+    }
+    const int last = x.rows[1] > 0 ? x.p0[1] + x.rows[1] - 1 : x.p0[0] + x.rows[0] - 1;
+    const SeenKeys f = seen_keys(x.p0[0], x.kl, a.window, a.sinks),
+                   e = seen_keys(last, x.kl, a.window, a.sinks);
+    x.lo = f.lo, x.hi = e.hi;
+    x.sink_keys = min(e.s1, f.lo);
+    x.sink_tiles = (x.sink_keys + BN - 1) / BN;
+    x.n = x.rows[0] > 0 ? x.sink_tiles + (x.hi > x.lo ? (x.hi - x.lo + BN - 1) / BN : 0) : 0;
+    return x;
+}
+
+template <int D>
+__global__ void __launch_bounds__(NT, 1)
+    window_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                     const __grid_constant__ CUtensorMap tmv, const TcArgs g) {
+    using L = Layout<D>;
+    extern __shared__ uint8_t raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    Barriers *bars = reinterpret_cast<Barriers *>(sm + L::BAR);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const WindowArgs &a = g.w;
+
+    bool bad = false;
+    const Item x = make_item(g, blockIdx.x, &bad);
+    if (bad && tid == 0) atomicOr(&g_wtc_error, kAttnIndex);
+    if (x.rows[0] == 0) return;
+
+    if (tid == 0) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&bars->qfull[t], 1);
+            mbar_init(&bars->sfull[t], 1);
+            mbar_init(&bars->pready[t], 4);
+            mbar_init(&bars->ofull[t], 1);
+        }
+        mbar_init(&bars->fin, 1);
+        for (int s = 0; s < L::NS; ++s) {
+            mbar_init(&bars->full[s], 1);
+            mbar_init(&bars->empty[s], 1);
+        }
+        fence_mbar_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(&bars->tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = bars->tmem;
+    bool ok = true;
+
+    if (warp == 9) {
+        // ============================================================ loads
+        if (lane == 0) {
+            for (int t = 0; t < 2; ++t) {
+                if (x.rows[t] == 0) continue;
+                mbar_expect_tx(&bars->qfull[t], L::TILE);
+                for (int kb = 0; kb < L::KB; ++kb)
+                    tma_load_4d(sm + L::Q + t * L::TILE + kb * 16384, &tmq, kb * 64, x.i0[t],
+                                x.head[t], x.b, &bars->qfull[t]);
+            }
+            int seq = 0;
+            for (int it = 0; it < x.n && ok; ++it) {
+                for (int kv = 0; kv < 2 && ok; ++kv, ++seq) {
+                    const int s = seq % L::NS;
+                    if (seq >= L::NS) ok = mbar_wait(&bars->empty[s], (seq / L::NS - 1) & 1);
+                    if (!ok) break;
+                    mbar_expect_tx(&bars->full[s], L::TILE);
+                    for (int kb = 0; kb < L::KB; ++kb)
+                        tma_load_4d(sm + L::KV + s * L::TILE + kb * 16384, kv ? &tmv : &tmk, kb * 64,
+                                    x.key0(it), x.hk, x.b, &bars->full[s]);
+                }
+            }
+            // never leave with copies into shared memory in flight
+            for (int t = 0; t < 2; ++t)
+                if (x.rows[t] > 0 && !mbar_wait(&bars->qfull[t], 0)) ok = false;
+            for (int i = max(0, seq - L::NS); i < seq; ++i)
+                if (!mbar_wait(&bars->full[i % L::NS], (i / L::NS) & 1)) ok = false;
+        }
+    } else if (warp == 8) {
+        // ========================================================= products
+        if (lane == 0 && x.n > 0) {
+            const uint32_t q_s = smem_u32(sm + L::Q), kv_s = smem_u32(sm + L::KV);
+            int upto[2] = {-1, -1}, done[2] = {0, 0};
+            auto stage_wait = [&](int seq) {
+                return mbar_wait(&bars->full[seq % L::NS], (seq / L::NS) & 1);
+            };
+            // S_t = Q_t K(it)^T; the key tile is free once both query tiles have used it
+            auto scores = [&](int t, int it) {
+                ok = stage_wait(2 * it);
+                if (!ok) return;
+                const int s = (2 * it) % L::NS;
+                const uint32_t id = idesc_bf16_f32(BM, x.width(it)) | g.negate;
+                const uint64_t da = tile_desc(q_s + t * L::TILE, 128, 0, 0),
+                               db = tile_desc(kv_s + s * L::TILE, 128, 0, 0);
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_bf16(tmem + kS + t * BN, kdesc_step(da, 128, ks), kdesc_step(db, 128, ks), id,
+                             ks > 0);
+                mma_commit(&bars->sfull[t]);
+                upto[t] = it;
+                if (!x.active(1 - t, it, a) || upto[1 - t] >= it) mma_commit(&bars->empty[s]);
+            };
+            for (int t = 0; t < 2 && ok; ++t) {
+                const int f = x.next(t, 0, a);
+                if (f >= x.n) continue;
+                ok = mbar_wait(&bars->qfull[t], 0);
+                if (ok) scores(t, f);
+            }
+            for (int it = 0; it < x.n && ok; ++it) {
+                const int vs = (2 * it + 1) % L::NS;
+                const bool act[2] = {x.active(0, it, a), x.active(1, it, a)};
+                ok = stage_wait(2 * it + 1);
+                if (!act[0] && !act[1]) {  // loaded for nobody
+                    if (ok) ok = stage_wait(2 * it);
+                    mbar_arrive(&bars->empty[(2 * it) % L::NS]);
+                    mbar_arrive(&bars->empty[vs]);
+                    continue;
+                }
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (!act[t]) continue;
+                    ok = mbar_wait(&bars->pready[t], done[t] & 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    const uint32_t id = idesc_bf16_f32_mn(BM, D, false, true);
+                    const uint64_t dv = tile_desc_mn(kv_s + vs * L::TILE, 128, 0);
+                    const int steps = x.width(it) >> 4;
+                    for (int ks = 0; ks < steps; ++ks)
+                        mma_bf16_ta(tmem + kO + t * 128, tmem + kS + t * BN + 8 * ks,
+                                    mndesc_step(dv, ks), id, done[t] > 0 || ks > 0);
+                    ++done[t];
+                    if (t == 1 || !act[1]) mma_commit(&bars->empty[vs]);
+                    const int nx = x.next(t, it + 1, a);
+                    if (nx < x.n) scores(t, nx);
+                    else mma_commit(&bars->ofull[t]);
+                }
+            }
+            mma_commit(&bars->fin);
+            if (!mbar_wait(&bars->fin, 0)) ok = false;
+        }
+    } else {
+        // ========================================= softmax, then the output
+        const int t = warp >> 2, row = tid & 127;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t ts = tmem + lanes + kS + t * BN, to = tmem + lanes + kO + t * 128;
+        const int p = x.p0[t] + row;
+        const long long plo = (long long)p - a.window + 1;
+        const int rlo = plo < 0 ? 0 : (int)plo;
+        float m = -INFINITY, l = 0.f;
+        int seen = 0;
+        for (int it = 0; it < x.n && ok; ++it) {
+            if (!x.active(t, it, a)) continue;
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars->sfull[t], seen & 1));
+            if (!ok) break;
+            tc_fence_after();
+            const int nch = x.width(it) >> 5;
+            float s[4][32];
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch)
+                if (ch < nch) tmem_ld32(ts + 32 * ch, s[ch]);
+            tmem_ld_wait(s[0], s[1], s[2], s[3]);
+            if (!x.whole(t, it, a)) {
+                const int k0 = x.key0(it), hi = min(p, x.limit(it) - 1);
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) {
+                    if (ch < nch) {
+                        const int kc = k0 + 32 * ch;
+                        const uint32_t keep = low_bits(hi + 1 - kc) &
+                                              (~low_bits(rlo - kc) | low_bits(a.sinks - kc));
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!((keep >> i) & 1u)) s[ch][i] = -INFINITY;
+                    }
+                }
+            }
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch)
+                if (ch < nch) {
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[ch][i]);
+                }
+            const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+            const bool grow = mn > m && (m == -INFINITY || (mn - m) * g.c > 8.f);
+            // a row that has seen nothing yet has l = 0 and zeros in O (or O unset)
+            if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
+                const float f = grow && m != -INFINITY ? ex2((m - mn) * g.c) : 1.f;
+                l *= f;
+#pragma unroll 1
+                for (int ch = 0; ch < D / 16; ++ch) {
+                    float v[16];
+                    tmem_ld16(to + 16 * ch, v);
+                    tmem_ld_wait(v);
+                    uint32_t r[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i] * f);
+                    tmem_st16(to + 16 * ch, r);
+                }
+            }
+            if (grow) m = mn;
+            const float base = m == -INFINITY ? 0.f : m * g.c;
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int ch = 0; ch < 4; ++ch)
+                if (ch < nch) {
+                    uint32_t r[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        const float u = ex2(fmaf(s[ch][2 * i], g.c, -base)),
+                                    w = ex2(fmaf(s[ch][2 * i + 1], g.c, -base));
+                        sum[i & 1] += u;
+                        sum[2 + (i & 1)] += w;
+                        r[i] = pack2(u, w);
+                    }
+                    tmem_st16(ts + 16 * ch, r);
+                }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->pready[t]);
+            ++seen;
+        }
+        const bool live = row < x.rows[t];
+        if (seen > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->ofull[t], 0));
+        tc_fence_after();
+        if (ok) {
+            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + x.b * a.os.b +
+                               x.head[t] * a.os.h + (long long)(x.i0[t] + row) * a.os.t;
+            const float inv = l == 0.f ? 0.f : 1.f / l;  // no key, or only scores of -inf
+            bool finite = true;
+#pragma unroll
+            for (int ch = 0; ch < D / 32; ++ch) {
+                float v[32];
+                if (seen > 0) {
+                    tmem_ld32(to + 32 * ch, v);
+                    tmem_ld_wait(v);
+                }
+                uint4 r[4];
+                uint32_t *w = reinterpret_cast<uint32_t *>(r);
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float y0 = seen > 0 ? v[2 * i] * inv : 0.f,
+                                y1 = seen > 0 ? v[2 * i + 1] * inv : 0.f;
+                    finite = finite && isfinite(y0) && isfinite(y1);
+                    w[i] = pack2(y0, y1);
+                }
+                if (live) {
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(o + 32 * ch + 8 * i) = r[i];
+                }
+            }
+            unsigned again = __ballot_sync(0xffffffffu, live && !finite);
+            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + x.b * a.qs.b +
+                                     x.head[t] * a.qs.h;
+            const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k) + x.b * a.ks.b + x.hk * a.ks.h;
+            const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + x.b * a.vs.b + x.hk * a.vs.h;
+            __syncwarp();
+            while (again) {
+                const int i = __ffs(again) - 1;
+                again &= again - 1;
+                const int r = 32 * (warp & 3) + i;
+                attn_row<__nv_bfloat16, D>(
+                    q + (long long)(x.i0[t] + r) * a.qs.t, k, v, a.ks.t, a.vs.t,
+                    static_cast<__nv_bfloat16 *>(a.o) + x.b * a.os.b + x.head[t] * a.os.h +
+                        (long long)(x.i0[t] + r) * a.os.t,
+                    seen_keys(x.p0[t] + r, x.kl, a.window, a.sinks), a.scale);
+            }
+        }
+    }
+
+    if (!ok) atomicOr(&g_wtc_error, kAttnTimeout);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult qr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &qr) == cudaSuccess &&
+            qr == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    });
+    return fn;
+}
+
+// A strided [B, H, T, d] tensor, boxes of 128 rows x 64 columns, 128-byte
+// swizzle, zero fill outside (also the columns of a box wider than d).
+cudaError_t rows_map(CUtensorMap *m, const void *base, const lr_strides &s, int B, int H, int T, int d) {
+    auto enc = encoder();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)T, (cuuint64_t)H, (cuuint64_t)B};
+    // a dimension of size 1 has stride 0 here: any valid one will do
+    auto bytes = [d](long long st) { return (cuuint64_t)(st ? st * 2 : d * 2); };
+    const cuuint64_t strides[3] = {bytes(s.t), bytes(s.h), bytes(s.b)};
+    const cuuint32_t box[4] = {64, 128, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims,
+                           strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                           CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+template <int D>
+cudaError_t launch(const WindowArgs &a, int slot, cudaStream_t stream) {
+    CUtensorMap mq, mk, mv;
+    cudaError_t e = rows_map(&mq, a.q, a.qs, a.B, a.Hq, a.Tq, D);
+    if (e == cudaSuccess) e = rows_map(&mk, a.k, a.ks, a.B, a.Hk, a.Tk, D);
+    if (e == cudaSuccess) e = rows_map(&mv, a.v, a.vs, a.B, a.Hk, a.Tk, D);
+    if (e == cudaSuccess)
+        e = ensure_smem_attr(reinterpret_cast<const void *>(&window_tc_kernel<D>), Layout<D>::ALLOC, slot);
+    if (e != cudaSuccess) return e;
+    TcArgs g;
+    g.w = a;
+    // scale 0 gives every key the same weight; a product with it would turn
+    // the mask's -inf into NaN, and 2^-100 rounds to the same weights
+    g.c = a.scale == 0.f ? 7.9e-31f : fabsf(a.scale) * 1.4426950408889634f;
+    g.negate = a.scale < 0.f ? 1u << 13 : 0u;
+    g.pair_heads = (a.Hq / a.Hk) % 2 == 0;
+    const int rows = g.pair_heads ? BM : 2 * BM;
+    g.tiles = (a.Tq + rows - 1) / rows;
+    const unsigned grid = (unsigned)(a.B * (g.pair_heads ? a.Hq / 2 : a.Hq) * g.tiles);
+    window_tc_kernel<D><<<grid, NT, Layout<D>::ALLOC, stream>>>(mq, mk, mv, g);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// ensure_smem_attr slots 214..216 belong to this file.
+cudaError_t launch_window_tc(const WindowArgs &a, int d, cudaStream_t stream) {
+    if (d == 32) return launch<32>(a, 214, stream);
+    if (d == 64) return launch<64>(a, 215, stream);
+    return launch<128>(a, 216, stream);
+}
+
+int attn_errors_window_tc() {
+    unsigned h = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&h, g_wtc_error, sizeof(h)) != cudaSuccess) return -1;
+    if (h) cudaMemcpyToSymbol(g_wtc_error, &zero, sizeof(h));
+    return (int)h;
+}
+
+}  // namespace lr
