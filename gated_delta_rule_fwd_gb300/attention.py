@@ -40,6 +40,9 @@ class QkMaps(ctypes.Structure):
                 ("inv_freq", ctypes.c_void_p)]
 
 
+_NO_STRIDES = Strides(0, 0, 0)
+
+
 def declare(L):
     """Argument types of the attention entry points on a loaded library."""
     vp, i, f, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_float, ctypes.c_size_t
@@ -59,37 +62,49 @@ def _base():
     return base
 
 
-def _strided(t, name, shape, dtype, device):
-    """Checks a [B, H, T, d] tensor with contiguous channels; its strides."""
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.stride(-1) != 1:
+# The checks below ask for everything at once and look for what is wrong only
+# when something is: these calls run once per layer and token, where the time
+# of the binding is the time of the step.
+
+def _want(t, name, shape, dtype, dev):
+    """A contiguous tensor of this shape, type and device."""
+    if t.dtype is not dtype or t.shape != shape or t.device != dev or not t.is_contiguous():
+        _base()._check(t, name, shape, dtype, dev)
+
+
+def _strided(t, name, shape, dtype, dev):
+    """A [B, H, T, d] tensor with contiguous channels; its strides."""
+    if t.dtype is not dtype or t.shape != shape or t.device != dev:
+        _base()._check(t, name, shape, dtype, dev)
+    st = t.stride()
+    if st[3] != 1 and shape[3] != 1:
         raise ValueError(f"{name} must have contiguous channels")
-    return Strides(t.stride(0), t.stride(1), t.stride(2))
+    return Strides(st[0], st[1], st[2])
 
 
-def _ints(t, name, shape, device):
+def _paged(k_cache, v_cache, table, rows, d, dtype, dev):
+    """Pools [P, Hk, page, d] and a table [rows, max_pages]."""
     import torch
-    if t is not None:
-        _base()._check(t, name, shape, torch.int32, device)
+    pool, most = k_cache.shape, table.shape
+    if len(pool) != 4 or pool[3] != d:
+        raise ValueError(f"k_cache must have shape (pages, heads, page, {d}), got {tuple(pool)}")
+    _want(k_cache, "k_cache", pool, dtype, dev)
+    _want(v_cache, "v_cache", pool, dtype, dev)
+    if len(most) != 2:
+        raise ValueError(f"table must have shape ({rows}, pages of a sequence), got {tuple(most)}")
+    _want(table, "table", (rows, most[1]), torch.int32, dev)
+    return Paged(k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), pool[0], pool[2], most[1])
 
 
-def _paged(base, k_cache, v_cache, table, rows, d, dtype, dev):
-    """Checks the pools [P, Hk, page, d] and the table [rows, max_pages]."""
-    import torch
-    if k_cache.dim() != 4 or k_cache.shape[-1] != d:
-        raise ValueError(f"k_cache must have shape (pages, heads, page, {d}), got {tuple(k_cache.shape)}")
-    base._check(k_cache, "k_cache", k_cache.shape, dtype, dev)
-    base._check(v_cache, "v_cache", k_cache.shape, dtype, dev)
-    if table.dim() != 2:
-        raise ValueError(f"table must have shape ({rows}, pages of a sequence), got {tuple(table.shape)}")
-    base._check(table, "table", (rows, table.shape[1]), torch.int32, dev)
-    return Paged(k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), k_cache.shape[0],
-                 k_cache.shape[2], table.shape[1])
+class _Here:
+    def __enter__(self):
+        return None
+
+    def __exit__(self, *exc):
+        return None
+
+
+_HERE = _Here()
 
 
 def _on(stream, dev):
@@ -97,10 +112,18 @@ def _on(stream, dev):
     current one.  What is allocated inside belongs to that stream."""
     import torch
     if stream is None:
-        return torch.cuda.device(dev)
+        return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
     if stream.device != dev:
         raise ValueError(f"stream must be on {dev}, got {stream.device}")
     return torch.cuda.stream(stream)
+
+
+def _handle(stream, dev):
+    import torch
+    if stream is not None:
+        return stream.cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return raw(dev.index) if raw else torch.cuda.current_stream(dev).cuda_stream
 
 
 def _int32(x, name):
@@ -131,49 +154,52 @@ def lr_qk_norm_rope(q, k, positions=None, *, norm=True, q_weight=None, k_weight=
     base._require_cuda(dev)
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q and k must have shape (B, heads, T, d)")
-    B, Hq, T, d = q.shape
-    Hk = k.shape[1]
+    q_shape, k_shape, dtype = q.shape, k.shape, q.dtype
+    B, Hq, T, d = q_shape
+    Hk = k_shape[1]
     dt = base._dtype_code(q)
-    qs = _strided(q, "q", (B, Hq, T, d), q.dtype, dev)
-    ks = _strided(k, "k", (B, Hk, T, d), q.dtype, dev)
-    _ints(positions, "positions", (B, T), dev)
-    for t, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None:
-            base._check(t, n, (d,), torch.float32, dev)
+    qs = _strided(q, "q", q_shape, dtype, dev)
+    ks = _strided(k, "k", (B, Hk, T, d), dtype, dev)
+    if positions is not None:
+        _want(positions, "positions", (B, T), torch.int32, dev)
+    if q_weight is not None:
+        _want(q_weight, "q_weight", (d,), torch.float32, dev)
+    if k_weight is not None:
+        _want(k_weight, "k_weight", (d,), torch.float32, dev)
     rot = 0
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
-        base._check(inv_freq, "inv_freq", (rot // 2,), torch.float64, dev)
-    cache = vs = None
+        _want(inv_freq, "inv_freq", (rot // 2,), torch.float64, dev)
+    cache, vs = None, _NO_STRIDES
     if k_cache is not None or v_cache is not None or table is not None or v is not None:
         if k_cache is None or v_cache is None or table is None or v is None:
             raise ValueError("a cache needs v, k_cache, v_cache and table together")
-        cache = _paged(base, k_cache, v_cache, table, B, d, q.dtype, dev)
+        cache = _paged(k_cache, v_cache, table, B, d, dtype, dev)
         if k_cache.shape[1] != Hk:
             raise ValueError(f"k_cache must have {Hk} heads, got {k_cache.shape[1]}")
-        vs = _strided(v, "v", (B, Hk, T, d), q.dtype, dev)
+        vs = _strided(v, "v", k_shape, dtype, dev)
     elif not write_k:
         raise ValueError("write_k=False needs a cache")
     if q_out is not None:
-        base._check(q_out, "q_out", (B, Hq, T, d), q.dtype, dev)
+        _want(q_out, "q_out", q_shape, dtype, dev)
     if k_out is not None:
         if not write_k:
             raise ValueError("k_out given with write_k=False")
-        base._check(k_out, "k_out", (B, Hk, T, d), q.dtype, dev)
+        _want(k_out, "k_out", k_shape, dtype, dev)
     maps = QkMaps((QK_NORM if norm else 0) | (QK_INTERLEAVED if interleaved else 0),
                   None if q_weight is None else q_weight.data_ptr(),
-                  None if k_weight is None else k_weight.data_ptr(), float(eps), rot,
+                  None if k_weight is None else k_weight.data_ptr(), eps, rot,
                   None if inv_freq is None else inv_freq.data_ptr())
     with _on(stream, dev):
         if q_out is None:
-            q_out = torch.empty((B, Hq, T, d), dtype=q.dtype, device=dev)
+            q_out = torch.empty(q_shape, dtype=dtype, device=dev)
         if k_out is None and write_k:
-            k_out = torch.empty((B, Hk, T, d), dtype=q.dtype, device=dev)
+            k_out = torch.empty(k_shape, dtype=dtype, device=dev)
         st = base.lib().lr_qk_norm_rope(
-            base._ptr(q), qs, base._ptr(k), ks, base._ptr(positions), ctypes.byref(maps),
-            base._ptr(q_out), base._ptr(k_out), base._ptr(v), vs or Strides(0, 0, 0),
-            None if cache is None else ctypes.byref(cache), B, T, Hq, Hk, d, dt,
-            base._stream_handle(stream, dev))
+            q.data_ptr(), qs, k.data_ptr(), ks, None if positions is None else positions.data_ptr(),
+            maps, q_out.data_ptr(), None if k_out is None else k_out.data_ptr(),
+            None if v is None else v.data_ptr(), vs, cache, B, T, Hq, Hk, d, dt,
+            _handle(stream, dev))
     if st != 0:
         raise base.LrError(st, "lr_qk_norm_rope")
     return q_out, k_out
@@ -197,26 +223,30 @@ def lr_fwd_window(q, k, v, *, window=None, sinks=0, q_len=None, k_len=None, scal
     base._require_cuda(dev)
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q, k and v must have shape (B, heads, T, d)")
-    B, Hq, Tq, d = q.shape
-    Hk, Tk = k.shape[1], k.shape[2]
+    q_shape, dtype = q.shape, q.dtype
+    B, Hq, Tq, d = q_shape
+    _, Hk, Tk, _ = k.shape
     dt = base._dtype_code(q)
-    qs = _strided(q, "q", (B, Hq, Tq, d), q.dtype, dev)
-    ks = _strided(k, "k", (B, Hk, Tk, d), q.dtype, dev)
-    vs = _strided(v, "v", (B, Hk, Tk, d), q.dtype, dev)
-    _ints(q_len, "q_len", (B,), dev)
-    _ints(k_len, "k_len", (B,), dev)
-    if o is not None:
-        _strided(o, "o", (B, Hq, Tq, d), q.dtype, dev)
+    qs = _strided(q, "q", q_shape, dtype, dev)
+    ks = _strided(k, "k", (B, Hk, Tk, d), dtype, dev)
+    vs = _strided(v, "v", (B, Hk, Tk, d), dtype, dev)
+    if q_len is not None:
+        _want(q_len, "q_len", (B,), torch.int32, dev)
+    if k_len is not None:
+        _want(k_len, "k_len", (B,), torch.int32, dev)
+    os_ = None if o is None else _strided(o, "o", q_shape, dtype, dev)
     window = NO_WINDOW if window is None else _int32(window, "window")
-    scale = d ** -0.5 if scale is None else float(scale)
+    sinks = _int32(sinks, "sinks")
+    scale = d ** -0.5 if scale is None else scale
     with _on(stream, dev):
         if o is None:
-            make = torch.empty if q_len is None else torch.zeros
-            o = make((B, Hq, Tq, d), dtype=q.dtype, device=dev)
+            o = (torch.empty if q_len is None else torch.zeros)(q_shape, dtype=dtype, device=dev)
+            os_ = _strided(o, "o", q_shape, dtype, dev)
         st = base.lib().lr_fwd_window(
-            base._ptr(q), qs, base._ptr(k), ks, base._ptr(v), vs, base._ptr(q_len),
-            base._ptr(k_len), base._ptr(o), Strides(o.stride(0), o.stride(1), o.stride(2)), B, Hq, Hk, Tq, Tk, d, window,
-            _int32(sinks, "sinks"), scale, dt, base._stream_handle(stream, dev))
+            q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+            None if q_len is None else q_len.data_ptr(),
+            None if k_len is None else k_len.data_ptr(), o.data_ptr(), os_, B, Hq, Hk, Tq, Tk, d,
+            window, sinks, scale, dt, _handle(stream, dev))
     if st != 0:
         raise base.LrError(st, "lr_fwd_window")
     return o
@@ -250,34 +280,36 @@ def lr_step_paged(q, k_cache, v_cache, table, lens, *, max_len=None, window=None
     base._require_cuda(dev)
     if q.dim() != 3:
         raise ValueError("q must have shape (N, heads, d)")
-    N, Hq, d = q.shape
+    q_shape, dtype = q.shape, q.dtype
+    N, Hq, d = q_shape
     dt = base._dtype_code(q)
-    base._check(q, "q", (N, Hq, d), q.dtype, dev)
-    cache = _paged(base, k_cache, v_cache, table, N, d, q.dtype, dev)
+    _want(q, "q", q_shape, dtype, dev)
+    cache = _paged(k_cache, v_cache, table, N, d, dtype, dev)
     Hk = k_cache.shape[1]
     if lens is None:
         raise ValueError("lens is required")
-    _ints(lens, "lens", (N,), dev)
+    _want(lens, "lens", (N,), torch.int32, dev)
     if o is not None:
-        base._check(o, "o", (N, Hq, d), q.dtype, dev)
-    holds = cache.page * cache.max_pages
-    max_len = holds if max_len is None else _int32(max_len, "max_len")
+        _want(o, "o", q_shape, dtype, dev)
+    max_len = cache.page * cache.max_pages if max_len is None else _int32(max_len, "max_len")
     window = NO_WINDOW if window is None else _int32(window, "window")
     sinks = _int32(sinks, "sinks")
-    scale = d ** -0.5 if scale is None else float(scale)
+    scale = d ** -0.5 if scale is None else scale
     L = base.lib()
-    need = int(L.lr_step_paged_workspace_size(N, Hq, Hk, d, max_len, window, sinks, dt))
-    if workspace is not None and (workspace.device != dev or not workspace.is_contiguous()):
+    need = 0
+    if workspace is None:
+        need = L.lr_step_paged_workspace_size(N, Hq, Hk, d, max_len, window, sinks, dt)
+    elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {dev}")
     with _on(stream, dev):
         if o is None:
-            o = torch.empty((N, Hq, d), dtype=q.dtype, device=dev)
-        if workspace is None and need > 0:
+            o = torch.empty(q_shape, dtype=dtype, device=dev)
+        if need > 0:
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-        st = L.lr_step_paged(base._ptr(q), ctypes.byref(cache), base._ptr(lens), base._ptr(o), N,
-                             Hq, Hk, d, max_len, window, sinks, scale, dt, base._ptr(workspace),
-                             ws_bytes, base._stream_handle(stream, dev))
+        ws, ws_bytes = ((None, 0) if workspace is None else
+                        (workspace.data_ptr(), workspace.numel() * workspace.element_size()))
+        st = L.lr_step_paged(q.data_ptr(), cache, lens.data_ptr(), o.data_ptr(), N, Hq, Hk, d,
+                             max_len, window, sinks, scale, dt, ws, ws_bytes, _handle(stream, dev))
     if st != 0:
         raise base.LrError(st, "lr_step_paged")
     return o

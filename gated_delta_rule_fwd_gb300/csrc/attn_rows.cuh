@@ -19,8 +19,8 @@ __device__ __forceinline__ float warp_sum(float x) {
 // q: the row's d channels; k, v: row 0 of its key head, rows `kt` and `vt`
 // elements apart.  Every lane of the warp calls this with the same arguments.
 template <typename E, int D>
-__device__ __noinline__ void attn_row(const E *q, const E *k, const E *v, long long kt, long long vt, E *o,
-                                      SeenKeys s, float scale) {
+__device__ __forceinline__ void attn_row(const E *q, const E *k, const E *v, long long kt,
+                                         long long vt, E *o, SeenKeys s, float scale) {
     constexpr int PL = D / 32;  // channels of a lane: lane + 32 i
     const int lane = threadIdx.x & 31;
     float qr[PL], acc[PL], m = -INFINITY, l = 0.f;
@@ -29,6 +29,7 @@ __device__ __noinline__ void attn_row(const E *q, const E *k, const E *v, long l
         qr[i] = to_f<E>(q[lane + 32 * i]) * scale;
         acc[i] = 0.f;
     }
+#pragma unroll 1
     for (int j = 0; j < s.hi; ++j) {
         if (j == s.s1 && j < s.lo) j = s.lo;
         if (j >= s.hi) break;

@@ -29,8 +29,9 @@
 // masked value row can disturb a result; rows whose output is not finite are
 // recomputed from the definition (attn_rows.cuh).
 //
-// Roles of the 320 threads: warps 0-3 softmax and output of query tile 0,
-// warps 4-7 of tile 1, warp 8 issues the products, warp 9 the TMA loads.
+// Roles of the 384 threads: warps 0-3 softmax and output of query tile 0,
+// warps 4-7 of tile 1, warps 8 and 9 issue the products of tiles 0 and 1, warp
+// 10 the TMA loads.
 // Every wait is bounded (lr_device_status).
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -49,7 +50,10 @@ using namespace tc;
 __device__ unsigned g_wtc_error = 0;
 
 constexpr int BM = 128, BN = 128;
-constexpr int NT = 320;
+// Threads and their registers: launched with 168 each (64,512 in all); the
+// softmax warpgroups take 216, the third one keeps 72.
+constexpr int NT = 384, kRegsSoftmax = 216, kRegsOther = 72;
+static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsOther <= NT * 168, "register shares");
 
 template <int D>
 struct Layout {
@@ -59,12 +63,13 @@ struct Layout {
     static constexpr int Q = 0;
     static constexpr int KV = 2 * TILE;
     static constexpr int BAR = KV + NS * TILE;
-    static constexpr int BYTES = BAR + 256;
+    static constexpr int ITEM = BAR + 256;           // struct Item
+    static constexpr int BYTES = ITEM + 256;
     static constexpr int ALLOC = BYTES + 1024;
 };
 
 struct Barriers {
-    uint64_t qfull[2], sfull[2], pready[2], ofull[2], fin;
+    uint64_t qfull[2], sfull[2], pready[2], ofull[2], fin[2];
     uint64_t full[8], empty[8];
     uint32_t tmem;
 };
@@ -76,7 +81,8 @@ struct TcArgs {
     float c;          // |scale| log2 e, positive
     unsigned negate;  // idesc bit: scores of -Q (scale < 0)
     int pair_heads;   // the two query tiles are two heads, else consecutive rows
-    int tiles;        // row blocks of a head (pair) per batch
+    int tiles;        // row blocks of a head (pair)
+    int span;         // heads (pairs) of all batches that are worked on together
 };
 
 // D[tmem] (+)= A[tmem] * B[smem]
@@ -121,15 +127,57 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+// One lane of a converged warp.
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+// Register shares of the warpgroups (all four warps execute these).
+template <int N> __device__ __forceinline__ void regs_up() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N> __device__ __forceinline__ void regs_down() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 // the lowest n bits (n clipped to 0..32)
 __device__ __forceinline__ uint32_t low_bits(int n) {
     return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
 }
 
-// What a CTA works on; every role derives the same from its block index.
+// What a CTA works on, kept in shared memory.  Key
+// tile `it` is a sink tile (it < sink_tiles) or window tile it - sink_tiles.
+// Sink tiles lie before the window of every row, so all rows see their keys.
+// Window tiles that query tile t needs form one run [act0, act1), those that
+// all its rows see entirely one inside it [all0, all1).
 struct Item {
     int b, hk, head[2], i0[2];  // first row of each query tile
     int rows[2], p0[2];         // valid rows, position of the first
+    int act0[2], act1[2], all0[2], all1[2];
     int kl, sink_keys, sink_tiles, lo, hi, n;
 
     __device__ __forceinline__ int key0(int it) const {
@@ -141,29 +189,17 @@ struct Item {
         const int w = limit(it) - key0(it);
         return w >= BN ? BN : (w + 31) & ~31;
     }
-    // some row of query tile t may see some key
-    __device__ __forceinline__ bool active(int t, int it, const WindowArgs &a) const {
-        const int k0 = key0(it), ke = min(k0 + BN, limit(it));
-        return rows[t] > 0 && k0 <= p0[t] + rows[t] - 1 &&
-               ((long long)ke - 1 > (long long)p0[t] - a.window || k0 < a.sinks);
-    }
-    // every row sees every column of the tile's width
-    __device__ __forceinline__ bool whole(int t, int it, const WindowArgs &a) const {
-        const int k0 = key0(it), ke = k0 + width(it);
-        return ke <= limit(it) && ke - 1 <= p0[t] &&
-               ((long long)k0 > (long long)p0[t] + BM - 1 - a.window || ke <= a.sinks);
-    }
-    __device__ __forceinline__ int next(int t, int it, const WindowArgs &a) const {
-        while (it < n && !active(t, it, a)) ++it;
-        return it;
-    }
 };
 
 __device__ __forceinline__ Item make_item(const TcArgs &g, int block, bool *bad) {
     const WindowArgs &a = g.w;
     Item x;
     const int groups = g.pair_heads ? a.Hq / 2 : a.Hq;
-    const int bh = block / g.tiles, tile = g.tiles - 1 - (block - bh * g.tiles);
+    // the last rows see the most keys: of the heads whose keys and values the
+    // L2 cache holds together, all longest tiles start first
+    const int span = block / (g.span * g.tiles), in = block - span * g.span * g.tiles;
+    const int wide = min(g.span, a.B * groups - span * g.span);
+    const int tile = g.tiles - 1 - in / wide, bh = span * g.span + in % wide;
     x.b = bh / groups;
     const int gh = bh - x.b * groups;
     const int ql = clamp_len(a.q_len, x.b, a.Tq, bad);
@@ -188,6 +224,19 @@ __device__ __forceinline__ Item make_item(const TcArgs &g, int block, bool *bad)
     x.sink_keys = min(e.s1, f.lo);
     x.sink_tiles = (x.sink_keys + BN - 1) / BN;
     x.n = x.rows[0] > 0 ? x.sink_tiles + (x.hi > x.lo ? (x.hi - x.lo + BN - 1) / BN : 0) : 0;
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+        const long long p = x.p0[t], lo = x.lo;
+        // first key that the tile's first row sees; sinks inside the window tiles keep all
+        const long long k = a.sinks > x.lo ? lo : p - a.window + 1;
+        x.act0[t] = x.sink_tiles + (k > lo ? (int)((k - lo) / BN) : 0);
+        const long long last_p = p + x.rows[t] - 1;
+        x.act1[t] = min(x.n, last_p < lo ? x.sink_tiles : x.sink_tiles + (int)((last_p - lo) / BN) + 1);
+        const long long f = p + BM - a.window - lo;  // first key of the last row
+        x.all0[t] = f > 0 ? (int)min((long long)x.n, x.sink_tiles + (f + BN - 1) / BN) : x.sink_tiles;
+        const long long e = min((long long)x.hi, p + 1) - lo;
+        x.all1[t] = x.sink_tiles + (e > 0 ? (int)(e / BN) : 0);
+    }
     return x;
 }
 
@@ -202,22 +251,21 @@ __global__ void __launch_bounds__(NT, 1)
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const WindowArgs &a = g.w;
 
-    bool bad = false;
-    const Item x = make_item(g, blockIdx.x, &bad);
-    if (bad && tid == 0) atomicOr(&g_wtc_error, kAttnIndex);
-    if (x.rows[0] == 0) return;
-
+    Item &x = *reinterpret_cast<Item *>(sm + L::ITEM);
     if (tid == 0) {
+        bool bad = false;
+        x = make_item(g, blockIdx.x, &bad);
+        if (bad) atomicOr(&g_wtc_error, kAttnIndex);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bars->qfull[t], 1);
             mbar_init(&bars->sfull[t], 1);
             mbar_init(&bars->pready[t], 4);
             mbar_init(&bars->ofull[t], 1);
+            mbar_init(&bars->fin[t], 1);
         }
-        mbar_init(&bars->fin, 1);
         for (int s = 0; s < L::NS; ++s) {
             mbar_init(&bars->full[s], 1);
-            mbar_init(&bars->empty[s], 1);
+            mbar_init(&bars->empty[s], 2);  // both query tiles
         }
         fence_mbar_init();
     }
@@ -231,7 +279,8 @@ __global__ void __launch_bounds__(NT, 1)
     const uint32_t tmem = bars->tmem;
     bool ok = true;
 
-    if (warp == 9) {
+    if (warp >= 8) regs_down<kRegsOther>();
+    if (warp == 10) {
         // ============================================================ loads
         if (lane == 0) {
             for (int t = 0; t < 2; ++t) {
@@ -259,144 +308,194 @@ __global__ void __launch_bounds__(NT, 1)
             for (int i = max(0, seq - L::NS); i < seq; ++i)
                 if (!mbar_wait(&bars->full[i % L::NS], (i / L::NS) & 1)) ok = false;
         }
-    } else if (warp == 8) {
+    } else if (warp == 8 || warp == 9) {
         // ========================================================= products
-        if (lane == 0 && x.n > 0) {
-            const uint32_t q_s = smem_u32(sm + L::Q), kv_s = smem_u32(sm + L::KV);
-            int upto[2] = {-1, -1}, done[2] = {0, 0};
-            auto stage_wait = [&](int seq) {
-                return mbar_wait(&bars->full[seq % L::NS], (seq / L::NS) & 1);
-            };
-            // S_t = Q_t K(it)^T; the key tile is free once both query tiles have used it
-            auto scores = [&](int t, int it) {
-                ok = stage_wait(2 * it);
-                if (!ok) return;
-                const int s = (2 * it) % L::NS;
-                const uint32_t id = idesc_bf16_f32(BM, x.width(it)) | g.negate;
-                const uint64_t da = tile_desc(q_s + t * L::TILE, 128, 0, 0),
-                               db = tile_desc(kv_s + s * L::TILE, 128, 0, 0);
+        // One warp per query tile.  It walks and waits as a whole; one elected
+        // lane issues.  What a step needs is worked out before its wait for P,
+        // so that the products of a step follow the wait at once.
+        const int t = warp - 8;
+        const bool has = x.rows[t] > 0;
+        const int n = x.n, sink_tiles = x.sink_tiles, act0 = has ? x.act0[t] : n, act1 = has ? x.act1[t] : n;
+        const int w_last = x.width(n - 1), w_sink = sink_tiles ? x.width(sink_tiles - 1) : BN;
+        const uint32_t q_s = smem_u32(sm + L::Q) + t * L::TILE, kv_s = smem_u32(sm + L::KV);
+        const uint32_t s_t = tmem + kS + t * BN, o_t = tmem + kO + t * 128;
+        const uint32_t id_o = idesc_bf16_f32_mn(BM, D, false, true);
+        const uint64_t dq = tile_desc(q_s, 128, 0, 0);
+        const bool lead = elect_one();
+        auto active = [&](int it) { return has && (it < sink_tiles || (it >= act0 && it < act1)); };
+        auto width = [&](int it) { return it == n - 1 ? w_last : (it == sink_tiles - 1 ? w_sink : BN); };
+        auto stage_wait = [&](int seq) {
+            return __all_sync(0xffffffffu, mbar_wait(&bars->full[seq % L::NS], (seq / L::NS) & 1));
+        };
+        // a tile that the query tile skips: its stages are free for it once loaded
+        auto skip = [&](int it) {
+            for (int kv = 0; kv < 2 && ok; ++kv) {
+                ok = stage_wait(2 * it + kv);
+                if (lead && ok) mbar_arrive(&bars->empty[(2 * it + kv) % L::NS]);
+            }
+        };
+        // S = Q K(it)^T
+        auto scores = [&](int it, int s, uint64_t dk, uint32_t id) {
 #pragma unroll
-                for (int ks = 0; ks < D / 16; ++ks)
-                    mma_bf16(tmem + kS + t * BN, kdesc_step(da, 128, ks), kdesc_step(db, 128, ks), id,
-                             ks > 0);
-                mma_commit(&bars->sfull[t]);
-                upto[t] = it;
-                if (!x.active(1 - t, it, a) || upto[1 - t] >= it) mma_commit(&bars->empty[s]);
-            };
-            for (int t = 0; t < 2 && ok; ++t) {
-                const int f = x.next(t, 0, a);
-                if (f >= x.n) continue;
-                ok = mbar_wait(&bars->qfull[t], 0);
-                if (ok) scores(t, f);
-            }
-            for (int it = 0; it < x.n && ok; ++it) {
-                const int vs = (2 * it + 1) % L::NS;
-                const bool act[2] = {x.active(0, it, a), x.active(1, it, a)};
-                ok = stage_wait(2 * it + 1);
-                if (!act[0] && !act[1]) {  // loaded for nobody
-                    if (ok) ok = stage_wait(2 * it);
-                    mbar_arrive(&bars->empty[(2 * it) % L::NS]);
-                    mbar_arrive(&bars->empty[vs]);
-                    continue;
-                }
-                for (int t = 0; t < 2 && ok; ++t) {
-                    if (!act[t]) continue;
-                    ok = mbar_wait(&bars->pready[t], done[t] & 1);
-                    if (!ok) break;
-                    tc_fence_after();
-                    const uint32_t id = idesc_bf16_f32_mn(BM, D, false, true);
-                    const uint64_t dv = tile_desc_mn(kv_s + vs * L::TILE, 128, 0);
-                    const int steps = x.width(it) >> 4;
-                    for (int ks = 0; ks < steps; ++ks)
-                        mma_bf16_ta(tmem + kO + t * 128, tmem + kS + t * BN + 8 * ks,
-                                    mndesc_step(dv, ks), id, done[t] > 0 || ks > 0);
-                    ++done[t];
-                    if (t == 1 || !act[1]) mma_commit(&bars->empty[vs]);
-                    const int nx = x.next(t, it + 1, a);
-                    if (nx < x.n) scores(t, nx);
-                    else mma_commit(&bars->ofull[t]);
-                }
-            }
-            mma_commit(&bars->fin);
-            if (!mbar_wait(&bars->fin, 0)) ok = false;
+            for (int ks = 0; ks < D / 16; ++ks)
+                mma_bf16(s_t, kdesc_step(dq, 128, ks), kdesc_step(dk, 128, ks), id, ks > 0);
+            mma_commit(&bars->sfull[t]);
+            mma_commit(&bars->empty[s]);
+        };
+        int it = 0, done = 0;
+        for (; it < n && ok && !active(it); ++it) skip(it);
+        if (it < n && ok) {
+            ok = __all_sync(0xffffffffu, mbar_wait(&bars->qfull[t], 0)) && stage_wait(2 * it);
+            const int s = (2 * it) % L::NS;
+            if (lead && ok)
+                scores(it, s, tile_desc(kv_s + s * L::TILE, 128, 0, 0),
+                       idesc_bf16_f32(BM, width(it)) | g.negate);
+            __syncwarp();
         }
-    } else {
+        while (it < n && ok) {
+            int nx = it + 1;
+            for (; nx < n && ok && !active(nx); ++nx) skip(nx);
+            if (ok && nx < n) ok = stage_wait(2 * nx);
+            if (ok) ok = stage_wait(2 * it + 1);
+            const int sk = (2 * nx) % L::NS, sv = (2 * it + 1) % L::NS;
+            const uint64_t dk = tile_desc(kv_s + sk * L::TILE, 128, 0, 0),
+                           dv = tile_desc_mn(kv_s + sv * L::TILE, 128, 0);
+            const uint32_t id_s = idesc_bf16_f32(BM, width(nx)) | g.negate;
+            const int steps = width(it) >> 4;
+            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->pready[t], done & 1));
+            if (!ok) break;
+            tc_fence_after();
+            if (lead) {
+                if (steps == BN / 16) {
+#pragma unroll
+                    for (int ks = 0; ks < BN / 16; ++ks)
+                        mma_bf16_ta(o_t, s_t + 8 * ks, mndesc_step(dv, ks), id_o, ks > 0 || done > 0);
+                } else {
+                    for (int ks = 0; ks < steps; ++ks)
+                        mma_bf16_ta(o_t, s_t + 8 * ks, mndesc_step(dv, ks), id_o, ks > 0 || done > 0);
+                }
+                mma_commit(&bars->empty[sv]);
+                if (nx < n) scores(nx, sk, dk, id_s);
+                else mma_commit(&bars->ofull[t]);
+            }
+            __syncwarp();
+            ++done;
+            it = nx;
+        }
+        if (lead) mma_commit(&bars->fin[t]);
+        __syncwarp();
+        if (!mbar_wait(&bars->fin[t], 0)) ok = false;
+    } else if (warp < 8) {
         // ========================================= softmax, then the output
+        regs_up<kRegsSoftmax>();
         const int t = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + lanes + kS + t * BN, to = tmem + lanes + kO + t * 128;
+        const int sink_tiles = x.sink_tiles, act0 = x.act0[t], act1 = x.act1[t], all0 = x.all0[t],
+                  all1 = x.all1[t], n = x.rows[t] > 0 ? x.n : 0;
         const int p = x.p0[t] + row;
         const long long plo = (long long)p - a.window + 1;
         const int rlo = plo < 0 ? 0 : (int)plo;
         float m = -INFINITY, l = 0.f;
         int seen = 0;
-        for (int it = 0; it < x.n && ok; ++it) {
-            if (!x.active(t, it, a)) continue;
+        for (int it = 0; it < n && ok; ++it) {
+            if (it >= sink_tiles && (it < act0 || it >= act1)) continue;
             ok = __all_sync(0xffffffffu, mbar_wait(&bars->sfull[t], seen & 1));
             if (!ok) break;
             tc_fence_after();
-            const int nch = x.width(it) >> 5;
-            float s[4][32];
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch)
-                if (ch < nch) tmem_ld32(ts + 32 * ch, s[ch]);
-            tmem_ld_wait(s[0], s[1], s[2], s[3]);
-            if (!x.whole(t, it, a)) {
-                const int k0 = x.key0(it), hi = min(p, x.limit(it) - 1);
-#pragma unroll
-                for (int ch = 0; ch < 4; ++ch) {
-                    if (ch < nch) {
-                        const int kc = k0 + 32 * ch;
-                        const uint32_t keep = low_bits(hi + 1 - kc) &
-                                              (~low_bits(rlo - kc) | low_bits(a.sinks - kc));
-#pragma unroll
-                        for (int i = 0; i < 32; ++i)
-                            if (!((keep >> i) & 1u)) s[ch][i] = -INFINITY;
-                    }
-                }
-            }
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch)
-                if (ch < nch) {
-#pragma unroll
-                    for (int i = 0; i < 32; ++i) mx[i & 3] = fmaxf(mx[i & 3], s[ch][i]);
-                }
-            const float mn = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
-            const bool grow = mn > m && (m == -INFINITY || (mn - m) * g.c > 8.f);
-            // a row that has seen nothing yet has l = 0 and zeros in O (or O unset)
-            if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
-                const float f = grow && m != -INFINITY ? ex2((m - mn) * g.c) : 1.f;
-                l *= f;
+            // raise the maximum in use, rescaling the sum and O, where a row needs it
+            auto raise = [&](float mn) {
+                const bool grow = mn > m && (m == -INFINITY || (mn - m) * g.c > 8.f);
+                // a row that has seen nothing yet has l = 0 and zeros in O (or O unset)
+                if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
+                    const float f = grow && m != -INFINITY ? ex2((m - mn) * g.c) : 1.f;
+                    l *= f;
 #pragma unroll 1
-                for (int ch = 0; ch < D / 16; ++ch) {
-                    float v[16];
-                    tmem_ld16(to + 16 * ch, v);
-                    tmem_ld_wait(v);
-                    uint32_t r[16];
+                    for (int ch = 0; ch < D / 16; ++ch) {
+                        float v[16];
+                        tmem_ld16(to + 16 * ch, v);
+                        tmem_ld_wait(v);
+                        uint32_t r[16];
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i] * f);
-                    tmem_st16(to + 16 * ch, r);
+                        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i] * f);
+                        tmem_st16(to + 16 * ch, r);
+                    }
+                }
+                if (grow) m = mn;
+                return m == -INFINITY ? 0.f : -m * g.c;
+            };
+            float2 sum[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.f, 0.f);
+            const float2 c2 = make_float2(g.c, g.c);
+            // weights of 32 columns: P over the first half of the scores' place
+            auto weights = [&](int ch, const float (&s)[32], float2 b2) {
+                uint32_t r[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    float2 e = fma2(make_float2(s[2 * i], s[2 * i + 1]), c2, b2);
+                    e.x = ex2(e.x);
+                    e.y = ex2(e.y);
+                    sum[i & 3] = add2(sum[i & 3], e);
+                    r[i] = pack2(e.x, e.y);
+                }
+                tmem_st16(ts + 16 * ch, r);
+            };
+            auto top = [&](float (&mx)[4], const float (&s)[32]) {
+#pragma unroll
+                for (int i = 0; i < 32; i += 2)
+                    mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], s[i], s[i + 1]);
+            };
+            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+            if (it >= all0 && it < all1) {
+                float s[4][32];
+                tmem_ld32(ts, s[0]);
+                tmem_ld32(ts + 32, s[1]);
+                tmem_ld_wait(s[0], s[1]);
+                tmem_ld32(ts + 64, s[2]);
+                tmem_ld32(ts + 96, s[3]);
+                top(mx, s[0]);
+                top(mx, s[1]);
+                tmem_ld_wait(s[2], s[3]);
+                top(mx, s[2]);
+                top(mx, s[3]);
+                const float base = raise(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                const float2 b2 = make_float2(base, base);
+#pragma unroll
+                for (int ch = 0; ch < 4; ++ch) weights(ch, s[ch], b2);
+            } else {
+                // masked or narrow: the scores are read twice, 32 columns at a time
+                const int nch = x.width(it) >> 5;
+                const int k0 = x.key0(it), hi = min(p, x.limit(it) - 1);
+                auto mask = [&](int ch, float (&s)[32]) {
+                    const int kc = k0 + 32 * ch;
+                    const uint32_t keep =
+                        low_bits(hi + 1 - kc) & (~low_bits(rlo - kc) | low_bits(a.sinks - kc));
+#pragma unroll
+                    for (int i = 0; i < 32; ++i)
+                        if (!((keep >> i) & 1u)) s[i] = -INFINITY;
+                };
+#pragma unroll 1
+                for (int ch = 0; ch < nch; ++ch) {
+                    float s[32];
+                    tmem_ld32(ts + 32 * ch, s);
+                    tmem_ld_wait(s);
+                    mask(ch, s);
+                    top(mx, s);
+                }
+                const float base = raise(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                const float2 b2 = make_float2(base, base);
+#pragma unroll 1
+                for (int ch = 0; ch < nch; ++ch) {
+                    float s[32];
+                    tmem_ld32(ts + 32 * ch, s);
+                    tmem_ld_wait(s);
+                    mask(ch, s);
+                    weights(ch, s, b2);  // columns whose scores have been read
                 }
             }
-            if (grow) m = mn;
-            const float base = m == -INFINITY ? 0.f : m * g.c;
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int ch = 0; ch < 4; ++ch)
-                if (ch < nch) {
-                    uint32_t r[16];
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const float u = ex2(fmaf(s[ch][2 * i], g.c, -base)),
-                                    w = ex2(fmaf(s[ch][2 * i + 1], g.c, -base));
-                        sum[i & 1] += u;
-                        sum[2 + (i & 1)] += w;
-                        r[i] = pack2(u, w);
-                    }
-                    tmem_st16(ts + 16 * ch, r);
-                }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            const float2 two = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+            l += two.x + two.y;
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -507,6 +606,10 @@ cudaError_t launch(const WindowArgs &a, int slot, cudaStream_t stream) {
     g.pair_heads = (a.Hq / a.Hk) % 2 == 0;
     const int rows = g.pair_heads ? BM : 2 * BM;
     g.tiles = (a.Tq + rows - 1) / rows;
+    // keys and values of the heads in flight stay within 48 MB of the L2's 129
+    const long long kv = 4ll * D * a.Tk, pairs = (long long)a.B * (g.pair_heads ? a.Hq / 2 : a.Hq);
+    const long long span = (48ll << 20) / kv;
+    g.span = (int)(span < 1 ? 1 : (span < pairs ? span : pairs));
     const unsigned grid = (unsigned)(a.B * (g.pair_heads ? a.Hq / 2 : a.Hq) * g.tiles);
     window_tc_kernel<D><<<grid, NT, Layout<D>::ALLOC, stream>>>(mq, mk, mv, g);
     return cudaGetLastError();
