@@ -59,19 +59,22 @@ template <int D>
 struct Layout {
     static constexpr int KB = D > 64 ? 2 : 1;        // 64-column blocks of a tile
     static constexpr int TILE = KB * 128 * 128;      // bytes of a 128-row tile
-    static constexpr int NS = D > 64 ? 5 : 8;        // key and value tiles in flight
+    static constexpr int NS = D > 64 ? 4 : 8;        // key and value tiles in flight
     static constexpr int Q = 0;
     static constexpr int KV = 2 * TILE;
-    static constexpr int BAR = KV + NS * TILE;
-    static constexpr int ITEM = BAR + 256;           // struct Item
-    static constexpr int BYTES = ITEM + 256;
+    static constexpr int OUT = KV + NS * TILE;       // 2 KB per softmax warp: rows on their way out
+    static constexpr int CLC = OUT + 8 * 2048;       // answer to a request for work, 16 bytes
+    static constexpr int BAR = CLC + 16;
+    static constexpr int ITEM = BAR + 320;           // two of struct Item
+    static constexpr int BYTES = ITEM + 2 * 128;
     static constexpr int ALLOC = BYTES + 1024;
 };
 
 struct Barriers {
-    uint64_t qfull[2], sfull[2], pready[2], ofull[2], fin[2];
+    uint64_t qfull[2], qempty[2], sfull[2], pready[2][2], ofull[2], oempty[2], fin[2];
     uint64_t full[8], empty[8];
-    uint32_t tmem;
+    uint64_t ifull[2], iempty[2], clc, loaded;
+    uint32_t tmem, pipe;  // pipe: 1 while a warp issues products
 };
 
 constexpr uint32_t kS = 0, kO = 256;  // TMEM columns: S0, S1 (P over them), then O0, O1
@@ -157,6 +160,20 @@ __device__ __forceinline__ bool elect_one() {
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
     return p != 0;
 }
+// The tensor pipe for one warp's products at a time: two warps that issue
+// together would both finish late, and their softmaxes then run together too,
+// with the pipe idle.  A hint for the order, not a lock: after the limit the
+// warp goes on, which changes no result.
+__device__ __forceinline__ void take_pipe(uint32_t *flag) {
+    for (int i = 0; i < 4096; ++i) {
+        uint32_t old;
+        asm volatile("atom.acquire.cta.shared::cta.exch.b32 %0, [%1], 1;" : "=r"(old) : "r"(smem_u32(flag)) : "memory");
+        if (!old) break;
+    }
+}
+__device__ __forceinline__ void free_pipe(uint32_t *flag) {
+    asm volatile("st.release.cta.shared::cta.b32 [%0], 0;" ::"r"(smem_u32(flag)) : "memory");
+}
 // Register shares of the warpgroups (all four warps execute these).
 template <int N> __device__ __forceinline__ void regs_up() {
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
@@ -169,7 +186,7 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
     return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
 }
 
-// What a CTA works on, kept in shared memory.  Key
+// A piece of work, kept in shared memory.  Key
 // tile `it` is a sink tile (it < sink_tiles) or window tile it - sink_tiles.
 // Sink tiles lie before the window of every row, so all rows see their keys.
 // Window tiles that query tile t needs form one run [act0, act1), those that
@@ -178,7 +195,9 @@ struct Item {
     int b, hk, head[2], i0[2];  // first row of each query tile
     int rows[2], p0[2];         // valid rows, position of the first
     int act0[2], act1[2], all0[2], all1[2];
+    int last[2];                // last key tile that the query tile needs, -1: none
     int kl, sink_keys, sink_tiles, lo, hi, n;
+    int valid;                  // 0: no work is left
 
     __device__ __forceinline__ int key0(int it) const {
         return it < sink_tiles ? it * BN : lo + (it - sink_tiles) * BN;
@@ -236,8 +255,35 @@ __device__ __forceinline__ Item make_item(const TcArgs &g, int block, bool *bad)
         x.all0[t] = f > 0 ? (int)min((long long)x.n, x.sink_tiles + (f + BN - 1) / BN) : x.sink_tiles;
         const long long e = min((long long)x.hi, p + 1) - lo;
         x.all1[t] = x.sink_tiles + (e > 0 ? (int)(e / BN) : 0);
+        x.last[t] = x.rows[t] == 0 ? -1 : (x.act1[t] > x.act0[t] ? x.act1[t] : x.sink_tiles) - 1;
     }
     return x;
+}
+
+static_assert(sizeof(Item) <= 128 && sizeof(Barriers) <= 320, "shared memory layout");
+
+// Ask for the index of a block that has not started, to do its work here; the
+// answer (16 bytes at `dst`) is counted on `bar`.
+__device__ __forceinline__ void request_block(void *dst, uint64_t *bar) {
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            smem_u32(dst)),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+// The index in the answer, -1 where no block was left.
+__device__ __forceinline__ int granted_block(const void *src) {
+    uint32_t got, x;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t.reg .b32 y, z, w;\n\t"
+        "ld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, w}, h;\n\t}"
+        : "=r"(got), "=r"(x)
+        : "r"(smem_u32(src))
+        : "memory");
+    return got ? (int)x : -1;
 }
 
 template <int D>
@@ -248,21 +294,26 @@ __global__ void __launch_bounds__(NT, 1)
     extern __shared__ uint8_t raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     Barriers *bars = reinterpret_cast<Barriers *>(sm + L::BAR);
+    Item *items = reinterpret_cast<Item *>(sm + L::ITEM);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const WindowArgs &a = g.w;
 
-    Item &x = *reinterpret_cast<Item *>(sm + L::ITEM);
     if (tid == 0) {
-        bool bad = false;
-        x = make_item(g, blockIdx.x, &bad);
-        if (bad) atomicOr(&g_wtc_error, kAttnIndex);
         for (int t = 0; t < 2; ++t) {
             mbar_init(&bars->qfull[t], 1);
+            mbar_init(&bars->qempty[t], 1);
             mbar_init(&bars->sfull[t], 1);
-            mbar_init(&bars->pready[t], 4);
+            mbar_init(&bars->pready[t][0], 4);  // the first 64 columns of P
+            mbar_init(&bars->pready[t][1], 4);  // the others
             mbar_init(&bars->ofull[t], 1);
+            mbar_init(&bars->oempty[t], 4);
             mbar_init(&bars->fin[t], 1);
+            mbar_init(&bars->ifull[t], 1);
+            mbar_init(&bars->iempty[t], 11);  // softmax, product and load warps
         }
+        bars->pipe = 0;
+        mbar_init(&bars->clc, 1);
+        mbar_init(&bars->loaded, 1);
         for (int s = 0; s < L::NS; ++s) {
             mbar_init(&bars->full[s], 1);
             mbar_init(&bars->empty[s], 2);  // both query tiles
@@ -279,32 +330,88 @@ __global__ void __launch_bounds__(NT, 1)
     const uint32_t tmem = bars->tmem;
     bool ok = true;
 
+    // A role's next piece of work (whole warp); null at the end or on a wait that gave up.
+    int piece = 0;
+    auto take = [&]() -> const Item * {
+        ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars->ifull[piece & 1], (piece >> 1) & 1));
+        return ok && items[piece & 1].valid ? &items[piece & 1] : nullptr;
+    };
+    auto give_back = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->iempty[piece & 1]);
+        ++piece;
+    };
+
     if (warp >= 8) regs_down<kRegsOther>();
-    if (warp == 10) {
-        // ============================================================ loads
+    if (warp == 11) {
+        // ==================================================== pieces of work
+        // The block's own, then those of blocks that have not started: the
+        // grid holds one block per piece, longest first, and each running CTA
+        // takes the next one once the loads of its last have been issued (not
+        // at once, or blocks that are about to start would be taken from idle
+        // SMs).
         if (lane == 0) {
-            for (int t = 0; t < 2; ++t) {
-                if (x.rows[t] == 0) continue;
-                mbar_expect_tx(&bars->qfull[t], L::TILE);
-                for (int kb = 0; kb < L::KB; ++kb)
-                    tma_load_4d(sm + L::Q + t * L::TILE + kb * 16384, &tmq, kb * 64, x.i0[t],
-                                x.head[t], x.b, &bars->qfull[t]);
-            }
-            int seq = 0;
-            for (int it = 0; it < x.n && ok; ++it) {
-                for (int kv = 0; kv < 2 && ok; ++kv, ++seq) {
-                    const int s = seq % L::NS;
-                    if (seq >= L::NS) ok = mbar_wait(&bars->empty[s], (seq / L::NS - 1) & 1);
+            int block = blockIdx.x;
+            for (int i = 0; ok; ++i) {
+                if (i >= 2) ok = mbar_wait(&bars->iempty[i & 1], ((i >> 1) - 1) & 1);
+                if (!ok) break;
+                if (i > 0) {
+                    ok = mbar_wait(&bars->loaded, (i - 1) & 1);
                     if (!ok) break;
-                    mbar_expect_tx(&bars->full[s], L::TILE);
-                    for (int kb = 0; kb < L::KB; ++kb)
-                        tma_load_4d(sm + L::KV + s * L::TILE + kb * 16384, kv ? &tmv : &tmk, kb * 64,
-                                    x.key0(it), x.hk, x.b, &bars->full[s]);
+                    fence_async_smem();  // the last answer was read
+                    mbar_expect_tx(&bars->clc, 16);
+                    request_block(sm + L::CLC, &bars->clc);
+                    ok = mbar_wait(&bars->clc, (i - 1) & 1);
+                    if (!ok) break;
+                    block = granted_block(sm + L::CLC);
                 }
+                Item &x = items[i & 1];
+                if (block >= 0) {
+                    bool bad = false;
+                    x = make_item(g, block, &bad);
+                    if (bad) atomicOr(&g_wtc_error, kAttnIndex);
+                }
+                x.valid = block >= 0;
+                mbar_arrive(&bars->ifull[i & 1]);
+                if (block < 0) break;
             }
-            // never leave with copies into shared memory in flight
+        }
+    } else if (warp == 10) {
+        // ============================================================ loads
+        int seq = 0, used[2] = {0, 0};
+        while (const Item *px = take()) {
+            const Item &x = *px;
+            if (lane == 0) {
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (x.last[t] < 0) continue;
+                    if (used[t] > 0) ok = mbar_wait(&bars->qempty[t], (used[t] - 1) & 1);
+                    if (!ok) break;
+                    ++used[t];
+                    mbar_expect_tx(&bars->qfull[t], L::TILE);
+                    for (int kb = 0; kb < L::KB; ++kb)
+                        tma_load_4d(sm + L::Q + t * L::TILE + kb * 16384, &tmq, kb * 64, x.i0[t],
+                                    x.head[t], x.b, &bars->qfull[t]);
+                }
+                for (int it = 0; it < x.n && ok; ++it) {
+                    const int k0 = x.key0(it);
+                    for (int kv = 0; kv < 2 && ok; ++kv, ++seq) {
+                        const int s = seq % L::NS;
+                        if (seq >= L::NS) ok = mbar_wait(&bars->empty[s], (seq / L::NS - 1) & 1);
+                        if (!ok) break;
+                        mbar_expect_tx(&bars->full[s], L::TILE);
+                        for (int kb = 0; kb < L::KB; ++kb)
+                            tma_load_4d(sm + L::KV + s * L::TILE + kb * 16384, kv ? &tmv : &tmk,
+                                        kb * 64, k0, x.hk, x.b, &bars->full[s]);
+                    }
+                }
+                mbar_arrive(&bars->loaded);
+            }
+            give_back();
+        }
+        // never leave with copies into shared memory in flight
+        if (lane == 0) {
             for (int t = 0; t < 2; ++t)
-                if (x.rows[t] > 0 && !mbar_wait(&bars->qfull[t], 0)) ok = false;
+                if (used[t] > 0 && !mbar_wait(&bars->qfull[t], (used[t] - 1) & 1)) ok = false;
             for (int i = max(0, seq - L::NS); i < seq; ++i)
                 if (!mbar_wait(&bars->full[i % L::NS], (i / L::NS) & 1)) ok = false;
         }
@@ -314,73 +421,108 @@ __global__ void __launch_bounds__(NT, 1)
         // lane issues.  What a step needs is worked out before its wait for P,
         // so that the products of a step follow the wait at once.
         const int t = warp - 8;
-        const bool has = x.rows[t] > 0;
-        const int n = x.n, sink_tiles = x.sink_tiles, act0 = has ? x.act0[t] : n, act1 = has ? x.act1[t] : n;
-        const int w_last = x.width(n - 1), w_sink = sink_tiles ? x.width(sink_tiles - 1) : BN;
         const uint32_t q_s = smem_u32(sm + L::Q) + t * L::TILE, kv_s = smem_u32(sm + L::KV);
         const uint32_t s_t = tmem + kS + t * BN, o_t = tmem + kO + t * 128;
         const uint32_t id_o = idesc_bf16_f32_mn(BM, D, false, true);
         const uint64_t dq = tile_desc(q_s, 128, 0, 0);
         const bool lead = elect_one();
-        auto active = [&](int it) { return has && (it < sink_tiles || (it >= act0 && it < act1)); };
-        auto width = [&](int it) { return it == n - 1 ? w_last : (it == sink_tiles - 1 ? w_sink : BN); };
+        int seq0 = 0;   // stages of earlier pieces
+        int done = 0;   // key tiles multiplied
+        int used = 0;   // pieces with any
         auto stage_wait = [&](int seq) {
             return __all_sync(0xffffffffu, mbar_wait(&bars->full[seq % L::NS], (seq / L::NS) & 1));
         };
-        // a tile that the query tile skips: its stages are free for it once loaded
-        auto skip = [&](int it) {
-            for (int kv = 0; kv < 2 && ok; ++kv) {
-                ok = stage_wait(2 * it + kv);
-                if (lead && ok) mbar_arrive(&bars->empty[(2 * it + kv) % L::NS]);
-            }
-        };
-        // S = Q K(it)^T
-        auto scores = [&](int it, int s, uint64_t dk, uint32_t id) {
-#pragma unroll
-            for (int ks = 0; ks < D / 16; ++ks)
-                mma_bf16(s_t, kdesc_step(dq, 128, ks), kdesc_step(dk, 128, ks), id, ks > 0);
-            mma_commit(&bars->sfull[t]);
-            mma_commit(&bars->empty[s]);
-        };
-        int it = 0, done = 0;
-        for (; it < n && ok && !active(it); ++it) skip(it);
-        if (it < n && ok) {
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars->qfull[t], 0)) && stage_wait(2 * it);
-            const int s = (2 * it) % L::NS;
-            if (lead && ok)
-                scores(it, s, tile_desc(kv_s + s * L::TILE, 128, 0, 0),
-                       idesc_bf16_f32(BM, width(it)) | g.negate);
-            __syncwarp();
-        }
-        while (it < n && ok) {
-            int nx = it + 1;
-            for (; nx < n && ok && !active(nx); ++nx) skip(nx);
-            if (ok && nx < n) ok = stage_wait(2 * nx);
-            if (ok) ok = stage_wait(2 * it + 1);
-            const int sk = (2 * nx) % L::NS, sv = (2 * it + 1) % L::NS;
-            const uint64_t dk = tile_desc(kv_s + sk * L::TILE, 128, 0, 0),
-                           dv = tile_desc_mn(kv_s + sv * L::TILE, 128, 0);
-            const uint32_t id_s = idesc_bf16_f32(BM, width(nx)) | g.negate;
-            const int steps = width(it) >> 4;
-            if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->pready[t], done & 1));
-            if (!ok) break;
-            tc_fence_after();
-            if (lead) {
-                if (steps == BN / 16) {
-#pragma unroll
-                    for (int ks = 0; ks < BN / 16; ++ks)
-                        mma_bf16_ta(o_t, s_t + 8 * ks, mndesc_step(dv, ks), id_o, ks > 0 || done > 0);
-                } else {
-                    for (int ks = 0; ks < steps; ++ks)
-                        mma_bf16_ta(o_t, s_t + 8 * ks, mndesc_step(dv, ks), id_o, ks > 0 || done > 0);
+        while (const Item *px = take()) {
+            const Item &x = *px;
+            const int n = x.n, sink_tiles = x.sink_tiles, act0 = x.act0[t], act1 = x.act1[t], last = x.last[t];
+            const int w_last = n > 0 ? x.width(n - 1) : 0, w_sink = sink_tiles ? x.width(sink_tiles - 1) : BN;
+            auto active = [&](int it) {
+                return last >= 0 && (it < sink_tiles || (it >= act0 && it < act1));
+            };
+            auto width = [&](int it) { return it == n - 1 ? w_last : (it == sink_tiles - 1 ? w_sink : BN); };
+            // a tile that the query tile skips: its stages are free for it once loaded
+            auto skip = [&](int it) {
+                for (int kv = 0; kv < 2 && ok; ++kv) {
+                    const int seq = seq0 + 2 * it + kv;
+                    ok = stage_wait(seq);
+                    if (lead && ok) mbar_arrive(&bars->empty[seq % L::NS]);
                 }
-                mma_commit(&bars->empty[sv]);
-                if (nx < n) scores(nx, sk, dk, id_s);
-                else mma_commit(&bars->ofull[t]);
+            };
+            // S = Q K(it)^T
+            auto scores = [&](int it, int s, uint64_t dk, uint32_t id) {
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_bf16(s_t, kdesc_step(dq, 128, ks), kdesc_step(dk, 128, ks), id, ks > 0);
+                mma_commit(&bars->sfull[t]);
+                mma_commit(&bars->empty[s]);
+                if (it == last) mma_commit(&bars->qempty[t]);
+            };
+            int it = 0;
+            for (; it < n && ok && !active(it); ++it) skip(it);
+            if (it < n && ok) {
+                const int seq = seq0 + 2 * it, s = seq % L::NS;
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars->qfull[t], used & 1)) && stage_wait(seq);
+                if (lead && ok)
+                    scores(it, s, tile_desc(kv_s + s * L::TILE, 128, 0, 0),
+                           idesc_bf16_f32(BM, width(it)) | g.negate);
+                __syncwarp();
             }
-            __syncwarp();
-            ++done;
-            it = nx;
+            bool first = true;
+            while (it < n && ok) {
+                int nx = it + 1;
+                for (; nx < n && ok && !active(nx); ++nx) skip(nx);
+                if (ok && nx < n) ok = stage_wait(seq0 + 2 * nx);
+                if (ok) ok = stage_wait(seq0 + 2 * it + 1);
+                const int sk = (seq0 + 2 * nx) % L::NS, sv = (seq0 + 2 * it + 1) % L::NS;
+                const uint64_t dk = tile_desc(kv_s + sk * L::TILE, 128, 0, 0),
+                               dv = tile_desc_mn(kv_s + sv * L::TILE, 128, 0);
+                const uint32_t id_s = idesc_bf16_f32(BM, width(nx)) | g.negate;
+                const int steps = width(it) >> 4;
+                // the last piece's output has left O
+                if (ok && first && used > 0)
+                    ok = __all_sync(0xffffffffu, mbar_wait(&bars->oempty[t], (used - 1) & 1));
+                if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->pready[t][0], done & 1));
+                if (!ok) break;
+                tc_fence_after();
+                // O += P V, 64 keys at a time as P comes
+                if (lead) {
+                    take_pipe(&bars->pipe);
+                    const int h = min(steps, 4);
+                    if (h == 4) {
+#pragma unroll
+                        for (int ks = 0; ks < 4; ++ks)
+                            mma_bf16_ta(o_t, s_t + 8 * ks, mndesc_step(dv, ks), id_o, ks > 0 || !first);
+                    } else {
+                        for (int ks = 0; ks < h; ++ks)
+                            mma_bf16_ta(o_t, s_t + 8 * ks, mndesc_step(dv, ks), id_o, ks > 0 || !first);
+                    }
+                }
+                __syncwarp();
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars->pready[t][1], done & 1));
+                if (!ok) break;
+                tc_fence_after();
+                if (lead) {
+                    if (steps == BN / 16) {
+#pragma unroll
+                        for (int ks = 4; ks < BN / 16; ++ks)
+                            mma_bf16_ta(o_t, s_t + 8 * ks, mndesc_step(dv, ks), id_o, 1);
+                    } else {
+                        for (int ks = 4; ks < steps; ++ks)
+                            mma_bf16_ta(o_t, s_t + 8 * ks, mndesc_step(dv, ks), id_o, 1);
+                    }
+                    mma_commit(&bars->empty[sv]);
+                    if (nx < n) scores(nx, sk, dk, id_s);
+                    else mma_commit(&bars->ofull[t]);
+                    free_pipe(&bars->pipe);
+                }
+                __syncwarp();
+                first = false;
+                ++done;
+                it = nx;
+            }
+            if (!first) ++used;
+            seq0 += 2 * n;
+            give_back();
         }
         if (lead) mma_commit(&bars->fin[t]);
         __syncwarp();
@@ -391,161 +533,196 @@ __global__ void __launch_bounds__(NT, 1)
         const int t = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
         const uint32_t ts = tmem + lanes + kS + t * BN, to = tmem + lanes + kO + t * 128;
-        const int sink_tiles = x.sink_tiles, act0 = x.act0[t], act1 = x.act1[t], all0 = x.all0[t],
-                  all1 = x.all1[t], n = x.rows[t] > 0 ? x.n : 0;
-        const int p = x.p0[t] + row;
-        const long long plo = (long long)p - a.window + 1;
-        const int rlo = plo < 0 ? 0 : (int)plo;
-        float m = -INFINITY, l = 0.f;
-        int seen = 0;
-        for (int it = 0; it < n && ok; ++it) {
-            if (it >= sink_tiles && (it < act0 || it >= act1)) continue;
-            ok = __all_sync(0xffffffffu, mbar_wait(&bars->sfull[t], seen & 1));
-            if (!ok) break;
-            tc_fence_after();
-            // raise the maximum in use, rescaling the sum and O, where a row needs it
-            auto raise = [&](float mn) {
-                const bool grow = mn > m && (m == -INFINITY || (mn - m) * g.c > 8.f);
-                // a row that has seen nothing yet has l = 0 and zeros in O (or O unset)
-                if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
-                    const float f = grow && m != -INFINITY ? ex2((m - mn) * g.c) : 1.f;
-                    l *= f;
+        const float2 c2 = make_float2(g.c, g.c);
+        int seen = 0, used = 0;
+        while (const Item *px = take()) {
+            const Item &x = *px;
+            const int sink_tiles = x.sink_tiles, act0 = x.act0[t], all0 = x.all0[t],
+                      all1 = x.all1[t], n = x.last[t] + 1;
+            const int p = x.p0[t] + row;
+            const long long plo = (long long)p - a.window + 1;
+            const int rlo = plo < 0 ? 0 : (int)plo;
+            float m = -INFINITY, l = 0.f;
+            for (int it = 0; it < n && ok; ++it) {
+                if (it >= sink_tiles && it < act0) continue;
+                const bool whole = it >= all0 && it < all1;
+                const int k0 = x.key0(it), end = min(p + 1, x.limit(it)), nch = x.width(it) >> 5;
+                ok = __all_sync(0xffffffffu, mbar_wait(&bars->sfull[t], seen & 1));
+                if (!ok) break;
+                tc_fence_after();
+                // raise the maximum in use, rescaling the sum and O, where a row needs it
+                auto raise = [&](float mn) {
+                    const bool grow = mn > m && (m == -INFINITY || (mn - m) * g.c > 8.f);
+                    // a row that has seen nothing yet has l = 0 and zeros in O (or O unset)
+                    if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
+                        const float f = grow && m != -INFINITY ? ex2((m - mn) * g.c) : 1.f;
+                        l *= f;
 #pragma unroll 1
-                    for (int ch = 0; ch < D / 16; ++ch) {
-                        float v[16];
-                        tmem_ld16(to + 16 * ch, v);
-                        tmem_ld_wait(v);
-                        uint32_t r[16];
+                        for (int ch = 0; ch < D / 16; ++ch) {
+                            float v[16];
+                            tmem_ld16(to + 16 * ch, v);
+                            tmem_ld_wait(v);
+                            uint32_t r[16];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i] * f);
-                        tmem_st16(to + 16 * ch, r);
+                            for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i] * f);
+                            tmem_st16(to + 16 * ch, r);
+                        }
                     }
-                }
-                if (grow) m = mn;
-                return m == -INFINITY ? 0.f : -m * g.c;
-            };
-            float2 sum[4];
+                    if (grow) m = mn;
+                    return m == -INFINITY ? 0.f : -m * g.c;
+                };
+                float2 sum[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.f, 0.f);
-            const float2 c2 = make_float2(g.c, g.c);
-            // weights of 32 columns: P over the first half of the scores' place
-            auto weights = [&](int ch, const float (&s)[32], float2 b2) {
-                uint32_t r[16];
+                for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.f, 0.f);
+                // weights of 32 columns: P over the first half of the scores' place
+                auto weights = [&](int ch, const float (&s)[32], float2 b2) {
+                    uint32_t r[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    float2 e = fma2(make_float2(s[2 * i], s[2 * i + 1]), c2, b2);
-                    e.x = ex2(e.x);
-                    e.y = ex2(e.y);
-                    sum[i & 3] = add2(sum[i & 3], e);
-                    r[i] = pack2(e.x, e.y);
-                }
-                tmem_st16(ts + 16 * ch, r);
-            };
-            auto top = [&](float (&mx)[4], const float (&s)[32]) {
+                    for (int i = 0; i < 16; ++i) {
+                        float2 e = fma2(make_float2(s[2 * i], s[2 * i + 1]), c2, b2);
+                        e.x = ex2(e.x);
+                        e.y = ex2(e.y);
+                        sum[i & 3] = add2(sum[i & 3], e);
+                        r[i] = pack2(e.x, e.y);
+                    }
+                    tmem_st16(ts + 16 * ch, r);
+                };
+                auto top = [&](float (&mx)[4], const float (&s)[32]) {
 #pragma unroll
-                for (int i = 0; i < 32; i += 2)
-                    mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], s[i], s[i + 1]);
-            };
-            float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-            if (it >= all0 && it < all1) {
-                float s[4][32];
-                tmem_ld32(ts, s[0]);
-                tmem_ld32(ts + 32, s[1]);
-                tmem_ld_wait(s[0], s[1]);
-                tmem_ld32(ts + 64, s[2]);
-                tmem_ld32(ts + 96, s[3]);
-                top(mx, s[0]);
-                top(mx, s[1]);
-                tmem_ld_wait(s[2], s[3]);
-                top(mx, s[2]);
-                top(mx, s[3]);
-                const float base = raise(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-                const float2 b2 = make_float2(base, base);
-#pragma unroll
-                for (int ch = 0; ch < 4; ++ch) weights(ch, s[ch], b2);
-            } else {
-                // masked or narrow: the scores are read twice, 32 columns at a time
-                const int nch = x.width(it) >> 5;
-                const int k0 = x.key0(it), hi = min(p, x.limit(it) - 1);
+                    for (int i = 0; i < 32; i += 2)
+                        mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], s[i], s[i + 1]);
+                };
                 auto mask = [&](int ch, float (&s)[32]) {
                     const int kc = k0 + 32 * ch;
                     const uint32_t keep =
-                        low_bits(hi + 1 - kc) & (~low_bits(rlo - kc) | low_bits(a.sinks - kc));
+                        low_bits(end - kc) & (~low_bits(rlo - kc) | low_bits(a.sinks - kc));
 #pragma unroll
                     for (int i = 0; i < 32; ++i)
                         if (!((keep >> i) & 1u)) s[i] = -INFINITY;
                 };
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+                auto publish = [&](int half) {
+                    tmem_st_wait();
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->pready[t][half]);
+                };
+                if (whole) {
+                    float s[4][32];
+                    tmem_ld32(ts, s[0]);
+                    tmem_ld32(ts + 32, s[1]);
+                    tmem_ld_wait(s[0], s[1]);
+                    tmem_ld32(ts + 64, s[2]);
+                    tmem_ld32(ts + 96, s[3]);
+                    top(mx, s[0]);
+                    top(mx, s[1]);
+                    tmem_ld_wait(s[2], s[3]);
+                    top(mx, s[2]);
+                    top(mx, s[3]);
+                    const float base = raise(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                    const float2 b2 = make_float2(base, base);
+                    weights(0, s[0], b2);
+                    weights(1, s[1], b2);
+                    publish(0);
+                    weights(2, s[2], b2);
+                    weights(3, s[3], b2);
+                    publish(1);
+                } else {
+                    // a masked or narrow tile, rare: the scores are read twice, 32
+                    // columns at a time, in little code (rarely run code comes
+                    // from far: unrolled it took longer)
 #pragma unroll 1
-                for (int ch = 0; ch < nch; ++ch) {
-                    float s[32];
-                    tmem_ld32(ts + 32 * ch, s);
-                    tmem_ld_wait(s);
-                    mask(ch, s);
-                    top(mx, s);
-                }
-                const float base = raise(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-                const float2 b2 = make_float2(base, base);
+                    for (int ch = 0; ch < nch; ++ch) {
+                        float s[32];
+                        tmem_ld32(ts + 32 * ch, s);
+                        tmem_ld_wait(s);
+                        mask(ch, s);
+                        top(mx, s);
+                    }
+                    const float base = raise(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                    const float2 b2 = make_float2(base, base);
 #pragma unroll 1
-                for (int ch = 0; ch < nch; ++ch) {
-                    float s[32];
-                    tmem_ld32(ts + 32 * ch, s);
-                    tmem_ld_wait(s);
-                    mask(ch, s);
-                    weights(ch, s, b2);  // columns whose scores have been read
+                    for (int ch = 0; ch < nch; ++ch) {
+                        float s[32];
+                        tmem_ld32(ts + 32 * ch, s);
+                        tmem_ld_wait(s);
+                        mask(ch, s);
+                        weights(ch, s, b2);  // columns whose scores have been read
+                        if (ch == 1) publish(0);
+                    }
+                    if (nch < 2) publish(0);
+                    publish(1);
                 }
+                const float2 two = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+                l += two.x + two.y;
+                ++seen;
             }
-            const float2 two = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
-            l += two.x + two.y;
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bars->pready[t]);
-            ++seen;
-        }
-        const bool live = row < x.rows[t];
-        if (seen > 0 && ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->ofull[t], 0));
-        tc_fence_after();
-        if (ok) {
-            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + x.b * a.os.b +
-                               x.head[t] * a.os.h + (long long)(x.i0[t] + row) * a.os.t;
+            const int rows = x.rows[t], i0 = x.i0[t], b = x.b, hk = x.hk, kl = x.kl, p0 = x.p0[t];
+            const bool any = n > 0, live = row < rows;
+            __nv_bfloat16 *ot = static_cast<__nv_bfloat16 *>(a.o) + b * a.os.b + x.head[t] * a.os.h +
+                                (long long)i0 * a.os.t;
+            const __nv_bfloat16 *qt = static_cast<const __nv_bfloat16 *>(a.q) + b * a.qs.b +
+                                      x.head[t] * a.qs.h + (long long)i0 * a.qs.t;
+            give_back();
+            if (any) {
+                if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->ofull[t], used & 1));
+                ++used;
+            }
+            if (!ok) break;
+            tc_fence_after();
             const float inv = l == 0.f ? 0.f : 1.f / l;  // no key, or only scores of -inf
-            bool finite = true;
-#pragma unroll
+            // Rows leave through the warp's shared memory, 32 channels at a time,
+            // so that a store writes whole 64-byte pieces of eight rows (with a
+            // row per lane it touched 32 lines at once).
+            uint8_t *out = sm + L::OUT + warp * 2048;
+            const int w0 = 32 * (warp & 3);
+            float odd = 0.f;  // NaN once a value is not finite
+#pragma unroll 1
             for (int ch = 0; ch < D / 32; ++ch) {
                 float v[32];
-                if (seen > 0) {
+                if (any) {
                     tmem_ld32(to + 32 * ch, v);
                     tmem_ld_wait(v);
+                    if (ch == D / 32 - 1) {  // O has been read
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bars->oempty[t]);
+                    }
                 }
-                uint4 r[4];
-                uint32_t *w = reinterpret_cast<uint32_t *>(r);
+                uint32_t w[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float y0 = seen > 0 ? v[2 * i] * inv : 0.f,
-                                y1 = seen > 0 ? v[2 * i + 1] * inv : 0.f;
-                    finite = finite && isfinite(y0) && isfinite(y1);
+                    const float y0 = any ? v[2 * i] * inv : 0.f, y1 = any ? v[2 * i + 1] * inv : 0.f;
+                    odd = fmaf(y0, 0.f, fmaf(y1, 0.f, odd));
                     w[i] = pack2(y0, y1);
                 }
-                if (live) {
+                __syncwarp();  // the last piece has left
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(o + 32 * ch + 8 * i) = r[i];
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4 *>(out + lane * 64 + (i ^ ((lane >> 1) & 3)) * 16) =
+                        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int rr = 8 * i + (lane >> 2), c = lane & 3;
+                    const uint4 y = *reinterpret_cast<const uint4 *>(out + rr * 64 + (c ^ ((rr >> 1) & 3)) * 16);
+                    if (w0 + rr < rows)
+                        *reinterpret_cast<uint4 *>(ot + (w0 + rr) * a.os.t + 32 * ch + 8 * c) = y;
                 }
             }
-            unsigned again = __ballot_sync(0xffffffffu, live && !finite);
-            const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + x.b * a.qs.b +
-                                     x.head[t] * a.qs.h;
-            const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k) + x.b * a.ks.b + x.hk * a.ks.h;
-            const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + x.b * a.vs.b + x.hk * a.vs.h;
+            const bool finite = odd == 0.f;
             __syncwarp();
-            while (again) {
-                const int i = __ffs(again) - 1;
-                again &= again - 1;
-                const int r = 32 * (warp & 3) + i;
-                attn_row<__nv_bfloat16, D>(
-                    q + (long long)(x.i0[t] + r) * a.qs.t, k, v, a.ks.t, a.vs.t,
-                    static_cast<__nv_bfloat16 *>(a.o) + x.b * a.os.b + x.head[t] * a.os.h +
-                        (long long)(x.i0[t] + r) * a.os.t,
-                    seen_keys(x.p0[t] + r, x.kl, a.window, a.sinks), a.scale);
+            unsigned again = __ballot_sync(0xffffffffu, live && !finite);
+            if (again) {
+                const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k) + b * a.ks.b + hk * a.ks.h;
+                const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + b * a.vs.b + hk * a.vs.h;
+                __syncwarp();
+                while (again) {
+                    const int rr = 32 * (warp & 3) + __ffs(again) - 1;
+                    again &= again - 1;
+                    attn_row<__nv_bfloat16, D>(qt + rr * a.qs.t, k, v, a.ks.t, a.vs.t, ot + rr * a.os.t,
+                                               seen_keys(p0 + rr, kl, a.window, a.sinks), a.scale);
+                }
             }
         }
     }
