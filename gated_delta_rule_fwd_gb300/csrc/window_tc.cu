@@ -79,11 +79,34 @@ struct Barriers {
 
 constexpr uint32_t kS = 0, kO = 256;  // TMEM columns: S0, S1 (P over them), then O0, O1
 
+// mbar_wait in few instructions: the loop stays a loop.  The kernel has some
+// thirty waits, and code that does not fit the instruction cache costs it more
+// than anything else it does between two pieces of work.
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+        "mov.u32 n, %3;\n"
+        "again_%=:\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "@p bra done_%=;\n\t"
+        "sub.u32 n, n, 1;\n\t"
+        "setp.ne.u32 q, n, 0;\n\t"
+        "@q bra again_%=;\n"
+        "done_%=:\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_u32(bar)), "r"(parity), "n"(kSpinLimit)
+        : "memory");
+    return done != 0;
+}
+
 struct TcArgs {
     WindowArgs w;
     float c;          // |scale| log2 e, positive
     unsigned negate;  // idesc bit: scores of -Q (scale < 0)
     int pair_heads;   // the two query tiles are two heads, else consecutive rows
+    int group;        // query heads of a key head
     int tiles;        // row blocks of a head (pair)
     int span;         // heads (pairs) of all batches that are worked on together
 };
@@ -106,6 +129,19 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
         "r"(r[15])
+        : "memory");
+}
+// The same, 32 columns.
+__device__ __forceinline__ void tmem_st32(uint32_t taddr, const float (&v)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+        "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(taddr),
+        "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]),
+        "f"(v[8]), "f"(v[9]), "f"(v[10]), "f"(v[11]), "f"(v[12]), "f"(v[13]), "f"(v[14]), "f"(v[15]),
+        "f"(v[16]), "f"(v[17]), "f"(v[18]), "f"(v[19]), "f"(v[20]), "f"(v[21]), "f"(v[22]),
+        "f"(v[23]), "f"(v[24]), "f"(v[25]), "f"(v[26]), "f"(v[27]), "f"(v[28]), "f"(v[29]),
+        "f"(v[30]), "f"(v[31])
         : "memory");
 }
 __device__ __forceinline__ void tmem_st_wait() {
@@ -195,7 +231,7 @@ struct Item {
     int b, hk, head[2], i0[2];  // first row of each query tile
     int rows[2], p0[2];         // valid rows, position of the first
     int act0[2], act1[2], all0[2], all1[2];
-    int last[2];                // last key tile that the query tile needs, -1: none
+    int last[2];                // last key tile that the query tile needs, -1: no rows
     int kl, sink_keys, sink_tiles, lo, hi, n;
     int valid;                  // 0: no work is left
 
@@ -206,23 +242,22 @@ struct Item {
     // columns that the tile needs, a multiple of 32
     __device__ __forceinline__ int width(int it) const {
         const int w = limit(it) - key0(it);
-        return w >= BN ? BN : (w + 31) & ~31;
+        return w >= BN ? BN : (w < 32 ? 32 : (w + 31) & ~31);
     }
 };
 
-__device__ __forceinline__ Item make_item(const TcArgs &g, int block, bool *bad) {
+__device__ __forceinline__ void make_item(const TcArgs &g, int block, Item &x, bool *bad) {
     const WindowArgs &a = g.w;
-    Item x;
     const int groups = g.pair_heads ? a.Hq / 2 : a.Hq;
     // the last rows see the most keys: of the heads whose keys and values the
     // L2 cache holds together, all longest tiles start first
-    const int span = block / (g.span * g.tiles), in = block - span * g.span * g.tiles;
-    const int wide = min(g.span, a.B * groups - span * g.span);
-    const int tile = g.tiles - 1 - in / wide, bh = span * g.span + in % wide;
-    x.b = bh / groups;
-    const int gh = bh - x.b * groups;
-    const int ql = clamp_len(a.q_len, x.b, a.Tq, bad);
-    x.kl = clamp_len(a.k_len, x.b, a.Tk, bad);
+    const unsigned size = g.span * g.tiles, span = (unsigned)block / size, in = block - span * size;
+    const unsigned wide = min(g.span, a.B * groups - (int)span * g.span), deep = in / wide;
+    const int tile = g.tiles - 1 - (int)deep, bh = span * g.span + in - deep * wide;
+    const int batch = (unsigned)bh / (unsigned)groups, gh = bh - batch * groups;
+    x.b = batch;
+    const int ql = clamp_len(a.q_len, batch, a.Tq, bad), kl = clamp_len(a.k_len, batch, a.Tk, bad);
+    x.kl = kl;
     if (g.pair_heads) {
         x.head[0] = 2 * gh, x.head[1] = 2 * gh + 1;
         x.i0[0] = x.i0[1] = tile * BM;
@@ -230,34 +265,39 @@ __device__ __forceinline__ Item make_item(const TcArgs &g, int block, bool *bad)
         x.head[0] = x.head[1] = gh;
         x.i0[0] = tile * 2 * BM, x.i0[1] = x.i0[0] + BM;
     }
-    x.hk = x.head[0] / (a.Hq / a.Hk);
+    x.hk = (unsigned)x.head[0] / (unsigned)g.group;
 #pragma unroll
     for (int t = 0; t < 2; ++t) {
         x.rows[t] = max(0, min(BM, ql - x.i0[t]));
-        x.p0[t] = x.kl - ql + x.i0[t];
+        x.p0[t] = kl - ql + x.i0[t];
     }
     const int last = x.rows[1] > 0 ? x.p0[1] + x.rows[1] - 1 : x.p0[0] + x.rows[0] - 1;
-    const SeenKeys f = seen_keys(x.p0[0], x.kl, a.window, a.sinks),
-                   e = seen_keys(last, x.kl, a.window, a.sinks);
+    const SeenKeys f = seen_keys(x.p0[0], kl, a.window, a.sinks),
+                   e = seen_keys(last, kl, a.window, a.sinks);
     x.lo = f.lo, x.hi = e.hi;
     x.sink_keys = min(e.s1, f.lo);
     x.sink_tiles = (x.sink_keys + BN - 1) / BN;
     x.n = x.rows[0] > 0 ? x.sink_tiles + (x.hi > x.lo ? (x.hi - x.lo + BN - 1) / BN : 0) : 0;
-#pragma unroll
+#pragma unroll 1
     for (int t = 0; t < 2; ++t) {
-        const long long p = x.p0[t], lo = x.lo;
+        // positions and keys lie within +-2^30, so differences of two fit an int
+        const int p = x.p0[t], lo = x.lo, far = min(a.window, 1 << 30);
         // first key that the tile's first row sees; sinks inside the window tiles keep all
-        const long long k = a.sinks > x.lo ? lo : p - a.window + 1;
-        x.act0[t] = x.sink_tiles + (k > lo ? (int)((k - lo) / BN) : 0);
-        const long long last_p = p + x.rows[t] - 1;
-        x.act1[t] = min(x.n, last_p < lo ? x.sink_tiles : x.sink_tiles + (int)((last_p - lo) / BN) + 1);
-        const long long f = p + BM - a.window - lo;  // first key of the last row
-        x.all0[t] = f > 0 ? (int)min((long long)x.n, x.sink_tiles + (f + BN - 1) / BN) : x.sink_tiles;
-        const long long e = min((long long)x.hi, p + 1) - lo;
-        x.all1[t] = x.sink_tiles + (e > 0 ? (int)(e / BN) : 0);
+        const int k = a.sinks > lo ? 0 : p - far + 1 - lo;
+        x.act0[t] = x.sink_tiles + (max(k, 0) / BN);
+        const int last_p = p + x.rows[t] - 1 - lo;
+        x.act1[t] = min(x.n, x.sink_tiles + (last_p < 0 ? 0 : last_p / BN + 1));
+        const int f = p + BM - far - lo;  // first key of the last row
+        x.all0[t] = min(x.n, x.sink_tiles + (f > 0 ? (f + BN - 1) / BN : 0));
+        const int e = min(x.hi, p + 1) - lo;
+        x.all1[t] = x.sink_tiles + (e > 0 ? e / BN : 0);
+        if (x.rows[t] > 0 && x.sink_tiles == 0 && x.act1[t] <= x.act0[t]) {
+            // no key for any row: one tile with everything masked gives the zeros
+            x.n = max(x.n, 1);
+            x.act0[t] = 0, x.act1[t] = 1, x.all0[t] = x.all1[t] = 0;
+        }
         x.last[t] = x.rows[t] == 0 ? -1 : (x.act1[t] > x.act0[t] ? x.act1[t] : x.sink_tiles) - 1;
     }
-    return x;
 }
 
 static_assert(sizeof(Item) <= 128 && sizeof(Barriers) <= 320, "shared memory layout");
@@ -333,7 +373,7 @@ __global__ void __launch_bounds__(NT, 1)
     // A role's next piece of work (whole warp); null at the end or on a wait that gave up.
     int piece = 0;
     auto take = [&]() -> const Item * {
-        ok = __all_sync(0xffffffffu, ok && mbar_wait(&bars->ifull[piece & 1], (piece >> 1) & 1));
+        ok = __all_sync(0xffffffffu, ok && wait_bar(&bars->ifull[piece & 1], (piece >> 1) & 1));
         return ok && items[piece & 1].valid ? &items[piece & 1] : nullptr;
     };
     auto give_back = [&]() {
@@ -353,22 +393,22 @@ __global__ void __launch_bounds__(NT, 1)
         if (lane == 0) {
             int block = blockIdx.x;
             for (int i = 0; ok; ++i) {
-                if (i >= 2) ok = mbar_wait(&bars->iempty[i & 1], ((i >> 1) - 1) & 1);
+                if (i >= 2) ok = wait_bar(&bars->iempty[i & 1], ((i >> 1) - 1) & 1);
                 if (!ok) break;
                 if (i > 0) {
-                    ok = mbar_wait(&bars->loaded, (i - 1) & 1);
+                    ok = wait_bar(&bars->loaded, (i - 1) & 1);
                     if (!ok) break;
                     fence_async_smem();  // the last answer was read
                     mbar_expect_tx(&bars->clc, 16);
                     request_block(sm + L::CLC, &bars->clc);
-                    ok = mbar_wait(&bars->clc, (i - 1) & 1);
+                    ok = wait_bar(&bars->clc, (i - 1) & 1);
                     if (!ok) break;
                     block = granted_block(sm + L::CLC);
                 }
                 Item &x = items[i & 1];
                 if (block >= 0) {
                     bool bad = false;
-                    x = make_item(g, block, &bad);
+                    make_item(g, block, x, &bad);
                     if (bad) atomicOr(&g_wtc_error, kAttnIndex);
                 }
                 x.valid = block >= 0;
@@ -382,9 +422,10 @@ __global__ void __launch_bounds__(NT, 1)
         while (const Item *px = take()) {
             const Item &x = *px;
             if (lane == 0) {
+#pragma unroll 1
                 for (int t = 0; t < 2 && ok; ++t) {
                     if (x.last[t] < 0) continue;
-                    if (used[t] > 0) ok = mbar_wait(&bars->qempty[t], (used[t] - 1) & 1);
+                    if (used[t] > 0) ok = wait_bar(&bars->qempty[t], (used[t] - 1) & 1);
                     if (!ok) break;
                     ++used[t];
                     mbar_expect_tx(&bars->qfull[t], L::TILE);
@@ -392,11 +433,13 @@ __global__ void __launch_bounds__(NT, 1)
                         tma_load_4d(sm + L::Q + t * L::TILE + kb * 16384, &tmq, kb * 64, x.i0[t],
                                     x.head[t], x.b, &bars->qfull[t]);
                 }
+#pragma unroll 1
                 for (int it = 0; it < x.n && ok; ++it) {
                     const int k0 = x.key0(it);
+#pragma unroll 1
                     for (int kv = 0; kv < 2 && ok; ++kv, ++seq) {
                         const int s = seq % L::NS;
-                        if (seq >= L::NS) ok = mbar_wait(&bars->empty[s], (seq / L::NS - 1) & 1);
+                        if (seq >= L::NS) ok = wait_bar(&bars->empty[s], (seq / L::NS - 1) & 1);
                         if (!ok) break;
                         mbar_expect_tx(&bars->full[s], L::TILE);
                         for (int kb = 0; kb < L::KB; ++kb)
@@ -411,9 +454,9 @@ __global__ void __launch_bounds__(NT, 1)
         // never leave with copies into shared memory in flight
         if (lane == 0) {
             for (int t = 0; t < 2; ++t)
-                if (used[t] > 0 && !mbar_wait(&bars->qfull[t], (used[t] - 1) & 1)) ok = false;
+                if (used[t] > 0 && !wait_bar(&bars->qfull[t], (used[t] - 1) & 1)) ok = false;
             for (int i = max(0, seq - L::NS); i < seq; ++i)
-                if (!mbar_wait(&bars->full[i % L::NS], (i / L::NS) & 1)) ok = false;
+                if (!wait_bar(&bars->full[i % L::NS], (i / L::NS) & 1)) ok = false;
         }
     } else if (warp == 8 || warp == 9) {
         // ========================================================= products
@@ -430,7 +473,7 @@ __global__ void __launch_bounds__(NT, 1)
         int done = 0;   // key tiles multiplied
         int used = 0;   // pieces with any
         auto stage_wait = [&](int seq) {
-            return __all_sync(0xffffffffu, mbar_wait(&bars->full[seq % L::NS], (seq / L::NS) & 1));
+            return __all_sync(0xffffffffu, wait_bar(&bars->full[seq % L::NS], (seq / L::NS) & 1));
         };
         while (const Item *px = take()) {
             const Item &x = *px;
@@ -442,6 +485,7 @@ __global__ void __launch_bounds__(NT, 1)
             auto width = [&](int it) { return it == n - 1 ? w_last : (it == sink_tiles - 1 ? w_sink : BN); };
             // a tile that the query tile skips: its stages are free for it once loaded
             auto skip = [&](int it) {
+#pragma unroll 1
                 for (int kv = 0; kv < 2 && ok; ++kv) {
                     const int seq = seq0 + 2 * it + kv;
                     ok = stage_wait(seq);
@@ -458,10 +502,11 @@ __global__ void __launch_bounds__(NT, 1)
                 if (it == last) mma_commit(&bars->qempty[t]);
             };
             int it = 0;
+#pragma unroll 1
             for (; it < n && ok && !active(it); ++it) skip(it);
             if (it < n && ok) {
                 const int seq = seq0 + 2 * it, s = seq % L::NS;
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars->qfull[t], used & 1)) && stage_wait(seq);
+                ok = __all_sync(0xffffffffu, wait_bar(&bars->qfull[t], used & 1)) && stage_wait(seq);
                 if (lead && ok)
                     scores(it, s, tile_desc(kv_s + s * L::TILE, 128, 0, 0),
                            idesc_bf16_f32(BM, width(it)) | g.negate);
@@ -470,6 +515,7 @@ __global__ void __launch_bounds__(NT, 1)
             bool first = true;
             while (it < n && ok) {
                 int nx = it + 1;
+#pragma unroll 1
                 for (; nx < n && ok && !active(nx); ++nx) skip(nx);
                 if (ok && nx < n) ok = stage_wait(seq0 + 2 * nx);
                 if (ok) ok = stage_wait(seq0 + 2 * it + 1);
@@ -480,36 +526,26 @@ __global__ void __launch_bounds__(NT, 1)
                 const int steps = width(it) >> 4;
                 // the last piece's output has left O
                 if (ok && first && used > 0)
-                    ok = __all_sync(0xffffffffu, mbar_wait(&bars->oempty[t], (used - 1) & 1));
-                if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->pready[t][0], done & 1));
+                    ok = __all_sync(0xffffffffu, wait_bar(&bars->oempty[t], (used - 1) & 1));
+                if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bars->pready[t][0], done & 1));
                 if (!ok) break;
                 tc_fence_after();
                 // O += P V, 64 keys at a time as P comes
                 if (lead) {
                     take_pipe(&bars->pipe);
-                    const int h = min(steps, 4);
-                    if (h == 4) {
 #pragma unroll
-                        for (int ks = 0; ks < 4; ++ks)
+                    for (int ks = 0; ks < 4; ++ks)
+                        if (ks < steps)
                             mma_bf16_ta(o_t, s_t + 8 * ks, mndesc_step(dv, ks), id_o, ks > 0 || !first);
-                    } else {
-                        for (int ks = 0; ks < h; ++ks)
-                            mma_bf16_ta(o_t, s_t + 8 * ks, mndesc_step(dv, ks), id_o, ks > 0 || !first);
-                    }
                 }
                 __syncwarp();
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars->pready[t][1], done & 1));
+                ok = __all_sync(0xffffffffu, wait_bar(&bars->pready[t][1], done & 1));
                 if (!ok) break;
                 tc_fence_after();
                 if (lead) {
-                    if (steps == BN / 16) {
 #pragma unroll
-                        for (int ks = 4; ks < BN / 16; ++ks)
-                            mma_bf16_ta(o_t, s_t + 8 * ks, mndesc_step(dv, ks), id_o, 1);
-                    } else {
-                        for (int ks = 4; ks < steps; ++ks)
-                            mma_bf16_ta(o_t, s_t + 8 * ks, mndesc_step(dv, ks), id_o, 1);
-                    }
+                    for (int ks = 4; ks < BN / 16; ++ks)
+                        if (ks < steps) mma_bf16_ta(o_t, s_t + 8 * ks, mndesc_step(dv, ks), id_o, 1);
                     mma_commit(&bars->empty[sv]);
                     if (nx < n) scores(nx, sk, dk, id_s);
                     else mma_commit(&bars->ofull[t]);
@@ -526,7 +562,7 @@ __global__ void __launch_bounds__(NT, 1)
         }
         if (lead) mma_commit(&bars->fin[t]);
         __syncwarp();
-        if (!mbar_wait(&bars->fin[t], 0)) ok = false;
+        if (!wait_bar(&bars->fin[t], 0)) ok = false;
     } else if (warp < 8) {
         // ========================================= softmax, then the output
         regs_up<kRegsSoftmax>();
@@ -546,8 +582,8 @@ __global__ void __launch_bounds__(NT, 1)
             for (int it = 0; it < n && ok; ++it) {
                 if (it >= sink_tiles && it < act0) continue;
                 const bool whole = it >= all0 && it < all1;
-                const int k0 = x.key0(it), end = min(p + 1, x.limit(it)), nch = x.width(it) >> 5;
-                ok = __all_sync(0xffffffffu, mbar_wait(&bars->sfull[t], seen & 1));
+                const int k0 = x.key0(it), end = min(p + 1, x.limit(it));
+                ok = __all_sync(0xffffffffu, wait_bar(&bars->sfull[t], seen & 1));
                 if (!ok) break;
                 tc_fence_after();
                 // raise the maximum in use, rescaling the sum and O, where a row needs it
@@ -592,14 +628,26 @@ __global__ void __launch_bounds__(NT, 1)
                     for (int i = 0; i < 32; i += 2)
                         mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], s[i], s[i + 1]);
                 };
-                auto mask = [&](int ch, float (&s)[32]) {
-                    const int kc = k0 + 32 * ch;
-                    const uint32_t keep =
-                        low_bits(end - kc) & (~low_bits(rlo - kc) | low_bits(a.sinks - kc));
+                if (!whole) {
+                    // A tile at the edge of what the rows see, or a narrow one:
+                    // -inf over the scores that a row does not see, in TMEM, so
+                    // that one code serves all tiles (unrolled code of its own
+                    // fell out of the instruction cache between its uses).
+#pragma unroll 1
+                    for (int ch = 0; ch < 4; ++ch) {
+                        const int kc = k0 + 32 * ch;
+                        const uint32_t keep = low_bits(end - kc) & (~low_bits(rlo - kc) | low_bits(a.sinks - kc));
+                        if (__all_sync(0xffffffffu, keep == 0xffffffffu)) continue;
+                        float s[32];
+                        tmem_ld32(ts + 32 * ch, s);
+                        tmem_ld_wait(s);
 #pragma unroll
-                    for (int i = 0; i < 32; ++i)
-                        if (!((keep >> i) & 1u)) s[i] = -INFINITY;
-                };
+                        for (int i = 0; i < 32; ++i)
+                            if (!((keep >> i) & 1u)) s[i] = -INFINITY;
+                        tmem_st32(ts + 32 * ch, s);
+                    }
+                    tmem_st_wait();
+                }
                 float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
                 auto publish = [&](int half) {
                     tmem_st_wait();
@@ -607,67 +655,35 @@ __global__ void __launch_bounds__(NT, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bars->pready[t][half]);
                 };
-                if (whole) {
-                    float s[4][32];
-                    tmem_ld32(ts, s[0]);
-                    tmem_ld32(ts + 32, s[1]);
-                    tmem_ld_wait(s[0], s[1]);
-                    tmem_ld32(ts + 64, s[2]);
-                    tmem_ld32(ts + 96, s[3]);
-                    top(mx, s[0]);
-                    top(mx, s[1]);
-                    tmem_ld_wait(s[2], s[3]);
-                    top(mx, s[2]);
-                    top(mx, s[3]);
-                    const float base = raise(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-                    const float2 b2 = make_float2(base, base);
-                    weights(0, s[0], b2);
-                    weights(1, s[1], b2);
-                    publish(0);
-                    weights(2, s[2], b2);
-                    weights(3, s[3], b2);
-                    publish(1);
-                } else {
-                    // a masked or narrow tile, rare: the scores are read twice, 32
-                    // columns at a time, in little code (rarely run code comes
-                    // from far: unrolled it took longer)
-#pragma unroll 1
-                    for (int ch = 0; ch < nch; ++ch) {
-                        float s[32];
-                        tmem_ld32(ts + 32 * ch, s);
-                        tmem_ld_wait(s);
-                        mask(ch, s);
-                        top(mx, s);
-                    }
-                    const float base = raise(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
-                    const float2 b2 = make_float2(base, base);
-#pragma unroll 1
-                    for (int ch = 0; ch < nch; ++ch) {
-                        float s[32];
-                        tmem_ld32(ts + 32 * ch, s);
-                        tmem_ld_wait(s);
-                        mask(ch, s);
-                        weights(ch, s, b2);  // columns whose scores have been read
-                        if (ch == 1) publish(0);
-                    }
-                    if (nch < 2) publish(0);
-                    publish(1);
-                }
+                float s[4][32];
+                tmem_ld32(ts, s[0]);
+                tmem_ld32(ts + 32, s[1]);
+                tmem_ld_wait(s[0], s[1]);
+                tmem_ld32(ts + 64, s[2]);
+                tmem_ld32(ts + 96, s[3]);
+                top(mx, s[0]);
+                top(mx, s[1]);
+                tmem_ld_wait(s[2], s[3]);
+                top(mx, s[2]);
+                top(mx, s[3]);
+                const float base = raise(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
+                const float2 b2 = make_float2(base, base);
+                weights(0, s[0], b2);
+                weights(1, s[1], b2);
+                publish(0);
+                weights(2, s[2], b2);
+                weights(3, s[3], b2);
+                publish(1);
                 const float2 two = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
                 l += two.x + two.y;
                 ++seen;
             }
-            const int rows = x.rows[t], i0 = x.i0[t], b = x.b, hk = x.hk, kl = x.kl, p0 = x.p0[t];
-            const bool any = n > 0, live = row < rows;
-            __nv_bfloat16 *ot = static_cast<__nv_bfloat16 *>(a.o) + b * a.os.b + x.head[t] * a.os.h +
-                                (long long)i0 * a.os.t;
-            const __nv_bfloat16 *qt = static_cast<const __nv_bfloat16 *>(a.q) + b * a.qs.b +
-                                      x.head[t] * a.qs.h + (long long)i0 * a.qs.t;
-            give_back();
-            if (any) {
-                if (ok) ok = __all_sync(0xffffffffu, mbar_wait(&bars->ofull[t], used & 1));
-                ++used;
+            if (n == 0) {
+                give_back();
+                continue;
             }
+            if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bars->ofull[t], used & 1));
+            ++used;
             if (!ok) break;
             tc_fence_after();
             const float inv = l == 0.f ? 0.f : 1.f / l;  // no key, or only scores of -inf
@@ -675,55 +691,62 @@ __global__ void __launch_bounds__(NT, 1)
             // so that a store writes whole 64-byte pieces of eight rows (with a
             // row per lane it touched 32 lines at once).
             uint8_t *out = sm + L::OUT + warp * 2048;
-            const int w0 = 32 * (warp & 3);
+            const int w0 = 32 * (warp & 3), rows = x.rows[t], r8 = lane >> 2, c8 = lane & 3;
+            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + x.b * a.os.b + x.head[t] * a.os.h +
+                               (long long)(x.i0[t] + w0 + r8) * a.os.t + 8 * c8;
+            const long long next8 = 8 * a.os.t;
             float odd = 0.f;  // NaN once a value is not finite
+            int last_ch;      // hidden from the compiler, which would unroll the last turn
+            asm volatile("mov.u32 %0, %1;" : "=r"(last_ch) : "n"(D / 32 - 1));
 #pragma unroll 1
             for (int ch = 0; ch < D / 32; ++ch) {
                 float v[32];
-                if (any) {
-                    tmem_ld32(to + 32 * ch, v);
-                    tmem_ld_wait(v);
-                    if (ch == D / 32 - 1) {  // O has been read
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bars->oempty[t]);
-                    }
+                tmem_ld32(to + 32 * ch, v);
+                tmem_ld_wait(v);
+                if (ch == last_ch) {  // O has been read
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->oempty[t]);
                 }
                 uint32_t w[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float y0 = any ? v[2 * i] * inv : 0.f, y1 = any ? v[2 * i + 1] * inv : 0.f;
+                    const float y0 = v[2 * i] * inv, y1 = v[2 * i + 1] * inv;
                     odd = fmaf(y0, 0.f, fmaf(y1, 0.f, odd));
                     w[i] = pack2(y0, y1);
                 }
-                __syncwarp();  // the last piece has left
+                __syncwarp();  // the last channels have left
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     *reinterpret_cast<uint4 *>(out + lane * 64 + (i ^ ((lane >> 1) & 3)) * 16) =
                         make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                 __syncwarp();
+                __nv_bfloat16 *oc = o + 32 * ch;
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int rr = 8 * i + (lane >> 2), c = lane & 3;
-                    const uint4 y = *reinterpret_cast<const uint4 *>(out + rr * 64 + (c ^ ((rr >> 1) & 3)) * 16);
-                    if (w0 + rr < rows)
-                        *reinterpret_cast<uint4 *>(ot + (w0 + rr) * a.os.t + 32 * ch + 8 * c) = y;
+                    const int rr = 8 * i + r8;
+                    const uint4 y = *reinterpret_cast<const uint4 *>(out + rr * 64 + (c8 ^ ((rr >> 1) & 3)) * 16);
+                    if (w0 + rr < rows) *reinterpret_cast<uint4 *>(oc) = y;
+                    oc += next8;
                 }
             }
-            const bool finite = odd == 0.f;
-            __syncwarp();
-            unsigned again = __ballot_sync(0xffffffffu, live && !finite);
+            unsigned again = __ballot_sync(0xffffffffu, row < rows && !(odd == 0.f));
             if (again) {
-                const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k) + b * a.ks.b + hk * a.ks.h;
-                const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + b * a.vs.b + hk * a.vs.h;
+                const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + x.b * a.qs.b +
+                                         x.head[t] * a.qs.h + (long long)x.i0[t] * a.qs.t;
+                const __nv_bfloat16 *k = static_cast<const __nv_bfloat16 *>(a.k) + x.b * a.ks.b + x.hk * a.ks.h;
+                const __nv_bfloat16 *v = static_cast<const __nv_bfloat16 *>(a.v) + x.b * a.vs.b + x.hk * a.vs.h;
+                __nv_bfloat16 *ot = static_cast<__nv_bfloat16 *>(a.o) + x.b * a.os.b + x.head[t] * a.os.h +
+                                    (long long)x.i0[t] * a.os.t;
                 __syncwarp();
                 while (again) {
-                    const int rr = 32 * (warp & 3) + __ffs(again) - 1;
+                    const int rr = w0 + __ffs(again) - 1;
                     again &= again - 1;
-                    attn_row<__nv_bfloat16, D>(qt + rr * a.qs.t, k, v, a.ks.t, a.vs.t, ot + rr * a.os.t,
-                                               seen_keys(p0 + rr, kl, a.window, a.sinks), a.scale);
+                    attn_row<__nv_bfloat16, D>(q + rr * a.qs.t, k, v, a.ks.t, a.vs.t, ot + rr * a.os.t,
+                                               seen_keys(x.p0[t] + rr, x.kl, a.window, a.sinks), a.scale);
                 }
             }
+            give_back();
         }
     }
 
@@ -780,7 +803,8 @@ cudaError_t launch(const WindowArgs &a, int slot, cudaStream_t stream) {
     // the mask's -inf into NaN, and 2^-100 rounds to the same weights
     g.c = a.scale == 0.f ? 7.9e-31f : fabsf(a.scale) * 1.4426950408889634f;
     g.negate = a.scale < 0.f ? 1u << 13 : 0u;
-    g.pair_heads = (a.Hq / a.Hk) % 2 == 0;
+    g.group = a.Hq / a.Hk;
+    g.pair_heads = g.group % 2 == 0;
     const int rows = g.pair_heads ? BM : 2 * BM;
     g.tiles = (a.Tq + rows - 1) / rows;
     // keys and values of the heads in flight stay within 48 MB of the L2's 129
