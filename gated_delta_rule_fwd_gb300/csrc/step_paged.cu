@@ -2,13 +2,21 @@
 //
 // The keys that a sequence sees (its sinks, then its window) form one list,
 // cut into chunks.  One CTA takes one chunk of one sequence and key head for
-// up to GC of the query heads that share it, so a chunk's keys and values are
-// read once for them.  Inside the CTA every group of d / 8 lanes takes keys
-// of its own, with a running maximum and sum of its own; the groups are
-// joined through shuffles and shared memory at the end.  With one chunk per
-// sequence the CTA writes the output; otherwise it writes (maximum, sum,
-// unnormalised output) to the workspace and a second kernel joins the chunks
-// in order.
+// the query heads that share it, so a chunk's keys and values are read once
+// for them.  With one chunk per sequence the CTA writes the output; otherwise
+// it writes (maximum, sum, unnormalised output) to the workspace and a second
+// kernel joins the chunks in order.  The bound is the read of the cache.
+//
+// bf16 (step_mma_kernel): warp-level products.  A warp takes 16 keys at a
+// time, S^T = K Q^T (16 keys x 8 heads) and O^T += V^T P^T, with keys and
+// values loaded from global memory straight into the fragments: the order of
+// the channels inside a product is free, so each lane loads 16 contiguous
+// bytes of a row; value pairs along the keys are made with byte permutes.  No
+// shared memory and no barrier stand between a load and its product, and the
+// next keys are on their way while the values of the last ones are used.
+//
+// fp32 (step_simt_kernel): CUDA cores.  Every group of d / 8 lanes takes keys
+// of its own, with a running maximum and sum of its own.
 #include "attn_internal.cuh"
 
 namespace lr {
@@ -31,22 +39,12 @@ __device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
                  b = __ldg(reinterpret_cast<const float4 *>(p + 4));
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
-    const uint4 r = __ldg(reinterpret_cast<const uint4 *>(p));
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-    }
-}
-
 // exp(m - base) with an empty part's maximum of -inf
 __device__ __forceinline__ float part_weight(float m, float base) {
     return m == -INFINITY ? 0.f : __expf(m - base);
 }
 
-template <typename E, int D, int GC>
+template <int D, int GC>
 __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts) {
     constexpr int LANES = D / 8;            // lanes of a key
     constexpr int GROUPS = NT / LANES;      // keys in flight
@@ -75,7 +73,7 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts) 
     const int h0 = hk * G + gi * GC, heads = min(GC, G - gi * GC);
     const int lane = tid % LANES, group = tid / LANES, ch = lane * 8;
 
-    const E *qn = static_cast<const E *>(a.q) + (size_t)n * a.Hq * D;
+    const float *qn = static_cast<const float *>(a.q) + (size_t)n * a.Hq * D;
     float q[GC][8], acc[GC][8], m[GC], l[GC];
 #pragma unroll
     for (int g = 0; g < GC; ++g) {
@@ -109,7 +107,7 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts) 
         for (int u = 0; u < U; ++u) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
-            if (row[u] >= 0) load8(static_cast<const E *>(a.k) + row[u], x[u]);
+            if (row[u] >= 0) load8(static_cast<const float *>(a.k) + row[u], x[u]);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -126,7 +124,7 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts) 
         for (int u = 0; u < U; ++u) {
 #pragma unroll
             for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
-            if (row[u] >= 0) load8(static_cast<const E *>(a.v) + row[u], x[u]);
+            if (row[u] >= 0) load8(static_cast<const float *>(a.v) + row[u], x[u]);
         }
 #pragma unroll
         for (int g = 0; g < GC; ++g) {
@@ -187,7 +185,7 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts) 
         }
         const size_t r = (size_t)n * a.Hq + h0 + g;
         if (parts.splits == 1) {
-            static_cast<E *>(a.o)[r * D + c] = from_f<E>(sum == 0.f ? 0.f : x / sum);
+            static_cast<float *>(a.o)[r * D + c] = sum == 0.f ? 0.f : x / sum;
         } else {
             parts.o[(r * parts.splits + split) * D + c] = x;
             if (c == 0) parts.ml[r * parts.splits + split] = make_float2(mn, sum);
@@ -195,28 +193,322 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts) 
     }
 }
 
-// One CTA of D threads per output row: the chunks' parts in order.
+// ------------------------------------------------------------------- bf16
+
+constexpr int kTile = 16;            // keys of a product
+constexpr int kMostTiles = 128;      // of a chunk
+
+// D (16x8, fp32) += A (16x16, bf16) B (16x8, bf16), fragments as in the PTX
+// m16n8k16 layout (g = lane / 4, t = lane % 4): a = {A[g][2t..], A[g+8][2t..],
+// A[g][2t+8..], A[g+8][2t+8..]}, b = {B[2t..][g], B[2t+8..][g]}, d = {D[g][2t],
+// D[g][2t+1], D[g+8][2t], D[g+8][2t+1]}.
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// An 8 x 8 matrix of 16-bit values, two per lane, transposed across the warp.
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// Cache rows are read once: past L1.
+__device__ __forceinline__ uint4 load_once16(const void *p) {
+    uint4 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
+                 : "l"(p));
+    return r;
+}
+__device__ __forceinline__ uint2 load_once8(const void *p) {
+    uint2 r;
+    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
+    return r;
+}
+
+// NH: 8-head column blocks of the products.  c = |scale| log2 e; flip: sign
+// bits of a bf16 pair where scale is negative.
+template <int D, int NH>
+__global__ void __launch_bounds__(NT)
+    step_mma_kernel(StepArgs a, Parts parts, float c, uint32_t flip) {
+    constexpr int KC = D / 32;   // 32-channel pieces of a key: 16 bytes per lane and row
+    constexpr int VW = D / 16;   // words of a value row per lane = 16-channel blocks of O^T
+    constexpr int HEADS = 8 * NH;
+    __shared__ float so[NT / 32][HEADS][D + 8];
+    __shared__ float sml[NT / 32][HEADS][2];
+    __shared__ long long rows[kMostTiles];  // first cache row of each tile, -1: a bad page
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int G = a.Hq / a.Hk, gq = (G + HEADS - 1) / HEADS;
+    int id = blockIdx.x;
+    const int split = id % parts.splits;
+    id /= parts.splits;
+    const int gi = id % gq;
+    id /= gq;
+    const int hk = id % a.Hk, n = id / a.Hk;
+    const int len = a.lens[n];
+    if (len < 0) return;
+    if (len > a.max_len) {
+        if (tid == 0 && split == 0 && gi == 0 && hk == 0) atomicOr(&g_step_error, kAttnIndex);
+        return;
+    }
+    const SeenKeys s = seen_keys(len - 1, len, a.window, a.sinks);
+    const int sink_tiles = (s.s1 + kTile - 1) / kTile;
+    const int k_first = max(s.lo / kTile, sink_tiles);  // a tile that holds both is a sink tile
+    const int tiles = sink_tiles + max(0, (s.hi + kTile - 1) / kTile - k_first);
+    const int per = parts.chunk / kTile, t0 = split * per, t1 = min(tiles, t0 + per);
+    if (t0 >= tiles && split > 0) return;  // the join knows how many chunks there are
+    const int h0 = hk * G + gi * HEADS, heads = min(HEADS, G - gi * HEADS);
+
+    auto key_of = [&](int i) { return kTile * (i < sink_tiles ? i : i - sink_tiles + k_first); };
+    for (int i = tid; i < t1 - t0; i += NT) {
+        const int key = key_of(t0 + i);
+        const int page = a.table[(size_t)n * a.max_pages + (key >> a.page_log2)];
+        const bool ok = page >= 0 && page < a.num_pages;
+        if (!ok) atomicOr(&g_step_error, kAttnIndex);
+        rows[i] = ok ? (((long long)page * a.Hk + hk) << a.page_log2) + (key & ((1 << a.page_log2) - 1)) : -1;
+    }
+
+    // queries: head g of each block, the channels that the lane's keys hold
+    uint32_t q[NH][2 * KC][2];
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh) {
+        const bool live = 8 * nh + g < heads;
+        const __nv_bfloat16 *p = static_cast<const __nv_bfloat16 *>(a.q) +
+                                 ((size_t)n * a.Hq + h0 + (live ? 8 * nh + g : 0)) * D + 8 * t;
+#pragma unroll
+        for (int i = 0; i < KC; ++i) {
+            uint4 x = make_uint4(0, 0, 0, 0);
+            if (live) x = *reinterpret_cast<const uint4 *>(p + 32 * i);
+            q[nh][2 * i][0] = x.x ^ flip, q[nh][2 * i][1] = x.y ^ flip;
+            q[nh][2 * i + 1][0] = x.z ^ flip, q[nh][2 * i + 1][1] = x.w ^ flip;
+        }
+    }
+    __syncthreads();
+
+    float acc[VW][NH][4], m[NH][2], l[NH][2];
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh) {
+        m[nh][0] = m[nh][1] = -INFINITY;
+        l[nh][0] = l[nh][1] = 0.f;
+#pragma unroll
+        for (int j = 0; j < VW; ++j)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) acc[j][nh][i] = 0.f;
+    }
+    uint4 kr[2][KC];        // keys g and g + 8
+    uint32_t vr[4][VW];     // values of keys 2t, 2t+1, 2t+8, 2t+9
+    const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16 *>(a.k),
+                        *vp = static_cast<const __nv_bfloat16 *>(a.v);
+    // Rows that the sequence does not see are not read: zeros.
+    auto sees = [&](int key) { return key < s.hi && (key >= s.lo || key < s.s1); };
+    auto load_k = [&](int i) {
+        const long long row = rows[i - t0];
+        const int key = key_of(i);
+        const bool all = row >= 0 && sees(key) && sees(key + kTile - 1) && (key >= s.lo || key + kTile <= s.s1);
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const bool on = all || (row >= 0 && sees(key + g + 8 * r));
+            const __nv_bfloat16 *p = kp + (row + g + 8 * r) * D + 8 * t;
+#pragma unroll
+            for (int i2 = 0; i2 < KC; ++i2) {
+                kr[r][i2] = make_uint4(0, 0, 0, 0);
+                if (on) kr[r][i2] = load_once16(p + 32 * i2);
+            }
+        }
+    };
+    auto load_v = [&](int i) {
+        const long long row = rows[i - t0];
+        const int key = key_of(i);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const int kk = 2 * t + (r & 1) + 8 * (r >> 1);
+            const bool on = row >= 0 && sees(key + kk);
+            const __nv_bfloat16 *p = vp + (row + kk) * D;
+#pragma unroll
+            for (int w = 0; w < VW; ++w) vr[r][w] = 0u;
+            if (on) {
+                if (D == 32) {
+                    const uint2 x = load_once8(p + 4 * g);
+                    vr[r][0] = x.x, vr[r][1] = x.y;
+                } else {
+#pragma unroll
+                    for (int w = 0; w < VW / 4; ++w) {
+                        const uint4 x = load_once16(p + 64 * w + 8 * g);
+                        vr[r][4 * w] = x.x, vr[r][4 * w + 1] = x.y, vr[r][4 * w + 2] = x.z,
+                                   vr[r][4 * w + 3] = x.w;
+                    }
+                }
+            }
+        }
+    };
+
+    const int first = t0 + warp;
+    if (first < t1) {
+        load_k(first);
+        load_v(first);
+    }
+    for (int i = first; i < t1; i += NT / 32) {
+        float sc[NH][4];
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) sc[nh][e] = 0.f;
+#pragma unroll
+            for (int i2 = 0; i2 < KC; ++i2) {
+                mma16816(sc[nh], kr[0][i2].x, kr[1][i2].x, kr[0][i2].y, kr[1][i2].y, q[nh][2 * i2][0],
+                         q[nh][2 * i2][1]);
+                mma16816(sc[nh], kr[0][i2].z, kr[1][i2].z, kr[0][i2].w, kr[1][i2].w,
+                         q[nh][2 * i2 + 1][0], q[nh][2 * i2 + 1][1]);
+            }
+        }
+        const bool page_ok = rows[i - t0] >= 0;
+        const int key = key_of(i);
+        const bool see0 = page_ok && sees(key + g), see1 = page_ok && sees(key + g + 8);
+        const int next = i + NT / 32;
+        if (next < t1) load_k(next);
+        bool grow = false;
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x = (e < 2 ? see0 : see1) ? sc[nh][e] : -INFINITY, y = m[nh][e & 1];
+                sc[nh][e] = x;
+                grow = grow || (x > y && !((x - y) * c <= 8.f));
+            }
+        // the maximum in use is raised only when a score passes it by 2^8
+        if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+            for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(sc[nh][e], sc[nh][e + 2]);
+#pragma unroll
+                    for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+                    const float mn = fmaxf(m[nh][e], mx);
+                    const float f = m[nh][e] == -INFINITY ? 0.f : ex2((m[nh][e] - mn) * c);
+                    m[nh][e] = mn;
+                    // nothing seen yet: sums and output are zero (or NaN, which stays)
+                    l[nh][e] *= f;
+#pragma unroll
+                    for (int j = 0; j < VW; ++j) acc[j][nh][e] *= f, acc[j][nh][e + 2] *= f;
+                }
+        }
+        uint32_t p[NH][2];
+#pragma unroll
+        for (int nh = 0; nh < NH; ++nh) {
+            const float b0 = m[nh][0] == -INFINITY ? 0.f : m[nh][0], b1 = m[nh][1] == -INFINITY ? 0.f : m[nh][1];
+            // differences first: a product of one large score would overflow
+            const float e0 = ex2((sc[nh][0] - b0) * c), e1 = ex2((sc[nh][1] - b1) * c),
+                        e2 = ex2((sc[nh][2] - b0) * c), e3 = ex2((sc[nh][3] - b1) * c);
+            l[nh][0] += e0 + e2;
+            l[nh][1] += e1 + e3;
+            p[nh][0] = transpose8x8(pack2(e0, e1));
+            p[nh][1] = transpose8x8(pack2(e2, e3));
+        }
+#pragma unroll
+        for (int j = 0; j < VW; ++j) {
+            const uint32_t a0 = __byte_perm(vr[0][j], vr[1][j], 0x5410), a1 = __byte_perm(vr[0][j], vr[1][j], 0x7632),
+                           a2 = __byte_perm(vr[2][j], vr[3][j], 0x5410), a3 = __byte_perm(vr[2][j], vr[3][j], 0x7632);
+#pragma unroll
+            for (int nh = 0; nh < NH; ++nh) mma16816(acc[j][nh], a0, a1, a2, a3, p[nh][0], p[nh][1]);
+        }
+        if (next < t1) load_v(next);
+    }
+    // this warp's part: word j of a lane holds channels col_j and col_j + 1
+#pragma unroll
+    for (int nh = 0; nh < NH; ++nh)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float sum = l[nh][e];
+#pragma unroll
+            for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+            const int h = 8 * nh + 2 * t + e;
+            if (g == 0) sml[warp][h][0] = m[nh][e], sml[warp][h][1] = sum;
+#pragma unroll
+            for (int j = 0; j < VW; ++j) {
+                const int col = D == 32 ? 4 * g + 2 * j : 64 * (j >> 2) + 8 * g + 2 * (j & 3);
+                *reinterpret_cast<float2 *>(&so[warp][h][col]) = make_float2(acc[j][nh][e], acc[j][nh][e + 2]);
+            }
+        }
+    __syncthreads();
+    for (int i = tid; i < heads * D; i += NT) {
+        const int h = i / D, ch = i - h * D;
+        float mn = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) mn = fmaxf(mn, sml[w][h][0]);
+        float sum = 0.f, x = 0.f;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) {
+            const float mw = sml[w][h][0], f = mw == -INFINITY ? 0.f : ex2((mw - mn) * c);
+            // a warp whose scores were all NaN has a maximum of -inf and a sum of NaN
+            sum += f * sml[w][h][1];
+            x += f * so[w][h][ch];
+        }
+        const size_t r = (size_t)n * a.Hq + h0 + h;
+        if (parts.splits == 1) {
+            static_cast<__nv_bfloat16 *>(a.o)[r * D + ch] = bf16_rn(sum == 0.f ? 0.f : x / sum);
+        } else {
+            parts.o[(r * parts.splits + split) * D + ch] = x;
+            if (ch == 0) parts.ml[r * parts.splits + split] = make_float2(mn, sum);
+        }
+    }
+}
+
+// One CTA of D threads per output row: the chunks' parts in order.  c: the
+// scores' factor to powers of two.
 template <typename E, int D>
-__global__ void __launch_bounds__(D) step_join_kernel(StepArgs a, Parts parts) {
-    const int r = blockIdx.x, n = r / a.Hq, c = threadIdx.x;
+__global__ void __launch_bounds__(D) step_join_kernel(StepArgs a, Parts parts, float c) {
+    const int r = blockIdx.x, n = r / a.Hq, ch = threadIdx.x;
     const int len = a.lens[n];
     if (len < 0 || len > a.max_len) return;
     const SeenKeys s = seen_keys(len - 1, len, a.window, a.sinks);
-    const int seen = s.s1 + s.hi - s.lo;
+    int seen = s.s1 + s.hi - s.lo;
+    if (sizeof(E) == 2) {  // whole tiles of 16 keys (step_mma_kernel)
+        const int sink_tiles = (s.s1 + kTile - 1) / kTile, k_first = max(s.lo / kTile, sink_tiles);
+        seen = kTile * (sink_tiles + max(0, (s.hi + kTile - 1) / kTile - k_first));
+    }
     const int used = max(1, (seen + parts.chunk - 1) / parts.chunk);
     const float2 *ml = parts.ml + (size_t)r * parts.splits;
-    const float *po = parts.o + (size_t)r * parts.splits * D + c;
+    const float *po = parts.o + (size_t)r * parts.splits * D + ch;
     float m = -INFINITY, l = 0.f, x = 0.f;
-    for (int i = 0; i < used; ++i) {
-        const float2 t = ml[i];
-        const float y = po[(size_t)i * D];
-        const float mn = fmaxf(m, t.x);
-        const float f = part_weight(m, mn), g = part_weight(t.x, mn);
-        l = l * f + t.y * g;
-        x = x * f + y * g;
+    for (int i0 = 0; i0 < used; i0 += 8) {
+        float2 t[8];
+        float y[8], mn = m;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            t[i] = i0 + i < used ? ml[i0 + i] : make_float2(-INFINITY, 0.f);
+            y[i] = i0 + i < used ? po[(size_t)(i0 + i) * D] : 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mn = fmaxf(mn, t[i].x);
+        const float f = m == -INFINITY ? 0.f : ex2((m - mn) * c);
+        l *= f;
+        x *= f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            // a part without a key weighs nothing; one whose scores were all
+            // NaN has no maximum either, but a sum of NaN
+            const float w = t[i].x == -INFINITY ? 0.f : ex2((t[i].x - mn) * c);
+            l += t[i].y * w;
+            x += y[i] * w;
+        }
         m = mn;
     }
-    static_cast<E *>(a.o)[(size_t)r * D + c] = from_f<E>(l == 0.f ? 0.f : x / l);
+    static_cast<E *>(a.o)[(size_t)r * D + ch] = from_f<E>(l == 0.f ? 0.f : x / l);
 }
 
 Parts parts_of(const StepArgs &a, int d, const StepPlan &p, void *ws) {
@@ -229,43 +521,61 @@ Parts parts_of(const StepArgs &a, int d, const StepPlan &p, void *ws) {
     return r;
 }
 
-template <typename E, int D>
-cudaError_t launch(const StepArgs &a, void *ws, lr_dtype dt, cudaStream_t stream) {
-    const StepPlan p = step_plan(a.N, a.Hq, a.Hk, a.max_len, a.window, a.sinks, dt);
-    const Parts parts = parts_of(a, D, p, ws);
+// |scale| log2 e.  Scale 0 gives every key the same weight; a product with it
+// would turn -inf into NaN, and 2^-100 rounds to the same weights.
+float exp2_scale(float scale) {
+    return scale == 0.f ? 7.9e-31f : fabsf(scale) * 1.4426950408889634f;
+}
+
+template <int D>
+cudaError_t launch_f32(const StepArgs &a, const Parts &parts, cudaStream_t stream) {
     const int G = a.Hq / a.Hk;
     const int gc = G == 1 ? 1 : G == 2 ? 2 : 4;
-    const unsigned grid = (unsigned)(a.N * a.Hk * ((G + gc - 1) / gc) * p.splits);
-    if (gc == 1) step_simt_kernel<E, D, 1><<<grid, NT, 0, stream>>>(a, parts);
-    else if (gc == 2) step_simt_kernel<E, D, 2><<<grid, NT, 0, stream>>>(a, parts);
-    else step_simt_kernel<E, D, 4><<<grid, NT, 0, stream>>>(a, parts);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.splits == 1) return e;
-    step_join_kernel<E, D><<<(unsigned)(a.N * a.Hq), D, 0, stream>>>(a, parts);
+    const unsigned grid = (unsigned)(a.N * a.Hk * ((G + gc - 1) / gc) * parts.splits);
+    if (gc == 1) step_simt_kernel<D, 1><<<grid, NT, 0, stream>>>(a, parts);
+    else if (gc == 2) step_simt_kernel<D, 2><<<grid, NT, 0, stream>>>(a, parts);
+    else step_simt_kernel<D, 4><<<grid, NT, 0, stream>>>(a, parts);
     return cudaGetLastError();
 }
 
-template <typename E>
-cudaError_t launch_d(const StepArgs &a, int d, void *ws, lr_dtype dt, cudaStream_t stream) {
-    if (d == 32) return launch<E, 32>(a, ws, dt, stream);
-    if (d == 64) return launch<E, 64>(a, ws, dt, stream);
-    return launch<E, 128>(a, ws, dt, stream);
+template <int D>
+cudaError_t launch_bf16(const StepArgs &a, const Parts &parts, cudaStream_t stream) {
+    const int G = a.Hq / a.Hk, heads = G <= 8 ? 8 : 16;
+    const unsigned grid = (unsigned)(a.N * a.Hk * ((G + heads - 1) / heads) * parts.splits);
+    const float c = exp2_scale(a.scale);
+    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
+    if (heads == 8) step_mma_kernel<D, 1><<<grid, NT, 0, stream>>>(a, parts, c, flip);
+    else step_mma_kernel<D, 2><<<grid, NT, 0, stream>>>(a, parts, c, flip);
+    return cudaGetLastError();
+}
+
+template <int D>
+cudaError_t launch(const StepArgs &a, void *ws, lr_dtype dt, cudaStream_t stream) {
+    const StepPlan p = step_plan(a.N, a.Hq, a.Hk, a.max_len, a.window, a.sinks, dt);
+    const Parts parts = parts_of(a, D, p, ws);
+    const cudaError_t e = dt == LR_DT_F32 ? launch_f32<D>(a, parts, stream) : launch_bf16<D>(a, parts, stream);
+    if (e != cudaSuccess || p.splits == 1) return e;
+    const unsigned rows = (unsigned)(a.N * a.Hq);
+    if (dt == LR_DT_F32) step_join_kernel<float, D><<<rows, D, 0, stream>>>(a, parts, 1.4426950408889634f);
+    else step_join_kernel<__nv_bfloat16, D><<<rows, D, 0, stream>>>(a, parts, exp2_scale(a.scale));
+    return cudaGetLastError();
 }
 
 }  // namespace
 
 StepPlan step_plan(int N, int Hq, int Hk, int max_len, int window, int sinks, lr_dtype dt) {
-    (void)dt;
     (void)Hq;
     const long long w = (long long)window + sinks;
-    const int seen = w < max_len ? (int)w : max_len;
+    // whole tiles in bf16: the sinks' and the window's first and last may be cut
+    const long long most = w < max_len ? w + (dt == LR_DT_BF16 ? 2 * kTile + (sinks > 0 ? kTile : 0) : 0) : max_len;
+    const int seen = (int)(most < max_len ? most : max_len);
     // about four CTAs per SM in all, chunks of 128 to 2048 keys
     const long long rows = (long long)N * Hk;
     const long long want = (608 + rows - 1) / rows;
     long long chunk = (seen + want - 1) / want;
     chunk = (chunk + 63) / 64 * 64;
     if (chunk < 128) chunk = 128;
-    if (chunk > 2048) chunk = 2048;
+    if (chunk > kTile * kMostTiles) chunk = kTile * kMostTiles;
     StepPlan p;
     p.chunk = (int)chunk;
     p.splits = (seen + p.chunk - 1) / p.chunk;
@@ -278,8 +588,9 @@ size_t step_workspace_bytes(int N, int Hq, int d, const StepPlan &p) {
 }
 
 cudaError_t launch_step_paged(const StepArgs &a, int d, lr_dtype dt, void *ws, cudaStream_t stream) {
-    return dt == LR_DT_F32 ? launch_d<float>(a, d, ws, dt, stream)
-                           : launch_d<__nv_bfloat16>(a, d, ws, dt, stream);
+    if (d == 32) return launch<32>(a, ws, dt, stream);
+    if (d == 64) return launch<64>(a, ws, dt, stream);
+    return launch<128>(a, ws, dt, stream);
 }
 
 int attn_errors_step() {
