@@ -15,6 +15,7 @@ there, on its current stream unless one is given.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 NO_WINDOW = (1 << 31) - 1   # a window that hides nothing
 QK_NORM = 0x1
@@ -252,14 +253,20 @@ def lr_fwd_window(q, k, v, *, window=None, sinks=0, q_len=None, k_len=None, scal
     return o
 
 
+@functools.lru_cache(maxsize=1024)
+def _step_workspace(N, Hq, Hk, d, max_len, window, sinks, dt):
+    """lr_step_paged_workspace_size, a function of the sizes alone."""
+    return int(_base().lib().lr_step_paged_workspace_size(N, Hq, Hk, d, max_len, window, sinks, dt))
+
+
 def step_paged_workspace_size(N, Hq, Hk, d, max_len, dtype, window=None, sinks=0) -> int:
     """lr_step_paged_workspace_size for these sizes (dtype: torch dtype)."""
     import torch
     base = _base()
     dt = base.F32 if dtype == torch.float32 else base.BF16
     window = NO_WINDOW if window is None else _int32(window, "window")
-    return int(base.lib().lr_step_paged_workspace_size(N, Hq, Hk, d, _int32(max_len, "max_len"),
-                                                       window, _int32(sinks, "sinks"), dt))
+    return _step_workspace(N, Hq, Hk, d, _int32(max_len, "max_len"), window,
+                           _int32(sinks, "sinks"), dt)
 
 
 def lr_step_paged(q, k_cache, v_cache, table, lens, *, max_len=None, window=None, sinks=0,
@@ -295,10 +302,9 @@ def lr_step_paged(q, k_cache, v_cache, table, lens, *, max_len=None, window=None
     window = NO_WINDOW if window is None else _int32(window, "window")
     sinks = _int32(sinks, "sinks")
     scale = d ** -0.5 if scale is None else scale
-    L = base.lib()
     need = 0
     if workspace is None:
-        need = L.lr_step_paged_workspace_size(N, Hq, Hk, d, max_len, window, sinks, dt)
+        need = _step_workspace(N, Hq, Hk, d, max_len, window, sinks, dt)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {dev}")
     with _on(stream, dev):
@@ -308,8 +314,9 @@ def lr_step_paged(q, k_cache, v_cache, table, lens, *, max_len=None, window=None
             workspace = torch.empty(need, dtype=torch.uint8, device=dev)
         ws, ws_bytes = ((None, 0) if workspace is None else
                         (workspace.data_ptr(), workspace.numel() * workspace.element_size()))
-        st = L.lr_step_paged(q.data_ptr(), cache, lens.data_ptr(), o.data_ptr(), N, Hq, Hk, d,
-                             max_len, window, sinks, scale, dt, ws, ws_bytes, _handle(stream, dev))
+        st = base.lib().lr_step_paged(q.data_ptr(), cache, lens.data_ptr(), o.data_ptr(), N, Hq,
+                                      Hk, d, max_len, window, sinks, scale, dt, ws, ws_bytes,
+                                      _handle(stream, dev))
     if st != 0:
         raise base.LrError(st, "lr_step_paged")
     return o

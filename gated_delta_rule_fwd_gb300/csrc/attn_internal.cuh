@@ -73,9 +73,11 @@ struct StepArgs {
     int N, Hq, Hk, max_len, window, sinks, num_pages, page_log2, max_pages;
     float scale;
 };
-// How a step's keys are cut: chunks of `chunk` keys, at most `splits` of them.
+// How a step's keys are cut: chunks of `chunk` keys, at most `splits` of them,
+// joined by a cluster or by a second kernel.
 struct StepPlan {
     int chunk, splits;
+    bool cluster;
 };
 StepPlan step_plan(int N, int Hq, int Hk, int max_len, int window, int sinks, lr_dtype dt);
 size_t step_workspace_bytes(int N, int Hq, int d, const StepPlan &p);

@@ -3,9 +3,11 @@
 // The keys that a sequence sees (its sinks, then its window) form one list,
 // cut into chunks.  One CTA takes one chunk of one sequence and key head for
 // the query heads that share it, so a chunk's keys and values are read once
-// for them.  With one chunk per sequence the CTA writes the output; otherwise
-// it writes (maximum, sum, unnormalised output) to the workspace and a second
-// kernel joins the chunks in order.  The bound is the read of the cache.
+// for them.  With one chunk per sequence the CTA writes the output.  A few
+// chunks of a small call are the CTAs of a thread-block cluster, which join
+// their parts through distributed shared memory in the same launch.  Otherwise
+// each CTA writes (maximum, sum, unnormalised output) to the workspace and a
+// second kernel joins the chunks in order.  The bound is the read of the cache.
 //
 // bf16 (step_mma_kernel): warp-level products.  A warp takes 16 keys at a
 // time, S^T = K Q^T (16 keys x 8 heads) and O^T += V^T P^T, with keys and
@@ -18,6 +20,7 @@
 // fp32 (step_simt_kernel): CUDA cores.  Every group of d / 8 lanes takes keys
 // of its own, with a running maximum and sum of its own.
 #include "attn_internal.cuh"
+#include "tc_common.cuh"
 
 namespace lr {
 namespace {
@@ -25,6 +28,7 @@ namespace {
 __device__ unsigned g_step_error = 0;
 
 constexpr int NT = 128;
+constexpr int kMostCluster = 8;  // chunks that a cluster joins
 
 // fp32 partial results in the workspace: [N * Hq][splits][d], then
 // (maximum, sum) [N * Hq][splits].
@@ -32,7 +36,85 @@ struct Parts {
     float *o;
     float2 *ml;
     int splits, chunk;
+    bool cluster;  // the chunks of a row are the CTAs of a cluster
 };
+
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ float ld_cluster(uint32_t addr) {
+    float r;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r) : "r"(addr) : "memory");
+    return r;
+}
+
+// The end of a CTA: joins its warps' parts and hands the result on.  so: the
+// warps' unnormalised outputs, P floats a head; sml: their (maximum, sum); c:
+// the scores' factor to powers of two; row0: output row of head 0.  A part
+// without a key has a maximum of -inf and weighs nothing; one whose scores
+// were all NaN too, but its sum of NaN stays.
+template <typename E, int D, int HEADS, int P>
+__device__ __forceinline__ void finish(float (&so)[NT / 32][HEADS][P], float (&sml)[NT / 32][HEADS][2],
+                                       int heads, size_t row0, int split, float c, E *out,
+                                       const Parts &parts) {
+    const int tid = threadIdx.x;
+    __syncthreads();
+    for (int i = tid; i < heads * D; i += NT) {
+        const int h = i / D, ch = i - h * D;
+        float mn = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) mn = fmaxf(mn, sml[w][h][0]);
+        float sum = 0.f, x = 0.f;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) {
+            const float mw = sml[w][h][0], f = mw == -INFINITY ? 0.f : ex2((mw - mn) * c);
+            sum += f * sml[w][h][1];
+            x += f * so[w][h][ch];
+        }
+        const size_t r = row0 + h;
+        if (parts.splits == 1) {
+            out[r * D + ch] = from_f<E>(sum == 0.f ? 0.f : x / sum);
+        } else if (parts.cluster) {
+            so[0][h][ch] = x;  // read and written by this thread alone
+        } else {
+            parts.o[(r * parts.splits + split) * D + ch] = x;
+            if (ch == 0) parts.ml[r * parts.splits + split] = make_float2(mn, sum);
+        }
+    }
+    if (!parts.cluster) return;
+    __syncthreads();
+    if (tid < heads) {
+        float mn = -INFINITY, sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w) mn = fmaxf(mn, sml[w][tid][0]);
+#pragma unroll
+        for (int w = 0; w < NT / 32; ++w)
+            sum += sml[w][tid][1] * (sml[w][tid][0] == -INFINITY ? 0.f : ex2((sml[w][tid][0] - mn) * c));
+        sml[0][tid][0] = mn, sml[0][tid][1] = sum;
+    }
+    tc::cluster_sync_all();
+    const uint32_t o_at = tc::smem_u32(&so[0][0][0]), ml_at = tc::smem_u32(&sml[0][0][0]);
+    for (int i = split * NT + tid; i < heads * D; i += parts.splits * NT) {
+        const int h = i / D, ch = i - h * D;
+        float m[kMostCluster], mn = -INFINITY, sum = 0.f, x = 0.f;
+#pragma unroll
+        for (int r = 0; r < kMostCluster; ++r) {
+            m[r] = r < parts.splits ? ld_cluster(tc::map_to_rank(ml_at + 8 * h, r)) : -INFINITY;
+            mn = fmaxf(mn, m[r]);
+        }
+#pragma unroll
+        for (int r = 0; r < kMostCluster; ++r)
+            if (r < parts.splits) {
+                const float f = m[r] == -INFINITY ? 0.f : ex2((m[r] - mn) * c);
+                sum += f * ld_cluster(tc::map_to_rank(ml_at + 8 * h + 4, r));
+                x += f * ld_cluster(tc::map_to_rank(o_at + 4 * (h * P + ch), r));
+            }
+        out[(row0 + h) * D + ch] = from_f<E>(sum == 0.f ? 0.f : x / sum);
+    }
+    tc::cluster_sync_all();  // no CTA leaves while another reads its part
+}
 
 __device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
     const float4 a = __ldg(reinterpret_cast<const float4 *>(p)),
@@ -68,7 +150,7 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts) 
     const SeenKeys s = seen_keys(len - 1, len, a.window, a.sinks);
     const int seen = s.s1 + s.hi - s.lo;
     const int c0 = split * parts.chunk;
-    if (c0 >= seen && split > 0) return;  // the join knows how many chunks there are
+    if (c0 >= seen && split > 0 && !parts.cluster) return;  // the join knows how many chunks there are
     const int c1 = min(seen, c0 + parts.chunk);
     const int h0 = hk * G + gi * GC, heads = min(GC, G - gi * GC);
     const int lane = tid % LANES, group = tid / LANES, ch = lane * 8;
@@ -170,33 +252,14 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts) 
             if (lane == 0) sml[warp][g][0] = mn, sml[warp][g][1] = l[g];
         }
     }
-    __syncthreads();
-    for (int i = tid; i < heads * D; i += NT) {
-        const int g = i / D, c = i - g * D;
-        float mn = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < NT / 32; ++w) mn = fmaxf(mn, sml[w][g][0]);
-        float sum = 0.f, x = 0.f;
-#pragma unroll
-        for (int w = 0; w < NT / 32; ++w) {
-            const float f = part_weight(sml[w][g][0], mn);
-            sum += f * sml[w][g][1];
-            x += f * so[w][g][c];
-        }
-        const size_t r = (size_t)n * a.Hq + h0 + g;
-        if (parts.splits == 1) {
-            static_cast<float *>(a.o)[r * D + c] = sum == 0.f ? 0.f : x / sum;
-        } else {
-            parts.o[(r * parts.splits + split) * D + c] = x;
-            if (c == 0) parts.ml[r * parts.splits + split] = make_float2(mn, sum);
-        }
-    }
+    finish<float, D, GC, D>(so, sml, heads, (size_t)n * a.Hq + h0, split, 1.4426950408889634f,
+                            static_cast<float *>(a.o), parts);
 }
 
 // ------------------------------------------------------------------- bf16
 
 constexpr int kTile = 16;            // keys of a product
-constexpr int kMostTiles = 128;      // of a chunk
+constexpr int kMostTiles = 256;      // of a chunk
 
 // D (16x8, fp32) += A (16x16, bf16) B (16x8, bf16), fragments as in the PTX
 // m16n8k16 layout (g = lane / 4, t = lane % 4): a = {A[g][2t..], A[g+8][2t..],
@@ -219,11 +282,6 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
 __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     uint32_t r;
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
 // Cache rows are read once: past L1.
@@ -270,7 +328,7 @@ __global__ void __launch_bounds__(NT)
     const int k_first = max(s.lo / kTile, sink_tiles);  // a tile that holds both is a sink tile
     const int tiles = sink_tiles + max(0, (s.hi + kTile - 1) / kTile - k_first);
     const int per = parts.chunk / kTile, t0 = split * per, t1 = min(tiles, t0 + per);
-    if (t0 >= tiles && split > 0) return;  // the join knows how many chunks there are
+    if (t0 >= tiles && split > 0 && !parts.cluster) return;  // the join knows how many chunks there are
     const int h0 = hk * G + gi * HEADS, heads = min(HEADS, G - gi * HEADS);
 
     auto key_of = [&](int i) { return kTile * (i < sink_tiles ? i : i - sink_tiles + k_first); };
@@ -444,28 +502,8 @@ __global__ void __launch_bounds__(NT)
                 *reinterpret_cast<float2 *>(&so[warp][h][col]) = make_float2(acc[j][nh][e], acc[j][nh][e + 2]);
             }
         }
-    __syncthreads();
-    for (int i = tid; i < heads * D; i += NT) {
-        const int h = i / D, ch = i - h * D;
-        float mn = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < NT / 32; ++w) mn = fmaxf(mn, sml[w][h][0]);
-        float sum = 0.f, x = 0.f;
-#pragma unroll
-        for (int w = 0; w < NT / 32; ++w) {
-            const float mw = sml[w][h][0], f = mw == -INFINITY ? 0.f : ex2((mw - mn) * c);
-            // a warp whose scores were all NaN has a maximum of -inf and a sum of NaN
-            sum += f * sml[w][h][1];
-            x += f * so[w][h][ch];
-        }
-        const size_t r = (size_t)n * a.Hq + h0 + h;
-        if (parts.splits == 1) {
-            static_cast<__nv_bfloat16 *>(a.o)[r * D + ch] = bf16_rn(sum == 0.f ? 0.f : x / sum);
-        } else {
-            parts.o[(r * parts.splits + split) * D + ch] = x;
-            if (ch == 0) parts.ml[r * parts.splits + split] = make_float2(mn, sum);
-        }
-    }
+    finish<__nv_bfloat16, D, HEADS, D + 8>(so, sml, heads, (size_t)n * a.Hq + h0, split, c,
+                                           static_cast<__nv_bfloat16 *>(a.o), parts);
 }
 
 // One CTA of D threads per output row: the chunks' parts in order.  c: the
@@ -513,12 +551,31 @@ __global__ void __launch_bounds__(D) step_join_kernel(StepArgs a, Parts parts, f
 
 Parts parts_of(const StepArgs &a, int d, const StepPlan &p, void *ws) {
     Parts r{};
-    r.splits = p.splits, r.chunk = p.chunk;
-    if (p.splits > 1) {
+    r.splits = p.splits, r.chunk = p.chunk, r.cluster = p.cluster;
+    if (p.splits > 1 && !p.cluster) {
         r.o = static_cast<float *>(ws);
         r.ml = reinterpret_cast<float2 *>(r.o + (size_t)a.N * a.Hq * p.splits * d);
     }
     return r;
+}
+
+// Launches a step kernel, its chunks as clusters where the plan says so.
+template <typename... A>
+cudaError_t launch_parts(void (*fn)(StepArgs, Parts, A...), unsigned grid, cudaStream_t stream,
+                         const StepArgs &a, const Parts &parts, A... rest) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(NT);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    if (parts.cluster) {
+        at[0].id = cudaLaunchAttributeClusterDimension;
+        at[0].val.clusterDim.x = (unsigned)parts.splits;
+        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+        cfg.attrs = at;
+        cfg.numAttrs = 1;
+    }
+    return cudaLaunchKernelEx(&cfg, fn, a, parts, rest...);
 }
 
 // |scale| log2 e.  Scale 0 gives every key the same weight; a product with it
@@ -532,10 +589,9 @@ cudaError_t launch_f32(const StepArgs &a, const Parts &parts, cudaStream_t strea
     const int G = a.Hq / a.Hk;
     const int gc = G == 1 ? 1 : G == 2 ? 2 : 4;
     const unsigned grid = (unsigned)(a.N * a.Hk * ((G + gc - 1) / gc) * parts.splits);
-    if (gc == 1) step_simt_kernel<D, 1><<<grid, NT, 0, stream>>>(a, parts);
-    else if (gc == 2) step_simt_kernel<D, 2><<<grid, NT, 0, stream>>>(a, parts);
-    else step_simt_kernel<D, 4><<<grid, NT, 0, stream>>>(a, parts);
-    return cudaGetLastError();
+    if (gc == 1) return launch_parts(&step_simt_kernel<D, 1>, grid, stream, a, parts);
+    if (gc == 2) return launch_parts(&step_simt_kernel<D, 2>, grid, stream, a, parts);
+    return launch_parts(&step_simt_kernel<D, 4>, grid, stream, a, parts);
 }
 
 template <int D>
@@ -544,9 +600,8 @@ cudaError_t launch_bf16(const StepArgs &a, const Parts &parts, cudaStream_t stre
     const unsigned grid = (unsigned)(a.N * a.Hk * ((G + heads - 1) / heads) * parts.splits);
     const float c = exp2_scale(a.scale);
     const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
-    if (heads == 8) step_mma_kernel<D, 1><<<grid, NT, 0, stream>>>(a, parts, c, flip);
-    else step_mma_kernel<D, 2><<<grid, NT, 0, stream>>>(a, parts, c, flip);
-    return cudaGetLastError();
+    if (heads == 8) return launch_parts(&step_mma_kernel<D, 1>, grid, stream, a, parts, c, flip);
+    return launch_parts(&step_mma_kernel<D, 2>, grid, stream, a, parts, c, flip);
 }
 
 template <int D>
@@ -554,7 +609,7 @@ cudaError_t launch(const StepArgs &a, void *ws, lr_dtype dt, cudaStream_t stream
     const StepPlan p = step_plan(a.N, a.Hq, a.Hk, a.max_len, a.window, a.sinks, dt);
     const Parts parts = parts_of(a, D, p, ws);
     const cudaError_t e = dt == LR_DT_F32 ? launch_f32<D>(a, parts, stream) : launch_bf16<D>(a, parts, stream);
-    if (e != cudaSuccess || p.splits == 1) return e;
+    if (e != cudaSuccess || p.splits == 1 || p.cluster) return e;
     const unsigned rows = (unsigned)(a.N * a.Hq);
     if (dt == LR_DT_F32) step_join_kernel<float, D><<<rows, D, 0, stream>>>(a, parts, 1.4426950408889634f);
     else step_join_kernel<__nv_bfloat16, D><<<rows, D, 0, stream>>>(a, parts, exp2_scale(a.scale));
@@ -569,21 +624,40 @@ StepPlan step_plan(int N, int Hq, int Hk, int max_len, int window, int sinks, lr
     // whole tiles in bf16: the sinks' and the window's first and last may be cut
     const long long most = w < max_len ? w + (dt == LR_DT_BF16 ? 2 * kTile + (sinks > 0 ? kTile : 0) : 0) : max_len;
     const int seen = (int)(most < max_len ? most : max_len);
-    // about four CTAs per SM in all, chunks of 128 to 2048 keys
-    const long long rows = (long long)N * Hk;
-    const long long want = (608 + rows - 1) / rows;
-    long long chunk = (seen + want - 1) / want;
-    chunk = (chunk + 63) / 64 * 64;
-    if (chunk < 128) chunk = 128;
-    if (chunk > kTile * kMostTiles) chunk = kTile * kMostTiles;
+    // CTAs that run at once: three per SM hold the registers of the bf16 kernel
+    // at d = 128 (more at smaller widths, where one wave matters less), four in fp32.
+    const long long rows = (long long)N * Hk, wave = 152 * (dt == LR_DT_BF16 ? 3 : 4);
+    auto cut = [](long long keys, long long parts) {  // chunks of whole 64s, 64 at least
+        const long long c = ((keys + parts - 1) / parts + 63) / 64 * 64;
+        return c < 64 ? 64 : c;
+    };
     StepPlan p;
+    // Chunks of 64 to 1024 keys that one wave holds (a wave and a third took
+    // 113 us on two 131K caches, one 87); for few rows up to 4096 keys, with
+    // more rows pieces of 1024, which even out sequences of different lengths
+    // (128 of 500 to 8192 keys: 355 us with 1024, 378 with 4096, 411 with 256).
+    long long chunk = cut(seen, rows < wave ? wave / rows : 1);
+    if (chunk > (4 * rows <= wave ? kTile * kMostTiles : 1024)) chunk = 1024;
     p.chunk = (int)chunk;
-    p.splits = (seen + p.chunk - 1) / p.chunk;
+    p.splits = (int)((seen + chunk - 1) / chunk);
+    // Eight chunks or fewer in one wave: a cluster joins them.  It does so too
+    // where 512 keys for a CTA still leave eight chunks: one launch less is
+    // worth more than the rest of the wave.
+    const long long eighth = cut(seen, kMostCluster);
+    p.cluster = false;
+    if (p.splits > 1 && rows * (p.splits < kMostCluster ? p.splits : kMostCluster) <= wave &&
+        (p.splits <= kMostCluster || eighth <= 512)) {
+        if (p.splits > kMostCluster) {
+            p.chunk = (int)eighth;
+            p.splits = (int)((seen + eighth - 1) / eighth);
+        }
+        p.cluster = p.splits > 1;
+    }
     return p;
 }
 
 size_t step_workspace_bytes(int N, int Hq, int d, const StepPlan &p) {
-    if (p.splits <= 1) return 0;
+    if (p.splits <= 1 || p.cluster) return 0;
     return (size_t)N * Hq * p.splits * ((size_t)d * 4 + 8);
 }
 

@@ -83,14 +83,14 @@ def win(**kw):
                            a['w'], a['s'], a['scale'], a['dt'], None)
 def step(**kw):
     a = dict(q=A[0], ck=A[1], cv=A[2], tab=A[3], lens=A[4], o=A[5], ws=A[6], wsb=1 << 26, N=3, Hq=4,
-             Hk=2, d=64, most_len=300, w=1 << 30, s=0, scale=0.5, dt=1, pages=9, page=16, most=32, cache=True)
+             Hk=2, d=64, most_len=9000, w=1 << 30, s=0, scale=0.5, dt=1, pages=9, page=16, most=600, cache=True)
     a.update(kw)
     c = Paged(a['ck'], a['cv'], a['tab'], a['pages'], a['page'], a['most'])
     return L.lr_step_paged(P(a['q']), ctypes.byref(c) if a['cache'] else None, P(a['lens']), P(a['o']), a['N'],
                            a['Hq'], a['Hk'], a['d'], a['most_len'], a['w'], a['s'], a['scale'], a['dt'],
                            P(a['ws']), a['wsb'], None)
 wsz = lambda *a: L.lr_step_paged_workspace_size(*a)
-need = wsz(3, 4, 2, 64, 300, 1 << 30, 0, 1)
+need = wsz(3, 4, 2, 64, 9000, 1 << 30, 0, 1)
 inf, nan = float('inf'), float('nan')
 cases = [
     ("rope-ok", rope(), 7), ("rope-nocache-ok", rope(cache=False, v=None), 7),
@@ -128,13 +128,14 @@ cases = [
     ("step-ok", step(), 7), ("step-dtype", step(dt=9), 3), ("step-d16", step(d=16), 6), ("step-N0", step(N=0), 2),
     ("step-heads", step(Hq=3), 2), ("step-window", step(w=0), 2), ("step-sinks", step(s=-2), 2),
     ("step-scale", step(scale=nan), 2), ("step-maxlen0", step(most_len=0), 2),
-    ("step-maxlen-table", step(most_len=16 * 32 + 1), 2), ("step-null", step(lens=None), 1),
+    ("step-maxlen-table", step(most_len=16 * 600 + 1), 2), ("step-null", step(lens=None), 1),
     ("step-null-cache", step(cache=False), 1), ("step-null-pool", step(cv=None), 1), ("step-page", step(page=512), 6),
     ("step-align", step(o=A[5] + 8), 4), ("step-alias-q", step(o=A[0]), 8), ("step-alias-pool", step(o=A[2] + 64), 8),
     ("step-ws-null", step(ws=None), 10), ("step-ws-short", step(wsb=need - 1), 10),
     ("step-ws-align", step(ws=A[6] + 8), 4), ("step-ws-alias", step(ws=A[5]), 8),
     ("step-many", step(N=1 << 30, Hq=4, Hk=4), 2),
-    ("ws-split", int(need > 0), 1), ("ws-one-chunk", wsz(3, 4, 2, 64, 100, 1 << 30, 0, 1), 0),
+    ("ws-split", int(need > 0), 1), ("ws-one-chunk", wsz(3, 4, 2, 64, 64, 1 << 30, 0, 1), 0),
+    ("ws-cluster", wsz(3, 4, 2, 64, 300, 1 << 30, 0, 1), 0),
     ("ws-window", wsz(3, 4, 2, 64, 30000, 60, 4, 1), 0), ("ws-bad", wsz(3, 4, 3, 64, 300, 1, 0, 1), 0),
     ("ws-overflow", int(wsz(1, 1, 1, 128, 1 << 30, 0x7fffffff, 0x7fffffff, 0) > 0), 1),
 ]

@@ -284,6 +284,20 @@ LENS = [1, 0, 15, 16, 17, -1, 127, 128, 129, 300, 601]
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("max_len,window,sinks", [(64, NW, 0), (65, NW, 0), (700, NW, 0), (4096, NW, 0), (4097, NW, 0),
+                                                  (20000, 300, 0), (20000, 300, 7), (20000, 4000, 64)])
+def test_step_cut_by_the_bound_on_the_length(dev, dtype, max_len, window, sinks):
+    """The same short and long sequences under bounds that give one chunk, a
+    cluster's few, and many joined by a kernel."""
+    lens = [x for x in (1, 0, 64, -1, 63, 700, 4096, 7000) if x <= max_len]
+    kc, vc, table = paged(21, lens, 2, 64, 64, dtype, dev)
+    wide = torch.zeros(len(lens), -(-max_len // 64), dtype=torch.int32, device=dev)
+    most = min(wide.shape[1], table.shape[1])
+    wide[:, :most] = table[:, :most]
+    check_step(dev, rnd(37, len(lens), 6, 64, dtype=dtype), kc, vc, wide, lens, window, sinks, max_len=max_len)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("d", [32, 64, 128])
 @pytest.mark.parametrize("Hq,Hk", [(1, 1), (4, 2), (3, 1), (8, 1), (5, 1), (17, 1), (6, 6)])
 @pytest.mark.parametrize("page,window,sinks", [(16, NW, 0), (64, 40, 5), (128, 130, 20)])
@@ -586,13 +600,13 @@ def test_prompt_then_steps_together(dev, dtype, window, sinks):
 def test_operators_capture_into_graphs_and_follow_their_inputs(dev):
     """One graph of append + step replayed as its lengths, positions and
     inputs change; a second graph shares the workspace on the same stream."""
-    B, Hq, Hk, d, page, most = 2, 4, 1, 128, 16, 60
+    B, Hq, Hk, d, page, most = 2, 4, 1, 128, 16, 400
     f = torch.tensor(10000.0 ** (-np.arange(64) / 64), device=dev)
     table = torch.arange(B * most, dtype=torch.int32, device=dev).view(B, most)
     kc, vc = (rnd(s, B * most, Hk, page, d, dtype=BF16).to(dev) for s in (60, 61))
     x = rnd(62, B, 1, Hq + 2 * Hk, d, dtype=BF16).to(dev)
-    pos = torch.tensor([[900], [4]], dtype=torch.int32, device=dev)
-    lens = torch.tensor([901, 5], dtype=torch.int32, device=dev)
+    pos = torch.tensor([[5900], [4]], dtype=torch.int32, device=dev)
+    lens = torch.tensor([5901, 5], dtype=torch.int32, device=dev)
     ws = torch.empty(lr.step_paged_workspace_size(B, Hq, Hk, d, most * page, BF16), dtype=torch.uint8, device=dev)
     assert ws.numel() > 0
 
@@ -606,7 +620,7 @@ def test_operators_capture_into_graphs_and_follow_their_inputs(dev):
     once(None), once(700)
     torch.cuda.synchronize()
     graphs, outs = [], []
-    for window in (None, 700):
+    for window in (None, 700):   # chunks joined by a kernel, and by a cluster
         g = torch.cuda.CUDAGraph()
         with torch.cuda.graph(g):
             outs.append(once(window))
