@@ -4,13 +4,16 @@
 // A row (one head of one token) is held by d / 8 lanes of a warp, eight
 // channels each, so that its sum of squares and the partner channels of the
 // split-half rotation come from shuffles.  The angles of a token are the same
-// for all its heads: a CTA takes a few tokens, forms their cosines and sines
-// once in shared memory and then streams the rows of all their heads.
+// for all its heads: a lane forms the cosines and sines of its channels once
+// and then walks the heads of its token, several rows in flight; no lane waits
+// for another outside the shuffles.  With few tokens the lanes of a CTA are
+// shared out over the heads instead.
 //
 // Angle: th = p f.  With s = frac(f / 2 pi) as a 64-bit fixed-point fraction
 // of a turn, p s mod 2^64 is the exact fraction of the product, so the only
 // errors are those of s (2^-53 relative) and of the final fp32 conversion
-// (2^-25 of a half turn), whatever the position.
+// (2^-25 of a half turn), whatever the position.  s is formed once per CTA: it
+// takes the fp64 pipe, which does two operations a cycle.
 #include "attn_internal.cuh"
 
 namespace lr {
@@ -19,7 +22,12 @@ namespace {
 __device__ unsigned g_rope_error = 0;
 
 constexpr int NT = 256;
-constexpr int kMostTokens = 16;  // tokens of one CTA
+// Rows in flight per lane, and CTAs per SM: the reads are what bounds the
+// kernel, and both hold them in flight.  On 2 x 16384 tokens of 16 + 4 heads
+// (bf16, 336 MB): 4 rows and 3 CTAs 72 us, 2 rows and 4 CTAs 79, 4 rows and 2
+// CTAs 85.  fp32 rows take twice the registers: two CTAs.
+constexpr int U = 4;
+template <typename E> constexpr int kCtas = sizeof(E) == 2 ? 3 : 2;
 
 struct RopeArgs {
     const void *q, *k, *v;
@@ -28,167 +36,199 @@ struct RopeArgs {
     lr_strides qs, ks, vs;
     QkMaps maps;
     int T, Hq, Hk, num_pages, page_log2, max_pages;
-    int tokens;  // per CTA
-    int rows;    // rows of a token: Hq + Hk (+ Hk values with a cache)
+    int tokens;  // of a group: a power of two
     int total;   // B * T
 };
 
-// Eight consecutive channels as fp32.
-__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
-    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __nv_bfloat16 *p, float (&x)[8]) {
-    const uint4 r = *reinterpret_cast<const uint4 *>(p);
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        x[2 * i] = __uint_as_float(w[i] << 16);
-        x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+// Eight consecutive channels of a row as they are moved (16 or 32 bytes a
+// lane) and as fp32 pairs.
+template <typename E> struct Row8;
+template <> struct Row8<float> {
+    float2 x[4];
+    __device__ __forceinline__ float2 pair(int i) const { return x[i]; }
+    __device__ __forceinline__ void set(int i, float2 v) { x[i] = v; }
+    // the same channels of another lane
+    __device__ __forceinline__ float2 pair_of(int i, int lane) const {
+        return make_float2(__shfl_sync(0xffffffffu, x[i].x, lane), __shfl_sync(0xffffffffu, x[i].y, lane));
     }
+};
+template <> struct Row8<__nv_bfloat16> {
+    uint32_t x[4];
+    __device__ __forceinline__ float2 pair(int i) const { return unpack2(x[i]); }
+    __device__ __forceinline__ void set(int i, float2 v) { x[i] = pack2(v.x, v.y); }
+    __device__ __forceinline__ float2 pair_of(int i, int lane) const {
+        return unpack2(__shfl_sync(0xffffffffu, x[i], lane));
+    }
+};
+__device__ __forceinline__ Row8<float> fetch(const float *p) {
+    const float4 a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+    return {{{a.x, a.y}, {a.z, a.w}, {b.x, b.y}, {b.z, b.w}}};
 }
-__device__ __forceinline__ void store8(float *p, const float (&x)[8]) {
-    *reinterpret_cast<float4 *>(p) = make_float4(x[0], x[1], x[2], x[3]);
-    *reinterpret_cast<float4 *>(p + 4) = make_float4(x[4], x[5], x[6], x[7]);
+__device__ __forceinline__ Row8<__nv_bfloat16> fetch(const __nv_bfloat16 *p) {
+    const uint4 a = *reinterpret_cast<const uint4 *>(p);
+    return {{a.x, a.y, a.z, a.w}};
 }
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
+__device__ __forceinline__ void put(float *p, const Row8<float> &r) {
+    *reinterpret_cast<float4 *>(p) = make_float4(r.x[0].x, r.x[0].y, r.x[1].x, r.x[1].y);
+    *reinterpret_cast<float4 *>(p + 4) = make_float4(r.x[2].x, r.x[2].y, r.x[3].x, r.x[3].y);
 }
-__device__ __forceinline__ void store8(__nv_bfloat16 *p, const float (&x)[8]) {
-    *reinterpret_cast<uint4 *>(p) =
-        make_uint4(pack2(x[0], x[1]), pack2(x[2], x[3]), pack2(x[4], x[5]), pack2(x[6], x[7]));
+__device__ __forceinline__ void put(__nv_bfloat16 *p, const Row8<__nv_bfloat16> &r) {
+    *reinterpret_cast<uint4 *>(p) = make_uint4(r.x[0], r.x[1], r.x[2], r.x[3]);
 }
 
 template <typename E, int D>
-__global__ void __launch_bounds__(NT) qk_norm_rope_kernel(RopeArgs a) {
-    constexpr int LANES = D / 8;       // lanes of a row
-    constexpr int ROWS = NT / LANES;   // rows in flight
-    __shared__ float2 cs[kMostTokens][D / 2];
-    __shared__ int pos[kMostTokens];
-    __shared__ long long slot[kMostTokens];  // first cache row of the token (head 0), -1: none
-    const int tid = threadIdx.x;
-    const int n0 = blockIdx.x * a.tokens;
-    const int nt = min(a.tokens, a.total - n0);
-    const int half = a.maps.rot >> 1;
+__global__ void __launch_bounds__(NT, kCtas<E>) qk_norm_rope_kernel(RopeArgs a) {
+    constexpr int LANES = D / 8;      // lanes of a row
+    constexpr int ROWS = NT / LANES;  // rows at once: tokens x head parts
+    __shared__ unsigned long long step[D / 2];
+    const int tid = threadIdx.x, half = a.maps.rot >> 1;
+    const bool norm = a.maps.flags & LR_QK_NORM, inter = a.maps.flags & LR_QK_INTERLEAVED;
+    // the lane's place: channels c0.., token `mine` of the group, every parts-th head
+    const int c0 = tid % LANES * 8, row = tid / LANES;
+    const int mine = row & (a.tokens - 1), part = row / a.tokens, parts = ROWS / a.tokens;
+    const bool turns_here = c0 < a.maps.rot, low = c0 < half;
+    // split halves: the partner channel c +- half sits half / 8 lanes away
+    const int hop = turns_here && !inter ? (low ? half : -half) : 0;
+    const int from = (tid & 31) + hop / 8;
+    if (tid < half) {
+        double turns = a.maps.inv_freq[tid] * 0.15915494309189533577;  // 1 / (2 pi)
+        turns -= floor(turns);
+        step[tid] = __double2ull_rz(turns * 18446744073709551616.0);
+    }
+    __syncthreads();
 
-    for (int i = tid; i < nt; i += NT) {
-        const int n = n0 + i, b = n / a.T;
-        const int p = a.positions ? a.positions[n] : n - b * a.T;
-        pos[i] = p;
-        long long s = -1;
-        if (a.ck && p >= 0) {
+    const int groups = (a.total + a.tokens - 1) / a.tokens;
+    for (int group = blockIdx.x; group < groups; group += gridDim.x) {
+        const int n0 = group * a.tokens + mine, n = n0 < a.total ? n0 : a.total - 1;
+        const int b = n / a.T, t = n - b * a.T;
+        const int p = a.positions ? a.positions[n] : t;
+        const bool on = n0 < a.total && p >= 0;
+        auto fetch_rows = [&](Row8<E>(&r)[U], const E *src, long long stride, int count, int h0) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                r[u] = Row8<E>{};
+                if (on && h0 + u * parts < count) r[u] = fetch(src + (h0 + u * parts) * stride);
+            }
+        };
+        // the first rows are on their way while the angles are formed
+        const E *q_from = static_cast<const E *>(a.q) + b * a.qs.b + t * a.qs.t + c0;
+        Row8<E> r[U];
+        fetch_rows(r, q_from, a.qs.h, a.Hq, part);
+        long long place = -1;  // first cache row of the token (head 0)
+        if (a.ck && on) {
             const int pg = p >> a.page_log2;
             const int page = pg < a.max_pages ? a.table[(size_t)b * a.max_pages + pg] : -1;
             if (page >= 0 && page < a.num_pages)
-                s = (((long long)page * a.Hk) << a.page_log2) + (p & ((1 << a.page_log2) - 1));
+                place = (((long long)page * a.Hk) << a.page_log2) + (p & ((1 << a.page_log2) - 1));
             else
                 atomicOr(&g_rope_error, kAttnIndex);
         }
-        slot[i] = s;
-    }
-    __syncthreads();
-    if (half) {
-        for (int i = tid; i < nt * half; i += NT) {
-            const int t = i / half, c = i - t * half;
-            double turns = a.maps.inv_freq[c] * 0.15915494309189533577;  // 1 / (2 pi)
-            turns -= floor(turns);
-            const unsigned long long step = __double2ull_rz(turns * 18446744073709551616.0);
-            const unsigned long long phase = step * (unsigned long long)(long long)pos[t];
+        float co[8], si[8];  // of the lane's channels, the partner's sign in si
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            co[i] = 1.f, si[i] = 0.f;
+            if (!turns_here) continue;
+            if (inter && (i & 1)) {
+                co[i] = co[i - 1], si[i] = -si[i - 1];
+                continue;
+            }
+            const int c = inter ? (c0 + i) >> 1 : (low ? c0 + i : c0 + i - half);
+            const unsigned long long phase = step[c] * (unsigned long long)(long long)p;
             // signed half turns in [-1, 1)
             const float x = (float)(int)(phase >> 32) * 4.656612873077392578125e-10f;  // 2^-31
-            float sn, cn;
-            sincospif(x, &sn, &cn);
-            cs[t][c] = make_float2(cn, sn);
+            sincospif(x, &si[i], &co[i]);
+            if (inter || low) si[i] = -si[i];
         }
-    }
-    __syncthreads();
-
-    const int lane = tid % LANES, c0 = lane * 8;
-    const int r0 = blockIdx.y * ROWS + tid / LANES;
-    // every lane of a warp takes part in the shuffles: rows past the end compute nothing kept
-    const int all = nt * a.rows;
-    const int step = gridDim.y * ROWS;
-    for (int base = 0; base < all; base += step) {
-        const int r = base + r0;
-        const bool live = r < all;
-        const int head = live ? r / nt : 0, t = live ? r - head * nt : 0;
-        const int n = n0 + t, b = n / a.T, tt = n - b * a.T;
-        const bool is_q = head < a.Hq, is_v = head >= a.Hq + a.Hk;
-        const int h = is_q ? head : (is_v ? head - a.Hq - a.Hk : head - a.Hq);
-        const bool on = live && pos[t] >= 0;
-        const lr_strides &st = is_q ? a.qs : (is_v ? a.vs : a.ks);
-        const E *src = static_cast<const E *>(is_q ? a.q : (is_v ? a.v : a.k)) + b * st.b +
-                       h * st.h + tt * st.t + c0;
-        float x[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        if (on) load8(src, x);
-        if (a.maps.flags & LR_QK_NORM) {
-            float ss = 0.f;
+        // All heads of queries or keys, the first rows already in r; `keep`
+        // stores a finished row.  A pair of channels becomes
+        // (x wc + partner ws) / rms, the weight in the rotation's factors.
+        auto heads = [&](const E *src, long long stride, int count, const float *weight, auto keep) {
+            float2 wc[4], ws[4];
 #pragma unroll
-            for (int i = 0; i < 8; ++i) ss += x[i] * x[i];
-#pragma unroll
-            for (int m = 1; m < LANES; m <<= 1) ss += __shfl_xor_sync(0xffffffffu, ss, m);
-            if (!is_v) {
-                const float inv = 1.f / sqrtf(ss * (1.f / D) + a.maps.eps);
-                const float *w = is_q ? a.maps.qw : a.maps.kw;
-                float wv[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-                if (w) load8(w + c0, wv);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] *= inv * wv[i];
+            for (int i = 0; i < 8; ++i) {
+                const int c = c0 + i;
+                const float w = weight ? weight[c] : 1.f;
+                const float pw = weight ? weight[inter ? c ^ 1 : c + hop] : 1.f;
+                float &fc = i & 1 ? wc[i / 2].y : wc[i / 2].x, &fs = i & 1 ? ws[i / 2].y : ws[i / 2].x;
+                fc = w * co[i], fs = pw * si[i];
             }
-        }
-        if (half) {
-            if (a.maps.flags & LR_QK_INTERLEAVED) {
-                if (!is_v && c0 < a.maps.rot) {
+#pragma unroll 1
+            for (int h0 = part; h0 - part < count; h0 += parts * U) {
+                if (h0 != part) fetch_rows(r, src, stride, count, h0);
+#pragma unroll
+                for (int u = 0; u < U; ++u) {
+                    if (h0 - part + u * parts >= count) break;  // for all lanes
+                    float inv = 1.f;
+                    if (norm) {
+                        float2 ss = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) ss = fma2(r[u].pair(i), r[u].pair(i), ss);
+                        float sum = ss.x + ss.y;
+#pragma unroll
+                        for (int m = 1; m < LANES; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+                        inv = rsqrtf(sum * (1.f / D) + a.maps.eps);
+                    }
+                    const float2 inv2 = make_float2(inv, inv);
+                    Row8<E> y;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float2 f = cs[t][(c0 >> 1) + i];
-                        const float u = x[2 * i], w = x[2 * i + 1];
-                        x[2 * i] = u * f.x - w * f.y;
-                        x[2 * i + 1] = w * f.x + u * f.y;
+                        const float2 x = r[u].pair(i);
+                        float2 z = mul2(x, wc[i]);
+                        if (half) {
+                            // where nothing turns the partner is not looked at (it may be infinite)
+                            float2 w = inter ? make_float2(x.y, x.x) : r[u].pair_of(i, from);
+                            if (!turns_here) w = make_float2(0.f, 0.f);
+                            z = fma2(w, ws[i], z);
+                        }
+                        y.set(i, mul2(z, inv2));
                     }
-                }
-            } else {
-                // the partner channel c +- half sits half / 8 lanes away
-                const int hl = half >> 3;
-                const bool lo = c0 < half;
-                const int from = (tid & 31) + (c0 < a.maps.rot ? (lo ? hl : -hl) : 0);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float y = __shfl_sync(0xffffffffu, x[i], from);
-                    if (!is_v && c0 < a.maps.rot) {
-                        const float2 f = cs[t][lo ? c0 + i : c0 - half + i];
-                        x[i] = lo ? x[i] * f.x - y * f.y : x[i] * f.x + y * f.y;
-                    }
+                    if (on && h0 + u * parts < count) keep(h0 + u * parts, y);
                 }
             }
-        }
-        if (!on) continue;
-        if (is_q) {
-            store8(static_cast<E *>(a.qo) + (((size_t)b * a.Hq + h) * a.T + tt) * D + c0, x);
-        } else {
-            if (!is_v && a.ko)
-                store8(static_cast<E *>(a.ko) + (((size_t)b * a.Hk + h) * a.T + tt) * D + c0, x);
-            if (a.ck && slot[t] >= 0)
-                store8(static_cast<E *>(is_v ? a.cv : a.ck) +
-                           ((size_t)slot[t] + ((size_t)h << a.page_log2)) * D + c0, x);
+        };
+        E *q_to = static_cast<E *>(a.qo) + ((size_t)b * a.Hq * a.T + t) * D + c0;
+        heads(q_from, a.qs.h, a.Hq, a.maps.qw,
+              [&](int h, const Row8<E> &y) { put(q_to + (size_t)h * a.T * D, y); });
+        const E *k_from = static_cast<const E *>(a.k) + b * a.ks.b + t * a.ks.t + c0;
+        fetch_rows(r, k_from, a.ks.h, a.Hk, part);
+        E *k_to = a.ko ? static_cast<E *>(a.ko) + ((size_t)b * a.Hk * a.T + t) * D + c0 : nullptr;
+        E *kept = place >= 0 ? static_cast<E *>(a.ck) + place * D + c0 : nullptr;
+        heads(k_from, a.ks.h, a.Hk, a.maps.kw, [&](int h, const Row8<E> &y) {
+            if (k_to) put(k_to + (size_t)h * a.T * D, y);
+            if (kept) put(kept + ((size_t)h << a.page_log2) * D, y);
+        });
+        if (a.ck) {
+            const E *v_from = static_cast<const E *>(a.v) + b * a.vs.b + t * a.vs.t + c0;
+            E *to = static_cast<E *>(a.cv) + place * D + c0;
+#pragma unroll 1
+            for (int h0 = part; h0 < a.Hk; h0 += parts * U) {
+                fetch_rows(r, v_from, a.vs.h, a.Hk, h0);
+#pragma unroll
+                for (int u = 0; u < U; ++u)
+                    if (place >= 0 && h0 + u * parts < a.Hk)
+                        put(to + ((size_t)(h0 + u * parts) << a.page_log2) * D, r[u]);
+            }
         }
     }
 }
 
-template <typename E>
-cudaError_t launch(const RopeArgs &a, int d, cudaStream_t stream) {
-    const int gx = (a.total + a.tokens - 1) / a.tokens;
-    const int in_flight = NT / (d / 8);
-    // few tokens: their rows are spread over more CTAs
-    int gy = 1;
-    while (gx * gy < 304 && gy * in_flight < a.tokens * a.rows) gy *= 2;
-    const dim3 grid(gx, gy);
-    if (d == 32) qk_norm_rope_kernel<E, 32><<<grid, NT, 0, stream>>>(a);
-    else if (d == 64) qk_norm_rope_kernel<E, 64><<<grid, NT, 0, stream>>>(a);
-    else qk_norm_rope_kernel<E, 128><<<grid, NT, 0, stream>>>(a);
+template <typename E, int D>
+cudaError_t launch(RopeArgs &a, cudaStream_t stream) {
+    // as many tokens at once as leave two CTAs for every SM
+    constexpr int ROWS = NT / (D / 8);
+    a.tokens = 1;
+    while (a.tokens < ROWS && (a.total + a.tokens - 1) / a.tokens > 304) a.tokens *= 2;
+    const int groups = (a.total + a.tokens - 1) / a.tokens;
+    const int most = 152 * kCtas<E>;
+    qk_norm_rope_kernel<E, D><<<groups < most ? groups : most, NT, 0, stream>>>(a);
     return cudaGetLastError();
+}
+
+template <typename E>
+cudaError_t launch_d(RopeArgs &a, int d, cudaStream_t stream) {
+    if (d == 32) return launch<E, 32>(a, stream);
+    if (d == 64) return launch<E, 64>(a, stream);
+    return launch<E, 128>(a, stream);
 }
 
 }  // namespace
@@ -203,17 +243,13 @@ cudaError_t launch_qk_norm_rope(const void *q, lr_strides qs, const void *k, lr_
     a.qs = qs, a.ks = ks, a.vs = vs;
     a.maps = maps;
     a.T = T, a.Hq = Hq, a.Hk = Hk;
-    a.rows = Hq + Hk;
     if (cache) {
         a.ck = cache->k, a.cv = cache->v, a.table = cache->table;
         a.num_pages = cache->num_pages, a.max_pages = cache->max_pages;
         while ((1 << a.page_log2) < cache->page) ++a.page_log2;
-        a.rows += Hk;
     }
     a.total = B * T;
-    a.tokens = kMostTokens;
-    while (a.tokens > 1 && (a.total + a.tokens - 1) / a.tokens < 608) a.tokens /= 2;
-    return dt == LR_DT_F32 ? launch<float>(a, d, stream) : launch<__nv_bfloat16>(a, d, stream);
+    return dt == LR_DT_F32 ? launch_d<float>(a, d, stream) : launch_d<__nv_bfloat16>(a, d, stream);
 }
 
 int attn_errors_rope() {
