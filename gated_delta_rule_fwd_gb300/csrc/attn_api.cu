@@ -236,7 +236,7 @@ lr_status lr_fwd_window(const void *q, lr_strides qs, const void *k, lr_strides 
                        scale};
     if (Tk == 0) return done(launch_window_zero(a, d, dt, stream));
     return done(dt == LR_DT_BF16 ? launch_window_tc(a, d, stream)
-                                 : launch_window_simt(a, d, stream));
+                                 : launch_window_f32(a, d, stream));
 }
 
 size_t lr_step_paged_workspace_size(int N, int Hq, int Hk, int d, int max_len, int window,

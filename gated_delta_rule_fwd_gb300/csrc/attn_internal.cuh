@@ -104,11 +104,11 @@ struct WindowArgs {
     int B, Hq, Hk, Tq, Tk, window, sinks;
     float scale;
 };
-// CUDA cores, fp32 (window_simt.cu).
-cudaError_t launch_window_simt(const WindowArgs &a, int d, cudaStream_t stream);
+// fp32, Tk >= 1 (window_f32.cu).
+cudaError_t launch_window_f32(const WindowArgs &a, int d, cudaStream_t stream);
 // Tensor cores, bf16, Tk >= 1 (window_tc.cu).
 cudaError_t launch_window_tc(const WindowArgs &a, int d, cudaStream_t stream);
-// Zeros in every row that is written (Tk == 0), either type (window_simt.cu).
+// Zeros in every row that is written (Tk == 0), either type (window_f32.cu).
 cudaError_t launch_window_zero(const WindowArgs &a, int d, lr_dtype dt, cudaStream_t stream);
 
 struct StepArgs {
@@ -130,7 +130,7 @@ cudaError_t launch_step_paged(const StepArgs &a, int d, lr_dtype dt, void *ws, c
 
 // Return and clear the error bits of each unit (-1: the device could not be read).
 int attn_errors_rope();
-int attn_errors_window_simt();
+int attn_errors_window_f32();
 int attn_errors_window_tc();
 int attn_errors_step();
 

@@ -399,7 +399,7 @@ lr_status lr_device_status(void) {
     const int e = read_and_clear_tc_error(), eg = read_and_clear_gd_tc_error();
     if (e < 0 || eg < 0) return LR_ERR_CUDA;
     unsigned attn = 0;
-    for (int a : {attn_errors_rope(), attn_errors_window_simt(),
+    for (int a : {attn_errors_rope(), attn_errors_window_f32(),
                   attn_errors_window_tc(), attn_errors_step()}) {
         if (a < 0) return LR_ERR_CUDA;
         attn |= (unsigned)a;
