@@ -6,9 +6,15 @@
 // accumulation: what is left out is 2^-22 of it, so the result is that of fp32
 // arithmetic.  Three tf32 products are 100 TFLOP/s on this GPU, the CUDA cores'
 // fp32 peak is 74 and in a tiled kernel they are held up by shared memory.
+// The products' accumulators are cut, not rounded, so long sums in them drift
+// (2e-6 of the output when the whole sum stayed there, 4e-7 now): only a few
+// products are summed there and then added in ordinary fp32.
 //
-// A CTA of 4 warps holds 64 query rows of one head, 16 per warp, in registers.
-// Tiles of 32 keys and values come by asynchronous copies into two buffers.
+// A CTA holds 64 query rows of one head, 16 per warp, in registers; tiles of
+// 32 keys and values come by asynchronous copies into two buffers.  At d = 128,
+// where registers leave eight warps to an SM, two groups of four warps hold the
+// same rows and take every other tile; their parts are joined at the end (8
+// heads x 2048 rows, causal: 228 -> 159 us; at d = 64 one group is 6 % faster).
 // The order of channels inside a product, and of keys inside the second one,
 // is free: it is chosen so that every lane reads 16 contiguous bytes of a row
 // without bank conflicts, and the weights stay in the registers that the
@@ -22,14 +28,20 @@ namespace {
 
 __device__ unsigned g_window_error = 0;
 
-constexpr int BQ = 64, BK = 32, NT = 128;
+constexpr int BQ = 64, BK = 32, GT = 128;  // GT: threads of a group
 
-template <int D>
+template <int D, int G>
 struct Smem {
     static constexpr int KS = D + 16, VS = D + 4;  // floats of a row: see the fragment loads
-    float k[2][BK * KS];
-    float v[2][BK * VS];
+    struct Group {
+        float k[2][BK * KS];
+        float v[2][BK * VS];
+    } group[G];
+    static_assert(G == 1 || sizeof(Group) >= GT * (D / 2 + 4) * sizeof(float), "room for a group's part");
 };
+__device__ __forceinline__ void group_sync(int group) {
+    asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(GT) : "memory");
+}
 
 __device__ __forceinline__ void copy16(float *dst, const float *src, bool on) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(tc::smem_u32(dst)), "l"(src),
@@ -51,19 +63,20 @@ __device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo) {
 // A[g][t+4], A[g+8][t+4]}, b = {B[t][g], B[t+4][g]}, d = {D[g][2t], D[g][2t+1],
 // D[g+8][2t], D[g+8][2t+1]}.
 __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.tf32.tf32.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
         "{%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D>
-__global__ void __launch_bounds__(NT) window_f32_kernel(WindowArgs a, float c, float sign) {
+template <int D, int G>
+__global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float c, float sign) {
     extern __shared__ __align__(16) uint8_t raw[];
-    using S = Smem<D>;
+    using S = Smem<D, G>;
     S &sm = *reinterpret_cast<S *>(raw);
-    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    const int group = G == 1 ? 0 : threadIdx.x / GT, tid = threadIdx.x % GT, warp = tid >> 5, lane = tid & 31,
+              g = lane >> 2, t = lane & 3;
+    typename S::Group &buf = sm.group[group];
 
     const int tiles = (a.Tq + BQ - 1) / BQ;
     // the last rows see the most keys: of all heads they start first
@@ -72,7 +85,7 @@ __global__ void __launch_bounds__(NT) window_f32_kernel(WindowArgs a, float c, f
     const int b = bh / a.Hq, h = bh - b * a.Hq, hk = h / (a.Hq / a.Hk);
     bool bad = false;
     const int ql = clamp_len(a.q_len, b, a.Tq, &bad), kl = clamp_len(a.k_len, b, a.Tk, &bad);
-    if (bad && tid == 0) atomicOr(&g_window_error, kAttnIndex);
+    if (bad && threadIdx.x == 0) atomicOr(&g_window_error, kAttnIndex);
     const int i0 = tile * BQ;
     if (i0 >= ql) return;
     const int rows = min(BQ, ql - i0), p0 = kl - ql + i0;
@@ -91,17 +104,17 @@ __global__ void __launch_bounds__(NT) window_f32_kernel(WindowArgs a, float c, f
     // keys and values past the tile's limit are zeros
     auto load = [&](int it) {
         const int k0 = key0(it), end = limit(it);
-        float *kd = sm.k[it & 1], *vd = sm.v[it & 1];
+        float *kd = buf.k[(it / G) & 1], *vd = buf.v[(it / G) & 1];
 #pragma unroll
-        for (int i = 0; i < BK * D / 4 / NT; ++i) {
-            const int e = i * NT + tid, r = e / (D / 4), ch = (e - r * (D / 4)) * 4;
+        for (int i = 0; i < BK * D / 4 / GT; ++i) {
+            const int e = i * GT + tid, r = e / (D / 4), ch = (e - r * (D / 4)) * 4;
             const bool on = k0 + r < end;
             const long long row = on ? k0 + r : 0;
             copy16(kd + r * S::KS + ch, k + row * a.ks.t + ch, on);
             copy16(vd + r * S::VS + ch, v + row * a.vs.t + ch, on);
         }
     };
-    if (n > 0) load(0);
+    if (group < n) load(group);
     copies_commit();
 
     // queries: channels 16 i + 4 t .. + 3 of rows g and g + 8, which are two
@@ -122,21 +135,21 @@ __global__ void __launch_bounds__(NT) window_f32_kernel(WindowArgs a, float c, f
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
 
-    for (int it = 0; it < n; ++it) {
-        if (it + 1 < n) load(it + 1);
+    for (int it = group; it < n; it += G) {
+        if (it + G < n) load(it + G);
         copies_commit();
         copies_wait<1>();
-        __syncthreads();
+        group_sync(group);
         const int k0 = key0(it), end = limit(it);
         // the warp's rows: positions pw .. pw + 15
         const bool some = k0 <= pw + 15 && ((long long)k0 + BK - 1 > (long long)pw - a.window || k0 < a.sinks);
         if (some) {
-            const float *ks = sm.k[it & 1], *vs = sm.v[it & 1];
-            float s[BK / 8][4];
+            const float *ks = buf.k[(it / G) & 1], *vs = buf.v[(it / G) & 1];
+            float s[BK / 8][4], low[BK / 8][4];  // low: the parts with a lo factor
 #pragma unroll
             for (int j = 0; j < BK / 8; ++j)
 #pragma unroll
-                for (int e = 0; e < 4; ++e) s[j][e] = 0.f;
+                for (int e = 0; e < 4; ++e) s[j][e] = low[j][e] = 0.f;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
                 uint32_t ah[2][4], al[2][4];
@@ -144,20 +157,34 @@ __global__ void __launch_bounds__(NT) window_f32_kernel(WindowArgs a, float c, f
                 split(qr[i][0].y, ah[0][2], al[0][2]), split(qr[i][1].y, ah[0][3], al[0][3]);
                 split(qr[i][0].z, ah[1][0], al[1][0]), split(qr[i][1].z, ah[1][1], al[1][1]);
                 split(qr[i][0].w, ah[1][2], al[1][2]), split(qr[i][1].w, ah[1][3], al[1][3]);
+                uint32_t bh_[BK / 8][4], bl[BK / 8][4];
 #pragma unroll
                 for (int j = 0; j < BK / 8; ++j) {
                     const float4 x = *reinterpret_cast<const float4 *>(ks + (8 * j + g) * S::KS + 16 * i + 4 * t);
-                    uint32_t bh_[4], bl[4];
-                    split(x.x, bh_[0], bl[0]), split(x.y, bh_[1], bl[1]);
-                    split(x.z, bh_[2], bl[2]), split(x.w, bh_[3], bl[3]);
+                    split(x.x, bh_[j][0], bl[j][0]), split(x.y, bh_[j][1], bl[j][1]);
+                    split(x.z, bh_[j][2], bl[j][2]), split(x.w, bh_[j][3], bl[j][3]);
+                }
+                float part[BK / 8][4];
+#pragma unroll
+                for (int j = 0; j < BK / 8; ++j) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) part[j][e] = 0.f;
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        mma_tf32(s[j], al[u], bh_[2 * u], bh_[2 * u + 1]);
-                        mma_tf32(s[j], ah[u], bl[2 * u], bl[2 * u + 1]);
-                        mma_tf32(s[j], ah[u], bh_[2 * u], bh_[2 * u + 1]);
+                        mma_tf32(part[j], ah[u], bh_[j][2 * u], bh_[j][2 * u + 1]);
+                        mma_tf32(low[j], al[u], bh_[j][2 * u], bh_[j][2 * u + 1]);
+                        mma_tf32(low[j], ah[u], bl[j][2 * u], bl[j][2 * u + 1]);
                     }
                 }
+#pragma unroll
+                for (int j = 0; j < BK / 8; ++j)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[j][e] += part[j][e];
             }
+#pragma unroll
+            for (int j = 0; j < BK / 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[j][e] += low[j][e];
             const bool whole = k0 + BK <= end && k0 + BK - 1 <= pw && (long long)k0 > (long long)pw + 15 - a.window;
             if (!whole) {
 #pragma unroll
@@ -169,6 +196,7 @@ __global__ void __launch_bounds__(NT) window_f32_kernel(WindowArgs a, float c, f
                         if (!seen) s[j][e] = -INFINITY;
                     }
             }
+            float f[2];  // of what the sums hold, as the maximum grows
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 float mx = -INFINITY;
@@ -177,7 +205,7 @@ __global__ void __launch_bounds__(NT) window_f32_kernel(WindowArgs a, float c, f
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
                 mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
                 const float mn = fmaxf(m[r], mx), base = mn == -INFINITY ? 0.f : mn;
-                const float f = m[r] == -INFINITY ? 0.f : ex2((m[r] - base) * c);
+                f[r] = m[r] == -INFINITY ? 0.f : ex2((m[r] - base) * c);
                 m[r] = mn;
                 float sum = 0.f;
 #pragma unroll
@@ -186,18 +214,24 @@ __global__ void __launch_bounds__(NT) window_f32_kernel(WindowArgs a, float c, f
                     s[j][2 * r + 1] = ex2((s[j][2 * r + 1] - base) * c);
                     sum += s[j][2 * r] + s[j][2 * r + 1];
                 }
-                l[r] = l[r] * f + sum;  // this lane's columns; joined at the end
-#pragma unroll
-                for (int j = 0; j < D / 8; ++j) acc[j][2 * r] *= f, acc[j][2 * r + 1] *= f;
+                l[r] = l[r] * f[r] + sum;  // this lane's columns; joined at the end
             }
             // weights of keys 8 j + 2 t and + 1 stand for k = t and t + 4
+            uint32_t ah[BK / 8][4], al[BK / 8][4];
 #pragma unroll
             for (int j = 0; j < BK / 8; ++j) {
-                uint32_t ah[4], al[4];
-                split(s[j][0], ah[0], al[0]), split(s[j][2], ah[1], al[1]);
-                split(s[j][1], ah[2], al[2]), split(s[j][3], ah[3], al[3]);
+                split(s[j][0], ah[j][0], al[j][0]), split(s[j][2], ah[j][1], al[j][1]);
+                split(s[j][1], ah[j][2], al[j][2]), split(s[j][3], ah[j][3], al[j][3]);
+            }
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i) {
+            for (int i = 0; i < D / 32; ++i) {
+                float high[4][4], small[4][4];
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) high[u][e] = small[u][e] = 0.f;
+#pragma unroll
+                for (int j = 0; j < BK / 8; ++j) {
                     const float4 x = *reinterpret_cast<const float4 *>(vs + (8 * j + 2 * t) * S::VS + 32 * i + 4 * g);
                     const float4 y = *reinterpret_cast<const float4 *>(vs + (8 * j + 2 * t + 1) * S::VS + 32 * i + 4 * g);
                     const float xv[4] = {x.x, x.y, x.z, x.w}, yv[4] = {y.x, y.y, y.z, y.w};
@@ -205,14 +239,47 @@ __global__ void __launch_bounds__(NT) window_f32_kernel(WindowArgs a, float c, f
                     for (int u = 0; u < 4; ++u) {
                         uint32_t b0h, b0l, b1h, b1l;
                         split(xv[u], b0h, b0l), split(yv[u], b1h, b1l);
-                        mma_tf32(acc[4 * i + u], al, b0h, b1h);
-                        mma_tf32(acc[4 * i + u], ah, b0l, b1l);
-                        mma_tf32(acc[4 * i + u], ah, b0h, b1h);
+                        mma_tf32(high[u], ah[j], b0h, b1h);
+                        mma_tf32(small[u], al[j], b0h, b1h);
+                        mma_tf32(small[u], ah[j], b0l, b1l);
                     }
                 }
+#pragma unroll
+                for (int u = 0; u < 4; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        acc[4 * i + u][e] = fmaf(acc[4 * i + u][e], f[e >> 1], high[u][e] + small[u][e]);
             }
         }
-        __syncthreads();  // the buffer is free for the tile after next
+        group_sync(group);  // the buffer is free for the tile after next
+    }
+    copies_wait<0>();
+    if constexpr (G == 2) {
+        // the second group hands its part over, each lane to its twin
+        __syncthreads();
+        float *part = reinterpret_cast<float *>(&sm.group[1]);
+        if (group == 1) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) part[(2 * r) * GT + tid] = m[r], part[(2 * r + 1) * GT + tid] = l[r];
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) part[(4 + 4 * j + e) * GT + tid] = acc[j][e];
+        }
+        __syncthreads();
+        if (group == 1) return;
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const float m1 = part[(2 * r) * GT + tid], l1 = part[(2 * r + 1) * GT + tid];
+            const float mn = fmaxf(m[r], m1);
+            const float f0 = m[r] == -INFINITY ? 0.f : ex2((m[r] - mn) * c), f1 = m1 == -INFINITY ? 0.f : ex2((m1 - mn) * c);
+            l[r] = l[r] * f0 + l1 * f1;
+#pragma unroll
+            for (int j = 0; j < D / 8; ++j)
+#pragma unroll
+                for (int e = 2 * r; e < 2 * r + 2; ++e)
+                    acc[j][e] = acc[j][e] * f0 + part[(4 + 4 * j + e) * GT + tid] * f1;
+        }
     }
     // columns 32 i + 8 t .. + 7 of rows g and g + 8
 #pragma unroll
@@ -251,14 +318,16 @@ __global__ void __launch_bounds__(NT) window_f32_kernel(WindowArgs a, float c, f
 
 template <int D>
 cudaError_t launch(const WindowArgs &a, int slot, cudaStream_t stream) {
-    auto *fn = window_f32_kernel<D>;
-    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(fn), sizeof(Smem<D>), slot);
+    constexpr int G = D == 128 ? 2 : 1;
+    auto *fn = window_f32_kernel<D, G>;
+    constexpr int bytes = sizeof(Smem<D, G>);
+    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(fn), bytes, slot);
     if (e != cudaSuccess) return e;
     const int tiles = (a.Tq + BQ - 1) / BQ;
     // scale 0 gives every key the same weight; a product with it would turn
     // the mask's -inf into NaN, and 2^-100 rounds to the same weights
     const float c = a.scale == 0.f ? 7.9e-31f : fabsf(a.scale) * 1.4426950408889634f;
-    fn<<<(unsigned)(a.B * a.Hq * tiles), NT, sizeof(Smem<D>), stream>>>(a, c, a.scale < 0.f ? -1.f : 1.f);
+    fn<<<(unsigned)(a.B * a.Hq * tiles), G * GT, bytes, stream>>>(a, c, a.scale < 0.f ? -1.f : 1.f);
     return cudaGetLastError();
 }
 
