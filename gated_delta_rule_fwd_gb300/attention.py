@@ -83,9 +83,8 @@ def _strided(t, name, shape, dtype, dev):
     return Strides(st[0], st[1], st[2])
 
 
-def _paged(k_cache, v_cache, table, rows, d, dtype, dev):
+def _paged(torch, k_cache, v_cache, table, rows, d, dtype, dev):
     """Pools [P, Hk, page, d] and a table [rows, max_pages]."""
-    import torch
     pool, most = k_cache.shape, table.shape
     if len(pool) != 4 or pool[3] != d:
         raise ValueError(f"k_cache must have shape (pages, heads, page, {d}), got {tuple(pool)}")
@@ -97,32 +96,18 @@ def _paged(k_cache, v_cache, table, rows, d, dtype, dev):
     return Paged(k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), pool[0], pool[2], most[1])
 
 
-class _Here:
-    def __enter__(self):
-        return None
-
-    def __exit__(self, *exc):
-        return None
-
-
-_HERE = _Here()
-
-
-def _on(stream, dev):
-    """Where a call allocates and launches: the given stream, or the device's
-    current one.  What is allocated inside belongs to that stream."""
-    import torch
+def _place(torch, stream, dev):
+    """The given stream, or the device's current one, made current: a call
+    allocates and launches there, and what it allocates belongs to it."""
     if stream is None:
-        return _HERE if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+        return torch.cuda.device(dev)
     if stream.device != dev:
         raise ValueError(f"stream must be on {dev}, got {stream.device}")
     return torch.cuda.stream(stream)
 
 
-def _handle(stream, dev):
-    import torch
-    if stream is not None:
-        return stream.cuda_stream
+def _handle(torch, dev):
+    """The current stream of the device."""
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
     return raw(dev.index) if raw else torch.cuda.current_stream(dev).cuda_stream
 
@@ -153,6 +138,12 @@ def lr_qk_norm_rope(q, k, positions=None, *, norm=True, q_weight=None, k_weight=
     base = _base()
     dev = q.device
     base._require_cuda(dev)
+    if stream is not None or torch.cuda.current_device() != dev.index:
+        with _place(torch, stream, dev):
+            return lr_qk_norm_rope(q, k, positions, norm=norm, q_weight=q_weight, k_weight=k_weight,
+                                   eps=eps, inv_freq=inv_freq, interleaved=interleaved, v=v,
+                                   k_cache=k_cache, v_cache=v_cache, table=table, write_k=write_k,
+                                   q_out=q_out, k_out=k_out)
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q and k must have shape (B, heads, T, d)")
     q_shape, k_shape, dtype = q.shape, k.shape, q.dtype
@@ -175,7 +166,7 @@ def lr_qk_norm_rope(q, k, positions=None, *, norm=True, q_weight=None, k_weight=
     if k_cache is not None or v_cache is not None or table is not None or v is not None:
         if k_cache is None or v_cache is None or table is None or v is None:
             raise ValueError("a cache needs v, k_cache, v_cache and table together")
-        cache = _paged(k_cache, v_cache, table, B, d, dtype, dev)
+        cache = _paged(torch, k_cache, v_cache, table, B, d, dtype, dev)
         if k_cache.shape[1] != Hk:
             raise ValueError(f"k_cache must have {Hk} heads, got {k_cache.shape[1]}")
         vs = _strided(v, "v", k_shape, dtype, dev)
@@ -191,16 +182,14 @@ def lr_qk_norm_rope(q, k, positions=None, *, norm=True, q_weight=None, k_weight=
                   None if q_weight is None else q_weight.data_ptr(),
                   None if k_weight is None else k_weight.data_ptr(), eps, rot,
                   None if inv_freq is None else inv_freq.data_ptr())
-    with _on(stream, dev):
-        if q_out is None:
-            q_out = torch.empty(q_shape, dtype=dtype, device=dev)
-        if k_out is None and write_k:
-            k_out = torch.empty(k_shape, dtype=dtype, device=dev)
-        st = base.lib().lr_qk_norm_rope(
-            q.data_ptr(), qs, k.data_ptr(), ks, None if positions is None else positions.data_ptr(),
-            maps, q_out.data_ptr(), None if k_out is None else k_out.data_ptr(),
-            None if v is None else v.data_ptr(), vs, cache, B, T, Hq, Hk, d, dt,
-            _handle(stream, dev))
+    if q_out is None:
+        q_out = torch.empty(q_shape, dtype=dtype, device=dev)
+    if k_out is None and write_k:
+        k_out = torch.empty(k_shape, dtype=dtype, device=dev)
+    st = base.lib().lr_qk_norm_rope(
+        q.data_ptr(), qs, k.data_ptr(), ks, None if positions is None else positions.data_ptr(),
+        maps, q_out.data_ptr(), None if k_out is None else k_out.data_ptr(),
+        None if v is None else v.data_ptr(), vs, cache, B, T, Hq, Hk, d, dt, _handle(torch, dev))
     if st != 0:
         raise base.LrError(st, "lr_qk_norm_rope")
     return q_out, k_out
@@ -222,6 +211,10 @@ def lr_fwd_window(q, k, v, *, window=None, sinks=0, q_len=None, k_len=None, scal
     base = _base()
     dev = q.device
     base._require_cuda(dev)
+    if stream is not None or torch.cuda.current_device() != dev.index:
+        with _place(torch, stream, dev):
+            return lr_fwd_window(q, k, v, window=window, sinks=sinks, q_len=q_len, k_len=k_len,
+                                 scale=scale, o=o)
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q, k and v must have shape (B, heads, T, d)")
     q_shape, dtype = q.shape, q.dtype
@@ -239,15 +232,13 @@ def lr_fwd_window(q, k, v, *, window=None, sinks=0, q_len=None, k_len=None, scal
     window = NO_WINDOW if window is None else _int32(window, "window")
     sinks = _int32(sinks, "sinks")
     scale = d ** -0.5 if scale is None else scale
-    with _on(stream, dev):
-        if o is None:
-            o = (torch.empty if q_len is None else torch.zeros)(q_shape, dtype=dtype, device=dev)
-            os_ = _strided(o, "o", q_shape, dtype, dev)
-        st = base.lib().lr_fwd_window(
-            q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
-            None if q_len is None else q_len.data_ptr(),
-            None if k_len is None else k_len.data_ptr(), o.data_ptr(), os_, B, Hq, Hk, Tq, Tk, d,
-            window, sinks, scale, dt, _handle(stream, dev))
+    if o is None:
+        o = (torch.empty if q_len is None else torch.zeros)(q_shape, dtype=dtype, device=dev)
+        os_ = _strided(o, "o", q_shape, dtype, dev)
+    st = base.lib().lr_fwd_window(
+        q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs,
+        None if q_len is None else q_len.data_ptr(), None if k_len is None else k_len.data_ptr(),
+        o.data_ptr(), os_, B, Hq, Hk, Tq, Tk, d, window, sinks, scale, dt, _handle(torch, dev))
     if st != 0:
         raise base.LrError(st, "lr_fwd_window")
     return o
@@ -285,13 +276,17 @@ def lr_step_paged(q, k_cache, v_cache, table, lens, *, max_len=None, window=None
     base = _base()
     dev = q.device
     base._require_cuda(dev)
+    if stream is not None or torch.cuda.current_device() != dev.index:
+        with _place(torch, stream, dev):
+            return lr_step_paged(q, k_cache, v_cache, table, lens, max_len=max_len, window=window,
+                                 sinks=sinks, scale=scale, o=o, workspace=workspace)
     if q.dim() != 3:
         raise ValueError("q must have shape (N, heads, d)")
     q_shape, dtype = q.shape, q.dtype
     N, Hq, d = q_shape
     dt = base._dtype_code(q)
     _want(q, "q", q_shape, dtype, dev)
-    cache = _paged(k_cache, v_cache, table, N, d, dtype, dev)
+    cache = _paged(torch, k_cache, v_cache, table, N, d, dtype, dev)
     Hk = k_cache.shape[1]
     if lens is None:
         raise ValueError("lens is required")
@@ -307,16 +302,15 @@ def lr_step_paged(q, k_cache, v_cache, table, lens, *, max_len=None, window=None
         need = _step_workspace(N, Hq, Hk, d, max_len, window, sinks, dt)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {dev}")
-    with _on(stream, dev):
-        if o is None:
-            o = torch.empty(q_shape, dtype=dtype, device=dev)
-        if need > 0:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-        ws, ws_bytes = ((None, 0) if workspace is None else
-                        (workspace.data_ptr(), workspace.numel() * workspace.element_size()))
-        st = base.lib().lr_step_paged(q.data_ptr(), cache, lens.data_ptr(), o.data_ptr(), N, Hq,
-                                      Hk, d, max_len, window, sinks, scale, dt, ws, ws_bytes,
-                                      _handle(stream, dev))
+    if o is None:
+        o = torch.empty(q_shape, dtype=dtype, device=dev)
+    if need > 0:
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws, ws_bytes = ((None, 0) if workspace is None else
+                    (workspace.data_ptr(), workspace.numel() * workspace.element_size()))
+    st = base.lib().lr_step_paged(q.data_ptr(), cache, lens.data_ptr(), o.data_ptr(), N, Hq, Hk, d,
+                                  max_len, window, sinks, scale, dt, ws, ws_bytes,
+                                  _handle(torch, dev))
     if st != 0:
         raise base.LrError(st, "lr_step_paged")
     return o

@@ -169,17 +169,20 @@ __device__ __forceinline__ bool elect_one() {
 }
 // The tensor pipe for one warp's products at a time: two warps that issue
 // together would both finish late, and their softmaxes then run together too,
-// with the pipe idle.  A hint for the order, not a lock: after the limit the
-// warp goes on, which changes no result.
+// with the pipe idle.  A hint for the order, not a lock: two warps may see the
+// flag free at once, and after the limit a warp goes on; no result depends on it.
 __device__ __forceinline__ void take_pipe(uint32_t *flag) {
+    const uint32_t at = smem_u32(flag);
+#pragma unroll 1
     for (int i = 0; i < 4096; ++i) {
         uint32_t old;
-        asm volatile("atom.acquire.cta.shared::cta.exch.b32 %0, [%1], 1;" : "=r"(old) : "r"(smem_u32(flag)) : "memory");
+        asm volatile("ld.volatile.shared.u32 %0, [%1];" : "=r"(old) : "r"(at) : "memory");
         if (!old) break;
     }
+    asm volatile("st.volatile.shared.u32 [%0], 1;" ::"r"(at) : "memory");
 }
 __device__ __forceinline__ void free_pipe(uint32_t *flag) {
-    asm volatile("st.release.cta.shared::cta.b32 [%0], 0;" ::"r"(smem_u32(flag)) : "memory");
+    asm volatile("st.volatile.shared.u32 [%0], 0;" ::"r"(smem_u32(flag)) : "memory");
 }
 // Register shares of the warpgroups (all four warps execute these).
 template <int N> __device__ __forceinline__ void regs_up() {
@@ -330,6 +333,10 @@ __global__ void __launch_bounds__(NT, 1)
             mbar_init(&bars->empty[s], 2);  // both query tiles
         }
         fence_mbar_init();
+    }
+    if (warp == 10 && lane == 0) {
+        for (const CUtensorMap *map : {&tmq, &tmk, &tmv})
+            asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
     }
     if (warp == 8) {
         tmem_alloc(&bars->tmem, 512);
@@ -629,12 +636,11 @@ __global__ void __launch_bounds__(NT, 1)
                 float s[4][32];
                 tmem_ld32(ts, s[0]);
                 tmem_ld32(ts + 32, s[1]);
-                tmem_ld_wait(s[0], s[1]);
                 tmem_ld32(ts + 64, s[2]);
                 tmem_ld32(ts + 96, s[3]);
+                tmem_ld_wait(s[0], s[1], s[2], s[3]);
                 top(mx, s[0]);
                 top(mx, s[1]);
-                tmem_ld_wait(s[2], s[3]);
                 top(mx, s[2]);
                 top(mx, s[3]);
                 const float base = raise(fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])));
@@ -666,7 +672,7 @@ __global__ void __launch_bounds__(NT, 1)
             __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + x.b * a.os.b + x.head[t] * a.os.h +
                                (long long)(x.i0[t] + w0 + r8) * a.os.t + 8 * c8;
             const long long next8 = 8 * a.os.t;
-            float odd = 0.f;  // NaN once a value is not finite
+            float odd[4] = {0.f, 0.f, 0.f, 0.f};  // NaN once a value is not finite
             int last_ch;      // hidden from the compiler, which would unroll the last turn
             asm volatile("mov.u32 %0, %1;" : "=r"(last_ch) : "n"(D / 32 - 1));
 #pragma unroll 1
@@ -683,7 +689,7 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
                     const float y0 = v[2 * i] * inv, y1 = v[2 * i + 1] * inv;
-                    odd = fmaf(y0, 0.f, fmaf(y1, 0.f, odd));
+                    odd[i & 3] = fmaf(y0, 0.f, fmaf(y1, 0.f, odd[i & 3]));
                     w[i] = pack2(y0, y1);
                 }
                 __syncwarp();  // the last channels have left
@@ -701,7 +707,7 @@ __global__ void __launch_bounds__(NT, 1)
                     oc += next8;
                 }
             }
-            unsigned again = __ballot_sync(0xffffffffu, row < rows && !(odd == 0.f));
+            unsigned again = __ballot_sync(0xffffffffu, row < rows && !(odd[0] + odd[1] + odd[2] + odd[3] == 0.f));
             if (again) {
                 const __nv_bfloat16 *q = static_cast<const __nv_bfloat16 *>(a.q) + x.b * a.qs.b +
                                          x.head[t] * a.qs.h + (long long)x.i0[t] * a.qs.t;

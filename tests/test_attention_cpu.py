@@ -162,8 +162,23 @@ class _NoLaunch:
 def lr(monkeypatch):
     import gated_delta_rule_fwd_gb300 as lr
     monkeypatch.setattr(lr, "_require_cuda", lambda dev: None)   # CPU tensors stand in
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
     monkeypatch.setattr(lr, "lib", lambda: _NoLaunch())
     return lr
+
+
+def test_binding_accepts_what_it_should(lr):
+    """The refusals below are the changes' own: unchanged, the calls get as far as the library."""
+    f = torch.zeros(32, dtype=torch.float64)
+    with pytest.raises(AssertionError, match="lr_fwd_window"):
+        lr.lr_fwd_window(_t(1, 4, 9, 64), _t(1, 2, 9, 64), _t(1, 2, 9, 64))
+    with pytest.raises(AssertionError, match="lr_step_paged"):
+        lr.lr_step_paged(_t(3, 4, 64), _t(5, 2, 16, 64), _t(5, 2, 16, 64), torch.zeros(3, 4, dtype=torch.int32),
+                         torch.zeros(3, dtype=torch.int32), max_len=60)
+    with pytest.raises(AssertionError, match="lr_qk_norm_rope"):
+        lr.lr_qk_norm_rope(_t(2, 4, 9, 64), _t(2, 2, 9, 64), torch.zeros(2, 9, dtype=torch.int32), inv_freq=f,
+                           v=_t(2, 2, 9, 64), k_cache=_t(5, 2, 16, 64), v_cache=_t(5, 2, 16, 64),
+                           table=torch.zeros(2, 4, dtype=torch.int32), write_k=False)
 
 
 def _t(*shape, dtype=torch.bfloat16):
