@@ -180,7 +180,7 @@ def lr_qk_norm_rope(q, k, positions=None, *, norm=True, q_weight=None, k_weight=
         _want(k_out, "k_out", k_shape, dtype, dev)
     maps = QkMaps((QK_NORM if norm else 0) | (QK_INTERLEAVED if interleaved else 0),
                   None if q_weight is None else q_weight.data_ptr(),
-                  None if k_weight is None else k_weight.data_ptr(), eps, rot,
+                  None if k_weight is None else k_weight.data_ptr(), float(eps), rot,
                   None if inv_freq is None else inv_freq.data_ptr())
     if q_out is None:
         q_out = torch.empty(q_shape, dtype=dtype, device=dev)
@@ -231,7 +231,7 @@ def lr_fwd_window(q, k, v, *, window=None, sinks=0, q_len=None, k_len=None, scal
     os_ = None if o is None else _strided(o, "o", q_shape, dtype, dev)
     window = NO_WINDOW if window is None else _int32(window, "window")
     sinks = _int32(sinks, "sinks")
-    scale = d ** -0.5 if scale is None else scale
+    scale = d ** -0.5 if scale is None else float(scale)
     if o is None:
         o = (torch.empty if q_len is None else torch.zeros)(q_shape, dtype=dtype, device=dev)
         os_ = _strided(o, "o", q_shape, dtype, dev)
@@ -296,7 +296,7 @@ def lr_step_paged(q, k_cache, v_cache, table, lens, *, max_len=None, window=None
     max_len = cache.page * cache.max_pages if max_len is None else _int32(max_len, "max_len")
     window = NO_WINDOW if window is None else _int32(window, "window")
     sinks = _int32(sinks, "sinks")
-    scale = d ** -0.5 if scale is None else scale
+    scale = d ** -0.5 if scale is None else float(scale)
     need = 0
     if workspace is None:
         need = _step_workspace(N, Hq, Hk, d, max_len, window, sinks, dt)

@@ -1,9 +1,24 @@
-// One attention row by a warp, straight from the definition: only the keys
-// the row sees are read.  The tiled kernels multiply whole tiles, where a
-// weight of zero times a NaN or an infinity in a masked row of v would reach
-// rows that do not see it; a row whose result is not finite is therefore
-// recomputed here (such rows are rare: finite inputs of ordinary size never
-// take this path).
+// Rows whose result is not finite, put right by a warp.
+//
+// The tiled kernels multiply whole tiles, where a weight of zero times a NaN
+// or an infinity in a masked row of v reaches rows that do not see it.  Such
+// rows come out not finite, and only then is this called (finite inputs of
+// ordinary size never are).  What is right for them:
+//
+//   - a sum of weights that is not finite: where a score that the row sees is
+//     NaN or +inf every channel is NaN.  Operands at the type's ends make the
+//     sum NaN as well (their products with the scale, or their split parts,
+//     leave the range), so the scores are formed once more to tell, 32 keys at
+//     a time; if none is NaN or +inf the row is computed again;
+//   - a channel in which the row sees a NaN, or infinities of both signs, is
+//     NaN; one in which it sees infinities of one sign is that infinity (every
+//     weight is positive);
+//   - any other channel takes its value from finite numbers alone: the row is
+//     computed once more from the definition, reading only what it sees.
+//
+// The search goes back from the newest key and ends as soon as every channel
+// is explained, so that a batch full of NaN costs little; the full row is
+// computed for rows next to a masked one that is not finite.
 #pragma once
 
 #include "attn_internal.cuh"
@@ -17,37 +32,94 @@ __device__ __forceinline__ float warp_sum(float x) {
 }
 
 // q: the row's d channels; k, v: row 0 of its key head, rows `kt` and `vt`
-// elements apart.  Every lane of the warp calls this with the same arguments.
+// elements apart; o: the row as the kernel left it.  Every lane of the warp
+// calls this with the same arguments.
 template <typename E, int D>
-__device__ __forceinline__ void attn_row(const E *q, const E *k, const E *v, long long kt,
-                                         long long vt, E *o, SeenKeys s, float scale) {
+__device__ __forceinline__ void mend_row(const E *q, const E *k, const E *v, long long kt, long long vt,
+                                         E *o, SeenKeys s, float scale, bool sum_finite) {
     constexpr int PL = D / 32;  // channels of a lane: lane + 32 i
     const int lane = threadIdx.x & 31;
-    float qr[PL], acc[PL], m = -INFINITY, l = 0.f;
+    bool whole_row = false;
+    if (!sum_finite) {
+        bool bad = false;
+#pragma unroll 1
+        for (int j0 = s.hi - 1; j0 >= 0 && !bad; j0 -= 32) {
+            if (j0 < s.lo && j0 >= s.s1) j0 = s.s1 - 1;
+            const int j = j0 - lane;
+            float x = 0.f;
+            if (j >= 0 && (j >= s.lo || j < s.s1)) {
+#pragma unroll 4
+                for (int c = 0; c < D; c += 4) {
+                    const float4 a = load4(q + c), b = load4(k + j * kt + c);
+                    x += a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
+                }
+            }
+            bad = __any_sync(0xffffffffu, !(x * scale < INFINITY));
+        }
+        if (bad) {
+#pragma unroll
+            for (int i = 0; i < PL; ++i) o[lane + 32 * i] = from_f<E>(NAN);
+            return;
+        }
+        whole_row = true;
+    }
+    // seen in a channel: 1 +inf, 2 -inf, 4 NaN
+    unsigned found[PL], odd[PL];
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
-        qr[i] = to_f<E>(q[lane + 32 * i]) * scale;
-        acc[i] = 0.f;
+        found[i] = 0;
+        odd[i] = whole_row || !isfinite(to_f<E>(o[lane + 32 * i]));
     }
 #pragma unroll 1
-    for (int j = 0; j < s.hi; ++j) {
-        if (j == s.s1 && j < s.lo) j = s.lo;
-        if (j >= s.hi) break;
-        float x = 0.f;
+    for (int j = s.hi - 1; j >= 0; --j) {
+        if (j < s.lo && j >= s.s1) {
+            j = s.s1;
+            continue;
+        }
+        bool open = false;  // a channel that more keys could still change
 #pragma unroll
-        for (int i = 0; i < PL; ++i) x += qr[i] * to_f<E>(k[j * kt + lane + 32 * i]);
-        x = warp_sum(x);
-        if (x == -INFINITY) continue;  // weight zero
-        const float mn = x > m || !(x == x) ? x : m;
-        const float c = m == -INFINITY ? 0.f : expf(m - mn), p = expf(x - mn);
-        m = mn;
-        l = l * c + p;
+        for (int i = 0; i < PL; ++i) {
+            const float x = to_f<E>(v[j * vt + lane + 32 * i]);
+            if (!isfinite(x)) found[i] |= x > 0.f ? 1u : (x < 0.f ? 2u : 4u);
+            open = open || (odd[i] && found[i] < 3u);
+        }
+        if (!__any_sync(0xffffffffu, open)) break;
+    }
+    bool unexplained = false;
 #pragma unroll
-        for (int i = 0; i < PL; ++i) acc[i] = acc[i] * c + p * to_f<E>(v[j * vt + lane + 32 * i]);
+    for (int i = 0; i < PL; ++i) unexplained = unexplained || (odd[i] && !found[i]);
+    float acc[PL];
+#pragma unroll
+    for (int i = 0; i < PL; ++i) acc[i] = 0.f;
+    const bool again = __any_sync(0xffffffffu, unexplained);
+    if (again) {
+        float qr[PL], m = -INFINITY, l = 0.f;
+#pragma unroll
+        for (int i = 0; i < PL; ++i) qr[i] = to_f<E>(q[lane + 32 * i]) * scale;
+#pragma unroll 1
+        for (int j = 0; j < s.hi; ++j) {
+            if (j == s.s1 && j < s.lo) j = s.lo;
+            if (j >= s.hi) break;
+            float x = 0.f;
+#pragma unroll
+            for (int i = 0; i < PL; ++i) x += qr[i] * to_f<E>(k[j * kt + lane + 32 * i]);
+            x = warp_sum(x);
+            if (x == -INFINITY) continue;  // weight zero
+            // a running mean, which no large value can drive out of range
+            const float mn = fmaxf(m, x), old = l * (m == -INFINITY ? 0.f : expf(m - mn)), p = expf(x - mn);
+            m = mn;
+            l = old + p;
+            const float keep = old / l, take = p / l;
+#pragma unroll
+            for (int i = 0; i < PL; ++i) acc[i] = acc[i] * keep + take * to_f<E>(v[j * vt + lane + 32 * i]);
+        }
     }
 #pragma unroll
-    for (int i = 0; i < PL; ++i)
-        o[lane + 32 * i] = from_f<E>(m == -INFINITY ? 0.f : acc[i] / l);
+    for (int i = 0; i < PL; ++i) {
+        const float inf = found[i] == 1u ? INFINITY : (found[i] == 2u ? -INFINITY : NAN);
+        if (odd[i] && found[i]) o[lane + 32 * i] = from_f<E>(inf);
+        else if (odd[i]) o[lane + 32 * i] = from_f<E>(acc[i]);
+    }
 }
 
 }  // namespace lr

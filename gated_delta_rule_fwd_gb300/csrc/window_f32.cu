@@ -53,7 +53,9 @@ template <int N> __device__ __forceinline__ void copies_wait() {
     asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
-// x = hi + lo, hi with 11 significant bits (nearest); lo is cut to as many by the product.
+// x = hi + lo, hi with 11 significant bits (nearest); lo is cut to as many by the
+// product.  Infinities and the type's largest values give a NaN: rows that meet
+// one are put right afterwards.
 __device__ __forceinline__ void split(float x, uint32_t &hi, uint32_t &lo) {
     hi = (__float_as_uint(x) + 0x1000u) & 0xffffe000u;
     lo = __float_as_uint(x - __uint_as_float(hi));
@@ -310,8 +312,9 @@ __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float 
         for (int x = 0; x < 8; ++x) {
             if (!((again >> (4 * x)) & 0xfu)) continue;
             const int rr = 16 * warp + x + 8 * r;
-            attn_row<float, D>(q + rr * a.qs.t, k, v, a.ks.t, a.vs.t, o + rr * a.os.t,
-                               seen_keys(p0 + rr, kl, a.window, a.sinks), a.scale);
+            mend_row<float, D>(q + rr * a.qs.t, k, v, a.ks.t, a.vs.t, o + rr * a.os.t,
+                               seen_keys(p0 + rr, kl, a.window, a.sinks), a.scale,
+                               isfinite(__shfl_sync(0xffffffffu, sum, 4 * x)));
         }
     }
 }

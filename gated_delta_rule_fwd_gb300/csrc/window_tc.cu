@@ -27,7 +27,8 @@
 // see entirely skips the mask; one that none sees is skipped; a short one
 // takes fewer columns.  Masked weights are exact zeros, so only a non-finite
 // masked value row can disturb a result; rows whose output is not finite are
-// recomputed from the definition (attn_rows.cuh).
+// put right one by one (attn_rows.cuh).  Padding behind a sequence's last key
+// is set to zero as it is loaded.
 //
 // Roles of the 384 threads: warps 0-3 softmax and output of query tile 0,
 // warps 4-7 of tile 1, warps 8 and 9 issue the products of tiles 0 and 1, warp
@@ -65,7 +66,7 @@ struct Layout {
     static constexpr int OUT = KV + NS * TILE;       // 2 KB per softmax warp: rows on their way out
     static constexpr int CLC = OUT + 8 * 2048;       // answer to a request for work, 16 bytes
     static constexpr int BAR = CLC + 16;
-    static constexpr int ITEM = BAR + 320;           // two of struct Item
+    static constexpr int ITEM = BAR + 384;           // two of struct Item
     static constexpr int BYTES = ITEM + 2 * 128;
     static constexpr int ALLOC = BYTES + 1024;
 };
@@ -73,7 +74,7 @@ struct Layout {
 struct Barriers {
     uint64_t qfull[2], qempty[2], sfull[2], pready[2][2], ofull[2], oempty[2], fin[2];
     uint64_t full[8], empty[8];
-    uint64_t ifull[2], iempty[2], clc, loaded;
+    uint64_t ifull[2], iempty[2], clc, loaded, pad;
     uint32_t tmem, pipe;  // pipe: 1 while a warp issues products
 };
 
@@ -274,7 +275,7 @@ __device__ __forceinline__ void make_item(const TcArgs &g, int block, Item &x, b
     }
 }
 
-static_assert(sizeof(Item) <= 128 && sizeof(Barriers) <= 320, "shared memory layout");
+static_assert(sizeof(Item) <= 128 && sizeof(Barriers) <= 384, "shared memory layout");
 
 // Ask for the index of a block that has not started, to do its work here; the
 // answer (16 bytes at `dst`) is counted on `bar`.
@@ -328,6 +329,7 @@ __global__ void __launch_bounds__(NT, 1)
         bars->pipe = 0;
         mbar_init(&bars->clc, 1);
         mbar_init(&bars->loaded, 1);
+        mbar_init(&bars->pad, 1);
         for (int s = 0; s < L::NS; ++s) {
             mbar_init(&bars->full[s], 1);
             mbar_init(&bars->empty[s], 2);  // both query tiles
@@ -396,37 +398,53 @@ __global__ void __launch_bounds__(NT, 1)
         }
     } else if (warp == 10) {
         // ============================================================ loads
-        int seq = 0, used[2] = {0, 0};
+        int seq = 0, used[2] = {0, 0}, pads = 0;
         while (const Item *px = take()) {
             const Item &x = *px;
-            if (lane == 0) {
 #pragma unroll 1
-                for (int t = 0; t < 2 && ok; ++t) {
-                    if (x.last[t] < 0) continue;
-                    if (used[t] > 0) ok = wait_bar(&bars->qempty[t], (used[t] - 1) & 1);
-                    if (!ok) break;
-                    ++used[t];
+            for (int t = 0; t < 2 && ok; ++t) {
+                if (x.last[t] < 0) continue;
+                if (used[t] > 0) ok = __all_sync(0xffffffffu, wait_bar(&bars->qempty[t], (used[t] - 1) & 1));
+                if (!ok) break;
+                ++used[t];
+                if (lane == 0) {
                     mbar_expect_tx(&bars->qfull[t], L::TILE);
                     for (int kb = 0; kb < L::KB; ++kb)
                         tma_load_4d(sm + L::Q + t * L::TILE + kb * 16384, &tmq, kb * 64, x.i0[t],
                                     x.head[t], x.b, &bars->qfull[t]);
                 }
-#pragma unroll 1
-                for (int it = 0; it < x.n && ok; ++it) {
-                    const int k0 = x.key0(it);
-#pragma unroll 1
-                    for (int kv = 0; kv < 2 && ok; ++kv, ++seq) {
-                        const int s = seq % L::NS;
-                        if (seq >= L::NS) ok = wait_bar(&bars->empty[s], (seq / L::NS - 1) & 1);
-                        if (!ok) break;
-                        mbar_expect_tx(&bars->full[s], L::TILE);
-                        for (int kb = 0; kb < L::KB; ++kb)
-                            tma_load_4d(sm + L::KV + s * L::TILE + kb * 16384, kv ? &tmv : &tmk,
-                                        kb * 64, k0, x.hk, x.b, &bars->full[s]);
-                    }
-                }
-                mbar_arrive(&bars->loaded);
             }
+            const int n = x.n;
+#pragma unroll 1
+            for (int i = 0; i < 2 * n && ok; ++i, ++seq) {
+                const int s = seq % L::NS, k0 = x.key0(i >> 1);
+                if (seq >= L::NS)
+                    ok = __all_sync(0xffffffffu, wait_bar(&bars->empty[s], (seq / L::NS - 1) & 1));
+                if (!ok) break;
+                uint8_t *to = sm + L::KV + s * L::TILE;
+                // values behind the last key: zeros, whatever the padding holds
+                const bool pad = (i & 1) && x.kl < a.Tk && k0 + BN > x.kl;
+                uint64_t *bar = pad ? &bars->pad : &bars->full[s];
+                if (lane == 0) {
+                    mbar_expect_tx(bar, L::TILE);
+                    for (int kb = 0; kb < L::KB; ++kb)
+                        tma_load_4d(to + kb * 16384, i & 1 ? &tmv : &tmk, kb * 64, k0, x.hk, x.b, bar);
+                }
+                if (pad) {
+                    ok = __all_sync(0xffffffffu, wait_bar(&bars->pad, pads & 1));
+                    ++pads;
+                    const int from = max(0, x.kl - k0) * 8;  // 16-byte units of 128-byte rows
+#pragma unroll 1
+                    for (int u = from + lane; u < BN * 8; u += 32)
+                        for (int kb = 0; kb < L::KB; ++kb)
+                            *reinterpret_cast<uint4 *>(to + kb * 16384 + u * 16) = make_uint4(0, 0, 0, 0);
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->full[s]);
+                }
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->loaded);
             give_back();
         }
         // never leave with copies into shared memory in flight
@@ -717,10 +735,11 @@ __global__ void __launch_bounds__(NT, 1)
                                     (long long)x.i0[t] * a.os.t;
                 __syncwarp();
                 while (again) {
-                    const int rr = w0 + __ffs(again) - 1;
+                    const int src = __ffs(again) - 1, rr = w0 + src;
                     again &= again - 1;
-                    attn_row<__nv_bfloat16, D>(q + rr * a.qs.t, k, v, a.ks.t, a.vs.t, ot + rr * a.os.t,
-                                               seen_keys(x.p0[t] + rr, x.kl, a.window, a.sinks), a.scale);
+                    mend_row<__nv_bfloat16, D>(q + rr * a.qs.t, k, v, a.ks.t, a.vs.t, ot + rr * a.os.t,
+                                               seen_keys(x.p0[t] + rr, x.kl, a.window, a.sinks), a.scale,
+                                               isfinite(__shfl_sync(0xffffffffu, l, src)));
                 }
             }
             give_back();

@@ -146,6 +146,68 @@ def test_window_masked_values_cannot_reach_other_rows(dev, dtype, d, bad):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_window_infinities_and_nan_of_the_values(dev, dtype):
+    """A channel with one seen infinity is that infinity, with both signs or a
+    NaN it is NaN, and otherwise it is finite, whatever the masked rows beside
+    it hold; values near the type's end average without overflow."""
+    T, d, window, inf = 200, 64, 40, float("inf")
+    q, k, v = (rnd(s, 1, 1, T, d, dtype=dtype) for s in (80, 81, 82))
+    ref, size, reach, _ = oa.window(np64(q), np64(k), np64(v), window, 3, d ** -0.5)
+    bound = oa.attention_bound(ref, size, reach, T, d, BITS[dtype], 8 if dtype == BF16 else None)
+    marks = [(1, 3, inf), (70, 0, inf), (70, 1, -inf), (75, 0, -inf), (80, 2, float("nan")), (90, 2, inf), (150, 5, -inf)]
+    for j, ch, x in marks:
+        v[0, 0, j, ch] = x
+    o = np64(lr.lr_fwd_window(q.to(dev), k.to(dev), v.to(dev), window=window, sinks=3))[0, 0]
+    for p in range(T):
+        want = {}
+        for j, ch, x in marks:
+            if oa.sees(p, j, T, window, 3):
+                want.setdefault(ch, []).append(x)
+        for ch in range(d):
+            got = o[p, ch]
+            if ch not in want:
+                assert abs(got - ref[0, 0, p, ch]) <= bound[0, 0, p, ch], (p, ch, got)
+            elif any(np.isnan(x) for x in want[ch]) or len(set(want[ch])) > 1:
+                assert np.isnan(got), (p, ch, got)
+            else:
+                assert got == want[ch][0], (p, ch, got)
+    big = torch.finfo(dtype).max / 2
+    o = lr.lr_fwd_window(torch.zeros(1, 1, T, d, dtype=dtype, device=dev), k.to(dev),
+                         torch.full((1, 1, T, d), big, dtype=dtype, device=dev))
+    assert ((o.double() / big - 1).abs() <= 2.0 ** -7).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("which", ["q", "k", "v"])
+def test_window_batch_full_of_nan_stays_quick(dev, dtype, which):
+    """Everything NaN in one input: every row is NaN, and the call does not
+    fall back to a row at a time for each (that took seconds at this size)."""
+    import time
+    T = 4096
+    x = {n: rnd(s, 1, 8, T, 128, dtype=dtype).to(dev) for s, n in ((83, "q"), (84, "k"), (85, "v"))}
+    x[which].fill_(float("nan"))
+    torch.cuda.synchronize()
+    start = time.perf_counter()
+    o = lr.lr_fwd_window(x["q"], x["k"], x["v"])
+    torch.cuda.synchronize()
+    assert time.perf_counter() - start < 1.0
+    assert o.isnan().all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_window_overlapping_inputs(dev, dtype):
+    """Rows that overlap in memory (a sliding view) and one row for all heads."""
+    T, d = 140, 64
+    line = rnd(86, T * 16 + d, dtype=dtype)
+    v = torch.as_strided(line, (1, 2, T, d), (16, 16, 16, 1))
+    q, k = (rnd(s, 1, 2, T, d, dtype=dtype) for s in (87, 88))
+    dl = line.to(dev)
+    o = lr.lr_fwd_window(q.to(dev), k.to(dev), torch.as_strided(dl, (1, 2, T, d), (16, 16, 16, 1)), window=33)
+    ref, size, reach, _ = oa.window(np64(q), np64(k), np64(v), 33, 0, d ** -0.5)
+    within(o, ref, oa.attention_bound(ref, size, reach, T, d, BITS[dtype], 8 if dtype == BF16 else None))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 def test_window_extreme_scores(dev, dtype):
     """Scores far beyond exp's range either way, the type's lowest value, and
     -inf: one key decides; equal extremes average; all -inf gives zeros."""
@@ -412,6 +474,22 @@ def test_step_bad_pages_and_lengths_are_reported(dev):
                          max_len=40, o=o)
         assert lr.device_status() == LR_ERR_INDEX
         assert torch.equal(o[0], good[0]) and (o[1:] == 7).all()
+        # the same where chunks are joined by a cluster, and by a second kernel
+        for bound_on_len in (300, 20000):
+            wide = torch.zeros(3, bound_on_len // page + 1, dtype=torch.int32, device=dev)
+            wide[:, :3] = table[:, :3]
+            o = torch.full_like(q, 7.0)
+            lr.lr_step_paged(q, kc, vc, wide, torch.tensor([40, bound_on_len + 1, -5], dtype=torch.int32, device=dev),
+                             max_len=bound_on_len, o=o)
+            assert lr.device_status() == LR_ERR_INDEX
+            assert torch.equal(o[0], good[0]) and (o[1:] == 7).all()
+            wide[0, 1] = -1
+            broken = table.clone()
+            broken[0, 1] = -1
+            a = lr.lr_step_paged(q, kc, vc, wide, ld, max_len=bound_on_len)
+            b = lr.lr_step_paged(q, kc, vc, broken, ld)
+            assert lr.device_status() == LR_ERR_INDEX
+            assert torch.equal(a, b)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
@@ -633,6 +711,52 @@ def test_operators_capture_into_graphs_and_follow_their_inputs(dev):
             assert torch.equal(outs[i], once(window))
         pos += 1
         lens += 1
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_window_captures_into_a_graph(dev, dtype):
+    """Replays follow inputs and lengths; more pieces of work than SMs."""
+    B, T = 3, 700
+    q, k, v = (rnd(s, B, h, T, 64, dtype=dtype).to(dev) for s, h in ((90, 16), (91, 8), (92, 8)))
+    ql = torch.tensor([700, 300, 5], dtype=torch.int32, device=dev)
+    kl = ql.clone()
+    call = lambda: lr.lr_fwd_window(q, k, v, window=130, sinks=4, q_len=ql, k_len=kl)
+    call()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        o = call()
+    for s in range(3):
+        q.copy_(rnd(93 + s, *q.shape, dtype=dtype))
+        g.replay()
+        assert torch.equal(o, call())
+        ql -= 2
+        kl -= 1
+
+
+def test_two_calls_at_once(dev):
+    """Two streams run the three operators at the same time: the same bits as alone."""
+    q, k, v = (rnd(s, 2, h, 3000, 128, dtype=BF16).to(dev) for s, h in ((96, 8), (97, 8), (98, 8)))
+    f = torch.tensor(10000.0 ** (-np.arange(64) / 64), device=dev)
+    kc, vc, table = paged(12, [4000] * 3, 2, 64, 128, BF16, dev)
+    lens = torch.tensor([4000] * 3, dtype=torch.int32, device=dev)
+    x = rnd(99, 3, 8, 128, dtype=BF16).to(dev)
+
+    def three(window):
+        a, b = lr.lr_qk_norm_rope(q, k, inv_freq=f)
+        return a, b, lr.lr_fwd_window(a, b, v, window=window), lr.lr_step_paged(x, kc, vc, table, lens, window=window)
+
+    want = [three(None), three(500)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(dev) for _ in range(2)]
+    for _ in range(3):
+        got = []
+        for s, w in zip(streams, (None, 500)):
+            with torch.cuda.stream(s):
+                got.append(three(w))
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert all(torch.equal(x, y) for x, y in zip(a, b))
 
 
 def test_operators_on_another_stream_and_repeated(dev):
