@@ -76,26 +76,30 @@ __device__ __forceinline__ void put(__nv_bfloat16 *p, const Row8<__nv_bfloat16> 
     *reinterpret_cast<uint4 *>(p) = make_uint4(r.x[0], r.x[1], r.x[2], r.x[3]);
 }
 
-template <typename E, int D>
+enum Rotation { kNone, kHalves, kPairs };  // channels (i, i + rot/2) or (2i, 2i+1)
+
+template <typename E, int D, Rotation ROT>
 __global__ void __launch_bounds__(NT, kCtas<E>) qk_norm_rope_kernel(RopeArgs a) {
     constexpr int LANES = D / 8;      // lanes of a row
     constexpr int ROWS = NT / LANES;  // rows at once: tokens x head parts
     __shared__ unsigned long long step[D / 2];
     const int tid = threadIdx.x, half = a.maps.rot >> 1;
-    const bool norm = a.maps.flags & LR_QK_NORM, inter = a.maps.flags & LR_QK_INTERLEAVED;
+    const bool norm = a.maps.flags & LR_QK_NORM, partial = a.maps.rot < D;
     // the lane's place: channels c0.., token `mine` of the group, every parts-th head
     const int c0 = tid % LANES * 8, row = tid / LANES;
     const int mine = row & (a.tokens - 1), part = row / a.tokens, parts = ROWS / a.tokens;
-    const bool turns_here = c0 < a.maps.rot, low = c0 < half;
+    const bool turns_here = ROT != kNone && c0 < a.maps.rot, low = c0 < half;
     // split halves: the partner channel c +- half sits half / 8 lanes away
-    const int hop = turns_here && !inter ? (low ? half : -half) : 0;
+    const int hop = ROT == kHalves && turns_here ? (low ? half : -half) : 0;
     const int from = (tid & 31) + hop / 8;
-    if (tid < half) {
-        double turns = a.maps.inv_freq[tid] * 0.15915494309189533577;  // 1 / (2 pi)
-        turns -= floor(turns);
-        step[tid] = __double2ull_rz(turns * 18446744073709551616.0);
+    if (ROT != kNone) {
+        if (tid < half) {
+            double turns = a.maps.inv_freq[tid] * 0.15915494309189533577;  // 1 / (2 pi)
+            turns -= floor(turns);
+            step[tid] = __double2ull_rz(turns * 18446744073709551616.0);
+        }
+        __syncthreads();
     }
-    __syncthreads();
 
     const int groups = (a.total + a.tokens - 1) / a.tokens;
     for (int group = blockIdx.x; group < groups; group += gridDim.x) {
@@ -103,12 +107,11 @@ __global__ void __launch_bounds__(NT, kCtas<E>) qk_norm_rope_kernel(RopeArgs a) 
         const int b = n / a.T, t = n - b * a.T;
         const int p = a.positions ? a.positions[n] : t;
         const bool on = n0 < a.total && p >= 0;
-        auto fetch_rows = [&](Row8<E>(&r)[U], const E *src, long long stride, int count, int h0) {
+        // U rows of heads h, h + parts, ... (the last head where there are none:
+        // every address is a row of the tensor, and nothing of it is kept)
+        auto fetch_rows = [&](Row8<E>(&r)[U], const E *src, long long stride, int count, int h) {
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
-                r[u] = Row8<E>{};
-                if (on && h0 + u * parts < count) r[u] = fetch(src + (h0 + u * parts) * stride);
-            }
+            for (int u = 0; u < U; ++u) r[u] = fetch(src + min(h + u * parts, count - 1) * stride);
         };
         // the first rows are on their way while the angles are formed
         const E *q_from = static_cast<const E *>(a.q) + b * a.qs.b + t * a.qs.t + c0;
@@ -125,19 +128,42 @@ __global__ void __launch_bounds__(NT, kCtas<E>) qk_norm_rope_kernel(RopeArgs a) 
         }
         float co[8], si[8];  // of the lane's channels, the partner's sign in si
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            co[i] = 1.f, si[i] = 0.f;
-            if (!turns_here) continue;
-            if (inter && (i & 1)) {
-                co[i] = co[i - 1], si[i] = -si[i - 1];
-                continue;
+        for (int i = 0; i < 8; ++i) co[i] = 1.f, si[i] = 0.f;
+        if (turns_here) {
+            // halves: both lanes of a pair need the same eight angles, each forms four
+            constexpr int N = 4;
+            float c4[N], s4[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const int c = ROT == kPairs ? (c0 >> 1) + i : (low ? c0 + i : c0 - half + 4 + i);
+                const unsigned long long phase = step[c] * (unsigned long long)(long long)p;
+                // signed half turns in [-1, 1)
+                const float x = (float)(int)(phase >> 32) * 4.656612873077392578125e-10f;  // 2^-31
+                sincospif(x, &s4[i], &c4[i]);
             }
-            const int c = inter ? (c0 + i) >> 1 : (low ? c0 + i : c0 + i - half);
-            const unsigned long long phase = step[c] * (unsigned long long)(long long)p;
-            // signed half turns in [-1, 1)
-            const float x = (float)(int)(phase >> 32) * 4.656612873077392578125e-10f;  // 2^-31
-            sincospif(x, &si[i], &co[i]);
-            if (inter || low) si[i] = -si[i];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                if (ROT == kPairs) {
+                    co[2 * i] = co[2 * i + 1] = c4[i];
+                    si[2 * i] = -s4[i], si[2 * i + 1] = s4[i];
+                } else {
+                    co[i] = co[4 + i] = c4[i];  // one half is replaced by the other lane's below
+                    si[i] = si[4 + i] = s4[i];
+                }
+            }
+        }
+        if (ROT == kHalves) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float c = __shfl_sync(0xffffffffu, co[i], from), s = __shfl_sync(0xffffffffu, si[i], from);
+                if (turns_here) {
+                    if (low) co[4 + i] = c, si[4 + i] = s;
+                    else co[i] = c, si[i] = s;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (low) si[i] = -si[i];
         }
         // All heads of queries or keys, the first rows already in r; `keep`
         // stores a finished row.  A pair of channels becomes
@@ -148,7 +174,7 @@ __global__ void __launch_bounds__(NT, kCtas<E>) qk_norm_rope_kernel(RopeArgs a) 
             for (int i = 0; i < 8; ++i) {
                 const int c = c0 + i;
                 const float w = weight ? weight[c] : 1.f;
-                const float pw = weight ? weight[inter ? c ^ 1 : c + hop] : 1.f;
+                const float pw = weight ? weight[ROT == kPairs ? c ^ 1 : c + hop] : 1.f;
                 float &fc = i & 1 ? wc[i / 2].y : wc[i / 2].x, &fs = i & 1 ? ws[i / 2].y : ws[i / 2].x;
                 fc = w * co[i], fs = pw * si[i];
             }
@@ -158,11 +184,14 @@ __global__ void __launch_bounds__(NT, kCtas<E>) qk_norm_rope_kernel(RopeArgs a) 
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     if (h0 - part + u * parts >= count) break;  // for all lanes
+                    float2 x[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) x[i] = r[u].pair(i);
                     float inv = 1.f;
                     if (norm) {
-                        float2 ss = make_float2(0.f, 0.f);
+                        float2 ss = mul2(x[0], x[0]);
 #pragma unroll
-                        for (int i = 0; i < 4; ++i) ss = fma2(r[u].pair(i), r[u].pair(i), ss);
+                        for (int i = 1; i < 4; ++i) ss = fma2(x[i], x[i], ss);
                         float sum = ss.x + ss.y;
 #pragma unroll
                         for (int m = 1; m < LANES; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
@@ -172,12 +201,11 @@ __global__ void __launch_bounds__(NT, kCtas<E>) qk_norm_rope_kernel(RopeArgs a) 
                     Row8<E> y;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        const float2 x = r[u].pair(i);
-                        float2 z = mul2(x, wc[i]);
-                        if (half) {
+                        float2 z = mul2(x[i], wc[i]);
+                        if (ROT != kNone) {
+                            float2 w = ROT == kPairs ? make_float2(x[i].y, x[i].x) : r[u].pair_of(i, from);
                             // where nothing turns the partner is not looked at (it may be infinite)
-                            float2 w = inter ? make_float2(x.y, x.x) : r[u].pair_of(i, from);
-                            if (!turns_here) w = make_float2(0.f, 0.f);
+                            if (partial && !turns_here) w = make_float2(0.f, 0.f);
                             z = fma2(w, ws[i], z);
                         }
                         y.set(i, mul2(z, inv2));
@@ -220,7 +248,10 @@ cudaError_t launch(RopeArgs &a, cudaStream_t stream) {
     while (a.tokens < ROWS && (a.total + a.tokens - 1) / a.tokens > 304) a.tokens *= 2;
     const int groups = (a.total + a.tokens - 1) / a.tokens;
     const int most = 152 * kCtas<E>;
-    qk_norm_rope_kernel<E, D><<<groups < most ? groups : most, NT, 0, stream>>>(a);
+    const int grid = groups < most ? groups : most;
+    if (a.maps.rot == 0) qk_norm_rope_kernel<E, D, kNone><<<grid, NT, 0, stream>>>(a);
+    else if (a.maps.flags & LR_QK_INTERLEAVED) qk_norm_rope_kernel<E, D, kPairs><<<grid, NT, 0, stream>>>(a);
+    else qk_norm_rope_kernel<E, D, kHalves><<<grid, NT, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
