@@ -166,7 +166,7 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts) 
     bool bad = false;
     for (int base = c0 + group; base < c1; base += GROUPS * U) {
         long long row[U];
-        float x[U][8], sc[U][GC];
+        float x[U][8], y[U][8], sc[U][GC];  // keys, values: all on their way at once
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int i = base + u * GROUPS;
@@ -183,8 +183,11 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts) 
 #pragma unroll
         for (int u = 0; u < U; ++u) {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
-            if (row[u] >= 0) load8(static_cast<const float *>(a.k) + row[u], x[u]);
+            for (int i = 0; i < 8; ++i) x[u][i] = y[u][i] = 0.f;
+            if (row[u] >= 0) {
+                load8(static_cast<const float *>(a.k) + row[u], x[u]);
+                load8(static_cast<const float *>(a.v) + row[u], y[u]);
+            }
         }
 #pragma unroll
         for (int u = 0; u < U; ++u)
@@ -197,12 +200,6 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts) 
                 for (int w = 1; w < LANES; w <<= 1) t += __shfl_xor_sync(mask, t, w);
                 sc[u][g] = row[u] >= 0 ? t : -INFINITY;
             }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) x[u][i] = 0.f;
-            if (row[u] >= 0) load8(static_cast<const float *>(a.v) + row[u], x[u]);
-        }
 #pragma unroll
         for (int g = 0; g < GC; ++g) {
             float mn = m[g];
@@ -219,7 +216,7 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts) 
                 const float p = __expf(sc[u][g] - b);
                 l[g] += p;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) acc[g][i] += p * x[u][i];
+                for (int i = 0; i < 8; ++i) acc[g][i] += p * y[u][i];
             }
         }
     }
