@@ -127,7 +127,7 @@ def lr_qk_norm_rope(q, k, positions=None, *, norm=True, q_weight=None, k_weight=
     q: [B,Hq,T,d]; k: [B,Hk,T,d] (float32 or bfloat16), any strides with
     contiguous channels, e.g. transposed views of one projection;
     positions: [B,T] int32 (negative: padding, left out) or None for 0..T-1;
-    q_weight, k_weight: [d] float32 or None; inv_freq: [rot/2] float64 radians
+    q_weight, k_weight: [d] float32 or None, of the norm; inv_freq: [rot/2] float64 radians
     per position, or None for no rotation; ``interleaved`` rotates channels
     (2i, 2i+1) instead of (i, i + rot/2).  With k_cache, v_cache
     [pages,Hk,page,d], table [B,max_pages] int32 and v [B,Hk,T,d], the keys

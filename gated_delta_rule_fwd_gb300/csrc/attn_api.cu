@@ -47,7 +47,7 @@ size_t esize(lr_dtype dt) { return dt == LR_DT_F32 ? 4 : 2; }
 
 // Strides of a [B, H, T, d] tensor: positive and whole 16-byte units where
 // the size is above 1 (a size of 1 never uses its stride: it is replaced by 0).
-lr_status check_strides(lr_strides *s, int B, int H, int T, int d, lr_dtype dt) {
+lr_status check_strides(lr_strides *s, int B, int H, int T, lr_dtype dt) {
     const long long unit = 16 / (long long)esize(dt);
     long long *st[3] = {&s->b, &s->h, &s->t};
     const int n[3] = {B, H, T};
@@ -59,7 +59,6 @@ lr_status check_strides(lr_strides *s, int B, int H, int T, int d, lr_dtype dt) 
         if (*st[i] <= 0 || *st[i] > kMostElements / n[i]) return LR_ERR_SHAPE;
         if (*st[i] % unit) return LR_ERR_ALIGN;
     }
-    (void)d;
     return LR_OK;
 }
 Span strided_span(const void *p, const lr_strides &s, int B, int H, int T, int d, lr_dtype dt) {
@@ -132,7 +131,7 @@ lr_status check_step_sizes(int N, int Hq, int Hk, int d, int max_len, int window
     if (N < 1 || max_len < 1 || window < 1 || sinks < 0) return LR_ERR_SHAPE;
     if (max_len > (1 << 30) || !count_ok(N, Hq, d, 1)) return LR_ERR_SHAPE;
     // CTAs of one launch
-    const StepPlan p = step_plan(N, Hq, Hk, max_len, window, sinks, dt);
+    const StepPlan p = step_plan(N, Hk, max_len, window, sinks, dt);
     if (!count_ok(N, Hq, p.splits, 1) || (long long)N * Hq * p.splits > 0x7fffffffll)
         return LR_ERR_SHAPE;
     return LR_OK;
@@ -171,9 +170,9 @@ lr_status lr_qk_norm_rope(const void *q, lr_strides qs, const void *k, lr_stride
                           (const void *)maps->k_weight})
         if (!aligned16(p)) return LR_ERR_ALIGN;
     if (!aligned4(positions)) return LR_ERR_ALIGN;
-    if ((st = check_strides(&qs, B, Hq, T, d, dt)) != LR_OK) return st;
-    if ((st = check_strides(&ks, B, Hk, T, d, dt)) != LR_OK) return st;
-    if (cache && (st = check_strides(&vs, B, Hk, T, d, dt)) != LR_OK) return st;
+    if ((st = check_strides(&qs, B, Hq, T, dt)) != LR_OK) return st;
+    if ((st = check_strides(&ks, B, Hk, T, dt)) != LR_OK) return st;
+    if (cache && (st = check_strides(&vs, B, Hk, T, dt)) != LR_OK) return st;
 
     const size_t es = esize(dt), rows = (size_t)B * T;
     const Span in[] = {strided_span(q, qs, B, Hq, T, d, dt),
@@ -221,10 +220,10 @@ lr_status lr_fwd_window(const void *q, lr_strides qs, const void *k, lr_strides 
     for (const void *p : {q, k, v, (const void *)o})
         if (!aligned16(p)) return LR_ERR_ALIGN;
     if (!aligned4(q_len) || !aligned4(k_len)) return LR_ERR_ALIGN;
-    if ((st = check_strides(&qs, B, Hq, Tq, d, dt)) != LR_OK) return st;
-    if ((st = check_strides(&os, B, Hq, Tq, d, dt)) != LR_OK) return st;
-    if ((st = check_strides(&ks, B, Hk, Tk, d, dt)) != LR_OK) return st;
-    if ((st = check_strides(&vs, B, Hk, Tk, d, dt)) != LR_OK) return st;
+    if ((st = check_strides(&qs, B, Hq, Tq, dt)) != LR_OK) return st;
+    if ((st = check_strides(&os, B, Hq, Tq, dt)) != LR_OK) return st;
+    if ((st = check_strides(&ks, B, Hk, Tk, dt)) != LR_OK) return st;
+    if ((st = check_strides(&vs, B, Hk, Tk, dt)) != LR_OK) return st;
     if (!distinct_rows(os, B, Hq, Tq, d)) return LR_ERR_ALIAS;
     const Span so = strided_span(o, os, B, Hq, Tq, d, dt);
     for (const Span &i :
@@ -242,7 +241,7 @@ lr_status lr_fwd_window(const void *q, lr_strides qs, const void *k, lr_strides 
 size_t lr_step_paged_workspace_size(int N, int Hq, int Hk, int d, int max_len, int window,
                                     int sinks, lr_dtype dt) {
     if (check_step_sizes(N, Hq, Hk, d, max_len, window, sinks, dt) != LR_OK) return 0;
-    return step_workspace_bytes(N, Hq, d, step_plan(N, Hq, Hk, max_len, window, sinks, dt));
+    return step_workspace_bytes(N, Hq, d, step_plan(N, Hk, max_len, window, sinks, dt));
 }
 
 lr_status lr_step_paged(const void *q, const lr_paged *cache, const int *lens, void *o, int N,

@@ -124,7 +124,7 @@ struct StepPlan {
     int chunk, splits;
     bool cluster;
 };
-StepPlan step_plan(int N, int Hq, int Hk, int max_len, int window, int sinks, lr_dtype dt);
+StepPlan step_plan(int N, int Hk, int max_len, int window, int sinks, lr_dtype dt);
 size_t step_workspace_bytes(int N, int Hq, int d, const StepPlan &p);
 cudaError_t launch_step_paged(const StepArgs &a, int d, lr_dtype dt, void *ws, cudaStream_t stream);
 

@@ -22,10 +22,11 @@ namespace {
 __device__ unsigned g_rope_error = 0;
 
 constexpr int NT = 256;
-// Rows in flight per lane, and CTAs per SM: the reads are what bounds the
-// kernel, and both hold them in flight.  On 2 x 16384 tokens of 16 + 4 heads
-// (bf16, 336 MB): 4 rows and 3 CTAs 72 us, 2 rows and 4 CTAs 79, 4 rows and 2
-// CTAs 85.  fp32 rows take twice the registers: two CTAs.
+// Rows in flight per lane, and CTAs per SM: both hold the reads in flight that
+// bound the kernel (with the issue of about 110 instructions a pair of rows).
+// On 2 x 16384 tokens of 16 + 4 heads (bf16, 336 MB): 65 us, 5.2 TB/s, with 4
+// rows and 3 CTAs; before the last cut in instructions 72, and 79 with 2 rows
+// and 4 CTAs, 85 with 4 rows and 2.  fp32 rows take twice the registers: two CTAs.
 constexpr int U = 4;
 template <typename E> constexpr int kCtas = sizeof(E) == 2 ? 3 : 2;
 

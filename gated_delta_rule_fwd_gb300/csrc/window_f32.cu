@@ -14,7 +14,12 @@
 // 32 keys and values come by asynchronous copies into two buffers.  At d = 128,
 // where registers leave eight warps to an SM, two groups of four warps hold the
 // same rows and take every other tile; their parts are joined at the end (8
-// heads x 2048 rows, causal: 228 -> 159 us; at d = 64 one group is 6 % faster).
+// heads x 2048 rows, causal: 228 -> 177 us; at d = 64 one group is 6 % faster).
+//
+// Measured: 4 x 8 heads x 2048 with window 512, d = 64: 160 us, 47 TFLOP/s of
+// visible work; the tensor pipe is busy 37 % of the time of an SM that has work.
+// What bounds it is the issue of about 1000 instructions per warp and tile, a
+// third of them the splitting, by few warps (registers).
 // The order of channels inside a product, and of keys inside the second one,
 // is free: it is chosen so that every lane reads 16 contiguous bytes of a row
 // without bank conflicts, and the weights stay in the registers that the

@@ -18,8 +18,8 @@
 // single tile would.
 //
 // The maximum is raised only when a row's new one exceeds the one in use by a
-// factor of 2^8 (weights then stay below 2^8, exact in the sums' fp32 range);
-// only then O in TMEM is rescaled, by the softmax warp itself: the commit that
+// factor of 2^8 (a weight is then at most 2^8, which costs fp32 sums and bf16
+// weights no precision); only then O in TMEM is rescaled, by the softmax warp itself: the commit that
 // announced the scores also covers the tile's earlier products.
 //
 // Key tiles: the sinks' (before the window of every row), then the window's
@@ -32,8 +32,14 @@
 //
 // Roles of the 384 threads: warps 0-3 softmax and output of query tile 0,
 // warps 4-7 of tile 1, warps 8 and 9 issue the products of tiles 0 and 1, warp
-// 10 the TMA loads.
+// 10 the TMA loads, warp 11 fetches the next piece of work.
 // Every wait is bounded (lr_device_status).
+//
+// Measured (d = 128): 16384 causal rows of 16 heads on 4 in 620 us, 1.77
+// PFLOP/s of visible work; with a window of 1024 and 4 sinks 126 us; 4096
+// causal rows of 32 heads 111 us.  A pair of tiles takes 2690 cycles for 2048
+// of the tensor pipe: the chain of a tile is scores -> first half of the weights
+// (1100) -> its turn on the pipe (200) -> its 16 products (930) -> scores (460).
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -451,6 +457,7 @@ __global__ void __launch_bounds__(NT, 1)
         if (lane == 0) {
             for (int t = 0; t < 2; ++t)
                 if (used[t] > 0 && !wait_bar(&bars->qfull[t], (used[t] - 1) & 1)) ok = false;
+            if (pads > 0 && !wait_bar(&bars->pad, (pads - 1) & 1)) ok = false;
             for (int i = max(0, seq - L::NS); i < seq; ++i)
                 if (!wait_bar(&bars->full[i % L::NS], (i / L::NS) & 1)) ok = false;
         }

@@ -60,8 +60,8 @@ typedef struct {
 
 typedef struct {
     unsigned flags;          /* OR of LR_QK_*                                       */
-    const float *q_weight;   /* [d] fp32, or NULL for ones                          */
-    const float *k_weight;   /* [d] fp32, or NULL for ones                          */
+    const float *q_weight;   /* [d] fp32, or NULL for ones (LR_QK_NORM)             */
+    const float *k_weight;   /* [d] fp32, or NULL for ones (LR_QK_NORM)             */
     float eps;               /* >= 0, finite                                        */
     int rot;                 /* rotated channels, the first of each head: a
                                 multiple of 16 up to d; 0: no rotation              */
@@ -140,12 +140,14 @@ lr_status lr_fwd_window(const void *q, lr_strides qs, const void *k, lr_strides 
  *   max_len bound on lens, 1 <= max_len <= page * max_pages: it sets how the
  *           work is split, so a tight bound is faster.  A longer sequence is
  *           reported as LR_ERR_INDEX and its row is left as it was.
- *   workspace   lr_step_paged_workspace_size(...) bytes (0 where the work is
- *           not split); calls that share one are ordered on one stream
+ *   workspace   lr_step_paged_workspace_size(...) bytes, 16-byte aligned (0
+ *           where the work is not split, or its parts are joined on the chip);
+ *           its contents on entry do not matter.  Calls that share one are
+ *           ordered on one stream.
  *
- * The keys a sequence sees are cut into chunks of equal size; with more than
- * one chunk a second kernel joins the parts in a fixed order, so a repeated
- * call gives the same bits.
+ * The keys a sequence sees are cut into chunks of equal size, which the CTAs
+ * of a cluster or a second kernel join in a fixed order: a repeated call gives
+ * the same bits.
  */
 lr_status lr_step_paged(const void *q, const lr_paged *cache, const int *lens, void *o, int N,
                         int Hq, int Hk, int d, int max_len, int window, int sinks, float scale,
