@@ -16,6 +16,10 @@
 // same rows and take every other tile; their parts are joined at the end (8
 // heads x 2048 rows, causal: 228 -> 177 us; at d = 64 one group is 6 % faster).
 //
+// Where the row blocks would leave most SMs idle, up to eight CTAs of a cluster
+// share one, each a run of its key tiles, and join their parts through
+// distributed shared memory (16 rows of 8 heads on 8192 keys: 680 -> 93 us).
+//
 // Measured: 4 x 8 heads x 2048 with window 512, d = 64: 160 us, 47 TFLOP/s of
 // visible work; the tensor pipe is busy 37 % of the time of an SM that has work.
 // What bounds it is the issue of about 1000 instructions per warp and tile, a
@@ -24,7 +28,10 @@
 // is free: it is chosen so that every lane reads 16 contiguous bytes of a row
 // without bank conflicts, and the weights stay in the registers that the
 // scores' product left them in.
+#include <algorithm>
+
 #include "attn_internal.cuh"
+#include "attn_join.cuh"
 #include "attn_rows.cuh"
 #include "tc_common.cuh"
 
@@ -43,6 +50,7 @@ struct Smem {
         float v[2][BK * VS];
     } group[G];
     static_assert(G == 1 || sizeof(Group) >= GT * (D / 2 + 4) * sizeof(float), "room for a group's part");
+    static_assert(sizeof(Group) >= BQ * (D + 2) * sizeof(float), "room for a CTA's part");
 };
 __device__ __forceinline__ void group_sync(int group) {
     asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(GT) : "memory");
@@ -76,8 +84,8 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-template <int D, int G>
-__global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float c, float sign) {
+template <int D, int G, bool SPLIT>
+__global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float c, float sign, int splits) {
     extern __shared__ __align__(16) uint8_t raw[];
     using S = Smem<D, G>;
     S &sm = *reinterpret_cast<S *>(raw);
@@ -87,7 +95,8 @@ __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float 
 
     const int tiles = (a.Tq + BQ - 1) / BQ;
     // the last rows see the most keys: of all heads they start first
-    const unsigned heads = (unsigned)(a.B * a.Hq), turn = blockIdx.x / heads, bh = blockIdx.x - turn * heads;
+    const unsigned block = SPLIT ? blockIdx.x / splits : blockIdx.x, rank = SPLIT ? blockIdx.x - block * splits : 0;
+    const unsigned heads = (unsigned)(a.B * a.Hq), turn = block / heads, bh = block - turn * heads;
     const int tile = tiles - 1 - (int)turn;
     const int b = bh / a.Hq, h = bh - b * a.Hq, hk = h / (a.Hq / a.Hk);
     bool bad = false;
@@ -105,13 +114,16 @@ __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float 
     const SeenKeys first = seen_keys(p0, kl, a.window, a.sinks);
     const SeenKeys last = seen_keys(p0 + rows - 1, kl, a.window, a.sinks);
     const int sink_keys = min(last.s1, first.lo), sink_tiles = (sink_keys + BK - 1) / BK;
-    const int n = sink_tiles + (last.hi > first.lo ? (last.hi - first.lo + BK - 1) / BK : 0);
+    const int all = sink_tiles + (last.hi > first.lo ? (last.hi - first.lo + BK - 1) / BK : 0);
+    const int begin = SPLIT ? (int)((long long)all * rank / splits) : 0,
+              n = SPLIT ? (int)((long long)all * (rank + 1) / splits) : all;
     auto key0 = [&](int it) { return it < sink_tiles ? it * BK : first.lo + (it - sink_tiles) * BK; };
     auto limit = [&](int it) { return it < sink_tiles ? sink_keys : last.hi; };
     // keys and values past the tile's limit are zeros
     auto load = [&](int it) {
         const int k0 = key0(it), end = limit(it);
-        float *kd = buf.k[(it / G) & 1], *vd = buf.v[(it / G) & 1];
+        const int half = ((it - begin) / G) & 1;
+        float *kd = buf.k[half], *vd = buf.v[half];
 #pragma unroll
         for (int i = 0; i < BK * D / 4 / GT; ++i) {
             const int e = i * GT + tid, r = e / (D / 4), ch = (e - r * (D / 4)) * 4;
@@ -121,7 +133,7 @@ __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float 
             copy16(vd + r * S::VS + ch, v + row * a.vs.t + ch, on);
         }
     };
-    if (group < n) load(group);
+    if (begin + group < n) load(begin + group);
     copies_commit();
 
     // queries: channels 16 i + 4 t .. + 3 of rows g and g + 8, which are two
@@ -142,7 +154,7 @@ __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float 
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
 
-    for (int it = group; it < n; it += G) {
+    for (int it = begin + group; it < n; it += G) {
         if (it + G < n) load(it + G);
         copies_commit();
         copies_wait<1>();
@@ -151,7 +163,8 @@ __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float 
         // the warp's rows: positions pw .. pw + 15
         const bool some = k0 <= pw + 15 && ((long long)k0 + BK - 1 > (long long)pw - a.window || k0 < a.sinks);
         if (some) {
-            const float *ks = buf.k[(it / G) & 1], *vs = buf.v[(it / G) & 1];
+            const int half = ((it - begin) / G) & 1;
+            const float *ks = buf.k[half], *vs = buf.v[half];
             float s[BK / 8][4], low[BK / 8][4];  // low: the parts with a lo factor
 #pragma unroll
             for (int j = 0; j < BK / 8; ++j)
@@ -274,19 +287,53 @@ __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float 
                 for (int e = 0; e < 4; ++e) part[(4 + 4 * j + e) * GT + tid] = acc[j][e];
         }
         __syncthreads();
-        if (group == 1) return;
+        if (!SPLIT && group == 1) return;
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const float m1 = part[(2 * r) * GT + tid], l1 = part[(2 * r + 1) * GT + tid];
             const float mn = fmaxf(m[r], m1);
             const float f0 = m[r] == -INFINITY ? 0.f : ex2((m[r] - mn) * c), f1 = m1 == -INFINITY ? 0.f : ex2((m1 - mn) * c);
             l[r] = l[r] * f0 + l1 * f1;
+            m[r] = mn;
 #pragma unroll
             for (int j = 0; j < D / 8; ++j)
 #pragma unroll
                 for (int e = 2 * r; e < 2 * r + 2; ++e)
                     acc[j][e] = acc[j][e] * f0 + part[(4 + 4 * j + e) * GT + tid] * f1;
         }
+    }
+    if constexpr (SPLIT) {
+        // the part over the first buffers, which no one reads any more
+        __syncthreads();
+        uint8_t *part = reinterpret_cast<uint8_t *>(&sm.group[0]);
+        float2 *stats = reinterpret_cast<float2 *>(part + BQ * D * 4);
+        if (group == 0) {
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                float sum = l[r];
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                const int row = r0 + 8 * r;
+                if (t == 0) stats[row] = make_float2(m[r], sum);
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e)
+                        *reinterpret_cast<float4 *>(part + part_at<D>(row, 8 * i + 2 * t + e)) =
+                            make_float4(acc[4 * i][2 * r + e], acc[4 * i + 1][2 * r + e],
+                                        acc[4 * i + 2][2 * r + e], acc[4 * i + 3][2 * r + e]);
+            }
+        }
+        tc::cluster_sync_all();
+        for (int row = (int)rank * (G * 4) + (int)(threadIdx.x >> 5); row < rows; row += splits * (G * 4)) {
+            float sum;
+            if (join_row<float, D>(tc::smem_u32(part), tc::smem_u32(stats), row, splits, c, o + row * a.os.t, sum))
+                continue;
+            mend_row<float, D>(q + row * a.qs.t, k, v, a.ks.t, a.vs.t, o + row * a.os.t,
+                               seen_keys(p0 + row, kl, a.window, a.sinks), a.scale, isfinite(sum));
+        }
+        tc::cluster_sync_all();  // no CTA leaves while another reads its part
+        return;
     }
     // columns 32 i + 8 t .. + 7 of rows g and g + 8
 #pragma unroll
@@ -326,20 +373,35 @@ __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float 
 
 template <int D>
 cudaError_t launch(const WindowArgs &a, int slot, cudaStream_t stream) {
-    constexpr int G = D == 128 ? 2 : 1;
-    auto *fn = window_f32_kernel<D, G>;
-    constexpr int bytes = sizeof(Smem<D, G>);
-    const cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(fn), bytes, slot);
+    constexpr int G = D == 128 ? 2 : 1, bytes = sizeof(Smem<D, G>);
+    const long long ctas = (long long)a.B * a.Hq * ((a.Tq + BQ - 1) / BQ);
+    // key tiles of a row block at most; a CTA of a cluster gets four or more of them
+    const long long most = std::min<long long>(a.Tk, (long long)a.window + BQ);
+    const long long tiles = (most + BK - 1) / BK + (std::min(a.sinks, a.Tk) + BK - 1) / BK;
+    // as many CTAs as clusters of eight find room for at once: one per SM at d = 128, two below
+    int splits = (int)std::min<long long>(std::min<long long>(8, (D == 128 ? 128 : 256) / ctas), tiles / 4);
+    if (splits < 2) splits = 1;
+    auto *fn = splits > 1 ? window_f32_kernel<D, G, true> : window_f32_kernel<D, G, false>;
+    cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(fn), bytes, slot + (splits > 1 ? 12 : 0));
     if (e != cudaSuccess) return e;
-    const int tiles = (a.Tq + BQ - 1) / BQ;
     // scale 0 gives every key the same weight; a product with it would turn
     // the mask's -inf into NaN, and 2^-100 rounds to the same weights
     const float c = a.scale == 0.f ? 7.9e-31f : fabsf(a.scale) * 1.4426950408889634f;
-    fn<<<(unsigned)(a.B * a.Hq * tiles), G * GT, bytes, stream>>>(a, c, a.scale < 0.f ? -1.f : 1.f);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(ctas * splits));
+    cfg.blockDim = dim3(G * GT);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)splits;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = splits > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, fn, a, c, a.scale < 0.f ? -1.f : 1.f, splits);
 }
 
-constexpr int kSlot = 208;  // ensure_smem_attr slots 208..210
+constexpr int kSlot = 208;  // ensure_smem_attr slots 208..210 and 220..222
 
 template <typename E>
 __global__ void window_zero_kernel(WindowArgs a, int units, long long n) {

@@ -30,6 +30,11 @@
 // put right one by one (attn_rows.cuh).  Padding behind a sequence's last key
 // is set to zero as it is loaded.
 //
+// Few rows and many keys: where the pieces of work would leave most SMs idle, a
+// cluster of up to eight CTAs takes one piece, each a run of its key tiles, and
+// joins the parts through distributed shared memory (16 rows of 8 heads on
+// 8192 keys: 88 -> 23 us).
+//
 // Roles of the 384 threads: warps 0-3 softmax and output of query tile 0,
 // warps 4-7 of tile 1, warps 8 and 9 issue the products of tiles 0 and 1, warp
 // 10 the TMA loads, warp 11 fetches the next piece of work.
@@ -43,9 +48,11 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <mutex>
 
 #include "attn_internal.cuh"
+#include "attn_join.cuh"
 #include "attn_rows.cuh"
 #include "tc_common.cuh"
 
@@ -69,7 +76,8 @@ struct Layout {
     static constexpr int NS = D > 64 ? 4 : 8;        // key and value tiles in flight
     static constexpr int Q = 0;
     static constexpr int KV = 2 * TILE;
-    static constexpr int OUT = KV + NS * TILE;       // 2 KB per softmax warp: rows on their way out
+    static constexpr int OUT = KV + NS * TILE;       // 2 KB per softmax warp: rows on their way out,
+                                                     // or (maximum, sum) of the rows of a part
     static constexpr int CLC = OUT + 8 * 2048;       // answer to a request for work, 16 bytes
     static constexpr int BAR = CLC + 16;
     static constexpr int ITEM = BAR + 384;           // two of struct Item
@@ -116,6 +124,7 @@ struct TcArgs {
     int group;        // query heads of a key head
     int tiles;        // row blocks of a head (pair)
     int span;         // heads (pairs) of all batches that are worked on together
+    int splits;       // CTAs that share a piece (a cluster)
 };
 
 // D[tmem] (+)= A[tmem] * B[smem]
@@ -212,8 +221,9 @@ struct Item {
     int b, hk, head[2], i0[2];  // first row of each query tile
     int rows[2], p0[2];         // valid rows, position of the first
     int act0[2], act1[2], all0[2], all1[2];
-    int last[2];                // last key tile that the query tile needs, -1: no rows
-    int kl, sink_keys, sink_tiles, lo, hi, n;
+    int last[2];                // last key tile that the query tile needs, -1: none
+    int kl, sink_keys, sink_tiles, lo, hi;
+    int first, n;               // the piece's key tiles: [first, n)
     int valid;                  // 0: no work is left
 
     __device__ __forceinline__ int key0(int it) const {
@@ -227,7 +237,9 @@ struct Item {
     }
 };
 
-__device__ __forceinline__ void make_item(const TcArgs &g, int block, Item &x, bool *bad) {
+// rank: of the CTA among those that share the piece (0 of 1: the whole piece).
+template <bool SPLIT>
+__device__ __forceinline__ void make_item(const TcArgs &g, int block, int rank, Item &x, bool *bad) {
     const WindowArgs &a = g.w;
     const int groups = g.pair_heads ? a.Hq / 2 : a.Hq;
     // the last rows see the most keys: of the heads whose keys and values the
@@ -272,12 +284,26 @@ __device__ __forceinline__ void make_item(const TcArgs &g, int block, Item &x, b
         x.all0[t] = min(x.n, x.sink_tiles + (f > 0 ? (f + BN - 1) / BN : 0));
         const int e = min(x.hi, p + 1) - lo;
         x.all1[t] = x.sink_tiles + (e > 0 ? e / BN : 0);
-        if (x.rows[t] > 0 && x.sink_tiles == 0 && x.act1[t] <= x.act0[t]) {
+        if (!SPLIT && x.rows[t] > 0 && x.sink_tiles == 0 && x.act1[t] <= x.act0[t]) {
             // no key for any row: one tile with everything masked gives the zeros
             x.n = max(x.n, 1);
             x.act0[t] = 0, x.act1[t] = 1, x.all0[t] = x.all1[t] = 0;
         }
         x.last[t] = x.rows[t] == 0 ? -1 : (x.act1[t] > x.act0[t] ? x.act1[t] : x.sink_tiles) - 1;
+    }
+    x.first = 0;
+    if (SPLIT) {
+        const int n = x.n;
+        x.first = (int)((long long)n * rank / g.splits);
+        x.n = (int)((long long)n * (rank + 1) / g.splits);
+#pragma unroll 1
+        for (int t = 0; t < 2; ++t) {
+            const int w = min(x.act1[t], x.n), k = min(x.sink_tiles, x.n);
+            x.last[t] = x.rows[t] == 0                     ? -1
+                        : w > max(x.act0[t], x.first)      ? w - 1
+                        : k > x.first                      ? k - 1
+                                                           : -1;
+        }
     }
 }
 
@@ -307,7 +333,29 @@ __device__ __forceinline__ int granted_block(const void *src) {
     return got ? (int)x : -1;
 }
 
+// Joins the parts of a piece, which the CTAs left as join_row wants them: one
+// warp per row, the rows shared out over the cluster.
 template <int D>
+__device__ __forceinline__ void join_parts(const TcArgs &g, const Item &x, uint32_t part, uint32_t stats) {
+    const WindowArgs &a = g.w;
+    const int warp = threadIdx.x >> 5, rank = (int)cluster_rank();
+    for (int r = rank * (NT / 32) + warp; r < 2 * BM; r += g.splits * (NT / 32)) {
+        const int t = r >> 7, row = r & (BM - 1);
+        if (row >= x.rows[t]) continue;
+        __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(a.o) + x.b * a.os.b + x.head[t] * a.os.h +
+                            (long long)(x.i0[t] + row) * a.os.t;
+        float sum;
+        if (join_row<__nv_bfloat16, D>(part, stats, r, g.splits, g.c, to, sum)) continue;
+        mend_row<__nv_bfloat16, D>(
+            static_cast<const __nv_bfloat16 *>(a.q) + x.b * a.qs.b + x.head[t] * a.qs.h +
+                (long long)(x.i0[t] + row) * a.qs.t,
+            static_cast<const __nv_bfloat16 *>(a.k) + x.b * a.ks.b + x.hk * a.ks.h,
+            static_cast<const __nv_bfloat16 *>(a.v) + x.b * a.vs.b + x.hk * a.vs.h, a.ks.t, a.vs.t, to,
+            seen_keys(x.p0[t] + row, x.kl, a.window, a.sinks), a.scale, isfinite(sum));
+    }
+}
+
+template <int D, bool SPLIT>
 __global__ void __launch_bounds__(NT, 1)
     window_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv, const TcArgs g) {
@@ -377,11 +425,13 @@ __global__ void __launch_bounds__(NT, 1)
         // at once, or blocks that are about to start would be taken from idle
         // SMs).
         if (lane == 0) {
-            int block = blockIdx.x;
+            int block = SPLIT ? blockIdx.x / g.splits : blockIdx.x;
             for (int i = 0; ok; ++i) {
                 if (i >= 2) ok = wait_bar(&bars->iempty[i & 1], ((i >> 1) - 1) & 1);
                 if (!ok) break;
-                if (i > 0) {
+                if (SPLIT && i > 0) {
+                    block = -1;  // one piece for a cluster
+                } else if (i > 0) {
                     ok = wait_bar(&bars->loaded, (i - 1) & 1);
                     if (!ok) break;
                     fence_async_smem();  // the last answer was read
@@ -394,7 +444,7 @@ __global__ void __launch_bounds__(NT, 1)
                 Item &x = items[i & 1];
                 if (block >= 0) {
                     bool bad = false;
-                    make_item(g, block, x, &bad);
+                    make_item<SPLIT>(g, block, SPLIT ? blockIdx.x % g.splits : 0, x, &bad);
                     if (bad) atomicOr(&g_wtc_error, kAttnIndex);
                 }
                 x.valid = block >= 0;
@@ -422,7 +472,7 @@ __global__ void __launch_bounds__(NT, 1)
             }
             const int n = x.n;
 #pragma unroll 1
-            for (int i = 0; i < 2 * n && ok; ++i, ++seq) {
+            for (int i = 2 * x.first; i < 2 * n && ok; ++i, ++seq) {
                 const int s = seq % L::NS, k0 = x.key0(i >> 1);
                 if (seq >= L::NS)
                     ok = __all_sync(0xffffffffu, wait_bar(&bars->empty[s], (seq / L::NS - 1) & 1));
@@ -472,7 +522,7 @@ __global__ void __launch_bounds__(NT, 1)
         const uint32_t id_o = idesc_bf16_f32_mn(BM, D, false, true);
         const uint64_t dq = tile_desc(q_s, 128, 0, 0);
         const bool lead = elect_one();
-        int seq0 = 0;   // stages of earlier pieces
+        int done_stages = 0;  // of earlier pieces
         int done = 0;   // key tiles multiplied
         int used = 0;   // pieces with any
         auto stage_wait = [&](int seq) {
@@ -481,6 +531,7 @@ __global__ void __launch_bounds__(NT, 1)
         while (const Item *px = take()) {
             const Item &x = *px;
             const int n = x.n, sink_tiles = x.sink_tiles, act0 = x.act0[t], act1 = x.act1[t], last = x.last[t];
+            const int seq0 = done_stages - 2 * x.first;  // stage of key tile 0
             const int w_last = n > 0 ? x.width(n - 1) : 0, w_sink = sink_tiles ? x.width(sink_tiles - 1) : BN;
             auto active = [&](int it) {
                 return last >= 0 && (it < sink_tiles || (it >= act0 && it < act1));
@@ -504,7 +555,7 @@ __global__ void __launch_bounds__(NT, 1)
                 mma_commit(&bars->empty[s]);
                 if (it == last) mma_commit(&bars->qempty[t]);
             };
-            int it = 0;
+            int it = x.first;
 #pragma unroll 1
             for (; it < n && ok && !active(it); ++it) skip(it);
             if (it < n && ok) {
@@ -560,7 +611,7 @@ __global__ void __launch_bounds__(NT, 1)
                 it = nx;
             }
             if (!first) ++used;
-            seq0 += 2 * n;
+            done_stages += 2 * (n - x.first);
             give_back();
         }
         if (lead) mma_commit(&bars->fin[t]);
@@ -582,7 +633,7 @@ __global__ void __launch_bounds__(NT, 1)
             const long long plo = (long long)p - a.window + 1;
             const int rlo = plo < 0 ? 0 : (int)plo;
             float m = -INFINITY, l = 0.f;
-            for (int it = 0; it < n && ok; ++it) {
+            for (int it = x.first; it < n && ok; ++it) {
                 if (it >= sink_tiles && it < act0) continue;
                 const bool whole = it >= all0 && it < all1;
                 const int k0 = x.key0(it), end = min(p + 1, x.limit(it));
@@ -680,6 +731,27 @@ __global__ void __launch_bounds__(NT, 1)
                 l += two.x + two.y;
                 ++seen;
             }
+            if (SPLIT) {
+                // the part, once the products of both query tiles have read their operands
+                for (int u = 0; u < 2; ++u)
+                    if (x.last[u] >= 0 && ok) ok = __all_sync(0xffffffffu, wait_bar(&bars->ofull[u], 0));
+                tc_fence_after();
+                *reinterpret_cast<float2 *>(sm + L::OUT + (t * BM + row) * 8) = make_float2(m, l);
+                if (n > 0 && ok) {
+#pragma unroll 1
+                    for (int ch = 0; ch < D / 32; ++ch) {
+                        float v[32];
+                        tmem_ld32(to + 32 * ch, v);
+                        tmem_ld_wait(v);
+#pragma unroll
+                        for (int i = 0; i < 8; ++i)
+                            *reinterpret_cast<float4 *>(sm + part_at<D>(t * BM + row, 8 * ch + i)) =
+                                make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                    }
+                }
+                give_back();
+                continue;
+            }
             if (n == 0) {
                 give_back();
                 continue;
@@ -757,6 +829,11 @@ __global__ void __launch_bounds__(NT, 1)
     tc_fence_before();
     __syncthreads();
     if (warp == 8) tmem_dealloc(tmem, 512);
+    if (SPLIT) {
+        cluster_sync_all();
+        join_parts<D>(g, items[0], smem_u32(sm), smem_u32(sm + L::OUT));
+        cluster_sync_all();  // no CTA leaves while another reads its part
+    }
 }
 
 PFN_cuTensorMapEncodeTiled_v12000 encoder() {
@@ -797,8 +874,6 @@ cudaError_t launch(const WindowArgs &a, int slot, cudaStream_t stream) {
     cudaError_t e = rows_map(&mq, a.q, a.qs, a.B, a.Hq, a.Tq, D);
     if (e == cudaSuccess) e = rows_map(&mk, a.k, a.ks, a.B, a.Hk, a.Tk, D);
     if (e == cudaSuccess) e = rows_map(&mv, a.v, a.vs, a.B, a.Hk, a.Tk, D);
-    if (e == cudaSuccess)
-        e = ensure_smem_attr(reinterpret_cast<const void *>(&window_tc_kernel<D>), Layout<D>::ALLOC, slot);
     if (e != cudaSuccess) return e;
     TcArgs g;
     g.w = a;
@@ -814,14 +889,33 @@ cudaError_t launch(const WindowArgs &a, int slot, cudaStream_t stream) {
     const long long kv = 4ll * D * a.Tk, pairs = (long long)a.B * (g.pair_heads ? a.Hq / 2 : a.Hq);
     const long long span = (48ll << 20) / kv;
     g.span = (int)(span < 1 ? 1 : (span < pairs ? span : pairs));
-    const unsigned grid = (unsigned)(a.B * (g.pair_heads ? a.Hq / 2 : a.Hq) * g.tiles);
-    window_tc_kernel<D><<<grid, NT, Layout<D>::ALLOC, stream>>>(mq, mk, mv, g);
-    return cudaGetLastError();
+    const long long pieces = pairs * g.tiles;
+    // Key tiles of a piece at most; a CTA of a cluster gets two or more of them.
+    const long long most = std::min<long long>(a.Tk, (long long)a.window + 2 * BM);
+    const long long tiles = (most + BN - 1) / BN + (std::min(a.sinks, a.Tk) + BN - 1) / BN;
+    // 128 CTAs: as many as clusters of eight find room for at once
+    g.splits = (int)std::min<long long>(std::min<long long>(8, 128 / pieces), tiles / 2);
+    if (g.splits < 2) g.splits = 1;
+    auto *fn = g.splits > 1 ? window_tc_kernel<D, true> : window_tc_kernel<D, false>;
+    e = ensure_smem_attr(reinterpret_cast<const void *>(fn), Layout<D>::ALLOC, slot + (g.splits > 1 ? 3 : 0));
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(pieces * g.splits));
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = Layout<D>::ALLOC;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = (unsigned)g.splits;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = g.splits > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, fn, mq, mk, mv, g);
 }
 
 }  // namespace
 
-// ensure_smem_attr slots 214..216 belong to this file.
+// ensure_smem_attr slots 214..219 belong to this file.
 cudaError_t launch_window_tc(const WindowArgs &a, int d, cudaStream_t stream) {
     if (d == 32) return launch<32>(a, 214, stream);
     if (d == 64) return launch<64>(a, 215, stream);

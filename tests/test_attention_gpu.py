@@ -82,6 +82,63 @@ def test_window_parity(dev, shape, d, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("d,Hq,Hk", [(32, 1, 1), (64, 2, 1), (128, 3, 1), (128, 4, 2)])
+@pytest.mark.parametrize("Tq,Tk,window,sinks", [(1, 700, NW, 0), (3, 1100, 600, 4), (130, 900, NW, 0), (129, 1500, 1200, 200),
+                                                (300, 520, NW, 3), (17, 4000, NW, 0)])
+def test_window_few_rows_and_many_keys(dev, dtype, d, Hq, Hk, Tq, Tk, window, sinks):
+    """Few pieces of work: the keys are shared out over the CTAs of a cluster."""
+    q, k, v = (rnd(s, 1, h, t, d, dtype=dtype) for s, h, t in ((100, Hq, Tq), (101, Hk, Tk), (102, Hk, Tk)))
+    check_window(dev, q, k, v, window, sinks, d ** -0.5, dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_window_few_rows_ragged_empty_and_not_finite(dev, dtype):
+    """The same with lengths from none on, NaN in the padding, parts of a
+    cluster without any key, a NaN that some rows see and a masked infinity."""
+    B, d, Tq, Tk = 4, 128, 40, 1400
+    q_len, k_len = [40, 7, 0, 33], [1400, 3, 900, 0]
+    q, k, v = (rnd(s, B, 2, t, d, dtype=dtype) for s, t in ((103, Tq), (104, Tk), (105, Tk)))
+    ref, size, reach, written = oa.window(*(np64(t) for t in (q, k, v)), 1300, 2, d ** -0.5, q_len, k_len)
+    bound = oa.attention_bound(ref, size, reach, Tk, d, BITS[dtype], 8 if dtype == BF16 else None)
+    for b in range(B):
+        k[b, :, k_len[b]:] = float("nan")
+        v[b, :, k_len[b]:] = float("inf")
+    v[0, 0, 70, 5] = float("inf")   # rows at 1360.. see keys from 61.. on, those at 1371.. not key 70
+    o = torch.full(q.shape, 7.0, dtype=dtype, device=dev)
+    ql, kl = (torch.tensor(x, dtype=torch.int32, device=dev) for x in (q_len, k_len))
+    lr.lr_fwd_window(q.to(dev), k.to(dev), v.to(dev), window=1300, sinks=2, q_len=ql, k_len=kl, o=o)
+    o = o.cpu()
+    sees = [oa.sees(1360 + i, 70, 1400, 1300, 2) for i in range(Tq)]
+    assert 0 < sum(sees) < Tq
+    assert all((o[0, 0, i, 5] == float("inf")) == sees[i] for i in range(Tq))
+    o[0, 0, torch.tensor(sees), 5] = 0
+    ref[0, 0, sees, 5], bound[0, 0, sees, 5] = 0, 0
+    w = np.broadcast_to(written[:, None, :, None], ref.shape)
+    within(o, np.where(w, ref, 7.0), np.where(w, bound, 0.0))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("Tk", [40, 1400])
+def test_window_infinite_value_of_a_key_without_weight(dev, Tk, dtype):
+    """A seen infinity shows even where the weight of its key, and of all keys
+    that are worked on with it, rounds to zero."""
+    d = 64
+    q, k, v = (rnd(s, 1, 1, t, d, dtype=dtype) for s, t in ((106, 4), (107, Tk), (108, Tk)))
+    q[..., 0] = 8
+    k[..., 0] = 0
+    k[:, :, :Tk // 2, 0] = -512     # scores 512 below the others'
+    v[0, 0, 3, 9] = float("-inf")
+    o = lr.lr_fwd_window(q.to(dev), k.to(dev), v.to(dev)).cpu()
+    assert (o[0, 0, :, 9] == float("-inf")).all()
+    o[..., 9] = 0
+    v[0, 0, 3, 9] = 0
+    ref, size, reach, _ = oa.window(*(np64(t) for t in (q, k, v)), NW, 0, d ** -0.5)
+    bound = oa.attention_bound(ref, size, reach, Tk, d, BITS[dtype], 8 if dtype == BF16 else None)
+    ref[..., 9], bound[..., 9] = 0, 0
+    within(o, ref, bound)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("window,sinks", [(1, 0), (5, 2), (64, 0), (64, 64), (100, 130), (NW, 0)])
 def test_window_sees_each_key_once(dev, window, sinks, dtype):
     """Zero keys weigh all seen keys alike; values that mark the key by its
