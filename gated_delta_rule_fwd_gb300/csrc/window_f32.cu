@@ -16,9 +16,9 @@
 // same rows and take every other tile; their parts are joined at the end (8
 // heads x 2048 rows, causal: 228 -> 177 us; at d = 64 one group is 6 % faster).
 //
-// Where the row blocks would leave most SMs idle, up to eight CTAs of a cluster
-// share one, each a run of its key tiles, and join their parts through
-// distributed shared memory (16 rows of 8 heads on 8192 keys: 680 -> 93 us).
+// Where the row blocks would leave SMs idle, up to eight CTAs of a cluster share
+// one, each a run of its key tiles, and join their parts through distributed
+// shared memory (cluster_size; 16 rows of 8 heads on 8192 keys: 680 -> 93 us).
 //
 // Measured: 4 x 8 heads x 2048 with window 512, d = 64: 160 us, 47 TFLOP/s of
 // visible work; the tensor pipe is busy 37 % of the time of an SM that has work.
@@ -333,54 +333,78 @@ __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float 
                                seen_keys(p0 + row, kl, a.window, a.sinks), a.scale, isfinite(sum));
         }
         tc::cluster_sync_all();  // no CTA leaves while another reads its part
-        return;
-    }
-    // columns 32 i + 8 t .. + 7 of rows g and g + 8
+    } else {
+        // columns 32 i + 8 t .. + 7 of rows g and g + 8
 #pragma unroll
-    for (int r = 0; r < 2; ++r) {
-        float sum = l[r];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key, or only scores of -inf
-        const int row = r0 + 8 * r;
-        float odd = 0.f;  // NaN once a value is not finite
+        for (int r = 0; r < 2; ++r) {
+            float sum = l[r];
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;  // no key, or only scores of -inf
+            const int row = r0 + 8 * r;
+            float odd = 0.f;  // NaN once a value is not finite
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            float y[8];
+            for (int i = 0; i < D / 32; ++i) {
+                float y[8];
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                y[u] = acc[4 * i + u][2 * r] * inv;
-                y[4 + u] = acc[4 * i + u][2 * r + 1] * inv;
-                odd = fmaf(y[u], 0.f, fmaf(y[4 + u], 0.f, odd));
+                for (int u = 0; u < 4; ++u) {
+                    y[u] = acc[4 * i + u][2 * r] * inv;
+                    y[4 + u] = acc[4 * i + u][2 * r + 1] * inv;
+                    odd = fmaf(y[u], 0.f, fmaf(y[4 + u], 0.f, odd));
+                }
+                if (row < rows) {
+                    float *to = o + row * a.os.t + 32 * i + 8 * t;
+                    *reinterpret_cast<float4 *>(to) = make_float4(y[0], y[1], y[2], y[3]);
+                    *reinterpret_cast<float4 *>(to + 4) = make_float4(y[4], y[5], y[6], y[7]);
+                }
             }
-            if (row < rows) {
-                float *to = o + row * a.os.t + 32 * i + 8 * t;
-                *reinterpret_cast<float4 *>(to) = make_float4(y[0], y[1], y[2], y[3]);
-                *reinterpret_cast<float4 *>(to + 4) = make_float4(y[4], y[5], y[6], y[7]);
+            unsigned again = __ballot_sync(0xffffffffu, row < rows && !(odd == 0.f));
+            __syncwarp();
+            for (int x = 0; x < 8; ++x) {
+                if (!((again >> (4 * x)) & 0xfu)) continue;
+                const int rr = 16 * warp + x + 8 * r;
+                mend_row<float, D>(q + rr * a.qs.t, k, v, a.ks.t, a.vs.t, o + rr * a.os.t,
+                                   seen_keys(p0 + rr, kl, a.window, a.sinks), a.scale,
+                                   isfinite(__shfl_sync(0xffffffffu, sum, 4 * x)));
             }
         }
-        unsigned again = __ballot_sync(0xffffffffu, row < rows && !(odd == 0.f));
-        __syncwarp();
-        for (int x = 0; x < 8; ++x) {
-            if (!((again >> (4 * x)) & 0xfu)) continue;
-            const int rr = 16 * warp + x + 8 * r;
-            mend_row<float, D>(q + rr * a.qs.t, k, v, a.ks.t, a.vs.t, o + rr * a.os.t,
-                               seen_keys(p0 + rr, kl, a.window, a.sinks), a.scale,
-                               isfinite(__shfl_sync(0xffffffffu, sum, 4 * x)));
-        }
     }
+}
+
+// Key tiles that row block i of a sequence without padding needs.
+int key_tiles(const WindowArgs &a, int i) {
+    const long long p0 = (long long)a.Tk - a.Tq + (long long)i * BQ, p1 = std::min<long long>(p0 + BQ, a.Tk);
+    const long long lo = std::max(0ll, p0 - a.window + 1), sinks = std::min<long long>(lo, a.sinks);
+    return p1 <= 0 ? 0 : (int)((p1 - lo + BK - 1) / BK + (sinks + BK - 1) / BK);
+}
+
+// CTAs that share a row block: what takes the least time, in key tiles of a
+// CTA.  The longest block counts, and the rounds of CTAs, each with the mean of
+// the blocks' tiles and what a CTA costs besides: its start, first loads and
+// join take as long as 4 tiles at d = 128 (2.7 us each), 9 below (1.3 us).
+// Measured, one CTA a block and as chosen: 80 blocks of 34 tiles, d = 128: 96
+// and 82 us (by 3; by 2, which needs two rounds as well, 108); 1024 rows of 8
+// heads, causal: 91 and 57 (by 2; by 3 75); d = 64, 2048 rows of 8 heads: 119
+// and 93 (by 2; by 3 97); 512 rows of 32: 34 (alone; by 2 38).
+int cluster_size(const WindowArgs &a, long long ctas, int per_sm, int over) {
+    if (ctas > 8 * kClusterRoom[per_sm - 1][1]) return 1;  // the last round hardly counts
+    const int blocks = (a.Tq + BQ - 1) / BQ;
+    const int longest = key_tiles(a, blocks - 1), mean = key_tiles(a, (blocks - 1) / 2);
+    int best = 1;
+    float least = 0.f;
+    for (int s = 1; s <= kMostSplits && (s == 1 || longest >= 4 * s); ++s) {
+        const long long room = kClusterRoom[per_sm - 1][s], rounds = (ctas * s + room - 1) / room;
+        const float cost = std::max((float)longest / s + over, rounds * ((float)mean / s + over));
+        if (s == 1 || cost < least) best = s, least = cost;
+    }
+    return best;
 }
 
 template <int D>
 cudaError_t launch(const WindowArgs &a, int slot, cudaStream_t stream) {
     constexpr int G = D == 128 ? 2 : 1, bytes = sizeof(Smem<D, G>);
     const long long ctas = (long long)a.B * a.Hq * ((a.Tq + BQ - 1) / BQ);
-    // key tiles of a row block at most; a CTA of a cluster gets four or more of them
-    const long long most = std::min<long long>(a.Tk, (long long)a.window + BQ);
-    const long long tiles = (most + BK - 1) / BK + (std::min(a.sinks, a.Tk) + BK - 1) / BK;
-    // as many CTAs as clusters of eight find room for at once: one per SM at d = 128, two below
-    int splits = (int)std::min<long long>(std::min<long long>(8, (D == 128 ? 128 : 256) / ctas), tiles / 4);
-    if (splits < 2) splits = 1;
+    const int splits = D == 128 ? cluster_size(a, ctas, 1, 4) : cluster_size(a, ctas, 2, 9);
     auto *fn = splits > 1 ? window_f32_kernel<D, G, true> : window_f32_kernel<D, G, false>;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(fn), bytes, slot + (splits > 1 ? 12 : 0));
     if (e != cudaSuccess) return e;
