@@ -131,7 +131,7 @@ lr_status check_step_sizes(int N, int Hq, int Hk, int d, int max_len, int window
     if (N < 1 || max_len < 1 || window < 1 || sinks < 0) return LR_ERR_SHAPE;
     if (max_len > (1 << 30) || !count_ok(N, Hq, d, 1)) return LR_ERR_SHAPE;
     // CTAs of one launch
-    const StepPlan p = step_plan(N, Hk, max_len, window, sinks, dt);
+    const StepPlan p = step_plan(N, Hq, Hk, d, max_len, window, sinks, dt);
     if (!count_ok(N, Hq, p.splits, 1) || (long long)N * Hq * p.splits > 0x7fffffffll)
         return LR_ERR_SHAPE;
     return LR_OK;
@@ -241,7 +241,7 @@ lr_status lr_fwd_window(const void *q, lr_strides qs, const void *k, lr_strides 
 size_t lr_step_paged_workspace_size(int N, int Hq, int Hk, int d, int max_len, int window,
                                     int sinks, lr_dtype dt) {
     if (check_step_sizes(N, Hq, Hk, d, max_len, window, sinks, dt) != LR_OK) return 0;
-    return step_workspace_bytes(N, Hq, d, step_plan(N, Hk, max_len, window, sinks, dt));
+    return step_workspace_bytes(N, Hq, d, step_plan(N, Hq, Hk, d, max_len, window, sinks, dt));
 }
 
 lr_status lr_step_paged(const void *q, const lr_paged *cache, const int *lens, void *o, int N,

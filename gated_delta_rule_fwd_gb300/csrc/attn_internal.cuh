@@ -96,6 +96,15 @@ cudaError_t launch_qk_norm_rope(const void *q, lr_strides qs, const void *k, lr_
                                 const void *v, lr_strides vs, const lr_paged *cache, int B, int T,
                                 int Hq, int Hk, int d, lr_dtype dt, cudaStream_t stream);
 
+constexpr int kMostCluster = 8;  // CTAs of the largest cluster that is always allowed
+// CTAs of clusters of 1, 2, .. 8 that find room on the GPU at once with one to
+// four of them on an SM (the occupancy calculator's answers: a cluster stays
+// within one of the GPU's groups of SMs, which it does not always fill).
+constexpr int kClusterRoom[4][kMostCluster + 1] = {{0, 152, 152, 138, 144, 140, 138, 105, 120},
+                                                   {0, 304, 304, 291, 296, 290, 276, 266, 288},
+                                                   {0, 456, 456, 444, 440, 435, 444, 413, 408},
+                                                   {0, 608, 608, 582, 592, 585, 582, 567, 592}};
+
 struct WindowArgs {
     const void *q, *k, *v;
     void *o;
@@ -124,7 +133,7 @@ struct StepPlan {
     int chunk, splits;
     bool cluster;
 };
-StepPlan step_plan(int N, int Hk, int max_len, int window, int sinks, lr_dtype dt);
+StepPlan step_plan(int N, int Hq, int Hk, int d, int max_len, int window, int sinks, lr_dtype dt);
 size_t step_workspace_bytes(int N, int Hq, int d, const StepPlan &p);
 cudaError_t launch_step_paged(const StepArgs &a, int d, lr_dtype dt, void *ws, cudaStream_t stream);
 

@@ -10,13 +10,6 @@
 
 namespace lr {
 
-constexpr int kMostSplits = 8;  // the largest cluster that is always allowed
-// CTAs of clusters of 1, 2, .. 8 that find room on the GPU at once with one and
-// with two on an SM (the occupancy calculator's answers: a cluster stays within
-// one of the GPU's groups of SMs, which it does not always fill).
-constexpr int kClusterRoom[2][kMostSplits + 1] = {{0, 152, 152, 138, 144, 140, 138, 105, 120},
-                                                  {0, 304, 304, 291, 296, 290, 276, 266, 288}};
-
 // Byte offset of a 16-byte chunk of a row.
 template <int D> __device__ __forceinline__ uint32_t part_at(int row, int chunk) {
     return (uint32_t)(row * D * 4 + ((chunk ^ (row & (D / 4 - 1))) * 16));

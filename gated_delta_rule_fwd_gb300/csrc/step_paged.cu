@@ -32,7 +32,6 @@ namespace {
 __device__ unsigned g_step_error = 0;
 
 constexpr int NT = 128;
-constexpr int kMostCluster = 8;  // chunks that a cluster joins
 
 // fp32 partial results in the workspace: [N * Hq][splits][d], then
 // (maximum, sum) [N * Hq][splits].
@@ -550,6 +549,12 @@ Parts parts_of(const StepArgs &a, int d, const StepPlan &p, void *ws) {
     return r;
 }
 
+// Query heads that a CTA takes, of G that share a key head.
+int heads_of_cta(int G, lr_dtype dt) {
+    if (dt == LR_DT_BF16) return G <= 8 ? 8 : 16;
+    return G == 1 ? 1 : G == 2 ? 2 : 4;
+}
+
 // Launches a step kernel, its chunks as clusters where the plan says so.
 template <typename... A>
 cudaError_t launch_parts(void (*fn)(StepArgs, Parts, A...), unsigned grid, cudaStream_t stream,
@@ -578,7 +583,7 @@ float exp2_scale(float scale) {
 template <int D>
 cudaError_t launch_f32(const StepArgs &a, const Parts &parts, cudaStream_t stream) {
     const int G = a.Hq / a.Hk;
-    const int gc = G == 1 ? 1 : G == 2 ? 2 : 4;
+    const int gc = heads_of_cta(G, LR_DT_F32);
     const unsigned grid = (unsigned)(a.N * a.Hk * ((G + gc - 1) / gc) * parts.splits);
     if (gc == 1) return launch_parts(&step_simt_kernel<D, 1>, grid, stream, a, parts);
     if (gc == 2) return launch_parts(&step_simt_kernel<D, 2>, grid, stream, a, parts);
@@ -587,7 +592,7 @@ cudaError_t launch_f32(const StepArgs &a, const Parts &parts, cudaStream_t strea
 
 template <int D>
 cudaError_t launch_bf16(const StepArgs &a, const Parts &parts, cudaStream_t stream) {
-    const int G = a.Hq / a.Hk, heads = G <= 8 ? 8 : 16;
+    const int G = a.Hq / a.Hk, heads = heads_of_cta(G, LR_DT_BF16);
     const unsigned grid = (unsigned)(a.N * a.Hk * ((G + heads - 1) / heads) * parts.splits);
     const float c = exp2_scale(a.scale);
     const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
@@ -597,7 +602,7 @@ cudaError_t launch_bf16(const StepArgs &a, const Parts &parts, cudaStream_t stre
 
 template <int D>
 cudaError_t launch(const StepArgs &a, void *ws, lr_dtype dt, cudaStream_t stream) {
-    const StepPlan p = step_plan(a.N, a.Hk, a.max_len, a.window, a.sinks, dt);
+    const StepPlan p = step_plan(a.N, a.Hq, a.Hk, D, a.max_len, a.window, a.sinks, dt);
     const Parts parts = parts_of(a, D, p, ws);
     const cudaError_t e = dt == LR_DT_F32 ? launch_f32<D>(a, parts, stream) : launch_bf16<D>(a, parts, stream);
     if (e != cudaSuccess || p.splits == 1 || p.cluster) return e;
@@ -609,16 +614,20 @@ cudaError_t launch(const StepArgs &a, void *ws, lr_dtype dt, cudaStream_t stream
 
 }  // namespace
 
-StepPlan step_plan(int N, int Hk, int max_len, int window, int sinks, lr_dtype dt) {
+StepPlan step_plan(int N, int Hq, int Hk, int d, int max_len, int window, int sinks, lr_dtype dt) {
     const long long w = (long long)window + sinks;
     // whole tiles in bf16: the sinks' and the window's first and last may be cut
     const long long most = w < max_len ? w + (dt == LR_DT_BF16 ? 2 * kTile + (sinks > 0 ? kTile : 0) : 0) : max_len;
     const int seen = (int)(most < max_len ? most : max_len);
-    // CTAs that run at once: three per SM hold the registers of the bf16 kernel
-    // at d = 128 (more at smaller widths, where one wave matters less), four or
-    // five in fp32 (33 sequences with window 1024: 26 us with 4, 39 with 3, 33
+    // CTAs that run at once: an SM holds the registers of three of the bf16
+    // kernel at d = 128 (two with more than 8 heads; more at smaller widths,
+    // where one wave matters less), of three in fp32 with four heads, else of
+    // four or five (33 sequences with window 1024: 26 us with 4, 39 with 3, 33
     // with 6).
-    const long long rows = (long long)N * Hk, wave = 152 * (dt == LR_DT_BF16 ? 3 : 4);
+    const int G = Hq / Hk, heads = heads_of_cta(G, dt);
+    const int per_sm = dt == LR_DT_BF16 ? (heads == 8 ? 3 : 2) : (heads == 4 ? 3 : 4);
+    const int *room = kClusterRoom[(dt == LR_DT_BF16 && d < 128 ? 4 : per_sm) - 1];
+    const long long rows = (long long)N * Hk * ((G + heads - 1) / heads), wave = 152 * per_sm;
     auto cut = [](long long keys, long long parts) {  // chunks of whole 64s, 64 at least
         const long long c = ((keys + parts - 1) / parts + 63) / 64 * 64;
         return c < 64 ? 64 : c;
@@ -628,16 +637,22 @@ StepPlan step_plan(int N, int Hk, int max_len, int window, int sinks, lr_dtype d
     // 113 us on two 131K caches, one 87); for few rows up to 4096 keys, with
     // more rows pieces of 1024, which even out sequences of different lengths
     // (128 of 500 to 8192 keys: 355 us with 1024, 378 with 4096, 411 with 256).
-    long long chunk = cut(seen, rows < wave ? wave / rows : 1);
+    long long parts = rows < wave ? wave / rows : 1;
+    // a cluster too many would be a second wave (8 sequences of 8192, 8 key
+    // heads: 47 us by 6, 71 by 7)
+    if (parts <= kMostCluster)
+        while (parts > 1 && rows * parts > room[parts]) --parts;
+    long long chunk = cut(seen, parts);
     if (chunk > (4 * rows <= wave ? kTile * kMostTiles : 1024)) chunk = 1024;
     p.chunk = (int)chunk;
     p.splits = (int)((seen + chunk - 1) / chunk);
-    // Eight chunks or fewer in one wave: a cluster joins them.  It does so too
+    // Eight chunks or fewer that find room: a cluster joins them.  It does so too
     // where 512 keys for a CTA still leave eight chunks: one launch less is
     // worth more than the rest of the wave.
     const long long eighth = cut(seen, kMostCluster);
     p.cluster = false;
-    if (p.splits > 1 && rows * (p.splits < kMostCluster ? p.splits : kMostCluster) <= wave &&
+    const int most_parts = p.splits < kMostCluster ? p.splits : kMostCluster;
+    if (p.splits > 1 && rows * most_parts <= room[most_parts] &&
         (p.splits <= kMostCluster || eighth <= 512)) {
         if (p.splits > kMostCluster) {
             p.chunk = (int)eighth;

@@ -392,7 +392,7 @@ int cluster_size(const WindowArgs &a, long long ctas, int per_sm, int over) {
     const int longest = key_tiles(a, blocks - 1), mean = key_tiles(a, (blocks - 1) / 2);
     int best = 1;
     float least = 0.f;
-    for (int s = 1; s <= kMostSplits && (s == 1 || longest >= 4 * s); ++s) {
+    for (int s = 1; s <= kMostCluster && (s == 1 || longest >= 4 * s); ++s) {
         const long long room = kClusterRoom[per_sm - 1][s], rounds = (ctas * s + room - 1) / room;
         const float cost = std::max((float)longest / s + over, rounds * ((float)mean / s + over));
         if (s == 1 || cost < least) best = s, least = cost;

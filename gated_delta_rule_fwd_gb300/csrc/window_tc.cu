@@ -894,7 +894,7 @@ cudaError_t launch(const WindowArgs &a, int slot, cudaStream_t stream) {
     const long long most = std::min<long long>(a.Tk, (long long)a.window + 2 * BM);
     const long long tiles = (most + BN - 1) / BN + (std::min(a.sinks, a.Tk) + BN - 1) / BN;
     // All clusters run at once: a second round would cost as much as the first.
-    g.splits = (int)std::max(1ll, std::min<long long>(kMostSplits, tiles / 2));
+    g.splits = (int)std::max(1ll, std::min<long long>(kMostCluster, tiles / 2));
     while (g.splits > 1 && pieces * g.splits > kClusterRoom[0][g.splits]) --g.splits;
     auto *fn = g.splits > 1 ? window_tc_kernel<D, true> : window_tc_kernel<D, false>;
     e = ensure_smem_attr(reinterpret_cast<const void *>(fn), Layout<D>::ALLOC, slot + (g.splits > 1 ? 3 : 0));
