@@ -380,21 +380,24 @@ int key_tiles(const WindowArgs &a, int i) {
 
 // CTAs that share a row block: what takes the least time, in key tiles of a
 // CTA.  The longest block counts, and the rounds of CTAs, each with the mean of
-// the blocks' tiles and what a CTA costs besides: its start, first loads and
-// join take as long as 4 tiles at d = 128 (2.7 us each), 9 below (1.3 us).
+// the blocks' tiles and what a CTA costs besides: `start` is the time of its
+// launch and first loads, `join` of joining the parts.  A tile takes 2.7 us at
+// d = 128, 1.3 below.
 // Measured, one CTA a block and as chosen: 80 blocks of 34 tiles, d = 128: 96
 // and 82 us (by 3; by 2, which needs two rounds as well, 108); 1024 rows of 8
 // heads, causal: 91 and 57 (by 2; by 3 75); d = 64, 2048 rows of 8 heads: 119
-// and 93 (by 2; by 3 97); 512 rows of 32: 34 (alone; by 2 38).
-int cluster_size(const WindowArgs &a, long long ctas, int per_sm, int over) {
+// and 93 (by 2; by 3 97); 512 rows of 32: 34 (alone; by 2 38); 215 rows of 6,
+// d = 128: 24 and 13 (by 5); 173 rows of 32, window 64, d = 64: 9.5 (alone; by
+// 3 14).
+int cluster_size(const WindowArgs &a, long long ctas, int per_sm, int start, int join) {
     if (ctas > 8 * kClusterRoom[per_sm - 1][1]) return 1;  // the last round hardly counts
     const int blocks = (a.Tq + BQ - 1) / BQ;
     const int longest = key_tiles(a, blocks - 1), mean = key_tiles(a, (blocks - 1) / 2);
     int best = 1;
     float least = 0.f;
-    for (int s = 1; s <= kMostCluster && (s == 1 || longest >= 4 * s); ++s) {
+    for (int s = 1; s <= kMostCluster && (s == 1 || longest >= s); ++s) {
         const long long room = kClusterRoom[per_sm - 1][s], rounds = (ctas * s + room - 1) / room;
-        const float cost = std::max((float)longest / s + over, rounds * ((float)mean / s + over));
+        const float cost = std::max((float)longest / s + start, rounds * ((float)mean / s + start)) + (s > 1 ? join : 0);
         if (s == 1 || cost < least) best = s, least = cost;
     }
     return best;
@@ -404,7 +407,7 @@ template <int D>
 cudaError_t launch(const WindowArgs &a, int slot, cudaStream_t stream) {
     constexpr int G = D == 128 ? 2 : 1, bytes = sizeof(Smem<D, G>);
     const long long ctas = (long long)a.B * a.Hq * ((a.Tq + BQ - 1) / BQ);
-    const int splits = D == 128 ? cluster_size(a, ctas, 1, 4) : cluster_size(a, ctas, 2, 9);
+    const int splits = D == 128 ? cluster_size(a, ctas, 1, 3, 1) : cluster_size(a, ctas, 2, 7, 5);
     auto *fn = splits > 1 ? window_f32_kernel<D, G, true> : window_f32_kernel<D, G, false>;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(fn), bytes, slot + (splits > 1 ? 12 : 0));
     if (e != cudaSuccess) return e;

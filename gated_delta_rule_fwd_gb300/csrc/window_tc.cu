@@ -890,12 +890,18 @@ cudaError_t launch(const WindowArgs &a, int slot, cudaStream_t stream) {
     const long long span = (48ll << 20) / kv;
     g.span = (int)(span < 1 ? 1 : (span < pairs ? span : pairs));
     const long long pieces = pairs * g.tiles;
-    // Key tiles of a piece at most; a CTA of a cluster gets two or more of them.
-    const long long most = std::min<long long>(a.Tk, (long long)a.window + 2 * BM);
-    const long long tiles = (most + BN - 1) / BN + (std::min(a.sinks, a.Tk) + BN - 1) / BN;
-    // All clusters run at once: a second round would cost as much as the first.
-    g.splits = (int)std::max(1ll, std::min<long long>(kMostCluster, tiles / 2));
-    while (g.splits > 1 && pieces * g.splits > kClusterRoom[0][g.splits]) --g.splits;
+    // Key tiles of a piece at most.  All clusters have to run at once: a second
+    // round would cost as much as the first.  The join takes as long as four
+    // tiles (64 rows of 32 heads on 4096 keys: 49 us alone, 20.6 by 6; 4 heads,
+    // d = 128, 100 rows: on 1024 keys 15.7 alone, 15.2 by 2, 10.9 by 8; on 512
+    // 10.6 alone, 12.5 by 2).
+    const long long most = std::min<long long>(a.Tk, (long long)a.window + (g.pair_heads ? 1 : 2) * BM);
+    const int tiles = (int)((most + BN - 1) / BN) + (std::min(a.sinks, a.Tk) + BN - 1) / BN;
+    g.splits = 1;
+    for (int s = 2, least = tiles; s <= kMostCluster && s <= tiles; ++s) {
+        const int cost = (tiles + s - 1) / s + 4;
+        if (pieces * s <= kClusterRoom[0][s] && cost < least) g.splits = s, least = cost;
+    }
     auto *fn = g.splits > 1 ? window_tc_kernel<D, true> : window_tc_kernel<D, false>;
     e = ensure_smem_attr(reinterpret_cast<const void *>(fn), Layout<D>::ALLOC, slot + (g.splits > 1 ? 3 : 0));
     if (e != cudaSuccess) return e;
