@@ -24,9 +24,11 @@ __device__ unsigned g_rope_error = 0;
 constexpr int NT = 256;
 // Rows in flight per lane, and CTAs per SM: both hold the reads in flight that
 // bound the kernel (with the issue of about 110 instructions a pair of rows).
-// On 2 x 16384 tokens of 16 + 4 heads (bf16, 336 MB): 65 us, 5.2 TB/s, with 4
-// rows and 3 CTAs; before the last cut in instructions 72, and 79 with 2 rows
-// and 4 CTAs, 85 with 4 rows and 2.  fp32 rows take twice the registers: two CTAs.
+// On 2 x 16384 tokens of 16 + 4 heads (bf16, 336 MB): 62 us, 5.4 TB/s, with 4
+// rows and 3 CTAs; before the last cuts in instructions 72, and 79 with 2 rows
+// and 4 CTAs, 85 with 4 rows and 2.  Fetching each next row as its place is
+// free, across queries, keys and tokens, costs more instructions than it hides
+// (65 to 67).  fp32 rows take twice the registers: two CTAs.
 constexpr int U = 4;
 template <typename E> constexpr int kCtas = sizeof(E) == 2 ? 3 : 2;
 
@@ -118,6 +120,7 @@ __global__ void __launch_bounds__(NT, kCtas<E>) qk_norm_rope_kernel(RopeArgs a) 
         const E *q_from = static_cast<const E *>(a.q) + b * a.qs.b + t * a.qs.t + c0;
         Row8<E> r[U];
         fetch_rows(r, q_from, a.qs.h, a.Hq, part);
+        if (!__any_sync(0xffffffffu, on)) continue;  // padding
         long long place = -1;  // first cache row of the token (head 0)
         if (a.ck && on) {
             const int pg = p >> a.page_log2;
@@ -182,23 +185,47 @@ __global__ void __launch_bounds__(NT, kCtas<E>) qk_norm_rope_kernel(RopeArgs a) 
 #pragma unroll 1
             for (int h0 = part; h0 - part < count; h0 += parts * U) {
                 if (h0 != part) fetch_rows(r, src, stride, count, h0);
+                // bf16: the sums of the U rows together, with half the shuffles; lane
+                // 4 j + u of a row ends up with row u's, takes its root and hands it to
+                // the others (2 x 16384 tokens of 16 + 4 heads: 64.1 -> 62.1 us; fp32,
+                // which is bound by its bytes, 107 -> 113).
+                constexpr bool TOGETHER = sizeof(E) == 2;
+                static_assert(U == 4, "four rows' sums");
+                float inv = 1.f;
+                if (TOGETHER && norm) {
+                    float sum[U];
+#pragma unroll
+                    for (int u = 0; u < U; ++u) {
+                        float2 ss = mul2(r[u].pair(0), r[u].pair(0));
+#pragma unroll
+                        for (int i = 1; i < 4; ++i) ss = fma2(r[u].pair(i), r[u].pair(i), ss);
+                        sum[u] = ss.x + ss.y;
+                    }
+                    const bool one = tid & 1, two = tid & 2;
+                    const float a0 = (one ? sum[1] : sum[0]) + __shfl_xor_sync(0xffffffffu, one ? sum[0] : sum[1], 1);
+                    const float a1 = (one ? sum[3] : sum[2]) + __shfl_xor_sync(0xffffffffu, one ? sum[2] : sum[3], 1);
+                    float all = (two ? a1 : a0) + __shfl_xor_sync(0xffffffffu, two ? a0 : a1, 2);
+#pragma unroll
+                    for (int m = 4; m < LANES; m <<= 1) all += __shfl_xor_sync(0xffffffffu, all, m);
+                    inv = rsqrtf(all * (1.f / D) + a.maps.eps);
+                }
 #pragma unroll
                 for (int u = 0; u < U; ++u) {
                     if (h0 - part + u * parts >= count) break;  // for all lanes
                     float2 x[4];
 #pragma unroll
                     for (int i = 0; i < 4; ++i) x[i] = r[u].pair(i);
-                    float inv = 1.f;
-                    if (norm) {
+                    float of_u = TOGETHER ? __shfl_sync(0xffffffffu, inv, (tid & 28) | u) : 1.f;
+                    if (!TOGETHER && norm) {
                         float2 ss = mul2(x[0], x[0]);
 #pragma unroll
                         for (int i = 1; i < 4; ++i) ss = fma2(x[i], x[i], ss);
                         float sum = ss.x + ss.y;
 #pragma unroll
                         for (int m = 1; m < LANES; m <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-                        inv = rsqrtf(sum * (1.f / D) + a.maps.eps);
+                        of_u = rsqrtf(sum * (1.f / D) + a.maps.eps);
                     }
-                    const float2 inv2 = make_float2(inv, inv);
+                    const float2 inv2 = make_float2(of_u, of_u);
                     Row8<E> y;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
