@@ -118,6 +118,26 @@ def test_window_few_rows_ragged_empty_and_not_finite(dev, dtype):
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("d,Tq,Tk", [(32, 1, 1100), (128, 2, 300), (64, 65, 200)])
+@pytest.mark.parametrize("H", [5, 13, 15, 16, 19, 23, 27, 33, 37, 45, 70, 76, 77, 150])
+def test_window_cluster_sizes(dev, dtype, d, Tq, Tk, H):
+    """Numbers of heads that are given to clusters of every size and to none,
+    with fewer and more key tiles than CTAs."""
+    q, k, v = (rnd(s, 1, H, t, d, dtype=dtype) for s, t in ((109, Tq), (110, Tk), (111, Tk)))
+    check_window(dev, q, k, v, NW, 0, d ** -0.5, dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_window_cluster_lengths(dev, dtype):
+    """Shared pieces where the lengths leave a CTA many tiles, one, or none."""
+    B, d, Tq, Tk = 6, 64, 70, 900
+    q, k, v = (rnd(s, B, 2, t, d, dtype=dtype) for s, t in ((112, Tq), (113, Tk), (114, Tk)))
+    for window, sinks in ((NW, 0), (300, 0), (300, 150)):
+        check_window(dev, q, k, v, window, sinks, d ** -0.5, [70, 1, 69, 70, 0, 3], [900, 128, 33, 70, 500, 897],
+                     dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("Tk", [40, 1400])
 def test_window_infinite_value_of_a_key_without_weight(dev, Tk, dtype):
     """A seen infinity shows even where the weight of its key, and of all keys
@@ -417,6 +437,16 @@ def test_step_cut_by_the_bound_on_the_length(dev, dtype, max_len, window, sinks)
 
 
 @pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("d,Hq,Hk", [(32, 8, 8), (128, 8, 2), (64, 17, 1)])
+@pytest.mark.parametrize("N", [6, 7, 8, 9, 13, 19, 26, 38])
+def test_step_cluster_sizes(dev, dtype, d, Hq, Hk, N):
+    """Numbers of sequences that are given to clusters of every size."""
+    lens = [(1500 - 41 * i) % 1501 for i in range(N)]
+    kc, vc, table = paged(N, lens, Hk, 64, d, dtype, dev)
+    check_step(dev, rnd(52, N, Hq, d, dtype=dtype), kc, vc, table, lens, NW, 0)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
 @pytest.mark.parametrize("d", [32, 64, 128])
 @pytest.mark.parametrize("Hq,Hk", [(1, 1), (4, 2), (3, 1), (8, 1), (5, 1), (17, 1), (6, 6)])
 @pytest.mark.parametrize("page,window,sinks", [(16, NW, 0), (64, 40, 5), (128, 130, 20)])
@@ -650,6 +680,24 @@ def test_norm_rope_parity(dev, case, dtype, append):
                     wk[tb[b, p // page], :, p % page] = kh[b, :, t]
                     wv[tb[b, p // page], :, p % page] = v[b, :, t]
         assert torch.equal(kc.cpu(), wk) and torch.equal(vc.cpu(), wv)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("d,B,T", [(128, 3, 1), (64, 2, 90), (32, 4, 3000)])
+def test_norm_rope_long_padding(dev, dtype, d, B, T):
+    """Whole stretches of padding: what is computed behind and before them is
+    as it is without them, and the padded rows stay as they were."""
+    q, k = (rnd(s, B, h, T, d, dtype=dtype).to(dev) for s, h in ((46, 5), (47, 2)))
+    f = torch.tensor(10000.0 ** (-np.arange(d // 2) / (d // 2)), device=dev)
+    pos = torch.arange(T, dtype=torch.int32, device=dev).expand(B, T).contiguous()
+    want = lr.lr_qk_norm_rope(q, k, pos, inv_freq=f)
+    pos[0] = -1
+    pos[1, T // 3:T // 3 * 2 + 1] = -1
+    got = (torch.full_like(want[0], 7.0), torch.full_like(want[1], 7.0))
+    lr.lr_qk_norm_rope(q, k, pos, inv_freq=f, q_out=got[0], k_out=got[1])
+    for g, w in zip(got, want):
+        on = (pos >= 0)[:, None, :, None]
+        assert torch.equal(g, torch.where(on, w, torch.full_like(w, 7.0)))
 
 
 def test_norm_rope_default_positions_and_cache_only_keys(dev):
