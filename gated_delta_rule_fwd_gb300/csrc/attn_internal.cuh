@@ -37,6 +37,18 @@ __device__ __forceinline__ int clamp_len(const int *len, int b, int most, bool *
     return x < 0 ? 0 : (x > most ? most : x);
 }
 
+// A score enters as sign * (q . k), formed in fp32 before any scale, and its
+// weight is 2^(c (score - maximum)): no finite scale can push a finite score
+// out of range.
+struct ScoreFactor {
+    float sign, c;
+};
+__host__ __device__ __forceinline__ ScoreFactor score_factor(float scale) {
+    // scale 0: all scores are zero, whatever c is
+    return {scale > 0.f ? 1.f : (scale < 0.f ? -1.f : 0.f),
+            scale == 0.f ? 1.f : fminf(fabsf(scale) * 1.4426950408889634f, 3.402823466e38f)};
+}
+
 // ------------------------------------------------------------------ arithmetic
 // 2^x, results below the normal range zero
 __device__ __forceinline__ float ex2(float x) {

@@ -7,9 +7,10 @@
 //
 //   - a sum of weights that is not finite: where a score that the row sees is
 //     NaN or +inf every channel is NaN.  Operands at the type's ends make the
-//     sum NaN as well (their products with the scale, or their split parts,
-//     leave the range), so the scores are formed once more to tell, 32 keys at
-//     a time; if none is NaN or +inf the row is computed again;
+//     sum NaN as well (their split parts, or the maximum times the scale, leave
+//     the range; window_tc.cu sets it to NaN where they made it vanish), so the
+//     scores are formed once more to tell, 32 keys at a time; if none is NaN or
+//     +inf the row is computed again, from differences of unscaled scores;
 //   - a channel in which the row sees a NaN, or infinities of both signs, is
 //     NaN; one in which it sees infinities of one sign is that infinity (every
 //     weight is positive);
@@ -36,7 +37,7 @@ __device__ __forceinline__ float warp_sum(float x) {
 // calls this with the same arguments.
 template <typename E, int D>
 __device__ __forceinline__ void mend_row(const E *q, const E *k, const E *v, long long kt, long long vt,
-                                         E *o, SeenKeys s, float scale, bool sum_finite) {
+                                         E *o, SeenKeys s, ScoreFactor f, bool sum_finite) {
     constexpr int PL = D / 32;  // channels of a lane: lane + 32 i
     const int lane = threadIdx.x & 31;
     bool whole_row = false;
@@ -54,7 +55,7 @@ __device__ __forceinline__ void mend_row(const E *q, const E *k, const E *v, lon
                     x += a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
                 }
             }
-            bad = __any_sync(0xffffffffu, !(x * scale < INFINITY));
+            bad = __any_sync(0xffffffffu, !(x * f.sign < INFINITY));
         }
         if (bad) {
 #pragma unroll
@@ -95,7 +96,7 @@ __device__ __forceinline__ void mend_row(const E *q, const E *k, const E *v, lon
     if (again) {
         float qr[PL], m = -INFINITY, l = 0.f;
 #pragma unroll
-        for (int i = 0; i < PL; ++i) qr[i] = to_f<E>(q[lane + 32 * i]) * scale;
+        for (int i = 0; i < PL; ++i) qr[i] = to_f<E>(q[lane + 32 * i]) * f.sign;
 #pragma unroll 1
         for (int j = 0; j < s.hi; ++j) {
             if (j == s.s1 && j < s.lo) j = s.lo;
@@ -106,7 +107,7 @@ __device__ __forceinline__ void mend_row(const E *q, const E *k, const E *v, lon
             x = warp_sum(x);
             if (x == -INFINITY) continue;  // weight zero
             // a running mean, which no large value can drive out of range
-            const float mn = fmaxf(m, x), old = l * (m == -INFINITY ? 0.f : expf(m - mn)), p = expf(x - mn);
+            const float mn = fmaxf(m, x), old = l * (m == -INFINITY ? 0.f : ex2((m - mn) * f.c)), p = ex2((x - mn) * f.c);
             m = mn;
             l = old + p;
             const float keep = old / l, take = p / l;

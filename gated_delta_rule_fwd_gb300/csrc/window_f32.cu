@@ -330,7 +330,7 @@ __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float 
             if (join_row<float, D>(tc::smem_u32(part), tc::smem_u32(stats), row, splits, c, o + row * a.os.t, sum))
                 continue;
             mend_row<float, D>(q + row * a.qs.t, k, v, a.ks.t, a.vs.t, o + row * a.os.t,
-                               seen_keys(p0 + row, kl, a.window, a.sinks), a.scale, isfinite(sum));
+                               seen_keys(p0 + row, kl, a.window, a.sinks), {sign, c}, isfinite(sum));
         }
         tc::cluster_sync_all();  // no CTA leaves while another reads its part
     } else {
@@ -364,7 +364,7 @@ __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float 
                 if (!((again >> (4 * x)) & 0xfu)) continue;
                 const int rr = 16 * warp + x + 8 * r;
                 mend_row<float, D>(q + rr * a.qs.t, k, v, a.ks.t, a.vs.t, o + rr * a.os.t,
-                                   seen_keys(p0 + rr, kl, a.window, a.sinks), a.scale,
+                                   seen_keys(p0 + rr, kl, a.window, a.sinks), {sign, c},
                                    isfinite(__shfl_sync(0xffffffffu, sum, 4 * x)));
             }
         }
@@ -413,7 +413,7 @@ cudaError_t launch(const WindowArgs &a, int slot, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     // scale 0 gives every key the same weight; a product with it would turn
     // the mask's -inf into NaN, and 2^-100 rounds to the same weights
-    const float c = a.scale == 0.f ? 7.9e-31f : fabsf(a.scale) * 1.4426950408889634f;
+    const float c = a.scale == 0.f ? 7.9e-31f : score_factor(a.scale).c;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(ctas * splits));
     cfg.blockDim = dim3(G * GT);

@@ -22,6 +22,14 @@
 // weights no precision); only then O in TMEM is rescaled, by the softmax warp itself: the commit that
 // announced the scores also covers the tile's earlier products.
 //
+// A weight is one fma and one exponential, 2^(c s - b) with b = c m rounded.
+// What was summed before is rescaled by the difference of the rounded b, so
+// all weights of a row refer to the same b exactly.  b is off from c m by up to
+// half a step, 2^5 where |c m| < 2^30, and the row's largest weight by as many
+// powers of two: a sum below 2^-40, or one that is not finite, tells of larger
+// ones, and such rows are computed again (attn_rows.cuh).  Differences first
+// would take a second instruction for every score.
+//
 // Key tiles: the sinks' (before the window of every row), then the window's
 // from the first key that any row sees.  A tile that all rows of a query tile
 // see entirely skips the mask; one that none sees is skipped; a short one
@@ -345,13 +353,14 @@ __device__ __forceinline__ void join_parts(const TcArgs &g, const Item &x, uint3
         __nv_bfloat16 *to = static_cast<__nv_bfloat16 *>(a.o) + x.b * a.os.b + x.head[t] * a.os.h +
                             (long long)(x.i0[t] + row) * a.os.t;
         float sum;
-        if (join_row<__nv_bfloat16, D>(part, stats, r, g.splits, g.c, to, sum)) continue;
+        // the parts' maxima come in powers of two
+        if (join_row<__nv_bfloat16, D>(part, stats, r, g.splits, 1.f, to, sum)) continue;
         mend_row<__nv_bfloat16, D>(
             static_cast<const __nv_bfloat16 *>(a.q) + x.b * a.qs.b + x.head[t] * a.qs.h +
                 (long long)(x.i0[t] + row) * a.qs.t,
             static_cast<const __nv_bfloat16 *>(a.k) + x.b * a.ks.b + x.hk * a.ks.h,
             static_cast<const __nv_bfloat16 *>(a.v) + x.b * a.vs.b + x.hk * a.vs.h, a.ks.t, a.vs.t, to,
-            seen_keys(x.p0[t] + row, x.kl, a.window, a.sinks), a.scale, isfinite(sum));
+            seen_keys(x.p0[t] + row, x.kl, a.window, a.sinks), score_factor(a.scale), isfinite(sum));
     }
 }
 
@@ -645,7 +654,10 @@ __global__ void __launch_bounds__(NT, 1)
                     const bool grow = mn > m && (m == -INFINITY || (mn - m) * g.c > 8.f);
                     // a row that has seen nothing yet has l = 0 and zeros in O (or O unset)
                     if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
-                        const float f = grow && m != -INFINITY ? ex2((m - mn) * g.c) : 1.f;
+                        // no fma here: both products as `base` has them
+                        const float f = grow && m != -INFINITY
+                                            ? ex2(__fsub_rn(__fmul_rn(m, g.c), __fmul_rn(mn, g.c)))
+                                            : 1.f;
                         l *= f;
 #pragma unroll 1
                         for (int ch = 0; ch < D / 16; ++ch) {
@@ -659,7 +671,7 @@ __global__ void __launch_bounds__(NT, 1)
                         }
                     }
                     if (grow) m = mn;
-                    return m == -INFINITY ? 0.f : -m * g.c;
+                    return m == -INFINITY ? 0.f : -__fmul_rn(m, g.c);
                 };
                 float2 sum[4];
 #pragma unroll
@@ -731,12 +743,14 @@ __global__ void __launch_bounds__(NT, 1)
                 l += two.x + two.y;
                 ++seen;
             }
+            // the rounding of the exponent's base took the weights' range
+            if (m != -INFINITY && !(l >= 0x1p-40f)) l = NAN;
             if (SPLIT) {
                 // the part, once the products of both query tiles have read their operands
                 for (int u = 0; u < 2; ++u)
                     if (x.last[u] >= 0 && ok) ok = __all_sync(0xffffffffu, wait_bar(&bars->ofull[u], 0));
                 tc_fence_after();
-                *reinterpret_cast<float2 *>(sm + L::OUT + (t * BM + row) * 8) = make_float2(m, l);
+                *reinterpret_cast<float2 *>(sm + L::OUT + (t * BM + row) * 8) = make_float2(__fmul_rn(m, g.c), l);
                 if (n > 0 && ok) {
 #pragma unroll 1
                     for (int ch = 0; ch < D / 32; ++ch) {
@@ -817,7 +831,7 @@ __global__ void __launch_bounds__(NT, 1)
                     const int src = __ffs(again) - 1, rr = w0 + src;
                     again &= again - 1;
                     mend_row<__nv_bfloat16, D>(q + rr * a.qs.t, k, v, a.ks.t, a.vs.t, ot + rr * a.os.t,
-                                               seen_keys(x.p0[t] + rr, x.kl, a.window, a.sinks), a.scale,
+                                               seen_keys(x.p0[t] + rr, x.kl, a.window, a.sinks), score_factor(a.scale),
                                                isfinite(__shfl_sync(0xffffffffu, l, src)));
                 }
             }
@@ -879,7 +893,7 @@ cudaError_t launch(const WindowArgs &a, int slot, cudaStream_t stream) {
     g.w = a;
     // scale 0 gives every key the same weight; a product with it would turn
     // the mask's -inf into NaN, and 2^-100 rounds to the same weights
-    g.c = a.scale == 0.f ? 7.9e-31f : fabsf(a.scale) * 1.4426950408889634f;
+    g.c = a.scale == 0.f ? 7.9e-31f : score_factor(a.scale).c;
     g.negate = a.scale < 0.f ? 1u << 13 : 0u;
     g.group = a.Hq / a.Hk;
     g.pair_heads = g.group % 2 == 0;

@@ -886,3 +886,54 @@ def test_operators_on_another_stream_and_repeated(dev):
         got = all_three()
     side.synchronize()
     assert all(torch.equal(x, y) for x, y in zip(got, want))
+
+
+def _scores_of_one_channel(scores, heads, rows, d, dtype, dev):
+    """q, k [1,heads,..,d] whose products are exactly `scores` (two bf16 parts
+    a key) for every row."""
+    q = torch.zeros(1, heads, rows, d, dtype=dtype)
+    q[..., :2] = 1
+    k = torch.zeros(1, heads, len(scores[0]), d, dtype=dtype)
+    k[..., 0], k[..., 1] = (torch.tensor(s, dtype=torch.float64).to(dtype) for s in scores)
+    return q.to(dev), k.to(dev)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("H", [1, 160], ids=["cluster", "alone"])
+@pytest.mark.parametrize("scale", [1.0, 2.5, -1.0])
+@pytest.mark.parametrize("top", [2.0 ** 33, 2.0 ** 40, 2.0 ** 66, 2.0 ** 126, None], ids=lambda t: f"{t or 'max'}")
+def test_window_large_finite_scores(dev, top, scale, H, dtype):
+    """Scores from 1e10 to the type's largest: those alike share the weight,
+    and one that is a 64th part above them takes all of it."""
+    d, Tq, Tk, at = 32, 30, 700, 685
+    top = torch.finfo(dtype).max if top is None else top
+    key = np.full(Tk, top * (1 - 2.0 ** -6))
+    key[at] = top
+    q, k = _scores_of_one_channel((key * np.sign(scale), np.zeros(Tk)), H, Tq, d, dtype, dev)
+    v = rnd(120, 1, 1, Tk, d, dtype=dtype)
+    o = lr.lr_fwd_window(q, k, v.expand(1, H, Tk, d).contiguous().to(dev), scale=scale)
+    ref, size, reach, _ = oa.window(np64(q[:, :1]), np64(k[:, :1]), np64(v), NW, 0, scale)
+    # products with 0 and 1 are exact, so the scores are: reach 0
+    bound = oa.attention_bound(ref, size, np.zeros_like(reach), Tk, d, BITS[dtype], 8 if dtype == BF16 else None)
+    within(o, np.broadcast_to(ref, o.shape), np.broadcast_to(bound, o.shape))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("H", [1, 160], ids=["cluster", "alone"])
+@pytest.mark.parametrize("base", [1.8125, 1.46875, -1.8125])
+def test_window_weights_of_tiles_agree_at_large_scores(dev, base, H, dtype):
+    """512 keys and, in a later tile, one that is 7 above them: the weights of
+    both tiles refer to the same maximum, however large the scores are.  These
+    are exact in fp32 (2^21 and small integers), and what the exponential takes
+    is below 32, so its roundings are those of scores of that size."""
+    d, Tq, Tk, at = 32, 30, 700, 660
+    big, small = np.full(Tk, base * 2.0 ** 21), np.zeros(Tk)
+    small[512:] = -100.0
+    small[at] = 7.0
+    q, k = _scores_of_one_channel((big, small), H, Tq, d, dtype, dev)
+    v = torch.ones(1, H, Tk, d, dtype=dtype)
+    v[:, :, at] = -1
+    o = lr.lr_fwd_window(q, k, v.to(dev), scale=1.0)
+    ref, size, reach, _ = oa.window(np64(q[:, :1]), np64(k[:, :1]), np64(v[:, :1]), NW, 0, 1.0)
+    bound = oa.attention_bound(ref, size, np.full_like(reach, 32.0), Tk, d, BITS[dtype], 8 if dtype == BF16 else None)
+    within(o, np.broadcast_to(ref, o.shape), np.broadcast_to(bound, o.shape))
