@@ -1,9 +1,11 @@
 // Rows whose result is not finite, put right by a warp.
 //
 // The tiled kernels multiply whole tiles, where a weight of zero times a NaN
-// or an infinity in a masked row of v reaches rows that do not see it.  Such
-// rows come out not finite, and only then is this called (finite inputs of
-// ordinary size never are).  What is right for them:
+// or an infinity in a masked row of v reaches rows that do not see it.  In all
+// kernels a weight that underflows meets an infinity of v as 0 x inf, and the
+// unnormalised sum of weights and values may overflow where their mean does
+// not.  Such rows come out not finite, and only then is this called (finite
+// inputs of ordinary size never are).  What is right for them:
 //
 //   - a sum of weights that is not finite: where a score that the row sees is
 //     NaN or +inf every channel is NaN.  Operands at the type's ends make the
@@ -32,12 +34,12 @@ __device__ __forceinline__ float warp_sum(float x) {
     return x;
 }
 
-// q: the row's d channels; k, v: row 0 of its key head, rows `kt` and `vt`
-// elements apart; o: the row as the kernel left it.  Every lane of the warp
+// q: the row's d channels; keys(j, kj, vj): whether key j can be read, and its
+// rows of k and v; o: the row as the kernel left it.  Every lane of the warp
 // calls this with the same arguments.
-template <typename E, int D>
-__device__ __forceinline__ void mend_row(const E *q, const E *k, const E *v, long long kt, long long vt,
-                                         E *o, SeenKeys s, ScoreFactor f, bool sum_finite) {
+template <typename E, int D, typename Keys>
+__device__ __forceinline__ void mend_row_of(const E *q, const Keys &keys, E *o, SeenKeys s, ScoreFactor f,
+                                            bool sum_finite) {
     constexpr int PL = D / 32;  // channels of a lane: lane + 32 i
     const int lane = threadIdx.x & 31;
     bool whole_row = false;
@@ -48,10 +50,11 @@ __device__ __forceinline__ void mend_row(const E *q, const E *k, const E *v, lon
             if (j0 < s.lo && j0 >= s.s1) j0 = s.s1 - 1;
             const int j = j0 - lane;
             float x = 0.f;
-            if (j >= 0 && (j >= s.lo || j < s.s1)) {
+            const E *kj, *vj;
+            if (j >= 0 && (j >= s.lo || j < s.s1) && keys(j, kj, vj)) {
 #pragma unroll 4
                 for (int c = 0; c < D; c += 4) {
-                    const float4 a = load4(q + c), b = load4(k + j * kt + c);
+                    const float4 a = load4(q + c), b = load4(kj + c);
                     x += a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
                 }
             }
@@ -77,10 +80,12 @@ __device__ __forceinline__ void mend_row(const E *q, const E *k, const E *v, lon
             j = s.s1;
             continue;
         }
+        const E *kj, *vj;
+        if (!keys(j, kj, vj)) continue;
         bool open = false;  // a channel that more keys could still change
 #pragma unroll
         for (int i = 0; i < PL; ++i) {
-            const float x = to_f<E>(v[j * vt + lane + 32 * i]);
+            const float x = to_f<E>(vj[lane + 32 * i]);
             if (!isfinite(x)) found[i] |= x > 0.f ? 1u : (x < 0.f ? 2u : 4u);
             open = open || (odd[i] && found[i] < 3u);
         }
@@ -101,9 +106,11 @@ __device__ __forceinline__ void mend_row(const E *q, const E *k, const E *v, lon
         for (int j = 0; j < s.hi; ++j) {
             if (j == s.s1 && j < s.lo) j = s.lo;
             if (j >= s.hi) break;
+            const E *kj, *vj;
+            if (!keys(j, kj, vj)) continue;
             float x = 0.f;
 #pragma unroll
-            for (int i = 0; i < PL; ++i) x += qr[i] * to_f<E>(k[j * kt + lane + 32 * i]);
+            for (int i = 0; i < PL; ++i) x += qr[i] * to_f<E>(kj[lane + 32 * i]);
             x = warp_sum(x);
             if (x == -INFINITY) continue;  // weight zero
             // a running mean, which no large value can drive out of range
@@ -112,7 +119,7 @@ __device__ __forceinline__ void mend_row(const E *q, const E *k, const E *v, lon
             l = old + p;
             const float keep = old / l, take = p / l;
 #pragma unroll
-            for (int i = 0; i < PL; ++i) acc[i] = acc[i] * keep + take * to_f<E>(v[j * vt + lane + 32 * i]);
+            for (int i = 0; i < PL; ++i) acc[i] = acc[i] * keep + take * to_f<E>(vj[lane + 32 * i]);
         }
     }
 #pragma unroll
@@ -121,6 +128,19 @@ __device__ __forceinline__ void mend_row(const E *q, const E *k, const E *v, lon
         if (odd[i] && found[i]) o[lane + 32 * i] = from_f<E>(inf);
         else if (odd[i]) o[lane + 32 * i] = from_f<E>(acc[i]);
     }
+}
+
+// The same with the key head's rows `kt` and `vt` elements apart.
+template <typename E, int D>
+__device__ __forceinline__ void mend_row(const E *q, const E *k, const E *v, long long kt, long long vt,
+                                         E *o, SeenKeys s, ScoreFactor f, bool sum_finite) {
+    mend_row_of<E, D>(
+        q,
+        [&](int j, const E *&kj, const E *&vj) {
+            kj = k + j * kt, vj = v + j * vt;
+            return true;
+        },
+        o, s, f, sum_finite);
 }
 
 }  // namespace lr

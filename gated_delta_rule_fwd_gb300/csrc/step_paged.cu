@@ -17,13 +17,18 @@
 // shared memory and no barrier stand between a load and its product, and the
 // next keys are on their way while the values of the last ones are used.
 //
-// Measured: 128 sequences of 500 to 8192 tokens, 32 heads on 8, 356 us (94 % of
-// the copy bandwidth); two caches of 131K 87 us (91 %).
+// Measured: 128 sequences of 500 to 8192 tokens, 32 heads on 8, 351 us (95 % of
+// the copy bandwidth); two caches of 131K 82 us (96 %).
 //
 // fp32 (step_simt_kernel): CUDA cores.  Every group of d / 8 lanes takes keys
 // of its own, with a running maximum and sum of its own (33 sequences with
-// window 1024, 139 MB: 25.7 us).
+// window 1024, 139 MB: 24.2 us).
+//
+// Rows that come out not finite are explained or computed again from the keys
+// they see (attn_rows.cuh), as in the window form; one vote of the CTA that
+// writes a row finds them.
 #include "attn_internal.cuh"
+#include "attn_rows.cuh"
 #include "tc_common.cuh"
 
 namespace lr {
@@ -48,16 +53,44 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     return r;
 }
 
+// Output row `head` of sequence n by one warp, put right where it is not
+// finite.  sum(): of its weights.  Keys of pages outside the pool are left out.
+template <typename E, int D, typename Sum>
+__device__ __forceinline__ void mend_step_row(const StepArgs &a, int n, int head, ScoreFactor f, Sum sum) {
+    const int lane = threadIdx.x & 31, hk = head / (a.Hq / a.Hk), len = a.lens[n];
+    const size_t at = ((size_t)n * a.Hq + head) * D;
+    E *o = static_cast<E *>(a.o) + at;
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) odd = odd || !isfinite(to_f<E>(o[lane + 32 * i]));
+    if (!__any_sync(0xffffffffu, odd)) return;
+    const int *table = a.table + (size_t)n * a.max_pages;
+    mend_row_of<E, D>(
+        static_cast<const E *>(a.q) + at,
+        [&](int j, const E *&kj, const E *&vj) {
+            const int page = table[j >> a.page_log2];
+            if (page < 0 || page >= a.num_pages) return false;
+            const long long row = (((long long)page * a.Hk + hk) << a.page_log2) + (j & ((1 << a.page_log2) - 1));
+            kj = static_cast<const E *>(a.k) + row * D, vj = static_cast<const E *>(a.v) + row * D;
+            return true;
+        },
+        o, seen_keys(len - 1, len, a.window, a.sinks), f, isfinite(sum()));
+}
+
 // The end of a CTA: joins its warps' parts and hands the result on.  so: the
-// warps' unnormalised outputs, P floats a head; sml: their (maximum, sum); c:
-// the scores' factor to powers of two; row0: output row of head 0.  A part
-// without a key has a maximum of -inf and weighs nothing; one whose scores
-// were all NaN too, but its sum of NaN stays.
+// warps' unnormalised outputs, P floats a head; sml: their (maximum, sum); f:
+// the scores' factor; n, h0: sequence and first head.  A part without a key has
+// a maximum of -inf and weighs nothing; one whose scores were all NaN too, but
+// its sum of NaN stays.
 template <typename E, int D, int HEADS, int P>
 __device__ __forceinline__ void finish(float (&so)[NT / 32][HEADS][P], float (&sml)[NT / 32][HEADS][2],
-                                       int heads, size_t row0, int split, float c, E *out,
+                                       int heads, int n, int h0, int split, ScoreFactor f, const StepArgs &a,
                                        const Parts &parts) {
     const int tid = threadIdx.x;
+    const size_t row0 = (size_t)n * a.Hq + h0;
+    const float c = f.c;
+    E *out = static_cast<E *>(a.o);
+    bool odd = false;  // a value that is not finite
     __syncthreads();
     for (int i = tid; i < heads * D; i += NT) {
         const int h = i / D, ch = i - h * D;
@@ -67,13 +100,15 @@ __device__ __forceinline__ void finish(float (&so)[NT / 32][HEADS][P], float (&s
         float sum = 0.f, x = 0.f;
 #pragma unroll
         for (int w = 0; w < NT / 32; ++w) {
-            const float mw = sml[w][h][0], f = mw == -INFINITY ? 0.f : ex2((mw - mn) * c);
-            sum += f * sml[w][h][1];
-            x += f * so[w][h][ch];
+            const float mw = sml[w][h][0], fw = mw == -INFINITY ? 0.f : ex2((mw - mn) * c);
+            sum += fw * sml[w][h][1];
+            x += fw * so[w][h][ch];
         }
         const size_t r = row0 + h;
         if (parts.splits == 1) {
-            out[r * D + ch] = from_f<E>(sum == 0.f ? 0.f : x / sum);
+            const float y = sum == 0.f ? 0.f : x / sum;
+            out[r * D + ch] = from_f<E>(y);
+            odd = odd || !isfinite(y);
         } else if (parts.cluster) {
             so[0][h][ch] = x;  // read and written by this thread alone
         } else {
@@ -81,15 +116,30 @@ __device__ __forceinline__ void finish(float (&so)[NT / 32][HEADS][P], float (&s
             if (ch == 0) parts.ml[r * parts.splits + split] = make_float2(mn, sum);
         }
     }
-    if (!parts.cluster) return;
-    __syncthreads();
-    if (tid < heads) {
-        float mn = -INFINITY, sum = 0.f;
+    // the warps' parts of a head as one
+    auto whole = [&](int h, float &mn) {
+        float sum = 0.f;
+        mn = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < NT / 32; ++w) mn = fmaxf(mn, sml[w][tid][0]);
+        for (int w = 0; w < NT / 32; ++w) mn = fmaxf(mn, sml[w][h][0]);
 #pragma unroll
         for (int w = 0; w < NT / 32; ++w)
-            sum += sml[w][tid][1] * (sml[w][tid][0] == -INFINITY ? 0.f : ex2((sml[w][tid][0] - mn) * c));
+            sum += sml[w][h][1] * (sml[w][h][0] == -INFINITY ? 0.f : ex2((sml[w][h][0] - mn) * c));
+        return sum;
+    };
+    if (!parts.cluster) {
+        if (parts.splits == 1 && __syncthreads_or(odd))
+            for (int h = tid >> 5; h < heads; h += NT / 32)
+                mend_step_row<E, D>(a, n, h0 + h, f, [&] {
+                    float mn;
+                    return whole(h, mn);
+                });
+        return;
+    }
+    __syncthreads();
+    if (tid < heads) {
+        float mn;
+        const float sum = whole(tid, mn);
         sml[0][tid][0] = mn, sml[0][tid][1] = sum;
     }
     tc::cluster_sync_all();
@@ -105,13 +155,21 @@ __device__ __forceinline__ void finish(float (&so)[NT / 32][HEADS][P], float (&s
 #pragma unroll
         for (int r = 0; r < kMostCluster; ++r)
             if (r < parts.splits) {
-                const float f = m[r] == -INFINITY ? 0.f : ex2((m[r] - mn) * c);
-                sum += f * ld_cluster(tc::map_to_rank(ml_at + 8 * h + 4, r));
-                x += f * ld_cluster(tc::map_to_rank(o_at + 4 * (h * P + ch), r));
+                const float fr = m[r] == -INFINITY ? 0.f : ex2((m[r] - mn) * c);
+                sum += fr * ld_cluster(tc::map_to_rank(ml_at + 8 * h + 4, r));
+                x += fr * ld_cluster(tc::map_to_rank(o_at + 4 * (h * P + ch), r));
             }
-        out[(row0 + h) * D + ch] = from_f<E>(sum == 0.f ? 0.f : x / sum);
+        const float y = sum == 0.f ? 0.f : x / sum;
+        out[(row0 + h) * D + ch] = from_f<E>(y);
+        odd = odd || !isfinite(y);
+        if (ch == 0) sml[1][h][1] = sum;  // only the first pair is read by other CTAs
     }
+    const int again = __syncthreads_or(odd);
     tc::cluster_sync_all();  // no CTA leaves while another reads its part
+    if (again)
+        for (int h = tid >> 5; h < heads; h += NT / 32)
+            if (h * D / NT % parts.splits == split)  // a row that was written here
+                mend_step_row<E, D>(a, n, h0 + h, f, [&] { return sml[1][h][1]; });
 }
 
 __device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
@@ -119,13 +177,9 @@ __device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
                  b = __ldg(reinterpret_cast<const float4 *>(p + 4));
     x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
-// exp(m - base) with an empty part's maximum of -inf
-__device__ __forceinline__ float part_weight(float m, float base) {
-    return m == -INFINITY ? 0.f : __expf(m - base);
-}
 
 template <int D, int GC>
-__global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts) {
+__global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts, ScoreFactor f) {
     constexpr int LANES = D / 8;            // lanes of a key
     constexpr int GROUPS = NT / LANES;      // keys in flight
     constexpr int U = 4;                    // keys of a group per pass
@@ -159,7 +213,7 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts) 
     for (int g = 0; g < GC; ++g) {
         load8(qn + (size_t)(h0 + min(g, heads - 1)) * D + ch, q[g]);
 #pragma unroll
-        for (int i = 0; i < 8; ++i) q[g][i] *= a.scale, acc[g][i] = 0.f;
+        for (int i = 0; i < 8; ++i) q[g][i] *= f.sign, acc[g][i] = 0.f;
         m[g] = -INFINITY, l[g] = 0.f;
     }
     const int *table = a.table + (size_t)n * a.max_pages;
@@ -209,14 +263,14 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts) 
 #pragma unroll
             for (int u = 0; u < U; ++u) mn = fmaxf(mn, sc[u][g]);
             const float b = mn == -INFINITY ? 0.f : mn;
-            const float c = __expf(m[g] - b);
+            const float c = ex2((m[g] - b) * f.c);
             m[g] = mn;
             l[g] *= c;
 #pragma unroll
             for (int i = 0; i < 8; ++i) acc[g][i] *= c;
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                const float p = __expf(sc[u][g] - b);
+                const float p = ex2((sc[u][g] - b) * f.c);
                 l[g] += p;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) acc[g][i] += p * y[u][i];
@@ -231,7 +285,7 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts) 
         float mn = m[g];
 #pragma unroll
         for (int w = LANES; w < 32; w <<= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, w));
-        const float c = part_weight(m[g], mn);
+        const float c = m[g] == -INFINITY ? 0.f : ex2((m[g] - mn) * f.c);
         l[g] *= c;
 #pragma unroll
         for (int i = 0; i < 8; ++i) acc[g][i] *= c;
@@ -247,8 +301,7 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts) 
             if (lane == 0) sml[warp][g][0] = mn, sml[warp][g][1] = l[g];
         }
     }
-    finish<float, D, GC, D>(so, sml, heads, (size_t)n * a.Hq + h0, split, 1.4426950408889634f,
-                            static_cast<float *>(a.o), parts);
+    finish<float, D, GC, D>(so, sml, heads, n, h0, split, f, a, parts);
 }
 
 // ------------------------------------------------------------------- bf16
@@ -288,11 +341,12 @@ __device__ __forceinline__ uint2 load_once8(const void *p) {
     return r;
 }
 
-// NH: 8-head column blocks of the products.  c = |scale| log2 e; flip: sign
-// bits of a bf16 pair where scale is negative.
+// NH: 8-head column blocks of the products.
 template <int D, int NH>
 __global__ void __launch_bounds__(NT)
-    step_mma_kernel(StepArgs a, Parts parts, float c, uint32_t flip) {
+    step_mma_kernel(StepArgs a, Parts parts, ScoreFactor f) {
+    const float c = f.c;
+    const uint32_t flip = f.sign < 0.f ? 0x80008000u : 0u;  // sign bits of a pair
     constexpr int KC = D / 32;   // 32-channel pieces of a key: 16 bytes per lane and row
     constexpr int VW = D / 16;   // words of a value row per lane = 16-channel blocks of O^T
     constexpr int HEADS = 8 * NH;
@@ -447,12 +501,12 @@ __global__ void __launch_bounds__(NT)
 #pragma unroll
                     for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
                     const float mn = fmaxf(m[nh][e], mx);
-                    const float f = m[nh][e] == -INFINITY ? 0.f : ex2((m[nh][e] - mn) * c);
+                    const float less = m[nh][e] == -INFINITY ? 0.f : ex2((m[nh][e] - mn) * c);
                     m[nh][e] = mn;
                     // nothing seen yet: sums and output are zero (or NaN, which stays)
-                    l[nh][e] *= f;
+                    l[nh][e] *= less;
 #pragma unroll
-                    for (int j = 0; j < VW; ++j) acc[j][nh][e] *= f, acc[j][nh][e + 2] *= f;
+                    for (int j = 0; j < VW; ++j) acc[j][nh][e] *= less, acc[j][nh][e + 2] *= less;
                 }
         }
         uint32_t p[NH][2];
@@ -492,14 +546,13 @@ __global__ void __launch_bounds__(NT)
                 *reinterpret_cast<float2 *>(&so[warp][h][col]) = make_float2(acc[j][nh][e], acc[j][nh][e + 2]);
             }
         }
-    finish<__nv_bfloat16, D, HEADS, D + 8>(so, sml, heads, (size_t)n * a.Hq + h0, split, c,
-                                           static_cast<__nv_bfloat16 *>(a.o), parts);
+    finish<__nv_bfloat16, D, HEADS, D + 8>(so, sml, heads, n, h0, split, f, a, parts);
 }
 
-// One CTA of D threads per output row: the chunks' parts in order.  c: the
-// scores' factor to powers of two.
+// One CTA of D threads per output row: the chunks' parts in order.
 template <typename E, int D>
-__global__ void __launch_bounds__(D) step_join_kernel(StepArgs a, Parts parts, float c) {
+__global__ void __launch_bounds__(D) step_join_kernel(StepArgs a, Parts parts, ScoreFactor factor) {
+    const float c = factor.c;
     const int r = blockIdx.x, n = r / a.Hq, ch = threadIdx.x;
     const int len = a.lens[n];
     if (len < 0 || len > a.max_len) return;
@@ -536,7 +589,10 @@ __global__ void __launch_bounds__(D) step_join_kernel(StepArgs a, Parts parts, f
         }
         m = mn;
     }
-    static_cast<E *>(a.o)[(size_t)r * D + ch] = from_f<E>(l == 0.f ? 0.f : x / l);
+    const float out = l == 0.f ? 0.f : x / l;
+    static_cast<E *>(a.o)[(size_t)r * D + ch] = from_f<E>(out);
+    if (__syncthreads_or(!isfinite(out)) && ch < 32)
+        mend_step_row<E, D>(a, n, r - n * a.Hq, factor, [&] { return l; });
 }
 
 Parts parts_of(const StepArgs &a, int d, const StepPlan &p, void *ws) {
@@ -556,9 +612,8 @@ int heads_of_cta(int G, lr_dtype dt) {
 }
 
 // Launches a step kernel, its chunks as clusters where the plan says so.
-template <typename... A>
-cudaError_t launch_parts(void (*fn)(StepArgs, Parts, A...), unsigned grid, cudaStream_t stream,
-                         const StepArgs &a, const Parts &parts, A... rest) {
+cudaError_t launch_parts(void (*fn)(StepArgs, Parts, ScoreFactor), unsigned grid, cudaStream_t stream,
+                         const StepArgs &a, const Parts &parts, ScoreFactor f) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3(NT);
@@ -571,13 +626,15 @@ cudaError_t launch_parts(void (*fn)(StepArgs, Parts, A...), unsigned grid, cudaS
         cfg.attrs = at;
         cfg.numAttrs = 1;
     }
-    return cudaLaunchKernelEx(&cfg, fn, a, parts, rest...);
+    return cudaLaunchKernelEx(&cfg, fn, a, parts, f);
 }
 
-// |scale| log2 e.  Scale 0 gives every key the same weight; a product with it
-// would turn -inf into NaN, and 2^-100 rounds to the same weights.
-float exp2_scale(float scale) {
-    return scale == 0.f ? 7.9e-31f : fabsf(scale) * 1.4426950408889634f;
+// The factor of fp32 and bf16 scores.  Scale 0 gives every key the same weight;
+// a product with it would turn -inf into NaN, and 2^-100 rounds to the same
+// weights.
+ScoreFactor factor_of(float scale) {
+    if (scale == 0.f) return {1.f, 7.9e-31f};
+    return score_factor(scale);
 }
 
 template <int D>
@@ -585,19 +642,19 @@ cudaError_t launch_f32(const StepArgs &a, const Parts &parts, cudaStream_t strea
     const int G = a.Hq / a.Hk;
     const int gc = heads_of_cta(G, LR_DT_F32);
     const unsigned grid = (unsigned)(a.N * a.Hk * ((G + gc - 1) / gc) * parts.splits);
-    if (gc == 1) return launch_parts(&step_simt_kernel<D, 1>, grid, stream, a, parts);
-    if (gc == 2) return launch_parts(&step_simt_kernel<D, 2>, grid, stream, a, parts);
-    return launch_parts(&step_simt_kernel<D, 4>, grid, stream, a, parts);
+    const ScoreFactor f = factor_of(a.scale);
+    if (gc == 1) return launch_parts(&step_simt_kernel<D, 1>, grid, stream, a, parts, f);
+    if (gc == 2) return launch_parts(&step_simt_kernel<D, 2>, grid, stream, a, parts, f);
+    return launch_parts(&step_simt_kernel<D, 4>, grid, stream, a, parts, f);
 }
 
 template <int D>
 cudaError_t launch_bf16(const StepArgs &a, const Parts &parts, cudaStream_t stream) {
     const int G = a.Hq / a.Hk, heads = heads_of_cta(G, LR_DT_BF16);
     const unsigned grid = (unsigned)(a.N * a.Hk * ((G + heads - 1) / heads) * parts.splits);
-    const float c = exp2_scale(a.scale);
-    const uint32_t flip = a.scale < 0.f ? 0x80008000u : 0u;
-    if (heads == 8) return launch_parts(&step_mma_kernel<D, 1>, grid, stream, a, parts, c, flip);
-    return launch_parts(&step_mma_kernel<D, 2>, grid, stream, a, parts, c, flip);
+    const ScoreFactor f = factor_of(a.scale);
+    if (heads == 8) return launch_parts(&step_mma_kernel<D, 1>, grid, stream, a, parts, f);
+    return launch_parts(&step_mma_kernel<D, 2>, grid, stream, a, parts, f);
 }
 
 template <int D>
@@ -607,8 +664,9 @@ cudaError_t launch(const StepArgs &a, void *ws, lr_dtype dt, cudaStream_t stream
     const cudaError_t e = dt == LR_DT_F32 ? launch_f32<D>(a, parts, stream) : launch_bf16<D>(a, parts, stream);
     if (e != cudaSuccess || p.splits == 1 || p.cluster) return e;
     const unsigned rows = (unsigned)(a.N * a.Hq);
-    if (dt == LR_DT_F32) step_join_kernel<float, D><<<rows, D, 0, stream>>>(a, parts, 1.4426950408889634f);
-    else step_join_kernel<__nv_bfloat16, D><<<rows, D, 0, stream>>>(a, parts, exp2_scale(a.scale));
+    const ScoreFactor f = factor_of(a.scale);
+    if (dt == LR_DT_F32) step_join_kernel<float, D><<<rows, D, 0, stream>>>(a, parts, f);
+    else step_join_kernel<__nv_bfloat16, D><<<rows, D, 0, stream>>>(a, parts, f);
     return cudaGetLastError();
 }
 

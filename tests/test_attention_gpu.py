@@ -937,3 +937,73 @@ def test_window_weights_of_tiles_agree_at_large_scores(dev, base, H, dtype):
     ref, size, reach, _ = oa.window(np64(q[:, :1]), np64(k[:, :1]), np64(v[:, :1]), NW, 0, 1.0)
     bound = oa.attention_bound(ref, size, np.full_like(reach, 32.0), Tk, d, BITS[dtype], 8 if dtype == BF16 else None)
     within(o, np.broadcast_to(ref, o.shape), np.broadcast_to(bound, o.shape))
+
+
+STEP_CUTS = [64, 700, 40000]   # bounds on the length: one chunk, a cluster's few, many joined by a kernel
+
+
+def _wide(table, max_len, page, dev):
+    """The table with room for max_len tokens (page 0 where the sequences end)."""
+    wide = torch.zeros(table.shape[0], -(-max_len // page), dtype=torch.int32, device=dev)
+    most = min(wide.shape[1], table.shape[1])
+    wide[:, :most] = table[:, :most]
+    return wide
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("d,Hq,Hk", [(32, 2, 1), (64, 17, 1), (128, 6, 2)])
+@pytest.mark.parametrize("max_len", STEP_CUTS)
+def test_step_values_that_are_not_finite_or_overflow_a_sum(dev, max_len, d, Hq, Hk, dtype):
+    """The step's row is the window's: a channel with a seen infinity is that
+    infinity (of a key whose weight underflows, too), with both signs or a NaN
+    it is NaN, any other is as without them; values near the type's end average
+    without overflow; a page outside the pool is left out of all this."""
+    page, inf, lens = 16, float("inf"), [50, 61, 64, 33, 40]
+    kc, vc, table = paged(130, lens, Hk, page, d, dtype, dev)
+    q = rnd(131, len(lens), Hq, d, dtype=dtype)
+    place = lambda n, j: (int(table[n, j // page]), slice(None), j % page)
+    q[0] = 1
+    kc[place(0, 9)] = -1e4                     # score -1e4 sqrt(d): no weight
+    for n, j in ((2, j) for j in range(lens[2])):
+        vc[place(n, j)] = torch.finfo(dtype).max / 2
+    ref, size, reach, _ = oa.step(np64(q), np64(kc), np64(vc), table.cpu().numpy(), lens, NW, 0, d ** -0.5)
+    marks = [(0, 9, 3, inf), (0, 9, 5, -inf), (1, 0, 1, inf), (1, 60, 1, -inf), (1, 17, 2, float("nan")),
+             (1, 31, 4, -inf), (1, 32, 4, -inf), (4, 3, 0, inf)]
+    want, bound = ref.copy(), oa.attention_bound(ref, size, reach, 64, d, BITS[dtype], 8 if dtype == BF16 else None)
+    # sequence 4: its second page is outside the pool
+    left = [j for j in range(lens[4]) if j // page != 1]
+    rows = (table[4].cpu().numpy()[np.array(left) // page], slice(None), np.array(left) % page)
+    for h in range(Hq):
+        a, s, r = oa.row(np64(q)[4, h], np64(kc)[rows][:, h // (Hq // Hk)], np64(vc)[rows][:, h // (Hq // Hk)], d ** -0.5)
+        want[4, h], bound[4, h] = a, oa.attention_bound(a, s, np.array(r), 64, d, BITS[dtype], 8 if dtype == BF16 else None)
+    for n, j, ch, x in marks:
+        vc[place(n, j)][:, ch] = x
+    wide = _wide(table, max_len, page, dev)
+    wide[4, 1] = kc.shape[0]
+    need = lr.step_paged_workspace_size(len(lens), Hq, Hk, d, max_len, dtype)
+    assert (need > 0) == (max_len == STEP_CUTS[2])
+    o = lr.lr_step_paged(q.to(dev), kc, vc, wide, torch.tensor(lens, dtype=torch.int32, device=dev), max_len=max_len)
+    assert lr.device_status() == LR_ERR_INDEX
+    got = np64(o)
+    for n, ch, x in ((0, 3, inf), (0, 5, -inf), (1, 1, np.nan), (1, 2, np.nan), (1, 4, -inf), (4, 0, inf)):
+        assert np.array_equal(got[n, :, ch], np.full(Hq, x), equal_nan=True), (n, ch, got[n, :, ch])
+        got[n, :, ch] = want[n, :, ch] = 0
+    within(torch.from_numpy(got), want, bound)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("which", ["k", "v"])
+def test_step_batch_full_of_nan_stays_quick(dev, which, dtype):
+    """Every row NaN: found from a few keys, not by a row at a time over all."""
+    import time
+    N, L, page = 64, 4096, 64
+    pools = {n: rnd(132, N * L // page, 2, page, 64, dtype=dtype).to(dev) for n in ("k", "v")}
+    pools[which].fill_(float("nan"))
+    table = torch.arange(N * L // page, dtype=torch.int32, device=dev).view(N, -1)
+    q, lens = rnd(133, N, 8, 64, dtype=dtype).to(dev), torch.full((N,), L, dtype=torch.int32, device=dev)
+    torch.cuda.synchronize()
+    start = time.perf_counter()
+    o = lr.lr_step_paged(q, pools["k"], pools["v"], table, lens)
+    torch.cuda.synchronize()
+    assert time.perf_counter() - start < 1.0
+    assert o.isnan().all()
