@@ -39,7 +39,8 @@ __device__ __forceinline__ int clamp_len(const int *len, int b, int most, bool *
 
 // A score enters as sign * (q . k), formed in fp32 before any scale, and its
 // weight is 2^(c (score - maximum)): no finite scale can push a finite score
-// out of range.
+// out of range.  Scale 0 gives sign 0: scores of zero, so that masked ones can
+// stay -inf (their product with a factor of 0 would be NaN).
 struct ScoreFactor {
     float sign, c;
 };

@@ -346,7 +346,11 @@ template <int D, int NH>
 __global__ void __launch_bounds__(NT)
     step_mma_kernel(StepArgs a, Parts parts, ScoreFactor f) {
     const float c = f.c;
-    const uint32_t flip = f.sign < 0.f ? 0x80008000u : 0u;  // sign bits of a pair
+    const __nv_bfloat162 sign = __float2bfloat162_rn(f.sign);
+    auto with_sign = [&](uint32_t x) {  // exact: 1, -1 or 0 times a pair
+        const __nv_bfloat162 y = __hmul2(reinterpret_cast<const __nv_bfloat162 &>(x), sign);
+        return reinterpret_cast<const uint32_t &>(y);
+    };
     constexpr int KC = D / 32;   // 32-channel pieces of a key: 16 bytes per lane and row
     constexpr int VW = D / 16;   // words of a value row per lane = 16-channel blocks of O^T
     constexpr int HEADS = 8 * NH;
@@ -395,8 +399,8 @@ __global__ void __launch_bounds__(NT)
         for (int i = 0; i < KC; ++i) {
             uint4 x = make_uint4(0, 0, 0, 0);
             if (live) x = *reinterpret_cast<const uint4 *>(p + 32 * i);
-            q[nh][2 * i][0] = x.x ^ flip, q[nh][2 * i][1] = x.y ^ flip;
-            q[nh][2 * i + 1][0] = x.z ^ flip, q[nh][2 * i + 1][1] = x.w ^ flip;
+            q[nh][2 * i][0] = with_sign(x.x), q[nh][2 * i][1] = with_sign(x.y);
+            q[nh][2 * i + 1][0] = with_sign(x.z), q[nh][2 * i + 1][1] = with_sign(x.w);
         }
     }
     __syncthreads();
@@ -629,20 +633,12 @@ cudaError_t launch_parts(void (*fn)(StepArgs, Parts, ScoreFactor), unsigned grid
     return cudaLaunchKernelEx(&cfg, fn, a, parts, f);
 }
 
-// The factor of fp32 and bf16 scores.  Scale 0 gives every key the same weight;
-// a product with it would turn -inf into NaN, and 2^-100 rounds to the same
-// weights.
-ScoreFactor factor_of(float scale) {
-    if (scale == 0.f) return {1.f, 7.9e-31f};
-    return score_factor(scale);
-}
-
 template <int D>
 cudaError_t launch_f32(const StepArgs &a, const Parts &parts, cudaStream_t stream) {
     const int G = a.Hq / a.Hk;
     const int gc = heads_of_cta(G, LR_DT_F32);
     const unsigned grid = (unsigned)(a.N * a.Hk * ((G + gc - 1) / gc) * parts.splits);
-    const ScoreFactor f = factor_of(a.scale);
+    const ScoreFactor f = score_factor(a.scale);
     if (gc == 1) return launch_parts(&step_simt_kernel<D, 1>, grid, stream, a, parts, f);
     if (gc == 2) return launch_parts(&step_simt_kernel<D, 2>, grid, stream, a, parts, f);
     return launch_parts(&step_simt_kernel<D, 4>, grid, stream, a, parts, f);
@@ -652,7 +648,7 @@ template <int D>
 cudaError_t launch_bf16(const StepArgs &a, const Parts &parts, cudaStream_t stream) {
     const int G = a.Hq / a.Hk, heads = heads_of_cta(G, LR_DT_BF16);
     const unsigned grid = (unsigned)(a.N * a.Hk * ((G + heads - 1) / heads) * parts.splits);
-    const ScoreFactor f = factor_of(a.scale);
+    const ScoreFactor f = score_factor(a.scale);
     if (heads == 8) return launch_parts(&step_mma_kernel<D, 1>, grid, stream, a, parts, f);
     return launch_parts(&step_mma_kernel<D, 2>, grid, stream, a, parts, f);
 }
@@ -664,7 +660,7 @@ cudaError_t launch(const StepArgs &a, void *ws, lr_dtype dt, cudaStream_t stream
     const cudaError_t e = dt == LR_DT_F32 ? launch_f32<D>(a, parts, stream) : launch_bf16<D>(a, parts, stream);
     if (e != cudaSuccess || p.splits == 1 || p.cluster) return e;
     const unsigned rows = (unsigned)(a.N * a.Hq);
-    const ScoreFactor f = factor_of(a.scale);
+    const ScoreFactor f = score_factor(a.scale);
     if (dt == LR_DT_F32) step_join_kernel<float, D><<<rows, D, 0, stream>>>(a, parts, f);
     else step_join_kernel<__nv_bfloat16, D><<<rows, D, 0, stream>>>(a, parts, f);
     return cudaGetLastError();

@@ -411,9 +411,7 @@ cudaError_t launch(const WindowArgs &a, int slot, cudaStream_t stream) {
     auto *fn = splits > 1 ? window_f32_kernel<D, G, true> : window_f32_kernel<D, G, false>;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(fn), bytes, slot + (splits > 1 ? 12 : 0));
     if (e != cudaSuccess) return e;
-    // scale 0 gives every key the same weight; a product with it would turn
-    // the mask's -inf into NaN, and 2^-100 rounds to the same weights
-    const float c = a.scale == 0.f ? 7.9e-31f : score_factor(a.scale).c;
+    const ScoreFactor f = score_factor(a.scale);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(ctas * splits));
     cfg.blockDim = dim3(G * GT);
@@ -425,7 +423,7 @@ cudaError_t launch(const WindowArgs &a, int slot, cudaStream_t stream) {
     at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
     cfg.attrs = at;
     cfg.numAttrs = splits > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, fn, a, c, a.scale < 0.f ? -1.f : 1.f, splits);
+    return cudaLaunchKernelEx(&cfg, fn, a, f.c, f.sign, splits);
 }
 
 constexpr int kSlot = 208;  // ensure_smem_attr slots 208..210 and 220..222

@@ -126,7 +126,7 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity) {
 
 struct TcArgs {
     WindowArgs w;
-    float c;          // |scale| log2 e, positive
+    float c;          // the scores' factor, positive
     unsigned negate;  // idesc bit: scores of -Q (scale < 0)
     int pair_heads;   // the two query tiles are two heads, else consecutive rows
     int group;        // query heads of a key head
@@ -891,9 +891,10 @@ cudaError_t launch(const WindowArgs &a, int slot, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     TcArgs g;
     g.w = a;
-    // scale 0 gives every key the same weight; a product with it would turn
-    // the mask's -inf into NaN, and 2^-100 rounds to the same weights
-    g.c = a.scale == 0.f ? 7.9e-31f : score_factor(a.scale).c;
+    // The queries reach the products as they are, so for scale 0 c is fp32's
+    // smallest value: 2^(c s) is 1 within 2^-20 for every finite score, and a
+    // masked -inf stays one
+    g.c = a.scale == 0.f ? 0x1p-149f : score_factor(a.scale).c;
     g.negate = a.scale < 0.f ? 1u << 13 : 0u;
     g.group = a.Hq / a.Hk;
     g.pair_heads = g.group % 2 == 0;

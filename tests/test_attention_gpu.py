@@ -1007,3 +1007,64 @@ def test_step_batch_full_of_nan_stays_quick(dev, which, dtype):
     torch.cuda.synchronize()
     assert time.perf_counter() - start < 1.0
     assert o.isnan().all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.5])
+@pytest.mark.parametrize("max_len", STEP_CUTS)
+def test_step_scales(dev, max_len, scale, dtype):
+    lens = [64, 1, 17, 0, 33]
+    kc, vc, table = paged(134, lens, 2, 16, 64, dtype, dev)
+    wide = _wide(table, max_len, 16, dev)
+    check_step(dev, rnd(135, len(lens), 6, 64, dtype=dtype), kc, vc, wide, lens, NW, 0, scale, max_len=max_len)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("scale", [0.0, -0.3, 2.5])
+def test_window_scales_of_few_rows_and_many_keys(dev, scale, dtype):
+    q, k, v = (rnd(s, 1, 2, t, 64, dtype=dtype) for s, t in ((136, 17), (137, 1500), (138, 1500)))
+    check_window(dev, q, k, v, NW, 0, scale, dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_scale_of_zero_averages_whatever_the_scores_are(dev, dtype):
+    """q . k from the type's lowest to its largest value: times zero all alike."""
+    d, T = 64, 60
+    q = torch.zeros(1, 2, T, d, dtype=dtype)
+    q[..., 0] = 1
+    k = rnd(139, 1, 2, T, d, dtype=dtype)
+    k[..., 0] = torch.finfo(dtype).max / 4 * k[..., 0].float().clamp(-4, 4).to(dtype)
+    k[:, :, 5, 0], k[:, :, 6, 0] = torch.finfo(dtype).min, torch.finfo(dtype).max
+    v = rnd(140, 1, 2, T, d, dtype=dtype)
+    ref, size, reach, _ = oa.window(np64(q), np64(k), np64(v), NW, 0, 0.0)
+    bound = oa.attention_bound(ref, size, np.zeros_like(reach), T, d, BITS[dtype], 8 if dtype == BF16 else None)
+    within(lr.lr_fwd_window(q.to(dev), k.to(dev), v.to(dev), scale=0.0), ref, bound, "window")
+    for H in (1, 160):   # few rows: a cluster's parts, and alone
+        big = [t[:, :1].expand(1, H, T, d).repeat(1, 1, 12, 1).contiguous().to(dev) for t in (k, v)]
+        o = lr.lr_fwd_window(q[:, :1, :9].expand(1, H, 9, d).contiguous().to(dev), *big, scale=0.0)
+        a, s, _, _ = oa.window(np64(q[:, :1, :9]), *(np64(t[:, :1]) for t in big), NW, 0, 0.0)
+        b = oa.attention_bound(a, s, np.zeros(a.shape[:3]), 12 * T, d, BITS[dtype], 8 if dtype == BF16 else None)
+        within(o, np.broadcast_to(a, o.shape), np.broadcast_to(b, o.shape), f"window, {H} heads")
+    pool = lambda t: torch.cat((t, torch.zeros(1, 2, 4, d, dtype=dtype)), 2).view(2, 4, 16, d).transpose(0, 1).contiguous().to(dev)
+    table = torch.arange(4, dtype=torch.int32, device=dev).view(1, 4)
+    for max_len in STEP_CUTS:
+        o = lr.lr_step_paged(q[:, :, -1].contiguous().to(dev), pool(k), pool(v), _wide(table, max_len, 16, dev),
+                             torch.tensor([T], dtype=torch.int32, device=dev), max_len=max_len, scale=0.0)
+        within(o, ref[:, :, -1], bound[:, :, -1], f"step, {max_len}")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+def test_scales_at_the_ends_of_fp32(dev, dtype):
+    """The largest scale leaves the largest score alone, the smallest averages."""
+    d, T = 32, 50
+    q, k, v = (rnd(s, 1, 1, T, d, dtype=dtype) for s in (141, 142, 143))
+    for scale in (3.4e38, -3.4e38, 1e-44):
+        ref, size, reach, _ = oa.window(np64(q), np64(k), np64(v), NW, 0, scale)
+        # the scores of these seeds are far enough apart for fp32 to order them
+        bound = oa.attention_bound(ref, size, np.zeros_like(reach), T, d, BITS[dtype], 8 if dtype == BF16 else None)
+        within(lr.lr_fwd_window(q.to(dev), k.to(dev), v.to(dev), scale=scale), ref, bound, f"window, {scale}")
+        pool = lambda t: torch.cat((t, torch.zeros(1, 1, 14, d, dtype=dtype)), 2).view(4, 1, 16, d).to(dev)
+        o = lr.lr_step_paged(q[:, :, -1].contiguous().to(dev), pool(k), pool(v),
+                             torch.arange(4, dtype=torch.int32, device=dev).view(1, 4),
+                             torch.tensor([T], dtype=torch.int32, device=dev), scale=scale)
+        within(o, ref[:, :, -1], bound[:, :, -1], f"step, {scale}")
