@@ -20,7 +20,9 @@ import functools
 NO_WINDOW = (1 << 31) - 1   # a window that hides nothing
 QK_NORM = 0x1
 QK_INTERLEAVED = 0x2
-ATTN_SYMBOLS = ("lr_qk_norm_rope", "lr_fwd_window", "lr_step_paged", "lr_step_paged_workspace_size")
+QK_ZERO_Q, QK_ZERO_K = 0x8, 0x10
+ATTN_SYMBOLS = ("lr_qk_norm_rope", "lr_fwd_window", "lr_step_paged", "lr_step_paged_fill",
+                "lr_step_paged_workspace_size")
 
 
 class Strides(ctypes.Structure):
@@ -52,8 +54,9 @@ def declare(L):
                                   Strides, ctypes.POINTER(Paged)] + [i] * 6 + [vp]
     L.lr_fwd_window.restype = i
     L.lr_fwd_window.argtypes = ([vp, Strides] * 3 + [vp, vp, vp, Strides] + [i] * 8 + [f, i, vp])
-    L.lr_step_paged.restype = i
-    L.lr_step_paged.argtypes = ([vp, ctypes.POINTER(Paged), vp, vp] + [i] * 7 + [f, i, vp, sz, vp])
+    for step in (L.lr_step_paged, L.lr_step_paged_fill):
+        step.restype = i
+        step.argtypes = ([vp, ctypes.POINTER(Paged), vp, vp] + [i] * 7 + [f, i, vp, sz, vp])
     L.lr_step_paged_workspace_size.restype = sz
     L.lr_step_paged_workspace_size.argtypes = [i] * 8
 
@@ -133,7 +136,8 @@ def lr_qk_norm_rope(q, k, positions=None, *, norm=True, q_weight=None, k_weight=
     [pages,Hk,page,d], table [B,max_pages] int32 and v [B,Hk,T,d], the keys
     and v are also written at their positions in the cache; then
     ``write_k=False`` leaves out the contiguous keys.  Returns (q_out, k_out)
-    [B,H,T,d] contiguous (k_out None without ``write_k``)."""
+    [B,H,T,d] contiguous (k_out None without ``write_k``); rows of padding are
+    left as they were in outputs that are given, zeros in those made here."""
     import torch
     base = _base()
     dev = q.device
@@ -178,7 +182,10 @@ def lr_qk_norm_rope(q, k, positions=None, *, norm=True, q_weight=None, k_weight=
         if not write_k:
             raise ValueError("k_out given with write_k=False")
         _want(k_out, "k_out", k_shape, dtype, dev)
-    maps = QkMaps((QK_NORM if norm else 0) | (QK_INTERLEAVED if interleaved else 0),
+    flags = (QK_NORM if norm else 0) | (QK_INTERLEAVED if interleaved else 0)
+    if positions is not None:
+        flags |= (QK_ZERO_Q if q_out is None else 0) | (QK_ZERO_K if k_out is None else 0)
+    maps = QkMaps(flags,
                   None if q_weight is None else q_weight.data_ptr(),
                   None if k_weight is None else k_weight.data_ptr(), float(eps), rot,
                   None if inv_freq is None else inv_freq.data_ptr())
@@ -267,7 +274,8 @@ def lr_step_paged(q, k_cache, v_cache, table, lens, *, max_len=None, window=None
 
     q: [N,Hq,d]; k_cache, v_cache: [pages,Hk,page,d]; table: [N,max_pages]
     int32; lens: [N] int32 tokens in the cache, this one included (0: a row of
-    zeros, negative: an unused slot, left as it was); max_len: bound on lens
+    zeros, negative: an unused slot, whose row is left as it was in an ``o``
+    that is given, zeros in one made here); max_len: bound on lens
     (default: what the table can hold; a tight one is faster); window, sinks,
     scale as for :func:`lr_fwd_window`.  ``workspace`` is a uint8 CUDA tensor
     of at least ``step_paged_workspace_size(...)`` bytes, allocated here when
@@ -302,15 +310,16 @@ def lr_step_paged(q, k_cache, v_cache, table, lens, *, max_len=None, window=None
         need = _step_workspace(N, Hq, Hk, d, max_len, window, sinks, dt)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {dev}")
+    call = base.lib().lr_step_paged
     if o is None:
         o = torch.empty(q_shape, dtype=dtype, device=dev)
+        call = base.lib().lr_step_paged_fill
     if need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     ws, ws_bytes = ((None, 0) if workspace is None else
                     (workspace.data_ptr(), workspace.numel() * workspace.element_size()))
-    st = base.lib().lr_step_paged(q.data_ptr(), cache, lens.data_ptr(), o.data_ptr(), N, Hq, Hk, d,
-                                  max_len, window, sinks, scale, dt, ws, ws_bytes,
-                                  _handle(torch, dev))
+    st = call(q.data_ptr(), cache, lens.data_ptr(), o.data_ptr(), N, Hq, Hk, d, max_len, window,
+              sinks, scale, dt, ws, ws_bytes, _handle(torch, dev))
     if st != 0:
         raise base.LrError(st, "lr_step_paged")
     return o

@@ -137,6 +137,32 @@ lr_status check_step_sizes(int N, int Hq, int Hk, int d, int max_len, int window
     return LR_OK;
 }
 
+lr_status step_paged(const void *q, const lr_paged *cache, const int *lens, void *o, int N, int Hq,
+                     int Hk, int d, int max_len, int window, int sinks, float scale, lr_dtype dt,
+                     void *workspace, size_t workspace_bytes, bool fill, cudaStream_t stream) {
+    lr_status st = check_step_sizes(N, Hq, Hk, d, max_len, window, sinks, dt);
+    if (st != LR_OK) return st;
+    if (!isfinite(scale)) return LR_ERR_SHAPE;
+    if (!q || !cache || !lens || !o) return LR_ERR_NULL;
+    Span ck, cv, ct;
+    if ((st = check_paged(cache, N, Hk, d, dt, &ck, &cv, &ct)) != LR_OK) return st;
+    if ((long long)max_len > (long long)cache->page * cache->max_pages) return LR_ERR_SHAPE;
+    if (!aligned16(q) || !aligned16(o) || !aligned4(lens)) return LR_ERR_ALIGN;
+    const size_t need = lr_step_paged_workspace_size(N, Hq, Hk, d, max_len, window, sinks, dt);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return LR_ERR_WORKSPACE;
+    if (need > 0 && !aligned16(workspace)) return LR_ERR_ALIGN;
+    const size_t rows = (size_t)N * Hq * d * esize(dt);
+    const Span so = span(o, rows), sq = span(q, rows), sl = span(lens, (size_t)N * 4);
+    const Span sw = span(need > 0 ? workspace : nullptr, need);
+    for (const Span &i : {sq, sl, ck, cv, ct, sw})
+        if (overlap(so, i)) return LR_ERR_ALIAS;
+    for (const Span &i : {sq, sl, ck, cv, ct})
+        if (overlap(sw, i)) return LR_ERR_ALIAS;
+    const StepArgs a{q, cache->k, cache->v, o, cache->table, lens, N, Hq, Hk, max_len, window,
+                     sinks, cache->num_pages, log2_of(cache->page), cache->max_pages, scale, fill};
+    return done(launch_step_paged(a, d, dt, workspace, stream));
+}
+
 }  // namespace
 
 extern "C" {
@@ -152,7 +178,8 @@ lr_status lr_qk_norm_rope(const void *q, lr_strides qs, const void *k, lr_stride
         (long long)Hq + 2ll * Hk > 65535)
         return LR_ERR_SHAPE;
     if (!maps) return LR_ERR_NULL;
-    if (maps->flags & ~(LR_QK_NORM | LR_QK_INTERLEAVED)) return LR_ERR_FUSE;
+    if (maps->flags & ~(LR_QK_NORM | LR_QK_INTERLEAVED | LR_QK_ZERO_Q | LR_QK_ZERO_K))
+        return LR_ERR_FUSE;
     const bool norm = maps->flags & LR_QK_NORM;
     if (norm && !(maps->eps >= 0.f && maps->eps <= 3.4e38f)) return LR_ERR_FUSE;
     if (maps->rot < 0 || maps->rot > d || maps->rot % 16) return LR_ERR_UNSUPPORTED;
@@ -247,27 +274,16 @@ size_t lr_step_paged_workspace_size(int N, int Hq, int Hk, int d, int max_len, i
 lr_status lr_step_paged(const void *q, const lr_paged *cache, const int *lens, void *o, int N,
                         int Hq, int Hk, int d, int max_len, int window, int sinks, float scale,
                         lr_dtype dt, void *workspace, size_t workspace_bytes, cudaStream_t stream) {
-    lr_status st = check_step_sizes(N, Hq, Hk, d, max_len, window, sinks, dt);
-    if (st != LR_OK) return st;
-    if (!isfinite(scale)) return LR_ERR_SHAPE;
-    if (!q || !cache || !lens || !o) return LR_ERR_NULL;
-    Span ck, cv, ct;
-    if ((st = check_paged(cache, N, Hk, d, dt, &ck, &cv, &ct)) != LR_OK) return st;
-    if ((long long)max_len > (long long)cache->page * cache->max_pages) return LR_ERR_SHAPE;
-    if (!aligned16(q) || !aligned16(o) || !aligned4(lens)) return LR_ERR_ALIGN;
-    const size_t need = lr_step_paged_workspace_size(N, Hq, Hk, d, max_len, window, sinks, dt);
-    if (need > 0 && (!workspace || workspace_bytes < need)) return LR_ERR_WORKSPACE;
-    if (need > 0 && !aligned16(workspace)) return LR_ERR_ALIGN;
-    const size_t rows = (size_t)N * Hq * d * esize(dt);
-    const Span so = span(o, rows), sq = span(q, rows), sl = span(lens, (size_t)N * 4);
-    const Span sw = span(need > 0 ? workspace : nullptr, need);
-    for (const Span &i : {sq, sl, ck, cv, ct, sw})
-        if (overlap(so, i)) return LR_ERR_ALIAS;
-    for (const Span &i : {sq, sl, ck, cv, ct})
-        if (overlap(sw, i)) return LR_ERR_ALIAS;
-    const StepArgs a{q, cache->k, cache->v, o, cache->table, lens, N, Hq, Hk, max_len, window,
-                     sinks, cache->num_pages, log2_of(cache->page), cache->max_pages, scale};
-    return done(launch_step_paged(a, d, dt, workspace, stream));
+    return step_paged(q, cache, lens, o, N, Hq, Hk, d, max_len, window, sinks, scale, dt, workspace,
+                      workspace_bytes, false, stream);
+}
+
+lr_status lr_step_paged_fill(const void *q, const lr_paged *cache, const int *lens, void *o, int N,
+                             int Hq, int Hk, int d, int max_len, int window, int sinks, float scale,
+                             lr_dtype dt, void *workspace, size_t workspace_bytes,
+                             cudaStream_t stream) {
+    return step_paged(q, cache, lens, o, N, Hq, Hk, d, max_len, window, sinks, scale, dt, workspace,
+                      workspace_bytes, true, stream);
 }
 
 }  // extern "C"

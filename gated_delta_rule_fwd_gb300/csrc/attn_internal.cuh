@@ -139,6 +139,7 @@ struct StepArgs {
     const int *table, *lens;
     int N, Hq, Hk, max_len, window, sinks, num_pages, page_log2, max_pages;
     float scale;
+    int fill;  // rows that are not computed are zeros
 };
 // How a step's keys are cut: chunks of `chunk` keys, at most `splits` of them,
 // joined by a cluster or by a second kernel.

@@ -120,6 +120,15 @@ __global__ void __launch_bounds__(NT, kCtas<E>) qk_norm_rope_kernel(RopeArgs a) 
         const E *q_from = static_cast<const E *>(a.q) + b * a.qs.b + t * a.qs.t + c0;
         Row8<E> r[U];
         fetch_rows(r, q_from, a.qs.h, a.Hq, part);
+        if (!on && n0 < a.total && (a.maps.flags & (LR_QK_ZERO_Q | LR_QK_ZERO_K))) {
+            const Row8<E> zero{};
+            if (a.maps.flags & LR_QK_ZERO_Q)
+                for (int h = part; h < a.Hq; h += parts)
+                    put(static_cast<E *>(a.qo) + (((size_t)b * a.Hq + h) * a.T + t) * D + c0, zero);
+            if (a.ko && (a.maps.flags & LR_QK_ZERO_K))
+                for (int h = part; h < a.Hk; h += parts)
+                    put(static_cast<E *>(a.ko) + (((size_t)b * a.Hk + h) * a.T + t) * D + c0, zero);
+        }
         if (!__any_sync(0xffffffffu, on)) continue;  // padding
         long long place = -1;  // first cache row of the token (head 0)
         if (a.ck && on) {

@@ -53,6 +53,13 @@ __device__ __forceinline__ float ld_cluster(uint32_t addr) {
     return r;
 }
 
+// Rows of a sequence that is not computed.
+template <typename E, int D>
+__device__ __forceinline__ void zero_rows(const StepArgs &a, int n, int h0, int heads) {
+    E *o = static_cast<E *>(a.o) + ((size_t)n * a.Hq + h0) * D;
+    for (int i = threadIdx.x; i < heads * D; i += NT) o[i] = from_f<E>(0.f);
+}
+
 // Output row `head` of sequence n by one warp, put right where it is not
 // finite.  sum(): of its weights.  Keys of pages outside the pool are left out.
 template <typename E, int D, typename Sum>
@@ -194,9 +201,10 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts, 
     id /= gq;
     const int hk = id % a.Hk, n = id / a.Hk;
     const int len = a.lens[n];
-    if (len < 0) return;
-    if (len > a.max_len) {
-        if (tid == 0 && split == 0 && gi == 0 && hk == 0) atomicOr(&g_step_error, kAttnIndex);
+    const int h0 = hk * G + gi * GC, heads = min(GC, G - gi * GC);
+    if (len < 0 || len > a.max_len) {
+        if (len > 0 && tid == 0 && split == 0 && gi == 0 && hk == 0) atomicOr(&g_step_error, kAttnIndex);
+        if (a.fill && split == 0) zero_rows<float, D>(a, n, h0, heads);
         return;
     }
     const SeenKeys s = seen_keys(len - 1, len, a.window, a.sinks);
@@ -204,7 +212,6 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts, 
     const int c0 = split * parts.chunk;
     if (c0 >= seen && split > 0 && !parts.cluster) return;  // the join knows how many chunks there are
     const int c1 = min(seen, c0 + parts.chunk);
-    const int h0 = hk * G + gi * GC, heads = min(GC, G - gi * GC);
     const int lane = tid % LANES, group = tid / LANES, ch = lane * 8;
 
     const float *qn = static_cast<const float *>(a.q) + (size_t)n * a.Hq * D;
@@ -366,9 +373,10 @@ __global__ void __launch_bounds__(NT)
     id /= gq;
     const int hk = id % a.Hk, n = id / a.Hk;
     const int len = a.lens[n];
-    if (len < 0) return;
-    if (len > a.max_len) {
-        if (tid == 0 && split == 0 && gi == 0 && hk == 0) atomicOr(&g_step_error, kAttnIndex);
+    const int h0 = hk * G + gi * HEADS, heads = min(HEADS, G - gi * HEADS);
+    if (len < 0 || len > a.max_len) {
+        if (len > 0 && tid == 0 && split == 0 && gi == 0 && hk == 0) atomicOr(&g_step_error, kAttnIndex);
+        if (a.fill && split == 0) zero_rows<__nv_bfloat16, D>(a, n, h0, heads);
         return;
     }
     const SeenKeys s = seen_keys(len - 1, len, a.window, a.sinks);
@@ -377,7 +385,6 @@ __global__ void __launch_bounds__(NT)
     const int tiles = sink_tiles + max(0, (s.hi + kTile - 1) / kTile - k_first);
     const int per = parts.chunk / kTile, t0 = split * per, t1 = min(tiles, t0 + per);
     if (t0 >= tiles && split > 0 && !parts.cluster) return;  // the join knows how many chunks there are
-    const int h0 = hk * G + gi * HEADS, heads = min(HEADS, G - gi * HEADS);
 
     auto key_of = [&](int i) { return kTile * (i < sink_tiles ? i : i - sink_tiles + k_first); };
     for (int i = tid; i < t1 - t0; i += NT) {

@@ -57,6 +57,8 @@ typedef struct {
 
 #define LR_QK_NORM 0x1u        /* y = weight * x / sqrt(mean(x^2) + eps), per head */
 #define LR_QK_INTERLEAVED 0x2u /* rotate channels (2i, 2i+1), else (i, i + rot/2)  */
+#define LR_QK_ZERO_Q 0x8u      /* padding's rows of q_out are written as zeros     */
+#define LR_QK_ZERO_K 0x10u     /* the same for k_out (where it is given)           */
 
 typedef struct {
     unsigned flags;          /* OR of LR_QK_*                                       */
@@ -82,7 +84,8 @@ typedef struct {
  *   q, qs      [B, Hq, T, d] with strides qs
  *   k, ks      [B, Hk, T, d] with strides ks
  *   positions  [B, T] int32, or NULL for p = t.  A negative position marks
- *              padding: nothing of that token is written anywhere.
+ *              padding: nothing of that token is written anywhere, but for the
+ *              zeros that LR_QK_ZERO_Q and LR_QK_ZERO_K ask for.
  *   q_out      [B, Hq, T, d] contiguous, written
  *   k_out      [B, Hk, T, d] contiguous, written, or NULL
  *   v, vs      [B, Hk, T, d] with strides vs: with a cache only, else NULL
@@ -153,8 +156,15 @@ lr_status lr_step_paged(const void *q, const lr_paged *cache, const int *lens, v
                         int Hq, int Hk, int d, int max_len, int window, int sinks, float scale,
                         lr_dtype dt, void *workspace, size_t workspace_bytes, cudaStream_t stream);
 
-/* Workspace bytes lr_step_paged needs (0 as well for arguments it would
- * reject). */
+/* lr_step_paged for an output that held nothing before: the rows that it would
+ * leave as they were (unused slots, lengths beyond max_len) are zeros. */
+lr_status lr_step_paged_fill(const void *q, const lr_paged *cache, const int *lens, void *o, int N,
+                             int Hq, int Hk, int d, int max_len, int window, int sinks, float scale,
+                             lr_dtype dt, void *workspace, size_t workspace_bytes,
+                             cudaStream_t stream);
+
+/* Workspace bytes lr_step_paged and lr_step_paged_fill need (0 as well for
+ * arguments they would reject). */
 size_t lr_step_paged_workspace_size(int N, int Hq, int Hk, int d, int max_len, int window,
                                     int sinks, lr_dtype dt);
 

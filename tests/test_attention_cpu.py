@@ -226,3 +226,38 @@ def test_norm_rope_binding_refuses(lr, change):
     q, k = a.pop("q"), a.pop("k")
     with pytest.raises((ValueError, TypeError)):
         lr.lr_qk_norm_rope(q, k, **a)
+
+
+def test_step_fill_refuses_what_the_step_refuses(lib):
+    """The same table of refusals for lr_step_paged_fill; the flags that ask for zeros are known ones."""
+    child = _CHILD.replace("L.lr_step_paged(", "L.lr_step_paged_fill(").replace(
+        "bad = [", 'cases += [("rope-zero", rope(flags=0x19), 7), ("rope-flag-next", rope(flags=0x20), 12)]\nbad = [')
+    assert child.count("lr_step_paged_fill") == 1 and "rope-zero" in child
+    env = dict(os.environ, CUDA_VISIBLE_DEVICES="")
+    r = subprocess.run([sys.executable, "-c", child, ROOT], env=env, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_binding_asks_for_zeros_only_in_outputs_that_it_makes(lr, monkeypatch):
+    from gated_delta_rule_fwd_gb300 import attention as at
+    calls = []
+
+    class Records:
+        def __getattr__(self, name):
+            return lambda *a: calls.append((name, a)) or 0
+    monkeypatch.setattr(lr, "lib", lambda: Records())
+    monkeypatch.setattr(at, "_handle", lambda torch, dev: None)
+    monkeypatch.setattr(at, "_step_workspace", lambda *a: 0)
+    q, k, pos = _t(2, 4, 9, 64), _t(2, 2, 9, 64), torch.zeros(2, 9, dtype=torch.int32)
+    for kw, want in ((dict(), 0x18), (dict(q_out=_t(2, 4, 9, 64)), 0x10), (dict(k_out=_t(2, 2, 9, 64)), 0x8),
+                     (dict(q_out=_t(2, 4, 9, 64), k_out=_t(2, 2, 9, 64)), 0)):
+        lr.lr_qk_norm_rope(q, k, pos, **kw)
+        assert calls[-1][1][5].flags & 0x18 == want
+    lr.lr_qk_norm_rope(q, k)   # no padding without positions
+    assert calls[-1][1][5].flags & 0x18 == 0
+    args = (_t(3, 4, 64), _t(5, 2, 16, 64), _t(5, 2, 16, 64), torch.zeros(3, 4, dtype=torch.int32),
+            torch.zeros(3, dtype=torch.int32))
+    lr.lr_step_paged(*args)
+    assert calls[-1][0] == "lr_step_paged_fill"
+    lr.lr_step_paged(*args, o=_t(3, 4, 64))
+    assert calls[-1][0] == "lr_step_paged"

@@ -1068,3 +1068,50 @@ def test_scales_at_the_ends_of_fp32(dev, dtype):
                              torch.arange(4, dtype=torch.int32, device=dev).view(1, 4),
                              torch.tensor([T], dtype=torch.int32, device=dev), scale=scale)
         within(o, ref[:, :, -1], bound[:, :, -1], f"step, {scale}")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("d,B,T,Hq,Hk", [(128, 3, 1, 4, 1), (64, 2, 90, 5, 2), (32, 4, 3000, 3, 1)])
+def test_norm_rope_own_outputs_are_zero_in_the_padding(dev, d, B, T, Hq, Hk, dtype):
+    """Outputs that the call makes have zeros where nothing is computed,
+    whatever their memory held, and the other rows as in given outputs."""
+    q, k, v = (rnd(s, B, h, T, d, dtype=dtype).to(dev) for s, h in ((150, Hq), (151, Hk), (152, Hk)))
+    f = torch.tensor(10000.0 ** (-np.arange(d // 2) / (d // 2)), device=dev)
+    pos = torch.arange(T, dtype=torch.int32, device=dev).expand(B, T).contiguous()
+    pos[0] = -1
+    pos[1, T // 3:T // 3 * 2 + 1] = -5
+    most = -(-T // 16)
+    cache = dict(v=v, table=torch.arange(B * most, dtype=torch.int32, device=dev).view(B, most))
+    for write_k in (True, False):
+        kc, vc = (torch.full((B * most, Hk, 16, d), 7.0, dtype=dtype, device=dev) for _ in range(2))
+        want = [torch.full_like(q, 7.0), torch.full_like(k, 7.0)]
+        lr.lr_qk_norm_rope(q, k, pos, inv_freq=f, q_out=want[0], k_out=want[1], k_cache=kc, v_cache=vc, **cache)
+        pools = [kc.clone(), vc.clone()]
+        on = (pos >= 0)[:, None, :, None]
+        junk = [torch.full_like(t, float("nan")) for t in (q, k, q, k)]
+        del junk   # what the allocator hands out next
+        got = lr.lr_qk_norm_rope(q, k, pos, inv_freq=f, write_k=write_k, k_cache=kc, v_cache=vc, **cache)
+        assert torch.equal(got[0], torch.where(on, want[0], torch.zeros_like(q)))
+        assert got[1] is None if not write_k else torch.equal(got[1], torch.where(on, want[1], torch.zeros_like(k)))
+        assert torch.equal(kc, pools[0]) and torch.equal(vc, pools[1])
+    junk = [torch.full_like(t, float("nan")) for t in (q, k)]
+    given, junk = junk[0], None   # one output given, one made
+    got = lr.lr_qk_norm_rope(q, k, pos, inv_freq=f, q_out=given.fill_(7.0))
+    assert torch.equal(given, want[0]) and torch.equal(got[1], torch.where(on, want[1], torch.zeros_like(k)))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("d,Hq,Hk", [(32, 3, 3), (64, 17, 1), (128, 8, 2)])
+@pytest.mark.parametrize("max_len", STEP_CUTS)
+def test_step_own_output_is_zero_in_unused_slots(dev, max_len, d, Hq, Hk, dtype):
+    """The same for unused slots and lengths beyond the bound."""
+    lens = [64, -1, 17, max_len + 1, -2 ** 31, 3]
+    kc, vc, table = paged(153, [64, 0, 17, 0, 0, 3], Hk, 16, d, dtype, dev)
+    wide = _wide(table, max_len, 16, dev)
+    q, ld = rnd(154, len(lens), Hq, d, dtype=dtype).to(dev), torch.tensor(lens, dtype=torch.int32, device=dev)
+    want = lr.lr_step_paged(q, kc, vc, wide, ld, max_len=max_len, o=torch.zeros_like(q))
+    junk = [torch.full_like(q, float("nan")) for _ in range(4)]
+    del junk
+    got = lr.lr_step_paged(q, kc, vc, wide, ld, max_len=max_len)
+    assert lr.device_status() == LR_ERR_INDEX
+    assert torch.equal(got, want) and (got[[1, 3, 4]] == 0).all() and (got[[0, 2, 5]] != 0).any()
