@@ -174,8 +174,9 @@ lr_status lr_qk_norm_rope(const void *q, lr_strides qs, const void *k, lr_stride
     lr_status st = check_types(d, dt);
     if (st != LR_OK) return st;
     if (B < 1 || T < 0 || Hq < 1 || Hk < 1) return LR_ERR_SHAPE;
+    // the kernel's head index runs up to 4 x 64 beyond the last head
     if (!count_ok(B, T, Hq > Hk ? Hq : Hk, d) || (long long)B * T > (1ll << 30) ||
-        (long long)Hq + 2ll * Hk > 65535)
+        Hq > (1 << 30) || Hk > (1 << 30))
         return LR_ERR_SHAPE;
     if (!maps) return LR_ERR_NULL;
     if (maps->flags & ~(LR_QK_NORM | LR_QK_INTERLEAVED | LR_QK_ZERO_Q | LR_QK_ZERO_K))

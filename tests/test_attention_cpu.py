@@ -261,3 +261,14 @@ def test_binding_asks_for_zeros_only_in_outputs_that_it_makes(lr, monkeypatch):
     assert calls[-1][0] == "lr_step_paged_fill"
     lr.lr_step_paged(*args, o=_t(3, 4, 64))
     assert calls[-1][0] == "lr_step_paged"
+
+
+def test_norm_rope_takes_any_number_of_heads_that_fits(lib):
+    child = _CHILD[:_CHILD.index("cases = [")] + '''
+cases = [("many-q", rope(B=1, T=1, Hq=70000, Hk=1, cache=False, v=None, d=32, rot=32), 7),
+         ("many-k", rope(B=1, T=1, Hq=3, Hk=40000, cache=False, v=None, d=32, rot=32), 7),
+         ("too-many", rope(B=1, T=1, Hq=(1 << 30) + 1, Hk=1, cache=False, v=None, d=32, rot=32), 2)]
+''' + _CHILD[_CHILD.index("bad = ["):]
+    env = dict(os.environ, CUDA_VISIBLE_DEVICES="")
+    r = subprocess.run([sys.executable, "-c", child, ROOT], env=env, capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0, r.stdout + r.stderr

@@ -1115,3 +1115,12 @@ def test_step_own_output_is_zero_in_unused_slots(dev, max_len, d, Hq, Hk, dtype)
     got = lr.lr_step_paged(q, kc, vc, wide, ld, max_len=max_len)
     assert lr.device_status() == LR_ERR_INDEX
     assert torch.equal(got, want) and (got[[1, 3, 4]] == 0).all() and (got[[0, 2, 5]] != 0).any()
+
+
+@pytest.mark.parametrize("Hq,Hk", [(70000, 1), (3, 40000)])
+def test_norm_rope_of_many_heads(dev, Hq, Hk):
+    q, k = (rnd(s, 1, h, 1, 32, dtype=BF16) for s, h in ((160, Hq), (161, Hk)))
+    got = lr.lr_qk_norm_rope(q.to(dev), k.to(dev), eps=1e-5)
+    for t, out in ((q, got[0]), (k, got[1])):
+        y, size = oa.qk_norm_rope(np64(t), np.zeros((1, 1)), None, 1e-5)
+        within(out, y, rope_bound(y, size, 32, BF16))
