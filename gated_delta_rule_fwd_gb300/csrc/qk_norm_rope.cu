@@ -11,9 +11,12 @@
 //
 // Angle: th = p f.  With s = frac(f / 2 pi) as a 64-bit fixed-point fraction
 // of a turn, p s mod 2^64 is the exact fraction of the product, so the only
-// errors are those of s (2^-53 relative) and of the final fp32 conversion
-// (2^-25 of a half turn), whatever the position.  s is formed once per CTA: it
-// takes the fp64 pipe, which does two operations a cycle.
+// errors are those of s (2^-64 of a turn) and of the final fp32 conversion
+// (2^-25 of a half turn), whatever the position and the frequency.  s takes the
+// product f / 2 pi with what its rounding and that of 1 / 2 pi leave out (fp64
+// alone would be off by 2^-53 of the turns of a position, which shows at the
+// far end of an int from about one turn on).  It is formed once per CTA on the
+// fp64 pipe, which does two operations a cycle.
 #include "attn_internal.cuh"
 
 namespace lr {
@@ -97,9 +100,12 @@ __global__ void __launch_bounds__(NT, kCtas<E>) qk_norm_rope_kernel(RopeArgs a) 
     const int from = (tid & 31) + hop / 8;
     if (ROT != kNone) {
         if (tid < half) {
-            double turns = a.maps.inv_freq[tid] * 0.15915494309189533577;  // 1 / (2 pi)
-            turns -= floor(turns);
-            step[tid] = __double2ull_rz(turns * 18446744073709551616.0);
+            // 1 / (2 pi) as a sum of two; below, 2^64 units of a turn
+            constexpr double kHigh = 0x1.45f306dc9c883p-3, kLow = -0x1.6b01ec5417056p-57;
+            const double f = a.maps.inv_freq[tid], turns = f * kHigh;
+            const double rest = fma(f, kLow, fma(f, kHigh, -turns));
+            step[tid] = __double2ull_rz((turns - floor(turns)) * 0x1p64) +
+                        (unsigned long long)__double2ll_rn(rest * 0x1p64);
         }
         __syncthreads();
     }

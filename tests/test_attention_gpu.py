@@ -1124,3 +1124,30 @@ def test_norm_rope_of_many_heads(dev, Hq, Hk):
     for t, out in ((q, got[0]), (k, got[1])):
         y, size = oa.qk_norm_rope(np64(t), np.zeros((1, 1)), None, 1e-5)
         within(out, y, rope_bound(y, size, 32, BF16))
+
+
+def _turned(x, p, f):
+    """x [d] turned in split halves by p f, the angle reduced in rationals."""
+    from fractions import Fraction
+    turn = 2 * Fraction(3141592653589793238462643383279502884197169399375105820974944592, 10 ** 63)
+    th = np.array([float(p * Fraction(y) % turn) for y in f])
+    a, b = x[:len(f)], x[len(f):]
+    c, s = np.cos(th), np.sin(th)
+    return np.concatenate((a * c - b * s, b * c + a * s)), np.tile(np.abs(a) + np.abs(b), 2)
+
+
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_norm_rope_fast_angles_at_far_positions(dev, interleaved):
+    """Radians per position of any size, at positions up to an int's end."""
+    f = np.array([6.1, -2.9, 1e3 / 7, -1.0 / 3, 2.0 ** 40 / 3, 1e-30, -1e-30, 0.0, 3.0, 5.5, 1.0, 0.7, 40.0, -77.7, 1e6 / 3, 2.0])
+    pos = np.array([1, 2 ** 31 - 1, 2 ** 31 - 2, 1000003, 131071, 0], np.int32)
+    x = rnd(162, 1, 1, len(pos), 32)
+    x[0, 0] = x[0, 0, 0]
+    laid = x[..., torch.arange(32).view(2, 16).T.reshape(-1)] if interleaved else x
+    got = lr.lr_qk_norm_rope(laid.to(dev), laid.to(dev), torch.from_numpy(pos)[None].to(dev), norm=False,
+                             inv_freq=torch.from_numpy(f).to(dev), interleaved=interleaved)[0].cpu()
+    if interleaved:
+        got = torch.cat((got[..., 0::2], got[..., 1::2]), -1)
+    for i, p in enumerate(pos):
+        y, size = _turned(np64(x[0, 0, i]), int(p), f)
+        within(got[0, 0, i], y, rope_bound(y, size, 32, F32), f"position {p}")
