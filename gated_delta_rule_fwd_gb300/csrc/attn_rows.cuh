@@ -119,7 +119,11 @@ __device__ __forceinline__ void mend_row_of(const E *q, const Keys &keys, E *o, 
             l = old + p;
             const float keep = old / l, take = p / l;
 #pragma unroll
-            for (int i = 0; i < PL; ++i) acc[i] = acc[i] * keep + take * to_f<E>(vj[lane + 32 * i]);
+            for (int i = 0; i < PL; ++i) {
+                const float y = acc[i] * keep + take * to_f<E>(vj[lane + 32 * i]);
+                // a mean of the type's largest values, but for its rounding
+                acc[i] = fminf(fmaxf(y, -3.402823466e38f), 3.402823466e38f);
+            }
         }
     }
 #pragma unroll

@@ -1151,3 +1151,24 @@ def test_norm_rope_fast_angles_at_far_positions(dev, interleaved):
     for i, p in enumerate(pos):
         y, size = _turned(np64(x[0, 0, i]), int(p), f)
         within(got[0, 0, i], y, rope_bound(y, size, 32, F32), f"position {p}")
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["f32", "bf16"])
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_means_of_values_at_the_end_of_the_type_are_finite(dev, sign, d, dtype):
+    """Every value the type's largest: whatever the weights round to, the mean
+    is that value, and no rounding of it may leave the type."""
+    top = sign * torch.finfo(dtype).max
+    for B, Hq, Hk, Tq, Tk in ((1, 160, 160, 40, 300), (1, 2, 1, 40, 700), (1, 3, 1, 9, 200)):
+        q, k = (rnd(s, B, h, t, d, dtype=dtype).to(dev) for s, h, t in ((170, Hq, Tq), (171, Hk, Tk)))
+        v = torch.full((B, Hk, Tk, d), top, dtype=dtype, device=dev)
+        o = lr.lr_fwd_window(q, k, v, window=250, sinks=2)
+        assert ((o.double() / top - 1).abs() <= 2.0 ** -7).all()
+    lens = [64, 1, 17, 50]
+    kc, vc, table = paged(172, lens, 1, 16, d, dtype, dev)
+    vc.fill_(top)
+    q, ld = rnd(173, len(lens), 8, d, dtype=dtype).to(dev), torch.tensor(lens, dtype=torch.int32, device=dev)
+    for max_len in STEP_CUTS:
+        o = lr.lr_step_paged(q, kc, vc, _wide(table, max_len, 16, dev), ld, max_len=max_len)
+        assert ((o.double() / top - 1).abs() <= 2.0 ** -7).all()
