@@ -310,15 +310,16 @@ def lr_step_paged(q, k_cache, v_cache, table, lens, *, max_len=None, window=None
         need = _step_workspace(N, Hq, Hk, d, max_len, window, sinks, dt)
     elif workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {dev}")
-    call = base.lib().lr_step_paged
+    L = base.lib()
+    step = L.lr_step_paged
     if o is None:
         o = torch.empty(q_shape, dtype=dtype, device=dev)
-        call = base.lib().lr_step_paged_fill
+        step = L.lr_step_paged_fill
     if need > 0:
         workspace = torch.empty(need, dtype=torch.uint8, device=dev)
     ws, ws_bytes = ((None, 0) if workspace is None else
                     (workspace.data_ptr(), workspace.numel() * workspace.element_size()))
-    st = call(q.data_ptr(), cache, lens.data_ptr(), o.data_ptr(), N, Hq, Hk, d, max_len, window,
+    st = step(q.data_ptr(), cache, lens.data_ptr(), o.data_ptr(), N, Hq, Hk, d, max_len, window,
               sinks, scale, dt, ws, ws_bytes, _handle(torch, dev))
     if st != 0:
         raise base.LrError(st, "lr_step_paged")

@@ -111,8 +111,11 @@ cudaError_t launch_qk_norm_rope(const void *q, lr_strides qs, const void *k, lr_
 
 constexpr int kMostCluster = 8;  // CTAs of the largest cluster that is always allowed
 // CTAs of clusters of 1, 2, .. 8 that find room on the GPU at once with one to
-// four of them on an SM (the occupancy calculator's answers: a cluster stays
-// within one of the GPU's groups of SMs, which it does not always fill).
+// four of them on an SM (the occupancy calculator's answers on a GPU of 152 SMs:
+// a cluster stays within one of the GPU's groups of SMs, which it does not
+// always fill).  Another chip may have other SMs of a group switched off: plans
+// then meet a second round that they meant to avoid, and results stay the same.
+// A table, so that plans and workspace sizes need no device.
 constexpr int kClusterRoom[4][kMostCluster + 1] = {{0, 152, 152, 138, 144, 140, 138, 105, 120},
                                                    {0, 304, 304, 291, 296, 290, 276, 266, 288},
                                                    {0, 456, 456, 444, 440, 435, 444, 413, 408},

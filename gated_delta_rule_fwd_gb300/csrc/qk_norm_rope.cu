@@ -31,7 +31,8 @@ constexpr int NT = 256;
 // rows and 3 CTAs; before the last cuts in instructions 72, and 79 with 2 rows
 // and 4 CTAs, 85 with 4 rows and 2.  Fetching each next row as its place is
 // free, across queries, keys and tokens, costs more instructions than it hides
-// (65 to 67).  fp32 rows take twice the registers: two CTAs.
+// (65 to 67).  fp32 rows take twice the registers: two CTAs.  The bf16 form with
+// split halves spills 12 bytes a thread at its 80 registers.
 constexpr int U = 4;
 template <typename E> constexpr int kCtas = sizeof(E) == 2 ? 3 : 2;
 

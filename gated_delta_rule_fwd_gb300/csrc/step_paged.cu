@@ -22,7 +22,12 @@
 //
 // fp32 (step_simt_kernel): CUDA cores.  Every group of d / 8 lanes takes keys
 // of its own, with a running maximum and sum of its own (33 sequences with
-// window 1024, 139 MB: 24.2 us).
+// window 1024, 139 MB: 24.2 us).  With up to two heads on a key head it reads
+// the cache at the copy rate; more heads cost instructions, and more than four
+// are parts that read the cache again (32 sequences of 4096, 4 key heads, d =
+// 128, 537 MB: 81 us with 1 head on each, 84 with 2, 147 with 4, 205 with 8, 324
+// with 16).  bf16 takes up to 16 heads in one read (268 MB: 60 us with 1, 63 with
+// 8, 68 with 16, 124 with 32).
 //
 // Rows that come out not finite are explained or computed again from the keys
 // they see (attn_rows.cuh), as in the window form; one vote of the CTA that

@@ -48,9 +48,9 @@
 // 10 the TMA loads, warp 11 fetches the next piece of work.
 // Every wait is bounded (lr_device_status).
 //
-// Measured (d = 128): 16384 causal rows of 16 heads on 4 in 620 us, 1.77
-// PFLOP/s of visible work; with a window of 1024 and 4 sinks 126 us; 4096
-// causal rows of 32 heads 111 us.  A pair of tiles takes 2690 cycles for 2048
+// Measured (d = 128): 16384 causal rows of 16 heads on 4 in 620 to 670 us, 1.64
+// to 1.77 PFLOP/s of visible work (by the clock under the power limit); with a
+// window of 1024 and 4 sinks 125 us; 4096 causal rows of 32 heads 110.5 us.  A pair of tiles takes 2690 cycles for 2048
 // of the tensor pipe: the chain of a tile is scores -> first half of the weights
 // (1100) -> its turn on the pipe (200) -> its 16 products (930) -> scores (460).
 #include <cuda.h>

@@ -190,8 +190,9 @@ lr_status lr_step(const void *q, const void *k, const void *v,
  * completion signal that never arrived); such a kernel stops early and its
  * outputs are incomplete.  Also reports and clears what the attention kernels
  * (lr_attn.h) found out of range on the device.  Synchronises the current
- * device first.  Returns LR_OK, LR_ERR_TIMEOUT, LR_ERR_INDEX, or LR_ERR_CUDA
- * if the device cannot be queried.
+ * device first.  Returns LR_OK, LR_ERR_TIMEOUT, LR_ERR_INDEX (LR_ERR_TIMEOUT
+ * where both were found; both are cleared), or LR_ERR_CUDA if the device cannot
+ * be queried.
  */
 lr_status lr_device_status(void);
 

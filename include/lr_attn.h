@@ -16,7 +16,18 @@
  * the current device without synchronising; no allocation, no state kept
  * between calls, no exceptions.  Values are fp32 or bf16 (lr_dtype); sums,
  * norms, rotations and softmax statistics are fp32, and each result is
- * rounded once when it is stored.
+ * rounded once when it is stored.  One rounding more: where the type is bf16,
+ * a softmax weight is rounded to bf16 for its product with a value (the sum of
+ * the weights takes it unrounded), which moves an output by up to 2^-8 of the
+ * weighted mean of |v|; against weights of 32 bits the error of a result is
+ * 1.2 to 1.4 times as large.
+ *
+ * Scores: q . k is formed in fp32, and the scale applies to differences of it,
+ * so a finite scale takes no finite q . k out of range.  A key whose q . k
+ * times the scale's sign is -inf weighs nothing; one where it is NaN or +inf
+ * makes its rows NaN.  With all scores in range, a channel in which a row sees
+ * an infinite value is that infinity however small the weight, with both signs
+ * or a NaN it is NaN, and finite values average without overflow.
  *
  * Heads: Hq query heads share Hk key/value heads, Hq a multiple of Hk; query
  * head h reads key head h / (Hq / Hk).  Head widths d: 32, 64, 128.
@@ -79,7 +90,7 @@ typedef struct {
  *
  * for each query and key head.  Angles are formed from the product taken
  * modulo a full turn in 64-bit fixed point, so they stay accurate to fp32 at
- * every position an int holds.
+ * every position an int holds and every frequency up to 2^50.
  *
  *   q, qs      [B, Hq, T, d] with strides qs
  *   k, ks      [B, Hk, T, d] with strides ks
@@ -141,8 +152,11 @@ lr_status lr_fwd_window(const void *q, lr_strides qs, const void *k, lr_strides 
  *           Negative: an unused slot, its row is left as it was.
  *   o       [N, Hq, d], written; overlaps no input
  *   max_len bound on lens, 1 <= max_len <= page * max_pages: it sets how the
- *           work is split, so a tight bound is faster.  A longer sequence is
- *           reported as LR_ERR_INDEX and its row is left as it was.
+ *           work is split, so a tight bound is faster and needs less workspace
+ *           (128 sequences of 500 to 8192 tokens, 32 heads on 8, bf16: 351 us
+ *           and 16 MB under a bound of 8192, 369 us and 65 MB under 32768, 465
+ *           us and 260 MB under 131072).  A longer sequence is reported as
+ *           LR_ERR_INDEX and its row is left as it was.
  *   workspace   lr_step_paged_workspace_size(...) bytes, 16-byte aligned (0
  *           where the work is not split, or its parts are joined on the chip);
  *           its contents on entry do not matter.  Calls that share one are
@@ -150,7 +164,9 @@ lr_status lr_fwd_window(const void *q, lr_strides qs, const void *k, lr_strides 
  *
  * The keys a sequence sees are cut into chunks of equal size, which the CTAs
  * of a cluster or a second kernel join in a fixed order: a repeated call gives
- * the same bits.
+ * the same bits.  Up to 16 query heads of a key head in bf16, and 4 in fp32,
+ * share one read of its keys and values; more are worked on in parts that each
+ * read them.
  */
 lr_status lr_step_paged(const void *q, const lr_paged *cache, const int *lens, void *o, int N,
                         int Hq, int Hk, int d, int max_len, int window, int sinks, float scale,
