@@ -88,9 +88,11 @@ typedef struct {
  *     (a', b') = (a cos th - b sin th, b cos th + a sin th),  th = p inv_freq[i],
  *                for the rot/2 channel pairs (a, b) of y; other channels pass
  *
- * for each query and key head.  Angles are formed from the product taken
- * modulo a full turn in 64-bit fixed point, so they stay accurate to fp32 at
- * every position an int holds and every frequency up to 2^50.
+ * for each query and key head.  Squares are summed in fp32: a head whose
+ * values pass 1.8e19 has a norm beyond it and comes out as zeros.  Angles are
+ * formed from the product taken modulo a full turn in 64-bit fixed point, so
+ * they stay accurate to fp32 at every position an int holds and every frequency
+ * up to 2^50.
  *
  *   q, qs      [B, Hq, T, d] with strides qs
  *   k, ks      [B, Hk, T, d] with strides ks
