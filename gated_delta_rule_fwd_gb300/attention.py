@@ -3,6 +3,8 @@
     lr_qk_norm_rope(q, k, positions, ...) -> (q_out, k_out)
         RMS norm of every query and key head and the position rotation in one
         pass, with an optional write of keys and values into a paged cache
+    lr_qk_norm_rope_axes(q, k, positions, axis, places, ...) -> (q_out, k_out)
+        the same with positions of several axes
     lr_fwd_window(q, k, v, window=..., sinks=...) -> o
         causal attention over whole sequences with a sliding window and sinks
     lr_step_paged(q, k_cache, v_cache, table, lens, ...) -> o
@@ -21,7 +23,8 @@ NO_WINDOW = (1 << 31) - 1   # a window that hides nothing
 QK_NORM = 0x1
 QK_INTERLEAVED = 0x2
 QK_ZERO_Q, QK_ZERO_K = 0x8, 0x10
-ATTN_SYMBOLS = ("lr_qk_norm_rope", "lr_fwd_window", "lr_step_paged", "lr_step_paged_fill",
+MAX_AXES = 16               # LR_MAX_AXES
+ATTN_SYMBOLS = ("lr_qk_norm_rope", "lr_qk_norm_rope_axes", "lr_fwd_window", "lr_step_paged", "lr_step_paged_fill",
                 "lr_step_paged_workspace_size")
 
 
@@ -52,6 +55,9 @@ def declare(L):
     L.lr_qk_norm_rope.restype = i
     L.lr_qk_norm_rope.argtypes = [vp, Strides, vp, Strides, vp, ctypes.POINTER(QkMaps), vp, vp, vp,
                                   Strides, ctypes.POINTER(Paged)] + [i] * 6 + [vp]
+    L.lr_qk_norm_rope_axes.restype = i
+    L.lr_qk_norm_rope_axes.argtypes = [vp, Strides, vp, Strides, vp, vp, i, vp, ctypes.POINTER(QkMaps),
+                                       vp, vp, vp, Strides, ctypes.POINTER(Paged)] + [i] * 6 + [vp]
     L.lr_fwd_window.restype = i
     L.lr_fwd_window.argtypes = ([vp, Strides] * 3 + [vp, vp, vp, Strides] + [i] * 8 + [f, i, vp])
     for step in (L.lr_step_paged, L.lr_step_paged_fill):
@@ -148,6 +154,41 @@ def lr_qk_norm_rope(q, k, positions=None, *, norm=True, q_weight=None, k_weight=
                                    eps=eps, inv_freq=inv_freq, interleaved=interleaved, v=v,
                                    k_cache=k_cache, v_cache=v_cache, table=table, write_k=write_k,
                                    q_out=q_out, k_out=k_out)
+    return _norm_rope(torch, base, q, k, positions, None, None, norm, q_weight, k_weight, eps, inv_freq,
+                      interleaved, v, k_cache, v_cache, table, write_k, q_out, k_out)
+
+
+def lr_qk_norm_rope_axes(q, k, positions, axis, places=None, *, norm=True, q_weight=None, k_weight=None,
+                         eps=1e-6, inv_freq=None, interleaved=False, v=None, k_cache=None, v_cache=None,
+                         table=None, write_k=True, q_out=None, k_out=None, stream=None):
+    """Norm and rotation by positions of several axes (``lr_qk_norm_rope_axes`` in
+    include/lr_attn.h).
+
+    positions: [axes,B,T] int32, e.g. time, height and width of every token;
+    axis: [rot/2] int32, the axis of each frequency's channel pair (in runs or
+    in turn, as the model has it); places: [B,T] int32 rows of the tokens in
+    their sequence's cache (negative: padding, left out) or None for 0..T-1.
+    The other arguments and the results are those of :func:`lr_qk_norm_rope`."""
+    import torch
+    base = _base()
+    dev = q.device
+    base._require_cuda(dev)
+    if stream is not None or torch.cuda.current_device() != dev.index:
+        with _place(torch, stream, dev):
+            return lr_qk_norm_rope_axes(q, k, positions, axis, places, norm=norm, q_weight=q_weight,
+                                        k_weight=k_weight, eps=eps, inv_freq=inv_freq, interleaved=interleaved,
+                                        v=v, k_cache=k_cache, v_cache=v_cache, table=table, write_k=write_k,
+                                        q_out=q_out, k_out=k_out)
+    if positions is None or axis is None:
+        raise ValueError("positions and axis are required")
+    return _norm_rope(torch, base, q, k, places, positions, axis, norm, q_weight, k_weight, eps, inv_freq,
+                      interleaved, v, k_cache, v_cache, table, write_k, q_out, k_out)
+
+
+def _norm_rope(torch, base, q, k, places, positions, axis, norm, q_weight, k_weight, eps, inv_freq, interleaved,
+               v, k_cache, v_cache, table, write_k, q_out, k_out):
+    """Either norm and rotation; without ``axis`` the places are the positions."""
+    dev = q.device
     if q.dim() != 4 or k.dim() != 4:
         raise ValueError("q and k must have shape (B, heads, T, d)")
     q_shape, k_shape, dtype = q.shape, k.shape, q.dtype
@@ -156,8 +197,8 @@ def lr_qk_norm_rope(q, k, positions=None, *, norm=True, q_weight=None, k_weight=
     dt = base._dtype_code(q)
     qs = _strided(q, "q", q_shape, dtype, dev)
     ks = _strided(k, "k", (B, Hk, T, d), dtype, dev)
-    if positions is not None:
-        _want(positions, "positions", (B, T), torch.int32, dev)
+    if places is not None:
+        _want(places, "positions" if axis is None else "places", (B, T), torch.int32, dev)
     if q_weight is not None:
         _want(q_weight, "q_weight", (d,), torch.float32, dev)
     if k_weight is not None:
@@ -166,6 +207,12 @@ def lr_qk_norm_rope(q, k, positions=None, *, norm=True, q_weight=None, k_weight=
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
         _want(inv_freq, "inv_freq", (rot // 2,), torch.float64, dev)
+    if axis is not None:
+        axes = positions.shape[0] if positions.dim() == 3 else 0
+        if not 1 <= axes <= MAX_AXES:
+            raise ValueError(f"positions must have shape (1 to {MAX_AXES}, {B}, {T}), got {tuple(positions.shape)}")
+        _want(positions, "positions", (axes, B, T), torch.int32, dev)
+        _want(axis, "axis", (rot // 2,), torch.int32, dev)
     cache, vs = None, _NO_STRIDES
     if k_cache is not None or v_cache is not None or table is not None or v is not None:
         if k_cache is None or v_cache is None or table is None or v is None:
@@ -183,7 +230,7 @@ def lr_qk_norm_rope(q, k, positions=None, *, norm=True, q_weight=None, k_weight=
             raise ValueError("k_out given with write_k=False")
         _want(k_out, "k_out", k_shape, dtype, dev)
     flags = (QK_NORM if norm else 0) | (QK_INTERLEAVED if interleaved else 0)
-    if positions is not None:
+    if places is not None:
         flags |= (QK_ZERO_Q if q_out is None else 0) | (QK_ZERO_K if k_out is None else 0)
     maps = QkMaps(flags,
                   None if q_weight is None else q_weight.data_ptr(),
@@ -193,12 +240,17 @@ def lr_qk_norm_rope(q, k, positions=None, *, norm=True, q_weight=None, k_weight=
         q_out = torch.empty(q_shape, dtype=dtype, device=dev)
     if k_out is None and write_k:
         k_out = torch.empty(k_shape, dtype=dtype, device=dev)
-    st = base.lib().lr_qk_norm_rope(
-        q.data_ptr(), qs, k.data_ptr(), ks, None if positions is None else positions.data_ptr(),
-        maps, q_out.data_ptr(), None if k_out is None else k_out.data_ptr(),
-        None if v is None else v.data_ptr(), vs, cache, B, T, Hq, Hk, d, dt, _handle(torch, dev))
+    L, turns = base.lib(), ()
+    if axis is None:
+        name, call = "lr_qk_norm_rope", L.lr_qk_norm_rope
+    else:
+        name, call = "lr_qk_norm_rope_axes", L.lr_qk_norm_rope_axes
+        turns = (positions.data_ptr(), axis.data_ptr(), axes)
+    st = call(q.data_ptr(), qs, k.data_ptr(), ks, *turns, None if places is None else places.data_ptr(),
+              maps, q_out.data_ptr(), None if k_out is None else k_out.data_ptr(),
+              None if v is None else v.data_ptr(), vs, cache, B, T, Hq, Hk, d, dt, _handle(torch, dev))
     if st != 0:
-        raise base.LrError(st, "lr_qk_norm_rope")
+        raise base.LrError(st, name)
     return q_out, k_out
 
 

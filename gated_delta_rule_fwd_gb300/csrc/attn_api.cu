@@ -163,14 +163,11 @@ lr_status step_paged(const void *q, const lr_paged *cache, const int *lens, void
     return done(launch_step_paged(a, d, dt, workspace, stream));
 }
 
-}  // namespace
-
-extern "C" {
-
-lr_status lr_qk_norm_rope(const void *q, lr_strides qs, const void *k, lr_strides ks,
-                          const int *positions, const lr_qk_maps *maps, void *q_out, void *k_out,
-                          const void *v, lr_strides vs, const lr_paged *cache, int B, int T,
-                          int Hq, int Hk, int d, lr_dtype dt, cudaStream_t stream) {
+// axes.count 0: positions of one axis; else `positions` are the tokens' places.
+lr_status qk_norm_rope(const void *q, lr_strides qs, const void *k, lr_strides ks,
+                       const int *positions, const QkAxes &axes, const lr_qk_maps *maps, void *q_out,
+                       void *k_out, const void *v, lr_strides vs, const lr_paged *cache, int B, int T,
+                       int Hq, int Hk, int d, lr_dtype dt, cudaStream_t stream) {
     lr_status st = check_types(d, dt);
     if (st != LR_OK) return st;
     if (B < 1 || T < 0 || Hq < 1 || Hk < 1) return LR_ERR_SHAPE;
@@ -185,6 +182,8 @@ lr_status lr_qk_norm_rope(const void *q, lr_strides qs, const void *k, lr_stride
     if (norm && !(maps->eps >= 0.f && maps->eps <= 3.4e38f)) return LR_ERR_FUSE;
     if (maps->rot < 0 || maps->rot > d || maps->rot % 16) return LR_ERR_UNSUPPORTED;
     if (maps->rot && !maps->inv_freq) return LR_ERR_NULL;
+    const bool turned = axes.count && maps->rot;  // by several axes
+    if (turned && !axes.axis) return LR_ERR_NULL;
     Span ck, cv, ct;
     if (cache) {
         st = check_paged(cache, B, Hk, d, dt, &ck, &cv, &ct);
@@ -192,12 +191,14 @@ lr_status lr_qk_norm_rope(const void *q, lr_strides qs, const void *k, lr_stride
     }
     if (T == 0) return LR_OK;
     if (!q || !k || !q_out || (!k_out && !cache) || (cache && !v)) return LR_ERR_NULL;
+    if (turned && !axes.positions) return LR_ERR_NULL;
     if (!cache) v = nullptr;
     for (const void *p : {q, k, v, (const void *)q_out, (const void *)k_out,
                           (const void *)maps->inv_freq, (const void *)maps->q_weight,
                           (const void *)maps->k_weight})
         if (!aligned16(p)) return LR_ERR_ALIGN;
     if (!aligned4(positions)) return LR_ERR_ALIGN;
+    if (turned && (!aligned4(axes.positions) || !aligned4(axes.axis))) return LR_ERR_ALIGN;
     if ((st = check_strides(&qs, B, Hq, T, dt)) != LR_OK) return st;
     if ((st = check_strides(&ks, B, Hk, T, dt)) != LR_OK) return st;
     if (cache && (st = check_strides(&vs, B, Hk, T, dt)) != LR_OK) return st;
@@ -210,6 +211,8 @@ lr_status lr_qk_norm_rope(const void *q, lr_strides qs, const void *k, lr_stride
                        span(maps->rot ? maps->inv_freq : nullptr, (size_t)maps->rot / 2 * 8),
                        span(norm ? maps->q_weight : nullptr, (size_t)d * 4),
                        span(norm ? maps->k_weight : nullptr, (size_t)d * 4),
+                       span(turned ? axes.positions : nullptr, (size_t)axes.count * rows * 4),
+                       span(turned ? axes.axis : nullptr, (size_t)maps->rot / 2 * 4),
                        ct};
     const Span out[] = {span(q_out, rows * Hq * d * es), span(k_out, rows * Hk * d * es), ck, cv};
     for (int a = 0; a < 4; ++a) {
@@ -225,8 +228,30 @@ lr_status lr_qk_norm_rope(const void *q, lr_strides qs, const void *k, lr_stride
     m.eps = maps->eps;
     m.rot = maps->rot;
     m.flags = maps->flags;
-    return done(launch_qk_norm_rope(q, qs, k, ks, positions, m, q_out, k_out, v, vs, cache, B, T,
+    return done(launch_qk_norm_rope(q, qs, k, ks, positions, axes, m, q_out, k_out, v, vs, cache, B, T,
                                     Hq, Hk, d, dt, stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+lr_status lr_qk_norm_rope(const void *q, lr_strides qs, const void *k, lr_strides ks,
+                          const int *positions, const lr_qk_maps *maps, void *q_out, void *k_out,
+                          const void *v, lr_strides vs, const lr_paged *cache, int B, int T,
+                          int Hq, int Hk, int d, lr_dtype dt, cudaStream_t stream) {
+    return qk_norm_rope(q, qs, k, ks, positions, QkAxes{nullptr, nullptr, 0}, maps, q_out, k_out, v, vs,
+                        cache, B, T, Hq, Hk, d, dt, stream);
+}
+
+lr_status lr_qk_norm_rope_axes(const void *q, lr_strides qs, const void *k, lr_strides ks,
+                               const int *positions, const int *axis, int axes, const int *places,
+                               const lr_qk_maps *maps, void *q_out, void *k_out, const void *v,
+                               lr_strides vs, const lr_paged *cache, int B, int T, int Hq, int Hk,
+                               int d, lr_dtype dt, cudaStream_t stream) {
+    if (axes < 1 || axes > LR_MAX_AXES) return LR_ERR_SHAPE;
+    return qk_norm_rope(q, qs, k, ks, places, QkAxes{positions, axis, axes}, maps, q_out, k_out, v, vs,
+                        cache, B, T, Hq, Hk, d, dt, stream);
 }
 
 lr_status lr_fwd_window(const void *q, lr_strides qs, const void *k, lr_strides ks, const void *v,

@@ -103,11 +103,20 @@ struct QkMaps {
     unsigned flags;
 };
 
+// Positions of several axes, [count][B][T], and the axis of each channel pair;
+// count 0: one axis.
+struct QkAxes {
+    const int *positions, *axis;
+    int count;
+};
+
 // ------------------------------------------------------------------ launchers
+// positions: of the tokens (one axis), or their places in the cache.
 cudaError_t launch_qk_norm_rope(const void *q, lr_strides qs, const void *k, lr_strides ks,
-                                const int *positions, const QkMaps &maps, void *q_out, void *k_out,
-                                const void *v, lr_strides vs, const lr_paged *cache, int B, int T,
-                                int Hq, int Hk, int d, lr_dtype dt, cudaStream_t stream);
+                                const int *positions, const QkAxes &axes, const QkMaps &maps,
+                                void *q_out, void *k_out, const void *v, lr_strides vs,
+                                const lr_paged *cache, int B, int T, int Hq, int Hk, int d,
+                                lr_dtype dt, cudaStream_t stream);
 
 constexpr int kMostCluster = 8;  // CTAs of the largest cluster that is always allowed
 // CTAs of clusters of 1, 2, .. 8 that find room on the GPU at once with one to

@@ -1,5 +1,6 @@
-// lr_qk_norm_rope: RMS norm of each query and key head, the position rotation
-// and the write of keys and values into a paged cache, in one pass.
+// lr_qk_norm_rope and lr_qk_norm_rope_axes: RMS norm of each query and key head,
+// the position rotation and the write of keys and values into a paged cache, in
+// one pass.
 //
 // A row (one head of one token) is held by d / 8 lanes of a warp, eight
 // channels each, so that its sum of squares and the partner channels of the
@@ -40,6 +41,8 @@ struct RopeArgs {
     const void *q, *k, *v;
     void *qo, *ko, *ck, *cv;
     const int *positions, *table;
+    const int *turns, *axis;  // several axes: positions [axes][B][T] and the axis of each
+    int axes;                 // channel pair; `positions` then are places in the cache
     lr_strides qs, ks, vs;
     QkMaps maps;
     int T, Hq, Hk, num_pages, page_log2, max_pages;
@@ -85,11 +88,13 @@ __device__ __forceinline__ void put(__nv_bfloat16 *p, const Row8<__nv_bfloat16> 
 
 enum Rotation { kNone, kHalves, kPairs };  // channels (i, i + rot/2) or (2i, 2i+1)
 
-template <typename E, int D, Rotation ROT>
+// AXES: the angles come from positions of several axes.
+template <typename E, int D, Rotation ROT, bool AXES>
 __global__ void __launch_bounds__(NT, kCtas<E>) qk_norm_rope_kernel(RopeArgs a) {
     constexpr int LANES = D / 8;      // lanes of a row
     constexpr int ROWS = NT / LANES;  // rows at once: tokens x head parts
     __shared__ unsigned long long step[D / 2];
+    __shared__ const int *along[AXES ? D / 2 : 1];  // positions of the pair's axis
     const int tid = threadIdx.x, half = a.maps.rot >> 1;
     const bool norm = a.maps.flags & LR_QK_NORM, partial = a.maps.rot < D;
     // the lane's place: channels c0.., token `mine` of the group, every parts-th head
@@ -107,6 +112,14 @@ __global__ void __launch_bounds__(NT, kCtas<E>) qk_norm_rope_kernel(RopeArgs a) 
             const double rest = fma(f, kLow, fma(f, kHigh, -turns));
             step[tid] = __double2ull_rz((turns - floor(turns)) * 0x1p64) +
                         (unsigned long long)__double2ll_rn(rest * 0x1p64);
+            if (AXES) {
+                int axis = a.axis[tid];
+                if (axis < 0 || axis >= a.axes) {
+                    atomicOr(&g_rope_error, kAttnIndex);
+                    axis = 0;
+                }
+                along[tid] = a.turns + (size_t)axis * a.total;
+            }
         }
         __syncthreads();
     }
@@ -156,7 +169,8 @@ __global__ void __launch_bounds__(NT, kCtas<E>) qk_norm_rope_kernel(RopeArgs a) 
 #pragma unroll
             for (int i = 0; i < N; ++i) {
                 const int c = ROT == kPairs ? (c0 >> 1) + i : (low ? c0 + i : c0 - half + 4 + i);
-                const unsigned long long phase = step[c] * (unsigned long long)(long long)p;
+                const int at = AXES ? along[c][n] : p;
+                const unsigned long long phase = step[c] * (unsigned long long)(long long)at;
                 // signed half turns in [-1, 1)
                 const float x = (float)(int)(phase >> 32) * 4.656612873077392578125e-10f;  // 2^-31
                 sincospif(x, &s4[i], &c4[i]);
@@ -293,9 +307,12 @@ cudaError_t launch(RopeArgs &a, cudaStream_t stream) {
     const int groups = (a.total + a.tokens - 1) / a.tokens;
     const int most = 152 * kCtas<E>;
     const int grid = groups < most ? groups : most;
-    if (a.maps.rot == 0) qk_norm_rope_kernel<E, D, kNone><<<grid, NT, 0, stream>>>(a);
-    else if (a.maps.flags & LR_QK_INTERLEAVED) qk_norm_rope_kernel<E, D, kPairs><<<grid, NT, 0, stream>>>(a);
-    else qk_norm_rope_kernel<E, D, kHalves><<<grid, NT, 0, stream>>>(a);
+    const bool pairs = a.maps.flags & LR_QK_INTERLEAVED;
+    if (a.maps.rot == 0) qk_norm_rope_kernel<E, D, kNone, false><<<grid, NT, 0, stream>>>(a);
+    else if (a.axes && pairs) qk_norm_rope_kernel<E, D, kPairs, true><<<grid, NT, 0, stream>>>(a);
+    else if (a.axes) qk_norm_rope_kernel<E, D, kHalves, true><<<grid, NT, 0, stream>>>(a);
+    else if (pairs) qk_norm_rope_kernel<E, D, kPairs, false><<<grid, NT, 0, stream>>>(a);
+    else qk_norm_rope_kernel<E, D, kHalves, false><<<grid, NT, 0, stream>>>(a);
     return cudaGetLastError();
 }
 
@@ -309,10 +326,12 @@ cudaError_t launch_d(RopeArgs &a, int d, cudaStream_t stream) {
 }  // namespace
 
 cudaError_t launch_qk_norm_rope(const void *q, lr_strides qs, const void *k, lr_strides ks,
-                                const int *positions, const QkMaps &maps, void *q_out, void *k_out,
-                                const void *v, lr_strides vs, const lr_paged *cache, int B, int T,
-                                int Hq, int Hk, int d, lr_dtype dt, cudaStream_t stream) {
+                                const int *positions, const QkAxes &axes, const QkMaps &maps,
+                                void *q_out, void *k_out, const void *v, lr_strides vs,
+                                const lr_paged *cache, int B, int T, int Hq, int Hk, int d,
+                                lr_dtype dt, cudaStream_t stream) {
     RopeArgs a{};
+    a.turns = axes.positions, a.axis = axes.axis, a.axes = axes.count;
     a.q = q, a.k = k, a.v = v, a.qo = q_out, a.ko = k_out;
     a.positions = positions;
     a.qs = qs, a.ks = ks, a.vs = vs;

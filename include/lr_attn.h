@@ -5,6 +5,8 @@
  *   lr_qk_norm_rope   RMS norm of every query and key head and the position
  *                     rotation in one pass, with an optional write of keys
  *                     and values into a paged cache
+ *   lr_qk_norm_rope_axes  the same with positions of several axes (time, height,
+ *                     width), as prompts with images and video have them
  *   lr_fwd_window     causal attention over whole sequences, limited to a
  *                     sliding window and a few first tokens (sinks)
  *   lr_step_paged     the same attention for one new token per sequence over
@@ -114,6 +116,28 @@ lr_status lr_qk_norm_rope(const void *q, lr_strides qs, const void *k, lr_stride
                           const int *positions, const lr_qk_maps *maps, void *q_out, void *k_out,
                           const void *v, lr_strides vs, const lr_paged *cache, int B, int T,
                           int Hq, int Hk, int d, lr_dtype dt, cudaStream_t stream);
+
+#define LR_MAX_AXES 16
+
+/*
+ * lr_qk_norm_rope with positions of several axes: channel pair i of a token is
+ * turned by th = positions[axis[i]][b][t] inv_freq[i].  Where a token's keys go
+ * in the cache is a matter of its place in the sequence, not of its positions:
+ *
+ *   positions  [axes, B, T] int32, any values; 1 <= axes <= LR_MAX_AXES
+ *   axis       [rot / 2] int32, 0..axes-1 (others count as 0 and are reported
+ *              as LR_ERR_INDEX); positions and axis are not read where rot is 0
+ *   places     [B, T] int32, the cache row of the token, or NULL for t.  A
+ *              negative place marks padding, as a negative position does there.
+ *
+ * All else is as for lr_qk_norm_rope.  The places of a sequence in one call are
+ * distinct.
+ */
+lr_status lr_qk_norm_rope_axes(const void *q, lr_strides qs, const void *k, lr_strides ks,
+                               const int *positions, const int *axis, int axes, const int *places,
+                               const lr_qk_maps *maps, void *q_out, void *k_out, const void *v,
+                               lr_strides vs, const lr_paged *cache, int B, int T, int Hq, int Hk,
+                               int d, lr_dtype dt, cudaStream_t stream);
 
 /*
  * Causal attention with a sliding window and sinks.  Query row i of sequence

@@ -1,5 +1,5 @@
 """fp64 definition of the attention operators (numpy): the norm and rotation
-of queries and keys, attention with a sliding window and sinks, and its step
+of queries and keys (by positions of one axis or several), attention with a sliding window and sinks, and its step
 over a paged cache.  Test infrastructure; no code shared with the library.
 """
 from __future__ import annotations
@@ -29,6 +29,24 @@ def qk_norm_rope(x, positions, weight=None, eps=None, inv_freq=None, interleaved
             u, w = y[..., a].copy(), y[..., b].copy()
             y[..., a], y[..., b] = u * c - w * s, w * c + u * s
             size[..., a] = size[..., b] = np.abs(u) + np.abs(w)
+    return y, size
+
+
+def qk_norm_rope_axes(x, positions, axis, weight=None, eps=None, inv_freq=None, interleaved=False):
+    """The same with positions [axes,B,T] and the axis of each pair [rot/2]."""
+    x = np.asarray(x, np.float64)
+    y, size = qk_norm_rope(x, np.zeros(np.asarray(positions).shape[1:]), weight, eps)
+    if inv_freq is None:
+        return y, size
+    half = len(inv_freq)
+    z, y = y, y.copy()
+    for i in range(half):
+        a, b = (2 * i, 2 * i + 1) if interleaved else (i, i + half)
+        th = np.asarray(positions, np.float64)[axis[i]][:, None, :] * float(inv_freq[i])
+        # the pair as one complex number, turned
+        turned = (z[..., a] + 1j * z[..., b]) * np.exp(1j * th)
+        y[..., a], y[..., b] = turned.real, turned.imag
+        size[..., a] = size[..., b] = np.abs(z[..., a]) + np.abs(z[..., b])
     return y, size
 
 

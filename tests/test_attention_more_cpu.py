@@ -1,0 +1,119 @@
+"""CPU-side checks of the rotation by several axes: refusals before any launch
+and the binding's checks."""
+import os
+import subprocess
+import sys
+
+import pytest
+import torch
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+_START = r"""
+import ctypes, sys
+sys.path.insert(0, sys.argv[1])
+import gated_delta_rule_fwd_gb300 as lr
+from gated_delta_rule_fwd_gb300.attention import Strides, Paged, QkMaps
+L = lr.lib()
+A = [0x10000000 * (i + 1) for i in range(16)]   # distinct, aligned, never dereferenced
+P = lambda a: None if a is None else ctypes.c_void_p(a)
+def contig(H, T, d): return (H * T * d, T * d, d)
+inf, nan = float('inf'), float('nan')
+"""
+_END = r"""
+bad = [(n, got, want) for n, got, want in cases if got != want]
+print("BAD", bad)
+sys.exit(1 if bad else 0)
+"""
+
+_AXES = r"""
+def axes(**kw):
+    a = dict(q=A[0], k=A[1], pos=A[2], qo=A[3], ko=A[4], v=A[5], ck=A[6], cv=A[7], tab=A[8], qw=A[9], kw=A[10],
+             f=A[11], axis=A[12], places=A[13], axes=3, flags=1, eps=1e-6, rot=32, pages=4, page=16, most=4,
+             B=2, T=5, Hq=4, Hk=2, d=64, dt=1, cache=True, maps=True, qs=None, ks=None, vs=None)
+    a.update(kw)
+    S = lambda s, H: Strides(*(s or contig(H, max(a['T'], 1), a['d'])))
+    m = QkMaps(a['flags'], a['qw'], a['kw'], a['eps'], a['rot'], a['f'])
+    c = Paged(a['ck'], a['cv'], a['tab'], a['pages'], a['page'], a['most'])
+    return L.lr_qk_norm_rope_axes(P(a['q']), S(a['qs'], a['Hq']), P(a['k']), S(a['ks'], a['Hk']), P(a['pos']),
+                                  P(a['axis']), a['axes'], P(a['places']), ctypes.byref(m) if a['maps'] else None,
+                                  P(a['qo']), P(a['ko']), P(a['v']), S(a['vs'], a['Hk']),
+                                  ctypes.byref(c) if a['cache'] else None, a['B'], a['T'], a['Hq'], a['Hk'],
+                                  a['d'], a['dt'], None)
+cases = [
+    ("ok", axes(), 7), ("nocache-ok", axes(cache=False, v=None), 7), ("places-null-ok", axes(places=None), 7),
+    ("T0", axes(T=0, q=None), 0), ("axes0", axes(axes=0), 2), ("axes-neg", axes(axes=-3), 2),
+    ("axes16-ok", axes(axes=16), 7), ("axes17", axes(axes=17), 2),
+    ("null-axis", axes(axis=None), 1), ("null-pos", axes(pos=None), 1), ("no-rotation-ok", axes(axis=None, pos=None, f=None, rot=0), 7),
+    ("align-axis", axes(axis=A[12] + 2), 4), ("align-axis-ok", axes(axis=A[12] + 4), 7), ("align-pos", axes(pos=A[2] + 1), 4),
+    ("align-places", axes(places=A[13] + 2), 4),
+    ("alias-axis", axes(qo=A[12]), 8), ("alias-pos", axes(ko=A[2]), 8),
+    # the last axis's positions, 2 x 5 x 4 bytes an axis
+    ("alias-pos-last", axes(ko=A[2] + 112), 8), ("alias-pos-behind-ok", axes(ko=A[2] + 128), 7),
+    ("alias-places", axes(qo=A[13]), 8), ("alias-unused-axis", axes(qo=A[12], rot=0), 7),
+    ("dtype", axes(dt=2), 3), ("d48", axes(d=48), 6), ("flag", axes(flags=4), 12), ("rot-odd", axes(rot=24), 6),
+    ("null-maps", axes(maps=False), 1), ("null-freq", axes(f=None), 1), ("null-v", axes(v=None), 1),
+    ("page", axes(page=24), 6), ("stride-odd", axes(qs=(1280, 320, 68)), 4), ("alias-qo-q", axes(qo=A[0]), 8),
+]
+"""
+
+
+def _child(body):
+    from gated_delta_rule_fwd_gb300.build import build
+    build()
+    env = dict(os.environ, CUDA_VISIBLE_DEVICES="")
+    r = subprocess.run([sys.executable, "-c", _START + body + _END, ROOT], env=env, capture_output=True, text=True,
+                       timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_axes_arguments_rejected_before_launch():
+    """In a child without a GPU: a call that passes validation then fails at
+    its launch (LR_ERR_CUDA, 7)."""
+    _child(_AXES)
+
+
+class _NoLaunch:
+    def __getattr__(self, name):
+        raise AssertionError(f"the binding reached the library ({name}) with invalid arguments")
+
+
+@pytest.fixture
+def lr(monkeypatch):
+    import gated_delta_rule_fwd_gb300 as lr
+    monkeypatch.setattr(lr, "_require_cuda", lambda dev: None)   # CPU tensors stand in
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    monkeypatch.setattr(lr, "lib", lambda: _NoLaunch())
+    return lr
+
+
+def _t(*shape, dtype=torch.bfloat16):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def _i(*shape, dtype=torch.int32):
+    return torch.zeros(*shape, dtype=dtype)
+
+
+def _axes_args(**change):
+    a = dict(q=_t(2, 4, 9, 64), k=_t(2, 2, 9, 64), positions=_i(3, 2, 9), axis=_i(32), places=_i(2, 9),
+             inv_freq=torch.zeros(32, dtype=torch.float64))
+    a.update(change)
+    return a
+
+
+def test_axes_binding_accepts_what_it_should(lr):
+    for change in (dict(), dict(places=None), dict(positions=_i(1, 2, 9)), dict(inv_freq=None, axis=_i(0))):
+        with pytest.raises(AssertionError, match="lr_qk_norm_rope_axes"):
+            lr.lr_qk_norm_rope_axes(**_axes_args(**change))
+
+
+@pytest.mark.parametrize("change", [
+    dict(positions=None), dict(axis=None), dict(positions=_i(2, 9)), dict(positions=_i(3, 2, 8)),
+    dict(positions=_i(17, 2, 9)), dict(positions=_i(0, 2, 9)), dict(positions=_i(3, 2, 9, dtype=torch.int64)),
+    dict(positions=_i(2, 9, 3).permute(2, 0, 1)), dict(axis=_i(31)), dict(axis=_i(32, dtype=torch.int64)),
+    dict(axis=_i(64)[::2]), dict(places=_i(9)), dict(places=_i(2, 9, dtype=torch.int64)), dict(inv_freq=None),
+    dict(v=_t(2, 2, 9, 64)), dict(write_k=False), dict(k=_t(2, 2, 8, 64))], ids=lambda c: "-".join(c))
+def test_axes_binding_refuses(lr, change):
+    with pytest.raises((ValueError, TypeError)):
+        lr.lr_qk_norm_rope_axes(**_axes_args(**change))
