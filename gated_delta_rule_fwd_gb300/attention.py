@@ -9,6 +9,8 @@
         causal attention over whole sequences with a sliding window and sinks
     lr_step_paged(q, k_cache, v_cache, table, lens, ...) -> o
         the same attention for one new token per sequence over the cache
+    lr_fwd_diff(q, k, v, lam, ...) -> o
+        differential attention over whole sequences
 
 Like the rest of the package this only marshals arguments; the functions are
 offered by the package itself.  Tensors may be on any device: the calls run
@@ -23,9 +25,10 @@ NO_WINDOW = (1 << 31) - 1   # a window that hides nothing
 QK_NORM = 0x1
 QK_INTERLEAVED = 0x2
 QK_ZERO_Q, QK_ZERO_K = 0x8, 0x10
+DIFF_NORM = 0x1
 MAX_AXES = 16               # LR_MAX_AXES
 ATTN_SYMBOLS = ("lr_qk_norm_rope", "lr_qk_norm_rope_axes", "lr_fwd_window", "lr_step_paged", "lr_step_paged_fill",
-                "lr_step_paged_workspace_size")
+                "lr_step_paged_workspace_size", "lr_fwd_diff", "lr_fwd_diff_workspace_size")
 
 
 class Strides(ctypes.Structure):
@@ -46,6 +49,12 @@ class QkMaps(ctypes.Structure):
                 ("inv_freq", ctypes.c_void_p)]
 
 
+class DiffMaps(ctypes.Structure):
+    """lr_diff_maps (include/lr_attn.h)."""
+    _fields_ = [("flags", ctypes.c_uint), ("lam", ctypes.c_void_p), ("weight", ctypes.c_void_p),
+                ("eps", ctypes.c_float)]
+
+
 _NO_STRIDES = Strides(0, 0, 0)
 
 
@@ -60,6 +69,11 @@ def declare(L):
                                        vp, vp, vp, Strides, ctypes.POINTER(Paged)] + [i] * 6 + [vp]
     L.lr_fwd_window.restype = i
     L.lr_fwd_window.argtypes = ([vp, Strides] * 3 + [vp, vp, vp, Strides] + [i] * 8 + [f, i, vp])
+    L.lr_fwd_diff.restype = i
+    L.lr_fwd_diff.argtypes = ([vp, Strides] * 3 + [vp, vp, ctypes.POINTER(DiffMaps), vp, Strides] + [i] * 8 +
+                              [f, i, vp, sz, vp])
+    L.lr_fwd_diff_workspace_size.restype = sz
+    L.lr_fwd_diff_workspace_size.argtypes = [i] * 7
     for step in (L.lr_step_paged, L.lr_step_paged_fill):
         step.restype = i
         step.argtypes = ([vp, ctypes.POINTER(Paged), vp, vp] + [i] * 7 + [f, i, vp, sz, vp])
@@ -300,6 +314,97 @@ def lr_fwd_window(q, k, v, *, window=None, sinks=0, q_len=None, k_len=None, scal
         o.data_ptr(), os_, B, Hq, Hk, Tq, Tk, d, window, sinks, scale, dt, _handle(torch, dev))
     if st != 0:
         raise base.LrError(st, "lr_fwd_window")
+    return o
+
+
+def _diff_maps(torch, lam, norm, norm_weight, eps, H, d, dev):
+    """lr_diff_maps of H pairs of heads."""
+    _want(lam, "lam", (H,), torch.float32, dev)
+    if norm_weight is not None:
+        if not norm:
+            raise ValueError("norm_weight given with norm=False")
+        _want(norm_weight, "norm_weight", (2 * d,), torch.float32, dev)
+    return DiffMaps(DIFF_NORM if norm else 0, lam.data_ptr(),
+                    None if norm_weight is None else norm_weight.data_ptr(), float(eps))
+
+
+def _scratch(torch, workspace, need, dev):
+    """A call's workspace, the given one or one made here: its holder, address and size."""
+    if workspace is None:
+        if need == 0:
+            return None, None, 0
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    elif workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {dev}")
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+@functools.lru_cache(maxsize=1024)
+def _diff_workspace(B, H, Hk, Tq, Tk, d, dt):
+    """lr_fwd_diff_workspace_size, a function of the sizes alone."""
+    return int(_base().lib().lr_fwd_diff_workspace_size(B, H, Hk, Tq, Tk, d, dt))
+
+
+def diff_workspace_size(B, H, Hk, Tq, Tk, d, dtype) -> int:
+    """lr_fwd_diff_workspace_size for these sizes (H and Hk pairs of heads; dtype: torch dtype)."""
+    import torch
+    base = _base()
+    return _diff_workspace(B, H, Hk, Tq, Tk, d, base.F32 if dtype == torch.float32 else base.BF16)
+
+
+def lr_fwd_diff(q, k, v, lam, *, window=None, sinks=0, q_len=None, k_len=None, scale=None, norm=True,
+                norm_weight=None, eps=1e-6, o=None, workspace=None, stream=None):
+    """Differential attention over whole sequences (``lr_fwd_diff`` in
+    include/lr_attn.h).
+
+    q: [B,2H,Tq,d]; k, v: [B,2Hk,Tk,d] (float32 or bfloat16), any strides with
+    contiguous channels; H a multiple of Hk.  Heads 2h and 2h+1 of q and k are
+    the two maps of pair h; those of v and o are the halves of its 2d value
+    channels.  lam: [H] float32, the second map's factor.  ``norm``: the
+    root-mean-square norm of every pair's row, times norm_weight ([2d] float32 or
+    None for ones; a factor 1 - lambda_init belongs into it).  window, sinks,
+    q_len, k_len, scale and ``o`` as for :func:`lr_fwd_window`.  ``workspace`` is
+    a uint8 CUDA tensor of at least ``diff_workspace_size(...)`` bytes, allocated
+    here when None.  Returns o: [B,2H,Tq,d]."""
+    import torch
+    base = _base()
+    dev = q.device
+    base._require_cuda(dev)
+    if stream is not None or torch.cuda.current_device() != dev.index:
+        with _place(torch, stream, dev):
+            return lr_fwd_diff(q, k, v, lam, window=window, sinks=sinks, q_len=q_len, k_len=k_len, scale=scale,
+                               norm=norm, norm_weight=norm_weight, eps=eps, o=o, workspace=workspace)
+    if q.dim() != 4 or k.dim() != 4:
+        raise ValueError("q, k and v must have shape (B, heads, T, d)")
+    q_shape, dtype = q.shape, q.dtype
+    B, H2, Tq, d = q_shape
+    _, Hk2, Tk, _ = k.shape
+    if H2 % 2 or Hk2 % 2:
+        raise ValueError(f"heads come in pairs, got {H2} and {Hk2}")
+    dt = base._dtype_code(q)
+    qs = _strided(q, "q", q_shape, dtype, dev)
+    ks = _strided(k, "k", (B, Hk2, Tk, d), dtype, dev)
+    vs = _strided(v, "v", (B, Hk2, Tk, d), dtype, dev)
+    if q_len is not None:
+        _want(q_len, "q_len", (B,), torch.int32, dev)
+    if k_len is not None:
+        _want(k_len, "k_len", (B,), torch.int32, dev)
+    maps = _diff_maps(torch, lam, norm, norm_weight, eps, H2 // 2, d, dev)
+    os_ = None if o is None else _strided(o, "o", q_shape, dtype, dev)
+    window = NO_WINDOW if window is None else _int32(window, "window")
+    sinks = _int32(sinks, "sinks")
+    scale = d ** -0.5 if scale is None else float(scale)
+    L = base.lib().lr_fwd_diff
+    need = 0 if workspace is not None else _diff_workspace(B, H2 // 2, Hk2 // 2, Tq, Tk, d, dt)
+    held, ws, ws_bytes = _scratch(torch, workspace, need, dev)
+    if o is None:
+        o = (torch.empty if q_len is None else torch.zeros)(q_shape, dtype=dtype, device=dev)
+        os_ = _strided(o, "o", q_shape, dtype, dev)
+    st = L(q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, None if q_len is None else q_len.data_ptr(),
+           None if k_len is None else k_len.data_ptr(), maps, o.data_ptr(), os_, B, H2 // 2, Hk2 // 2, Tq, Tk, d,
+           window, sinks, scale, dt, ws, ws_bytes, _handle(torch, dev))
+    if st != 0:
+        raise base.LrError(st, "lr_fwd_diff")
     return o
 
 

@@ -163,6 +163,36 @@ lr_status step_paged(const void *q, const lr_paged *cache, const int *lens, void
     return done(launch_step_paged(a, d, dt, workspace, stream));
 }
 
+// Sizes of differential attention; shared by the call and its workspace query.
+lr_status check_diff_sizes(int B, int H, int Hk, int Tq, int Tk, int d, lr_dtype dt) {
+    const lr_status st = check_types(d, dt);
+    if (st != LR_OK) return st;
+    if (check_heads(H, Hk) != LR_OK || B < 1 || Tq < 0 || Tk < 0 || H > (1 << 29)) return LR_ERR_SHAPE;
+    if (Tq > (1 << 30) || Tk > (1 << 30) || !count_ok(B, 2ll * H, Tq, 2ll * d) ||
+        !count_ok(B, 2ll * Hk, Tk, d))
+        return LR_ERR_SHAPE;
+    // row tiles, counted as CTAs of one launch
+    if (!count_ok(B, 2ll * H, Tq / 64 + 1, 1) || 2ll * B * H * (Tq / 64 + 1) > 0x7fffffffll)
+        return LR_ERR_SHAPE;
+    return LR_OK;
+}
+// fp32 keeps the maps' own outputs
+size_t diff_workspace(int B, int H, int Tq, int Tk, int d, lr_dtype dt) {
+    return dt == LR_DT_F32 && Tk > 0 ? diff_f32_workspace_bytes(B, H, Tq, d) : 0;
+}
+
+lr_status check_diff_maps(const lr_diff_maps *m, int H, int d, Span *lambda, Span *weight) {
+    if (!m) return LR_ERR_NULL;
+    if (m->flags & ~LR_DIFF_NORM) return LR_ERR_FUSE;
+    const bool norm = m->flags & LR_DIFF_NORM;
+    if (norm && !(m->eps >= 0.f && m->eps <= 3.4e38f)) return LR_ERR_FUSE;
+    if (!m->lambda) return LR_ERR_NULL;
+    if (!aligned4(m->lambda) || !aligned4(m->weight)) return LR_ERR_ALIGN;
+    *lambda = span(m->lambda, (size_t)H * 4);
+    *weight = span(norm ? m->weight : nullptr, (size_t)d * 8);
+    return LR_OK;
+}
+
 // axes.count 0: positions of one axis; else `positions` are the tokens' places.
 lr_status qk_norm_rope(const void *q, lr_strides qs, const void *k, lr_strides ks,
                        const int *positions, const QkAxes &axes, const lr_qk_maps *maps, void *q_out,
@@ -289,6 +319,51 @@ lr_status lr_fwd_window(const void *q, lr_strides qs, const void *k, lr_strides 
     if (Tk == 0) return done(launch_window_zero(a, d, dt, stream));
     return done(dt == LR_DT_BF16 ? launch_window_tc(a, d, stream)
                                  : launch_window_f32(a, d, stream));
+}
+
+lr_status lr_fwd_diff(const void *q, lr_strides qs, const void *k, lr_strides ks, const void *v,
+                      lr_strides vs, const int *q_len, const int *k_len, const lr_diff_maps *maps,
+                      void *o, lr_strides os, int B, int H, int Hk, int Tq, int Tk, int d,
+                      int window, int sinks, float scale, lr_dtype dt, void *workspace,
+                      size_t workspace_bytes, cudaStream_t stream) {
+    lr_status st = check_diff_sizes(B, H, Hk, Tq, Tk, d, dt);
+    if (st != LR_OK) return st;
+    if (window < 1 || sinks < 0 || !isfinite(scale)) return LR_ERR_SHAPE;
+    Span lambda, weight;
+    if ((st = check_diff_maps(maps, H, d, &lambda, &weight)) != LR_OK) return st;
+    if (Tq == 0) return LR_OK;
+    if (!q || !o || (Tk > 0 && (!k || !v))) return LR_ERR_NULL;
+    for (const void *p : {q, k, v, (const void *)o})
+        if (!aligned16(p)) return LR_ERR_ALIGN;
+    if (!aligned4(q_len) || !aligned4(k_len)) return LR_ERR_ALIGN;
+    if ((st = check_strides(&qs, B, 2 * H, Tq, dt)) != LR_OK) return st;
+    if ((st = check_strides(&os, B, 2 * H, Tq, dt)) != LR_OK) return st;
+    if ((st = check_strides(&ks, B, 2 * Hk, Tk, dt)) != LR_OK) return st;
+    if ((st = check_strides(&vs, B, 2 * Hk, Tk, dt)) != LR_OK) return st;
+    if (!distinct_rows(os, B, 2 * H, Tq, d)) return LR_ERR_ALIAS;
+    const size_t need = diff_workspace(B, H, Tq, Tk, d, dt);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return LR_ERR_WORKSPACE;
+    if (need > 0 && !aligned16(workspace)) return LR_ERR_ALIGN;
+    const Span so = strided_span(o, os, B, 2 * H, Tq, d, dt), sw = span(need > 0 ? workspace : nullptr, need);
+    for (const Span &i :
+         {strided_span(q, qs, B, 2 * H, Tq, d, dt), strided_span(k, ks, B, 2 * Hk, Tk, d, dt),
+          strided_span(v, vs, B, 2 * Hk, Tk, d, dt), span(q_len, (size_t)B * 4),
+          span(k_len, (size_t)B * 4), lambda, weight})
+        if (overlap(so, i) || overlap(sw, i)) return LR_ERR_ALIAS;
+    if (overlap(so, sw)) return LR_ERR_ALIAS;
+    if (Tk == 0) {
+        const WindowArgs w{q, k, v, o, qs, ks, vs, os, q_len, k_len, B, 2 * H, 2 * Hk, Tq, Tk, window,
+                           sinks, scale};
+        return done(launch_window_zero(w, d, dt, stream));
+    }
+    const DiffArgs a{q, k, v, o, qs, ks, vs, os, q_len, k_len, maps->lambda, maps->weight, B, H, Hk,
+                     Tq, Tk, window, sinks, scale, maps->eps, (maps->flags & LR_DIFF_NORM) != 0};
+    return done(dt == LR_DT_BF16 ? launch_diff_tc(a, d, stream) : launch_diff_f32(a, d, workspace, stream));
+}
+
+size_t lr_fwd_diff_workspace_size(int B, int H, int Hk, int Tq, int Tk, int d, lr_dtype dt) {
+    if (check_diff_sizes(B, H, Hk, Tq, Tk, d, dt) != LR_OK) return 0;
+    return diff_workspace(B, H, Tq, Tk, d, dt);
 }
 
 size_t lr_step_paged_workspace_size(int N, int Hq, int Hk, int d, int max_len, int window,

@@ -145,6 +145,24 @@ cudaError_t launch_window_tc(const WindowArgs &a, int d, cudaStream_t stream);
 // Zeros in every row that is written (Tk == 0), either type (window_f32.cu).
 cudaError_t launch_window_zero(const WindowArgs &a, int d, lr_dtype dt, cudaStream_t stream);
 
+// Differential attention: H pairs of heads on Hk pairs of key heads, tensors
+// [B, 2 H or 2 Hk, T, d].
+struct DiffArgs {
+    const void *q, *k, *v;
+    void *o;
+    lr_strides qs, ks, vs, os;
+    const int *q_len, *k_len;
+    const float *lambda, *weight;
+    int B, H, Hk, Tq, Tk, window, sinks;
+    float scale, eps;
+    bool norm;
+};
+// fp32, Tk >= 1, through the maps' own outputs in the workspace (diff_f32.cu).
+cudaError_t launch_diff_f32(const DiffArgs &a, int d, void *ws, cudaStream_t stream);
+size_t diff_f32_workspace_bytes(int B, int H, int Tq, int d);
+// Tensor cores, bf16, Tk >= 1 (diff_tc.cu).
+cudaError_t launch_diff_tc(const DiffArgs &a, int d, cudaStream_t stream);
+
 struct StepArgs {
     const void *q, *k, *v;
     void *o;
@@ -168,5 +186,6 @@ int attn_errors_rope();
 int attn_errors_window_f32();
 int attn_errors_window_tc();
 int attn_errors_step();
+int attn_errors_diff_tc();
 
 }  // namespace lr

@@ -35,10 +35,12 @@ __device__ __forceinline__ float warp_sum(float x) {
 }
 
 // q: the row's d channels; keys(j, kj, vj): whether key j can be read, and its
-// rows of k and v; o: the row as the kernel left it.  Every lane of the warp
-// calls this with the same arguments.
+// rows of k and v.  odd: which of the lane's channels lane + 32 i want a value
+// (all of them, on return, where the sum of weights is not finite); y: their
+// values.  Every lane of the warp calls this with the same arguments.
 template <typename E, int D, typename Keys>
-__device__ __forceinline__ void mend_row_of(const E *q, const Keys &keys, E *o, SeenKeys s, ScoreFactor f,
+__device__ __forceinline__ void mend_values(const E *q, const Keys &keys, float (&y)[D / 32],
+                                            unsigned (&odd)[D / 32], SeenKeys s, ScoreFactor f,
                                             bool sum_finite) {
     constexpr int PL = D / 32;  // channels of a lane: lane + 32 i
     const int lane = threadIdx.x & 31;
@@ -62,17 +64,17 @@ __device__ __forceinline__ void mend_row_of(const E *q, const Keys &keys, E *o, 
         }
         if (bad) {
 #pragma unroll
-            for (int i = 0; i < PL; ++i) o[lane + 32 * i] = from_f<E>(NAN);
+            for (int i = 0; i < PL; ++i) y[i] = NAN, odd[i] = 1;
             return;
         }
         whole_row = true;
     }
     // seen in a channel: 1 +inf, 2 -inf, 4 NaN
-    unsigned found[PL], odd[PL];
+    unsigned found[PL];
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
         found[i] = 0;
-        odd[i] = whole_row || !isfinite(to_f<E>(o[lane + 32 * i]));
+        if (whole_row) odd[i] = 1;
     }
 #pragma unroll 1
     for (int j = s.hi - 1; j >= 0; --j) {
@@ -120,18 +122,32 @@ __device__ __forceinline__ void mend_row_of(const E *q, const Keys &keys, E *o, 
             const float keep = old / l, take = p / l;
 #pragma unroll
             for (int i = 0; i < PL; ++i) {
-                const float y = acc[i] * keep + take * to_f<E>(vj[lane + 32 * i]);
+                const float x = acc[i] * keep + take * to_f<E>(vj[lane + 32 * i]);
                 // a mean of the type's largest values, but for its rounding
-                acc[i] = fminf(fmaxf(y, -3.402823466e38f), 3.402823466e38f);
+                acc[i] = fminf(fmaxf(x, -3.402823466e38f), 3.402823466e38f);
             }
         }
     }
 #pragma unroll
     for (int i = 0; i < PL; ++i) {
         const float inf = found[i] == 1u ? INFINITY : (found[i] == 2u ? -INFINITY : NAN);
-        if (odd[i] && found[i]) o[lane + 32 * i] = from_f<E>(inf);
-        else if (odd[i]) o[lane + 32 * i] = from_f<E>(acc[i]);
+        y[i] = found[i] ? inf : acc[i];
     }
+}
+
+// The same for a row o as the kernel left it.
+template <typename E, int D, typename Keys>
+__device__ __forceinline__ void mend_row_of(const E *q, const Keys &keys, E *o, SeenKeys s, ScoreFactor f,
+                                            bool sum_finite) {
+    const int lane = threadIdx.x & 31;
+    float y[D / 32];
+    unsigned odd[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) odd[i] = !isfinite(to_f<E>(o[lane + 32 * i]));
+    mend_values<E, D>(q, keys, y, odd, s, f, sum_finite);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i)
+        if (odd[i]) o[lane + 32 * i] = from_f<E>(y[i]);
 }
 
 // The same with the key head's rows `kt` and `vt` elements apart.

@@ -1,0 +1,81 @@
+// lr_fwd_diff in fp32: the two maps of a pair by the fp32 window kernel
+// (window_f32.cu), each over both halves of the value row, into the workspace,
+// then one pass that takes the difference and its norm (attn_diff.cuh).
+#include "attn_diff.cuh"
+#include "attn_internal.cuh"
+
+namespace lr {
+namespace {
+
+constexpr int NT = 128;
+
+// maps: [map][half][B][H][Tq][D].  A warp per row of a pair.
+template <int D>
+__global__ void __launch_bounds__(NT) diff_join_kernel(DiffArgs a, const float *maps) {
+    constexpr int PL = D / 32;
+    const int lane = threadIdx.x & 31;
+    const long long rows = (long long)a.B * a.H * a.Tq;
+    const long long r = (long long)blockIdx.x * (NT / 32) + (threadIdx.x >> 5);
+    if (r >= rows) return;
+    const int i = (int)(r % a.Tq), bh = (int)(r / a.Tq), b = bh / a.H, h = bh - b * a.H;
+    bool bad = false;  // reported by the maps' own kernels
+    if (i >= clamp_len(a.q_len, b, a.Tq, &bad)) return;
+    const float lambda = a.lambda[h];
+    float y[2][PL], sum = 0.f;
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int c = 0; c < PL; ++c) {
+            const float *x = maps + (half * rows + r) * D + lane + 32 * c;
+            y[half][c] = fmaf(-lambda, x[2 * rows * D], x[0]);
+            sum = fmaf(y[half][c], y[half][c], sum);
+        }
+    const float f = a.norm ? diff_rms(warp_sum(sum), D, a.eps) : 1.f;
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        float *o = static_cast<float *>(a.o) + b * a.os.b + (2 * h + half) * a.os.h + i * a.os.t + lane;
+#pragma unroll
+        for (int c = 0; c < PL; ++c)
+            o[32 * c] = y[half][c] * f * (a.norm && a.weight ? a.weight[half * D + lane + 32 * c] : 1.f);
+    }
+}
+
+template <int D>
+void join(const DiffArgs &a, const float *maps, cudaStream_t stream) {
+    const long long rows = (long long)a.B * a.H * a.Tq;
+    diff_join_kernel<D><<<(unsigned)((rows + NT / 32 - 1) / (NT / 32)), NT, 0, stream>>>(a, maps);
+}
+
+}  // namespace
+
+size_t diff_f32_workspace_bytes(int B, int H, int Tq, int d) { return (size_t)B * H * Tq * d * 16; }
+
+cudaError_t launch_diff_f32(const DiffArgs &a, int d, void *ws, cudaStream_t stream) {
+    float *maps = static_cast<float *>(ws);
+    const long long rows = (long long)a.B * a.H * a.Tq;
+    auto pairs = [](lr_strides s) {
+        s.h *= 2;
+        return s;
+    };
+    for (int m = 0; m < 2; ++m)
+        for (int half = 0; half < 2; ++half) {
+            WindowArgs w{};
+            w.q = static_cast<const float *>(a.q) + m * a.qs.h;
+            w.k = static_cast<const float *>(a.k) + m * a.ks.h;
+            w.v = static_cast<const float *>(a.v) + half * a.vs.h;
+            w.o = maps + (2 * m + half) * rows * d;
+            w.qs = pairs(a.qs), w.ks = pairs(a.ks), w.vs = pairs(a.vs);
+            w.os = {(long long)a.H * a.Tq * d, (long long)a.Tq * d, d};
+            w.q_len = a.q_len, w.k_len = a.k_len;
+            w.B = a.B, w.Hq = a.H, w.Hk = a.Hk, w.Tq = a.Tq, w.Tk = a.Tk;
+            w.window = a.window, w.sinks = a.sinks, w.scale = a.scale;
+            const cudaError_t e = launch_window_f32(w, d, stream);
+            if (e != cudaSuccess) return e;
+        }
+    if (d == 32) join<32>(a, maps, stream);
+    else if (d == 64) join<64>(a, maps, stream);
+    else join<128>(a, maps, stream);
+    return cudaGetLastError();
+}
+
+}  // namespace lr

@@ -1,0 +1,633 @@
+// lr_fwd_diff in bf16 on the tensor cores (tcgen05): both softmax maps of a pair
+// of heads in one pass over the keys, their difference and its norm in the
+// epilogue (attn_diff.cuh has the formula).
+//
+// A CTA takes 128 query rows of a pair.  Per 128-key tile and map m:
+//
+//     S_m = Q_m K_m^T   (tcgen05.mma, both operands in shared memory, S in TMEM)
+//     P_m = exp2(c S_m - b) row by row, one softmax thread per row (softmax_tile)
+//     O_m += P_m V      (P from TMEM, V from shared memory MN-major, 2 d columns)
+//
+// The maps alternate on the tensor pipe, one's softmax under the other's
+// products, and share the value tile.  Both outputs stay in tensor memory, so
+// the difference is formed there in fp32 and rounded once: at the end each of
+// the two softmax warpgroups reads half of the channels of both outputs.
+//
+// Tensor memory holds 2 x 128 columns of scores and 2 x 128 of output.  With d =
+// 128 the values have 256 channels: two CTAs of a cluster take a half each and
+// both form all scores (8 units of products where 6 would do).  A row's sum of
+// squares is exchanged through distributed shared memory.
+//
+// A row's non-finite values, padding and the rounding of the exponent's base are
+// dealt with as in window_tc.cu.
+//
+// Roles of the 384 threads: warps 0-3 softmax of map 0 and the first half of the
+// CTA's channels, warps 4-7 of map 1 and the second half, warps 8 and 9 issue the
+// products of maps 0 and 1, warp 10 the TMA loads, warp 11 works out the pieces.
+// The CTAs stay and take every n-th piece, longest first and in turning order, so
+// that loads and products of the next piece run under the last one's epilogue.
+// Every wait is bounded (lr_device_status).
+#include <algorithm>
+
+#include "attn_diff.cuh"
+#include "attn_internal.cuh"
+#include "attn_rows.cuh"
+#include "attn_tc.cuh"
+#include "tc_common.cuh"
+
+namespace lr {
+namespace {
+
+using namespace tc;
+
+__device__ unsigned g_diff_error = 0;
+
+constexpr int BM = 128, BN = 128;
+// Threads and their registers: launched with 168 each (64,512 in all); the
+// softmax warpgroups take 216, the third one keeps 72.
+constexpr int NT = 384, kRegsSoftmax = 216, kRegsOther = 72;
+static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsOther <= NT * 168, "register shares");
+
+template <int D>
+struct Layout {
+    static constexpr int KB = D > 64 ? 2 : 1;        // 64-column blocks of a query or key tile
+    static constexpr int CS = D > 64 ? 2 : 1;        // CTAs of a cluster, each a part of the channels
+    static constexpr int DV = 2 * D / CS;            // value channels of a CTA
+    static constexpr int TILE = KB * 128 * 128;      // bytes of a query or key tile
+    static constexpr int VTILE = 2 * 128 * 128;      // of a value tile: two 64-column blocks
+    static constexpr int NK = D > 64 ? 1 : 2;        // key tiles in flight per map
+    static constexpr int NV = 2;                     // value tiles in flight
+    static constexpr int Q = 0;
+    static constexpr int K = 2 * TILE;               // [map][slot]
+    static constexpr int V = K + 2 * NK * TILE;
+    static constexpr int OUT = V + NV * VTILE;       // 2 KB per softmax warp: rows on their way out
+    static constexpr int SUM = OUT + 8 * 2048;       // [2][map][128] sums of weights
+    static constexpr int SQ = SUM + 2 * 2 * 128 * 4; // [2][2 CS][128] sums of squares
+    static constexpr int W = SQ + 2 * 2 * CS * 128 * 4;  // [2 D] weights of the norm
+    static constexpr int BAR = W + 2 * D * 4;
+    static constexpr int ITEM = BAR + 384;           // two of struct Item
+    static constexpr int BYTES = ITEM + 2 * 128;
+    static constexpr int ALLOC = BYTES + 1024;
+};
+
+struct Barriers {
+    uint64_t qfull[2], qempty[2], sfull[2], pready[2][2], ofull[2], oempty, fin[2];
+    uint64_t kfull[2][2], kempty[2][2], vfull[2], vempty[2];
+    uint64_t ifull[2], iempty[2], lfull, sqready, sqfull[2], pad;
+    uint32_t tmem, pipe;  // pipe: 1 while a warp issues products
+};
+
+constexpr uint32_t kS = 0, kO = 256;  // TMEM columns: S0, S1 (P over them), then O0, O1
+
+struct TcArgs {
+    DiffArgs a;
+    float c;          // the scores' factor, positive
+    unsigned negate;  // idesc bit: scores of -Q (scale < 0)
+    int group;        // pairs of heads that share keys
+    int tiles;        // row blocks of a pair
+    int span;         // pairs of all batches that are worked on together
+    int pieces;
+};
+
+// A piece of work, kept in shared memory.  Key tile `it` is a sink tile (it <
+// sink_tiles), whose keys all rows see, or window tile it - sink_tiles; those
+// that all rows see entirely form one run [all0, all1).
+struct Item {
+    int b, h, hk, i0, rows, p0, kl;
+    int all0, all1, sink_keys, sink_tiles, lo, hi;
+    int n;      // key tiles; 0: no rows
+    int valid;  // 0: no work is left
+
+    __device__ __forceinline__ int key0(int it) const {
+        return it < sink_tiles ? it * BN : lo + (it - sink_tiles) * BN;
+    }
+    __device__ __forceinline__ int limit(int it) const { return it < sink_tiles ? sink_keys : hi; }
+    // columns that the tile needs, a multiple of 32
+    __device__ __forceinline__ int width(int it) const {
+        const int w = limit(it) - key0(it);
+        return w >= BN ? BN : (w < 32 ? 32 : (w + 31) & ~31);
+    }
+};
+static_assert(sizeof(Item) <= 128 && sizeof(Barriers) <= 384, "shared memory layout");
+
+__device__ __forceinline__ void make_item(const TcArgs &g, int block, Item &x, bool *bad) {
+    const DiffArgs &a = g.a;
+    // the last rows see the most keys: of the pairs whose keys and values the L2
+    // cache holds together, all longest tiles start first
+    const unsigned size = g.span * g.tiles, span = (unsigned)block / size, in = block - span * size;
+    const unsigned wide = min(g.span, a.B * a.H - (int)span * g.span), deep = in / wide;
+    const int tile = g.tiles - 1 - (int)deep, bh = span * g.span + in - deep * wide;
+    x.b = (unsigned)bh / (unsigned)a.H;
+    x.h = bh - x.b * a.H;
+    x.hk = (unsigned)x.h / (unsigned)g.group;
+    const int ql = clamp_len(a.q_len, x.b, a.Tq, bad), kl = clamp_len(a.k_len, x.b, a.Tk, bad);
+    x.kl = kl;
+    x.i0 = tile * BM;
+    x.rows = max(0, min(BM, ql - x.i0));
+    x.p0 = kl - ql + x.i0;
+    const SeenKeys f = seen_keys(x.p0, kl, a.window, a.sinks),
+                   e = seen_keys(x.p0 + x.rows - 1, kl, a.window, a.sinks);
+    x.lo = f.lo, x.hi = e.hi;
+    x.sink_keys = min(e.s1, f.lo);
+    x.sink_tiles = (x.sink_keys + BN - 1) / BN;
+    x.n = x.sink_tiles + (x.hi > x.lo ? (x.hi - x.lo + BN - 1) / BN : 0);
+    // no key for any row: one tile with everything masked gives the zeros
+    x.n = x.rows > 0 ? max(x.n, 1) : 0;
+    // positions and keys lie within +-2^30, so differences of two fit an int
+    const int far = x.p0 + BM - min(a.window, 1 << 30) - x.lo;  // first key of the last row
+    x.all0 = x.sink_tiles + (far > 0 ? (far + BN - 1) / BN : 0);
+    const int end = min(x.hi, x.p0 + 1) - x.lo;
+    x.all1 = x.sink_tiles + (end > 0 ? end / BN : 0);
+}
+
+// One row by a warp, put right; this CTA and warpgroup write channels c0 ..
+// c0 + n - 1 of the pair's 2 D.
+template <int D>
+__device__ __forceinline__ void mend_row(const TcArgs &g, const Item &x, int row, int c0, int n, bool fin0, bool fin1) {
+    using E = __nv_bfloat16;
+    const DiffArgs &a = g.a;
+    const int lane = threadIdx.x & 31;
+    const E *q = static_cast<const E *>(a.q) + x.b * a.qs.b + 2 * x.h * a.qs.h + (long long)(x.i0 + row) * a.qs.t;
+    const E *k = static_cast<const E *>(a.k) + x.b * a.ks.b + 2 * x.hk * a.ks.h;
+    const E *v = static_cast<const E *>(a.v) + x.b * a.vs.b + 2 * x.hk * a.vs.h;
+    E *o = static_cast<E *>(a.o) + x.b * a.os.b + 2 * x.h * a.os.h + (long long)(x.i0 + row) * a.os.t;
+    float y[2][D / 32];
+    mend_diff<E, D>(
+        q, q + a.qs.h,
+        [&](int map, int half, int j, const E *&kj, const E *&vj) {
+            kj = k + map * a.ks.h + j * a.ks.t, vj = v + half * a.vs.h + j * a.vs.t;
+            return true;
+        },
+        a.lambda[x.h], a.norm, a.weight, a.eps, seen_keys(x.p0 + row, x.kl, a.window, a.sinks),
+        score_factor(a.scale), fin0, fin1, y);
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            const int ch = half * D + lane + 32 * i;
+            if (ch >= c0 && ch < c0 + n) o[half * a.os.h + lane + 32 * i] = from_f<E>(y[half][i]);
+        }
+}
+
+template <int D>
+__global__ void __launch_bounds__(NT, 1)
+    diff_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                   const __grid_constant__ CUtensorMap tmv, const TcArgs g) {
+    using L = Layout<D>;
+    constexpr int NK = L::NK, NV = L::NV, CS = L::CS, DV = L::DV;
+    extern __shared__ uint8_t raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    Barriers *bars = reinterpret_cast<Barriers *>(sm + L::BAR);
+    Item *items = reinterpret_cast<Item *>(sm + L::ITEM);
+    float *wsm = reinterpret_cast<float *>(sm + L::W);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const DiffArgs &a = g.a;
+    const int rank = CS == 1 ? 0 : (int)cluster_rank();  // which part of the channels
+    constexpr uint32_t kSqBytes = 2 * CS * 128 * 4;
+
+    if (tid == 0) {
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&bars->qfull[t], 1);
+            mbar_init(&bars->qempty[t], 1);
+            mbar_init(&bars->sfull[t], 1);
+            mbar_init(&bars->pready[t][0], 4);  // the first 64 columns of P
+            mbar_init(&bars->pready[t][1], 4);  // the others
+            mbar_init(&bars->ofull[t], 1);
+            mbar_init(&bars->fin[t], 1);
+            for (int s = 0; s < NK; ++s) {
+                mbar_init(&bars->kfull[t][s], 1);
+                mbar_init(&bars->kempty[t][s], 1);
+            }
+            mbar_init(&bars->ifull[t], 1);
+            mbar_init(&bars->iempty[t], 11);  // softmax, product and load warps
+            mbar_init(&bars->sqfull[t], 1);
+        }
+        for (int s = 0; s < NV; ++s) {
+            mbar_init(&bars->vfull[s], 1);
+            mbar_init(&bars->vempty[s], 2);  // both maps
+        }
+        mbar_init(&bars->oempty, 8);
+        mbar_init(&bars->lfull, 8);
+        mbar_init(&bars->sqready, 8);
+        mbar_init(&bars->pad, 1);
+        bars->pipe = 0;
+        fence_mbar_init();
+        for (int t = 0; t < 2; ++t) mbar_expect_tx(&bars->sqfull[t], kSqBytes);
+    }
+    for (int i = tid; i < 2 * D; i += NT) wsm[i] = a.norm && a.weight ? a.weight[i] : 1.f;
+    if (warp == 10 && lane == 0) {
+        for (const CUtensorMap *map : {&tmq, &tmk, &tmv})
+            asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+    }
+    if (warp == 8) {
+        tmem_alloc(&bars->tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    // the other CTA's barriers stand before it is sent anything
+    if (CS > 1) cluster_sync_all();
+    const uint32_t tmem = bars->tmem;
+    bool ok = true;
+
+    // A role's next piece of work (whole warp); null at the end or on a wait that gave up.
+    int piece = 0;
+    auto take = [&]() -> const Item * {
+        ok = __all_sync(0xffffffffu, ok && wait_bar(&bars->ifull[piece & 1], (piece >> 1) & 1));
+        return ok && items[piece & 1].valid ? &items[piece & 1] : nullptr;
+    };
+    auto give_back = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->iempty[piece & 1]);
+        ++piece;
+    };
+
+    if (warp >= 8) regs_down<kRegsOther>();
+    if (warp == 11) {
+        // ==================================================== pieces of work
+        if (lane == 0) {
+            const int me = blockIdx.x / CS, all = gridDim.x / CS;
+            for (int i = 0; ok; ++i) {
+                if (i >= 2) ok = wait_bar(&bars->iempty[i & 1], ((i >> 1) - 1) & 1);
+                if (!ok) break;
+                const long long block = (long long)i * all + (i & 1 ? all - 1 - me : me);
+                Item &x = items[i & 1];
+                const bool some = block < g.pieces;
+                if (some) {
+                    bool bad = false;
+                    make_item(g, (int)block, x, &bad);
+                    if (bad) atomicOr(&g_diff_error, kAttnIndex);
+                }
+                x.valid = some;
+                mbar_arrive(&bars->ifull[i & 1]);
+                if (!some) break;
+            }
+        }
+    } else if (warp == 10) {
+        // ============================================================ loads
+        int queries[2] = {0, 0}, keys[2] = {0, 0}, done = 0, pads = 0;  // loaded: per map, value tiles
+        while (const Item *px = take()) {
+            const Item &x = *px;
+            const int n = x.n;
+            if (n > 0) {
+#pragma unroll 1
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (queries[t] > 0)
+                        ok = __all_sync(0xffffffffu, wait_bar(&bars->qempty[t], (queries[t] - 1) & 1));
+                    if (!ok) break;
+                    ++queries[t];
+                    if (lane == 0) {
+                        mbar_expect_tx(&bars->qfull[t], L::TILE);
+                        for (int kb = 0; kb < L::KB; ++kb)
+                            tma_load_4d(sm + L::Q + t * L::TILE + kb * 16384, &tmq, kb * 64, x.i0, 2 * x.h + t, x.b,
+                                        &bars->qfull[t]);
+                    }
+                }
+            }
+#pragma unroll 1
+            for (int it = 0; it < n && ok; ++it) {
+                const int k0 = x.key0(it), ks = done % NK, vs = done % NV;
+#pragma unroll 1
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (done >= NK)
+                        ok = __all_sync(0xffffffffu, wait_bar(&bars->kempty[t][ks], (done / NK - 1) & 1));
+                    if (!ok) break;
+                    ++keys[t];
+                    if (lane == 0) {
+                        mbar_expect_tx(&bars->kfull[t][ks], L::TILE);
+                        for (int kb = 0; kb < L::KB; ++kb)
+                            tma_load_4d(sm + L::K + (t * NK + ks) * L::TILE + kb * 16384, &tmk, kb * 64, k0,
+                                        2 * x.hk + t, x.b, &bars->kfull[t][ks]);
+                    }
+                }
+                if (ok && done >= NV) ok = __all_sync(0xffffffffu, wait_bar(&bars->vempty[vs], (done / NV - 1) & 1));
+                if (!ok) break;
+                uint8_t *to = sm + L::V + vs * L::VTILE;
+                // values behind the last key: zeros, whatever the padding holds
+                const bool pad = x.kl < a.Tk && k0 + BN > x.kl;
+                uint64_t *bar = pad ? &bars->pad : &bars->vfull[vs];
+                if (lane == 0) {
+                    mbar_expect_tx(bar, L::VTILE);
+                    for (int j = 0; j < 2; ++j)
+                        tma_load_4d(to + j * 16384, &tmv, CS == 1 ? 0 : 64 * j, k0,
+                                    2 * x.hk + (CS == 1 ? j : rank), x.b, bar);
+                }
+                if (pad) {
+                    ok = __all_sync(0xffffffffu, wait_bar(&bars->pad, pads & 1));
+                    ++pads;
+                    const int from = max(0, x.kl - k0) * 8;  // 16-byte units of 128-byte rows
+#pragma unroll 1
+                    for (int u = from + lane; u < BN * 8; u += 32)
+                        for (int j = 0; j < 2; ++j)
+                            *reinterpret_cast<uint4 *>(to + j * 16384 + u * 16) = make_uint4(0, 0, 0, 0);
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->vfull[vs]);
+                }
+                ++done;
+            }
+            give_back();
+        }
+        // never leave with copies into shared memory in flight: the last phases
+        // of every barrier that this warp armed
+        if (lane == 0) {
+            for (int t = 0; t < 2; ++t) {
+                if (queries[t] > 0 && !wait_bar(&bars->qfull[t], (queries[t] - 1) & 1)) ok = false;
+                for (int i = max(0, keys[t] - NK); i < keys[t]; ++i)
+                    if (!wait_bar(&bars->kfull[t][i % NK], (i / NK) & 1)) ok = false;
+            }
+            for (int i = max(0, done - NV); i < done; ++i)
+                if (!wait_bar(&bars->vfull[i % NV], (i / NV) & 1)) ok = false;
+            if (pads > 0 && !wait_bar(&bars->pad, (pads - 1) & 1)) ok = false;
+        }
+    } else if (warp == 8 || warp == 9) {
+        // ========================================================= products
+        // One warp per map.  It walks and waits as a whole; one elected lane
+        // issues.  What a step needs is worked out before its wait for P.
+        const int t = warp - 8;
+        const uint32_t s_t = tmem + kS + t * BN, o_t = tmem + kO + t * 128;
+        // d = 32: the halves' 32 columns lie in two 64-column blocks, a product each
+        constexpr int NO = D == 32 ? 2 : 1;
+        const uint32_t id_o = idesc_bf16_f32_mn(BM, DV / NO, false, true);
+        const uint64_t dq = tile_desc(smem_u32(sm + L::Q) + t * L::TILE, 128, 0, 0);
+        const uint32_t k_s = smem_u32(sm + L::K) + t * NK * L::TILE, v_s = smem_u32(sm + L::V);
+        const bool lead = elect_one();
+        int done = 0, used = 0;  // key tiles and pieces multiplied
+        auto k_wait = [&](int i) {
+            return __all_sync(0xffffffffu, wait_bar(&bars->kfull[t][i % NK], (i / NK) & 1));
+        };
+        while (const Item *px = take()) {
+            const Item &x = *px;
+            const int n = x.n;
+            if (n == 0) {
+                give_back();
+                continue;
+            }
+            const int w_last = x.width(n - 1), w_sink = x.sink_tiles ? x.width(x.sink_tiles - 1) : BN;
+            const int sink_tiles = x.sink_tiles;
+            auto width = [&](int it) { return it == n - 1 ? w_last : (it == sink_tiles - 1 ? w_sink : BN); };
+            // S = Q K(it)^T; i: tiles multiplied before it
+            auto scores = [&](int it, int i) {
+                const uint64_t dk = tile_desc(k_s + (i % NK) * L::TILE, 128, 0, 0);
+                const uint32_t id = idesc_bf16_f32(BM, width(it)) | g.negate;
+#pragma unroll
+                for (int ks = 0; ks < D / 16; ++ks)
+                    mma_bf16(s_t, kdesc_step(dq, 128, ks), kdesc_step(dk, 128, ks), id, ks > 0);
+                mma_commit(&bars->sfull[t]);
+                mma_commit(&bars->kempty[t][i % NK]);
+                if (it == n - 1) mma_commit(&bars->qempty[t]);
+            };
+            ok = __all_sync(0xffffffffu, wait_bar(&bars->qfull[t], used & 1)) && k_wait(done);
+            if (lead && ok) scores(0, done);
+            __syncwarp();
+#pragma unroll 1
+            for (int it = 0; it < n && ok; ++it) {
+                if (it + 1 < n) ok = k_wait(done + 1);
+                if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bars->vfull[done % NV], (done / NV) & 1));
+                const uint64_t dv = tile_desc_mn(v_s + (done % NV) * L::VTILE, 128, 0);
+                const int steps = width(it) >> 4;
+                auto values = [&](int ks) {
+#pragma unroll
+                    for (int j = 0; j < NO; ++j)
+                        mma_bf16_ta(o_t + j * (DV / NO), s_t + 8 * ks, mndesc_step(dv, ks) + j * (16384u >> 4), id_o,
+                                    ks > 0 || it > 0);
+                };
+                // the last piece's outputs have left
+                if (ok && it == 0 && used > 0)
+                    ok = __all_sync(0xffffffffu, wait_bar(&bars->oempty, (used - 1) & 1));
+                if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bars->pready[t][0], done & 1));
+                if (!ok) break;
+                tc_fence_after();
+                // O += P V, 64 keys at a time as P comes
+                if (lead) {
+                    take_pipe(&bars->pipe);
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        if (ks < steps) values(ks);
+                }
+                __syncwarp();
+                ok = __all_sync(0xffffffffu, wait_bar(&bars->pready[t][1], done & 1));
+                if (!ok) break;
+                tc_fence_after();
+                if (lead) {
+#pragma unroll
+                    for (int ks = 4; ks < BN / 16; ++ks)
+                        if (ks < steps) values(ks);
+                    mma_commit(&bars->vempty[done % NV]);
+                    if (it + 1 < n) scores(it + 1, done + 1);
+                    else mma_commit(&bars->ofull[t]);
+                    free_pipe(&bars->pipe);
+                }
+                __syncwarp();
+                ++done;
+            }
+            ++used;
+            give_back();
+        }
+        if (lead) mma_commit(&bars->fin[t]);
+        __syncwarp();
+        if (!wait_bar(&bars->fin[t], 0)) ok = false;
+    } else if (warp < 8) {
+        // ========================== softmax, then the difference and its norm
+        regs_up<kRegsSoftmax>();
+        const int t = warp >> 2, row = tid & 127;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16;
+        const uint32_t ts = tmem + lanes + kS + t * BN, to = tmem + lanes + kO + t * 128;
+        constexpr int CH = DV / 2;  // channels of this warpgroup
+        const int col = t * CH;     // the first of them in the outputs
+        const int ch0 = rank * DV + col, half = ch0 / D, in_half = ch0 - half * D;
+        int seen = 0, used = 0;
+        while (const Item *px = take()) {
+            const Item &x = *px;
+            const int n = x.n, all0 = x.all0, all1 = x.all1;
+            if (n == 0) {
+                give_back();
+                continue;
+            }
+            const int p = x.p0 + row;
+            const long long plo = (long long)p - a.window + 1;
+            const int rlo = plo < 0 ? 0 : (int)plo;
+            float m = -INFINITY, l = 0.f;
+            for (int it = 0; it < n && ok; ++it) {
+                const bool whole = it >= all0 && it < all1;
+                const int k0 = x.key0(it), end = min(p + 1, x.limit(it));
+                ok = __all_sync(0xffffffffu, wait_bar(&bars->sfull[t], seen & 1));
+                if (!ok) break;
+                tc_fence_after();
+                auto keep = [&](int ch) {
+                    const int kc = k0 + 32 * ch;
+                    return low_bits(end - kc) & (~low_bits(rlo - kc) | low_bits(a.sinks - kc));
+                };
+                softmax_tile<DV>(ts, to, g.c, whole, keep, m, l, &bars->pready[t][0], &bars->pready[t][1]);
+                ++seen;
+            }
+            // the rounding of the exponent's base took the weights' range
+            if (m != -INFINITY && !(l >= 0x1p-40f)) l = NAN;
+            const int slot = used & 1;
+            float *sums = reinterpret_cast<float *>(sm + L::SUM) + slot * 256;
+            sums[t * 128 + row] = l;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->lfull);
+            if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bars->lfull, used & 1));
+            if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bars->ofull[0], used & 1));
+            if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bars->ofull[1], used & 1));
+            if (!ok) break;
+            tc_fence_after();
+            const float l0 = sums[row], l1 = sums[128 + row];
+            // no key, or only scores of -inf: zeros
+            const float f0 = l0 == 0.f ? 0.f : 1.f / l0, f1 = (l1 == 0.f ? 0.f : 1.f / l1) * -a.lambda[x.h];
+            float y[CH], squares = 0.f;
+#pragma unroll
+            for (int c = 0; c < CH; c += 32) {
+                float u[32], w[32];
+                tmem_ld32(tmem + lanes + kO + col + c, u);
+                tmem_ld32(tmem + lanes + kO + 128 + col + c, w);
+                tmem_ld_wait(u, w);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    // each product rounded, so that equal maps cancel exactly
+                    y[c + i] = __fadd_rn(__fmul_rn(u[i], f0), __fmul_rn(w[i], f1));
+                    squares = fmaf(y[c + i], y[c + i], squares);
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->oempty);
+            float scale = 1.f;
+            if (a.norm) {
+                // the other channels' sums of this row, from both warpgroups
+                float *sq = reinterpret_cast<float *>(sm + L::SQ) + slot * 2 * CS * 128;
+                if (CS == 1) {
+                    sq[t * 128 + row] = squares;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->sqready);
+                    ok = __all_sync(0xffffffffu, wait_bar(&bars->sqready, used & 1));
+                } else {
+                    // and of both CTAs: every warp sends its rows' sums to each, four a lane
+                    float four[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) four[i] = __shfl_sync(0xffffffffu, squares, (4 * lane + i) & 31);
+                    if (lane < 8) {
+                        const uint32_t dst = smem_u32(sq + (rank * 2 + t) * 128 + (row & ~31) + 4 * lane);
+#pragma unroll
+                        for (int r = 0; r < CS; ++r)
+                            st_async_v4(map_to_rank(dst, r), four[0], four[1], four[2], four[3],
+                                        map_to_rank(smem_u32(&bars->sqfull[slot]), r));
+                    }
+                    ok = __all_sync(0xffffffffu, wait_bar(&bars->sqfull[slot], (used >> 1) & 1));
+                }
+                if (!ok) break;
+                float total = 0.f;
+#pragma unroll
+                for (int i = 0; i < 2 * CS; ++i) total += sq[i * 128 + row];
+                // the slot's next use is two pieces on (its sums may come before it is armed)
+                if (CS > 1 && tid == 0) mbar_expect_tx(&bars->sqfull[slot], kSqBytes);
+                scale = diff_rms(total, D, a.eps);
+                squares = total;
+            }
+            ++used;
+            // Rows leave through the warp's shared memory, 32 channels at a time,
+            // so that a store writes whole 64-byte pieces of eight rows.
+            uint8_t *out = sm + L::OUT + warp * 2048;
+            const int w0 = 32 * (warp & 3), rows = x.rows, r8 = lane >> 2, c8 = lane & 3;
+            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + x.b * a.os.b + (2 * x.h + half) * a.os.h +
+                               (long long)(x.i0 + w0 + r8) * a.os.t + in_half + 8 * c8;
+            float odd[4] = {0.f, 0.f, 0.f, 0.f};  // NaN once a value is not finite
+#pragma unroll
+            for (int c = 0; c < CH; c += 32) {
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float y0 = y[c + 2 * i] * scale * wsm[ch0 + c + 2 * i],
+                                y1 = y[c + 2 * i + 1] * scale * wsm[ch0 + c + 2 * i + 1];
+                    odd[i & 3] = fmaf(y0, 0.f, fmaf(y1, 0.f, odd[i & 3]));
+                    w[i] = pack2(y0, y1);
+                }
+                __syncwarp();  // the last channels have left
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4 *>(out + lane * 64 + (i ^ ((lane >> 1) & 3)) * 16) =
+                        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int rr = 8 * i + r8;
+                    const uint4 z = *reinterpret_cast<const uint4 *>(out + rr * 64 + (c8 ^ ((rr >> 1) & 3)) * 16);
+                    if (w0 + rr < rows) *reinterpret_cast<uint4 *>(o + 8 * i * a.os.t + c) = z;
+                }
+            }
+            unsigned again = __ballot_sync(
+                0xffffffffu, row < rows && !(odd[0] + odd[1] + odd[2] + odd[3] == 0.f && (!a.norm || squares < INFINITY)));
+            __syncwarp();
+            while (again) {
+                const int src = __ffs(again) - 1;
+                again &= again - 1;
+                mend_row<D>(g, x, w0 + src, ch0, CH, isfinite(__shfl_sync(0xffffffffu, l0, src)),
+                            isfinite(__shfl_sync(0xffffffffu, l1, src)));
+            }
+            give_back();
+        }
+    }
+
+    if (!ok) atomicOr(&g_diff_error, kAttnTimeout);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+    if (CS > 1) cluster_sync_all();  // no CTA leaves while another may send to it
+}
+
+template <int D>
+cudaError_t launch(const DiffArgs &a, int slot, cudaStream_t stream) {
+    using L = Layout<D>;
+    CUtensorMap mq, mk, mv;
+    cudaError_t e = rows_map(&mq, a.q, a.qs, a.B, 2 * a.H, a.Tq, D);
+    if (e == cudaSuccess) e = rows_map(&mk, a.k, a.ks, a.B, 2 * a.Hk, a.Tk, D);
+    if (e == cudaSuccess) e = rows_map(&mv, a.v, a.vs, a.B, 2 * a.Hk, a.Tk, D);
+    if (e != cudaSuccess) return e;
+    TcArgs g;
+    g.a = a;
+    // scale 0: as in window_tc.cu
+    g.c = a.scale == 0.f ? 0x1p-149f : score_factor(a.scale).c;
+    g.negate = a.scale < 0.f ? 1u << 13 : 0u;
+    g.group = a.H / a.Hk;
+    g.tiles = (a.Tq + BM - 1) / BM;
+    // keys and values of the pairs in flight stay within 48 MB of the L2's 129
+    const long long kv = 8ll * D * a.Tk, pairs = (long long)a.B * a.H;
+    const long long span = (48ll << 20) / kv;
+    g.span = (int)(span < 1 ? 1 : (span < pairs ? span : pairs));
+    g.pieces = (int)(pairs * g.tiles);
+    auto *fn = diff_tc_kernel<D>;
+    e = ensure_smem_attr(reinterpret_cast<const void *>(fn), L::ALLOC, slot);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(std::min(g.pieces, kClusterRoom[0][L::CS] / L::CS) * L::CS));
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = L::ALLOC;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = L::CS;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = L::CS > 1 ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, fn, mq, mk, mv, g);
+}
+
+}  // namespace
+
+// ensure_smem_attr slots 224..226 belong to this file.
+cudaError_t launch_diff_tc(const DiffArgs &a, int d, cudaStream_t stream) {
+    if (d == 32) return launch<32>(a, 224, stream);
+    if (d == 64) return launch<64>(a, 225, stream);
+    return launch<128>(a, 226, stream);
+}
+
+int attn_errors_diff_tc() {
+    unsigned h = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&h, g_diff_error, sizeof(h)) != cudaSuccess) return -1;
+    if (h) cudaMemcpyToSymbol(g_diff_error, &zero, sizeof(h));
+    return (int)h;
+}
+
+}  // namespace lr

@@ -11,7 +11,7 @@ namespace lr {
 namespace {
 
 constexpr int kMaxDevices = 64;
-constexpr int kMaxSlots = 224;
+constexpr int kMaxSlots = 256;
 std::atomic<int> g_smem_bytes[kMaxDevices][kMaxSlots];
 
 bool supported_dim(int d) { return d == 32 || d == 64 || d == 128; }
@@ -400,7 +400,7 @@ lr_status lr_device_status(void) {
     if (e < 0 || eg < 0) return LR_ERR_CUDA;
     unsigned attn = 0;
     for (int a : {attn_errors_rope(), attn_errors_window_f32(),
-                  attn_errors_window_tc(), attn_errors_step()}) {
+                  attn_errors_window_tc(), attn_errors_step(), attn_errors_diff_tc()}) {
         if (a < 0) return LR_ERR_CUDA;
         attn |= (unsigned)a;
     }

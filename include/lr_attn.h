@@ -11,6 +11,8 @@
  *                     sliding window and a few first tokens (sinks)
  *   lr_step_paged     the same attention for one new token per sequence over
  *                     the paged cache
+ *   lr_fwd_diff       differential attention over whole sequences: the
+ *                     difference of two softmax maps, with its norm
  *
  * Conventions are those of lr.h: device pointers owned by the caller, 16-byte
  * aligned (int32 arrays: 4-byte); arguments validated on the host before any launch, so that a call
@@ -166,6 +168,50 @@ lr_status lr_fwd_window(const void *q, lr_strides qs, const void *k, lr_strides 
                         lr_strides vs, const int *q_len, const int *k_len, void *o, lr_strides os,
                         int B, int Hq, int Hk, int Tq, int Tk, int d, int window, int sinks,
                         float scale, lr_dtype dt, cudaStream_t stream);
+
+/*
+ * Differential attention.  H pairs of query heads share Hk pairs of key heads
+ * (H a multiple of Hk; pair h reads pair g = h / (H / Hk)).  Pair h has the
+ * query heads 2h and 2h + 1, one for each softmax map, and the key heads 2g and
+ * 2g + 1 likewise; its value row is the 2 d channels of the value heads 2g and
+ * 2g + 1 in that order, and so is its output:
+ *
+ *     A_m  = softmax_j(scale q_(2h+m),i . k_(2g+m),j)      m = 0, 1
+ *     y_i  = sum_j (A_0 - lambda[h] A_1) [v_2g,j  v_(2g+1),j]
+ *     [o_2h,i  o_(2h+1),i] = y_i, or weight y_i / sqrt(mean(y_i^2) + eps)
+ *
+ * over the keys that row i sees, as for lr_fwd_window (window, sinks, lengths,
+ * strides and what a masked row may hold are as there).  The difference, its
+ * mean square and its norm are formed in fp32.  A row that sees no key, or whose y
+ * is zero, is zeros.  Where a map's row is not finite (lr_fwd_window says when)
+ * the formulas hold as fp32 arithmetic has them; a row whose squares sum to more
+ * than fp32 holds is divided by infinity.
+ */
+#define LR_DIFF_NORM 0x1u /* the root-mean-square norm over the pair's 2 d channels */
+
+typedef struct {
+    unsigned flags;       /* OR of LR_DIFF_*                            */
+    const float *lambda;  /* [H] fp32, 4-byte aligned                   */
+    const float *weight;  /* [2 d] fp32 of the norm, or NULL for ones   */
+    float eps;            /* >= 0, finite (LR_DIFF_NORM)                */
+} lr_diff_maps;
+
+/*
+ *   q, qs  [B, 2 H, Tq, d] with strides    k, ks, v, vs  [B, 2 Hk, Tk, d]
+ *   o, os  [B, 2 H, Tq, d] with strides, written; overlaps no input
+ *   workspace  lr_fwd_diff_workspace_size(...) bytes, 16-byte aligned (0 in
+ *              bf16); its contents on entry do not matter.  Calls that share
+ *              one are ordered on one stream.
+ * The other arguments are those of lr_fwd_window.  bf16: one kernel.
+ */
+lr_status lr_fwd_diff(const void *q, lr_strides qs, const void *k, lr_strides ks, const void *v,
+                      lr_strides vs, const int *q_len, const int *k_len, const lr_diff_maps *maps,
+                      void *o, lr_strides os, int B, int H, int Hk, int Tq, int Tk, int d,
+                      int window, int sinks, float scale, lr_dtype dt, void *workspace,
+                      size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes lr_fwd_diff needs (0 as well for arguments it would reject). */
+size_t lr_fwd_diff_workspace_size(int B, int H, int Hk, int Tq, int Tk, int d, lr_dtype dt);
 
 /*
  * One decode step: the row of position lens[n] - 1 of the attention above,

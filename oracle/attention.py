@@ -129,3 +129,71 @@ def attention_bound(o, size, reach, keys, d, dtype_bits, weight_bits=None):
     if weight_bits is not None:
         b = b + 2 * 2.0 ** -weight_bits * size
     return b + 1e-37
+
+
+def _maps(q, k, v, seen, scale):
+    """q [T,d], k [J,d], v [J,c], seen [T,J] -> output, sizes and reach as in row(), for all rows."""
+    used = seen.any(0)
+    k, v = np.where(used[:, None], k, 0.0), np.where(used[:, None], v, 0.0)
+    s = np.where(seen, (q @ k.T) * scale, -np.inf)
+    m = s.max(-1, keepdims=True, initial=-np.inf)
+    w = np.exp(s - np.where(np.isinf(m), 0.0, m))
+    n = w.sum(-1, keepdims=True)
+    w = w / np.where(n > 0, n, 1.0)
+    reach = np.where(seen, np.abs(q) @ np.abs(k).T, 0.0).max(-1, initial=0.0) * abs(scale)
+    return w @ v, w @ np.abs(v), reach
+
+
+def diff_rows(q0, q1, k0, k1, v, seen, scale, lam, d, dtype_bits, weight_bits=None, weight=None, eps=None):
+    """Rows of one pair of heads -> (o, bound), both [T,2d].  eps None: no norm.
+
+    The bound: each map's row is off as attention_bound has it but for the
+    result's rounding; the difference adds one rounding of each term.  The norm
+    r = sqrt(mean y^2 + eps) moves by at most the root mean square e of the errors,
+    so y / r by (err + |y| e / r) / (r - e); its own arithmetic adds (d + 8) 2^-24
+    of the result, which is then rounded once."""
+    keys = seen.shape[1]
+    y, err = 0.0, 0.0
+    for m, (q, k, factor) in enumerate(((q0, k0, 1.0), (q1, k1, lam))):
+        a, size, reach = _maps(q, k, v, seen, scale)
+        y = a if m == 0 else y - factor * a
+        part = attention_bound(a, size, reach, keys, d, 24, weight_bits)
+        err = part if m == 0 else err + abs(factor) * part
+        err = err + 2.0 ** -23 * abs(factor) * np.abs(a)
+    if eps is None:
+        return y, err + 2.0 ** -dtype_bits * np.abs(y)
+    r = np.sqrt(np.mean(y * y, -1, keepdims=True) + eps)
+    e = np.sqrt(np.mean(err * err, -1, keepdims=True))
+    none = ~(y != 0).any(-1, keepdims=True)
+    with np.errstate(divide="ignore", invalid="ignore"):
+        o = np.where(none, 0.0, y / r)
+        off = np.where(e < r, (err + np.abs(y) * e / r) / (r - e), np.inf)
+    w = 1.0 if weight is None else np.asarray(weight, np.float64)
+    o = o * w
+    seen_none = ~seen.any(-1)[:, None]
+    return o, np.where(seen_none, 0.0, off * np.abs(w) + ((d + 8) * 2.0 ** -24 + 2.0 ** -dtype_bits) * np.abs(o) + 1e-37)
+
+
+def diff(q, k, v, lam, window, sinks, scale, dtype_bits, weight_bits=None, weight=None, eps=None, q_len=None,
+         k_len=None):
+    """q [B,2H,Tq,d], k, v [B,2Hk,Tk,d] -> (o, bound, written [B,Tq])."""
+    q, k, v = (np.asarray(x, np.float64) for x in (q, k, v))
+    B, H2, Tq, d = q.shape
+    Hk2, Tk = k.shape[1:3]
+    G = H2 // Hk2
+    o, bound, written = np.zeros(q.shape), np.zeros(q.shape), np.zeros((B, Tq), bool)
+    for b in range(B):
+        ql = Tq if q_len is None else int(q_len[b])
+        kl = Tk if k_len is None else int(k_len[b])
+        written[b, :ql] = True
+        p, j = kl - ql + np.arange(ql)[:, None], np.arange(Tk)
+        seen = (j < kl) & (j <= p) & ((j > p - window) | (j < sinks))
+        for h in range(H2 // 2):
+            g = h // G
+            y, e = diff_rows(q[b, 2 * h, :ql], q[b, 2 * h + 1, :ql], k[b, 2 * g], k[b, 2 * g + 1],
+                             np.concatenate((v[b, 2 * g], v[b, 2 * g + 1]), -1), seen, scale, float(lam[h]), d,
+                             dtype_bits, weight_bits, weight, eps)
+            for half in range(2):
+                o[b, 2 * h + half, :ql] = y[:, half * d:(half + 1) * d]
+                bound[b, 2 * h + half, :ql] = e[:, half * d:(half + 1) * d]
+    return o, bound, written

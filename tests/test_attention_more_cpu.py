@@ -1,5 +1,5 @@
-"""CPU-side checks of the rotation by several axes: refusals before any launch
-and the binding's checks."""
+"""CPU-side checks of the rotation by several axes and of differential attention:
+refusals before any launch and the binding's checks."""
 import os
 import subprocess
 import sys
@@ -13,7 +13,7 @@ _START = r"""
 import ctypes, sys
 sys.path.insert(0, sys.argv[1])
 import gated_delta_rule_fwd_gb300 as lr
-from gated_delta_rule_fwd_gb300.attention import Strides, Paged, QkMaps
+from gated_delta_rule_fwd_gb300.attention import Strides, Paged, QkMaps, DiffMaps
 L = lr.lib()
 A = [0x10000000 * (i + 1) for i in range(16)]   # distinct, aligned, never dereferenced
 P = lambda a: None if a is None else ctypes.c_void_p(a)
@@ -58,6 +58,42 @@ cases = [
 """
 
 
+_DIFF = r"""
+def diff(**kw):
+    a = dict(q=A[0], k=A[1], v=A[2], ql=A[3], kl=A[4], o=A[5], lam=A[6], w=A[7], ws=A[8], wsb=1 << 26, flags=1,
+             eps=1e-6, B=2, H=4, Hk=2, Tq=5, Tk=9, d=64, win=4, s=1, scale=0.5, dt=1, qs=None, ks=None, vs=None,
+             os=None, maps=True)
+    a.update(kw)
+    S = lambda s, H, T: Strides(*(s or contig(2 * H, max(T, 1), a['d'])))
+    m = DiffMaps(a['flags'], a['lam'], a['w'], a['eps'])
+    return L.lr_fwd_diff(P(a['q']), S(a['qs'], a['H'], a['Tq']), P(a['k']), S(a['ks'], a['Hk'], a['Tk']),
+                         P(a['v']), S(a['vs'], a['Hk'], a['Tk']), P(a['ql']), P(a['kl']),
+                         ctypes.byref(m) if a['maps'] else None, P(a['o']), S(a['os'], a['H'], a['Tq']),
+                         a['B'], a['H'], a['Hk'], a['Tq'], a['Tk'], a['d'], a['win'], a['s'], a['scale'], a['dt'],
+                         P(a['ws']), a['wsb'], None)
+wsz = lambda *a: L.lr_fwd_diff_workspace_size(*a)
+need = wsz(2, 4, 2, 5, 9, 64, 0)
+cases = [
+    ("ok", diff(), 7), ("f32-ok", diff(dt=0), 7), ("Tq0", diff(Tq=0, q=None), 0), ("Tk0-ok", diff(Tk=0, k=None, v=None), 7),
+    ("dtype", diff(dt=-1), 3), ("d256", diff(d=256), 6), ("d16", diff(d=16), 6), ("heads", diff(H=5), 2), ("Hk0", diff(Hk=0), 2),
+    ("window0", diff(win=0), 2), ("sinks", diff(s=-1), 2), ("scale", diff(scale=inf), 2), ("B0", diff(B=0), 2),
+    ("Tneg", diff(Tk=-1), 2), ("huge", diff(Tq=1 << 30, B=1 << 10), 2), ("many", diff(H=1 << 30, Hk=1 << 30), 2),
+    ("null-maps", diff(maps=False), 1), ("null-lam", diff(lam=None), 1), ("null-w-ok", diff(w=None), 7),
+    ("flag", diff(flags=2), 12), ("eps", diff(eps=-1.0), 12), ("eps-nan", diff(eps=nan), 12), ("eps-unused", diff(flags=0, eps=nan), 7),
+    ("null-q", diff(q=None), 1), ("null-k", diff(k=None), 1), ("null-o", diff(o=None), 1), ("null-len-ok", diff(ql=None, kl=None), 7),
+    ("align-v", diff(v=A[2] + 4), 4), ("align-len", diff(kl=A[4] + 1), 4), ("align-lam", diff(lam=A[6] + 2), 4),
+    ("align-lam-ok", diff(lam=A[6] + 4), 7), ("align-w", diff(w=A[7] + 1), 4),
+    ("stride-k0", diff(ks=(2304, 0, 64)), 2), ("stride-odd", diff(vs=(2304, 576, 60)), 4),
+    ("o-rows-overlap", diff(os=(2560, 320, 32)), 8), ("o-tokens-first-ok", diff(os=(2560, 64, 512)), 7),
+    ("alias-q", diff(o=A[0] + 1024), 8), ("alias-len", diff(o=A[3] - 1024), 8), ("alias-lam", diff(o=A[6]), 8),
+    ("alias-w", diff(o=A[7]), 8), ("alias-w-unused", diff(o=A[7], flags=0), 7),
+    ("ws-null", diff(dt=0, ws=None), 10), ("ws-short", diff(dt=0, wsb=need - 1), 10), ("ws-align", diff(dt=0, ws=A[8] + 8), 4),
+    ("ws-alias-o", diff(dt=0, ws=A[5]), 8), ("ws-alias-q", diff(dt=0, ws=A[0]), 8), ("ws-unused-ok", diff(ws=None, wsb=0), 7),
+    ("ws-need", int(need > 0), 1), ("ws-bf16", wsz(2, 4, 2, 5, 9, 64, 1), 0), ("ws-bad", wsz(2, 4, 3, 5, 9, 64, 0), 0),
+]
+"""
+
+
 def _child(body):
     from gated_delta_rule_fwd_gb300.build import build
     build()
@@ -71,6 +107,10 @@ def test_axes_arguments_rejected_before_launch():
     """In a child without a GPU: a call that passes validation then fails at
     its launch (LR_ERR_CUDA, 7)."""
     _child(_AXES)
+
+
+def test_diff_arguments_rejected_before_launch():
+    _child(_DIFF)
 
 
 class _NoLaunch:
@@ -117,3 +157,26 @@ def test_axes_binding_accepts_what_it_should(lr):
 def test_axes_binding_refuses(lr, change):
     with pytest.raises((ValueError, TypeError)):
         lr.lr_qk_norm_rope_axes(**_axes_args(**change))
+
+
+def _diff_args(**change):
+    a = dict(q=_t(1, 4, 9, 64), k=_t(1, 2, 9, 64), v=_t(1, 2, 9, 64), lam=torch.zeros(2))
+    a.update(change)
+    return a
+
+
+def test_diff_binding_accepts_what_it_should(lr):
+    for change in (dict(), dict(norm=False), dict(norm_weight=torch.zeros(128)), dict(q_len=_i(1), k_len=_i(1))):
+        with pytest.raises(AssertionError, match="lr_fwd_diff"):
+            lr.lr_fwd_diff(**_diff_args(**change))
+
+
+@pytest.mark.parametrize("change", [
+    dict(q=_t(1, 3, 9, 64)), dict(k=_t(1, 3, 9, 64)), dict(k=_t(1, 2, 9, 32)), dict(v=_t(1, 2, 8, 64)), dict(v=_t(1, 1, 9, 128)),
+    dict(q=_t(4, 9, 64)), dict(q=_t(1, 4, 64, 9).transpose(2, 3)), dict(lam=torch.zeros(4)), dict(lam=_t(2)),
+    dict(lam=torch.zeros(4)[::2]), dict(norm_weight=torch.zeros(64)), dict(norm=False, norm_weight=torch.zeros(128)),
+    dict(q_len=_i(1, dtype=torch.int64)), dict(k_len=_i(2)), dict(o=_t(1, 4, 9, 32)), dict(window=1 << 40),
+    dict(q=_t(1, 4, 9, 64, dtype=torch.float16))], ids=lambda c: "-".join(c))
+def test_diff_binding_refuses(lr, change):
+    with pytest.raises((ValueError, TypeError)):
+        lr.lr_fwd_diff(**_diff_args(**change))
