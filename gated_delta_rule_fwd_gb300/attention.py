@@ -11,6 +11,8 @@
         the same attention for one new token per sequence over the cache
     lr_fwd_diff(q, k, v, lam, ...) -> o
         differential attention over whole sequences
+    lr_step_paged_diff(q, k_cache, v_cache, table, lens, lam, ...) -> o
+        the same for one new token per sequence over the cache
 
 Like the rest of the package this only marshals arguments; the functions are
 offered by the package itself.  Tensors may be on any device: the calls run
@@ -25,10 +27,11 @@ NO_WINDOW = (1 << 31) - 1   # a window that hides nothing
 QK_NORM = 0x1
 QK_INTERLEAVED = 0x2
 QK_ZERO_Q, QK_ZERO_K = 0x8, 0x10
-DIFF_NORM = 0x1
+DIFF_NORM, DIFF_FILL = 0x1, 0x2
 MAX_AXES = 16               # LR_MAX_AXES
 ATTN_SYMBOLS = ("lr_qk_norm_rope", "lr_qk_norm_rope_axes", "lr_fwd_window", "lr_step_paged", "lr_step_paged_fill",
-                "lr_step_paged_workspace_size", "lr_fwd_diff", "lr_fwd_diff_workspace_size")
+                "lr_step_paged_workspace_size", "lr_fwd_diff", "lr_fwd_diff_workspace_size",
+                "lr_step_paged_diff", "lr_step_paged_diff_workspace_size")
 
 
 class Strides(ctypes.Structure):
@@ -74,6 +77,11 @@ def declare(L):
                               [f, i, vp, sz, vp])
     L.lr_fwd_diff_workspace_size.restype = sz
     L.lr_fwd_diff_workspace_size.argtypes = [i] * 7
+    L.lr_step_paged_diff.restype = i
+    L.lr_step_paged_diff.argtypes = ([vp, ctypes.POINTER(Paged), vp, ctypes.POINTER(DiffMaps), vp] + [i] * 7 +
+                                     [f, i, vp, sz, vp])
+    L.lr_step_paged_diff_workspace_size.restype = sz
+    L.lr_step_paged_diff_workspace_size.argtypes = [i] * 8
     for step in (L.lr_step_paged, L.lr_step_paged_fill):
         step.restype = i
         step.argtypes = ([vp, ctypes.POINTER(Paged), vp, vp] + [i] * 7 + [f, i, vp, sz, vp])
@@ -480,4 +488,74 @@ def lr_step_paged(q, k_cache, v_cache, table, lens, *, max_len=None, window=None
               sinks, scale, dt, ws, ws_bytes, _handle(torch, dev))
     if st != 0:
         raise base.LrError(st, "lr_step_paged")
+    return o
+
+
+@functools.lru_cache(maxsize=1024)
+def _step_diff_workspace(N, H, Hk, d, max_len, window, sinks, dt):
+    """lr_step_paged_diff_workspace_size, a function of the sizes alone."""
+    return int(_base().lib().lr_step_paged_diff_workspace_size(N, H, Hk, d, max_len, window, sinks, dt))
+
+
+def step_paged_diff_workspace_size(N, H, Hk, d, max_len, dtype, window=None, sinks=0) -> int:
+    """lr_step_paged_diff_workspace_size for these sizes (H and Hk pairs of heads; dtype: torch dtype)."""
+    import torch
+    base = _base()
+    dt = base.F32 if dtype == torch.float32 else base.BF16
+    window = NO_WINDOW if window is None else _int32(window, "window")
+    return _step_diff_workspace(N, H, Hk, d, _int32(max_len, "max_len"), window, _int32(sinks, "sinks"), dt)
+
+
+def lr_step_paged_diff(q, k_cache, v_cache, table, lens, lam, *, max_len=None, window=None, sinks=0, scale=None,
+                       norm=True, norm_weight=None, eps=1e-6, o=None, workspace=None, stream=None):
+    """Differential attention of one new token per sequence over the paged cache
+    (``lr_step_paged_diff`` in include/lr_attn.h).
+
+    q: [N,2H,d]; k_cache, v_cache: [pages,2Hk,page,d], heads in pairs as for
+    :func:`lr_fwd_diff`; lam, norm, norm_weight, eps as there; table, lens,
+    max_len, window, sinks, scale, ``o`` as for :func:`lr_step_paged`.
+    ``workspace`` is a uint8 CUDA tensor of at least
+    ``step_paged_diff_workspace_size(...)`` bytes, allocated here when None.
+    Returns o: [N,2H,d]."""
+    import torch
+    base = _base()
+    dev = q.device
+    base._require_cuda(dev)
+    if stream is not None or torch.cuda.current_device() != dev.index:
+        with _place(torch, stream, dev):
+            return lr_step_paged_diff(q, k_cache, v_cache, table, lens, lam, max_len=max_len, window=window,
+                                      sinks=sinks, scale=scale, norm=norm, norm_weight=norm_weight, eps=eps, o=o,
+                                      workspace=workspace)
+    if q.dim() != 3:
+        raise ValueError("q must have shape (N, heads, d)")
+    q_shape, dtype = q.shape, q.dtype
+    N, H2, d = q_shape
+    dt = base._dtype_code(q)
+    _want(q, "q", q_shape, dtype, dev)
+    cache = _paged(torch, k_cache, v_cache, table, N, d, dtype, dev)
+    Hk2 = k_cache.shape[1]
+    if H2 % 2 or Hk2 % 2:
+        raise ValueError(f"heads come in pairs, got {H2} and {Hk2}")
+    if lens is None:
+        raise ValueError("lens is required")
+    _want(lens, "lens", (N,), torch.int32, dev)
+    maps = _diff_maps(torch, lam, norm, norm_weight, eps, H2 // 2, d, dev)
+    if o is not None:
+        _want(o, "o", q_shape, dtype, dev)
+    max_len = cache.page * cache.max_pages if max_len is None else _int32(max_len, "max_len")
+    window = NO_WINDOW if window is None else _int32(window, "window")
+    sinks = _int32(sinks, "sinks")
+    scale = d ** -0.5 if scale is None else float(scale)
+    step = base.lib().lr_step_paged_diff
+    need = 0
+    if workspace is None:
+        need = _step_diff_workspace(N, H2 // 2, Hk2 // 2, d, max_len, window, sinks, dt)
+    held, ws, ws_bytes = _scratch(torch, workspace, need, dev)
+    if o is None:
+        o = torch.empty(q_shape, dtype=dtype, device=dev)
+        maps.flags |= DIFF_FILL
+    st = step(q.data_ptr(), cache, lens.data_ptr(), maps, o.data_ptr(), N, H2 // 2, Hk2 // 2, d, max_len, window,
+              sinks, scale, dt, ws, ws_bytes, _handle(torch, dev))
+    if st != 0:
+        raise base.LrError(st, "lr_step_paged_diff")
     return o

@@ -181,15 +181,26 @@ size_t diff_workspace(int B, int H, int Tq, int Tk, int d, lr_dtype dt) {
     return dt == LR_DT_F32 && Tk > 0 ? diff_f32_workspace_bytes(B, H, Tq, d) : 0;
 }
 
-lr_status check_diff_maps(const lr_diff_maps *m, int H, int d, Span *lambda, Span *weight) {
+lr_status check_diff_maps(const lr_diff_maps *m, unsigned known, int H, int d, Span *lambda, Span *weight) {
     if (!m) return LR_ERR_NULL;
-    if (m->flags & ~LR_DIFF_NORM) return LR_ERR_FUSE;
+    if (m->flags & ~known) return LR_ERR_FUSE;
     const bool norm = m->flags & LR_DIFF_NORM;
     if (norm && !(m->eps >= 0.f && m->eps <= 3.4e38f)) return LR_ERR_FUSE;
     if (!m->lambda) return LR_ERR_NULL;
     if (!aligned4(m->lambda) || !aligned4(m->weight)) return LR_ERR_ALIGN;
     *lambda = span(m->lambda, (size_t)H * 4);
     *weight = span(norm ? m->weight : nullptr, (size_t)d * 8);
+    return LR_OK;
+}
+
+lr_status check_diff_step_sizes(int N, int H, int Hk, int d, int max_len, int window, int sinks, lr_dtype dt) {
+    const lr_status st = check_types(d, dt);
+    if (st != LR_OK) return st;
+    if (check_heads(H, Hk) != LR_OK || N < 1 || max_len < 1 || window < 1 || sinks < 0) return LR_ERR_SHAPE;
+    if (max_len > (1 << 30) || H > (1 << 29) || !count_ok(N, 2ll * H, 2ll * d, 1)) return LR_ERR_SHAPE;
+    // CTAs of one launch
+    const StepPlan p = diff_step_plan(N, H, Hk, d, max_len, window, sinks, dt);
+    if (!count_ok(N, H, p.splits, 1) || (long long)N * H * p.splits > 0x7fffffffll) return LR_ERR_SHAPE;
     return LR_OK;
 }
 
@@ -330,7 +341,7 @@ lr_status lr_fwd_diff(const void *q, lr_strides qs, const void *k, lr_strides ks
     if (st != LR_OK) return st;
     if (window < 1 || sinks < 0 || !isfinite(scale)) return LR_ERR_SHAPE;
     Span lambda, weight;
-    if ((st = check_diff_maps(maps, H, d, &lambda, &weight)) != LR_OK) return st;
+    if ((st = check_diff_maps(maps, LR_DIFF_NORM, H, d, &lambda, &weight)) != LR_OK) return st;
     if (Tq == 0) return LR_OK;
     if (!q || !o || (Tk > 0 && (!k || !v))) return LR_ERR_NULL;
     for (const void *p : {q, k, v, (const void *)o})
@@ -385,6 +396,42 @@ lr_status lr_step_paged_fill(const void *q, const lr_paged *cache, const int *le
                              cudaStream_t stream) {
     return step_paged(q, cache, lens, o, N, Hq, Hk, d, max_len, window, sinks, scale, dt, workspace,
                       workspace_bytes, true, stream);
+}
+
+lr_status lr_step_paged_diff(const void *q, const lr_paged *cache, const int *lens,
+                             const lr_diff_maps *maps, void *o, int N, int H, int Hk, int d,
+                             int max_len, int window, int sinks, float scale, lr_dtype dt,
+                             void *workspace, size_t workspace_bytes, cudaStream_t stream) {
+    lr_status st = check_diff_step_sizes(N, H, Hk, d, max_len, window, sinks, dt);
+    if (st != LR_OK) return st;
+    if (!isfinite(scale)) return LR_ERR_SHAPE;
+    Span lambda, weight;
+    if ((st = check_diff_maps(maps, LR_DIFF_NORM | LR_DIFF_FILL, H, d, &lambda, &weight)) != LR_OK) return st;
+    if (!q || !cache || !lens || !o) return LR_ERR_NULL;
+    Span ck, cv, ct;
+    if ((st = check_paged(cache, N, 2 * Hk, d, dt, &ck, &cv, &ct)) != LR_OK) return st;
+    if ((long long)max_len > (long long)cache->page * cache->max_pages) return LR_ERR_SHAPE;
+    if (!aligned16(q) || !aligned16(o) || !aligned4(lens)) return LR_ERR_ALIGN;
+    const size_t need = lr_step_paged_diff_workspace_size(N, H, Hk, d, max_len, window, sinks, dt);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return LR_ERR_WORKSPACE;
+    if (need > 0 && !aligned16(workspace)) return LR_ERR_ALIGN;
+    const size_t rows = (size_t)N * 2 * H * d * esize(dt);
+    const Span so = span(o, rows), sq = span(q, rows), sl = span(lens, (size_t)N * 4);
+    const Span sw = span(need > 0 ? workspace : nullptr, need);
+    for (const Span &i : {sq, sl, ck, cv, ct, lambda, weight})
+        if (overlap(so, i) || overlap(sw, i)) return LR_ERR_ALIAS;
+    if (overlap(so, sw)) return LR_ERR_ALIAS;
+    const StepArgs a{q, cache->k, cache->v, o, cache->table, lens, N, H, Hk, max_len, window, sinks,
+                     cache->num_pages, log2_of(cache->page), cache->max_pages, scale,
+                     (maps->flags & LR_DIFF_FILL) != 0};
+    return done(launch_step_diff(a, maps->lambda, maps->weight, maps->eps, (maps->flags & LR_DIFF_NORM) != 0, d, dt,
+                                 workspace, stream));
+}
+
+size_t lr_step_paged_diff_workspace_size(int N, int H, int Hk, int d, int max_len, int window,
+                                         int sinks, lr_dtype dt) {
+    if (check_diff_step_sizes(N, H, Hk, d, max_len, window, sinks, dt) != LR_OK) return 0;
+    return diff_step_workspace_bytes(N, H, d, diff_step_plan(N, H, Hk, d, max_len, window, sinks, dt));
 }
 
 }  // extern "C"

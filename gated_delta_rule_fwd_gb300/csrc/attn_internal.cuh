@@ -177,8 +177,16 @@ struct StepPlan {
     int chunk, splits;
     bool cluster;
 };
+// The cut of `rows` CTAs' keys, `seen` at most, where per_sm of them run on an
+// SM and clusters find `room` (a row of kClusterRoom).
+StepPlan plan_chunks(int seen, long long rows, int per_sm, const int *room);
 StepPlan step_plan(int N, int Hq, int Hk, int d, int max_len, int window, int sinks, lr_dtype dt);
 size_t step_workspace_bytes(int N, int Hq, int d, const StepPlan &p);
+// Differential attention's step: a.Hq and a.Hk count pairs.
+StepPlan diff_step_plan(int N, int H, int Hk, int d, int max_len, int window, int sinks, lr_dtype dt);
+size_t diff_step_workspace_bytes(int N, int H, int d, const StepPlan &p);
+cudaError_t launch_step_diff(const StepArgs &a, const float *lambda, const float *weight, float eps, bool norm, int d,
+                             lr_dtype dt, void *ws, cudaStream_t stream);
 cudaError_t launch_step_paged(const StepArgs &a, int d, lr_dtype dt, void *ws, cudaStream_t stream);
 
 // Return and clear the error bits of each unit (-1: the device could not be read).
@@ -187,5 +195,6 @@ int attn_errors_window_f32();
 int attn_errors_window_tc();
 int attn_errors_step();
 int attn_errors_diff_tc();
+int attn_errors_step_diff();
 
 }  // namespace lr

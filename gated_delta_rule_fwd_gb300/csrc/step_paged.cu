@@ -34,6 +34,7 @@
 // writes a row finds them.
 #include "attn_internal.cuh"
 #include "attn_rows.cuh"
+#include "attn_step.cuh"
 #include "tc_common.cuh"
 
 namespace lr {
@@ -51,12 +52,6 @@ struct Parts {
     int splits, chunk;
     bool cluster;  // the chunks of a row are the CTAs of a cluster
 };
-
-__device__ __forceinline__ float ld_cluster(uint32_t addr) {
-    float r;
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(r) : "r"(addr) : "memory");
-    return r;
-}
 
 // Rows of a sequence that is not computed.
 template <typename E, int D>
@@ -182,12 +177,6 @@ __device__ __forceinline__ void finish(float (&so)[NT / 32][HEADS][P], float (&s
         for (int h = tid >> 5; h < heads; h += NT / 32)
             if (h * D / NT % parts.splits == split)  // a row that was written here
                 mend_step_row<E, D>(a, n, h0 + h, f, [&] { return sml[1][h][1]; });
-}
-
-__device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
-    const float4 a = __ldg(reinterpret_cast<const float4 *>(p)),
-                 b = __ldg(reinterpret_cast<const float4 *>(p + 4));
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
 }
 
 template <int D, int GC>
@@ -317,41 +306,6 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts, 
 }
 
 // ------------------------------------------------------------------- bf16
-
-constexpr int kTile = 16;            // keys of a product
-constexpr int kMostTiles = 256;      // of a chunk
-
-// D (16x8, fp32) += A (16x16, bf16) B (16x8, bf16), fragments as in the PTX
-// m16n8k16 layout (g = lane / 4, t = lane % 4): a = {A[g][2t..], A[g+8][2t..],
-// A[g][2t+8..], A[g+8][2t+8..]}, b = {B[2t..][g], B[2t+8..][g]}, d = {D[g][2t],
-// D[g][2t+1], D[g+8][2t], D[g+8][2t+1]}.
-__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
-                                         uint32_t a3, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-        "{%8,%9}, {%0,%1,%2,%3};"
-        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// An 8 x 8 matrix of 16-bit values, two per lane, transposed across the warp.
-__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
-    uint32_t r;
-    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
-    return r;
-}
-// Cache rows are read once: past L1.
-__device__ __forceinline__ uint4 load_once16(const void *p) {
-    uint4 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w)
-                 : "l"(p));
-    return r;
-}
-__device__ __forceinline__ uint2 load_once8(const void *p) {
-    uint2 r;
-    asm volatile("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "l"(p));
-    return r;
-}
 
 // NH: 8-head column blocks of the products.
 template <int D, int NH>
@@ -627,33 +581,15 @@ int heads_of_cta(int G, lr_dtype dt) {
     return G == 1 ? 1 : G == 2 ? 2 : 4;
 }
 
-// Launches a step kernel, its chunks as clusters where the plan says so.
-cudaError_t launch_parts(void (*fn)(StepArgs, Parts, ScoreFactor), unsigned grid, cudaStream_t stream,
-                         const StepArgs &a, const Parts &parts, ScoreFactor f) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(NT);
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    if (parts.cluster) {
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = (unsigned)parts.splits;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
-    }
-    return cudaLaunchKernelEx(&cfg, fn, a, parts, f);
-}
-
 template <int D>
 cudaError_t launch_f32(const StepArgs &a, const Parts &parts, cudaStream_t stream) {
     const int G = a.Hq / a.Hk;
     const int gc = heads_of_cta(G, LR_DT_F32);
     const unsigned grid = (unsigned)(a.N * a.Hk * ((G + gc - 1) / gc) * parts.splits);
     const ScoreFactor f = score_factor(a.scale);
-    if (gc == 1) return launch_parts(&step_simt_kernel<D, 1>, grid, stream, a, parts, f);
-    if (gc == 2) return launch_parts(&step_simt_kernel<D, 2>, grid, stream, a, parts, f);
-    return launch_parts(&step_simt_kernel<D, 4>, grid, stream, a, parts, f);
+    if (gc == 1) return launch_cut(&step_simt_kernel<D, 1>, grid, NT, parts.cluster ? parts.splits : 1, stream, a, parts, f);
+    if (gc == 2) return launch_cut(&step_simt_kernel<D, 2>, grid, NT, parts.cluster ? parts.splits : 1, stream, a, parts, f);
+    return launch_cut(&step_simt_kernel<D, 4>, grid, NT, parts.cluster ? parts.splits : 1, stream, a, parts, f);
 }
 
 template <int D>
@@ -661,8 +597,8 @@ cudaError_t launch_bf16(const StepArgs &a, const Parts &parts, cudaStream_t stre
     const int G = a.Hq / a.Hk, heads = heads_of_cta(G, LR_DT_BF16);
     const unsigned grid = (unsigned)(a.N * a.Hk * ((G + heads - 1) / heads) * parts.splits);
     const ScoreFactor f = score_factor(a.scale);
-    if (heads == 8) return launch_parts(&step_mma_kernel<D, 1>, grid, stream, a, parts, f);
-    return launch_parts(&step_mma_kernel<D, 2>, grid, stream, a, parts, f);
+    if (heads == 8) return launch_cut(&step_mma_kernel<D, 1>, grid, NT, parts.cluster ? parts.splits : 1, stream, a, parts, f);
+    return launch_cut(&step_mma_kernel<D, 2>, grid, NT, parts.cluster ? parts.splits : 1, stream, a, parts, f);
 }
 
 template <int D>
@@ -680,20 +616,8 @@ cudaError_t launch(const StepArgs &a, void *ws, lr_dtype dt, cudaStream_t stream
 
 }  // namespace
 
-StepPlan step_plan(int N, int Hq, int Hk, int d, int max_len, int window, int sinks, lr_dtype dt) {
-    const long long w = (long long)window + sinks;
-    // whole tiles in bf16: the sinks' and the window's first and last may be cut
-    const long long most = w < max_len ? w + (dt == LR_DT_BF16 ? 2 * kTile + (sinks > 0 ? kTile : 0) : 0) : max_len;
-    const int seen = (int)(most < max_len ? most : max_len);
-    // CTAs that run at once: an SM holds the registers of three of the bf16
-    // kernel at d = 128 (two with more than 8 heads; more at smaller widths,
-    // where one wave matters less), of three in fp32 with four heads, else of
-    // four or five (33 sequences with window 1024: 26 us with 4, 39 with 3, 33
-    // with 6).
-    const int G = Hq / Hk, heads = heads_of_cta(G, dt);
-    const int per_sm = dt == LR_DT_BF16 ? (heads == 8 ? 3 : 2) : (heads == 4 ? 3 : 4);
-    const int *room = kClusterRoom[(dt == LR_DT_BF16 && d < 128 ? 4 : per_sm) - 1];
-    const long long rows = (long long)N * Hk * ((G + heads - 1) / heads), wave = 152 * per_sm;
+StepPlan plan_chunks(int seen, long long rows, int per_sm, const int *room) {
+    const long long wave = 152 * per_sm;
     auto cut = [](long long keys, long long parts) {  // chunks of whole 64s, 64 at least
         const long long c = ((keys + parts - 1) / parts + 63) / 64 * 64;
         return c < 64 ? 64 : c;
@@ -727,6 +651,22 @@ StepPlan step_plan(int N, int Hq, int Hk, int d, int max_len, int window, int si
         p.cluster = p.splits > 1;
     }
     return p;
+}
+
+StepPlan step_plan(int N, int Hq, int Hk, int d, int max_len, int window, int sinks, lr_dtype dt) {
+    const long long w = (long long)window + sinks;
+    // whole tiles in bf16: the sinks' and the window's first and last may be cut
+    const long long most = w < max_len ? w + (dt == LR_DT_BF16 ? 2 * kTile + (sinks > 0 ? kTile : 0) : 0) : max_len;
+    const int seen = (int)(most < max_len ? most : max_len);
+    // CTAs that run at once: an SM holds the registers of three of the bf16
+    // kernel at d = 128 (two with more than 8 heads; more at smaller widths,
+    // where one wave matters less), of three in fp32 with four heads, else of
+    // four or five (33 sequences with window 1024: 26 us with 4, 39 with 3, 33
+    // with 6).
+    const int G = Hq / Hk, heads = heads_of_cta(G, dt);
+    const int per_sm = dt == LR_DT_BF16 ? (heads == 8 ? 3 : 2) : (heads == 4 ? 3 : 4);
+    const int *room = kClusterRoom[(dt == LR_DT_BF16 && d < 128 ? 4 : per_sm) - 1];
+    return plan_chunks(seen, (long long)N * Hk * ((G + heads - 1) / heads), per_sm, room);
 }
 
 size_t step_workspace_bytes(int N, int Hq, int d, const StepPlan &p) {

@@ -13,6 +13,8 @@
  *                     the paged cache
  *   lr_fwd_diff       differential attention over whole sequences: the
  *                     difference of two softmax maps, with its norm
+ *   lr_step_paged_diff  the same for one new token per sequence over the paged
+ *                     cache
  *
  * Conventions are those of lr.h: device pointers owned by the caller, 16-byte
  * aligned (int32 arrays: 4-byte); arguments validated on the host before any launch, so that a call
@@ -188,6 +190,7 @@ lr_status lr_fwd_window(const void *q, lr_strides qs, const void *k, lr_strides 
  * than fp32 holds is divided by infinity.
  */
 #define LR_DIFF_NORM 0x1u /* the root-mean-square norm over the pair's 2 d channels */
+#define LR_DIFF_FILL 0x2u /* lr_step_paged_diff: rows of unused slots are written as zeros */
 
 typedef struct {
     unsigned flags;       /* OR of LR_DIFF_*                            */
@@ -255,6 +258,30 @@ lr_status lr_step_paged_fill(const void *q, const lr_paged *cache, const int *le
  * arguments they would reject). */
 size_t lr_step_paged_workspace_size(int N, int Hq, int Hk, int d, int max_len, int window,
                                     int sinks, lr_dtype dt);
+
+/*
+ * One decode step of lr_fwd_diff, as lr_step_paged is one of lr_fwd_window.
+ *
+ *   q       [N, 2 H, d], contiguous
+ *   cache   pools [num_pages, 2 Hk, page, d]: the keys of both maps, and the two
+ *           halves of every value row, as lr_qk_norm_rope writes them from 2 Hk
+ *           heads
+ *   o       [N, 2 H, d], written; overlaps no input
+ *   lens, max_len, window, sinks, scale as for lr_step_paged (with LR_DIFF_FILL
+ *           the rows that it would leave as they were are zeros)
+ *   workspace   lr_step_paged_diff_workspace_size(...) bytes, 16-byte aligned
+ *
+ * A repeated call gives the same bits.  Up to 8 pairs of query heads of a pair
+ * of key heads in bf16, and 2 in fp32, share one read of the cache.
+ */
+lr_status lr_step_paged_diff(const void *q, const lr_paged *cache, const int *lens,
+                             const lr_diff_maps *maps, void *o, int N, int H, int Hk, int d,
+                             int max_len, int window, int sinks, float scale, lr_dtype dt,
+                             void *workspace, size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes lr_step_paged_diff needs (0 as well for arguments it would reject). */
+size_t lr_step_paged_diff_workspace_size(int N, int H, int Hk, int d, int max_len, int window,
+                                         int sinks, lr_dtype dt);
 
 #ifdef __cplusplus
 }

@@ -197,3 +197,26 @@ def diff(q, k, v, lam, window, sinks, scale, dtype_bits, weight_bits=None, weigh
                 o[b, 2 * h + half, :ql] = y[:, half * d:(half + 1) * d]
                 bound[b, 2 * h + half, :ql] = e[:, half * d:(half + 1) * d]
     return o, bound, written
+
+
+def diff_step(q, k_cache, v_cache, table, lens, lam, window, sinks, scale, dtype_bits, weight_bits=None, weight=None,
+              eps=None):
+    """q [N,2H,d], pools [P,2Hk,page,d] -> (o, bound, written [N])."""
+    q, k_cache, v_cache = (np.asarray(x, np.float64) for x in (q, k_cache, v_cache))
+    N, H2, d = q.shape
+    Hk2, page = k_cache.shape[1:3]
+    o, bound, written = np.zeros(q.shape), np.zeros(q.shape), np.zeros(N, bool)
+    for n in range(N):
+        L = int(lens[n])
+        written[n] = L >= 0
+        keys = np.array([j for j in range(L) if sees(L - 1, j, L, window, sinks)], int)
+        where, rows = np.asarray(table)[n][keys // page], keys % page
+        seen = np.ones((1, len(keys)), bool)
+        for h in range(H2 // 2):
+            g = h // (H2 // Hk2)
+            k = [k_cache[where, 2 * g + m, rows] for m in range(2)]
+            v = np.concatenate([v_cache[where, 2 * g + m, rows] for m in range(2)], -1)
+            y, e = diff_rows(q[n, 2 * h][None], q[n, 2 * h + 1][None], *k, v, seen, scale, float(lam[h]), d, dtype_bits,
+                             weight_bits, weight, eps)
+            o[n, 2 * h:2 * h + 2], bound[n, 2 * h:2 * h + 2] = y.reshape(2, d), e.reshape(2, d)
+    return o, bound, written

@@ -94,6 +94,38 @@ cases = [
 """
 
 
+_DIFF_STEP = r"""
+def step(**kw):
+    a = dict(q=A[0], ck=A[1], cv=A[2], tab=A[3], lens=A[4], o=A[5], lam=A[6], w=A[7], ws=A[8], wsb=1 << 27, flags=1,
+             eps=1e-6, N=3, H=4, Hk=2, d=64, most_len=9000, win=1 << 30, s=0, scale=0.5, dt=1, pages=9, page=16,
+             most=600, cache=True, maps=True)
+    a.update(kw)
+    c = Paged(a['ck'], a['cv'], a['tab'], a['pages'], a['page'], a['most'])
+    m = DiffMaps(a['flags'], a['lam'], a['w'], a['eps'])
+    return L.lr_step_paged_diff(P(a['q']), ctypes.byref(c) if a['cache'] else None, P(a['lens']),
+                                ctypes.byref(m) if a['maps'] else None, P(a['o']), a['N'], a['H'], a['Hk'], a['d'],
+                                a['most_len'], a['win'], a['s'], a['scale'], a['dt'], P(a['ws']), a['wsb'], None)
+wsz = lambda *a: L.lr_step_paged_diff_workspace_size(*a)
+need = wsz(3, 4, 2, 64, 9000, 1 << 30, 0, 1)
+cases = [
+    ("ok", step(), 7), ("f32-ok", step(dt=0), 7), ("fill-ok", step(flags=3), 7), ("flag", step(flags=4), 12),
+    ("dtype", step(dt=9), 3), ("d16", step(d=16), 6), ("N0", step(N=0), 2), ("heads", step(H=3), 2),
+    ("window", step(win=0), 2), ("sinks", step(s=-2), 2), ("scale", step(scale=nan), 2), ("maxlen0", step(most_len=0), 2),
+    ("maxlen-table", step(most_len=16 * 600 + 1), 2), ("null-lens", step(lens=None), 1), ("null-cache", step(cache=False), 1),
+    ("null-pool", step(cv=None), 1), ("null-maps", step(maps=False), 1), ("null-lam", step(lam=None), 1),
+    ("null-w-ok", step(w=None), 7), ("page", step(page=512), 6), ("eps", step(eps=inf), 12),
+    ("align-o", step(o=A[5] + 8), 4), ("align-lam", step(lam=A[6] + 2), 4), ("alias-q", step(o=A[0]), 8),
+    ("alias-pool", step(o=A[2] + 64), 8), ("alias-lam", step(o=A[6]), 8), ("alias-w", step(o=A[7]), 8),
+    # the pools hold 2 Hk heads: 9 x 4 x 16 x 64 x 2 bytes
+    ("alias-pool-end", step(o=A[2] + 9 * 4 * 16 * 64 * 2 - 16), 8), ("alias-pool-behind-ok", step(o=A[2] + 9 * 4 * 16 * 64 * 2), 7),
+    ("ws-null", step(ws=None), 10), ("ws-short", step(wsb=need - 1), 10), ("ws-align", step(ws=A[8] + 8), 4),
+    ("ws-alias", step(ws=A[5]), 8), ("many", step(N=1 << 30, H=4, Hk=4), 2),
+    ("ws-split", int(need > 0), 1), ("ws-one-chunk", wsz(3, 4, 2, 64, 64, 1 << 30, 0, 1), 0),
+    ("ws-cluster", wsz(3, 4, 2, 64, 300, 1 << 30, 0, 1), 0), ("ws-bad", wsz(3, 4, 3, 64, 300, 1, 0, 1), 0),
+]
+"""
+
+
 def _child(body):
     from gated_delta_rule_fwd_gb300.build import build
     build()
@@ -111,6 +143,24 @@ def test_axes_arguments_rejected_before_launch():
 
 def test_diff_arguments_rejected_before_launch():
     _child(_DIFF)
+
+
+def test_diff_step_arguments_rejected_before_launch():
+    _child(_DIFF_STEP)
+
+
+def test_struct_sizes_match_the_header():
+    import ctypes
+    from gated_delta_rule_fwd_gb300 import attention as at
+    src = ('#include "lr_attn.h"\n'
+           f"_Static_assert(sizeof(lr_diff_maps) == {ctypes.sizeof(at.DiffMaps)}, \"maps\");\n"
+           f"_Static_assert(LR_MAX_AXES == {at.MAX_AXES} && LR_DIFF_NORM == {at.DIFF_NORM}, \"values\");\n"
+           f"_Static_assert(LR_DIFF_FILL == {at.DIFF_FILL}, \"values\");\n"
+           "int main(void) { return 0; }\n")
+    inc = [a for d in ("/usr/local/cuda/include",) if os.path.isdir(d) for a in ("-I", d)]
+    r = subprocess.run(["gcc", "-std=c11", "-fsyntax-only", "-x", "c", "-I", os.path.join(ROOT, "include"),
+                        *inc, "-"], input=src, capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
 
 
 class _NoLaunch:
@@ -180,3 +230,26 @@ def test_diff_binding_accepts_what_it_should(lr):
 def test_diff_binding_refuses(lr, change):
     with pytest.raises((ValueError, TypeError)):
         lr.lr_fwd_diff(**_diff_args(**change))
+
+
+def _diff_step_args(**change):
+    a = dict(q=_t(3, 4, 64), k_cache=_t(5, 2, 16, 64), v_cache=_t(5, 2, 16, 64), table=_i(3, 4), lens=_i(3),
+             lam=torch.zeros(2))
+    a.update(change)
+    return a
+
+
+def test_diff_step_binding_accepts_what_it_should(lr):
+    for change in (dict(max_len=60), dict(norm=False), dict(norm_weight=torch.zeros(128))):
+        with pytest.raises(AssertionError, match="lr_step_paged_diff"):
+            lr.lr_step_paged_diff(**_diff_step_args(**change))
+
+
+@pytest.mark.parametrize("change", [
+    dict(q=_t(3, 3, 64)), dict(k_cache=_t(5, 3, 16, 64), v_cache=_t(5, 3, 16, 64)), dict(q=_t(1, 3, 4, 64)),
+    dict(v_cache=_t(5, 1, 16, 128)), dict(table=_i(2, 4)), dict(lens=_i(4)), dict(lens=None), dict(lam=torch.zeros(3)),
+    dict(lam=None), dict(norm=False, norm_weight=torch.zeros(128)), dict(o=_t(3, 4, 32)), dict(max_len=1 << 33)],
+    ids=lambda c: "-".join(c))
+def test_diff_step_binding_refuses(lr, change):
+    with pytest.raises((ValueError, TypeError, AttributeError)):
+        lr.lr_step_paged_diff(**_diff_step_args(**change))
