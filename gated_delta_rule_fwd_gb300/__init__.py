@@ -31,7 +31,8 @@ import os
 
 from .attention import (ATTN_SYMBOLS, NO_WINDOW, diff_workspace_size, lr_fwd_diff, lr_fwd_window,
                         lr_qk_norm_rope, lr_qk_norm_rope_axes, lr_step_paged, lr_step_paged_diff,
-                        step_paged_diff_workspace_size, step_paged_workspace_size)
+                        lr_step_paged_prefix, step_paged_diff_workspace_size,
+                        step_paged_prefix_workspace_size, step_paged_workspace_size)
 from .attention import declare as _declare_attention
 from .build import LIB_PATH
 

@@ -9,6 +9,8 @@
         causal attention over whole sequences with a sliding window and sinks
     lr_step_paged(q, k_cache, v_cache, table, lens, ...) -> o
         the same attention for one new token per sequence over the cache
+    lr_step_paged_prefix(q, k_cache, v_cache, prefix, prefix_len, table, lens, ...) -> o
+        that step for a batch that shares a long prefix
     lr_fwd_diff(q, k, v, lam, ...) -> o
         differential attention over whole sequences
     lr_step_paged_diff(q, k_cache, v_cache, table, lens, lam, ...) -> o
@@ -28,10 +30,12 @@ QK_NORM = 0x1
 QK_INTERLEAVED = 0x2
 QK_ZERO_Q, QK_ZERO_K = 0x8, 0x10
 DIFF_NORM, DIFF_FILL = 0x1, 0x2
+STEP_FILL = 0x1
 MAX_AXES = 16               # LR_MAX_AXES
 ATTN_SYMBOLS = ("lr_qk_norm_rope", "lr_qk_norm_rope_axes", "lr_fwd_window", "lr_step_paged", "lr_step_paged_fill",
                 "lr_step_paged_workspace_size", "lr_fwd_diff", "lr_fwd_diff_workspace_size",
-                "lr_step_paged_diff", "lr_step_paged_diff_workspace_size")
+                "lr_step_paged_diff", "lr_step_paged_diff_workspace_size", "lr_step_paged_prefix",
+                "lr_step_paged_prefix_workspace_size")
 
 
 class Strides(ctypes.Structure):
@@ -82,6 +86,11 @@ def declare(L):
                                      [f, i, vp, sz, vp])
     L.lr_step_paged_diff_workspace_size.restype = sz
     L.lr_step_paged_diff_workspace_size.argtypes = [i] * 8
+    L.lr_step_paged_prefix.restype = i
+    L.lr_step_paged_prefix.argtypes = ([vp, ctypes.POINTER(Paged), vp, i, vp, vp] + [i] * 7 +
+                                       [f, ctypes.c_uint, i, vp, sz, vp])
+    L.lr_step_paged_prefix_workspace_size.restype = sz
+    L.lr_step_paged_prefix_workspace_size.argtypes = [i] * 9
     for step in (L.lr_step_paged, L.lr_step_paged_fill):
         step.restype = i
         step.argtypes = ([vp, ctypes.POINTER(Paged), vp, vp] + [i] * 7 + [f, i, vp, sz, vp])
@@ -558,4 +567,77 @@ def lr_step_paged_diff(q, k_cache, v_cache, table, lens, lam, *, max_len=None, w
               sinks, scale, dt, ws, ws_bytes, _handle(torch, dev))
     if st != 0:
         raise base.LrError(st, "lr_step_paged_diff")
+    return o
+
+
+@functools.lru_cache(maxsize=1024)
+def _step_prefix_workspace(N, Hq, Hk, d, prefix_len, max_len, window, sinks, dt):
+    """lr_step_paged_prefix_workspace_size, a function of the sizes alone."""
+    return int(_base().lib().lr_step_paged_prefix_workspace_size(N, Hq, Hk, d, prefix_len, max_len, window, sinks, dt))
+
+
+def step_paged_prefix_workspace_size(N, Hq, Hk, d, prefix_len, max_len, dtype, window=None, sinks=0) -> int:
+    """lr_step_paged_prefix_workspace_size for these sizes (dtype: torch dtype)."""
+    import torch
+    base = _base()
+    dt = base.F32 if dtype == torch.float32 else base.BF16
+    window = NO_WINDOW if window is None else _int32(window, "window")
+    return _step_prefix_workspace(N, Hq, Hk, d, _int32(prefix_len, "prefix_len"), _int32(max_len, "max_len"), window,
+                                  _int32(sinks, "sinks"), dt)
+
+
+def lr_step_paged_prefix(q, k_cache, v_cache, prefix, prefix_len, table, lens, *, max_len=None, window=None, sinks=0,
+                         scale=None, o=None, workspace=None, stream=None):
+    """:func:`lr_step_paged` for sequences that begin with the same tokens
+    (``lr_step_paged_prefix`` in include/lr_attn.h).
+
+    prefix: [pages] int32 pages of the shared prefix, in the same pools;
+    prefix_len: its tokens (an int).  table and lens are of each sequence's own
+    tokens behind it (lens 0: the row of the prefix's last token).  window and
+    sinks count in positions of the whole sequence; q, k_cache, v_cache, max_len,
+    scale, ``o`` as for :func:`lr_step_paged`.  ``workspace`` is a uint8 CUDA
+    tensor of at least ``step_paged_prefix_workspace_size(...)`` bytes, allocated
+    here when None.  Returns o: [N,Hq,d]."""
+    import torch
+    base = _base()
+    dev = q.device
+    base._require_cuda(dev)
+    if stream is not None or torch.cuda.current_device() != dev.index:
+        with _place(torch, stream, dev):
+            return lr_step_paged_prefix(q, k_cache, v_cache, prefix, prefix_len, table, lens, max_len=max_len,
+                                        window=window, sinks=sinks, scale=scale, o=o, workspace=workspace)
+    if q.dim() != 3:
+        raise ValueError("q must have shape (N, heads, d)")
+    q_shape, dtype = q.shape, q.dtype
+    N, Hq, d = q_shape
+    dt = base._dtype_code(q)
+    _want(q, "q", q_shape, dtype, dev)
+    cache = _paged(torch, k_cache, v_cache, table, N, d, dtype, dev)
+    Hk = k_cache.shape[1]
+    prefix_len = _int32(prefix_len, "prefix_len")
+    if prefix is None or lens is None:
+        raise ValueError("prefix and lens are required")
+    if prefix.dim() != 1 or prefix.shape[0] * cache.page < prefix_len:
+        raise ValueError(f"prefix must have shape (pages,) with room for {prefix_len} tokens, got {tuple(prefix.shape)}")
+    _want(prefix, "prefix", prefix.shape, torch.int32, dev)
+    _want(lens, "lens", (N,), torch.int32, dev)
+    if o is not None:
+        _want(o, "o", q_shape, dtype, dev)
+    max_len = cache.page * cache.max_pages if max_len is None else _int32(max_len, "max_len")
+    window = NO_WINDOW if window is None else _int32(window, "window")
+    sinks = _int32(sinks, "sinks")
+    scale = d ** -0.5 if scale is None else float(scale)
+    step = base.lib().lr_step_paged_prefix
+    need = 0
+    if workspace is None:
+        need = _step_prefix_workspace(N, Hq, Hk, d, prefix_len, max_len, window, sinks, dt)
+    held, ws, ws_bytes = _scratch(torch, workspace, need, dev)
+    flags = 0
+    if o is None:
+        o = torch.empty(q_shape, dtype=dtype, device=dev)
+        flags = STEP_FILL
+    st = step(q.data_ptr(), cache, prefix.data_ptr(), prefix_len, lens.data_ptr(), o.data_ptr(), N, Hq, Hk, d, max_len,
+              window, sinks, scale, flags, dt, ws, ws_bytes, _handle(torch, dev))
+    if st != 0:
+        raise base.LrError(st, "lr_step_paged_prefix")
     return o

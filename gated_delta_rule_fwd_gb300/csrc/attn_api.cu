@@ -159,7 +159,8 @@ lr_status step_paged(const void *q, const lr_paged *cache, const int *lens, void
     for (const Span &i : {sq, sl, ck, cv, ct})
         if (overlap(sw, i)) return LR_ERR_ALIAS;
     const StepArgs a{q, cache->k, cache->v, o, cache->table, lens, N, Hq, Hk, max_len, window,
-                     sinks, cache->num_pages, log2_of(cache->page), cache->max_pages, scale, fill};
+                     sinks, cache->num_pages, log2_of(cache->page), cache->max_pages, scale, fill,
+                     nullptr, 0, sinks, 0, nullptr, nullptr};
     return done(launch_step_paged(a, d, dt, workspace, stream));
 }
 
@@ -190,6 +191,22 @@ lr_status check_diff_maps(const lr_diff_maps *m, unsigned known, int H, int d, S
     if (!aligned4(m->lambda) || !aligned4(m->weight)) return LR_ERR_ALIGN;
     *lambda = span(m->lambda, (size_t)H * 4);
     *weight = span(norm ? m->weight : nullptr, (size_t)d * 8);
+    return LR_OK;
+}
+
+// Sinks among a sequence's own tokens.
+int own_sinks(int sinks, int prefix_len) { return sinks > prefix_len ? sinks - prefix_len : 0; }
+
+lr_status check_prefix_sizes(int N, int Hq, int Hk, int d, int prefix_len, int max_len, int window, int sinks,
+                             lr_dtype dt) {
+    if (prefix_len < 0 || sinks < 0 || (long long)prefix_len + max_len > (1ll << 30)) return LR_ERR_SHAPE;
+    const lr_status st = check_step_sizes(N, Hq, Hk, d, max_len, window, own_sinks(sinks, prefix_len), dt);
+    if (st != LR_OK) return st;
+    // rows as an int, CTAs of one launch and the parts' elements
+    const PrefixPlan p = prefix_plan(N, Hq, Hk, d, prefix_len, window, sinks, dt);
+    if ((long long)N * Hq > (1ll << 30) || !count_ok(N, Hq, p.parts, d) ||
+        ((long long)N * (Hq / Hk) / 64 + 1) * Hk > 0x7fffffffll / (p.parts ? p.parts : 1))
+        return LR_ERR_SHAPE;
     return LR_OK;
 }
 
@@ -423,7 +440,7 @@ lr_status lr_step_paged_diff(const void *q, const lr_paged *cache, const int *le
     if (overlap(so, sw)) return LR_ERR_ALIAS;
     const StepArgs a{q, cache->k, cache->v, o, cache->table, lens, N, H, Hk, max_len, window, sinks,
                      cache->num_pages, log2_of(cache->page), cache->max_pages, scale,
-                     (maps->flags & LR_DIFF_FILL) != 0};
+                     (maps->flags & LR_DIFF_FILL) != 0, nullptr, 0, sinks, 0, nullptr, nullptr};
     return done(launch_step_diff(a, maps->lambda, maps->weight, maps->eps, (maps->flags & LR_DIFF_NORM) != 0, d, dt,
                                  workspace, stream));
 }
@@ -432,6 +449,44 @@ size_t lr_step_paged_diff_workspace_size(int N, int H, int Hk, int d, int max_le
                                          int sinks, lr_dtype dt) {
     if (check_diff_step_sizes(N, H, Hk, d, max_len, window, sinks, dt) != LR_OK) return 0;
     return diff_step_workspace_bytes(N, H, d, diff_step_plan(N, H, Hk, d, max_len, window, sinks, dt));
+}
+
+lr_status lr_step_paged_prefix(const void *q, const lr_paged *cache, const int *prefix,
+                               int prefix_len, const int *lens, void *o, int N, int Hq, int Hk,
+                               int d, int max_len, int window, int sinks, float scale,
+                               unsigned flags, lr_dtype dt, void *workspace,
+                               size_t workspace_bytes, cudaStream_t stream) {
+    lr_status st = check_prefix_sizes(N, Hq, Hk, d, prefix_len, max_len, window, sinks, dt);
+    if (st != LR_OK) return st;
+    if (!isfinite(scale)) return LR_ERR_SHAPE;
+    if (flags & ~LR_STEP_FILL) return LR_ERR_FUSE;
+    if (!q || !cache || !lens || !o || (prefix_len > 0 && !prefix)) return LR_ERR_NULL;
+    Span ck, cv, ct;
+    if ((st = check_paged(cache, N, Hk, d, dt, &ck, &cv, &ct)) != LR_OK) return st;
+    if ((long long)max_len > (long long)cache->page * cache->max_pages) return LR_ERR_SHAPE;
+    if (!aligned16(q) || !aligned16(o) || !aligned4(lens) || !aligned4(prefix)) return LR_ERR_ALIGN;
+    const size_t need =
+        lr_step_paged_prefix_workspace_size(N, Hq, Hk, d, prefix_len, max_len, window, sinks, dt);
+    if (need > 0 && (!workspace || workspace_bytes < need)) return LR_ERR_WORKSPACE;
+    if (need > 0 && !aligned16(workspace)) return LR_ERR_ALIGN;
+    const size_t rows = (size_t)N * Hq * d * esize(dt), pages = ((size_t)prefix_len + cache->page - 1) / cache->page;
+    const Span so = span(o, rows), sq = span(q, rows), sl = span(lens, (size_t)N * 4);
+    const Span sp = span(prefix, pages * 4), sw = span(need > 0 ? workspace : nullptr, need);
+    for (const Span &i : {sq, sl, ck, cv, ct, sp})
+        if (overlap(so, i) || overlap(sw, i)) return LR_ERR_ALIAS;
+    if (overlap(so, sw)) return LR_ERR_ALIAS;
+    const StepArgs a{q, cache->k, cache->v, o, cache->table, lens, N, Hq, Hk, max_len, window,
+                     own_sinks(sinks, prefix_len), cache->num_pages, log2_of(cache->page), cache->max_pages, scale,
+                     (flags & LR_STEP_FILL) != 0, prefix, prefix_len, sinks, 0, nullptr, nullptr};
+    return done(launch_step_prefix(a, d, dt, workspace, stream));
+}
+
+size_t lr_step_paged_prefix_workspace_size(int N, int Hq, int Hk, int d, int prefix_len,
+                                           int max_len, int window, int sinks, lr_dtype dt) {
+    if (check_prefix_sizes(N, Hq, Hk, d, prefix_len, max_len, window, sinks, dt) != LR_OK) return 0;
+    return prefix_workspace_bytes(N, Hq, d, prefix_plan(N, Hq, Hk, d, prefix_len, window, sinks, dt)) +
+           step_workspace_bytes(N, Hq, d,
+                                step_plan(N, Hq, Hk, d, max_len, window, own_sinks(sinks, prefix_len), dt));
 }
 
 }  // extern "C"

@@ -170,7 +170,28 @@ struct StepArgs {
     int N, Hq, Hk, max_len, window, sinks, num_pages, page_log2, max_pages;
     float scale;
     int fill;  // rows that are not computed are zeros
+    // A prefix shared by all sequences, before their own tokens: its pages, its
+    // length, the sinks of the whole sequence (`sinks` counts those among the own
+    // tokens), and its parts, `pre` of each of the N Hq rows: outputs [row][pre][d]
+    // and (maximum, sum) [row][pre].
+    const int *ptable;
+    int plen, all_sinks, pre;
+    float *po;
+    float2 *pml;
 };
+// First position of the window of the row at position p.
+__host__ __device__ __forceinline__ int window_start(int p, int window) {
+    const long long lo = (long long)p - window + 1;
+    return lo < 0 ? 0 : (int)lo;
+}
+// The tiles of a prefix that rows behind it see: the sinks', then the window's
+// from tile `first` on; runs of `chunk` tiles leave `parts` parts of a row.
+struct PrefixPlan {
+    int sink_tiles, first, tiles, chunk, parts;
+};
+PrefixPlan prefix_plan(int N, int Hq, int Hk, int d, int plen, int window, int sinks, lr_dtype dt);
+cudaError_t launch_prefix_tc(const StepArgs &a, const PrefixPlan &plan, int d, cudaStream_t stream);
+cudaError_t launch_prefix_f32(const StepArgs &a, const PrefixPlan &plan, int d, cudaStream_t stream);
 // How a step's keys are cut: chunks of `chunk` keys, at most `splits` of them,
 // joined by a cluster or by a second kernel.
 struct StepPlan {
@@ -182,12 +203,15 @@ struct StepPlan {
 StepPlan plan_chunks(int seen, long long rows, int per_sm, const int *room);
 StepPlan step_plan(int N, int Hq, int Hk, int d, int max_len, int window, int sinks, lr_dtype dt);
 size_t step_workspace_bytes(int N, int Hq, int d, const StepPlan &p);
+size_t prefix_workspace_bytes(int N, int Hq, int d, const PrefixPlan &p);
 // Differential attention's step: a.Hq and a.Hk count pairs.
 StepPlan diff_step_plan(int N, int H, int Hk, int d, int max_len, int window, int sinks, lr_dtype dt);
 size_t diff_step_workspace_bytes(int N, int H, int d, const StepPlan &p);
 cudaError_t launch_step_diff(const StepArgs &a, const float *lambda, const float *weight, float eps, bool norm, int d,
                              lr_dtype dt, void *ws, cudaStream_t stream);
 cudaError_t launch_step_paged(const StepArgs &a, int d, lr_dtype dt, void *ws, cudaStream_t stream);
+// The prefix's parts, then the step that joins them (po, pml and pre are set here).
+cudaError_t launch_step_prefix(StepArgs a, int d, lr_dtype dt, void *ws, cudaStream_t stream);
 
 // Return and clear the error bits of each unit (-1: the device could not be read).
 int attn_errors_rope();
@@ -196,5 +220,7 @@ int attn_errors_window_tc();
 int attn_errors_step();
 int attn_errors_diff_tc();
 int attn_errors_step_diff();
+int attn_errors_prefix_tc();
+int attn_errors_prefix_f32();
 
 }  // namespace lr

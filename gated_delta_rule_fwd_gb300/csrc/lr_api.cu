@@ -401,7 +401,7 @@ lr_status lr_device_status(void) {
     unsigned attn = 0;
     for (int a : {attn_errors_rope(), attn_errors_window_f32(),
                   attn_errors_window_tc(), attn_errors_step(), attn_errors_diff_tc(),
-                  attn_errors_step_diff()}) {
+                  attn_errors_step_diff(), attn_errors_prefix_tc(), attn_errors_prefix_f32()}) {
         if (a < 0) return LR_ERR_CUDA;
         attn |= (unsigned)a;
     }

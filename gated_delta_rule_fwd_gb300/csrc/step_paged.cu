@@ -75,13 +75,39 @@ __device__ __forceinline__ void mend_step_row(const StepArgs &a, int n, int head
     mend_row_of<E, D>(
         static_cast<const E *>(a.q) + at,
         [&](int j, const E *&kj, const E *&vj) {
-            const int page = table[j >> a.page_log2];
+            const bool shared = j < a.plen;
+            if (!shared) j -= a.plen;
+            const int page = (shared ? a.ptable : table)[j >> a.page_log2];
             if (page < 0 || page >= a.num_pages) return false;
             const long long row = (((long long)page * a.Hk + hk) << a.page_log2) + (j & ((1 << a.page_log2) - 1));
             kj = static_cast<const E *>(a.k) + row * D, vj = static_cast<const E *>(a.v) + row * D;
             return true;
         },
-        o, seen_keys(len - 1, len, a.window, a.sinks), f, isfinite(sum()));
+        o, seen_keys(a.plen + len - 1, a.plen + len, a.window, a.all_sinks), f, isfinite(sum()));
+}
+
+// Joins the prefix's parts of row r, where there are any, with what the row's
+// own keys gave: their maximum m, sum and, of channel ch, output x.  A part
+// without a key weighs nothing, but a sum of NaN stays.
+template <int D>
+__device__ __forceinline__ void join_prefix(const StepArgs &a, size_t r, int ch, float c, float &m, float &sum,
+                                            float &x) {
+    if (!a.pre) return;
+    const float2 *ml = a.pml + r * a.pre;
+    const float *o = a.po + r * a.pre * D + ch;
+    float top = m;
+    for (int i = 0; i < a.pre; ++i) top = fmaxf(top, ml[i].x);
+    const float f = m == -INFINITY ? 0.f : ex2((m - top) * c);
+    sum *= f;
+    x = m == -INFINITY ? 0.f : x * f;
+#pragma unroll 4
+    for (int i = 0; i < a.pre; ++i) {
+        const float2 t = ml[i];
+        const float y = o[(size_t)i * D], w = t.x == -INFINITY ? 0.f : ex2((t.x - top) * c);
+        sum += t.y * w;
+        if (t.x != -INFINITY) x += y * w;
+    }
+    m = top;
 }
 
 // The end of a CTA: joins its warps' parts and hands the result on.  so: the
@@ -113,6 +139,7 @@ __device__ __forceinline__ void finish(float (&so)[NT / 32][HEADS][P], float (&s
         }
         const size_t r = row0 + h;
         if (parts.splits == 1) {
+            join_prefix<D>(a, r, ch, c, mn, sum, x);
             const float y = sum == 0.f ? 0.f : x / sum;
             out[r * D + ch] = from_f<E>(y);
             odd = odd || !isfinite(y);
@@ -138,8 +165,9 @@ __device__ __forceinline__ void finish(float (&so)[NT / 32][HEADS][P], float (&s
         if (parts.splits == 1 && __syncthreads_or(odd))
             for (int h = tid >> 5; h < heads; h += NT / 32)
                 mend_step_row<E, D>(a, n, h0 + h, f, [&] {
-                    float mn;
-                    return whole(h, mn);
+                    float mn, x = 0.f, sum = whole(h, mn);
+                    join_prefix<D>(a, row0 + h, 0, c, mn, sum, x);
+                    return sum;
                 });
         return;
     }
@@ -166,6 +194,7 @@ __device__ __forceinline__ void finish(float (&so)[NT / 32][HEADS][P], float (&s
                 sum += fr * ld_cluster(tc::map_to_rank(ml_at + 8 * h + 4, r));
                 x += fr * ld_cluster(tc::map_to_rank(o_at + 4 * (h * P + ch), r));
             }
+        join_prefix<D>(a, row0 + h, ch, c, mn, sum, x);
         const float y = sum == 0.f ? 0.f : x / sum;
         out[(row0 + h) * D + ch] = from_f<E>(y);
         odd = odd || !isfinite(y);
@@ -559,6 +588,7 @@ __global__ void __launch_bounds__(D) step_join_kernel(StepArgs a, Parts parts, S
         }
         m = mn;
     }
+    join_prefix<D>(a, r, ch, c, m, l, x);
     const float out = l == 0.f ? 0.f : x / l;
     static_cast<E *>(a.o)[(size_t)r * D + ch] = from_f<E>(out);
     if (__syncthreads_or(!isfinite(out)) && ch < 32)
@@ -672,6 +702,39 @@ StepPlan step_plan(int N, int Hq, int Hk, int d, int max_len, int window, int si
 size_t step_workspace_bytes(int N, int Hq, int d, const StepPlan &p) {
     if (p.splits <= 1 || p.cluster) return 0;
     return (size_t)N * Hq * p.splits * ((size_t)d * 4 + 8);
+}
+
+PrefixPlan prefix_plan(int N, int Hq, int Hk, int d, int plen, int window, int sinks, lr_dtype dt) {
+    const int tile = dt == LR_DT_BF16 ? 128 : 32, block = dt == LR_DT_BF16 ? 256 : 64;
+    PrefixPlan p{};
+    if (plen == 0) return p;
+    // rows stand at positions from plen - 1 on
+    const int lo = window_start(plen - 1, window), most = (plen + tile - 1) / tile;
+    p.sink_tiles = ((sinks < plen ? sinks : plen) + tile - 1) / tile;
+    p.first = lo / tile > p.sink_tiles ? lo / tile : p.sink_tiles;
+    p.tiles = p.sink_tiles + (most > p.first ? most - p.first : 0);
+    // one wave of CTAs: one to an SM in bf16, two in fp32
+    const long long ctas = ((long long)N * (Hq / Hk) + block - 1) / block * Hk, wave = dt == LR_DT_BF16 ? 152 : 304;
+    const long long parts = ctas < wave ? wave / ctas : 1;
+    p.chunk = (int)((p.tiles + parts - 1) / parts);
+    p.parts = p.tiles ? (p.tiles + p.chunk - 1) / p.chunk : 0;
+    return p;
+}
+
+size_t prefix_workspace_bytes(int N, int Hq, int d, const PrefixPlan &p) {
+    return ((size_t)N * Hq * p.parts * ((size_t)d * 4 + 8) + 15) / 16 * 16;
+}
+
+cudaError_t launch_step_prefix(StepArgs a, int d, lr_dtype dt, void *ws, cudaStream_t stream) {
+    const PrefixPlan p = prefix_plan(a.N, a.Hq, a.Hk, d, a.plen, a.window, a.all_sinks, dt);
+    a.pre = p.parts;
+    if (p.parts) {
+        a.po = static_cast<float *>(ws);
+        a.pml = reinterpret_cast<float2 *>(a.po + (size_t)a.N * a.Hq * p.parts * d);
+        const cudaError_t e = dt == LR_DT_BF16 ? launch_prefix_tc(a, p, d, stream) : launch_prefix_f32(a, p, d, stream);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_step_paged(a, d, dt, static_cast<char *>(ws) + prefix_workspace_bytes(a.N, a.Hq, d, p), stream);
 }
 
 cudaError_t launch_step_paged(const StepArgs &a, int d, lr_dtype dt, void *ws, cudaStream_t stream) {

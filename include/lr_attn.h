@@ -11,6 +11,8 @@
  *                     sliding window and a few first tokens (sinks)
  *   lr_step_paged     the same attention for one new token per sequence over
  *                     the paged cache
+ *   lr_step_paged_prefix  that step for a batch that shares a long prefix, whose
+ *                     keys and values are read once for all
  *   lr_fwd_diff       differential attention over whole sequences: the
  *                     difference of two softmax maps, with its norm
  *   lr_step_paged_diff  the same for one new token per sequence over the paged
@@ -258,6 +260,42 @@ lr_status lr_step_paged_fill(const void *q, const lr_paged *cache, const int *le
  * arguments they would reject). */
 size_t lr_step_paged_workspace_size(int N, int Hq, int Hk, int d, int max_len, int window,
                                     int sinks, lr_dtype dt);
+
+#define LR_STEP_FILL 0x1u /* rows of unused slots are written as zeros */
+
+/*
+ * One decode step of lr_step_paged for N sequences that begin with the same
+ * prefix_len tokens, held once in the pages of `prefix`; a sequence's own tokens
+ * follow in its pages of the cache's table.  The row of sequence n stands at
+ * position prefix_len + lens[n] - 1 of the whole sequence; window and sinks count
+ * in it.  What it sees and returns is what lr_step_paged would for the pages of
+ * prefix and own tokens one behind the other.
+ *
+ *   prefix      [ceil(prefix_len / page)] int32 page numbers on the device, in
+ *               the cache's pools; NULL where prefix_len is 0.  Rows of its last
+ *               page behind the prefix are not read into any sum.
+ *   prefix_len  0 <= prefix_len, prefix_len + max_len <= 2^30
+ *   lens        [N] int32 own tokens, this one included (0: the row is that of the
+ *               prefix's last token, zeros where there is none; negative: an
+ *               unused slot, its row is left as it was)
+ *   max_len     bound on lens, as for lr_step_paged
+ *   flags       OR of LR_STEP_*
+ *   workspace   lr_step_paged_prefix_workspace_size(...) bytes, 16-byte aligned
+ *
+ * The other arguments are those of lr_step_paged.  The prefix is read once for up
+ * to 256 rows of a key head in bf16 and 64 in fp32 (a row: a sequence and one of
+ * the Hq / Hk query heads), by a kernel of its own; the own tokens' kernel joins
+ * both.  A repeated call gives the same bits.
+ */
+lr_status lr_step_paged_prefix(const void *q, const lr_paged *cache, const int *prefix,
+                               int prefix_len, const int *lens, void *o, int N, int Hq, int Hk,
+                               int d, int max_len, int window, int sinks, float scale,
+                               unsigned flags, lr_dtype dt, void *workspace,
+                               size_t workspace_bytes, cudaStream_t stream);
+
+/* Workspace bytes lr_step_paged_prefix needs (0 as well for arguments it would reject). */
+size_t lr_step_paged_prefix_workspace_size(int N, int Hq, int Hk, int d, int prefix_len,
+                                           int max_len, int window, int sinks, lr_dtype dt);
 
 /*
  * One decode step of lr_fwd_diff, as lr_step_paged is one of lr_fwd_window.

@@ -220,3 +220,26 @@ def diff_step(q, k_cache, v_cache, table, lens, lam, window, sinks, scale, dtype
                              weight_bits, weight, eps)
             o[n, 2 * h:2 * h + 2], bound[n, 2 * h:2 * h + 2] = y.reshape(2, d), e.reshape(2, d)
     return o, bound, written
+
+
+def step_prefix(q, k_cache, v_cache, prefix, prefix_len, table, lens, window, sinks, scale):
+    """step() of sequences whose first prefix_len tokens are in the pages of
+    `prefix`, their own lens[n] tokens behind them in those of table[n]."""
+    q, k_cache, v_cache = (np.asarray(x, np.float64) for x in (q, k_cache, v_cache))
+    N, Hq, d = q.shape
+    Hk, page = k_cache.shape[1:3]
+    o, size, reach = np.zeros(q.shape), np.zeros(q.shape), np.zeros((N, Hq))
+    written = np.zeros(N, bool)
+    for n in range(N):
+        written[n] = lens[n] >= 0
+        L = prefix_len + int(lens[n])
+        if lens[n] < 0:
+            continue
+        keys = [j for j in range(L) if sees(L - 1, j, L, window, sinks)]
+        at = [(prefix, j) if j < prefix_len else (table[n], j - prefix_len) for j in keys]
+        pages = np.array([int(t[j // page]) for t, j in at], int)
+        rows = np.array([j % page for _, j in at], int)
+        for h in range(Hq):
+            g = h // (Hq // Hk)
+            o[n, h], size[n, h], reach[n, h] = row(q[n, h], k_cache[pages, g, rows], v_cache[pages, g, rows], scale)
+    return o, size, reach, written

@@ -1,5 +1,6 @@
-"""CPU-side checks of the rotation by several axes and of differential attention:
-refusals before any launch and the binding's checks."""
+"""CPU-side checks of the rotation by several axes, of differential attention and
+of the step over a shared prefix: refusals before any launch and the binding's
+checks."""
 import os
 import subprocess
 import sys
@@ -126,6 +127,38 @@ cases = [
 """
 
 
+_PREFIX = r"""
+def step(**kw):
+    a = dict(q=A[0], ck=A[1], cv=A[2], tab=A[3], lens=A[4], o=A[5], pre=A[6], P=1000, ws=A[8], wsb=1 << 27, flags=0,
+             N=3, Hq=4, Hk=2, d=64, most_len=9000, win=1 << 30, s=0, scale=0.5, dt=1, pages=9, page=16, most=600,
+             cache=True)
+    a.update(kw)
+    c = Paged(a['ck'], a['cv'], a['tab'], a['pages'], a['page'], a['most'])
+    return L.lr_step_paged_prefix(P(a['q']), ctypes.byref(c) if a['cache'] else None, P(a['pre']), a['P'], P(a['lens']),
+                                  P(a['o']), a['N'], a['Hq'], a['Hk'], a['d'], a['most_len'], a['win'], a['s'],
+                                  a['scale'], a['flags'], a['dt'], P(a['ws']), a['wsb'], None)
+wsz = lambda *a: L.lr_step_paged_prefix_workspace_size(*a)
+need = wsz(3, 4, 2, 64, 1000, 9000, 1 << 30, 0, 1)
+cases = [
+    ("ok", step(), 7), ("f32-ok", step(dt=0), 7), ("fill-ok", step(flags=1), 7), ("flag", step(flags=2), 12),
+    ("P0-ok", step(P=0, pre=None), 7), ("P-neg", step(P=-1), 2), ("P-long", step(P=1 << 30), 2),
+    ("P-longest-ok", step(P=(1 << 30) - 9000, win=5, wsb=1 << 40), 7),
+    ("null-prefix", step(pre=None), 1), ("align-prefix", step(pre=A[6] + 2), 4), ("align-prefix-ok", step(pre=A[6] + 4), 7),
+    ("alias-prefix", step(o=A[6]), 8), ("alias-prefix-end", step(o=A[6] + 240), 8), ("alias-prefix-behind-ok", step(o=A[6] + 256), 7),
+    ("ws-alias-prefix", step(ws=A[6]), 8), ("ws-alias-o", step(ws=A[5]), 8),
+    ("dtype", step(dt=9), 3), ("d16", step(d=16), 6), ("N0", step(N=0), 2), ("heads", step(Hq=3), 2), ("window", step(win=0), 2),
+    ("sinks", step(s=-2), 2), ("scale", step(scale=nan), 2), ("maxlen0", step(most_len=0), 2),
+    ("maxlen-table", step(most_len=16 * 600 + 1), 2), ("null-lens", step(lens=None), 1), ("null-cache", step(cache=False), 1),
+    ("null-pool", step(cv=None), 1), ("page", step(page=512), 6), ("align-o", step(o=A[5] + 8), 4),
+    ("alias-q", step(o=A[0]), 8), ("alias-pool", step(o=A[2] + 64), 8), ("many", step(N=1 << 30, Hq=4, Hk=4), 2),
+    ("ws-null", step(ws=None), 10), ("ws-short", step(wsb=need - 1), 10), ("ws-align", step(ws=A[8] + 8), 4),
+    ("ws-need", int(need > 0), 1), ("ws-none", wsz(3, 4, 2, 64, 0, 64, 1 << 30, 0, 1), 0),
+    ("ws-left-behind", wsz(3, 4, 2, 64, 100000, 64, 1 << 30, 0, 1) > wsz(3, 4, 2, 64, 100000, 64, 50, 0, 1) > 0, True),
+    ("ws-bad", wsz(3, 4, 3, 64, 100, 300, 1, 0, 1), 0),
+]
+"""
+
+
 def _child(body):
     from gated_delta_rule_fwd_gb300.build import build
     build()
@@ -149,13 +182,17 @@ def test_diff_step_arguments_rejected_before_launch():
     _child(_DIFF_STEP)
 
 
+def test_prefix_arguments_rejected_before_launch():
+    _child(_PREFIX)
+
+
 def test_struct_sizes_match_the_header():
     import ctypes
     from gated_delta_rule_fwd_gb300 import attention as at
     src = ('#include "lr_attn.h"\n'
            f"_Static_assert(sizeof(lr_diff_maps) == {ctypes.sizeof(at.DiffMaps)}, \"maps\");\n"
            f"_Static_assert(LR_MAX_AXES == {at.MAX_AXES} && LR_DIFF_NORM == {at.DIFF_NORM}, \"values\");\n"
-           f"_Static_assert(LR_DIFF_FILL == {at.DIFF_FILL}, \"values\");\n"
+           f"_Static_assert(LR_DIFF_FILL == {at.DIFF_FILL} && LR_STEP_FILL == {at.STEP_FILL}, \"values\");\n"
            "int main(void) { return 0; }\n")
     inc = [a for d in ("/usr/local/cuda/include",) if os.path.isdir(d) for a in ("-I", d)]
     r = subprocess.run(["gcc", "-std=c11", "-fsyntax-only", "-x", "c", "-I", os.path.join(ROOT, "include"),
@@ -253,3 +290,25 @@ def test_diff_step_binding_accepts_what_it_should(lr):
 def test_diff_step_binding_refuses(lr, change):
     with pytest.raises((ValueError, TypeError, AttributeError)):
         lr.lr_step_paged_diff(**_diff_step_args(**change))
+
+
+def _prefix_args(**change):
+    a = dict(q=_t(3, 4, 64), k_cache=_t(5, 2, 16, 64), v_cache=_t(5, 2, 16, 64), prefix=_i(4), prefix_len=50,
+             table=_i(3, 4), lens=_i(3))
+    a.update(change)
+    return a
+
+
+def test_prefix_binding_accepts_what_it_should(lr):
+    for change in (dict(max_len=60), dict(prefix_len=64), dict(prefix=_i(0), prefix_len=0)):
+        with pytest.raises(AssertionError, match="lr_step_paged_prefix"):
+            lr.lr_step_paged_prefix(**_prefix_args(**change))
+
+
+@pytest.mark.parametrize("change", [
+    dict(prefix=None), dict(prefix=_i(3)), dict(prefix=_i(1, 4)), dict(prefix=_i(4, dtype=torch.int64)), dict(prefix=_i(8)[::2]),
+    dict(prefix_len=65), dict(prefix_len=1 << 40), dict(q=_t(1, 3, 4, 64)), dict(v_cache=_t(5, 1, 16, 128)), dict(table=_i(2, 4)),
+    dict(lens=_i(4)), dict(lens=None), dict(o=_t(3, 4, 32)), dict(max_len=1 << 33)], ids=lambda c: "-".join(c))
+def test_prefix_binding_refuses(lr, change):
+    with pytest.raises((ValueError, TypeError)):
+        lr.lr_step_paged_prefix(**_prefix_args(**change))
