@@ -86,28 +86,32 @@ __device__ __forceinline__ void mend_step_row(const StepArgs &a, int n, int head
         o, seen_keys(a.plen + len - 1, a.plen + len, a.window, a.all_sinks), f, isfinite(sum()));
 }
 
-// Joins the prefix's parts of row r, where there are any, with what the row's
-// own keys gave: their maximum m, sum and, of channel ch, output x.  A part
-// without a key weighs nothing, but a sum of NaN stays.
-template <int D>
-__device__ __forceinline__ void join_prefix(const StepArgs &a, size_t r, int ch, float c, float &m, float &sum,
-                                            float &x) {
-    if (!a.pre) return;
-    const float2 *ml = a.pml + r * a.pre;
-    const float *o = a.po + r * a.pre * D + ch;
-    float top = m;
-    for (int i = 0; i < a.pre; ++i) top = fmaxf(top, ml[i].x);
-    const float f = m == -INFINITY ? 0.f : ex2((m - top) * c);
-    sum *= f;
-    x = m == -INFINITY ? 0.f : x * f;
+// The prefix's parts of a CTA's rows (row0 on) joined to one, which the first
+// chunk's CTA adds to its warps' parts: (maximum, sum) in pml, outputs in po.  Done
+// while the first keys are on their way; four channels a thread.  A part without
+// a key weighs nothing, but a sum of NaN stays.
+template <int D, int HEADS, int P>
+__device__ __forceinline__ void load_prefix(const StepArgs &a, size_t row0, int heads, float c,
+                                            float (&po)[HEADS][P], float (&pml)[HEADS][2]) {
+    for (int i = threadIdx.x; i < heads * (D / 4); i += NT) {
+        const int h = i / (D / 4), ch = (i - h * (D / 4)) * 4;
+        const float2 *ml = a.pml + (row0 + h) * a.pre;
+        const float *o = a.po + (row0 + h) * a.pre * D + ch;
+        float top = -INFINITY, sum = 0.f;
+        float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int i = 0; i < a.pre; ++i) {
-        const float2 t = ml[i];
-        const float y = o[(size_t)i * D], w = t.x == -INFINITY ? 0.f : ex2((t.x - top) * c);
-        sum += t.y * w;
-        if (t.x != -INFINITY) x += y * w;
+        for (int j = 0; j < a.pre; ++j) top = fmaxf(top, ml[j].x);
+#pragma unroll 4
+        for (int j = 0; j < a.pre; ++j) {
+            const float2 t = ml[j];
+            const float4 y = *reinterpret_cast<const float4 *>(o + (size_t)j * D);
+            const float w = t.x == -INFINITY ? 0.f : ex2((t.x - top) * c);
+            sum += t.y * w;
+            if (t.x != -INFINITY) x.x += y.x * w, x.y += y.y * w, x.z += y.z * w, x.w += y.w * w;
+        }
+        *reinterpret_cast<float4 *>(&po[h][ch]) = x;
+        if (ch == 0) pml[h][0] = top, pml[h][1] = sum;
     }
-    m = top;
 }
 
 // The end of a CTA: joins its warps' parts and hands the result on.  so: the
@@ -115,8 +119,9 @@ __device__ __forceinline__ void join_prefix(const StepArgs &a, size_t r, int ch,
 // the scores' factor; n, h0: sequence and first head.  A part without a key has
 // a maximum of -inf and weighs nothing; one whose scores were all NaN too, but
 // its sum of NaN stays.
+// The part behind the warps' is the prefix's, where the first chunk has one.
 template <typename E, int D, int HEADS, int P>
-__device__ __forceinline__ void finish(float (&so)[NT / 32][HEADS][P], float (&sml)[NT / 32][HEADS][2],
+__device__ __forceinline__ void finish(float (&so)[NT / 32 + 1][HEADS][P], float (&sml)[NT / 32 + 1][HEADS][2],
                                        int heads, int n, int h0, int split, ScoreFactor f, const StepArgs &a,
                                        const Parts &parts) {
     const int tid = threadIdx.x;
@@ -124,22 +129,24 @@ __device__ __forceinline__ void finish(float (&so)[NT / 32][HEADS][P], float (&s
     const float c = f.c;
     E *out = static_cast<E *>(a.o);
     bool odd = false;  // a value that is not finite
+    const int count = NT / 32 + (a.pre && split == 0);
     __syncthreads();
     for (int i = tid; i < heads * D; i += NT) {
         const int h = i / D, ch = i - h * D;
         float mn = -INFINITY;
 #pragma unroll
-        for (int w = 0; w < NT / 32; ++w) mn = fmaxf(mn, sml[w][h][0]);
+        for (int w = 0; w <= NT / 32; ++w)
+            if (w < count) mn = fmaxf(mn, sml[w][h][0]);
         float sum = 0.f, x = 0.f;
 #pragma unroll
-        for (int w = 0; w < NT / 32; ++w) {
+        for (int w = 0; w <= NT / 32; ++w) {
+            if (w == count) break;
             const float mw = sml[w][h][0], fw = mw == -INFINITY ? 0.f : ex2((mw - mn) * c);
             sum += fw * sml[w][h][1];
             x += fw * so[w][h][ch];
         }
         const size_t r = row0 + h;
         if (parts.splits == 1) {
-            join_prefix<D>(a, r, ch, c, mn, sum, x);
             const float y = sum == 0.f ? 0.f : x / sum;
             out[r * D + ch] = from_f<E>(y);
             odd = odd || !isfinite(y);
@@ -154,10 +161,8 @@ __device__ __forceinline__ void finish(float (&so)[NT / 32][HEADS][P], float (&s
     auto whole = [&](int h, float &mn) {
         float sum = 0.f;
         mn = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < NT / 32; ++w) mn = fmaxf(mn, sml[w][h][0]);
-#pragma unroll
-        for (int w = 0; w < NT / 32; ++w)
+        for (int w = 0; w < count; ++w) mn = fmaxf(mn, sml[w][h][0]);
+        for (int w = 0; w < count; ++w)
             sum += sml[w][h][1] * (sml[w][h][0] == -INFINITY ? 0.f : ex2((sml[w][h][0] - mn) * c));
         return sum;
     };
@@ -165,9 +170,8 @@ __device__ __forceinline__ void finish(float (&so)[NT / 32][HEADS][P], float (&s
         if (parts.splits == 1 && __syncthreads_or(odd))
             for (int h = tid >> 5; h < heads; h += NT / 32)
                 mend_step_row<E, D>(a, n, h0 + h, f, [&] {
-                    float mn, x = 0.f, sum = whole(h, mn);
-                    join_prefix<D>(a, row0 + h, 0, c, mn, sum, x);
-                    return sum;
+                    float mn;
+                    return whole(h, mn);
                 });
         return;
     }
@@ -194,7 +198,6 @@ __device__ __forceinline__ void finish(float (&so)[NT / 32][HEADS][P], float (&s
                 sum += fr * ld_cluster(tc::map_to_rank(ml_at + 8 * h + 4, r));
                 x += fr * ld_cluster(tc::map_to_rank(o_at + 4 * (h * P + ch), r));
             }
-        join_prefix<D>(a, row0 + h, ch, c, mn, sum, x);
         const float y = sum == 0.f ? 0.f : x / sum;
         out[(row0 + h) * D + ch] = from_f<E>(y);
         odd = odd || !isfinite(y);
@@ -213,8 +216,8 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts, 
     constexpr int LANES = D / 8;            // lanes of a key
     constexpr int GROUPS = NT / LANES;      // keys in flight
     constexpr int U = 4;                    // keys of a group per pass
-    __shared__ float so[GROUPS / (32 / LANES)][GC][D];
-    __shared__ float sml[GROUPS / (32 / LANES)][GC][2];
+    __shared__ __align__(16) float so[NT / 32 + 1][GC][D];
+    __shared__ float sml[NT / 32 + 1][GC][2];
     const int tid = threadIdx.x, warp = tid >> 5;
     const int G = a.Hq / a.Hk, gq = (G + GC - 1) / GC;
     int id = blockIdx.x;
@@ -251,6 +254,8 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts, 
     const int lanes0 = (tid & 31) / LANES * LANES;
     const unsigned mask = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1) << lanes0;
     bool bad = false;
+    if (a.pre && split == 0)
+        load_prefix<D>(a, (size_t)n * a.Hq + h0, heads, f.c, so[NT / 32], sml[NT / 32]);
     for (int base = c0 + group; base < c1; base += GROUPS * U) {
         long long row[U];
         float x[U][8], y[U][8], sc[U][GC];  // keys, values: all on their way at once
@@ -349,8 +354,8 @@ __global__ void __launch_bounds__(NT)
     constexpr int KC = D / 32;   // 32-channel pieces of a key: 16 bytes per lane and row
     constexpr int VW = D / 16;   // words of a value row per lane = 16-channel blocks of O^T
     constexpr int HEADS = 8 * NH;
-    __shared__ float so[NT / 32][HEADS][D + 8];
-    __shared__ float sml[NT / 32][HEADS][2];
+    __shared__ __align__(16) float so[NT / 32 + 1][HEADS][D + 8];
+    __shared__ float sml[NT / 32 + 1][HEADS][2];
     __shared__ long long rows[kMostTiles];  // first cache row of each tile, -1: a bad page
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int G = a.Hq / a.Hk, gq = (G + HEADS - 1) / HEADS;
@@ -462,6 +467,7 @@ __global__ void __launch_bounds__(NT)
         load_k(first);
         load_v(first);
     }
+    if (a.pre && split == 0) load_prefix<D>(a, (size_t)n * a.Hq + h0, heads, c, so[NT / 32], sml[NT / 32]);
     for (int i = first; i < t1; i += NT / 32) {
         float sc[NH][4];
 #pragma unroll
@@ -588,7 +594,6 @@ __global__ void __launch_bounds__(D) step_join_kernel(StepArgs a, Parts parts, S
         }
         m = mn;
     }
-    join_prefix<D>(a, r, ch, c, m, l, x);
     const float out = l == 0.f ? 0.f : x / l;
     static_cast<E *>(a.o)[(size_t)r * D + ch] = from_f<E>(out);
     if (__syncthreads_or(!isfinite(out)) && ch < 32)
