@@ -120,17 +120,27 @@ __device__ __forceinline__ uint32_t low_bits(int n) {
     return n >= 32 ? 0xffffffffu : (n <= 0 ? 0u : (1u << n) - 1u);
 }
 
+// The bf16 pair nearest to x, and (in `rest`) to what that rounding left.
+__device__ __forceinline__ uint32_t pack2_rest(float2 x, uint32_t &rest) {
+    const uint32_t r = pack2(x.x, x.y);
+    const float2 y = unpack2(r);
+    rest = pack2(x.x - y.x, x.y - y.y);
+    return r;
+}
+
 // One 128-key tile of a row of scores, a row per thread: raises the row's
 // maximum m in use where a score passes it by 2^8 (rescaling the sum l and the
 // output's DV columns at `to`), replaces the 128 scores at `ts` by bf16 weights
-// over their first 64 columns, handing them over in halves (ready[0], ready[1],
-// one arrival a warp), and adds the weights to l.  A weight is 2^(c s - b) with
+// over their first 64 columns, handing them over in halves (ready0, ready1, one
+// arrival a warp), and adds the weights to l.  For the first 32 REST keys, columns
+// 64 on take what the weights' rounding left, as bf16 weights of their own, which
+// ready1 covers.  A weight is 2^(c s - b) with
 // b = c m rounded, so all of a row refer to the same b.  keep(i): which of the
 // columns 32 i .. 32 i + 31 the row sees; not asked where `whole`.
 //
 // A tile at the edge of what the rows see gets -inf over the scores that a row
 // does not see, in tensor memory, so that one code serves all tiles.
-template <int DV, typename Keep>
+template <int DV, int REST, typename Keep>
 __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, bool whole, const Keep &keep,
                                              float &m, float &l, uint64_t *ready0, uint64_t *ready1) {
     const float2 c2 = make_float2(c, c);
@@ -195,8 +205,15 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, 
             e.y = ex2(e.y);
             sum[i & 3] = add2(sum[i & 3], e);
             r[i] = pack2(e.x, e.y);
+            if (ch < REST) s[ch][2 * i] = e.x, s[ch][2 * i + 1] = e.y;
         }
         tmem_st16(ts + 16 * ch, r);
+        if (ch > 1 && ch - 2 < REST) {
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                pack2_rest(make_float2(s[ch - 2][2 * i], s[ch - 2][2 * i + 1]), r[i]);
+            tmem_st16(ts + 64 + 16 * (ch - 2), r);
+        }
         if (ch & 1) {
             tmem_st_wait();
             tc_fence_before();
@@ -237,6 +254,22 @@ inline cudaError_t rows_map(CUtensorMap *m, const void *base, const lr_strides &
                            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
                            CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// A pool [pages, heads, page, d], boxes of `rows` rows of a page x 64 columns,
+// 128-byte swizzle, zero fill of the columns of a box wider than d.
+inline cudaError_t pool_map(CUtensorMap *m, const void *pool, int d, int page, int heads, int pages, int rows) {
+    auto enc = encoder();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t row = 2ull * d;
+    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)page, (cuuint64_t)heads, (cuuint64_t)pages};
+    const cuuint64_t strides[3] = {row, row * page, row * page * heads};
+    const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(pool), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 

@@ -13,6 +13,12 @@
 // the difference is formed there in fp32 and rounded once: at the end each of
 // the two softmax warpgroups reads half of the channels of both outputs.
 //
+// The difference takes away what the maps have in common, but not the rounding of
+// their weights to bf16: against weights of 32 bits the error was 1.53 times as
+// large (lr_fwd_window: 1.35).  So a quarter of the keys, the first 32 of a tile,
+// multiply what that rounding left as well (1.39; 8192 causal tokens of 8 pairs, d
+// = 64: 155 -> 173 us; with half of them 1.27 and 196 us, with all 1.0 and 267 us).
+//
 // Tensor memory holds 2 x 128 columns of scores and 2 x 128 of output.  With d =
 // 128 the values have 256 channels: two CTAs of a cluster take a half each and
 // both form all scores (8 units of products where 6 would do).  A row's sum of
@@ -78,6 +84,7 @@ struct Barriers {
 };
 
 constexpr uint32_t kS = 0, kO = 256;  // TMEM columns: S0, S1 (P over them), then O0, O1
+constexpr int kRest = 1;              // of a tile's four 32-key pieces, those with the rest of P's rounding
 
 struct TcArgs {
     DiffArgs a;
@@ -387,12 +394,13 @@ __global__ void __launch_bounds__(NT, 1)
                 if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bars->vfull[done % NV], (done / NV) & 1));
                 const uint64_t dv = tile_desc_mn(v_s + (done % NV) * L::VTILE, 128, 0);
                 const int steps = width(it) >> 4;
-                auto values = [&](int ks) {
+                auto product = [&](uint32_t p, int ks, bool add) {
 #pragma unroll
                     for (int j = 0; j < NO; ++j)
-                        mma_bf16_ta(o_t + j * (DV / NO), s_t + 8 * ks, mndesc_step(dv, ks) + j * (16384u >> 4), id_o,
-                                    ks > 0 || it > 0);
+                        mma_bf16_ta(o_t + j * (DV / NO), p + 8 * ks, mndesc_step(dv, ks) + j * (16384u >> 4), id_o, add);
                 };
+                auto values = [&](int ks) { product(s_t, ks, ks > 0 || it > 0); };
+                auto rests = [&](int ks) { product(s_t + 64, ks, true); };
                 // the last piece's outputs have left
                 if (ok && it == 0 && used > 0)
                     ok = __all_sync(0xffffffffu, wait_bar(&bars->oempty, (used - 1) & 1));
@@ -414,6 +422,9 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
                     for (int ks = 4; ks < BN / 16; ++ks)
                         if (ks < steps) values(ks);
+#pragma unroll
+                    for (int ks = 0; ks < 2 * kRest; ++ks)
+                        if (ks < steps) rests(ks);
                     mma_commit(&bars->vempty[done % NV]);
                     if (it + 1 < n) scores(it + 1, done + 1);
                     else mma_commit(&bars->ofull[t]);
@@ -459,7 +470,7 @@ __global__ void __launch_bounds__(NT, 1)
                     const int kc = k0 + 32 * ch;
                     return low_bits(end - kc) & (~low_bits(rlo - kc) | low_bits(a.sinks - kc));
                 };
-                softmax_tile<DV>(ts, to, g.c, whole, keep, m, l, &bars->pready[t][0], &bars->pready[t][1]);
+                softmax_tile<DV, kRest>(ts, to, g.c, whole, keep, m, l, &bars->pready[t][0], &bars->pready[t][1]);
                 ++seen;
             }
             // the rounding of the exponent's base took the weights' range

@@ -285,7 +285,7 @@ __global__ void __launch_bounds__(NT, 1)
                     }
                 return see;
             };
-            softmax_tile<D>(ts, to, g.c, whole, keep, m, l, &bars->pready[t][0], &bars->pready[t][1]);
+            softmax_tile<D, 0>(ts, to, g.c, whole, keep, m, l, &bars->pready[t][0], &bars->pready[t][1]);
         }
         // every product of both tiles has read its operands: their place is free
         for (int u = 0; u < active; ++u)
@@ -328,28 +328,13 @@ __global__ void __launch_bounds__(NT, 1)
     if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
-// The pool's rows of one head, boxes of up to 128 rows of a page x 64 columns,
-// 128-byte swizzle, zero fill of the columns of a box wider than d.
-cudaError_t pool_map(CUtensorMap *m, const void *pool, const StepArgs &a, int d) {
-    auto enc = encoder();
-    if (!enc) return cudaErrorNotSupported;
-    const cuuint64_t page = 1ull << a.page_log2, row = 2ull * d;
-    const cuuint64_t dims[4] = {(cuuint64_t)d, page, (cuuint64_t)a.Hk, (cuuint64_t)a.num_pages};
-    const cuuint64_t strides[3] = {row, row * page, row * page * a.Hk};
-    const cuuint32_t box[4] = {64, (cuuint32_t)(page < 128 ? page : 128), 1, 1};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(pool), dims, strides, box, estr,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 template <int D>
 cudaError_t launch(const StepArgs &a, const PrefixPlan &plan, int slot, cudaStream_t stream) {
     using L = Layout<D>;
     CUtensorMap mk, mv;
-    cudaError_t e = pool_map(&mk, a.k, a, D);
-    if (e == cudaSuccess) e = pool_map(&mv, a.v, a, D);
+    const int page = 1 << a.page_log2, box = page < 128 ? page : 128;
+    cudaError_t e = pool_map(&mk, a.k, D, page, a.Hk, a.num_pages, box);
+    if (e == cudaSuccess) e = pool_map(&mv, a.v, D, page, a.Hk, a.num_pages, box);
     if (e != cudaSuccess) return e;
     TcArgs g;
     g.a = a;
