@@ -54,13 +54,14 @@ __device__ __forceinline__ uint2 load_once8(const void *p) {
     return r;
 }
 
-// Launches a step kernel; cluster: CTAs of a cluster, 1 for none.
+// Launches a step kernel; cluster: CTAs of a cluster, 1 for none; smem: dynamic bytes.
 template <typename... A, typename... B>
-inline cudaError_t launch_cut(void (*fn)(A...), unsigned grid, int threads, int cluster, cudaStream_t stream,
-                              const B &...args) {
+inline cudaError_t launch_cut(void (*fn)(A...), unsigned grid, int threads, int cluster, size_t smem,
+                              cudaStream_t stream, const B &...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute at[1];
     if (cluster > 1) {

@@ -6,11 +6,12 @@
 // them (2 in fp32); chunks are joined by a cluster or a second kernel, in their
 // order.  The bound is the read of the cache.
 //
-// bf16 (step_diff_mma_kernel): a warp works on one map, a tile of 16 keys at a
-// time, S^T = K Q^T and O^T += V^T P^T with fragments loaded straight from global
-// memory as in step_paged.cu.  The map's keys go past L1; the value row of both
-// halves is read by the two warps (one for each map) that walk the same tiles,
-// the second time from L1.
+// bf16 (step_diff_mma_kernel): one warp fills a ring of 16-key tiles by TMA, both
+// maps' keys and the value rows, so the reads in flight do not depend on registers;
+// four others each work on one map and every other tile, S^T = K Q^T and O^T += V^T
+// P^T with warp-level products, the values shared by the two maps' warps.  What the
+// rounding of a weight to bf16 left is multiplied as well: the difference of the
+// maps takes away what they have in common, but not their roundings.
 //
 // fp32 (step_diff_simt_kernel): CUDA cores; d / 8 lanes hold a key of both maps
 // and its value row.
@@ -18,6 +19,7 @@
 #include "attn_internal.cuh"
 #include "attn_rows.cuh"
 #include "attn_step.cuh"
+#include "attn_tc.cuh"
 #include "tc_common.cuh"
 
 namespace lr {
@@ -54,7 +56,7 @@ __device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
 template <typename E, int D>
 __device__ __forceinline__ void zero_rows(const StepArgs &a, int n, int h0, int heads) {
     E *o = static_cast<E *>(a.o) + ((size_t)n * a.Hq + h0) * 2 * D;
-    for (int i = threadIdx.x; i < heads * 2 * D; i += NT) o[i] = from_f<E>(0.f);
+    for (int i = threadIdx.x; i < heads * 2 * D; i += blockDim.x) o[i] = from_f<E>(0.f);
 }
 
 // The row of pair h of sequence n by one warp, from `count` parts of each map:
@@ -129,7 +131,7 @@ __device__ __forceinline__ void finish_pair(const DiffStep &s, int n, int h, int
 // The end of a CTA: its warps' parts of each map, streams of them, are joined
 // and handed on.  so[stream][map][head]: unnormalised outputs, P floats a row;
 // sml: their (maximum, sum).
-template <typename E, int D, int STREAMS, int HEADS, int P>
+template <typename E, int D, int STREAMS, int HEADS, int P, int THREADS>
 __device__ __forceinline__ void finish(float (&so)[STREAMS][2][HEADS][P], float2 (&sml)[STREAMS][2][HEADS], int heads,
                                        int n, int h0, int split, ScoreFactor f, const DiffStep &s,
                                        const Parts &parts) {
@@ -137,13 +139,13 @@ __device__ __forceinline__ void finish(float (&so)[STREAMS][2][HEADS][P], float2
     if (parts.cluster) tc::cluster_sync_all();
     else __syncthreads();
     if (parts.splits == 1) {
-        for (int h = warp; h < heads; h += NT / 32)
+        for (int h = warp; h < heads; h += THREADS / 32)
             finish_pair<E, D>(
                 s, n, h0 + h, STREAMS, f, [&](int i, int map) { return sml[i][map][h]; },
                 [&](int i, int map, int ch) { return so[i][map][h][ch]; });
     } else if (parts.cluster) {
         const uint32_t o_at = tc::smem_u32(&so[0][0][0][0]), ml_at = tc::smem_u32(&sml[0][0][0]);
-        for (int h = split * (NT / 32) + warp; h < heads; h += parts.splits * (NT / 32))
+        for (int h = split * (THREADS / 32) + warp; h < heads; h += parts.splits * (THREADS / 32))
             finish_pair<E, D>(
                 s, n, h0 + h, parts.splits * STREAMS, f,
                 [&](int i, int map) {
@@ -155,7 +157,7 @@ __device__ __forceinline__ void finish(float (&so)[STREAMS][2][HEADS][P], float2
                 });
         tc::cluster_sync_all();  // no CTA leaves while another reads its part
     } else {
-        for (int i = tid; i < 2 * heads * 2 * D; i += NT) {
+        for (int i = tid; i < 2 * heads * 2 * D; i += THREADS) {
             const int row = i / (2 * D), ch = i - row * 2 * D, map = row & 1, h = row >> 1;
             float mn = -INFINITY, sum = 0.f, x = 0.f;
 #pragma unroll
@@ -188,8 +190,30 @@ struct Tiles {
     __device__ __forceinline__ bool sees(int key) const { return key < s.hi && (key >= s.lo || key < s.s1); }
 };
 
+// Shared memory of the bf16 kernel: a ring of tiles, each 16 rows of both maps'
+// keys and of both halves of the values in 64-column blocks as TMA leaves them
+// (128-byte swizzle); the warps' parts lie over it when the tiles are used up.
 template <int D>
-__global__ void __launch_bounds__(NT) step_diff_mma_kernel(DiffStep s, Parts parts, ScoreFactor f) {
+struct Ring {
+    static constexpr int KB = D > 64 ? 2 : 1;    // 64-column blocks of a row
+    static constexpr int PIECE = KB * kTile * 128;
+    static constexpr int TILE = 4 * PIECE;
+    static constexpr int NS = D > 64 ? 6 : 8;    // tiles in flight
+    static constexpr int HEADS = 8, STREAMS = 2, P = 2 * D + 8;
+    struct Parts {
+        float so[STREAMS][2][HEADS][P];
+        float2 sml[STREAMS][2][HEADS];
+    };
+    static_assert(sizeof(Parts) <= NS * TILE, "the parts over the ring");
+    static constexpr int BYTES = NS * TILE + 1024;  // the ring starts on a 1024-byte boundary
+};
+constexpr int kMmaThreads = 160;  // four warps of products, one of loads
+
+template <int D>
+__global__ void __launch_bounds__(kMmaThreads)
+    step_diff_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv, DiffStep s,
+                         Parts parts, ScoreFactor f) {
+    using R = Ring<D>;
     const StepArgs &a = s.a;
     const float c = f.c;
     const __nv_bfloat162 sign = __float2bfloat162_rn(f.sign);
@@ -199,10 +223,11 @@ __global__ void __launch_bounds__(NT) step_diff_mma_kernel(DiffStep s, Parts par
     };
     constexpr int KC = D / 32;   // 32-channel pieces of a key: 16 bytes per lane and row
     constexpr int VW = D / 16;   // words of a value half-row per lane = 16-channel blocks of O^T
-    constexpr int HEADS = 8, STREAMS = NT / 64;
-    __shared__ float so[STREAMS][2][HEADS][2 * D + 8];
-    __shared__ float2 sml[STREAMS][2][HEADS];
-    __shared__ long long rows[kMostTiles];  // first cache row of each tile (head 0), -1: a bad page
+    constexpr int HEADS = R::HEADS, STREAMS = R::STREAMS;
+    extern __shared__ uint8_t raw[];
+    __shared__ int pages[kMostTiles];  // of each tile, -1: outside the pool
+    __shared__ uint64_t full[R::NS], empty[R::NS];
+    uint8_t *ring = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int map = warp & 1, stream = warp >> 1;
     const int G = a.Hq / a.Hk, gq = (G + HEADS - 1) / HEADS;
@@ -223,14 +248,19 @@ __global__ void __launch_bounds__(NT) step_diff_mma_kernel(DiffStep s, Parts par
     const int per = parts.chunk / kTile, t0 = split * per, t1 = min(tiles.count, t0 + per);
     if (t0 >= tiles.count && split > 0 && !parts.cluster) return;  // the join knows how many chunks there are
 
-    for (int i = tid; i < t1 - t0; i += NT) {
-        const int key = tiles.key(t0 + i);
-        const int page = a.table[(size_t)n * a.max_pages + (key >> a.page_log2)];
-        const bool ok = page >= 0 && page < a.num_pages;
-        if (!ok) atomicOr(&g_step_diff_error, kAttnIndex);
-        rows[i] = ok ? (((long long)page * 2 * a.Hk + 2 * hk) << a.page_log2) + (key & ((1 << a.page_log2) - 1)) : -1;
+    if (tid == 0) {
+        for (int i = 0; i < R::NS; ++i) {
+            tc::mbar_init(&full[i], 1);
+            tc::mbar_init(&empty[i], 2);  // the warps of both maps
+        }
+        tc::fence_mbar_init();
     }
-
+    for (int i = tid; i < t1 - t0; i += kMmaThreads) {
+        const int page = a.table[(size_t)n * a.max_pages + (tiles.key(t0 + i) >> a.page_log2)];
+        const bool in = page >= 0 && page < a.num_pages;
+        if (!in) atomicOr(&g_step_diff_error, kAttnIndex);
+        pages[i] = in ? page : -1;
+    }
     // queries of the warp's map: head g, the channels that the lane's keys hold
     uint32_t q[2 * KC][2];
     {
@@ -247,127 +277,143 @@ __global__ void __launch_bounds__(NT) step_diff_mma_kernel(DiffStep s, Parts par
     }
     __syncthreads();
 
+    bool ok = true;
     float acc[2 * VW][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
     for (int j = 0; j < 2 * VW; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
-    uint4 kr[2][KC];            // keys g and g + 8
-    uint32_t vr[4][2 * VW];     // values of keys 2t, 2t+1, 2t+8, 2t+9, both halves
-    const long long head_rows = 1ll << a.page_log2;  // rows of a head in a page
-    const __nv_bfloat16 *kp = static_cast<const __nv_bfloat16 *>(a.k) + map * head_rows * D,
-                        *vp = static_cast<const __nv_bfloat16 *>(a.v);
-    // Rows that the sequence does not see are not read: zeros.
-    auto load_k = [&](int i) {
-        const long long row = rows[i - t0];
-        const int key = tiles.key(i);
-#pragma unroll
-        for (int r = 0; r < 2; ++r) {
-            const bool on = row >= 0 && tiles.sees(key + g + 8 * r);
-            const __nv_bfloat16 *p = kp + (row + g + 8 * r) * D + 8 * t;
-#pragma unroll
-            for (int i2 = 0; i2 < KC; ++i2) {
-                kr[r][i2] = make_uint4(0, 0, 0, 0);
-                if (on) kr[r][i2] = load_once16(p + 32 * i2);
+    if (warp == 4) {
+        // loads: a box of 16 rows x 64 columns a lane
+        const int piece = lane / R::KB, kb = lane - piece * R::KB;
+        int i = t0;
+        for (; i < t1; ++i) {
+            const int k = i - t0, slot = k % R::NS, page = pages[k];
+            if (k >= R::NS) ok = __all_sync(0xffffffffu, tc::mbar_wait(&empty[slot], (k / R::NS - 1) & 1));
+            if (!ok) break;
+            if (lane == 0) {
+                if (page >= 0) tc::mbar_expect_tx(&full[slot], R::TILE);
+                else tc::mbar_arrive(&full[slot]);  // nothing is read of it
             }
+            __syncwarp();
+            if (page >= 0 && lane < 4 * R::KB)
+                tc::tma_load_4d(ring + slot * R::TILE + lane * (kTile * 128), piece < 2 ? &tmk : &tmv, 64 * kb,
+                                tiles.key(i) & ((1 << a.page_log2) - 1), 2 * hk + (piece & 1), page, &full[slot]);
         }
-    };
-    auto load_v = [&](int i) {
-        const long long row = rows[i - t0];
-        const int key = tiles.key(i);
+        // never leave with copies into shared memory in flight
+        for (int k = max(0, i - t0 - R::NS); k < i - t0; ++k)
+            if (!tc::mbar_wait(&full[k % R::NS], (k / R::NS) & 1)) ok = false;
+    } else {
+        for (int i = t0 + stream; i < t1; i += STREAMS) {
+            const int k = i - t0, slot = k % R::NS, key = tiles.key(i);
+            ok = __all_sync(0xffffffffu, tc::mbar_wait(&full[slot], (k / R::NS) & 1));
+            if (!ok) break;
+            const uint8_t *tile = ring + slot * R::TILE, *kt = tile + map * R::PIECE;
+            const bool page_ok = pages[k] >= 0;
+            // rows that the sequence does not see: scores of -inf, values of zero
+            const bool all = page_ok && tiles.sees(key) && tiles.sees(key + kTile - 1) &&
+                             (key >= tiles.s.lo || key + kTile <= tiles.s.s1);
+            float sc[4] = {0.f, 0.f, 0.f, 0.f}, sd[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const int kk = 2 * t + (r & 1) + 8 * (r >> 1);
-            const bool on = row >= 0 && tiles.sees(key + kk);
+            for (int j = 0; j < KC; ++j) {
+                // chunk of 8 channels (j & 1) 4 + t of block j / 2, rows g and g + 8
+                const uint8_t *p = kt + (j >> 1) * (kTile * 128) + g * 128 + ((((j & 1) * 4 + t) ^ g) << 4);
+                const uint4 x = *reinterpret_cast<const uint4 *>(p), y = *reinterpret_cast<const uint4 *>(p + 1024);
+                mma16816(sc, x.x, y.x, x.y, y.y, q[2 * j][0], q[2 * j][1]);
+                mma16816(sd, x.z, y.z, x.w, y.w, q[2 * j + 1][0], q[2 * j + 1][1]);
+            }
+            const bool see0 = all || (page_ok && tiles.sees(key + g)), see1 = all || (page_ok && tiles.sees(key + g + 8));
+            bool grow = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float x = (e < 2 ? see0 : see1) ? sc[e] + sd[e] : -INFINITY, y = m[e & 1];
+                sc[e] = x;
+                grow = grow || (x > y && !((x - y) * c <= 8.f));
+            }
+            // the maximum in use is raised only when a score passes it by 2^8
+            if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float mx = fmaxf(sc[e], sc[e + 2]);
+#pragma unroll
+                    for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+                    const float mn = fmaxf(m[e], mx);
+                    const float less = m[e] == -INFINITY ? 0.f : ex2((m[e] - mn) * c);
+                    m[e] = mn;
+                    // nothing seen yet: sums and output are zero (or NaN, which stays)
+                    l[e] *= less;
+#pragma unroll
+                    for (int j = 0; j < 2 * VW; ++j) acc[j][e] *= less, acc[j][e + 2] *= less;
+                }
+            }
+            const float b0 = m[0] == -INFINITY ? 0.f : m[0], b1 = m[1] == -INFINITY ? 0.f : m[1];
+            // differences first: a product of one large score would overflow
+            const float2 e0 = make_float2(ex2((sc[0] - b0) * c), ex2((sc[1] - b1) * c)),
+                         e1 = make_float2(ex2((sc[2] - b0) * c), ex2((sc[3] - b1) * c));
+            l[0] += e0.x + e1.x;
+            l[1] += e0.y + e1.y;
+            // the weights, and as weights of their own what their rounding left
+            uint32_t r0, r1;
+            const uint32_t p0 = transpose8x8(tc::pack2_rest(e0, r0)), p1 = transpose8x8(tc::pack2_rest(e1, r1));
+            r0 = transpose8x8(r0), r1 = transpose8x8(r1);
 #pragma unroll
             for (int half = 0; half < 2; ++half) {
-                const __nv_bfloat16 *p = vp + (row + half * head_rows + kk) * D;
+                uint32_t vr[4][VW];  // values of keys 2t, 2t+1, 2t+8, 2t+9
 #pragma unroll
-                for (int w = 0; w < VW; ++w) vr[r][half * VW + w] = 0u;
-                if (!on) continue;
-                if (D == 32) {
-                    const uint2 x = __ldg(reinterpret_cast<const uint2 *>(p + 4 * g));
-                    vr[r][half * VW] = x.x, vr[r][half * VW + 1] = x.y;
-                } else {
+                for (int r = 0; r < 4; ++r) {
+                    const int row = 2 * t + (r & 1) + 8 * (r >> 1);
+                    const uint8_t *p = tile + (2 + half) * R::PIECE + row * 128;
+                    if (D == 32) {
+                        const uint2 x = *reinterpret_cast<const uint2 *>(p + (((g >> 1) ^ (row & 7)) << 4) + (g & 1) * 8);
+                        vr[r][0] = x.x, vr[r][1] = x.y;
+                    } else {
 #pragma unroll
-                    for (int w = 0; w < VW / 4; ++w) {
-                        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(p + 64 * w + 8 * g));
-                        uint32_t *to = &vr[r][half * VW + 4 * w];
-                        to[0] = x.x, to[1] = x.y, to[2] = x.z, to[3] = x.w;
+                        for (int w = 0; w < VW / 4; ++w) {
+                            const uint4 x =
+                                *reinterpret_cast<const uint4 *>(p + w * (kTile * 128) + ((g ^ (row & 7)) << 4));
+                            vr[r][4 * w] = x.x, vr[r][4 * w + 1] = x.y, vr[r][4 * w + 2] = x.z, vr[r][4 * w + 3] = x.w;
+                        }
                     }
+                    if (!all && !(page_ok && tiles.sees(key + row))) {
+#pragma unroll
+                        for (int w = 0; w < VW; ++w) vr[r][w] = 0u;
+                    }
+                }
+                if (half == 1) {  // the tile has been read
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(&empty[slot]);
+                }
+#pragma unroll
+                for (int j = 0; j < VW; ++j) {
+                    const uint32_t a0 = __byte_perm(vr[0][j], vr[1][j], 0x5410), a1 = __byte_perm(vr[0][j], vr[1][j], 0x7632),
+                                   a2 = __byte_perm(vr[2][j], vr[3][j], 0x5410), a3 = __byte_perm(vr[2][j], vr[3][j], 0x7632);
+                    mma16816(acc[half * VW + j], a0, a1, a2, a3, p0, p1);
+                    mma16816(acc[half * VW + j], a0, a1, a2, a3, r0, r1);
                 }
             }
         }
-    };
-
-    const int first = t0 + stream;
-    if (first < t1) {
-        load_k(first);
-        load_v(first);
     }
-    for (int i = first; i < t1; i += STREAMS) {
-        float sc[4] = {0.f, 0.f, 0.f, 0.f};
+    if (!ok) atomicOr(&g_step_diff_error, kAttnTimeout);
+    __syncthreads();  // the ring is free
+    typename R::Parts &own = *reinterpret_cast<typename R::Parts *>(ring);
+    if (warp < 4) {
+        // this warp's part: word j of a half's lane holds channels col_j and col_j + 1
 #pragma unroll
-        for (int i2 = 0; i2 < KC; ++i2) {
-            mma16816(sc, kr[0][i2].x, kr[1][i2].x, kr[0][i2].y, kr[1][i2].y, q[2 * i2][0], q[2 * i2][1]);
-            mma16816(sc, kr[0][i2].z, kr[1][i2].z, kr[0][i2].w, kr[1][i2].w, q[2 * i2 + 1][0], q[2 * i2 + 1][1]);
-        }
-        const bool page_ok = rows[i - t0] >= 0;
-        const int key = tiles.key(i);
-        const bool see0 = page_ok && tiles.sees(key + g), see1 = page_ok && tiles.sees(key + g + 8);
-        const int next = i + STREAMS;
-        if (next < t1) load_k(next);
-        bool grow = false;
+        for (int e = 0; e < 2; ++e) {
+            float sum = l[e];
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const float x = (e < 2 ? see0 : see1) ? sc[e] : -INFINITY, y = m[e & 1];
-            sc[e] = x;
-            grow = grow || (x > y && !((x - y) * c <= 8.f));
-        }
-        // the maximum in use is raised only when a score passes it by 2^8
-        if (__any_sync(0xffffffffu, grow)) {
+            for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
+            const int h = 2 * t + e;
+            if (g == 0) own.sml[stream][map][h] = make_float2(m[e], sum);
 #pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float mx = fmaxf(sc[e], sc[e + 2]);
-#pragma unroll
-                for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-                const float mn = fmaxf(m[e], mx);
-                const float less = m[e] == -INFINITY ? 0.f : ex2((m[e] - mn) * c);
-                m[e] = mn;
-                // nothing seen yet: sums and output are zero (or NaN, which stays)
-                l[e] *= less;
-#pragma unroll
-                for (int j = 0; j < 2 * VW; ++j) acc[j][e] *= less, acc[j][e + 2] *= less;
+            for (int j = 0; j < 2 * VW; ++j) {
+                const int w = j % VW, col = D == 32 ? 4 * g + 2 * w : 64 * (w >> 2) + 8 * g + 2 * (w & 3);
+                *reinterpret_cast<float2 *>(&own.so[stream][map][h][j / VW * D + col]) =
+                    make_float2(acc[j][e], acc[j][e + 2]);
             }
         }
-        const float b0 = m[0] == -INFINITY ? 0.f : m[0], b1 = m[1] == -INFINITY ? 0.f : m[1];
-        // differences first: a product of one large score would overflow
-        const float e0 = ex2((sc[0] - b0) * c), e1 = ex2((sc[1] - b1) * c), e2 = ex2((sc[2] - b0) * c),
-                    e3 = ex2((sc[3] - b1) * c);
-        l[0] += e0 + e2;
-        l[1] += e1 + e3;
-        const uint32_t p0 = transpose8x8(pack2(e0, e1)), p1 = transpose8x8(pack2(e2, e3));
-#pragma unroll
-        for (int j = 0; j < 2 * VW; ++j)
-            mma16816(acc[j], __byte_perm(vr[0][j], vr[1][j], 0x5410), __byte_perm(vr[0][j], vr[1][j], 0x7632),
-                     __byte_perm(vr[2][j], vr[3][j], 0x5410), __byte_perm(vr[2][j], vr[3][j], 0x7632), p0, p1);
-        if (next < t1) load_v(next);
     }
-    // this warp's part: word j of a half's lane holds channels col_j and col_j + 1
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-        float sum = l[e];
-#pragma unroll
-        for (int w = 4; w < 32; w <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
-        const int h = 2 * t + e;
-        if (g == 0) sml[stream][map][h] = make_float2(m[e], sum);
-#pragma unroll
-        for (int j = 0; j < 2 * VW; ++j) {
-            const int w = j % VW, col = D == 32 ? 4 * g + 2 * w : 64 * (w >> 2) + 8 * g + 2 * (w & 3);
-            *reinterpret_cast<float2 *>(&so[stream][map][h][j / VW * D + col]) = make_float2(acc[j][e], acc[j][e + 2]);
-        }
-    }
-    finish<__nv_bfloat16, D, STREAMS, HEADS, 2 * D + 8>(so, sml, heads, n, h0, split, f, s, parts);
+    finish<__nv_bfloat16, D, STREAMS, HEADS, R::P, kMmaThreads>(own.so, own.sml, heads, n, h0, split, f, s, parts);
 }
 
 // ------------------------------------------------------------------- fp32
@@ -513,7 +559,7 @@ __global__ void __launch_bounds__(NT) step_diff_simt_kernel(DiffStep s, Parts pa
                 if (lane == 0) sml[warp][map][g] = make_float2(mn, l[map][g]);
             }
         }
-    finish<float, D, STREAMS, GC, 2 * D>(so, sml, heads, n, h0, split, f, s, parts);
+    finish<float, D, STREAMS, GC, 2 * D, NT>(so, sml, heads, n, h0, split, f, s, parts);
 }
 
 // A warp per pair of a sequence: the chunks' parts in order.
@@ -550,15 +596,29 @@ cudaError_t launch(const DiffStep &s, void *ws, lr_dtype dt, cudaStream_t stream
     const unsigned grid = (unsigned)(a.N * a.Hk * ((G + gc - 1) / gc) * p.splits);
     const int cluster = p.cluster ? p.splits : 1;
     const ScoreFactor f = score_factor(a.scale);
-    const cudaError_t e = dt == LR_DT_BF16 ? launch_cut(&step_diff_mma_kernel<D>, grid, NT, cluster, stream, s, parts, f)
-                          : gc == 1 ? launch_cut(&step_diff_simt_kernel<D, 1>, grid, NT, cluster, stream, s, parts, f)
-                                    : launch_cut(&step_diff_simt_kernel<D, 2>, grid, NT, cluster, stream, s, parts, f);
+    cudaError_t e;
+    if (dt == LR_DT_BF16) {
+        CUtensorMap mk, mv;
+        e = tc::pool_map(&mk, a.k, D, 1 << a.page_log2, 2 * a.Hk, a.num_pages, kTile);
+        if (e == cudaSuccess) e = tc::pool_map(&mv, a.v, D, 1 << a.page_log2, 2 * a.Hk, a.num_pages, kTile);
+        auto *fn = &step_diff_mma_kernel<D>;
+        if (e == cudaSuccess)
+            e = ensure_smem_attr(reinterpret_cast<const void *>(fn), Ring<D>::BYTES, 233 + D / 64);
+        if (e == cudaSuccess)
+            e = launch_cut(fn, grid, kMmaThreads, cluster, Ring<D>::BYTES, stream, mk, mv, s, parts, f);
+    } else if (gc == 1) {
+        e = launch_cut(&step_diff_simt_kernel<D, 1>, grid, NT, cluster, 0, stream, s, parts, f);
+    } else {
+        e = launch_cut(&step_diff_simt_kernel<D, 2>, grid, NT, cluster, 0, stream, s, parts, f);
+    }
     if (e != cudaSuccess || p.splits == 1 || p.cluster) return e;
     const unsigned rows = (unsigned)(a.N * a.Hq);
     if (dt == LR_DT_F32) step_diff_join_kernel<float, D><<<rows, 32, 0, stream>>>(s, parts, f);
     else step_diff_join_kernel<__nv_bfloat16, D><<<rows, 32, 0, stream>>>(s, parts, f);
     return cudaGetLastError();
 }
+
+// ensure_smem_attr slots 233..235 belong to this file.
 
 }  // namespace
 
@@ -568,7 +628,8 @@ StepPlan diff_step_plan(int N, int H, int Hk, int d, int max_len, int window, in
     const long long most = w < max_len ? w + (dt == LR_DT_BF16 ? 2 * kTile + (sinks > 0 ? kTile : 0) : 0) : max_len;
     const int seen = (int)(most < max_len ? most : max_len);
     const int G = H / Hk, pairs = pairs_of_cta(G, dt);
-    const int per_sm = dt == LR_DT_BF16 ? (d < 128 ? 4 : 2) : 3;
+    // CTAs on an SM: the rings fill its shared memory; registers in fp32
+    const int per_sm = dt == LR_DT_BF16 && d == 128 ? 2 : 3;
     return plan_chunks(seen, (long long)N * Hk * ((G + pairs - 1) / pairs), per_sm, kClusterRoom[per_sm - 1]);
 }
 

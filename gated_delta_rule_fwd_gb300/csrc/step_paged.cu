@@ -622,9 +622,9 @@ cudaError_t launch_f32(const StepArgs &a, const Parts &parts, cudaStream_t strea
     const int gc = heads_of_cta(G, LR_DT_F32);
     const unsigned grid = (unsigned)(a.N * a.Hk * ((G + gc - 1) / gc) * parts.splits);
     const ScoreFactor f = score_factor(a.scale);
-    if (gc == 1) return launch_cut(&step_simt_kernel<D, 1>, grid, NT, parts.cluster ? parts.splits : 1, stream, a, parts, f);
-    if (gc == 2) return launch_cut(&step_simt_kernel<D, 2>, grid, NT, parts.cluster ? parts.splits : 1, stream, a, parts, f);
-    return launch_cut(&step_simt_kernel<D, 4>, grid, NT, parts.cluster ? parts.splits : 1, stream, a, parts, f);
+    if (gc == 1) return launch_cut(&step_simt_kernel<D, 1>, grid, NT, parts.cluster ? parts.splits : 1, 0, stream, a, parts, f);
+    if (gc == 2) return launch_cut(&step_simt_kernel<D, 2>, grid, NT, parts.cluster ? parts.splits : 1, 0, stream, a, parts, f);
+    return launch_cut(&step_simt_kernel<D, 4>, grid, NT, parts.cluster ? parts.splits : 1, 0, stream, a, parts, f);
 }
 
 template <int D>
@@ -632,8 +632,8 @@ cudaError_t launch_bf16(const StepArgs &a, const Parts &parts, cudaStream_t stre
     const int G = a.Hq / a.Hk, heads = heads_of_cta(G, LR_DT_BF16);
     const unsigned grid = (unsigned)(a.N * a.Hk * ((G + heads - 1) / heads) * parts.splits);
     const ScoreFactor f = score_factor(a.scale);
-    if (heads == 8) return launch_cut(&step_mma_kernel<D, 1>, grid, NT, parts.cluster ? parts.splits : 1, stream, a, parts, f);
-    return launch_cut(&step_mma_kernel<D, 2>, grid, NT, parts.cluster ? parts.splits : 1, stream, a, parts, f);
+    if (heads == 8) return launch_cut(&step_mma_kernel<D, 1>, grid, NT, parts.cluster ? parts.splits : 1, 0, stream, a, parts, f);
+    return launch_cut(&step_mma_kernel<D, 2>, grid, NT, parts.cluster ? parts.splits : 1, 0, stream, a, parts, f);
 }
 
 template <int D>
