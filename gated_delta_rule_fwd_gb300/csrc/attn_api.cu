@@ -172,8 +172,8 @@ lr_status check_diff_sizes(int B, int H, int Hk, int Tq, int Tk, int d, lr_dtype
     if (Tq > (1 << 30) || Tk > (1 << 30) || !count_ok(B, 2ll * H, Tq, 2ll * d) ||
         !count_ok(B, 2ll * Hk, Tk, d))
         return LR_ERR_SHAPE;
-    // row tiles, counted as CTAs of one launch
-    if (!count_ok(B, 2ll * H, Tq / 64 + 1, 1) || 2ll * B * H * (Tq / 64 + 1) > 0x7fffffffll)
+    // row tiles of both maps over both halves of the values, counted as CTAs of one launch
+    if (!count_ok(B, 4ll * H, Tq / 64 + 1, 1) || 4ll * B * H * (Tq / 64 + 1) > 0x7fffffffll)
         return LR_ERR_SHAPE;
     return LR_OK;
 }
@@ -343,7 +343,7 @@ lr_status lr_fwd_window(const void *q, lr_strides qs, const void *k, lr_strides 
           span(k_len, (size_t)B * 4)})
         if (overlap(so, i)) return LR_ERR_ALIAS;
     const WindowArgs a{q, k, v, o, qs, ks, vs, os, q_len, k_len, B, Hq, Hk, Tq, Tk, window, sinks,
-                       scale};
+                       scale, 0};
     if (Tk == 0) return done(launch_window_zero(a, d, dt, stream));
     return done(dt == LR_DT_BF16 ? launch_window_tc(a, d, stream)
                                  : launch_window_f32(a, d, stream));
@@ -381,7 +381,7 @@ lr_status lr_fwd_diff(const void *q, lr_strides qs, const void *k, lr_strides ks
     if (overlap(so, sw)) return LR_ERR_ALIAS;
     if (Tk == 0) {
         const WindowArgs w{q, k, v, o, qs, ks, vs, os, q_len, k_len, B, 2 * H, 2 * Hk, Tq, Tk, window,
-                           sinks, scale};
+                           sinks, scale, 0};
         return done(launch_window_zero(w, d, dt, stream));
     }
     const DiffArgs a{q, k, v, o, qs, ks, vs, os, q_len, k_len, maps->lambda, maps->weight, B, H, Hk,

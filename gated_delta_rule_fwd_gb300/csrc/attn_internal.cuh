@@ -137,6 +137,10 @@ struct WindowArgs {
     const int *q_len, *k_len;
     int B, Hq, Hk, Tq, Tk, window, sinks;
     float scale;
+    // fp32: the parts of differential attention.  Of the Hq = 4 x pairs outputs, 4 h
+    // + 2 m + j is map m of pair h over half j of its values; Hk counts the pairs of
+    // key heads.
+    int pairs;
 };
 // fp32, Tk >= 1 (window_f32.cu).
 cudaError_t launch_window_f32(const WindowArgs &a, int d, cudaStream_t stream);

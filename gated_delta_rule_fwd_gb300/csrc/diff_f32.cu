@@ -1,6 +1,8 @@
 // lr_fwd_diff in fp32: the two maps of a pair by the fp32 window kernel
-// (window_f32.cu), each over both halves of the value row, into the workspace,
-// then one pass that takes the difference and its norm (attn_diff.cuh).
+// (window_f32.cu), each over both halves of the value row, into the workspace in
+// one launch, then one pass that takes the difference and its norm (attn_diff.cuh).
+// The scores are formed twice, once for each half (8 units of products where 6
+// would do): a row's 2 d channels of output leave no registers for both.
 #include "attn_diff.cuh"
 #include "attn_internal.cuh"
 
@@ -9,7 +11,7 @@ namespace {
 
 constexpr int NT = 128;
 
-// maps: [map][half][B][H][Tq][D].  A warp per row of a pair.
+// maps: [B][H][map][half][Tq][D].  A warp per row of a pair.
 template <int D>
 __global__ void __launch_bounds__(NT) diff_join_kernel(DiffArgs a, const float *maps) {
     constexpr int PL = D / 32;
@@ -26,8 +28,8 @@ __global__ void __launch_bounds__(NT) diff_join_kernel(DiffArgs a, const float *
     for (int half = 0; half < 2; ++half)
 #pragma unroll
         for (int c = 0; c < PL; ++c) {
-            const float *x = maps + (half * rows + r) * D + lane + 32 * c;
-            y[half][c] = fmaf(-lambda, x[2 * rows * D], x[0]);
+            const float *x = maps + (((long long)bh * 4 + half) * a.Tq + i) * D + lane + 32 * c;
+            y[half][c] = fmaf(-lambda, x[2ll * a.Tq * D], x[0]);
             sum = fmaf(y[half][c], y[half][c], sum);
         }
     const float f = a.norm ? diff_rms(warp_sum(sum), D, a.eps) : 1.f;
@@ -52,26 +54,11 @@ size_t diff_f32_workspace_bytes(int B, int H, int Tq, int d) { return (size_t)B 
 
 cudaError_t launch_diff_f32(const DiffArgs &a, int d, void *ws, cudaStream_t stream) {
     float *maps = static_cast<float *>(ws);
-    const long long rows = (long long)a.B * a.H * a.Tq;
-    auto pairs = [](lr_strides s) {
-        s.h *= 2;
-        return s;
-    };
-    for (int m = 0; m < 2; ++m)
-        for (int half = 0; half < 2; ++half) {
-            WindowArgs w{};
-            w.q = static_cast<const float *>(a.q) + m * a.qs.h;
-            w.k = static_cast<const float *>(a.k) + m * a.ks.h;
-            w.v = static_cast<const float *>(a.v) + half * a.vs.h;
-            w.o = maps + (2 * m + half) * rows * d;
-            w.qs = pairs(a.qs), w.ks = pairs(a.ks), w.vs = pairs(a.vs);
-            w.os = {(long long)a.H * a.Tq * d, (long long)a.Tq * d, d};
-            w.q_len = a.q_len, w.k_len = a.k_len;
-            w.B = a.B, w.Hq = a.H, w.Hk = a.Hk, w.Tq = a.Tq, w.Tk = a.Tk;
-            w.window = a.window, w.sinks = a.sinks, w.scale = a.scale;
-            const cudaError_t e = launch_window_f32(w, d, stream);
-            if (e != cudaSuccess) return e;
-        }
+    WindowArgs w{a.q, a.k, a.v, maps, a.qs, a.ks, a.vs, {}, a.q_len, a.k_len, a.B, 4 * a.H, a.Hk, a.Tq, a.Tk,
+                 a.window, a.sinks, a.scale, 1};
+    w.os = {4ll * a.H * a.Tq * d, (long long)a.Tq * d, d};
+    const cudaError_t e = launch_window_f32(w, d, stream);
+    if (e != cudaSuccess) return e;
     if (d == 32) join<32>(a, maps, stream);
     else if (d == 64) join<64>(a, maps, stream);
     else join<128>(a, maps, stream);

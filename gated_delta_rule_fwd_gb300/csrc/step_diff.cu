@@ -73,16 +73,30 @@ __device__ __forceinline__ void finish_pair(const DiffStep &s, int n, int h, int
     float y[N], sums[2];
 #pragma unroll
     for (int map = 0; map < 2; ++map) {
-        float mn = -INFINITY, sum = 0.f, x[N];
-        for (int i = 0; i < count; ++i) mn = fmaxf(mn, ml(i, map).x);
+        float top = -INFINITY, sum = 0.f, x[N];
 #pragma unroll
         for (int c = 0; c < N; ++c) x[c] = 0.f;
-        for (int i = 0; i < count; ++i) {
-            const float2 t = ml(i, map);
-            const float w = t.x == -INFINITY ? 0.f : ex2((t.x - mn) * f.c);
-            sum += w * t.y;
+        // a lane a part, then all lanes part by part: the loads of a batch do not
+        // wait for each other
+        for (int i0 = 0; i0 < count; i0 += 32) {
+            const float2 t = i0 + lane < count ? ml(i0 + lane, map) : make_float2(-INFINITY, 0.f);
+            float mn = t.x;
 #pragma unroll
-            for (int c = 0; c < N; ++c) x[c] += w * value(i, map, lane + 32 * c);
+            for (int w = 16; w; w >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, w));
+            mn = fmaxf(mn, top);
+            const float less = top == -INFINITY ? 0.f : ex2((top - mn) * f.c);
+            const float w = t.x == -INFINITY ? 0.f : ex2((t.x - mn) * f.c);
+            sum = sum * less + warp_sum(w * t.y);
+#pragma unroll
+            for (int c = 0; c < N; ++c) x[c] *= less;
+            const int many = min(32, count - i0);
+#pragma unroll 4
+            for (int j = 0; j < many; ++j) {
+                const float wj = __shfl_sync(0xffffffffu, w, j);
+#pragma unroll
+                for (int c = 0; c < N; ++c) x[c] += wj * value(i0 + j, map, lane + 32 * c);
+            }
+            top = mn;
         }
         sums[map] = sum;
         // no key, or only scores of -inf: zeros

@@ -73,16 +73,18 @@ __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float 
     const unsigned block = SPLIT ? blockIdx.x / splits : blockIdx.x, rank = SPLIT ? blockIdx.x - block * splits : 0;
     const unsigned heads = (unsigned)(a.B * a.Hq), turn = block / heads, bh = block - turn * heads;
     const int tile = tiles - 1 - (int)turn;
-    const int b = bh / a.Hq, h = bh - b * a.Hq, hk = h / (a.Hq / a.Hk);
+    const int b = bh / a.Hq, h = bh - b * a.Hq;
+    int hq = h, hk = h / (a.Hq / a.Hk), hv = hk;
+    if (a.pairs) hq = h >> 1, hv = 2 * hk + (h & 1), hk = 2 * hk + (hq & 1);
     bool bad = false;
     const int ql = clamp_len(a.q_len, b, a.Tq, &bad), kl = clamp_len(a.k_len, b, a.Tk, &bad);
     if (bad && threadIdx.x == 0) atomicOr(&g_window_error, kAttnIndex);
     const int i0 = tile * BQ;
     if (i0 >= ql) return;
     const int rows = min(BQ, ql - i0), p0 = kl - ql + i0;
-    const float *q = static_cast<const float *>(a.q) + b * a.qs.b + h * a.qs.h + (long long)i0 * a.qs.t;
+    const float *q = static_cast<const float *>(a.q) + b * a.qs.b + hq * a.qs.h + (long long)i0 * a.qs.t;
     const float *k = static_cast<const float *>(a.k) + b * a.ks.b + hk * a.ks.h;
-    const float *v = static_cast<const float *>(a.v) + b * a.vs.b + hk * a.vs.h;
+    const float *v = static_cast<const float *>(a.v) + b * a.vs.b + hv * a.vs.h;
     float *o = static_cast<float *>(a.o) + b * a.os.b + h * a.os.h + (long long)i0 * a.os.t;
 
     // key tiles: the sinks' before the window of every row, then the window's
