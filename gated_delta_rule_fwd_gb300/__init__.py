@@ -23,6 +23,9 @@ missing or cannot be loaded, every call raises.
         softmax attention with a sliding window and sinks, over whole sequences
         and for single tokens over a paged cache, and the norm and rotation of
         queries and keys before it (attention.py, ``include/lr_attn.h``)
+    lr_qk_norm_rope_axes / lr_step_paged_prefix / lr_fwd_diff / lr_step_paged_diff(...)
+        positions of several axes; the step of a batch that shares a prefix;
+        differential attention over whole sequences and its step
 """
 from __future__ import annotations
 

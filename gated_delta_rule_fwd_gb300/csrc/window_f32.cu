@@ -24,7 +24,7 @@
 // visible work; the tensor pipe is busy 37 % of the time of an SM that has work.
 // What bounds it is the issue of about 1000 instructions per warp and tile, a
 // third of them the splitting, by few warps (registers).  At d = 128 all 255
-// registers are taken and 360 bytes a thread spilled: queries and outputs of 16
+// registers are taken and about 300 bytes a thread spilled: queries and outputs of 16
 // rows are 128 of them, and one group of warps with fewer rows was slower.
 // The order of channels inside a product, and of keys inside the second one,
 // is free: it is chosen so that every lane reads 16 contiguous bytes of a row
