@@ -166,6 +166,7 @@ cudaError_t launch_diff_f32(const DiffArgs &a, int d, void *ws, cudaStream_t str
 size_t diff_f32_workspace_bytes(int B, int H, int Tq, int d);
 // Tensor cores, bf16, Tk >= 1 (diff_tc.cu).
 cudaError_t launch_diff_tc(const DiffArgs &a, int d, cudaStream_t stream);
+cudaError_t launch_diff_wide_tc(const DiffArgs &a, cudaStream_t stream);  // d = 128
 
 struct StepArgs {
     const void *q, *k, *v;
@@ -223,6 +224,7 @@ int attn_errors_window_f32();
 int attn_errors_window_tc();
 int attn_errors_step();
 int attn_errors_diff_tc();
+int attn_errors_diff_wide();
 int attn_errors_step_diff();
 int attn_errors_prefix_tc();
 int attn_errors_prefix_f32();

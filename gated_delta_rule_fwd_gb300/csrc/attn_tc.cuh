@@ -239,16 +239,17 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     return fn;
 }
 
-// A strided [B, H, T, d] tensor, boxes of 128 rows x 64 columns, 128-byte
+// A strided [B, H, T, d] tensor, boxes of `rows` rows x 64 columns, 128-byte
 // swizzle, zero fill outside (also the columns of a box wider than d).
-inline cudaError_t rows_map(CUtensorMap *m, const void *base, const lr_strides &s, int B, int H, int T, int d) {
+inline cudaError_t rows_map(CUtensorMap *m, const void *base, const lr_strides &s, int B, int H, int T, int d,
+                            int rows = 128) {
     auto enc = encoder();
     if (!enc) return cudaErrorNotSupported;
     const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)T, (cuuint64_t)H, (cuuint64_t)B};
     // a dimension of size 1 has stride 0 here: any valid one will do
     auto bytes = [d](long long st) { return (cuuint64_t)(st ? st * 2 : d * 2); };
     const cuuint64_t strides[3] = {bytes(s.t), bytes(s.h), bytes(s.b)};
-    const cuuint32_t box[4] = {64, 128, 1, 1};
+    const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims,
                            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,

@@ -19,25 +19,22 @@
 // multiply what that rounding left as well (1.39; 8192 causal tokens of 8 pairs, d
 // = 64: 155 -> 173 us; with half of them 1.27 and 196 us, with all 1.0 and 267 us).
 //
-// Tensor memory holds 2 x 128 columns of scores and 2 x 128 of output.  With d =
-// 128 the values have 256 channels: two CTAs of a cluster take a half each and
-// both form all scores (8 units of products where 6 would do).  A row's sum of
-// squares is exchanged through distributed shared memory.
+// Tensor memory holds 2 x 128 columns of scores and 2 x 128 of output, so d is 32
+// or 64 here (diff_wide_tc.cu: 128).
 //
 // A row's non-finite values, padding and the rounding of the exponent's base are
 // dealt with as in window_tc.cu.
 //
 // Roles of the 384 threads: warps 0-3 softmax of map 0 and the first half of the
-// CTA's channels, warps 4-7 of map 1 and the second half, warps 8 and 9 issue the
+// channels, warps 4-7 of map 1 and the second half, warps 8 and 9 issue the
 // products of maps 0 and 1, warp 10 the TMA loads, warp 11 works out the pieces.
 // The CTAs stay and take every n-th piece, longest first and in turning order, so
 // that loads and products of the next piece run under the last one's epilogue.
 // Every wait is bounded (lr_device_status).
 #include <algorithm>
 
-#include "attn_diff.cuh"
+#include "attn_diff_tc.cuh"
 #include "attn_internal.cuh"
-#include "attn_rows.cuh"
 #include "attn_tc.cuh"
 #include "tc_common.cuh"
 
@@ -48,7 +45,7 @@ using namespace tc;
 
 __device__ unsigned g_diff_error = 0;
 
-constexpr int BM = 128, BN = 128;
+constexpr int BM = kDiffRows, BN = kDiffKeys;
 // Threads and their registers: launched with 168 each (64,512 in all); the
 // softmax warpgroups take 216, the third one keeps 72.
 constexpr int NT = 384, kRegsSoftmax = 216, kRegsOther = 72;
@@ -56,22 +53,19 @@ static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsOther <= NT * 168, "register s
 
 template <int D>
 struct Layout {
-    static constexpr int KB = D > 64 ? 2 : 1;        // 64-column blocks of a query or key tile
-    static constexpr int CS = D > 64 ? 2 : 1;        // CTAs of a cluster, each a part of the channels
-    static constexpr int DV = 2 * D / CS;            // value channels of a CTA
-    static constexpr int TILE = KB * 128 * 128;      // bytes of a query or key tile
-    static constexpr int VTILE = 2 * 128 * 128;      // of a value tile: two 64-column blocks
-    static constexpr int NK = D > 64 ? 1 : 2;        // key tiles in flight per map
-    static constexpr int NV = 2;                     // value tiles in flight
+    static constexpr int DV = 2 * D;                 // value channels
+    static constexpr int TILE = 128 * 128;           // bytes of a query or key tile: one 64-column block
+    static constexpr int VTILE = 2 * 128 * 128;      // of a value tile: a block for each half
+    static constexpr int NK = 2, NV = 2;             // key tiles (per map) and value tiles in flight
     static constexpr int Q = 0;
     static constexpr int K = 2 * TILE;               // [map][slot]
     static constexpr int V = K + 2 * NK * TILE;
     static constexpr int OUT = V + NV * VTILE;       // 2 KB per softmax warp: rows on their way out
     static constexpr int SUM = OUT + 8 * 2048;       // [2][map][128] sums of weights
-    static constexpr int SQ = SUM + 2 * 2 * 128 * 4; // [2][2 CS][128] sums of squares
-    static constexpr int W = SQ + 2 * 2 * CS * 128 * 4;  // [2 D] weights of the norm
+    static constexpr int SQ = SUM + 2 * 2 * 128 * 4; // [2][2][128] sums of squares
+    static constexpr int W = SQ + 2 * 2 * 128 * 4;   // [2 D] weights of the norm
     static constexpr int BAR = W + 2 * D * 4;
-    static constexpr int ITEM = BAR + 384;           // two of struct Item
+    static constexpr int ITEM = BAR + 384;           // two of struct DiffItem
     static constexpr int BYTES = ITEM + 2 * 128;
     static constexpr int ALLOC = BYTES + 1024;
 };
@@ -79,118 +73,27 @@ struct Layout {
 struct Barriers {
     uint64_t qfull[2], qempty[2], sfull[2], pready[2][2], ofull[2], oempty, fin[2];
     uint64_t kfull[2][2], kempty[2][2], vfull[2], vempty[2];
-    uint64_t ifull[2], iempty[2], lfull, sqready, sqfull[2], pad;
+    uint64_t ifull[2], iempty[2], lfull, sqready, pad;
     uint32_t tmem, pipe;  // pipe: 1 while a warp issues products
 };
 
+static_assert(sizeof(Barriers) <= 384, "shared memory layout");
+
 constexpr uint32_t kS = 0, kO = 256;  // TMEM columns: S0, S1 (P over them), then O0, O1
-constexpr int kRest = 1;              // of a tile's four 32-key pieces, those with the rest of P's rounding
-
-struct TcArgs {
-    DiffArgs a;
-    float c;          // the scores' factor, positive
-    unsigned negate;  // idesc bit: scores of -Q (scale < 0)
-    int group;        // pairs of heads that share keys
-    int tiles;        // row blocks of a pair
-    int span;         // pairs of all batches that are worked on together
-    int pieces;
-};
-
-// A piece of work, kept in shared memory.  Key tile `it` is a sink tile (it <
-// sink_tiles), whose keys all rows see, or window tile it - sink_tiles; those
-// that all rows see entirely form one run [all0, all1).
-struct Item {
-    int b, h, hk, i0, rows, p0, kl;
-    int all0, all1, sink_keys, sink_tiles, lo, hi;
-    int n;      // key tiles; 0: no rows
-    int valid;  // 0: no work is left
-
-    __device__ __forceinline__ int key0(int it) const {
-        return it < sink_tiles ? it * BN : lo + (it - sink_tiles) * BN;
-    }
-    __device__ __forceinline__ int limit(int it) const { return it < sink_tiles ? sink_keys : hi; }
-    // columns that the tile needs, a multiple of 32
-    __device__ __forceinline__ int width(int it) const {
-        const int w = limit(it) - key0(it);
-        return w >= BN ? BN : (w < 32 ? 32 : (w + 31) & ~31);
-    }
-};
-static_assert(sizeof(Item) <= 128 && sizeof(Barriers) <= 384, "shared memory layout");
-
-__device__ __forceinline__ void make_item(const TcArgs &g, int block, Item &x, bool *bad) {
-    const DiffArgs &a = g.a;
-    // the last rows see the most keys: of the pairs whose keys and values the L2
-    // cache holds together, all longest tiles start first
-    const unsigned size = g.span * g.tiles, span = (unsigned)block / size, in = block - span * size;
-    const unsigned wide = min(g.span, a.B * a.H - (int)span * g.span), deep = in / wide;
-    const int tile = g.tiles - 1 - (int)deep, bh = span * g.span + in - deep * wide;
-    x.b = (unsigned)bh / (unsigned)a.H;
-    x.h = bh - x.b * a.H;
-    x.hk = (unsigned)x.h / (unsigned)g.group;
-    const int ql = clamp_len(a.q_len, x.b, a.Tq, bad), kl = clamp_len(a.k_len, x.b, a.Tk, bad);
-    x.kl = kl;
-    x.i0 = tile * BM;
-    x.rows = max(0, min(BM, ql - x.i0));
-    x.p0 = kl - ql + x.i0;
-    const SeenKeys f = seen_keys(x.p0, kl, a.window, a.sinks),
-                   e = seen_keys(x.p0 + x.rows - 1, kl, a.window, a.sinks);
-    x.lo = f.lo, x.hi = e.hi;
-    x.sink_keys = min(e.s1, f.lo);
-    x.sink_tiles = (x.sink_keys + BN - 1) / BN;
-    x.n = x.sink_tiles + (x.hi > x.lo ? (x.hi - x.lo + BN - 1) / BN : 0);
-    // no key for any row: one tile with everything masked gives the zeros
-    x.n = x.rows > 0 ? max(x.n, 1) : 0;
-    // positions and keys lie within +-2^30, so differences of two fit an int
-    const int far = x.p0 + BM - min(a.window, 1 << 30) - x.lo;  // first key of the last row
-    x.all0 = x.sink_tiles + (far > 0 ? (far + BN - 1) / BN : 0);
-    const int end = min(x.hi, x.p0 + 1) - x.lo;
-    x.all1 = x.sink_tiles + (end > 0 ? end / BN : 0);
-}
-
-// One row by a warp, put right; this CTA and warpgroup write channels c0 ..
-// c0 + n - 1 of the pair's 2 D.
-template <int D>
-__device__ __forceinline__ void mend_row(const TcArgs &g, const Item &x, int row, int c0, int n, bool fin0, bool fin1) {
-    using E = __nv_bfloat16;
-    const DiffArgs &a = g.a;
-    const int lane = threadIdx.x & 31;
-    const E *q = static_cast<const E *>(a.q) + x.b * a.qs.b + 2 * x.h * a.qs.h + (long long)(x.i0 + row) * a.qs.t;
-    const E *k = static_cast<const E *>(a.k) + x.b * a.ks.b + 2 * x.hk * a.ks.h;
-    const E *v = static_cast<const E *>(a.v) + x.b * a.vs.b + 2 * x.hk * a.vs.h;
-    E *o = static_cast<E *>(a.o) + x.b * a.os.b + 2 * x.h * a.os.h + (long long)(x.i0 + row) * a.os.t;
-    float y[2][D / 32];
-    mend_diff<E, D>(
-        q, q + a.qs.h,
-        [&](int map, int half, int j, const E *&kj, const E *&vj) {
-            kj = k + map * a.ks.h + j * a.ks.t, vj = v + half * a.vs.h + j * a.vs.t;
-            return true;
-        },
-        a.lambda[x.h], a.norm, a.weight, a.eps, seen_keys(x.p0 + row, x.kl, a.window, a.sinks),
-        score_factor(a.scale), fin0, fin1, y);
-#pragma unroll
-    for (int half = 0; half < 2; ++half)
-#pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            const int ch = half * D + lane + 32 * i;
-            if (ch >= c0 && ch < c0 + n) o[half * a.os.h + lane + 32 * i] = from_f<E>(y[half][i]);
-        }
-}
 
 template <int D>
 __global__ void __launch_bounds__(NT, 1)
     diff_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                   const __grid_constant__ CUtensorMap tmv, const TcArgs g) {
+                   const __grid_constant__ CUtensorMap tmv, const DiffTcArgs g) {
     using L = Layout<D>;
-    constexpr int NK = L::NK, NV = L::NV, CS = L::CS, DV = L::DV;
+    constexpr int NK = L::NK, NV = L::NV, DV = L::DV;
     extern __shared__ uint8_t raw[];
     uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
     Barriers *bars = reinterpret_cast<Barriers *>(sm + L::BAR);
-    Item *items = reinterpret_cast<Item *>(sm + L::ITEM);
+    DiffItem *items = reinterpret_cast<DiffItem *>(sm + L::ITEM);
     float *wsm = reinterpret_cast<float *>(sm + L::W);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const DiffArgs &a = g.a;
-    const int rank = CS == 1 ? 0 : (int)cluster_rank();  // which part of the channels
-    constexpr uint32_t kSqBytes = 2 * CS * 128 * 4;
 
     if (tid == 0) {
         for (int t = 0; t < 2; ++t) {
@@ -207,7 +110,6 @@ __global__ void __launch_bounds__(NT, 1)
             }
             mbar_init(&bars->ifull[t], 1);
             mbar_init(&bars->iempty[t], 11);  // softmax, product and load warps
-            mbar_init(&bars->sqfull[t], 1);
         }
         for (int s = 0; s < NV; ++s) {
             mbar_init(&bars->vfull[s], 1);
@@ -219,7 +121,6 @@ __global__ void __launch_bounds__(NT, 1)
         mbar_init(&bars->pad, 1);
         bars->pipe = 0;
         fence_mbar_init();
-        for (int t = 0; t < 2; ++t) mbar_expect_tx(&bars->sqfull[t], kSqBytes);
     }
     for (int i = tid; i < 2 * D; i += NT) wsm[i] = a.norm && a.weight ? a.weight[i] : 1.f;
     if (warp == 10 && lane == 0) {
@@ -233,14 +134,12 @@ __global__ void __launch_bounds__(NT, 1)
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    // the other CTA's barriers stand before it is sent anything
-    if (CS > 1) cluster_sync_all();
     const uint32_t tmem = bars->tmem;
     bool ok = true;
 
     // A role's next piece of work (whole warp); null at the end or on a wait that gave up.
     int piece = 0;
-    auto take = [&]() -> const Item * {
+    auto take = [&]() -> const DiffItem * {
         ok = __all_sync(0xffffffffu, ok && wait_bar(&bars->ifull[piece & 1], (piece >> 1) & 1));
         return ok && items[piece & 1].valid ? &items[piece & 1] : nullptr;
     };
@@ -254,16 +153,16 @@ __global__ void __launch_bounds__(NT, 1)
     if (warp == 11) {
         // ==================================================== pieces of work
         if (lane == 0) {
-            const int me = blockIdx.x / CS, all = gridDim.x / CS;
+            const int me = blockIdx.x, all = gridDim.x;
             for (int i = 0; ok; ++i) {
                 if (i >= 2) ok = wait_bar(&bars->iempty[i & 1], ((i >> 1) - 1) & 1);
                 if (!ok) break;
                 const long long block = (long long)i * all + (i & 1 ? all - 1 - me : me);
-                Item &x = items[i & 1];
+                DiffItem &x = items[i & 1];
                 const bool some = block < g.pieces;
                 if (some) {
                     bool bad = false;
-                    make_item(g, (int)block, x, &bad);
+                    make_diff_item(g, (int)block, x, &bad);
                     if (bad) atomicOr(&g_diff_error, kAttnIndex);
                 }
                 x.valid = some;
@@ -274,8 +173,8 @@ __global__ void __launch_bounds__(NT, 1)
     } else if (warp == 10) {
         // ============================================================ loads
         int queries[2] = {0, 0}, keys[2] = {0, 0}, done = 0, pads = 0;  // loaded: per map, value tiles
-        while (const Item *px = take()) {
-            const Item &x = *px;
+        while (const DiffItem *px = take()) {
+            const DiffItem &x = *px;
             const int n = x.n;
             if (n > 0) {
 #pragma unroll 1
@@ -286,9 +185,7 @@ __global__ void __launch_bounds__(NT, 1)
                     ++queries[t];
                     if (lane == 0) {
                         mbar_expect_tx(&bars->qfull[t], L::TILE);
-                        for (int kb = 0; kb < L::KB; ++kb)
-                            tma_load_4d(sm + L::Q + t * L::TILE + kb * 16384, &tmq, kb * 64, x.i0, 2 * x.h + t, x.b,
-                                        &bars->qfull[t]);
+                        tma_load_4d(sm + L::Q + t * L::TILE, &tmq, 0, x.i0, 2 * x.h + t, x.b, &bars->qfull[t]);
                     }
                 }
             }
@@ -303,9 +200,8 @@ __global__ void __launch_bounds__(NT, 1)
                     ++keys[t];
                     if (lane == 0) {
                         mbar_expect_tx(&bars->kfull[t][ks], L::TILE);
-                        for (int kb = 0; kb < L::KB; ++kb)
-                            tma_load_4d(sm + L::K + (t * NK + ks) * L::TILE + kb * 16384, &tmk, kb * 64, k0,
-                                        2 * x.hk + t, x.b, &bars->kfull[t][ks]);
+                        tma_load_4d(sm + L::K + (t * NK + ks) * L::TILE, &tmk, 0, k0, 2 * x.hk + t, x.b,
+                                    &bars->kfull[t][ks]);
                     }
                 }
                 if (ok && done >= NV) ok = __all_sync(0xffffffffu, wait_bar(&bars->vempty[vs], (done / NV - 1) & 1));
@@ -317,8 +213,7 @@ __global__ void __launch_bounds__(NT, 1)
                 if (lane == 0) {
                     mbar_expect_tx(bar, L::VTILE);
                     for (int j = 0; j < 2; ++j)
-                        tma_load_4d(to + j * 16384, &tmv, CS == 1 ? 0 : 64 * j, k0,
-                                    2 * x.hk + (CS == 1 ? j : rank), x.b, bar);
+                        tma_load_4d(to + j * 16384, &tmv, 0, k0, 2 * x.hk + j, x.b, bar);
                 }
                 if (pad) {
                     ok = __all_sync(0xffffffffu, wait_bar(&bars->pad, pads & 1));
@@ -364,8 +259,8 @@ __global__ void __launch_bounds__(NT, 1)
         auto k_wait = [&](int i) {
             return __all_sync(0xffffffffu, wait_bar(&bars->kfull[t][i % NK], (i / NK) & 1));
         };
-        while (const Item *px = take()) {
-            const Item &x = *px;
+        while (const DiffItem *px = take()) {
+            const DiffItem &x = *px;
             const int n = x.n;
             if (n == 0) {
                 give_back();
@@ -423,7 +318,7 @@ __global__ void __launch_bounds__(NT, 1)
                     for (int ks = 4; ks < BN / 16; ++ks)
                         if (ks < steps) values(ks);
 #pragma unroll
-                    for (int ks = 0; ks < 2 * kRest; ++ks)
+                    for (int ks = 0; ks < 2 * kDiffRest; ++ks)
                         if (ks < steps) rests(ks);
                     mma_commit(&bars->vempty[done % NV]);
                     if (it + 1 < n) scores(it + 1, done + 1);
@@ -447,10 +342,10 @@ __global__ void __launch_bounds__(NT, 1)
         const uint32_t ts = tmem + lanes + kS + t * BN, to = tmem + lanes + kO + t * 128;
         constexpr int CH = DV / 2;  // channels of this warpgroup
         const int col = t * CH;     // the first of them in the outputs
-        const int ch0 = rank * DV + col, half = ch0 / D, in_half = ch0 - half * D;
+        const int half = col / D, in_half = col - half * D;
         int seen = 0, used = 0;
-        while (const Item *px = take()) {
-            const Item &x = *px;
+        while (const DiffItem *px = take()) {
+            const DiffItem &x = *px;
             const int n = x.n, all0 = x.all0, all1 = x.all1;
             if (n == 0) {
                 give_back();
@@ -470,7 +365,7 @@ __global__ void __launch_bounds__(NT, 1)
                     const int kc = k0 + 32 * ch;
                     return low_bits(end - kc) & (~low_bits(rlo - kc) | low_bits(a.sinks - kc));
                 };
-                softmax_tile<DV, kRest>(ts, to, g.c, whole, keep, m, l, &bars->pready[t][0], &bars->pready[t][1]);
+                softmax_tile<DV, kDiffRest>(ts, to, g.c, whole, keep, m, l, &bars->pready[t][0], &bars->pready[t][1]);
                 ++seen;
             }
             // the rounding of the exponent's base took the weights' range
@@ -507,33 +402,14 @@ __global__ void __launch_bounds__(NT, 1)
             if (lane == 0) mbar_arrive(&bars->oempty);
             float scale = 1.f;
             if (a.norm) {
-                // the other channels' sums of this row, from both warpgroups
-                float *sq = reinterpret_cast<float *>(sm + L::SQ) + slot * 2 * CS * 128;
-                if (CS == 1) {
-                    sq[t * 128 + row] = squares;
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->sqready);
-                    ok = __all_sync(0xffffffffu, wait_bar(&bars->sqready, used & 1));
-                } else {
-                    // and of both CTAs: every warp sends its rows' sums to each, four a lane
-                    float four[4];
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) four[i] = __shfl_sync(0xffffffffu, squares, (4 * lane + i) & 31);
-                    if (lane < 8) {
-                        const uint32_t dst = smem_u32(sq + (rank * 2 + t) * 128 + (row & ~31) + 4 * lane);
-#pragma unroll
-                        for (int r = 0; r < CS; ++r)
-                            st_async_v4(map_to_rank(dst, r), four[0], four[1], four[2], four[3],
-                                        map_to_rank(smem_u32(&bars->sqfull[slot]), r));
-                    }
-                    ok = __all_sync(0xffffffffu, wait_bar(&bars->sqfull[slot], (used >> 1) & 1));
-                }
+                // the other channels' sum of this row, from the other warpgroup
+                float *sq = reinterpret_cast<float *>(sm + L::SQ) + slot * 256;
+                sq[t * 128 + row] = squares;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->sqready);
+                ok = __all_sync(0xffffffffu, wait_bar(&bars->sqready, used & 1));
                 if (!ok) break;
-                float total = 0.f;
-#pragma unroll
-                for (int i = 0; i < 2 * CS; ++i) total += sq[i * 128 + row];
-                // the slot's next use is two pieces on (its sums may come before it is armed)
-                if (CS > 1 && tid == 0) mbar_expect_tx(&bars->sqfull[slot], kSqBytes);
+                const float total = sq[row] + sq[128 + row];
                 scale = diff_rms(total, D, a.eps);
                 squares = total;
             }
@@ -550,8 +426,8 @@ __global__ void __launch_bounds__(NT, 1)
                 uint32_t w[16];
 #pragma unroll
                 for (int i = 0; i < 16; ++i) {
-                    const float y0 = y[c + 2 * i] * scale * wsm[ch0 + c + 2 * i],
-                                y1 = y[c + 2 * i + 1] * scale * wsm[ch0 + c + 2 * i + 1];
+                    const float y0 = y[c + 2 * i] * scale * wsm[col + c + 2 * i],
+                                y1 = y[c + 2 * i + 1] * scale * wsm[col + c + 2 * i + 1];
                     odd[i & 3] = fmaf(y0, 0.f, fmaf(y1, 0.f, odd[i & 3]));
                     w[i] = pack2(y0, y1);
                 }
@@ -574,7 +450,7 @@ __global__ void __launch_bounds__(NT, 1)
             while (again) {
                 const int src = __ffs(again) - 1;
                 again &= again - 1;
-                mend_row<D>(g, x, w0 + src, ch0, CH, isfinite(__shfl_sync(0xffffffffu, l0, src)),
+                mend_pair_row<D>(g, x, w0 + src, col, CH, isfinite(__shfl_sync(0xffffffffu, l0, src)),
                             isfinite(__shfl_sync(0xffffffffu, l1, src)));
             }
             give_back();
@@ -585,7 +461,6 @@ __global__ void __launch_bounds__(NT, 1)
     tc_fence_before();
     __syncthreads();
     if (warp == 8) tmem_dealloc(tmem, 512);
-    if (CS > 1) cluster_sync_all();  // no CTA leaves while another may send to it
 }
 
 template <int D>
@@ -596,42 +471,21 @@ cudaError_t launch(const DiffArgs &a, int slot, cudaStream_t stream) {
     if (e == cudaSuccess) e = rows_map(&mk, a.k, a.ks, a.B, 2 * a.Hk, a.Tk, D);
     if (e == cudaSuccess) e = rows_map(&mv, a.v, a.vs, a.B, 2 * a.Hk, a.Tk, D);
     if (e != cudaSuccess) return e;
-    TcArgs g;
-    g.a = a;
-    // scale 0: as in window_tc.cu
-    g.c = a.scale == 0.f ? 0x1p-149f : score_factor(a.scale).c;
-    g.negate = a.scale < 0.f ? 1u << 13 : 0u;
-    g.group = a.H / a.Hk;
-    g.tiles = (a.Tq + BM - 1) / BM;
-    // keys and values of the pairs in flight stay within 48 MB of the L2's 129
-    const long long kv = 8ll * D * a.Tk, pairs = (long long)a.B * a.H;
-    const long long span = (48ll << 20) / kv;
-    g.span = (int)(span < 1 ? 1 : (span < pairs ? span : pairs));
-    g.pieces = (int)(pairs * g.tiles);
+    const DiffTcArgs g = diff_tc_args(a, D);
     auto *fn = diff_tc_kernel<D>;
     e = ensure_smem_attr(reinterpret_cast<const void *>(fn), L::ALLOC, slot);
     if (e != cudaSuccess) return e;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(std::min(g.pieces, kClusterRoom[0][L::CS] / L::CS) * L::CS));
-    cfg.blockDim = dim3(NT);
-    cfg.dynamicSmemBytes = L::ALLOC;
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeClusterDimension;
-    at[0].val.clusterDim.x = L::CS;
-    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = L::CS > 1 ? 1 : 0;
-    return cudaLaunchKernelEx(&cfg, fn, mq, mk, mv, g);
+    fn<<<(unsigned)std::min(g.pieces, 152), NT, L::ALLOC, stream>>>(mq, mk, mv, g);
+    return cudaGetLastError();
 }
 
 }  // namespace
 
-// ensure_smem_attr slots 224..226 belong to this file.
+// ensure_smem_attr slots 224 and 225 belong to this file.
 cudaError_t launch_diff_tc(const DiffArgs &a, int d, cudaStream_t stream) {
     if (d == 32) return launch<32>(a, 224, stream);
     if (d == 64) return launch<64>(a, 225, stream);
-    return launch<128>(a, 226, stream);
+    return launch_diff_wide_tc(a, stream);
 }
 
 int attn_errors_diff_tc() {

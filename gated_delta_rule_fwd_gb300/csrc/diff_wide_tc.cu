@@ -1,0 +1,629 @@
+// lr_fwd_diff in bf16 at d = 128, where a pair's value row has 256 channels: both
+// maps' outputs of 128 rows would take all of tensor memory.  A cluster of two
+// CTAs takes 128 query rows of a pair, a CTA a map:
+//
+//     S = Q_m K_m^T   128 keys at a time, two buffers of 128 columns
+//     P = exp2(c S - b)
+//     O += P V        all 256 channels (products of N = 256)
+//
+// Scores are formed once, a buffer ahead: their products, the softmax of the other
+// buffer and the value products run at the same time.  Two softmax threads share a
+// row, 64 keys each; they exchange the tile's maximum, so that both raise the one in
+// use together.  At the end a CTA takes over the rows' 128 channels of its half: the
+// CTAs send each other the other half of their output, scaled, through distributed
+// shared memory in two rounds of 64 channels, and the rows' sums of squares.
+//
+// What the weights' rounding left is multiplied for a quarter of the keys as in
+// diff_tc.cu; a row's non-finite values, padding and the rounding of the exponent's
+// base are dealt with as in window_tc.cu.
+//
+// Roles of the 384 threads: warps 0-3 softmax of a tile's first 64 keys and the first
+// half of the CTA's channels, warps 4-7 of the others, warp 8 issues the value
+// products, warp 9 the scores', warp 10 loads the values, warp 11 works out the pieces
+// and loads their queries and keys.
+// Every wait is bounded (lr_device_status).
+#include <algorithm>
+
+#include "attn_diff_tc.cuh"
+#include "attn_internal.cuh"
+#include "attn_join.cuh"
+#include "attn_tc.cuh"
+#include "tc_common.cuh"
+
+namespace lr {
+namespace {
+
+using namespace tc;
+
+__device__ unsigned g_diff_wide_error = 0;
+
+constexpr int D = 128, DV = 256;
+constexpr int BM = kDiffRows;
+// Threads and their registers: launched with 168 each (64,512 in all); the
+// softmax warpgroups take 216, the third one keeps 72.
+constexpr int NT = 384, kRegsSoftmax = 216, kRegsOther = 72;
+static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsOther <= NT * 168, "register shares");
+
+constexpr int TILE = 2 * 128 * 128;             // bytes of a query or key tile: two 64-column blocks
+constexpr int VHALF = 4 * 64 * 128;             // of 64 value rows: four 64-column blocks
+constexpr int XBYTES = 2 * 128 * 32 * 4;        // a round of the exchange: 32 channels of both warpgroups' rows
+constexpr int SM_Q = 0;
+constexpr int SM_K = TILE;                      // [2]
+constexpr int SM_V = SM_K + 2 * TILE;           // [3] halves of a tile's rows; the third also
+constexpr int SM_X = SM_V + 2 * VHALF;          // takes received outputs, [warpgroup][128][32]
+constexpr int SM_OUT = SM_V + 3 * VHALF;        // 2 KB per softmax warp: rows on their way out
+static_assert(XBYTES <= VHALF, "a round of the exchange in the third slot");
+constexpr int SM_MAX = SM_OUT + 8 * 2048;       // [2][warpgroup][128] maxima of a tile
+constexpr int SM_SUM = SM_MAX + 2 * 2 * 128 * 4;  // [2][warpgroup][128] sums of weights
+constexpr int SM_SQ = SM_SUM + 2 * 2 * 128 * 4;   // [2][2 CTAs x 2][128] sums of squares
+constexpr int SM_W = SM_SQ + 2 * 4 * 128 * 4;     // [256] weights of the norm
+constexpr int SM_BAR = SM_W + DV * 4;
+constexpr int SM_ITEM = SM_BAR + 384;             // two of struct DiffItem
+constexpr int SM_ALLOC = SM_ITEM + 2 * 128 + 1024;
+
+struct Barriers {
+    uint64_t qfull, qempty, kfull[2], kempty[2], vfull[3], vempty[3];
+    uint64_t sfull[2], pready[2], vdone[2], ofull, oempty;
+    uint64_t ifull[2], iempty[2], pair[4], lfull, xfull, xempty, xdone, sqfull[2], pad, fin[2];
+    uint32_t tmem;
+};
+static_assert(sizeof(Barriers) <= 384, "shared memory layout");
+
+constexpr uint32_t kS = 0, kO = 256;  // TMEM columns: two score buffers (P over them), then O
+constexpr uint32_t kSqBytes = 4 * 128 * 4;
+
+// Arrive (count 1) on the mbarrier at cluster address `bar`.
+__device__ __forceinline__ void arrive_remote(uint32_t bar) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+__global__ void __launch_bounds__(NT, 1)
+    diff_wide_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+                     const __grid_constant__ CUtensorMap tmv, const DiffTcArgs g) {
+    extern __shared__ uint8_t raw[];
+    uint8_t *sm = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~(uintptr_t)1023);
+    Barriers *bars = reinterpret_cast<Barriers *>(sm + SM_BAR);
+    DiffItem *items = reinterpret_cast<DiffItem *>(sm + SM_ITEM);
+    float *wsm = reinterpret_cast<float *>(sm + SM_W);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const DiffArgs &a = g.a;
+    const int rank = (int)cluster_rank();  // the CTA's map, and the half of the channels it writes
+
+    if (tid == 0) {
+        for (uint64_t *bar : {&bars->qfull, &bars->qempty, &bars->ofull, &bars->pad, &bars->xfull}) mbar_init(bar, 1);
+        for (int s = 0; s < 2; ++s) {
+            for (uint64_t *bar : {&bars->kfull[s], &bars->kempty[s], &bars->sfull[s], &bars->vdone[s], &bars->ifull[s], &bars->sqfull[s], &bars->fin[s]})
+                mbar_init(bar, 1);
+            mbar_init(&bars->pready[s], 8);
+            mbar_init(&bars->iempty[s], 11);  // softmax, product and value load warps
+        }
+        for (int s = 0; s < 3; ++s) mbar_init(&bars->vfull[s], 1), mbar_init(&bars->vempty[s], 1);
+        for (int s = 0; s < 4; ++s) mbar_init(&bars->pair[s], 2);
+        mbar_init(&bars->oempty, 8);
+        mbar_init(&bars->lfull, 8);
+        mbar_init(&bars->xempty, 8);  // the other CTA's softmax warps
+        mbar_init(&bars->xdone, 8);
+        fence_mbar_init();
+        for (int s = 0; s < 2; ++s) mbar_expect_tx(&bars->sqfull[s], kSqBytes);
+        mbar_expect_tx(&bars->xfull, XBYTES);
+    }
+    for (int i = tid; i < DV; i += NT) wsm[i] = a.norm && a.weight ? a.weight[i] : 1.f;
+    if (warp == 10 && lane == 0) {
+        for (const CUtensorMap *map : {&tmq, &tmk, &tmv})
+            asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+    }
+    if (warp == 8) {
+        tmem_alloc(&bars->tmem, 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    cluster_sync_all();  // the other CTA's barriers stand before it is sent anything
+    const uint32_t tmem = bars->tmem;
+    bool ok = true;
+
+    // A role's next piece of work (whole warp); null at the end or on a wait that gave up.
+    int piece = 0;
+    auto wait = [&](uint64_t *bar, int phase) { return (bool)__all_sync(0xffffffffu, wait_bar(bar, phase & 1)); };
+    auto take = [&]() -> const DiffItem * {
+        ok = __all_sync(0xffffffffu, ok) && wait(&bars->ifull[piece & 1], piece >> 1);
+        return ok && items[piece & 1].valid ? &items[piece & 1] : nullptr;
+    };
+    auto give_back = [&]() {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&bars->iempty[piece & 1]);
+        ++piece;
+    };
+
+    if (warp >= 8) regs_down<kRegsOther>();
+    if (warp == 11) {
+        // ============================= pieces of work, their queries and keys
+        // One lane throughout: a wait that is over and a copy cost a whole warp twice
+        // as much, and what the loads take a tile bounds all else.
+        if (lane == 0) {
+            const int me = blockIdx.x / 2, all = gridDim.x / 2;
+            int queries = 0, keys = 0;  // tiles asked for
+            for (int i = 0; ok; ++i) {
+                if (i >= 2) ok = wait_bar(&bars->iempty[i & 1], ((i >> 1) - 1) & 1);
+                if (!ok) break;
+                const long long block = (long long)i * all + (i & 1 ? all - 1 - me : me);
+                DiffItem &x = items[i & 1];
+                const bool some = block < g.pieces;
+                if (some) {
+                    bool bad = false;
+                    make_diff_item(g, (int)block, x, &bad);
+                    if (bad) atomicOr(&g_diff_wide_error, kAttnIndex);
+                }
+                x.valid = some;
+                mbar_arrive(&bars->ifull[i & 1]);
+                if (!some) break;
+                const int n = x.n, b = x.b, hk = 2 * x.hk + rank;
+                if (n == 0) continue;
+                if (queries > 0) ok = wait_bar(&bars->qempty, (queries - 1) & 1);
+                if (!ok) break;
+                ++queries;
+                mbar_expect_tx(&bars->qfull, TILE);
+                for (int kb = 0; kb < 2; ++kb)
+                    tma_load_4d(sm + SM_Q + kb * 16384, &tmq, kb * 64, x.i0, 2 * x.h + rank, b, &bars->qfull);
+#pragma unroll 1
+                for (int it = 0; it < n && ok; ++it) {
+                    const int s = keys & 1, k0 = x.key0(it);
+                    if (keys >= 2) ok = wait_bar(&bars->kempty[s], ((keys >> 1) - 1) & 1);
+                    if (!ok) break;
+                    ++keys;
+                    mbar_expect_tx(&bars->kfull[s], TILE);
+                    for (int kb = 0; kb < 2; ++kb)
+                        tma_load_4d(sm + SM_K + s * TILE + kb * 16384, &tmk, kb * 64, k0, hk, b, &bars->kfull[s]);
+                }
+            }
+            // never leave with copies into shared memory in flight: the last phases
+            // of every barrier that was armed here
+            if (queries > 0 && !wait_bar(&bars->qfull, (queries - 1) & 1)) ok = false;
+            for (int i = max(0, keys - 2); i < keys; ++i)
+                if (!wait_bar(&bars->kfull[i & 1], (i >> 1) & 1)) ok = false;
+        }
+    } else if (warp == 10) {
+        // ============================================================ values
+        int values[3] = {0, 0, 0}, pads = 0, used = 0;  // halves asked for; pieces
+        while (const DiffItem *px = take()) {
+            const DiffItem &x = *px;
+            const int n = x.n, b = x.b, hk = 2 * x.hk, kl = x.kl;
+            if (n > 0) ++used;
+#pragma unroll 1
+            for (int half = 0; half < 2 * n && ok; ++half) {
+                // a piece's halves take the three slots in turn, from the first on
+                const int slot = half % 3, k0 = x.key0(half >> 1) + 64 * (half & 1);
+                const int uses = slot == 0 ? values[0] : (slot == 1 ? values[1] : values[2]);
+                if (slot == 0) ++values[0];
+                else if (slot == 1) ++values[1];
+                else ++values[2];
+                // values behind the last key: zeros, whatever the padding holds
+                const bool pad = kl < a.Tk && k0 + 64 > kl;
+                uint8_t *to = sm + SM_V + slot * VHALF;
+                if (lane == 0) {
+                    uint64_t *bar = pad ? &bars->pad : &bars->vfull[slot];
+                    if (uses > 0) ok = wait_bar(&bars->vempty[slot], (uses - 1) & 1);
+                    // the last piece's received outputs have been read
+                    if (ok && half == 2 && used > 1) ok = wait_bar(&bars->xdone, used & 1);
+                    if (ok) {
+                        mbar_expect_tx(bar, VHALF);
+                        for (int c = 0; c < 4; ++c)
+                            tma_load_4d(to + c * 8192, &tmv, 64 * (c & 1), k0, hk + (c >> 1), b, bar);
+                    } else {
+                        // not asked for: nothing to wait for at the end
+                        if (slot == 0) --values[0];
+                        else if (slot == 1) --values[1];
+                        else --values[2];
+                    }
+                }
+                if (pad) {
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    ok = wait(&bars->pad, pads);
+                    ++pads;
+                    const int from = max(0, kl - k0) * 8;  // 16-byte units of 128-byte rows
+#pragma unroll 1
+                    for (int u = from + lane; u < 64 * 8; u += 32)
+                        for (int c = 0; c < 4; ++c)
+                            *reinterpret_cast<uint4 *>(to + c * 8192 + u * 16) = make_uint4(0, 0, 0, 0);
+                    fence_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bars->vfull[slot]);
+                }
+            }
+            __syncwarp();
+            give_back();
+        }
+        if (lane == 0) {
+            for (int h = 0; h < 3; ++h)
+                if (values[h] > 0 && !wait_bar(&bars->vfull[h], (values[h] - 1) & 1)) ok = false;
+            if (pads > 0 && !wait_bar(&bars->pad, (pads - 1) & 1)) ok = false;
+        }
+    } else if (warp == 9) {
+        // ===================================================== scores' products
+        const bool lead = elect_one();
+        const uint64_t dq = tile_desc(smem_u32(sm + SM_Q), 128, 0, 0);
+        int done = 0, used = 0;  // tiles and pieces multiplied
+        while (const DiffItem *px = take()) {
+            const DiffItem &x = *px;
+            const int n = x.n;
+            if (n > 0) ok = wait(&bars->qfull, used);
+#pragma unroll 1
+            for (int it = 0; it < n && ok; ++it) {
+                const int u = done & 1;
+                const uint64_t dk = tile_desc(smem_u32(sm + SM_K) + u * TILE, 128, 0, 0);
+                const uint32_t id = idesc_bf16_f32(BM, x.width(it)) | g.negate;
+                ok = wait(&bars->kfull[u], done >> 1);
+                // the buffer's weights have been multiplied
+                if (ok && done >= 2) ok = wait(&bars->vdone[u], (done >> 1) - 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (lead) {
+#pragma unroll
+                    for (int ks = 0; ks < D / 16; ++ks)
+                        mma_bf16(tmem + kS + 128 * u, kdesc_step(dq, 128, ks), kdesc_step(dk, 128, ks), id, ks > 0);
+                    mma_commit(&bars->sfull[u]);
+                    mma_commit(&bars->kempty[u]);
+                    if (it == n - 1) mma_commit(&bars->qempty);
+                }
+                __syncwarp();
+                ++done;
+            }
+            if (n > 0) ++used;
+            give_back();
+        }
+        if (lead) mma_commit(&bars->fin[1]);
+        __syncwarp();
+        if (!wait_bar(&bars->fin[1], 0)) ok = false;
+    } else if (warp == 8) {
+        // ====================================================== value products
+        const bool lead = elect_one();
+        constexpr uint32_t id_o = idesc_bf16_f32_mn(BM, DV, false, true);
+        const uint64_t dv = tile_desc_mn(smem_u32(sm + SM_V), 64, 0);
+        const uint32_t o = tmem + kO;
+        int done = 0, used = 0;  // tiles and pieces multiplied
+        int values[3] = {0, 0, 0};
+        // a slot's next half is there
+        auto values_wait = [&](int slot) {
+            int &uses = slot == 0 ? values[0] : (slot == 1 ? values[1] : values[2]);
+            return wait(&bars->vfull[slot], uses++);
+        };
+        while (const DiffItem *px = take()) {
+            const DiffItem &x = *px;
+            const int n = x.n;
+#pragma unroll 1
+            for (int it = 0; it < n && ok; ++it) {
+                const int u = done & 1, steps = x.width(it) >> 4;
+                const uint32_t p = tmem + kS + 128 * u;
+                const int slot0 = 2 * it % 3, slot1 = (2 * it + 1) % 3;
+                const uint64_t dv0 = dv + (uint64_t)(slot0 * (VHALF >> 4)), dv1 = dv + (uint64_t)(slot1 * (VHALF >> 4));
+                ok = values_wait(slot0);
+                // the last piece's output has left
+                if (ok && it == 0 && used > 0) ok = wait(&bars->oempty, used - 1);
+                if (ok) ok = wait(&bars->pready[u], done >> 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (lead) {
+#pragma unroll
+                    for (int ks = 0; ks < 4; ++ks)
+                        if (ks < steps) mma_bf16_ta(o, p + 8 * ks, mndesc_step(dv0, ks), id_o, ks > 0 || it > 0);
+#pragma unroll
+                    for (int ks = 0; ks < 2 * kDiffRest; ++ks)
+                        if (ks < steps) mma_bf16_ta(o, p + 32 + 8 * ks, mndesc_step(dv0, ks), id_o, 1);
+                    mma_commit(&bars->vempty[slot0]);
+                }
+                __syncwarp();
+                ok = values_wait(slot1);
+                if (!ok) break;
+                tc_fence_after();
+                if (lead) {
+#pragma unroll
+                    for (int ks = 4; ks < 8; ++ks)
+                        if (ks < steps) mma_bf16_ta(o, p + 64 + 8 * (ks - 4), mndesc_step(dv1, ks - 4), id_o, 1);
+                    mma_commit(&bars->vempty[slot1]);
+                    mma_commit(&bars->vdone[u]);
+                    if (it == n - 1) mma_commit(&bars->ofull);
+                }
+                __syncwarp();
+                ++done;
+            }
+            if (n > 0) ++used;
+            give_back();
+        }
+        if (lead) mma_commit(&bars->fin[0]);
+        __syncwarp();
+        if (!wait_bar(&bars->fin[0], 0)) ok = false;
+    } else if (warp < 8) {
+        // ========================== softmax, then the difference and its norm
+        regs_up<kRegsSoftmax>();
+        const int t = warp >> 2, row = tid & 127;
+        const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, base_o = tmem + lanes + kO;
+        const float2 c2 = make_float2(g.c, g.c);
+        float *maxima = reinterpret_cast<float *>(sm + SM_MAX);
+        int seen = 0, used = 0, rounds = 0;
+        while (const DiffItem *px = take()) {
+            const DiffItem &x = *px;
+            const int n = x.n, all0 = x.all0, all1 = x.all1;
+            if (n == 0) {
+                give_back();
+                continue;
+            }
+            const int p = x.p0 + row;
+            const long long plo = (long long)p - a.window + 1;
+            const int rlo = plo < 0 ? 0 : (int)plo;
+            float m = -INFINITY, l = 0.f;
+            for (int it = 0; it < n && ok; ++it) {
+                const int u = seen & 1;
+                const uint32_t ts = tmem + lanes + kS + 128 * u + 64 * t;
+                const bool whole = it >= all0 && it < all1;
+                const int k0 = x.key0(it) + 64 * t, end = min(p + 1, x.limit(it));
+                ok = wait(&bars->sfull[u], seen >> 1);
+                if (!ok) break;
+                tc_fence_after();
+                if (!whole) {
+                    // -inf over the scores that a row does not see, in tensor memory, so
+                    // that one code serves all tiles
+#pragma unroll 1
+                    for (int ch = 0; ch < 2; ++ch) {
+                        const int kc = k0 + 32 * ch;
+                        const uint32_t keep = low_bits(end - kc) & (~low_bits(rlo - kc) | low_bits(a.sinks - kc));
+                        if (__all_sync(0xffffffffu, keep == 0xffffffffu)) continue;
+                        float s[32];
+                        tmem_ld32(ts + 32 * ch, s);
+                        tmem_ld_wait(s);
+#pragma unroll
+                        for (int i = 0; i < 32; ++i)
+                            if (!((keep >> i) & 1u)) s[i] = -INFINITY;
+                        tmem_st32(ts + 32 * ch, s);
+                    }
+                    tmem_st_wait();
+                }
+                float s[2][32];
+                tmem_ld32(ts, s[0]);
+                tmem_ld32(ts + 32, s[1]);
+                tmem_ld_wait(s[0], s[1]);
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int ch = 0; ch < 2; ++ch)
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) mx[(i >> 1) & 3] = max3(mx[(i >> 1) & 3], s[ch][i], s[ch][i + 1]);
+                // the other 64 keys' maximum, from the warp of the same rows
+                const float own = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3]));
+                maxima[(u * 2 + t) * 128 + row] = own;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->pair[warp & 3]);
+                ok = wait(&bars->pair[warp & 3], seen);
+                if (!ok) break;
+                const float mn = fmaxf(own, maxima[(u * 2 + (t ^ 1)) * 128 + row]);
+                const bool grow = mn > m && (m == -INFINITY || (mn - m) * g.c > 8.f);
+                // a row that has seen nothing yet has l = 0 and zeros in O (or O unset)
+                if (__any_sync(0xffffffffu, grow && m != -INFINITY)) {
+                    // the last tile's products are in O; this warpgroup's half of it
+                    ok = wait(&bars->vdone[u ^ 1], (seen - 1) >> 1);
+                    if (!ok) break;
+                    tc_fence_after();
+                    // no fma here: both products as the exponent's base has them
+                    const float f = grow && m != -INFINITY ? ex2(__fsub_rn(__fmul_rn(m, g.c), __fmul_rn(mn, g.c))) : 1.f;
+                    l *= f;
+#pragma unroll 1
+                    for (int ch = 0; ch < DV / 32; ++ch) {
+                        float v[16];
+                        tmem_ld16(base_o + 128 * t + 16 * ch, v);
+                        tmem_ld_wait(v);
+                        uint32_t r[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) r[i] = __float_as_uint(v[i] * f);
+                        tmem_st16(base_o + 128 * t + 16 * ch, r);
+                    }
+                }
+                if (grow) m = mn;
+                const float base = m == -INFINITY ? 0.f : -__fmul_rn(m, g.c);
+                const float2 b2 = make_float2(base, base);
+                float2 sum[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int ch = 0; ch < 2; ++ch) {
+                    uint32_t r[16];
+#pragma unroll
+                    for (int i = 0; i < 16; ++i) {
+                        float2 e = fma2(make_float2(s[ch][2 * i], s[ch][2 * i + 1]), c2, b2);
+                        e.x = ex2(e.x);
+                        e.y = ex2(e.y);
+                        sum[i & 3] = add2(sum[i & 3], e);
+                        r[i] = pack2(e.x, e.y);
+                        if (ch < kDiffRest) s[ch][2 * i] = e.x, s[ch][2 * i + 1] = e.y;
+                    }
+                    tmem_st16(ts + 16 * ch, r);
+                }
+                // what the rounding of the tile's first keys left
+                if (t == 0) {
+#pragma unroll
+                    for (int ch = 0; ch < kDiffRest; ++ch) {
+                        uint32_t r[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) pack2_rest(make_float2(s[ch][2 * i], s[ch][2 * i + 1]), r[i]);
+                        tmem_st16(ts + 32 + 16 * ch, r);
+                    }
+                }
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->pready[u]);
+                const float2 two = add2(add2(sum[0], sum[1]), add2(sum[2], sum[3]));
+                l += two.x + two.y;
+                ++seen;
+            }
+            const int slot = used & 1;
+            float *sums = reinterpret_cast<float *>(sm + SM_SUM) + slot * 256;
+            sums[t * 128 + row] = l;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->lfull);
+            if (ok) ok = wait(&bars->lfull, used);
+            if (ok) ok = wait(&bars->ofull, used);
+            if (!ok) break;
+            tc_fence_after();
+            // no product reads the slot that the other CTA sends to
+            const uint32_t credit = map_to_rank(smem_u32(&bars->xempty), rank ^ 1);
+            if (lane == 0) arrive_remote(credit);
+            l = sums[row] + sums[128 + row];
+            // the rounding of the exponent's base took the weights' range
+            if (m != -INFINITY && !(l >= 0x1p-40f)) l = NAN;
+            // no key, or only scores of -inf: zeros
+            const float f = (l == 0.f ? 0.f : 1.f / l) * (rank ? -a.lambda[x.h] : 1.f);
+            float y[64], squares = 0.f;
+            // 16-byte chunks of a row of received channels at chunk ^ row
+            const uint32_t x_at = smem_u32(sm + SM_X) + (t * 128 + row) * 128;
+#pragma unroll
+            for (int c = 0; c < 64; c += 32) {
+                float v[32];
+                tmem_ld32(base_o + 128 * (rank ^ 1) + 64 * t + c, v);
+                tmem_ld_wait(v);
+                // the other CTA has room, and has read what it was sent last
+                ok = wait(&bars->xempty, rounds);
+                if (!ok) break;
+                const uint32_t to = map_to_rank(x_at, rank ^ 1), bar = map_to_rank(smem_u32(&bars->xfull), rank ^ 1);
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    st_async_v4(to + (uint32_t)((i ^ (row & 7)) * 16), __fmul_rn(v[4 * i], f), __fmul_rn(v[4 * i + 1], f),
+                                __fmul_rn(v[4 * i + 2], f), __fmul_rn(v[4 * i + 3], f), bar);
+                tmem_ld32(base_o + 128 * rank + 64 * t + c, v);
+                tmem_ld_wait(v);
+                ok = wait(&bars->xfull, rounds);
+                if (!ok) break;
+                if (tid == 0) mbar_expect_tx(&bars->xfull, XBYTES);  // the next round's
+                const uint8_t *from = sm + SM_X + (t * 128 + row) * 128;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    const float4 z = *reinterpret_cast<const float4 *>(from + (i ^ (row & 7)) * 16);
+                    // each product rounded, so that equal maps cancel exactly
+                    y[c + 4 * i] = __fadd_rn(__fmul_rn(v[4 * i], f), z.x);
+                    y[c + 4 * i + 1] = __fadd_rn(__fmul_rn(v[4 * i + 1], f), z.y);
+                    y[c + 4 * i + 2] = __fadd_rn(__fmul_rn(v[4 * i + 2], f), z.z);
+                    y[c + 4 * i + 3] = __fadd_rn(__fmul_rn(v[4 * i + 3], f), z.w);
+                }
+#pragma unroll
+                for (int i = 0; i < 32; ++i) squares = fmaf(y[c + i], y[c + i], squares);
+                if (c) fence_async_smem();  // values come there next
+                __syncwarp();
+                if (lane == 0) {
+                    if (c) mbar_arrive(&bars->xdone);
+                    else arrive_remote(credit);
+                }
+                ++rounds;
+            }
+            if (!ok) break;
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->oempty);
+            float scale = 1.f;
+            if (a.norm) {
+                // the row's other channels: every warp sends its rows' sums to both CTAs,
+                // four a lane
+                const float *sq = reinterpret_cast<const float *>(sm + SM_SQ) + slot * 4 * 128;
+                float four[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) four[i] = __shfl_sync(0xffffffffu, squares, (4 * lane + i) & 31);
+                if (lane < 8) {
+                    const uint32_t dst = smem_u32(sq + (rank * 2 + t) * 128 + (row & ~31) + 4 * lane);
+#pragma unroll
+                    for (int r = 0; r < 2; ++r)
+                        st_async_v4(map_to_rank(dst, r), four[0], four[1], four[2], four[3],
+                                    map_to_rank(smem_u32(&bars->sqfull[slot]), r));
+                }
+                ok = wait(&bars->sqfull[slot], used >> 1);
+                if (!ok) break;
+                squares = (sq[row] + sq[128 + row]) + (sq[256 + row] + sq[384 + row]);
+                // the slot's next use is two pieces on (its sums may come before it is armed)
+                if (tid == 0) mbar_expect_tx(&bars->sqfull[slot], kSqBytes);
+                scale = diff_rms(squares, D, a.eps);
+            }
+            ++used;
+            // Rows leave through the warp's shared memory, 32 channels at a time, so
+            // that a store writes whole 64-byte pieces of eight rows.
+            uint8_t *out = sm + SM_OUT + warp * 2048;
+            const int w0 = 32 * (warp & 3), rows = x.rows, r8 = lane >> 2, c8 = lane & 3;
+            __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + x.b * a.os.b + (2 * x.h + rank) * a.os.h +
+                               (long long)(x.i0 + w0 + r8) * a.os.t + 64 * t + 8 * c8;
+            const float *weight = wsm + 128 * rank + 64 * t;
+            float odd[4] = {0.f, 0.f, 0.f, 0.f};  // NaN once a value is not finite
+#pragma unroll
+            for (int c = 0; c < 64; c += 32) {
+                uint32_t w[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                    const float y0 = y[c + 2 * i] * scale * weight[c + 2 * i],
+                                y1 = y[c + 2 * i + 1] * scale * weight[c + 2 * i + 1];
+                    odd[i & 3] = fmaf(y0, 0.f, fmaf(y1, 0.f, odd[i & 3]));
+                    w[i] = pack2(y0, y1);
+                }
+                __syncwarp();  // the last channels have left
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    *reinterpret_cast<uint4 *>(out + lane * 64 + (i ^ ((lane >> 1) & 3)) * 16) =
+                        make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+                __syncwarp();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int rr = 8 * i + r8;
+                    const uint4 z = *reinterpret_cast<const uint4 *>(out + rr * 64 + (c8 ^ ((rr >> 1) & 3)) * 16);
+                    if (w0 + rr < rows) *reinterpret_cast<uint4 *>(o + 8 * i * a.os.t + c) = z;
+                }
+            }
+            unsigned again = __ballot_sync(0xffffffffu, row < rows && !(odd[0] + odd[1] + odd[2] + odd[3] == 0.f &&
+                                                                        (!a.norm || squares < INFINITY)));
+            __syncwarp();
+            while (again) {
+                const int src = __ffs(again) - 1;
+                again &= again - 1;
+                // of the other map's sum nothing is known here
+                const bool fin = isfinite(__shfl_sync(0xffffffffu, l, src));
+                mend_pair_row<D>(g, x, w0 + src, 128 * rank + 64 * t, 64, rank == 0 && fin, rank == 1 && fin);
+            }
+            give_back();
+        }
+    }
+
+    if (!ok) atomicOr(&g_diff_wide_error, kAttnTimeout);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 8) tmem_dealloc(tmem, 512);
+    cluster_sync_all();  // no CTA leaves while another may send to it
+}
+
+}  // namespace
+
+// ensure_smem_attr slot 226 belongs to this file.
+cudaError_t launch_diff_wide_tc(const DiffArgs &a, cudaStream_t stream) {
+    CUtensorMap mq, mk, mv;
+    cudaError_t e = rows_map(&mq, a.q, a.qs, a.B, 2 * a.H, a.Tq, D);
+    if (e == cudaSuccess) e = rows_map(&mk, a.k, a.ks, a.B, 2 * a.Hk, a.Tk, D);
+    if (e == cudaSuccess) e = rows_map(&mv, a.v, a.vs, a.B, 2 * a.Hk, a.Tk, D, 64);
+    if (e != cudaSuccess) return e;
+    const DiffTcArgs g = diff_tc_args(a, D);
+    auto *fn = diff_wide_kernel;
+    e = ensure_smem_attr(reinterpret_cast<const void *>(fn), SM_ALLOC, 226);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(std::min(g.pieces, kClusterRoom[0][2] / 2) * 2));
+    cfg.blockDim = dim3(NT);
+    cfg.dynamicSmemBytes = SM_ALLOC;
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = 2;
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, fn, mq, mk, mv, g);
+}
+
+int attn_errors_diff_wide() {
+    unsigned h = 0, zero = 0;
+    if (cudaMemcpyFromSymbol(&h, g_diff_wide_error, sizeof(h)) != cudaSuccess) return -1;
+    if (h) cudaMemcpyToSymbol(g_diff_wide_error, &zero, sizeof(h));
+    return (int)h;
+}
+
+}  // namespace lr

@@ -400,7 +400,7 @@ lr_status lr_device_status(void) {
     if (e < 0 || eg < 0) return LR_ERR_CUDA;
     unsigned attn = 0;
     for (int a : {attn_errors_rope(), attn_errors_window_f32(),
-                  attn_errors_window_tc(), attn_errors_step(), attn_errors_diff_tc(),
+                  attn_errors_window_tc(), attn_errors_step(), attn_errors_diff_tc(), attn_errors_diff_wide(),
                   attn_errors_step_diff(), attn_errors_prefix_tc(), attn_errors_prefix_f32()}) {
         if (a < 0) return LR_ERR_CUDA;
         attn |= (unsigned)a;
