@@ -80,6 +80,15 @@ __device__ __forceinline__ void tma_load_4d(void *dst, const void *map, int x, i
         "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar))
         : "memory");
 }
+// The same of a 5-D box.
+__device__ __forceinline__ void tma_load_5d(void *dst, const void *map, int x, int y, int z, int w, int v,
+                                            uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_u32(bar))
+        : "memory");
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -239,17 +248,16 @@ inline PFN_cuTensorMapEncodeTiled_v12000 encoder() {
     return fn;
 }
 
-// A strided [B, H, T, d] tensor, boxes of `rows` rows x 64 columns, 128-byte
+// A strided [B, H, T, d] tensor, boxes of 128 rows x 64 columns, 128-byte
 // swizzle, zero fill outside (also the columns of a box wider than d).
-inline cudaError_t rows_map(CUtensorMap *m, const void *base, const lr_strides &s, int B, int H, int T, int d,
-                            int rows = 128) {
+inline cudaError_t rows_map(CUtensorMap *m, const void *base, const lr_strides &s, int B, int H, int T, int d) {
     auto enc = encoder();
     if (!enc) return cudaErrorNotSupported;
     const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)T, (cuuint64_t)H, (cuuint64_t)B};
     // a dimension of size 1 has stride 0 here: any valid one will do
     auto bytes = [d](long long st) { return (cuuint64_t)(st ? st * 2 : d * 2); };
     const cuuint64_t strides[3] = {bytes(s.t), bytes(s.h), bytes(s.b)};
-    const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
+    const cuuint32_t box[4] = {64, 128, 1, 1};
     const cuuint32_t estr[4] = {1, 1, 1, 1};
     const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(base), dims,
                            strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
@@ -258,20 +266,32 @@ inline cudaError_t rows_map(CUtensorMap *m, const void *base, const lr_strides &
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-// A pool [pages, heads, page, d], boxes of `rows` rows of a page x 64 columns,
-// 128-byte swizzle, zero fill of the columns of a box wider than d.
-inline cudaError_t pool_map(CUtensorMap *m, const void *pool, int d, int page, int heads, int pages, int rows) {
+// Rows of 64-column blocks: element (x, row, block, head, batch) of a strided [B, H,
+// T, d] tensor is channel 64 block + x.  A box holds `heads` heads, one behind the
+// other, each with all its blocks (or one) of `rows` rows, 128-byte swizzle, zero fill
+// of what lies outside (also the columns of a block wider than d), so one copy brings
+// a whole tile: a copy costs its issuing thread some 120 cycles whatever its size.
+inline cudaError_t blocks_map(CUtensorMap *m, const void *base, const lr_strides &s, int B, int H, int T, int d,
+                              int rows, int heads, bool one_block = false) {
     auto enc = encoder();
     if (!enc) return cudaErrorNotSupported;
-    const cuuint64_t row = 2ull * d;
-    const cuuint64_t dims[4] = {(cuuint64_t)d, (cuuint64_t)page, (cuuint64_t)heads, (cuuint64_t)pages};
-    const cuuint64_t strides[3] = {row, row * page, row * page * heads};
-    const cuuint32_t box[4] = {64, (cuuint32_t)rows, 1, 1};
-    const cuuint32_t estr[4] = {1, 1, 1, 1};
-    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, const_cast<void *>(pool), dims, strides, box, estr,
+    const int blocks = d > 64 ? 2 : 1;
+    const cuuint64_t dims[5] = {(cuuint64_t)(d / blocks), (cuuint64_t)T, (cuuint64_t)blocks, (cuuint64_t)H, (cuuint64_t)B};
+    // a dimension of size 1 has stride 0 here: any valid one will do
+    auto bytes = [d](long long st) { return (cuuint64_t)(st ? st * 2 : d * 2); };
+    const cuuint64_t strides[4] = {bytes(s.t), 128, bytes(s.h), bytes(s.b)};
+    const cuuint32_t box[5] = {64, (cuuint32_t)rows, (cuuint32_t)(one_block ? 1 : blocks), (cuuint32_t)heads, 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    const CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void *>(base), dims, strides, box, estr,
                            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                            CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+// The same of a pool [pages, H, page, d]: (x, row of the page, block, head, page).
+inline cudaError_t pool_map(CUtensorMap *m, const void *pool, int d, int page, int H, int pages, int rows, int heads,
+                            bool one_block = false) {
+    return blocks_map(m, pool, {(long long)H * page * d, (long long)page * d, d}, pages, H, page, d, rows, heads,
+                      one_block);
 }
 
 }  // namespace tc

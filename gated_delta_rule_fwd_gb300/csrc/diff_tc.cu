@@ -58,7 +58,7 @@ struct Layout {
     static constexpr int VTILE = 2 * 128 * 128;      // of a value tile: a block for each half
     static constexpr int NK = 2, NV = 2;             // key tiles (per map) and value tiles in flight
     static constexpr int Q = 0;
-    static constexpr int K = 2 * TILE;               // [map][slot]
+    static constexpr int K = 2 * TILE;               // [slot][map]
     static constexpr int V = K + 2 * NK * TILE;
     static constexpr int OUT = V + NV * VTILE;       // 2 KB per softmax warp: rows on their way out
     static constexpr int SUM = OUT + 8 * 2048;       // [2][map][128] sums of weights
@@ -71,8 +71,8 @@ struct Layout {
 };
 
 struct Barriers {
-    uint64_t qfull[2], qempty[2], sfull[2], pready[2][2], ofull[2], oempty, fin[2];
-    uint64_t kfull[2][2], kempty[2][2], vfull[2], vempty[2];
+    uint64_t qfull, qempty, sfull[2], pready[2][2], ofull[2], oempty, fin[2];
+    uint64_t kfull[2], kempty[2], vfull[2], vempty[2];
     uint64_t ifull[2], iempty[2], lfull, sqready, pad;
     uint32_t tmem, pipe;  // pipe: 1 while a warp issues products
 };
@@ -97,24 +97,24 @@ __global__ void __launch_bounds__(NT, 1)
 
     if (tid == 0) {
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&bars->qfull[t], 1);
-            mbar_init(&bars->qempty[t], 1);
             mbar_init(&bars->sfull[t], 1);
             mbar_init(&bars->pready[t][0], 4);  // the first 64 columns of P
             mbar_init(&bars->pready[t][1], 4);  // the others
             mbar_init(&bars->ofull[t], 1);
             mbar_init(&bars->fin[t], 1);
-            for (int s = 0; s < NK; ++s) {
-                mbar_init(&bars->kfull[t][s], 1);
-                mbar_init(&bars->kempty[t][s], 1);
-            }
             mbar_init(&bars->ifull[t], 1);
             mbar_init(&bars->iempty[t], 11);  // softmax, product and load warps
         }
+        for (int s = 0; s < NK; ++s) {
+            mbar_init(&bars->kfull[s], 1);
+            mbar_init(&bars->kempty[s], 2);  // both maps
+        }
         for (int s = 0; s < NV; ++s) {
             mbar_init(&bars->vfull[s], 1);
-            mbar_init(&bars->vempty[s], 2);  // both maps
+            mbar_init(&bars->vempty[s], 2);
         }
+        mbar_init(&bars->qfull, 1);
+        mbar_init(&bars->qempty, 2);
         mbar_init(&bars->oempty, 8);
         mbar_init(&bars->lfull, 8);
         mbar_init(&bars->sqready, 8);
@@ -172,39 +172,31 @@ __global__ void __launch_bounds__(NT, 1)
         }
     } else if (warp == 10) {
         // ============================================================ loads
-        int queries[2] = {0, 0}, keys[2] = {0, 0}, done = 0, pads = 0;  // loaded: per map, value tiles
+        int queries = 0, keys = 0, done = 0, pads = 0;  // asked for: pairs of query and key tiles, value tiles
         while (const DiffItem *px = take()) {
             const DiffItem &x = *px;
             const int n = x.n;
             if (n > 0) {
-#pragma unroll 1
-                for (int t = 0; t < 2 && ok; ++t) {
-                    if (queries[t] > 0)
-                        ok = __all_sync(0xffffffffu, wait_bar(&bars->qempty[t], (queries[t] - 1) & 1));
-                    if (!ok) break;
-                    ++queries[t];
+                if (queries > 0) ok = __all_sync(0xffffffffu, wait_bar(&bars->qempty, (queries - 1) & 1));
+                if (ok) {
+                    ++queries;
                     if (lane == 0) {
-                        mbar_expect_tx(&bars->qfull[t], L::TILE);
-                        tma_load_4d(sm + L::Q + t * L::TILE, &tmq, 0, x.i0, 2 * x.h + t, x.b, &bars->qfull[t]);
+                        mbar_expect_tx(&bars->qfull, 2 * L::TILE);
+                        tma_load_5d(sm + L::Q, &tmq, 0, x.i0, 0, 2 * x.h, x.b, &bars->qfull);
                     }
                 }
             }
 #pragma unroll 1
             for (int it = 0; it < n && ok; ++it) {
                 const int k0 = x.key0(it), ks = done % NK, vs = done % NV;
-#pragma unroll 1
-                for (int t = 0; t < 2 && ok; ++t) {
-                    if (done >= NK)
-                        ok = __all_sync(0xffffffffu, wait_bar(&bars->kempty[t][ks], (done / NK - 1) & 1));
-                    if (!ok) break;
-                    ++keys[t];
-                    if (lane == 0) {
-                        mbar_expect_tx(&bars->kfull[t][ks], L::TILE);
-                        tma_load_4d(sm + L::K + (t * NK + ks) * L::TILE, &tmk, 0, k0, 2 * x.hk + t, x.b,
-                                    &bars->kfull[t][ks]);
-                    }
+                if (done >= NK) ok = __all_sync(0xffffffffu, wait_bar(&bars->kempty[ks], (done / NK - 1) & 1));
+                if (!ok) break;
+                ++keys;
+                if (lane == 0) {
+                    mbar_expect_tx(&bars->kfull[ks], 2 * L::TILE);
+                    tma_load_5d(sm + L::K + ks * 2 * L::TILE, &tmk, 0, k0, 0, 2 * x.hk, x.b, &bars->kfull[ks]);
                 }
-                if (ok && done >= NV) ok = __all_sync(0xffffffffu, wait_bar(&bars->vempty[vs], (done / NV - 1) & 1));
+                if (done >= NV) ok = __all_sync(0xffffffffu, wait_bar(&bars->vempty[vs], (done / NV - 1) & 1));
                 if (!ok) break;
                 uint8_t *to = sm + L::V + vs * L::VTILE;
                 // values behind the last key: zeros, whatever the padding holds
@@ -212,8 +204,7 @@ __global__ void __launch_bounds__(NT, 1)
                 uint64_t *bar = pad ? &bars->pad : &bars->vfull[vs];
                 if (lane == 0) {
                     mbar_expect_tx(bar, L::VTILE);
-                    for (int j = 0; j < 2; ++j)
-                        tma_load_4d(to + j * 16384, &tmv, 0, k0, 2 * x.hk + j, x.b, bar);
+                    tma_load_5d(to, &tmv, 0, k0, 0, 2 * x.hk, x.b, bar);
                 }
                 if (pad) {
                     ok = __all_sync(0xffffffffu, wait_bar(&bars->pad, pads & 1));
@@ -234,11 +225,9 @@ __global__ void __launch_bounds__(NT, 1)
         // never leave with copies into shared memory in flight: the last phases
         // of every barrier that this warp armed
         if (lane == 0) {
-            for (int t = 0; t < 2; ++t) {
-                if (queries[t] > 0 && !wait_bar(&bars->qfull[t], (queries[t] - 1) & 1)) ok = false;
-                for (int i = max(0, keys[t] - NK); i < keys[t]; ++i)
-                    if (!wait_bar(&bars->kfull[t][i % NK], (i / NK) & 1)) ok = false;
-            }
+            if (queries > 0 && !wait_bar(&bars->qfull, (queries - 1) & 1)) ok = false;
+            for (int i = max(0, keys - NK); i < keys; ++i)
+                if (!wait_bar(&bars->kfull[i % NK], (i / NK) & 1)) ok = false;
             for (int i = max(0, done - NV); i < done; ++i)
                 if (!wait_bar(&bars->vfull[i % NV], (i / NV) & 1)) ok = false;
             if (pads > 0 && !wait_bar(&bars->pad, (pads - 1) & 1)) ok = false;
@@ -253,11 +242,11 @@ __global__ void __launch_bounds__(NT, 1)
         constexpr int NO = D == 32 ? 2 : 1;
         const uint32_t id_o = idesc_bf16_f32_mn(BM, DV / NO, false, true);
         const uint64_t dq = tile_desc(smem_u32(sm + L::Q) + t * L::TILE, 128, 0, 0);
-        const uint32_t k_s = smem_u32(sm + L::K) + t * NK * L::TILE, v_s = smem_u32(sm + L::V);
+        const uint32_t k_s = smem_u32(sm + L::K) + t * L::TILE, v_s = smem_u32(sm + L::V);
         const bool lead = elect_one();
         int done = 0, used = 0;  // key tiles and pieces multiplied
         auto k_wait = [&](int i) {
-            return __all_sync(0xffffffffu, wait_bar(&bars->kfull[t][i % NK], (i / NK) & 1));
+            return __all_sync(0xffffffffu, wait_bar(&bars->kfull[i % NK], (i / NK) & 1));
         };
         while (const DiffItem *px = take()) {
             const DiffItem &x = *px;
@@ -271,16 +260,16 @@ __global__ void __launch_bounds__(NT, 1)
             auto width = [&](int it) { return it == n - 1 ? w_last : (it == sink_tiles - 1 ? w_sink : BN); };
             // S = Q K(it)^T; i: tiles multiplied before it
             auto scores = [&](int it, int i) {
-                const uint64_t dk = tile_desc(k_s + (i % NK) * L::TILE, 128, 0, 0);
+                const uint64_t dk = tile_desc(k_s + (i % NK) * 2 * L::TILE, 128, 0, 0);
                 const uint32_t id = idesc_bf16_f32(BM, width(it)) | g.negate;
 #pragma unroll
                 for (int ks = 0; ks < D / 16; ++ks)
                     mma_bf16(s_t, kdesc_step(dq, 128, ks), kdesc_step(dk, 128, ks), id, ks > 0);
                 mma_commit(&bars->sfull[t]);
-                mma_commit(&bars->kempty[t][i % NK]);
-                if (it == n - 1) mma_commit(&bars->qempty[t]);
+                mma_commit(&bars->kempty[i % NK]);
+                if (it == n - 1) mma_commit(&bars->qempty);
             };
-            ok = __all_sync(0xffffffffu, wait_bar(&bars->qfull[t], used & 1)) && k_wait(done);
+            ok = __all_sync(0xffffffffu, wait_bar(&bars->qfull, used & 1)) && k_wait(done);
             if (lead && ok) scores(0, done);
             __syncwarp();
 #pragma unroll 1
@@ -467,9 +456,9 @@ template <int D>
 cudaError_t launch(const DiffArgs &a, int slot, cudaStream_t stream) {
     using L = Layout<D>;
     CUtensorMap mq, mk, mv;
-    cudaError_t e = rows_map(&mq, a.q, a.qs, a.B, 2 * a.H, a.Tq, D);
-    if (e == cudaSuccess) e = rows_map(&mk, a.k, a.ks, a.B, 2 * a.Hk, a.Tk, D);
-    if (e == cudaSuccess) e = rows_map(&mv, a.v, a.vs, a.B, 2 * a.Hk, a.Tk, D);
+    cudaError_t e = blocks_map(&mq, a.q, a.qs, a.B, 2 * a.H, a.Tq, D, BM, 2);
+    if (e == cudaSuccess) e = blocks_map(&mk, a.k, a.ks, a.B, 2 * a.Hk, a.Tk, D, BN, 2);
+    if (e == cudaSuccess) e = blocks_map(&mv, a.v, a.vs, a.B, 2 * a.Hk, a.Tk, D, BN, 2);
     if (e != cudaSuccess) return e;
     const DiffTcArgs g = diff_tc_args(a, D);
     auto *fn = diff_tc_kernel<D>;

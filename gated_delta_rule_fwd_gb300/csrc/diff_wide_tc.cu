@@ -164,8 +164,7 @@ __global__ void __launch_bounds__(NT, 1)
                 if (!ok) break;
                 ++queries;
                 mbar_expect_tx(&bars->qfull, TILE);
-                for (int kb = 0; kb < 2; ++kb)
-                    tma_load_4d(sm + SM_Q + kb * 16384, &tmq, kb * 64, x.i0, 2 * x.h + rank, b, &bars->qfull);
+                tma_load_5d(sm + SM_Q, &tmq, 0, x.i0, 0, 2 * x.h + rank, b, &bars->qfull);
 #pragma unroll 1
                 for (int it = 0; it < n && ok; ++it) {
                     const int s = keys & 1, k0 = x.key0(it);
@@ -173,8 +172,7 @@ __global__ void __launch_bounds__(NT, 1)
                     if (!ok) break;
                     ++keys;
                     mbar_expect_tx(&bars->kfull[s], TILE);
-                    for (int kb = 0; kb < 2; ++kb)
-                        tma_load_4d(sm + SM_K + s * TILE + kb * 16384, &tmk, kb * 64, k0, hk, b, &bars->kfull[s]);
+                    tma_load_5d(sm + SM_K + s * TILE, &tmk, 0, k0, 0, hk, b, &bars->kfull[s]);
                 }
             }
             // never leave with copies into shared memory in flight: the last phases
@@ -208,8 +206,7 @@ __global__ void __launch_bounds__(NT, 1)
                     if (ok && half == 2 && used > 1) ok = wait_bar(&bars->xdone, used & 1);
                     if (ok) {
                         mbar_expect_tx(bar, VHALF);
-                        for (int c = 0; c < 4; ++c)
-                            tma_load_4d(to + c * 8192, &tmv, 64 * (c & 1), k0, hk + (c >> 1), b, bar);
+                        tma_load_5d(to, &tmv, 0, k0, 0, hk, b, bar);
                     } else {
                         // not asked for: nothing to wait for at the end
                         if (slot == 0) --values[0];
@@ -597,9 +594,9 @@ __global__ void __launch_bounds__(NT, 1)
 // ensure_smem_attr slot 226 belongs to this file.
 cudaError_t launch_diff_wide_tc(const DiffArgs &a, cudaStream_t stream) {
     CUtensorMap mq, mk, mv;
-    cudaError_t e = rows_map(&mq, a.q, a.qs, a.B, 2 * a.H, a.Tq, D);
-    if (e == cudaSuccess) e = rows_map(&mk, a.k, a.ks, a.B, 2 * a.Hk, a.Tk, D);
-    if (e == cudaSuccess) e = rows_map(&mv, a.v, a.vs, a.B, 2 * a.Hk, a.Tk, D, 64);
+    cudaError_t e = blocks_map(&mq, a.q, a.qs, a.B, 2 * a.H, a.Tq, D, BM, 1);
+    if (e == cudaSuccess) e = blocks_map(&mk, a.k, a.ks, a.B, 2 * a.Hk, a.Tk, D, kDiffKeys, 1);
+    if (e == cudaSuccess) e = blocks_map(&mv, a.v, a.vs, a.B, 2 * a.Hk, a.Tk, D, 64, 2);
     if (e != cudaSuccess) return e;
     const DiffTcArgs g = diff_tc_args(a, D);
     auto *fn = diff_wide_kernel;

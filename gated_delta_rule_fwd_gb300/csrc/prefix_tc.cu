@@ -161,9 +161,10 @@ __global__ void __launch_bounds__(NT, 1)
                 const int key = k0 + lane * box;
                 int page = a.ptable[key >> a.page_log2];
                 if (page < 0 || page >= a.num_pages) page = 0;
-                for (int kb = 0; kb < L::KB; ++kb)
-                    tma_load_4d(to + kb * 16384 + lane * box * 128, seq & 1 ? &tmv : &tmk, kb * 64, key & in_page, hk,
-                                page, bar);
+                // the copies of whole tiles bring both blocks of columns
+                for (int kb = 0; kb < (box == BN ? 1 : L::KB); ++kb)
+                    tma_load_5d(to + kb * 16384 + lane * box * 128, seq & 1 ? &tmv : &tmk, 0, key & in_page, kb, hk, page,
+                                bar);
             }
             __syncwarp();
             if (pad) {
@@ -333,8 +334,8 @@ cudaError_t launch(const StepArgs &a, const PrefixPlan &plan, int slot, cudaStre
     using L = Layout<D>;
     CUtensorMap mk, mv;
     const int page = 1 << a.page_log2, box = page < 128 ? page : 128;
-    cudaError_t e = pool_map(&mk, a.k, D, page, a.Hk, a.num_pages, box);
-    if (e == cudaSuccess) e = pool_map(&mv, a.v, D, page, a.Hk, a.num_pages, box);
+    cudaError_t e = pool_map(&mk, a.k, D, page, a.Hk, a.num_pages, box, 1, box < BN);
+    if (e == cudaSuccess) e = pool_map(&mv, a.v, D, page, a.Hk, a.num_pages, box, 1, box < BN);
     if (e != cudaSuccess) return e;
     TcArgs g;
     g.a = a;

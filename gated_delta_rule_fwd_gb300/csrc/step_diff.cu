@@ -298,21 +298,24 @@ __global__ void __launch_bounds__(kMmaThreads)
 #pragma unroll
         for (int i = 0; i < 4; ++i) acc[j][i] = 0.f;
     if (warp == 4) {
-        // loads: a box of 16 rows x 64 columns a lane
-        const int piece = lane / R::KB, kb = lane - piece * R::KB;
+        // loads: both maps' keys, both halves of the values
         int i = t0;
         for (; i < t1; ++i) {
             const int k = i - t0, slot = k % R::NS, page = pages[k];
             if (k >= R::NS) ok = __all_sync(0xffffffffu, tc::mbar_wait(&empty[slot], (k / R::NS - 1) & 1));
             if (!ok) break;
             if (lane == 0) {
-                if (page >= 0) tc::mbar_expect_tx(&full[slot], R::TILE);
-                else tc::mbar_arrive(&full[slot]);  // nothing is read of it
+                if (page >= 0) {
+                    const int row = tiles.key(i) & ((1 << a.page_log2) - 1);
+                    uint8_t *to = ring + slot * R::TILE;
+                    tc::mbar_expect_tx(&full[slot], R::TILE);
+                    tc::tma_load_5d(to, &tmk, 0, row, 0, 2 * hk, page, &full[slot]);
+                    tc::tma_load_5d(to + 2 * R::PIECE, &tmv, 0, row, 0, 2 * hk, page, &full[slot]);
+                } else {
+                    tc::mbar_arrive(&full[slot]);  // nothing is read of it
+                }
             }
             __syncwarp();
-            if (page >= 0 && lane < 4 * R::KB)
-                tc::tma_load_4d(ring + slot * R::TILE + lane * (kTile * 128), piece < 2 ? &tmk : &tmv, 64 * kb,
-                                tiles.key(i) & ((1 << a.page_log2) - 1), 2 * hk + (piece & 1), page, &full[slot]);
         }
         // never leave with copies into shared memory in flight
         for (int k = max(0, i - t0 - R::NS); k < i - t0; ++k)
@@ -613,8 +616,8 @@ cudaError_t launch(const DiffStep &s, void *ws, lr_dtype dt, cudaStream_t stream
     cudaError_t e;
     if (dt == LR_DT_BF16) {
         CUtensorMap mk, mv;
-        e = tc::pool_map(&mk, a.k, D, 1 << a.page_log2, 2 * a.Hk, a.num_pages, kTile);
-        if (e == cudaSuccess) e = tc::pool_map(&mv, a.v, D, 1 << a.page_log2, 2 * a.Hk, a.num_pages, kTile);
+        e = tc::pool_map(&mk, a.k, D, 1 << a.page_log2, 2 * a.Hk, a.num_pages, kTile, 2);
+        if (e == cudaSuccess) e = tc::pool_map(&mv, a.v, D, 1 << a.page_log2, 2 * a.Hk, a.num_pages, kTile, 2);
         auto *fn = &step_diff_mma_kernel<D>;
         if (e == cudaSuccess)
             e = ensure_smem_attr(reinterpret_cast<const void *>(fn), Ring<D>::BYTES, 233 + D / 64);
