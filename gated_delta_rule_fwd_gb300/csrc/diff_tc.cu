@@ -409,16 +409,16 @@ __global__ void __launch_bounds__(NT, 1)
             const int w0 = 32 * (warp & 3), rows = x.rows, r8 = lane >> 2, c8 = lane & 3;
             __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + x.b * a.os.b + (2 * x.h + half) * a.os.h +
                                (long long)(x.i0 + w0 + r8) * a.os.t + in_half + 8 * c8;
-            float odd[4] = {0.f, 0.f, 0.f, 0.f};  // NaN once a value is not finite
+            const float4 *weight = reinterpret_cast<const float4 *>(wsm + col);
 #pragma unroll
             for (int c = 0; c < CH; c += 32) {
                 uint32_t w[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float y0 = y[c + 2 * i] * scale * wsm[col + c + 2 * i],
-                                y1 = y[c + 2 * i + 1] * scale * wsm[col + c + 2 * i + 1];
-                    odd[i & 3] = fmaf(y0, 0.f, fmaf(y1, 0.f, odd[i & 3]));
-                    w[i] = pack2(y0, y1);
+                for (int i = 0; i < 8; ++i) {
+                    const float4 z = weight[c / 4 + i];
+                    const float *yi = y + c + 4 * i;
+                    w[2 * i] = pack2(yi[0] * scale * z.x, yi[1] * scale * z.y);
+                    w[2 * i + 1] = pack2(yi[2] * scale * z.z, yi[3] * scale * z.w);
                 }
                 __syncwarp();  // the last channels have left
 #pragma unroll
@@ -433,8 +433,9 @@ __global__ void __launch_bounds__(NT, 1)
                     if (w0 + rr < rows) *reinterpret_cast<uint4 *>(o + 8 * i * a.os.t + c) = z;
                 }
             }
-            unsigned again = __ballot_sync(
-                0xffffffffu, row < rows && !(odd[0] + odd[1] + odd[2] + odd[3] == 0.f && (!a.norm || squares < INFINITY)));
+            // a value that is not finite shows in the squares, and so do finite ones past
+            // 1.8e19: these rows are computed again as well
+            unsigned again = __ballot_sync(0xffffffffu, row < rows && !(squares < INFINITY));
             __syncwarp();
             while (again) {
                 const int src = __ffs(again) - 1;

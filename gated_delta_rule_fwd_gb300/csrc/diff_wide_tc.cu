@@ -11,7 +11,8 @@
 // row, 64 keys each; they exchange the tile's maximum, so that both raise the one in
 // use together.  At the end a CTA takes over the rows' 128 channels of its half: the
 // CTAs send each other the other half of their output, scaled, through distributed
-// shared memory in two rounds of 64 channels, and the rows' sums of squares.
+// shared memory (over the value tiles, which are free then), and the rows' sums of
+// squares.
 //
 // What the weights' rounding left is multiplied for a quarter of the keys as in
 // diff_tc.cu; a row's non-finite values, padding and the rounding of the exponent's
@@ -46,13 +47,13 @@ static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsOther <= NT * 168, "register s
 
 constexpr int TILE = 2 * 128 * 128;             // bytes of a query or key tile: two 64-column blocks
 constexpr int VHALF = 4 * 64 * 128;             // of 64 value rows: four 64-column blocks
-constexpr int XBYTES = 2 * 128 * 32 * 4;        // a round of the exchange: 32 channels of both warpgroups' rows
+constexpr int XBYTES = 128 * 128 * 4;           // what a CTA is sent: 128 channels of all rows
 constexpr int SM_Q = 0;
 constexpr int SM_K = TILE;                      // [2]
-constexpr int SM_V = SM_K + 2 * TILE;           // [3] halves of a tile's rows; the third also
-constexpr int SM_X = SM_V + 2 * VHALF;          // takes received outputs, [warpgroup][128][32]
+constexpr int SM_V = SM_K + 2 * TILE;           // [3] halves of a tile's rows; between two pieces
+                                                // received outputs, [channel / 4][128 rows]
 constexpr int SM_OUT = SM_V + 3 * VHALF;        // 2 KB per softmax warp: rows on their way out
-static_assert(XBYTES <= VHALF, "a round of the exchange in the third slot");
+static_assert(XBYTES <= 3 * VHALF, "received outputs over the values");
 constexpr int SM_MAX = SM_OUT + 8 * 2048;       // [2][warpgroup][128] maxima of a tile
 constexpr int SM_SUM = SM_MAX + 2 * 2 * 128 * 4;  // [2][warpgroup][128] sums of weights
 constexpr int SM_SQ = SM_SUM + 2 * 2 * 128 * 4;   // [2][2 CTAs x 2][128] sums of squares
@@ -203,7 +204,7 @@ __global__ void __launch_bounds__(NT, 1)
                     uint64_t *bar = pad ? &bars->pad : &bars->vfull[slot];
                     if (uses > 0) ok = wait_bar(&bars->vempty[slot], (uses - 1) & 1);
                     // the last piece's received outputs have been read
-                    if (ok && half == 2 && used > 1) ok = wait_bar(&bars->xdone, used & 1);
+                    if (ok && half == 0 && used > 1) ok = wait_bar(&bars->xdone, used & 1);
                     if (ok) {
                         mbar_expect_tx(bar, VHALF);
                         tma_load_5d(to, &tmv, 0, k0, 0, hk, b, bar);
@@ -338,7 +339,7 @@ __global__ void __launch_bounds__(NT, 1)
         const uint32_t lanes = (uint32_t)(32 * (warp & 3)) << 16, base_o = tmem + lanes + kO;
         const float2 c2 = make_float2(g.c, g.c);
         float *maxima = reinterpret_cast<float *>(sm + SM_MAX);
-        int seen = 0, used = 0, rounds = 0;
+        int seen = 0, used = 0;
         while (const DiffItem *px = take()) {
             const DiffItem &x = *px;
             const int n = x.n, all0 = x.all0, all1 = x.all1;
@@ -461,59 +462,57 @@ __global__ void __launch_bounds__(NT, 1)
             if (ok) ok = wait(&bars->ofull, used);
             if (!ok) break;
             tc_fence_after();
-            // no product reads the slot that the other CTA sends to
-            const uint32_t credit = map_to_rank(smem_u32(&bars->xempty), rank ^ 1);
-            if (lane == 0) arrive_remote(credit);
+            // no product reads the values that the other CTA writes over
+            if (lane == 0) arrive_remote(map_to_rank(smem_u32(&bars->xempty), rank ^ 1));
             l = sums[row] + sums[128 + row];
             // the rounding of the exponent's base took the weights' range
             if (m != -INFINITY && !(l >= 0x1p-40f)) l = NAN;
             // no key, or only scores of -inf: zeros
             const float f = (l == 0.f ? 0.f : 1.f / l) * (rank ? -a.lambda[x.h] : 1.f);
+            // rows of a warp side by side, so that a store of it writes 512 bytes in a row
+            uint8_t *got = sm + SM_V + (t * 16 * 128 + row) * 16;
+            ok = wait(&bars->xempty, used);
+            if (!ok) break;
+            {
+                const uint32_t to = map_to_rank(smem_u32(got), rank ^ 1), bar = map_to_rank(smem_u32(&bars->xfull), rank ^ 1);
+#pragma unroll 1
+                for (int c = 0; c < 64; c += 32) {
+                    float v[32];
+                    tmem_ld32(base_o + 128 * (rank ^ 1) + 64 * t + c, v);
+                    tmem_ld_wait(v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i)
+                        st_async_v4(to + (uint32_t)((c / 4 + i) * 2048), __fmul_rn(v[4 * i], f), __fmul_rn(v[4 * i + 1], f),
+                                    __fmul_rn(v[4 * i + 2], f), __fmul_rn(v[4 * i + 3], f), bar);
+                }
+            }
             float y[64], squares = 0.f;
-            // 16-byte chunks of a row of received channels at chunk ^ row
-            const uint32_t x_at = smem_u32(sm + SM_X) + (t * 128 + row) * 128;
 #pragma unroll
             for (int c = 0; c < 64; c += 32) {
                 float v[32];
-                tmem_ld32(base_o + 128 * (rank ^ 1) + 64 * t + c, v);
-                tmem_ld_wait(v);
-                // the other CTA has room, and has read what it was sent last
-                ok = wait(&bars->xempty, rounds);
-                if (!ok) break;
-                const uint32_t to = map_to_rank(x_at, rank ^ 1), bar = map_to_rank(smem_u32(&bars->xfull), rank ^ 1);
-#pragma unroll
-                for (int i = 0; i < 8; ++i)
-                    st_async_v4(to + (uint32_t)((i ^ (row & 7)) * 16), __fmul_rn(v[4 * i], f), __fmul_rn(v[4 * i + 1], f),
-                                __fmul_rn(v[4 * i + 2], f), __fmul_rn(v[4 * i + 3], f), bar);
                 tmem_ld32(base_o + 128 * rank + 64 * t + c, v);
                 tmem_ld_wait(v);
-                ok = wait(&bars->xfull, rounds);
-                if (!ok) break;
-                if (tid == 0) mbar_expect_tx(&bars->xfull, XBYTES);  // the next round's
-                const uint8_t *from = sm + SM_X + (t * 128 + row) * 128;
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float4 z = *reinterpret_cast<const float4 *>(from + (i ^ (row & 7)) * 16);
-                    // each product rounded, so that equal maps cancel exactly
-                    y[c + 4 * i] = __fadd_rn(__fmul_rn(v[4 * i], f), z.x);
-                    y[c + 4 * i + 1] = __fadd_rn(__fmul_rn(v[4 * i + 1], f), z.y);
-                    y[c + 4 * i + 2] = __fadd_rn(__fmul_rn(v[4 * i + 2], f), z.z);
-                    y[c + 4 * i + 3] = __fadd_rn(__fmul_rn(v[4 * i + 3], f), z.w);
-                }
-#pragma unroll
-                for (int i = 0; i < 32; ++i) squares = fmaf(y[c + i], y[c + i], squares);
-                if (c) fence_async_smem();  // values come there next
-                __syncwarp();
-                if (lane == 0) {
-                    if (c) mbar_arrive(&bars->xdone);
-                    else arrive_remote(credit);
-                }
-                ++rounds;
+                for (int i = 0; i < 32; ++i) y[c + i] = __fmul_rn(v[i], f);
             }
-            if (!ok) break;
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->oempty);
+            ok = wait(&bars->xfull, used);
+            if (!ok) break;
+            if (tid == 0) mbar_expect_tx(&bars->xfull, XBYTES);  // the next piece's
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                const float4 z = *reinterpret_cast<const float4 *>(got + i * 2048);
+                // each product rounded, so that equal maps cancel exactly
+                y[4 * i] = __fadd_rn(y[4 * i], z.x), y[4 * i + 1] = __fadd_rn(y[4 * i + 1], z.y);
+                y[4 * i + 2] = __fadd_rn(y[4 * i + 2], z.z), y[4 * i + 3] = __fadd_rn(y[4 * i + 3], z.w);
+            }
+            fence_async_smem();  // values come there next
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bars->xdone);
+#pragma unroll
+            for (int i = 0; i < 64; ++i) squares = fmaf(y[i], y[i], squares);
             float scale = 1.f;
             if (a.norm) {
                 // the row's other channels: every warp sends its rows' sums to both CTAs,
@@ -543,17 +542,16 @@ __global__ void __launch_bounds__(NT, 1)
             const int w0 = 32 * (warp & 3), rows = x.rows, r8 = lane >> 2, c8 = lane & 3;
             __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + x.b * a.os.b + (2 * x.h + rank) * a.os.h +
                                (long long)(x.i0 + w0 + r8) * a.os.t + 64 * t + 8 * c8;
-            const float *weight = wsm + 128 * rank + 64 * t;
-            float odd[4] = {0.f, 0.f, 0.f, 0.f};  // NaN once a value is not finite
+            const float4 *weight = reinterpret_cast<const float4 *>(wsm + 128 * rank + 64 * t);
 #pragma unroll
             for (int c = 0; c < 64; c += 32) {
                 uint32_t w[16];
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const float y0 = y[c + 2 * i] * scale * weight[c + 2 * i],
-                                y1 = y[c + 2 * i + 1] * scale * weight[c + 2 * i + 1];
-                    odd[i & 3] = fmaf(y0, 0.f, fmaf(y1, 0.f, odd[i & 3]));
-                    w[i] = pack2(y0, y1);
+                for (int i = 0; i < 8; ++i) {
+                    const float4 z = weight[c / 4 + i];
+                    const float *yi = y + c + 4 * i;
+                    w[2 * i] = pack2(yi[0] * scale * z.x, yi[1] * scale * z.y);
+                    w[2 * i + 1] = pack2(yi[2] * scale * z.z, yi[3] * scale * z.w);
                 }
                 __syncwarp();  // the last channels have left
 #pragma unroll
@@ -568,8 +566,9 @@ __global__ void __launch_bounds__(NT, 1)
                     if (w0 + rr < rows) *reinterpret_cast<uint4 *>(o + 8 * i * a.os.t + c) = z;
                 }
             }
-            unsigned again = __ballot_sync(0xffffffffu, row < rows && !(odd[0] + odd[1] + odd[2] + odd[3] == 0.f &&
-                                                                        (!a.norm || squares < INFINITY)));
+            // a value that is not finite shows in the squares, and so do finite ones past
+            // 1.8e19: these rows are computed again as well
+            unsigned again = __ballot_sync(0xffffffffu, row < rows && !(squares < INFINITY));
             __syncwarp();
             while (again) {
                 const int src = __ffs(again) - 1;
