@@ -11,8 +11,8 @@
 // row, 64 keys each; they exchange the tile's maximum, so that both raise the one in
 // use together.  At the end a CTA takes over the rows' 128 channels of its half: the
 // CTAs send each other the other half of their output, scaled, through distributed
-// shared memory (over the value tiles, which are free then), and the rows' sums of
-// squares.
+// shared memory (over the key tiles, which are free from the last scores on), and the
+// rows' sums of squares.
 //
 // What the weights' rounding left is multiplied for a quarter of the keys as in
 // diff_tc.cu; a row's non-finite values, padding and the rounding of the exponent's
@@ -49,11 +49,11 @@ constexpr int TILE = 2 * 128 * 128;             // bytes of a query or key tile:
 constexpr int VHALF = 4 * 64 * 128;             // of 64 value rows: four 64-column blocks
 constexpr int XBYTES = 128 * 128 * 4;           // what a CTA is sent: 128 channels of all rows
 constexpr int SM_Q = 0;
-constexpr int SM_K = TILE;                      // [2]
-constexpr int SM_V = SM_K + 2 * TILE;           // [3] halves of a tile's rows; between two pieces
-                                                // received outputs, [channel / 4][128 rows]
+constexpr int SM_K = TILE;                      // [2]; between two pieces received outputs,
+                                                // [channel / 4][128 rows]
+constexpr int SM_V = SM_K + 2 * TILE;           // [3] halves of a tile's rows
 constexpr int SM_OUT = SM_V + 3 * VHALF;        // 2 KB per softmax warp: rows on their way out
-static_assert(XBYTES <= 3 * VHALF, "received outputs over the values");
+static_assert(XBYTES <= 2 * TILE, "received outputs over the keys");
 constexpr int SM_MAX = SM_OUT + 8 * 2048;       // [2][warpgroup][128] maxima of a tile
 constexpr int SM_SUM = SM_MAX + 2 * 2 * 128 * 4;  // [2][warpgroup][128] sums of weights
 constexpr int SM_SQ = SM_SUM + 2 * 2 * 128 * 4;   // [2][2 CTAs x 2][128] sums of squares
@@ -170,6 +170,8 @@ __global__ void __launch_bounds__(NT, 1)
                 for (int it = 0; it < n && ok; ++it) {
                     const int s = keys & 1, k0 = x.key0(it);
                     if (keys >= 2) ok = wait_bar(&bars->kempty[s], ((keys >> 1) - 1) & 1);
+                    // the last piece's received outputs have been read
+                    if (ok && it == 0 && queries > 1) ok = wait_bar(&bars->xdone, queries & 1);
                     if (!ok) break;
                     ++keys;
                     mbar_expect_tx(&bars->kfull[s], TILE);
@@ -184,11 +186,10 @@ __global__ void __launch_bounds__(NT, 1)
         }
     } else if (warp == 10) {
         // ============================================================ values
-        int values[3] = {0, 0, 0}, pads = 0, used = 0;  // halves asked for; pieces
+        int values[3] = {0, 0, 0}, pads = 0;  // halves asked for
         while (const DiffItem *px = take()) {
             const DiffItem &x = *px;
             const int n = x.n, b = x.b, hk = 2 * x.hk, kl = x.kl;
-            if (n > 0) ++used;
 #pragma unroll 1
             for (int half = 0; half < 2 * n && ok; ++half) {
                 // a piece's halves take the three slots in turn, from the first on
@@ -203,8 +204,6 @@ __global__ void __launch_bounds__(NT, 1)
                 if (lane == 0) {
                     uint64_t *bar = pad ? &bars->pad : &bars->vfull[slot];
                     if (uses > 0) ok = wait_bar(&bars->vempty[slot], (uses - 1) & 1);
-                    // the last piece's received outputs have been read
-                    if (ok && half == 0 && used > 1) ok = wait_bar(&bars->xdone, used & 1);
                     if (ok) {
                         mbar_expect_tx(bar, VHALF);
                         tma_load_5d(to, &tmv, 0, k0, 0, hk, b, bar);
@@ -359,6 +358,9 @@ __global__ void __launch_bounds__(NT, 1)
                 ok = wait(&bars->sfull[u], seen >> 1);
                 if (!ok) break;
                 tc_fence_after();
+                // the last scores are there: no product reads the keys that the other CTA
+                // writes its outputs over
+                if (it == n - 1 && lane == 0) arrive_remote(map_to_rank(smem_u32(&bars->xempty), rank ^ 1));
                 if (!whole) {
                     // -inf over the scores that a row does not see, in tensor memory, so
                     // that one code serves all tiles
@@ -462,15 +464,13 @@ __global__ void __launch_bounds__(NT, 1)
             if (ok) ok = wait(&bars->ofull, used);
             if (!ok) break;
             tc_fence_after();
-            // no product reads the values that the other CTA writes over
-            if (lane == 0) arrive_remote(map_to_rank(smem_u32(&bars->xempty), rank ^ 1));
             l = sums[row] + sums[128 + row];
             // the rounding of the exponent's base took the weights' range
             if (m != -INFINITY && !(l >= 0x1p-40f)) l = NAN;
             // no key, or only scores of -inf: zeros
             const float f = (l == 0.f ? 0.f : 1.f / l) * (rank ? -a.lambda[x.h] : 1.f);
             // rows of a warp side by side, so that a store of it writes 512 bytes in a row
-            uint8_t *got = sm + SM_V + (t * 16 * 128 + row) * 16;
+            uint8_t *got = sm + SM_K + (t * 16 * 128 + row) * 16;
             ok = wait(&bars->xempty, used);
             if (!ok) break;
             {
@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(NT, 1)
                 y[4 * i] = __fadd_rn(y[4 * i], z.x), y[4 * i + 1] = __fadd_rn(y[4 * i + 1], z.y);
                 y[4 * i + 2] = __fadd_rn(y[4 * i + 2], z.z), y[4 * i + 3] = __fadd_rn(y[4 * i + 3], z.w);
             }
-            fence_async_smem();  // values come there next
+            fence_async_smem();  // keys come there next
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->xdone);
 #pragma unroll
