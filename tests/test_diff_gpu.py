@@ -258,6 +258,24 @@ def test_diff_large_finite_scores(dev, top, dtype):
     within(o[0], np64(want), np.abs(np64(want)) * 2.0 ** -BITS[dtype] + 2.0 ** -22)
 
 
+@types
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("part", [1.0, 0.5])
+def test_diff_values_at_the_end_of_the_type(dev, part, d, dtype):
+    """Means of the type's largest values do not overflow; with the norm their
+    squares do, and the row is divided by infinity."""
+    T = 260
+    q, k, v, _ = inputs(1, 2, 1, T, T, d, dtype, seed=95)
+    v.fill_(torch.finfo(dtype).max * part)
+    lam = torch.tensor([0.5, 0.25], device=dev)
+    o = np64(lr.lr_fwd_diff(*(t.to(dev) for t in (q, k, v)), lam, norm=False))
+    top = float(v.double()[0, 0, 0, 0])
+    for h, x in enumerate((0.5, 0.75)):
+        # the two means are off by the weights' rounding, 2^-8 each in bf16
+        assert (np.abs(o[0, 2 * h:2 * h + 2] / top - x) <= (2.0 ** -7 if dtype == BF16 else 2.0 ** -14)).all()
+    assert (lr.lr_fwd_diff(*(t.to(dev) for t in (q, k, v)), lam) == 0).all()
+
+
 def _tokens_first(t):
     return t.transpose(1, 2).contiguous().transpose(1, 2)
 

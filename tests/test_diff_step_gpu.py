@@ -229,6 +229,24 @@ def test_diff_step_seen_infinities_and_nan(dev, max_len, d, H, Hk, dtype):
 
 
 @types
+@pytest.mark.parametrize("d", [32, 64, 128])
+@pytest.mark.parametrize("max_len", CUTS)
+def test_diff_step_values_at_the_end_of_the_type(dev, max_len, d, dtype):
+    """Means of the type's largest values do not overflow; with the norm their
+    squares do, and the row is divided by infinity."""
+    lens = [64, 37]
+    kc, vc, table = paged(132, lens, 1, 16, d, dtype, dev)
+    vc.fill_(torch.finfo(dtype).max)
+    lam = torch.tensor([0.5, 0.25], device=dev)
+    args = (rnd(133, 2, 4, d, dtype=dtype).to(dev), kc, vc, wider(table, max_len, 16, dev),
+            torch.tensor(lens, dtype=torch.int32, device=dev), lam)
+    o = np64(lr.lr_step_paged_diff(*args, max_len=max_len, norm=False)) / float(torch.finfo(dtype).max)
+    for h, x in enumerate((0.5, 0.75)):
+        assert (np.abs(o[:, 2 * h:2 * h + 2] - x) <= (2.0 ** -7 if dtype == BF16 else 2.0 ** -14)).all()
+    assert (lr.lr_step_paged_diff(*args, max_len=max_len) == 0).all()
+
+
+@types
 def test_diff_step_bad_pages_and_lengths_are_reported(dev, dtype):
     lens, d, page = [40, 40, 40], 64, 16
     kc, vc, table = paged(8, lens, 1, page, d, dtype, dev)
