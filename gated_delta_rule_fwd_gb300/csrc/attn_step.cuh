@@ -54,22 +54,36 @@ __device__ __forceinline__ uint2 load_once8(const void *p) {
     return r;
 }
 
-// Launches a step kernel; cluster: CTAs of a cluster, 1 for none; smem: dynamic bytes.
+// In a kernel that another one follows early: the follower's CTAs may take the SMs
+// that this kernel leaves free.
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// In the follower: the kernel before it has ended and what it wrote is there.  Every
+// CTA waits, also one that reads nothing of it, so that the follower never ends first.
+__device__ __forceinline__ void wait_for_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// Launches a step kernel; cluster: CTAs of a cluster, 1 for none; smem: dynamic bytes;
+// early: it may start before the kernel ahead of it has ended (and waits itself).
 template <typename... A, typename... B>
 inline cudaError_t launch_cut(void (*fn)(A...), unsigned grid, int threads, int cluster, size_t smem,
-                              cudaStream_t stream, const B &...args) {
+                              bool early, cudaStream_t stream, const B &...args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(grid);
     cfg.blockDim = dim3((unsigned)threads);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
-    cudaLaunchAttribute at[1];
+    cudaLaunchAttribute at[2];
+    cfg.attrs = at;
     if (cluster > 1) {
-        at[0].id = cudaLaunchAttributeClusterDimension;
-        at[0].val.clusterDim.x = (unsigned)cluster;
-        at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
-        cfg.attrs = at;
-        cfg.numAttrs = 1;
+        cudaLaunchAttribute &t = at[cfg.numAttrs++];
+        t.id = cudaLaunchAttributeClusterDimension;
+        t.val.clusterDim.x = (unsigned)cluster;
+        t.val.clusterDim.y = t.val.clusterDim.z = 1;
+    }
+    if (early) {
+        cudaLaunchAttribute &t = at[cfg.numAttrs++];
+        t.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+        t.val.programmaticStreamSerializationAllowed = 1;
     }
     return cudaLaunchKernelEx(&cfg, fn, args...);
 }

@@ -10,6 +10,7 @@
 
 #include "attn_f32.cuh"
 #include "attn_internal.cuh"
+#include "attn_step.cuh"
 #include "tc_common.cuh"
 
 namespace lr {
@@ -32,6 +33,7 @@ __global__ void __launch_bounds__(NT) prefix_f32_kernel(StepArgs a, PrefixPlan p
     extern __shared__ __align__(16) uint8_t raw[];
     Smem<D> &sm = *reinterpret_cast<Smem<D> *>(raw);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
+    let_next_start();
     const int G = a.Hq / a.Hk, rows = a.N * G;
     int id = blockIdx.x;
     const int run = id % plan.parts;

@@ -25,6 +25,7 @@
 #include <limits.h>
 
 #include "attn_internal.cuh"
+#include "attn_step.cuh"
 #include "attn_tc.cuh"
 #include "tc_common.cuh"
 
@@ -124,6 +125,7 @@ __global__ void __launch_bounds__(NT, 1)
         tmem_relinquish();
     }
     tc_fence_before();
+    let_next_start();
     __syncthreads();
     // pages of the run, 16 keys at a time
     for (int i = tid; i < n * (BN / 16); i += NT) {

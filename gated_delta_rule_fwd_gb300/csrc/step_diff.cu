@@ -622,11 +622,11 @@ cudaError_t launch(const DiffStep &s, void *ws, lr_dtype dt, cudaStream_t stream
         if (e == cudaSuccess)
             e = ensure_smem_attr(reinterpret_cast<const void *>(fn), Ring<D>::BYTES, 233 + D / 64);
         if (e == cudaSuccess)
-            e = launch_cut(fn, grid, kMmaThreads, cluster, Ring<D>::BYTES, stream, mk, mv, s, parts, f);
+            e = launch_cut(fn, grid, kMmaThreads, cluster, Ring<D>::BYTES, false, stream, mk, mv, s, parts, f);
     } else if (gc == 1) {
-        e = launch_cut(&step_diff_simt_kernel<D, 1>, grid, NT, cluster, 0, stream, s, parts, f);
+        e = launch_cut(&step_diff_simt_kernel<D, 1>, grid, NT, cluster, 0, false, stream, s, parts, f);
     } else {
-        e = launch_cut(&step_diff_simt_kernel<D, 2>, grid, NT, cluster, 0, stream, s, parts, f);
+        e = launch_cut(&step_diff_simt_kernel<D, 2>, grid, NT, cluster, 0, false, stream, s, parts, f);
     }
     if (e != cudaSuccess || p.splits == 1 || p.cluster) return e;
     const unsigned rows = (unsigned)(a.N * a.Hq);

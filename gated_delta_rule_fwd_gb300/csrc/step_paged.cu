@@ -230,13 +230,17 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts, 
     const int h0 = hk * G + gi * GC, heads = min(GC, G - gi * GC);
     if (len < 0 || len > a.max_len) {
         if (len > 0 && tid == 0 && split == 0 && gi == 0 && hk == 0) atomicOr(&g_step_error, kAttnIndex);
+        if (a.pre) wait_for_previous();
         if (a.fill && split == 0) zero_rows<float, D>(a, n, h0, heads);
         return;
     }
     const SeenKeys s = seen_keys(len - 1, len, a.window, a.sinks);
     const int seen = s.s1 + s.hi - s.lo;
     const int c0 = split * parts.chunk;
-    if (c0 >= seen && split > 0 && !parts.cluster) return;  // the join knows how many chunks there are
+    if (c0 >= seen && split > 0 && !parts.cluster) {  // the join knows how many chunks there are
+        if (a.pre) wait_for_previous();
+        return;
+    }
     const int c1 = min(seen, c0 + parts.chunk);
     const int lane = tid % LANES, group = tid / LANES, ch = lane * 8;
 
@@ -254,6 +258,7 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts, 
     const int lanes0 = (tid & 31) / LANES * LANES;
     const unsigned mask = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1) << lanes0;
     bool bad = false;
+    if (a.pre) wait_for_previous();
     if (a.pre && split == 0)
         load_prefix<D>(a, (size_t)n * a.Hq + h0, heads, f.c, so[NT / 32], sml[NT / 32]);
     for (int base = c0 + group; base < c1; base += GROUPS * U) {
@@ -369,6 +374,7 @@ __global__ void __launch_bounds__(NT)
     const int h0 = hk * G + gi * HEADS, heads = min(HEADS, G - gi * HEADS);
     if (len < 0 || len > a.max_len) {
         if (len > 0 && tid == 0 && split == 0 && gi == 0 && hk == 0) atomicOr(&g_step_error, kAttnIndex);
+        if (a.pre) wait_for_previous();
         if (a.fill && split == 0) zero_rows<__nv_bfloat16, D>(a, n, h0, heads);
         return;
     }
@@ -377,7 +383,10 @@ __global__ void __launch_bounds__(NT)
     const int k_first = max(s.lo / kTile, sink_tiles);  // a tile that holds both is a sink tile
     const int tiles = sink_tiles + max(0, (s.hi + kTile - 1) / kTile - k_first);
     const int per = parts.chunk / kTile, t0 = split * per, t1 = min(tiles, t0 + per);
-    if (t0 >= tiles && split > 0 && !parts.cluster) return;  // the join knows how many chunks there are
+    if (t0 >= tiles && split > 0 && !parts.cluster) {  // the join knows how many chunks there are
+        if (a.pre) wait_for_previous();
+        return;
+    }
 
     auto key_of = [&](int i) { return kTile * (i < sink_tiles ? i : i - sink_tiles + k_first); };
     for (int i = tid; i < t1 - t0; i += NT) {
@@ -467,6 +476,7 @@ __global__ void __launch_bounds__(NT)
         load_k(first);
         load_v(first);
     }
+    if (a.pre) wait_for_previous();
     if (a.pre && split == 0) load_prefix<D>(a, (size_t)n * a.Hq + h0, heads, c, so[NT / 32], sml[NT / 32]);
     for (int i = first; i < t1; i += NT / 32) {
         float sc[NH][4];
@@ -622,9 +632,9 @@ cudaError_t launch_f32(const StepArgs &a, const Parts &parts, cudaStream_t strea
     const int gc = heads_of_cta(G, LR_DT_F32);
     const unsigned grid = (unsigned)(a.N * a.Hk * ((G + gc - 1) / gc) * parts.splits);
     const ScoreFactor f = score_factor(a.scale);
-    if (gc == 1) return launch_cut(&step_simt_kernel<D, 1>, grid, NT, parts.cluster ? parts.splits : 1, 0, stream, a, parts, f);
-    if (gc == 2) return launch_cut(&step_simt_kernel<D, 2>, grid, NT, parts.cluster ? parts.splits : 1, 0, stream, a, parts, f);
-    return launch_cut(&step_simt_kernel<D, 4>, grid, NT, parts.cluster ? parts.splits : 1, 0, stream, a, parts, f);
+    if (gc == 1) return launch_cut(&step_simt_kernel<D, 1>, grid, NT, parts.cluster ? parts.splits : 1, 0, a.pre > 0, stream, a, parts, f);
+    if (gc == 2) return launch_cut(&step_simt_kernel<D, 2>, grid, NT, parts.cluster ? parts.splits : 1, 0, a.pre > 0, stream, a, parts, f);
+    return launch_cut(&step_simt_kernel<D, 4>, grid, NT, parts.cluster ? parts.splits : 1, 0, a.pre > 0, stream, a, parts, f);
 }
 
 template <int D>
@@ -632,8 +642,8 @@ cudaError_t launch_bf16(const StepArgs &a, const Parts &parts, cudaStream_t stre
     const int G = a.Hq / a.Hk, heads = heads_of_cta(G, LR_DT_BF16);
     const unsigned grid = (unsigned)(a.N * a.Hk * ((G + heads - 1) / heads) * parts.splits);
     const ScoreFactor f = score_factor(a.scale);
-    if (heads == 8) return launch_cut(&step_mma_kernel<D, 1>, grid, NT, parts.cluster ? parts.splits : 1, 0, stream, a, parts, f);
-    return launch_cut(&step_mma_kernel<D, 2>, grid, NT, parts.cluster ? parts.splits : 1, 0, stream, a, parts, f);
+    if (heads == 8) return launch_cut(&step_mma_kernel<D, 1>, grid, NT, parts.cluster ? parts.splits : 1, 0, a.pre > 0, stream, a, parts, f);
+    return launch_cut(&step_mma_kernel<D, 2>, grid, NT, parts.cluster ? parts.splits : 1, 0, a.pre > 0, stream, a, parts, f);
 }
 
 template <int D>
