@@ -65,7 +65,7 @@ constexpr int SM_ALLOC = SM_ITEM + 2 * 128 + 1024;
 struct Barriers {
     uint64_t qfull, qempty, kfull[2], kempty[2], vfull[3], vempty[3];
     uint64_t sfull[2], pready[2], vdone[2], ofull, oempty;
-    uint64_t ifull[2], iempty[2], pair[4], lfull, xfull, xempty, xdone, sqfull[2], pad, fin[2];
+    uint64_t ifull[2], iempty[2], pair[4], lfull, xfull, xempty, xdone, sqfull[2], pad[3], fin[2];
     uint32_t tmem;
 };
 static_assert(sizeof(Barriers) <= 384, "shared memory layout");
@@ -73,6 +73,23 @@ static_assert(sizeof(Barriers) <= 384, "shared memory layout");
 constexpr uint32_t kS = 0, kO = 256;  // TMEM columns: two score buffers (P over them), then O
 constexpr uint32_t kSqBytes = 4 * 128 * 4;
 
+// An arrival on this mbarrier of both CTAs when the products issued so far are done.
+__device__ __forceinline__ void mma_commit_both(uint64_t *bar) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(bar)),
+        "h"((uint16_t)3)
+        : "memory");
+}
+// tma_load_5d to the same place of both CTAs, counted on this mbarrier of each.
+__device__ __forceinline__ void tma_load_5d_both(void *dst, const void *map, int x, int y, int z, int w, int v,
+                                                 uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster "
+        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_u32(bar)), "h"((uint16_t)3)
+        : "memory");
+}
 // Arrive (count 1) on the mbarrier at cluster address `bar`.
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -91,14 +108,18 @@ __global__ void __launch_bounds__(NT, 1)
     const int rank = (int)cluster_rank();  // the CTA's map, and the half of the channels it writes
 
     if (tid == 0) {
-        for (uint64_t *bar : {&bars->qfull, &bars->qempty, &bars->ofull, &bars->pad, &bars->xfull}) mbar_init(bar, 1);
+        for (uint64_t *bar : {&bars->qfull, &bars->qempty, &bars->ofull, &bars->xfull}) mbar_init(bar, 1);
         for (int s = 0; s < 2; ++s) {
             for (uint64_t *bar : {&bars->kfull[s], &bars->kempty[s], &bars->sfull[s], &bars->vdone[s], &bars->ifull[s], &bars->sqfull[s], &bars->fin[s]})
                 mbar_init(bar, 1);
             mbar_init(&bars->pready[s], 8);
             mbar_init(&bars->iempty[s], 11);  // softmax, product and value load warps
         }
-        for (int s = 0; s < 3; ++s) mbar_init(&bars->vfull[s], 1), mbar_init(&bars->vempty[s], 1);
+        for (int s = 0; s < 3; ++s) {
+            mbar_init(&bars->vfull[s], 1);
+            mbar_init(&bars->pad[s], 1);
+            mbar_init(&bars->vempty[s], 2);  // both CTAs' products
+        }
         for (int s = 0; s < 4; ++s) mbar_init(&bars->pair[s], 2);
         mbar_init(&bars->oempty, 8);
         mbar_init(&bars->lfull, 8);
@@ -186,39 +207,35 @@ __global__ void __launch_bounds__(NT, 1)
         }
     } else if (warp == 10) {
         // ============================================================ values
-        int values[3] = {0, 0, 0}, pads = 0;  // halves asked for
+        // Both CTAs multiply the same values: each loads a head of them for both.  A slot
+        // is asked for again when both have used it, so its barriers' phases agree.
+        uint32_t asked = 0, turn = 0, padded = 0, pad_turn = 0;  // a bit a slot: ever, phase of the last time
         while (const DiffItem *px = take()) {
             const DiffItem &x = *px;
-            const int n = x.n, b = x.b, hk = 2 * x.hk, kl = x.kl;
+            const int n = x.n, b = x.b, hv = 2 * x.hk + rank, kl = x.kl;
 #pragma unroll 1
             for (int half = 0; half < 2 * n && ok; ++half) {
                 // a piece's halves take the three slots in turn, from the first on
                 const int slot = half % 3, k0 = x.key0(half >> 1) + 64 * (half & 1);
-                const int uses = slot == 0 ? values[0] : (slot == 1 ? values[1] : values[2]);
-                if (slot == 0) ++values[0];
-                else if (slot == 1) ++values[1];
-                else ++values[2];
+                const uint32_t bit = 1u << slot;
                 // values behind the last key: zeros, whatever the padding holds
                 const bool pad = kl < a.Tk && k0 + 64 > kl;
                 uint8_t *to = sm + SM_V + slot * VHALF;
                 if (lane == 0) {
-                    uint64_t *bar = pad ? &bars->pad : &bars->vfull[slot];
-                    if (uses > 0) ok = wait_bar(&bars->vempty[slot], (uses - 1) & 1);
+                    uint64_t *bar = pad ? &bars->pad[slot] : &bars->vfull[slot];
+                    if (asked & bit) ok = wait_bar(&bars->vempty[slot], (turn >> slot) & 1);
                     if (ok) {
                         mbar_expect_tx(bar, VHALF);
-                        tma_load_5d(to, &tmv, 0, k0, 0, hk, b, bar);
-                    } else {
-                        // not asked for: nothing to wait for at the end
-                        if (slot == 0) --values[0];
-                        else if (slot == 1) --values[1];
-                        else --values[2];
+                        tma_load_5d_both(to + rank * (VHALF / 2), &tmv, 0, k0, 0, hv, b, bar);
+                        if (asked & bit) turn ^= bit;
+                        asked |= bit;
                     }
                 }
-                if (pad) {
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    ok = wait(&bars->pad, pads);
-                    ++pads;
+                ok = __all_sync(0xffffffffu, ok);
+                if (pad && ok) {
+                    if (padded & bit) pad_turn ^= bit;
+                    padded |= bit;
+                    ok = wait(&bars->pad[slot], pad_turn >> slot);
                     const int from = max(0, kl - k0) * 8;  // 16-byte units of 128-byte rows
 #pragma unroll 1
                     for (int u = from + lane; u < 64 * 8; u += 32)
@@ -232,10 +249,13 @@ __global__ void __launch_bounds__(NT, 1)
             __syncwarp();
             give_back();
         }
+        // both CTAs' last copies and products
         if (lane == 0) {
-            for (int h = 0; h < 3; ++h)
-                if (values[h] > 0 && !wait_bar(&bars->vfull[h], (values[h] - 1) & 1)) ok = false;
-            if (pads > 0 && !wait_bar(&bars->pad, (pads - 1) & 1)) ok = false;
+            for (int s = 0; s < 3; ++s) {
+                if ((padded >> s & 1) && !wait_bar(&bars->pad[s], pad_turn >> s & 1)) ok = false;
+                if ((asked >> s & 1) && !wait_bar(&bars->vfull[s], turn >> s & 1)) ok = false;
+                if ((asked >> s & 1) && !wait_bar(&bars->vempty[s], turn >> s & 1)) ok = false;
+            }
         }
     } else if (warp == 9) {
         // ===================================================== scores' products
@@ -308,7 +328,7 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
                     for (int ks = 0; ks < 2 * kDiffRest; ++ks)
                         if (ks < steps) mma_bf16_ta(o, p + 32 + 8 * ks, mndesc_step(dv0, ks), id_o, 1);
-                    mma_commit(&bars->vempty[slot0]);
+                    mma_commit_both(&bars->vempty[slot0]);
                 }
                 __syncwarp();
                 ok = values_wait(slot1);
@@ -318,7 +338,7 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
                     for (int ks = 4; ks < 8; ++ks)
                         if (ks < steps) mma_bf16_ta(o, p + 64 + 8 * (ks - 4), mndesc_step(dv1, ks - 4), id_o, 1);
-                    mma_commit(&bars->vempty[slot1]);
+                    mma_commit_both(&bars->vempty[slot1]);
                     mma_commit(&bars->vdone[u]);
                     if (it == n - 1) mma_commit(&bars->ofull);
                 }
@@ -595,7 +615,7 @@ cudaError_t launch_diff_wide_tc(const DiffArgs &a, cudaStream_t stream) {
     CUtensorMap mq, mk, mv;
     cudaError_t e = blocks_map(&mq, a.q, a.qs, a.B, 2 * a.H, a.Tq, D, BM, 1);
     if (e == cudaSuccess) e = blocks_map(&mk, a.k, a.ks, a.B, 2 * a.Hk, a.Tk, D, kDiffKeys, 1);
-    if (e == cudaSuccess) e = blocks_map(&mv, a.v, a.vs, a.B, 2 * a.Hk, a.Tk, D, 64, 2);
+    if (e == cudaSuccess) e = blocks_map(&mv, a.v, a.vs, a.B, 2 * a.Hk, a.Tk, D, 64, 1);
     if (e != cudaSuccess) return e;
     const DiffTcArgs g = diff_tc_args(a, D);
     auto *fn = diff_wide_kernel;
