@@ -481,9 +481,7 @@ __global__ void __launch_bounds__(NT, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->lfull);
             if (ok) ok = wait(&bars->lfull, used);
-            if (ok) ok = wait(&bars->ofull, used);
             if (!ok) break;
-            tc_fence_after();
             l = sums[row] + sums[128 + row];
             // the rounding of the exponent's base took the weights' range
             if (m != -INFINITY && !(l >= 0x1p-40f)) l = NAN;
@@ -491,29 +489,26 @@ __global__ void __launch_bounds__(NT, 1)
             const float f = (l == 0.f ? 0.f : 1.f / l) * (rank ? -a.lambda[x.h] : 1.f);
             // rows of a warp side by side, so that a store of it writes 512 bytes in a row
             uint8_t *got = sm + SM_K + (t * 16 * 128 + row) * 16;
+            const uint32_t peer = map_to_rank(smem_u32(got), rank ^ 1),
+                           peer_bar = map_to_rank(smem_u32(&bars->xfull), rank ^ 1);
             ok = wait(&bars->xempty, used);
+            if (ok) ok = wait(&bars->ofull, used);
             if (!ok) break;
-            {
-                const uint32_t to = map_to_rank(smem_u32(got), rank ^ 1), bar = map_to_rank(smem_u32(&bars->xfull), rank ^ 1);
-#pragma unroll 1
-                for (int c = 0; c < 64; c += 32) {
-                    float v[32];
-                    tmem_ld32(base_o + 128 * (rank ^ 1) + 64 * t + c, v);
-                    tmem_ld_wait(v);
-#pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        st_async_v4(to + (uint32_t)((c / 4 + i) * 2048), __fmul_rn(v[4 * i], f), __fmul_rn(v[4 * i + 1], f),
-                                    __fmul_rn(v[4 * i + 2], f), __fmul_rn(v[4 * i + 3], f), bar);
-                }
-            }
-            float y[64], squares = 0.f;
+            tc_fence_after();
+            // what is sent leaves at some 32 bytes a cycle; the CTA's own channels meanwhile
+            float y[64];
 #pragma unroll
             for (int c = 0; c < 64; c += 32) {
-                float v[32];
-                tmem_ld32(base_o + 128 * rank + 64 * t + c, v);
-                tmem_ld_wait(v);
+                float v[32], own[32];
+                tmem_ld32(base_o + 128 * (rank ^ 1) + 64 * t + c, v);
+                tmem_ld32(base_o + 128 * rank + 64 * t + c, own);
+                tmem_ld_wait(v, own);
 #pragma unroll
-                for (int i = 0; i < 32; ++i) y[c + i] = __fmul_rn(v[i], f);
+                for (int i = 0; i < 8; ++i)
+                    st_async_v4(peer + (uint32_t)((c / 4 + i) * 2048), __fmul_rn(v[4 * i], f), __fmul_rn(v[4 * i + 1], f),
+                                __fmul_rn(v[4 * i + 2], f), __fmul_rn(v[4 * i + 3], f), peer_bar);
+#pragma unroll
+                for (int i = 0; i < 32; ++i) y[c + i] = __fmul_rn(own[i], f);
             }
             tc_fence_before();
             __syncwarp();
@@ -531,9 +526,10 @@ __global__ void __launch_bounds__(NT, 1)
             fence_async_smem();  // keys come there next
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->xdone);
+            float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < 64; ++i) squares = fmaf(y[i], y[i], squares);
-            float scale = 1.f;
+            for (int i = 0; i < 64; ++i) part[i & 3] = fmaf(y[i], y[i], part[i & 3]);
+            float squares = (part[0] + part[1]) + (part[2] + part[3]), scale = 1.f;
             if (a.norm) {
                 // the row's other channels: every warp sends its rows' sums to both CTAs,
                 // four a lane
