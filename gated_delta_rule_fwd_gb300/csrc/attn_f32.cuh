@@ -45,12 +45,13 @@ __device__ __forceinline__ void mma_tf32(float (&d)[4], const uint32_t (&a)[4], 
 // One tile: scores of the warp's rows g and g + 8 (g = lane / 4), their running
 // maximum m and sum l (the lane's own columns of it), and the outputs acc.
 //   qr      channels 16 i + 4 t .. + 3 of the two rows (t = lane % 4), signed
-//   ks, vs  the tile's keys and values, F32Rows<D> floats apart
+//   ks, vs  the tile's keys and values, F32Rows floats apart
 //   c       the scores' factor to powers of two
 //   seen(i, r)  whether row g + 8 r sees key i of the tile; not asked where `whole`
-template <int D, typename Seen>
+// DV: channels of a value row.
+template <int D, int DV = D, typename Seen>
 __device__ __forceinline__ void f32_tile(const float4 (&qr)[D / 16][2], const float *ks, const float *vs,
-                                         float (&acc)[D / 8][4], float (&m)[2], float (&l)[2], float c, bool whole,
+                                         float (&acc)[DV / 8][4], float (&m)[2], float (&l)[2], float c, bool whole,
                                          const Seen &seen) {
     constexpr int BK = kF32Keys;
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
@@ -129,7 +130,7 @@ __device__ __forceinline__ void f32_tile(const float4 (&qr)[D / 16][2], const fl
         split(s[j][1], ah[j][2], al[j][2]), split(s[j][3], ah[j][3], al[j][3]);
     }
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) {
+    for (int i = 0; i < DV / 32; ++i) {
         float high[4][4], small[4][4];
 #pragma unroll
         for (int u = 0; u < 4; ++u)
@@ -137,8 +138,8 @@ __device__ __forceinline__ void f32_tile(const float4 (&qr)[D / 16][2], const fl
             for (int e = 0; e < 4; ++e) high[u][e] = small[u][e] = 0.f;
 #pragma unroll
         for (int j = 0; j < BK / 8; ++j) {
-            const float4 x = *reinterpret_cast<const float4 *>(vs + (8 * j + 2 * t) * F32Rows<D>::VS + 32 * i + 4 * g);
-            const float4 y = *reinterpret_cast<const float4 *>(vs + (8 * j + 2 * t + 1) * F32Rows<D>::VS + 32 * i + 4 * g);
+            const float4 x = *reinterpret_cast<const float4 *>(vs + (8 * j + 2 * t) * F32Rows<DV>::VS + 32 * i + 4 * g);
+            const float4 y = *reinterpret_cast<const float4 *>(vs + (8 * j + 2 * t + 1) * F32Rows<DV>::VS + 32 * i + 4 * g);
             const float xv[4] = {x.x, x.y, x.z, x.w}, yv[4] = {y.x, y.y, y.z, y.w};
 #pragma unroll
             for (int u = 0; u < 4; ++u) {

@@ -137,9 +137,9 @@ struct WindowArgs {
     const int *q_len, *k_len;
     int B, Hq, Hk, Tq, Tk, window, sinks;
     float scale;
-    // fp32: the parts of differential attention.  Of the Hq = 4 x pairs outputs, 4 h
-    // + 2 m + j is map m of pair h over half j of its values; Hk counts the pairs of
-    // key heads.
+    // fp32: the parts of differential attention; Hk counts the pairs of key heads.  Of
+    // the Hq = 2 x pairs outputs, 2 h + m is map m of pair h over all 2 d channels of
+    // its values; at d = 128, of the Hq = 4 x pairs, 4 h + 2 m + j is map m over half j.
     int pairs;
 };
 // fp32, Tk >= 1 (window_f32.cu).

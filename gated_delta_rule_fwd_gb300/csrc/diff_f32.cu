@@ -1,8 +1,12 @@
 // lr_fwd_diff in fp32: the two maps of a pair by the fp32 window kernel
-// (window_f32.cu), each over both halves of the value row, into the workspace in
-// one launch, then one pass that takes the difference and its norm (attn_diff.cuh).
-// The scores are formed twice, once for each half (8 units of products where 6
+// (window_f32.cu), into the workspace in one launch, then one pass that takes the
+// difference and its norm (attn_diff.cuh).  At d = 128 the two halves of the value row
+// are apart and the scores are formed twice, once for each (8 units of products where 6
 // would do): a row's 2 d channels of output leave no registers for both.
+//
+// Measured: 2 x 350 rows on 1501 keys, 4 pairs, d = 64, window 300: 31.6 us, of them 2 for
+// the difference (with the scores formed twice 40.2; 2048 rows of 8 pairs, causal: 240
+// and 295).  The bound is that of window_f32.cu, the issue of split products.
 #include "attn_diff.cuh"
 #include "attn_internal.cuh"
 
@@ -11,10 +15,15 @@ namespace {
 
 constexpr int NT = 128;
 
-// maps: [B][H][map][half][Tq][D].  A warp per row of a pair.
+// The maps' outputs in the workspace, row i of a half of map m: [B][H][map][Tq][2 D],
+// or [B][H][map][half][Tq][D] at D = 128.
+__host__ __device__ constexpr int kept_halves(int d) { return d == 128 ? 2 : 1; }
+
+// A warp per row of a pair.
 template <int D>
 __global__ void __launch_bounds__(NT) diff_join_kernel(DiffArgs a, const float *maps) {
     constexpr int PL = D / 32;
+    constexpr bool APART = kept_halves(D) == 2;
     const int lane = threadIdx.x & 31;
     const long long rows = (long long)a.B * a.H * a.Tq;
     const long long r = (long long)blockIdx.x * (NT / 32) + (threadIdx.x >> 5);
@@ -28,7 +37,9 @@ __global__ void __launch_bounds__(NT) diff_join_kernel(DiffArgs a, const float *
     for (int half = 0; half < 2; ++half)
 #pragma unroll
         for (int c = 0; c < PL; ++c) {
-            const float *x = maps + (((long long)bh * 4 + half) * a.Tq + i) * D + lane + 32 * c;
+            const float *x = maps + lane + 32 * c +
+                             (APART ? (((long long)bh * 4 + half) * a.Tq + i) * D
+                                    : ((long long)bh * 2 * a.Tq + i) * 2 * D + half * D);
             y[half][c] = fmaf(-lambda, x[2ll * a.Tq * D], x[0]);
             sum = fmaf(y[half][c], y[half][c], sum);
         }
@@ -54,9 +65,10 @@ size_t diff_f32_workspace_bytes(int B, int H, int Tq, int d) { return (size_t)B 
 
 cudaError_t launch_diff_f32(const DiffArgs &a, int d, void *ws, cudaStream_t stream) {
     float *maps = static_cast<float *>(ws);
-    WindowArgs w{a.q, a.k, a.v, maps, a.qs, a.ks, a.vs, {}, a.q_len, a.k_len, a.B, 4 * a.H, a.Hk, a.Tq, a.Tk,
+    const int heads = 2 * kept_halves(d), width = 4 * d / heads;  // outputs of a pair, their channels
+    WindowArgs w{a.q, a.k, a.v, maps, a.qs, a.ks, a.vs, {}, a.q_len, a.k_len, a.B, heads * a.H, a.Hk, a.Tq, a.Tk,
                  a.window, a.sinks, a.scale, 1};
-    w.os = {4ll * a.H * a.Tq * d, (long long)a.Tq * d, d};
+    w.os = {4ll * a.H * a.Tq * d, (long long)a.Tq * width, width};
     const cudaError_t e = launch_window_f32(w, d, stream);
     if (e != cudaSuccess) return e;
     if (d == 32) join<32>(a, maps, stream);

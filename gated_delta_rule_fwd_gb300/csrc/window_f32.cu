@@ -45,24 +45,25 @@ __device__ unsigned g_window_error = 0;
 
 constexpr int BQ = 64, BK = kF32Keys, GT = 128;  // GT: threads of a group
 
-template <int D, int G>
+template <int D, int G, int DV>
 struct Smem {
-    static constexpr int KS = F32Rows<D>::KS, VS = F32Rows<D>::VS;
+    static constexpr int KS = F32Rows<D>::KS, VS = F32Rows<DV>::VS;
     struct Group {
         float k[2][BK * KS];
         float v[2][BK * VS];
     } group[G];
-    static_assert(G == 1 || sizeof(Group) >= GT * (D / 2 + 4) * sizeof(float), "room for a group's part");
-    static_assert(sizeof(Group) >= BQ * (D + 2) * sizeof(float), "room for a CTA's part");
+    static_assert(G == 1 || sizeof(Group) >= GT * (DV / 2 + 4) * sizeof(float), "room for a group's part");
+    static_assert(sizeof(Group) >= BQ * (DV + 2) * sizeof(float), "room for a CTA's part");
 };
 __device__ __forceinline__ void group_sync(int group) {
     asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "n"(GT) : "memory");
 }
 
-template <int D, int G, bool SPLIT>
+// DV: channels of a value row, 2 D where a pair's two value heads are taken together.
+template <int D, int G, bool SPLIT, int DV>
 __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float c, float sign, int splits) {
     extern __shared__ __align__(16) uint8_t raw[];
-    using S = Smem<D, G>;
+    using S = Smem<D, G, DV>;
     S &sm = *reinterpret_cast<S *>(raw);
     const int group = G == 1 ? 0 : threadIdx.x / GT, tid = threadIdx.x % GT, warp = tid >> 5, lane = tid & 31,
               g = lane >> 2, t = lane & 3;
@@ -75,7 +76,8 @@ __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float 
     const int tile = tiles - 1 - (int)turn;
     const int b = bh / a.Hq, h = bh - b * a.Hq;
     int hq = h, hk = h / (a.Hq / a.Hk), hv = hk;
-    if (a.pairs) hq = h >> 1, hv = 2 * hk + (h & 1), hk = 2 * hk + (hq & 1);
+    if (DV > D) hv = 2 * hk, hk = 2 * hk + (h & 1);
+    else if (a.pairs) hq = h >> 1, hv = 2 * hk + (h & 1), hk = 2 * hk + (hq & 1);
     bool bad = false;
     const int ql = clamp_len(a.q_len, b, a.Tq, &bad), kl = clamp_len(a.k_len, b, a.Tk, &bad);
     if (bad && threadIdx.x == 0) atomicOr(&g_window_error, kAttnIndex);
@@ -107,7 +109,8 @@ __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float 
             const bool on = k0 + r < end;
             const long long row = on ? k0 + r : 0;
             copy16(kd + r * S::KS + ch, k + row * a.ks.t + ch, on);
-            copy16(vd + r * S::VS + ch, v + row * a.vs.t + ch, on);
+#pragma unroll
+            for (int u = 0; u < DV / D; ++u) copy16(vd + r * S::VS + u * D + ch, v + u * a.vs.h + row * a.vs.t + ch, on);
         }
     };
     if (begin + group < n) load(begin + group);
@@ -125,9 +128,9 @@ __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float 
             if (r0 + 8 * r < rows) x = *reinterpret_cast<const float4 *>(q + (r0 + 8 * r) * a.qs.t + 16 * i + 4 * t);
             qr[i][r] = make_float4(x.x * sign, x.y * sign, x.z * sign, x.w * sign);
         }
-    float acc[D / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    float acc[DV / 8][4], m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 #pragma unroll
-    for (int j = 0; j < D / 8; ++j)
+    for (int j = 0; j < DV / 8; ++j)
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[j][e] = 0.f;
 
@@ -142,7 +145,7 @@ __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float 
         if (some) {
             const int half = ((it - begin) / G) & 1;
             const bool whole = k0 + BK <= end && k0 + BK - 1 <= pw && (long long)k0 > (long long)pw + 15 - a.window;
-            f32_tile<D>(qr, buf.k[half], buf.v[half], acc, m, l, c, whole, [&](int i, int r) {
+            f32_tile<D, DV>(qr, buf.k[half], buf.v[half], acc, m, l, c, whole, [&](int i, int r) {
                 const int key = k0 + i, p = pw + g + 8 * r;
                 return key <= p && key < end && (p - key < a.window || key < a.sinks);
             });
@@ -158,7 +161,7 @@ __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float 
 #pragma unroll
             for (int r = 0; r < 2; ++r) part[(2 * r) * GT + tid] = m[r], part[(2 * r + 1) * GT + tid] = l[r];
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j)
+            for (int j = 0; j < DV / 8; ++j)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) part[(4 + 4 * j + e) * GT + tid] = acc[j][e];
         }
@@ -172,17 +175,23 @@ __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float 
             l[r] = l[r] * f0 + l1 * f1;
             m[r] = mn;
 #pragma unroll
-            for (int j = 0; j < D / 8; ++j)
+            for (int j = 0; j < DV / 8; ++j)
 #pragma unroll
                 for (int e = 2 * r; e < 2 * r + 2; ++e)
                     acc[j][e] = acc[j][e] * f0 + part[(4 + 4 * j + e) * GT + tid] * f1;
         }
     }
+    auto mend = [&](int row, bool sum_finite) {
+#pragma unroll 1
+        for (int u = 0; u < DV / D; ++u)
+            mend_row<float, D>(q + row * a.qs.t, k, v + u * a.vs.h, a.ks.t, a.vs.t, o + row * a.os.t + u * D,
+                               seen_keys(p0 + row, kl, a.window, a.sinks), {sign, c}, sum_finite);
+    };
     if constexpr (SPLIT) {
         // the part over the first buffers, which no one reads any more
         __syncthreads();
         uint8_t *part = reinterpret_cast<uint8_t *>(&sm.group[0]);
-        float2 *stats = reinterpret_cast<float2 *>(part + BQ * D * 4);
+        float2 *stats = reinterpret_cast<float2 *>(part + BQ * DV * 4);
         if (group == 0) {
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
@@ -192,10 +201,10 @@ __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float 
                 const int row = r0 + 8 * r;
                 if (t == 0) stats[row] = make_float2(m[r], sum);
 #pragma unroll
-                for (int i = 0; i < D / 32; ++i)
+                for (int i = 0; i < DV / 32; ++i)
 #pragma unroll
                     for (int e = 0; e < 2; ++e)
-                        *reinterpret_cast<float4 *>(part + part_at<D>(row, 8 * i + 2 * t + e)) =
+                        *reinterpret_cast<float4 *>(part + part_at<DV>(row, 8 * i + 2 * t + e)) =
                             make_float4(acc[4 * i][2 * r + e], acc[4 * i + 1][2 * r + e],
                                         acc[4 * i + 2][2 * r + e], acc[4 * i + 3][2 * r + e]);
             }
@@ -203,10 +212,9 @@ __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float 
         tc::cluster_sync_all();
         for (int row = (int)rank * (G * 4) + (int)(threadIdx.x >> 5); row < rows; row += splits * (G * 4)) {
             float sum;
-            if (join_row<float, D>(tc::smem_u32(part), tc::smem_u32(stats), row, splits, c, o + row * a.os.t, sum))
+            if (join_row<float, DV>(tc::smem_u32(part), tc::smem_u32(stats), row, splits, c, o + row * a.os.t, sum))
                 continue;
-            mend_row<float, D>(q + row * a.qs.t, k, v, a.ks.t, a.vs.t, o + row * a.os.t,
-                               seen_keys(p0 + row, kl, a.window, a.sinks), {sign, c}, isfinite(sum));
+            mend(row, isfinite(sum));
         }
         tc::cluster_sync_all();  // no CTA leaves while another reads its part
     } else {
@@ -220,7 +228,7 @@ __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float 
             const int row = r0 + 8 * r;
             float odd = 0.f;  // NaN once a value is not finite
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
+            for (int i = 0; i < DV / 32; ++i) {
                 float y[8];
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
@@ -239,9 +247,7 @@ __global__ void __launch_bounds__(G * GT) window_f32_kernel(WindowArgs a, float 
             for (int x = 0; x < 8; ++x) {
                 if (!((again >> (4 * x)) & 0xfu)) continue;
                 const int rr = 16 * warp + x + 8 * r;
-                mend_row<float, D>(q + rr * a.qs.t, k, v, a.ks.t, a.vs.t, o + rr * a.os.t,
-                                   seen_keys(p0 + rr, kl, a.window, a.sinks), {sign, c},
-                                   isfinite(__shfl_sync(0xffffffffu, sum, 4 * x)));
+                mend(rr, isfinite(__shfl_sync(0xffffffffu, sum, 4 * x)));
             }
         }
     }
@@ -264,7 +270,8 @@ int key_tiles(const WindowArgs &a, int i) {
 // heads, causal: 91 and 57 (by 2; by 3 75); d = 64, 2048 rows of 8 heads: 119
 // and 93 (by 2; by 3 97); 512 rows of 32: 34 (alone; by 2 38); 215 rows of 6,
 // d = 128: 24 and 13 (by 5); 173 rows of 32, window 64, d = 64: 9.5 (alone; by
-// 3 14).
+// 3 14).  With both value heads of a pair a tile takes 2 us (starts of 3 to 8 tiles
+// chose alike but for 173 rows of 16 maps, window 64: 16.6 us alone, 19.5 split).
 int cluster_size(const WindowArgs &a, long long ctas, int per_sm, int start, int join) {
     if (ctas > 8 * kClusterRoom[per_sm - 1][1]) return 1;  // the last round hardly counts
     const int blocks = (a.Tq + BQ - 1) / BQ;
@@ -279,12 +286,12 @@ int cluster_size(const WindowArgs &a, long long ctas, int per_sm, int start, int
     return best;
 }
 
-template <int D>
+template <int D, int DV = D>
 cudaError_t launch(const WindowArgs &a, int slot, cudaStream_t stream) {
-    constexpr int G = D == 128 ? 2 : 1, bytes = sizeof(Smem<D, G>);
+    constexpr int G = D == 128 ? 2 : 1, bytes = sizeof(Smem<D, G, DV>);
     const long long ctas = (long long)a.B * a.Hq * ((a.Tq + BQ - 1) / BQ);
-    const int splits = D == 128 ? cluster_size(a, ctas, 1, 3, 1) : cluster_size(a, ctas, 2, 7, 5);
-    auto *fn = splits > 1 ? window_f32_kernel<D, G, true> : window_f32_kernel<D, G, false>;
+    const int splits = D == 128 ? cluster_size(a, ctas, 1, 3, 1) : cluster_size(a, ctas, 2, DV > D ? 5 : 7, DV > D ? 4 : 5);
+    auto *fn = splits > 1 ? window_f32_kernel<D, G, true, DV> : window_f32_kernel<D, G, false, DV>;
     cudaError_t e = ensure_smem_attr(reinterpret_cast<const void *>(fn), bytes, slot + (splits > 1 ? 12 : 0));
     if (e != cudaSuccess) return e;
     const ScoreFactor f = score_factor(a.scale);
@@ -302,7 +309,8 @@ cudaError_t launch(const WindowArgs &a, int slot, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, fn, a, f.c, f.sign, splits);
 }
 
-constexpr int kSlot = 208;  // ensure_smem_attr slots 208..210 and 220..222
+// ensure_smem_attr slots 208..210, 220..222, 236, 237, 248 and 249
+constexpr int kSlot = 208, kPairSlot = 236;
 
 template <typename E>
 __global__ void window_zero_kernel(WindowArgs a, int units, long long n) {
@@ -325,8 +333,8 @@ __global__ void window_zero_kernel(WindowArgs a, int units, long long n) {
 }  // namespace
 
 cudaError_t launch_window_f32(const WindowArgs &a, int d, cudaStream_t stream) {
-    if (d == 32) return launch<32>(a, kSlot, stream);
-    if (d == 64) return launch<64>(a, kSlot + 1, stream);
+    if (d == 32) return a.pairs ? launch<32, 64>(a, kPairSlot, stream) : launch<32>(a, kSlot, stream);
+    if (d == 64) return a.pairs ? launch<64, 128>(a, kPairSlot + 1, stream) : launch<64>(a, kSlot + 1, stream);
     return launch<128>(a, kSlot + 2, stream);
 }
 
