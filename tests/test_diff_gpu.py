@@ -217,6 +217,47 @@ def test_diff_seen_infinities_and_nan(dev, d, dtype):
 
 
 @types
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_diff_seen_infinities_in_one_tile_of_many_pieces(dev, d, dtype):
+    """As above with keys that no CTAs share out, in every batch and pair: each half of
+    a row is put right by itself, and rows before the infinity do not know of it."""
+    B, H, T, inf = 20, 8, 30, float("inf")
+    q, k, v, lam = inputs(B, H, 4, T, T, d, dtype, seed=65)
+    ref, bound, _ = oa.diff(np64(q), np64(k), np64(v), np64(lam), NW, 0, d ** -0.5, BITS[dtype],
+                            8 if dtype == BF16 else None)
+    v[:, 1, 9, d - 1] = inf  # the second half of the first pair's values, a positive lambda
+    got = np64(lr.lr_fwd_diff(*(x.to(dev) for x in (q, k, v)), lam.to(dev), norm=False))
+    assert np.isnan(got[:, 1:4:2, 9:, d - 1]).all()
+    got[:, 1:4:2, 9:, d - 1] = ref[:, 1:4:2, 9:, d - 1]
+    # rows that are computed again are rounded another way
+    within(torch.from_numpy(got), ref, 2 * bound)
+    normed = np64(lr.lr_fwd_diff(*(x.to(dev) for x in (q, k, v)), lam.to(dev), eps=EPS))
+    assert np.isnan(normed[:, :4, 9:]).all() and np.isfinite(normed[:, :4, :9]).all() and np.isfinite(normed[:, 4:]).all()
+
+
+@types
+@pytest.mark.parametrize("d", [32, 64, 128])
+def test_diff_calls_in_a_row_on_one_workspace(dev, d, dtype):
+    B, H, T, tries = 2, 3, 400, 6
+    sets = [inputs(B, H, 1, T, T, d, dtype, seed=200 + 10 * i) for i in range(tries)]
+    sets = [[t.to(dev) for t in x] for x in sets]
+    size = lr.diff_workspace_size(B, H, 1, T, T, d, dtype)
+    ws = torch.empty(max(size, 1), dtype=torch.uint8, device=dev)
+    want = []
+    for q, k, v, lam in sets:
+        want.append(lr.lr_fwd_diff(q, k, v, lam, window=150, workspace=ws))
+        torch.cuda.synchronize()
+        ws.fill_(255)
+    now, got = [t.clone() for t in sets[0]], []
+    for x in sets:
+        for a, b in zip(now, x):
+            a.copy_(b)
+        got.append(lr.lr_fwd_diff(*now, window=150, workspace=ws))
+        ws.fill_(255)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@types
 @pytest.mark.parametrize("which", ["k", "v"])
 def test_diff_batch_full_of_nan_stays_quick(dev, which, dtype):
     import time

@@ -428,6 +428,47 @@ def test_prefix_two_calls_at_once_and_another_stream(dev, dtype):
 
 
 @types
+@pytest.mark.parametrize("max_len", CUTS)
+def test_prefix_calls_in_a_row_on_one_workspace(dev, max_len, dtype):
+    """The own tokens' kernel may start under the prefix's last CTAs: calls that
+    follow each other without a pause, some with no sequence at all, some with new
+    queries and lengths written just before, give what single calls give."""
+    P, d, page, tries = 1500, 64, 64, 12
+    kc, vc, prefix, table = shared(140, P, [64] * 6, 2, page, d, dtype, dev)
+    table = wider(table, max_len, page, dev)
+    qs = [rnd(141 + i, 6, 4, d, dtype=dtype).to(dev) for i in range(tries)]
+    r = np.random.RandomState(3)
+    lens = [torch.tensor(r.randint(0, 65, 6) if i % 4 else [-1] * 6, dtype=torch.int32, device=dev) for i in range(tries)]
+    ws = torch.empty(lr.step_paged_prefix_workspace_size(6, 4, 2, d, P, max_len, dtype), dtype=torch.uint8, device=dev)
+    call = lambda q, ld: lr.lr_step_paged_prefix(q, kc, vc, prefix, P, table, ld, max_len=max_len, workspace=ws)
+    want = []
+    for q, ld in zip(qs, lens):
+        want.append(call(q, ld))
+        torch.cuda.synchronize()
+        ws.fill_(255)
+    q, ld, got = qs[0].clone(), lens[0].clone(), []
+    for i in range(tries):
+        q.copy_(qs[i])
+        ld.copy_(lens[i])
+        got.append(call(q, ld))
+        if i % 3 == 2:
+            ws.fill_(255)
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@types
+def test_prefix_pages_held_more_than_once(dev, dtype):
+    """A page twice in the prefix, the prefix's pages among the own ones, the same
+    own pages for several sequences."""
+    d, page, P, lens = 128, 16, 70, [40, 40, 17, 33]
+    kc, vc = (rnd(s, 9, 2, page, d, dtype=dtype).to(dev) for s in (150, 151))
+    prefix = torch.tensor([4, 1, 4, 0, 7], dtype=torch.int32, device=dev)
+    table = torch.tensor([[4, 0, 8], [4, 0, 8], [2, 2, 2], [8, 1, 3]], dtype=torch.int32, device=dev)
+    check(dev, rnd(152, 4, 6, d, dtype=dtype), kc, vc, prefix, P, table, lens, NW, 0)
+    check(dev, rnd(153, 4, 6, d, dtype=dtype), kc, vc, prefix, P, table, lens, 60, 20)
+
+
+@types
 def test_prefix_then_sequences_of_their_own(dev, dtype):
     """A prefix written once by the rotation's append, then a few tokens of each
     sequence one by one: every row is that of the whole sequence under
