@@ -7,11 +7,15 @@
 //     O += P V        all 256 channels (products of N = 256)
 //
 // Scores are formed once, a buffer ahead: their products, the softmax of the other
-// buffer and the value products run at the same time.  Two softmax threads share a
+// buffer and the value products run at the same time.  The pipe gets them in the order
+// P V of tile i, S of tile i + 2, P V of tile i + 1: a softmax takes as long as the
+// products of a tile, so scores that wait behind the next value products hold up all
+// (185 -> 200 us).  Both CTAs multiply the same values, so each loads one head of them
+// for both (192 -> 187 us).  Two softmax threads share a
 // row, 64 keys each; they exchange the tile's maximum, so that both raise the one in
 // use together.  At the end a CTA takes over the rows' 128 channels of its half: the
 // CTAs send each other the other half of their output, scaled, through distributed
-// shared memory (over the key tiles, which are free from the last scores on), and the
+// shared memory (over queries and keys, which are free from the last scores on), and the
 // rows' sums of squares.
 //
 // What the weights' rounding left is multiplied for a quarter of the keys as in
@@ -22,7 +26,14 @@
 // half of the CTA's channels, warps 4-7 of the others, warp 8 issues the value
 // products, warp 9 the scores', warp 10 loads the values, warp 11 works out the pieces
 // and loads their queries and keys.
-// Every wait is bounded (lr_device_status).
+// A load warp's work per copy counts: its code is cold each time it wakes (two copies
+// a tile by the whole warp took longer than the tile's products), hence one lane in
+// short loops, few barriers, whole boxes.  Every wait is bounded (lr_device_status).
+//
+// Measured: 2 x 4096 causal tokens of 8 pairs: 172 us, 1200 TFLOP/s of visible products.
+// A tile takes some 2000 cycles where its products need 1792; a piece costs 9000 to
+// 10000 more: its last products, the exchange (64 KB each way at some 32 bytes a
+// cycle), two rounds between the CTAs and the stores.
 #include <algorithm>
 
 #include "attn_diff_tc.cuh"
@@ -45,30 +56,32 @@ constexpr int BM = kDiffRows;
 constexpr int NT = 384, kRegsSoftmax = 216, kRegsOther = 72;
 static_assert(2 * 128 * kRegsSoftmax + 128 * kRegsOther <= NT * 168, "register shares");
 
-constexpr int TILE = 2 * 128 * 128;             // bytes of a query or key tile: two 64-column blocks
+constexpr int BLOCK = 128 * 128;                // bytes of 128 rows' 64 columns
 constexpr int VHALF = 4 * 64 * 128;             // of 64 value rows: four 64-column blocks
+constexpr int NK = 3, NV = 4;                   // blocks of keys, halves of values in flight
 constexpr int XBYTES = 128 * 128 * 4;           // what a CTA is sent: 128 channels of all rows
 constexpr int SM_Q = 0;
-constexpr int SM_K = TILE;                      // [2]; between two pieces received outputs,
-                                                // [channel / 4][128 rows]
-constexpr int SM_V = SM_K + 2 * TILE;           // [3] halves of a tile's rows
-constexpr int SM_OUT = SM_V + 3 * VHALF;        // 2 KB per softmax warp: rows on their way out
-static_assert(XBYTES <= 2 * TILE, "received outputs over the keys");
-constexpr int SM_MAX = SM_OUT + 8 * 2048;       // [2][warpgroup][128] maxima of a tile
+constexpr int SM_K = 2 * BLOCK;                 // [NK] blocks of a tile's columns
+constexpr int SM_V = SM_K + NK * BLOCK;         // [NV] halves of a tile's rows
+constexpr int SM_X = SM_V - XBYTES;             // received outputs between two pieces, [channel / 4][128 rows]
+static_assert(SM_X >= SM_Q, "received outputs over queries and keys");
+constexpr int SM_OUT = SM_V + NV * VHALF;       // 1 KB per softmax warp: rows on their way out
+constexpr int SM_MAX = SM_OUT + 8 * 1024;       // [2][warpgroup][128] maxima of a tile
 constexpr int SM_SUM = SM_MAX + 2 * 2 * 128 * 4;  // [2][warpgroup][128] sums of weights
 constexpr int SM_SQ = SM_SUM + 2 * 2 * 128 * 4;   // [2][2 CTAs x 2][128] sums of squares
 constexpr int SM_W = SM_SQ + 2 * 4 * 128 * 4;     // [256] weights of the norm
 constexpr int SM_BAR = SM_W + DV * 4;
-constexpr int SM_ITEM = SM_BAR + 384;             // two of struct DiffItem
+constexpr int SM_ITEM = SM_BAR + 448;             // two of struct DiffItem
 constexpr int SM_ALLOC = SM_ITEM + 2 * 128 + 1024;
+static_assert(SM_ALLOC <= 227 * 1024, "shared memory of a CTA");
 
 struct Barriers {
-    uint64_t qfull, qempty, kfull[2], kempty[2], vfull[3], vempty[3];
+    uint64_t qfull, qempty, kfull[2], kempty[2], vfull[NV], vempty[NV];
     uint64_t sfull[2], pready[2], vdone[2], ofull, oempty;
-    uint64_t ifull[2], iempty[2], pair[4], lfull, xfull, xempty, xdone, sqfull[2], pad[3], fin[2];
+    uint64_t ifull[2], iempty[2], pair[4], lfull, xfull, xempty, xdone, sqfull[2], pad[NV], fin[2], queued[2];
     uint32_t tmem;
 };
-static_assert(sizeof(Barriers) <= 384, "shared memory layout");
+static_assert(sizeof(Barriers) <= 448, "shared memory layout");
 
 constexpr uint32_t kS = 0, kO = 256;  // TMEM columns: two score buffers (P over them), then O
 constexpr uint32_t kSqBytes = 4 * 128 * 4;
@@ -110,12 +123,14 @@ __global__ void __launch_bounds__(NT, 1)
     if (tid == 0) {
         for (uint64_t *bar : {&bars->qfull, &bars->qempty, &bars->ofull, &bars->xfull}) mbar_init(bar, 1);
         for (int s = 0; s < 2; ++s) {
-            for (uint64_t *bar : {&bars->kfull[s], &bars->kempty[s], &bars->sfull[s], &bars->vdone[s], &bars->ifull[s], &bars->sqfull[s], &bars->fin[s]})
+            for (uint64_t *bar : {&bars->queued[s], &bars->sfull[s], &bars->vdone[s], &bars->ifull[s], &bars->sqfull[s], &bars->fin[s]})
                 mbar_init(bar, 1);
-            mbar_init(&bars->pready[s], 8);
+            mbar_init(&bars->kfull[s], 2);  // a tile's two blocks
+            mbar_init(&bars->kempty[s], 1);
+            mbar_init(&bars->pready[s], 9);  // softmax warps, and the next scores are queued
             mbar_init(&bars->iempty[s], 11);  // softmax, product and value load warps
         }
-        for (int s = 0; s < 3; ++s) {
+        for (int s = 0; s < NV; ++s) {
             mbar_init(&bars->vfull[s], 1);
             mbar_init(&bars->pad[s], 1);
             mbar_init(&bars->vempty[s], 2);  // both CTAs' products
@@ -165,7 +180,8 @@ __global__ void __launch_bounds__(NT, 1)
         // as much, and what the loads take a tile bounds all else.
         if (lane == 0) {
             const int me = blockIdx.x / 2, all = gridDim.x / 2;
-            int queries = 0, keys = 0;  // tiles asked for
+            int queries = 0, slot = 0;  // tiles asked for; the next block's slot
+            int blocks = 0;             // of keys asked for
             for (int i = 0; ok; ++i) {
                 if (i >= 2) ok = wait_bar(&bars->iempty[i & 1], ((i >> 1) - 1) & 1);
                 if (!ok) break;
@@ -182,76 +198,103 @@ __global__ void __launch_bounds__(NT, 1)
                 if (!some) break;
                 const int n = x.n, b = x.b, hk = 2 * x.hk + rank;
                 if (n == 0) continue;
-                if (queries > 0) ok = wait_bar(&bars->qempty, (queries - 1) & 1);
+                if (queries > 0) {
+                    ok = wait_bar(&bars->qempty, (queries - 1) & 1);
+                    // the last piece's received outputs have been read
+                    if (ok) ok = wait_bar(&bars->xdone, (queries - 1) & 1);
+                }
                 if (!ok) break;
                 ++queries;
-                mbar_expect_tx(&bars->qfull, TILE);
+                mbar_expect_tx(&bars->qfull, 2 * BLOCK);
                 tma_load_5d(sm + SM_Q, &tmq, 0, x.i0, 0, 2 * x.h + rank, b, &bars->qfull);
+                const int jump = 2 * x.sink_tiles, lo = x.lo;
+                int k0 = jump > 0 ? 0 : lo;
 #pragma unroll 1
-                for (int it = 0; it < n && ok; ++it) {
-                    const int s = keys & 1, k0 = x.key0(it);
-                    if (keys >= 2) ok = wait_bar(&bars->kempty[s], ((keys >> 1) - 1) & 1);
-                    // the last piece's received outputs have been read
-                    if (ok && it == 0 && queries > 1) ok = wait_bar(&bars->xdone, queries & 1);
-                    if (!ok) break;
-                    ++keys;
-                    mbar_expect_tx(&bars->kfull[s], TILE);
-                    tma_load_5d(sm + SM_K + s * TILE, &tmk, 0, k0, 0, hk, b, &bars->kfull[s]);
+                for (int j = 0; j < 2 * n; ++j, ++blocks) {
+                    if (blocks >= NK) {
+                        const int last = (blocks - NK) >> 1;  // the slot's last tile
+                        ok = wait_bar(&bars->kempty[last & 1], (last >> 1) & 1);
+                        if (!ok) break;
+                    }
+                    uint64_t *bar = &bars->kfull[(blocks >> 1) & 1];
+                    mbar_expect_tx(bar, BLOCK);
+                    tma_load_5d(sm + SM_K + slot * BLOCK, &tmk, 0, k0, j & 1, hk, b, bar);
+                    slot = slot == NK - 1 ? 0 : slot + 1;
+                    if (j & 1) k0 = j + 1 == jump ? lo : k0 + kDiffKeys;
                 }
             }
             // never leave with copies into shared memory in flight: the last phases
             // of every barrier that was armed here
             if (queries > 0 && !wait_bar(&bars->qfull, (queries - 1) & 1)) ok = false;
-            for (int i = max(0, keys - 2); i < keys; ++i)
-                if (!wait_bar(&bars->kfull[i & 1], (i >> 1) & 1)) ok = false;
+            for (int i = max(0, blocks - NK); i < blocks; ++i)
+                if (!wait_bar(&bars->kfull[(i >> 1) & 1], (i >> 2) & 1)) ok = false;
         }
     } else if (warp == 10) {
         // ============================================================ values
         // Both CTAs multiply the same values: each loads a head of them for both.  A slot
         // is asked for again when both have used it, so its barriers' phases agree.
         uint32_t asked = 0, turn = 0, padded = 0, pad_turn = 0;  // a bit a slot: ever, phase of the last time
+        int slot = 0;                                            // of the next half
+        // one lane throughout: see above
+        auto ask = [&](int k0, int hv, int b, uint64_t *bar) {
+            const uint32_t bit = 1u << slot;
+            if (asked & bit) {
+                ok = wait_bar(&bars->vempty[slot], (turn >> slot) & 1);
+                if (!ok) return;
+                turn ^= bit;
+            }
+            asked |= bit;
+            mbar_expect_tx(&bar[slot], VHALF);
+            tma_load_5d_both(sm + SM_V + slot * VHALF + rank * (VHALF / 2), &tmv, 0, k0, 0, hv, b, &bar[slot]);
+        };
         while (const DiffItem *px = take()) {
             const DiffItem &x = *px;
-            const int n = x.n, b = x.b, hv = 2 * x.hk + rank, kl = x.kl;
+            const int b = x.b, hv = 2 * x.hk + rank, kl = x.kl, jump = 2 * x.sink_tiles, lo = x.lo, all = 2 * x.n;
+            // halves that reach behind the last key, where padding follows, get zeros there: the
+            // last ones (or some, behind sinks that end near it)
+            int plain = kl < a.Tk && x.sink_tiles * kDiffKeys > kl ? 0 : all;
+            if (kl < a.Tk)
+                while (plain > 0 && x.key0((plain - 1) >> 1) + 64 * ((plain - 1) & 1) + 64 > kl) --plain;
+            const int first = slot;
+            if (lane == 0) {
+                int k0 = jump > 0 ? 0 : lo;
 #pragma unroll 1
-            for (int half = 0; half < 2 * n && ok; ++half) {
-                // a piece's halves take the three slots in turn, from the first on
-                const int slot = half % 3, k0 = x.key0(half >> 1) + 64 * (half & 1);
+                for (int half = 0; half < plain && ok;) {
+                    ask(k0, hv, b, bars->vfull);
+                    slot = (slot + 1) % NV;
+                    k0 = ++half == jump ? lo : k0 + 64;
+                }
+            }
+            slot = (first + plain) % NV;
+            ok = __all_sync(0xffffffffu, ok);
+#pragma unroll 1
+            for (int half = plain; half < all && ok; ++half, slot = (slot + 1) % NV) {
+                const int k0 = x.key0(half >> 1) + 64 * (half & 1);
                 const uint32_t bit = 1u << slot;
-                // values behind the last key: zeros, whatever the padding holds
-                const bool pad = kl < a.Tk && k0 + 64 > kl;
+                const bool pad = k0 + 64 > kl;
                 uint8_t *to = sm + SM_V + slot * VHALF;
-                if (lane == 0) {
-                    uint64_t *bar = pad ? &bars->pad[slot] : &bars->vfull[slot];
-                    if (asked & bit) ok = wait_bar(&bars->vempty[slot], (turn >> slot) & 1);
-                    if (ok) {
-                        mbar_expect_tx(bar, VHALF);
-                        tma_load_5d_both(to + rank * (VHALF / 2), &tmv, 0, k0, 0, hv, b, bar);
-                        if (asked & bit) turn ^= bit;
-                        asked |= bit;
-                    }
-                }
+                if (lane == 0) ask(k0, hv, b, pad ? bars->pad : bars->vfull);
                 ok = __all_sync(0xffffffffu, ok);
-                if (pad && ok) {
-                    if (padded & bit) pad_turn ^= bit;
-                    padded |= bit;
-                    ok = wait(&bars->pad[slot], pad_turn >> slot);
-                    const int from = max(0, kl - k0) * 8;  // 16-byte units of 128-byte rows
+                if (!ok) break;
+                if (!pad) continue;
+                if (padded & bit) pad_turn ^= bit;
+                padded |= bit;
+                ok = wait(&bars->pad[slot], pad_turn >> slot);
+                const int from = max(0, kl - k0) * 8;  // 16-byte units of 128-byte rows
 #pragma unroll 1
-                    for (int u = from + lane; u < 64 * 8; u += 32)
-                        for (int c = 0; c < 4; ++c)
-                            *reinterpret_cast<uint4 *>(to + c * 8192 + u * 16) = make_uint4(0, 0, 0, 0);
-                    fence_async_smem();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bars->vfull[slot]);
-                }
+                for (int u = from + lane; u < 64 * 8; u += 32)
+                    for (int c = 0; c < 4; ++c)
+                        *reinterpret_cast<uint4 *>(to + c * 8192 + u * 16) = make_uint4(0, 0, 0, 0);
+                fence_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bars->vfull[slot]);
             }
             __syncwarp();
             give_back();
         }
         // both CTAs' last copies and products
         if (lane == 0) {
-            for (int s = 0; s < 3; ++s) {
+            for (int s = 0; s < NV; ++s) {
                 if ((padded >> s & 1) && !wait_bar(&bars->pad[s], pad_turn >> s & 1)) ok = false;
                 if ((asked >> s & 1) && !wait_bar(&bars->vfull[s], turn >> s & 1)) ok = false;
                 if ((asked >> s & 1) && !wait_bar(&bars->vempty[s], turn >> s & 1)) ok = false;
@@ -261,7 +304,8 @@ __global__ void __launch_bounds__(NT, 1)
         // ===================================================== scores' products
         const bool lead = elect_one();
         const uint64_t dq = tile_desc(smem_u32(sm + SM_Q), 128, 0, 0);
-        int done = 0, used = 0;  // tiles and pieces multiplied
+        int done = 0, used = 0;           // tiles and pieces multiplied
+        int slot = 0;                     // of the next block of keys
         while (const DiffItem *px = take()) {
             const DiffItem &x = *px;
             const int n = x.n;
@@ -269,22 +313,30 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll 1
             for (int it = 0; it < n && ok; ++it) {
                 const int u = done & 1;
-                const uint64_t dk = tile_desc(smem_u32(sm + SM_K) + u * TILE, 128, 0, 0);
                 const uint32_t id = idesc_bf16_f32(BM, x.width(it)) | g.negate;
+                const int slot1 = slot == NK - 1 ? 0 : slot + 1;
                 ok = wait(&bars->kfull[u], done >> 1);
-                // the buffer's weights have been multiplied
-                if (ok && done >= 2) ok = wait(&bars->vdone[u], (done >> 1) - 1);
+                // the products of the buffer's weights are ahead on the pipe
+                if (ok && done >= 2) ok = wait(&bars->queued[u], (done >> 1) - 1);
                 if (!ok) break;
                 tc_fence_after();
                 if (lead) {
+                    const uint64_t dk = tile_desc(smem_u32(sm + SM_K), 128, 0, 0);
+                    const uint64_t dk0 = dk + (uint64_t)(slot * (BLOCK >> 4)), dk1 = dk + (uint64_t)(slot1 * (BLOCK >> 4));
 #pragma unroll
-                    for (int ks = 0; ks < D / 16; ++ks)
-                        mma_bf16(tmem + kS + 128 * u, kdesc_step(dq, 128, ks), kdesc_step(dk, 128, ks), id, ks > 0);
+                    for (int ks = 0; ks < 8; ++ks)
+                        mma_bf16(tmem + kS + 128 * u, kdesc_step(dq, 128, ks), kdesc_step(ks < 4 ? dk0 : dk1, 128, ks & 3), id,
+                                 ks > 0);
+                    // the last tile's value products may follow
+                    tc_fence_before();
+                    if (it > 0) mbar_arrive(&bars->pready[u ^ 1]);
+                    if (it == n - 1) mbar_arrive(&bars->pready[u]);
                     mma_commit(&bars->sfull[u]);
                     mma_commit(&bars->kempty[u]);
                     if (it == n - 1) mma_commit(&bars->qempty);
                 }
                 __syncwarp();
+                slot = slot1 == NK - 1 ? 0 : slot1 + 1;
                 ++done;
             }
             if (n > 0) ++used;
@@ -300,12 +352,6 @@ __global__ void __launch_bounds__(NT, 1)
         const uint64_t dv = tile_desc_mn(smem_u32(sm + SM_V), 64, 0);
         const uint32_t o = tmem + kO;
         int done = 0, used = 0;  // tiles and pieces multiplied
-        int values[3] = {0, 0, 0};
-        // a slot's next half is there
-        auto values_wait = [&](int slot) {
-            int &uses = slot == 0 ? values[0] : (slot == 1 ? values[1] : values[2]);
-            return wait(&bars->vfull[slot], uses++);
-        };
         while (const DiffItem *px = take()) {
             const DiffItem &x = *px;
             const int n = x.n;
@@ -313,9 +359,9 @@ __global__ void __launch_bounds__(NT, 1)
             for (int it = 0; it < n && ok; ++it) {
                 const int u = done & 1, steps = x.width(it) >> 4;
                 const uint32_t p = tmem + kS + 128 * u;
-                const int slot0 = 2 * it % 3, slot1 = (2 * it + 1) % 3;
+                const int slot0 = 2 * u, slot1 = 2 * u + 1;
                 const uint64_t dv0 = dv + (uint64_t)(slot0 * (VHALF >> 4)), dv1 = dv + (uint64_t)(slot1 * (VHALF >> 4));
-                ok = values_wait(slot0);
+                ok = wait(&bars->vfull[slot0], done >> 1);
                 // the last piece's output has left
                 if (ok && it == 0 && used > 0) ok = wait(&bars->oempty, used - 1);
                 if (ok) ok = wait(&bars->pready[u], done >> 1);
@@ -331,13 +377,15 @@ __global__ void __launch_bounds__(NT, 1)
                     mma_commit_both(&bars->vempty[slot0]);
                 }
                 __syncwarp();
-                ok = values_wait(slot1);
+                ok = wait(&bars->vfull[slot1], done >> 1);
                 if (!ok) break;
                 tc_fence_after();
                 if (lead) {
 #pragma unroll
                     for (int ks = 4; ks < 8; ++ks)
                         if (ks < steps) mma_bf16_ta(o, p + 64 + 8 * (ks - 4), mndesc_step(dv1, ks - 4), id_o, 1);
+                    tc_fence_before();
+                    mbar_arrive(&bars->queued[u]);
                     mma_commit_both(&bars->vempty[slot1]);
                     mma_commit(&bars->vdone[u]);
                     if (it == n - 1) mma_commit(&bars->ofull);
@@ -488,7 +536,7 @@ __global__ void __launch_bounds__(NT, 1)
             // no key, or only scores of -inf: zeros
             const float f = (l == 0.f ? 0.f : 1.f / l) * (rank ? -a.lambda[x.h] : 1.f);
             // rows of a warp side by side, so that a store of it writes 512 bytes in a row
-            uint8_t *got = sm + SM_K + (t * 16 * 128 + row) * 16;
+            uint8_t *got = sm + SM_X + (t * 16 * 128 + row) * 16;
             const uint32_t peer = map_to_rank(smem_u32(got), rank ^ 1),
                            peer_bar = map_to_rank(smem_u32(&bars->xfull), rank ^ 1);
             ok = wait(&bars->xempty, used);
@@ -523,7 +571,7 @@ __global__ void __launch_bounds__(NT, 1)
                 y[4 * i] = __fadd_rn(y[4 * i], z.x), y[4 * i + 1] = __fadd_rn(y[4 * i + 1], z.y);
                 y[4 * i + 2] = __fadd_rn(y[4 * i + 2], z.z), y[4 * i + 3] = __fadd_rn(y[4 * i + 3], z.w);
             }
-            fence_async_smem();  // keys come there next
+            fence_async_smem();  // queries and keys come there next
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->xdone);
             float part[4] = {0.f, 0.f, 0.f, 0.f};
@@ -552,18 +600,18 @@ __global__ void __launch_bounds__(NT, 1)
                 scale = diff_rms(squares, D, a.eps);
             }
             ++used;
-            // Rows leave through the warp's shared memory, 32 channels at a time, so
-            // that a store writes whole 64-byte pieces of eight rows.
-            uint8_t *out = sm + SM_OUT + warp * 2048;
-            const int w0 = 32 * (warp & 3), rows = x.rows, r8 = lane >> 2, c8 = lane & 3;
+            // Rows leave through the warp's shared memory, 16 channels at a time, so that a
+            // store writes whole 32-byte sectors of 16 rows.
+            uint8_t *out = sm + SM_OUT + warp * 1024;
+            const int w0 = 32 * (warp & 3), rows = x.rows, r16 = lane >> 1, c2 = lane & 1;
             __nv_bfloat16 *o = static_cast<__nv_bfloat16 *>(a.o) + x.b * a.os.b + (2 * x.h + rank) * a.os.h +
-                               (long long)(x.i0 + w0 + r8) * a.os.t + 64 * t + 8 * c8;
+                               (long long)(x.i0 + w0 + r16) * a.os.t + 64 * t + 8 * c2;
             const float4 *weight = reinterpret_cast<const float4 *>(wsm + 128 * rank + 64 * t);
 #pragma unroll
-            for (int c = 0; c < 64; c += 32) {
-                uint32_t w[16];
+            for (int c = 0; c < 64; c += 16) {
+                uint32_t w[8];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) {
+                for (int i = 0; i < 4; ++i) {
                     const float4 z = weight[c / 4 + i];
                     const float *yi = y + c + 4 * i;
                     w[2 * i] = pack2(yi[0] * scale * z.x, yi[1] * scale * z.y);
@@ -571,15 +619,15 @@ __global__ void __launch_bounds__(NT, 1)
                 }
                 __syncwarp();  // the last channels have left
 #pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    *reinterpret_cast<uint4 *>(out + lane * 64 + (i ^ ((lane >> 1) & 3)) * 16) =
+                for (int i = 0; i < 2; ++i)
+                    *reinterpret_cast<uint4 *>(out + lane * 32 + (i ^ ((lane >> 2) & 1)) * 16) =
                         make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
                 __syncwarp();
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int rr = 8 * i + r8;
-                    const uint4 z = *reinterpret_cast<const uint4 *>(out + rr * 64 + (c8 ^ ((rr >> 1) & 3)) * 16);
-                    if (w0 + rr < rows) *reinterpret_cast<uint4 *>(o + 8 * i * a.os.t + c) = z;
+                for (int i = 0; i < 2; ++i) {
+                    const int rr = 16 * i + r16;
+                    const uint4 z = *reinterpret_cast<const uint4 *>(out + rr * 32 + (c2 ^ ((rr >> 2) & 1)) * 16);
+                    if (w0 + rr < rows) *reinterpret_cast<uint4 *>(o + 16 * i * a.os.t + c) = z;
                 }
             }
             // a value that is not finite shows in the squares, and so do finite ones past
@@ -610,7 +658,7 @@ __global__ void __launch_bounds__(NT, 1)
 cudaError_t launch_diff_wide_tc(const DiffArgs &a, cudaStream_t stream) {
     CUtensorMap mq, mk, mv;
     cudaError_t e = blocks_map(&mq, a.q, a.qs, a.B, 2 * a.H, a.Tq, D, BM, 1);
-    if (e == cudaSuccess) e = blocks_map(&mk, a.k, a.ks, a.B, 2 * a.Hk, a.Tk, D, kDiffKeys, 1);
+    if (e == cudaSuccess) e = blocks_map(&mk, a.k, a.ks, a.B, 2 * a.Hk, a.Tk, D, kDiffKeys, 1, true);
     if (e == cudaSuccess) e = blocks_map(&mv, a.v, a.vs, a.B, 2 * a.Hk, a.Tk, D, 64, 1);
     if (e != cudaSuccess) return e;
     const DiffTcArgs g = diff_tc_args(a, D);
