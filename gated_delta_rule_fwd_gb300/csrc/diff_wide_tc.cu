@@ -11,12 +11,11 @@
 // P V of tile i, S of tile i + 2, P V of tile i + 1: a softmax takes as long as the
 // products of a tile, so scores that wait behind the next value products hold up all
 // (185 -> 200 us).  Both CTAs multiply the same values, so each loads one head of them
-// for both (192 -> 187 us).  Two softmax threads share a
-// row, 64 keys each; they exchange the tile's maximum, so that both raise the one in
-// use together.  At the end a CTA takes over the rows' 128 channels of its half: the
-// CTAs send each other the other half of their output, scaled, through distributed
-// shared memory (over queries and keys, which are free from the last scores on), and the
-// rows' sums of squares.
+// for both (192 -> 187 us).  Two softmax threads share a row, 64 keys each; they
+// exchange the tile's maximum, so that both raise the one in use together.  At the end
+// a CTA takes over the rows' 128 channels of its half: the CTAs send each other the
+// other half of their output, scaled, through distributed shared memory (over queries
+// and keys, which are free from the last scores on), and the rows' sums of squares.
 //
 // What the weights' rounding left is multiplied for a quarter of the keys as in
 // diff_tc.cu; a row's non-finite values, padding and the rounding of the exponent's
@@ -26,11 +25,13 @@
 // half of the CTA's channels, warps 4-7 of the others, warp 8 issues the value
 // products, warp 9 the scores', warp 10 loads the values, warp 11 works out the pieces
 // and loads their queries and keys.
+//
 // A load warp's work per copy counts: its code is cold each time it wakes (two copies
 // a tile by the whole warp took longer than the tile's products), hence one lane in
 // short loops, few barriers, whole boxes.  Every wait is bounded (lr_device_status).
 //
-// Measured: 2 x 4096 causal tokens of 8 pairs: 172 us, 1200 TFLOP/s of visible products.
+// Measured: 2 x 4096 causal tokens of 8 pairs: 172 us, 1194 TFLOP/s of visible products
+// (16384 tokens: 1621).
 // A tile takes some 2000 cycles where its products need 1792; a piece costs 9000 to
 // 10000 more: its last products, the exchange (64 KB each way at some 32 bytes a
 // cycle), two rounds between the CTAs and the stores.
@@ -316,7 +317,8 @@ __global__ void __launch_bounds__(NT, 1)
                 const uint32_t id = idesc_bf16_f32(BM, x.width(it)) | g.negate;
                 const int slot1 = slot == NK - 1 ? 0 : slot + 1;
                 ok = wait(&bars->kfull[u], done >> 1);
-                // the products of the buffer's weights are ahead on the pipe
+                // the products of the buffer's weights are ahead on the pipe, which takes
+                // products in order (the fences on both sides hold it between the two warps)
                 if (ok && done >= 2) ok = wait(&bars->queued[u], (done >> 1) - 1);
                 if (!ok) break;
                 tc_fence_after();

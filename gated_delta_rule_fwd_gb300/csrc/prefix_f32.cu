@@ -6,6 +6,10 @@
 // window_f32.cu.  The prefix is cut into runs of 32-key tiles; every CTA leaves
 // (maximum, sum, unnormalised output) of its run for its rows, and the step over
 // each sequence's own keys joins them (step_paged.cu).
+//
+// Measured: 33 sequences behind 1501 tokens, window 1024, 20.5 us with their own tokens
+// (25.4 when the parts were joined at the end of the own ones); the bound is the issue of
+// split products, as in window_f32.cu.
 #include <limits.h>
 
 #include "attn_f32.cuh"

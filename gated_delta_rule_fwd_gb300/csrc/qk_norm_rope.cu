@@ -34,6 +34,7 @@ constexpr int NT = 256;
 // free, across queries, keys and tokens, costs more instructions than it hides
 // (65 to 67).  fp32 rows take twice the registers: two CTAs.  The bf16 form with
 // split halves spills 12 bytes a thread at its 80 registers.
+// With positions of three axes and the append: 76 us, 85 % of the copy rate.
 constexpr int U = 4;
 template <typename E> constexpr int kCtas = sizeof(E) == 2 ? 3 : 2;
 

@@ -12,6 +12,9 @@
 // P^T with warp-level products, the values shared by the two maps' warps.  What the
 // rounding of a weight to bf16 left is multiplied as well: the difference of the
 // maps takes away what they have in common, but not their roundings.
+// Measured: 64 sequences of 500 to 8192 tokens, 16 pairs on 4, d = 128: 184 us, 92 % of the
+// copy rate (fragments loaded to registers as in step_paged.cu: 262, 216 registers); one
+// sequence of 1200, d = 64: 12.3 us, length, page and rows one after the other.
 //
 // fp32 (step_diff_simt_kernel): CUDA cores; d / 8 lanes hold a key of both maps
 // and its value row.
