@@ -183,6 +183,7 @@ struct StepArgs {
     int plen, all_sinks, pre;
     float *po;
     float2 *pml;
+    int longest_first;  // the sequences are taken in the order of their lengths
 };
 // First position of the window of the row at position p.
 __host__ __device__ __forceinline__ int window_start(int p, int window) {

@@ -32,6 +32,8 @@
 // Rows that come out not finite are explained or computed again from the keys
 // they see (attn_rows.cuh), as in the window form; one vote of the CTA that
 // writes a row finds them.
+#include <limits.h>
+
 #include "attn_internal.cuh"
 #include "attn_rows.cuh"
 #include "attn_step.cuh"
@@ -346,9 +348,37 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts, 
 
 // ------------------------------------------------------------------- bf16
 
+// The sequence at place `place` when the longest comes first: its rank counted by the
+// thread that holds it.  room: kSorted ints and one of shared memory.
+constexpr int kSorted = 2 * NT;
+__device__ __forceinline__ int by_length(const int *lens, int N, int place, int *room) {
+    for (int i = threadIdx.x; i < kSorted; i += NT) room[i] = i < N ? lens[i] : INT_MIN;
+    __syncthreads();
+    for (int i = threadIdx.x; i < N; i += NT) {
+        const int mine = room[i];
+        int rank = 0;
+#pragma unroll 8
+        for (int j = 0; j < (N + 3) / 4; ++j) {
+            const int4 x = reinterpret_cast<const int4 *>(room)[j];
+            rank += x.x > mine || (x.x == mine && 4 * j < i);
+            rank += x.y > mine || (x.y == mine && 4 * j + 1 < i);
+            rank += x.z > mine || (x.z == mine && 4 * j + 2 < i);
+            rank += x.w > mine || (x.w == mine && 4 * j + 3 < i);
+        }
+        if (rank == place) room[kSorted] = i;
+    }
+    __syncthreads();
+    const int n = room[kSorted];
+    __syncthreads();  // the room is used again
+    return n;
+}
+
 // NH: 8-head column blocks of the products.
-template <int D, int NH>
-__global__ void __launch_bounds__(NT)
+// PRE: behind a shared prefix.  Own tokens are short lists, so a CTA's start and its
+// longest sequence count: four CTAs to an SM and the longest first (128 sequences of 100
+// to 1024, 8 key heads: 57 -> 50 us; either alone changed nothing).
+template <int D, int NH, bool PRE>
+__global__ void __launch_bounds__(NT, PRE && NH == 1 ? 4 : 1)
     step_mma_kernel(StepArgs a, Parts parts, ScoreFactor f) {
     const float c = f.c;
     const __nv_bfloat162 sign = __float2bfloat162_rn(f.sign);
@@ -361,7 +391,7 @@ __global__ void __launch_bounds__(NT)
     constexpr int HEADS = 8 * NH;
     __shared__ __align__(16) float so[NT / 32 + 1][HEADS][D + 8];
     __shared__ float sml[NT / 32 + 1][HEADS][2];
-    __shared__ long long rows[kMostTiles];  // first cache row of each tile, -1: a bad page
+    __shared__ __align__(16) long long rows[kMostTiles];  // first cache row of each tile, -1: a bad page
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int G = a.Hq / a.Hk, gq = (G + HEADS - 1) / HEADS;
     int id = blockIdx.x;
@@ -369,12 +399,14 @@ __global__ void __launch_bounds__(NT)
     id /= parts.splits;
     const int gi = id % gq;
     id /= gq;
-    const int hk = id % a.Hk, n = id / a.Hk;
+    const int hk = id % a.Hk;
+    int n = id / a.Hk;
+    if (PRE && a.longest_first) n = by_length(a.lens, a.N, n, reinterpret_cast<int *>(rows));
     const int len = a.lens[n];
     const int h0 = hk * G + gi * HEADS, heads = min(HEADS, G - gi * HEADS);
     if (len < 0 || len > a.max_len) {
         if (len > 0 && tid == 0 && split == 0 && gi == 0 && hk == 0) atomicOr(&g_step_error, kAttnIndex);
-        if (a.pre) wait_for_previous();
+        if (PRE) wait_for_previous();
         if (a.fill && split == 0) zero_rows<__nv_bfloat16, D>(a, n, h0, heads);
         return;
     }
@@ -384,7 +416,7 @@ __global__ void __launch_bounds__(NT)
     const int tiles = sink_tiles + max(0, (s.hi + kTile - 1) / kTile - k_first);
     const int per = parts.chunk / kTile, t0 = split * per, t1 = min(tiles, t0 + per);
     if (t0 >= tiles && split > 0 && !parts.cluster) {  // the join knows how many chunks there are
-        if (a.pre) wait_for_previous();
+        if (PRE) wait_for_previous();
         return;
     }
 
@@ -476,8 +508,8 @@ __global__ void __launch_bounds__(NT)
         load_k(first);
         load_v(first);
     }
-    if (a.pre) wait_for_previous();
-    if (a.pre && split == 0) load_prefix<D>(a, (size_t)n * a.Hq + h0, heads, c, so[NT / 32], sml[NT / 32]);
+    if (PRE) wait_for_previous();
+    if (PRE && split == 0) load_prefix<D>(a, (size_t)n * a.Hq + h0, heads, c, so[NT / 32], sml[NT / 32]);
     for (int i = first; i < t1; i += NT / 32) {
         float sc[NH][4];
 #pragma unroll
@@ -642,8 +674,10 @@ cudaError_t launch_bf16(const StepArgs &a, const Parts &parts, cudaStream_t stre
     const int G = a.Hq / a.Hk, heads = heads_of_cta(G, LR_DT_BF16);
     const unsigned grid = (unsigned)(a.N * a.Hk * ((G + heads - 1) / heads) * parts.splits);
     const ScoreFactor f = score_factor(a.scale);
-    if (heads == 8) return launch_cut(&step_mma_kernel<D, 1>, grid, NT, parts.cluster ? parts.splits : 1, 0, a.pre > 0, stream, a, parts, f);
-    return launch_cut(&step_mma_kernel<D, 2>, grid, NT, parts.cluster ? parts.splits : 1, 0, a.pre > 0, stream, a, parts, f);
+    const int cluster = parts.cluster ? parts.splits : 1;
+    auto go = [&](auto *fn) { return launch_cut(fn, grid, NT, cluster, 0, a.pre > 0, stream, a, parts, f); };
+    if (a.pre) return heads == 8 ? go(&step_mma_kernel<D, 1, true>) : go(&step_mma_kernel<D, 2, true>);
+    return heads == 8 ? go(&step_mma_kernel<D, 1, false>) : go(&step_mma_kernel<D, 2, false>);
 }
 
 template <int D>
@@ -743,6 +777,9 @@ size_t prefix_workspace_bytes(int N, int Hq, int d, const PrefixPlan &p) {
 cudaError_t launch_step_prefix(StepArgs a, int d, lr_dtype dt, void *ws, cudaStream_t stream) {
     const PrefixPlan p = prefix_plan(a.N, a.Hq, a.Hk, d, a.plen, a.window, a.all_sinks, dt);
     a.pre = p.parts;
+    // more CTAs than run at once; beyond kSorted sequences the last ones hardly count
+    const int G = a.Hq / a.Hk, heads = heads_of_cta(G, dt);
+    a.longest_first = dt == LR_DT_BF16 && a.N <= kSorted && (long long)a.N * a.Hk * ((G + heads - 1) / heads) > 4 * 152;
     if (p.parts) {
         a.po = static_cast<float *>(ws);
         a.pml = reinterpret_cast<float2 *>(a.po + (size_t)a.N * a.Hq * p.parts * d);

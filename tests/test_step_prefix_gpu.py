@@ -457,6 +457,19 @@ def test_prefix_calls_in_a_row_on_one_workspace(dev, max_len, dtype):
 
 
 @types
+@pytest.mark.parametrize("N", [123, 256, 257])
+def test_prefix_batches_taken_by_length(dev, N, dtype):
+    """More CTAs than run at once: the longest sequences come first, equal lengths,
+    empty and unused slots among them; beyond 256 sequences in their order."""
+    Hk, d, page, P = 5, 32, 16, 70
+    lens = np.random.RandomState(N).choice([-1, 0, 1, 7, 16, 40, 40, 61], N)
+    lens[[0, N // 2, N - 1]] = 61, -1, 33
+    kc, vc, prefix, table = shared(160, P, lens.tolist(), Hk, page, d, dtype, dev)
+    check(dev, rnd(161, N, 2 * Hk, d, dtype=dtype), kc, vc, prefix, P, table, lens.tolist(), NW, 0)
+    check(dev, rnd(162, N, 2 * Hk, d, dtype=dtype), kc, vc, prefix, P, table, lens.tolist(), 50, 3)
+
+
+@types
 def test_prefix_pages_held_more_than_once(dev, dtype):
     """A page twice in the prefix, the prefix's pages among the own ones, the same
     own pages for several sequences."""
