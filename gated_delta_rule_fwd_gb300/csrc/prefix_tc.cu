@@ -131,17 +131,6 @@ __global__ void __launch_bounds__(NT, 1)
     tc_fence_before();
     let_next_start();
     __syncthreads();
-    // pages of the run, 16 keys at a time
-    for (int i = tid; i < n * (BN / 16); i += NT) {
-        const int key = key0(i / (BN / 16)) + i % (BN / 16) * 16;
-        if (key >= a.plen) continue;
-        const int page = a.ptable[key >> a.page_log2];
-        if (page < 0 || page >= a.num_pages) {
-            bars->broken = 1;
-            atomicOr(&g_prefix_error, kAttnIndex);
-        }
-    }
-    __syncthreads();
     tc_fence_after();
     const uint32_t tmem = bars->tmem;
     bool ok = true;
@@ -274,6 +263,17 @@ __global__ void __launch_bounds__(NT, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->qfull[t]);
         }
+        // pages of the run, 16 keys at a time, while the first tiles are on their way
+        for (int i = tid; i < n * (BN / 16); i += active * BM) {
+            const int key = key0(i / (BN / 16)) + i % (BN / 16) * 16;
+            if (key >= a.plen) continue;
+            const int page = a.ptable[key >> a.page_log2];
+            if (page < 0 || page >= a.num_pages) {
+                bars->broken = 1;
+                atomicOr(&g_prefix_error, kAttnIndex);
+            }
+        }
+        asm volatile("bar.sync 1, %0;" ::"r"(active * BM) : "memory");  // the softmax warps
         const bool broken = bars->broken;
         float m = -INFINITY, l = 0.f;
         for (int it = 0; it < n && ok; ++it) {
