@@ -18,7 +18,7 @@
 // Measured (d = 128, 32 heads on 8): 128 sequences behind 16384 tokens 36 us, 1.5 us a key
 // tile of both query tiles (70 % of the pipe's rate; the chain is that of diff_tc.cu) and
 // 14 us to start, to write 19 MB of parts and to read them; 4 sequences behind 2048, with
-// their own tokens, 12.6 us.  Tiles in 64-key halves: 44 instead of 37 us.
+// their own tokens, 12.5 us.  Tiles in 64-key halves: 44 instead of 37 us.
 // Pages: a tile is copied in boxes of min(page, 128) rows.  Rows of the last page
 // behind the prefix are set to zero as they are loaded; a page outside the pool is
 // read as page 0 and masked.
