@@ -62,9 +62,11 @@ __device__ __forceinline__ void zero_rows(const StepArgs &a, int n, int h0, int 
     for (int i = threadIdx.x; i < heads * D; i += NT) o[i] = from_f<E>(0.f);
 }
 
+// PRE, here and below: a prefix may lie ahead of the sequence's own tokens.
+//
 // Output row `head` of sequence n by one warp, put right where it is not
 // finite.  sum(): of its weights.  Keys of pages outside the pool are left out.
-template <typename E, int D, typename Sum>
+template <typename E, int D, bool PRE, typename Sum>
 __device__ __forceinline__ void mend_step_row(const StepArgs &a, int n, int head, ScoreFactor f, Sum sum) {
     const int lane = threadIdx.x & 31, hk = head / (a.Hq / a.Hk), len = a.lens[n];
     const size_t at = ((size_t)n * a.Hq + head) * D;
@@ -77,15 +79,16 @@ __device__ __forceinline__ void mend_step_row(const StepArgs &a, int n, int head
     mend_row_of<E, D>(
         static_cast<const E *>(a.q) + at,
         [&](int j, const E *&kj, const E *&vj) {
-            const bool shared = j < a.plen;
-            if (!shared) j -= a.plen;
+            const bool shared = PRE && j < a.plen;
+            if (PRE && !shared) j -= a.plen;
             const int page = (shared ? a.ptable : table)[j >> a.page_log2];
             if (page < 0 || page >= a.num_pages) return false;
             const long long row = (((long long)page * a.Hk + hk) << a.page_log2) + (j & ((1 << a.page_log2) - 1));
             kj = static_cast<const E *>(a.k) + row * D, vj = static_cast<const E *>(a.v) + row * D;
             return true;
         },
-        o, seen_keys(a.plen + len - 1, a.plen + len, a.window, a.all_sinks), f, isfinite(sum()));
+        o, PRE ? seen_keys(a.plen + len - 1, a.plen + len, a.window, a.all_sinks) : seen_keys(len - 1, len, a.window, a.sinks),
+        f, isfinite(sum()));
 }
 
 // The prefix's parts of a CTA's rows (row0 on) joined to one, which the first
@@ -122,8 +125,8 @@ __device__ __forceinline__ void load_prefix(const StepArgs &a, size_t row0, int 
 // a maximum of -inf and weighs nothing; one whose scores were all NaN too, but
 // its sum of NaN stays.
 // The part behind the warps' is the prefix's, where the first chunk has one.
-template <typename E, int D, int HEADS, int P>
-__device__ __forceinline__ void finish(float (&so)[NT / 32 + 1][HEADS][P], float (&sml)[NT / 32 + 1][HEADS][2],
+template <typename E, int D, bool PRE, int HEADS, int P>
+__device__ __forceinline__ void finish(float (&so)[NT / 32 + PRE][HEADS][P], float (&sml)[NT / 32 + PRE][HEADS][2],
                                        int heads, int n, int h0, int split, ScoreFactor f, const StepArgs &a,
                                        const Parts &parts) {
     const int tid = threadIdx.x;
@@ -131,17 +134,17 @@ __device__ __forceinline__ void finish(float (&so)[NT / 32 + 1][HEADS][P], float
     const float c = f.c;
     E *out = static_cast<E *>(a.o);
     bool odd = false;  // a value that is not finite
-    const int count = NT / 32 + (a.pre && split == 0);
+    const int count = NT / 32 + (PRE && split == 0);
     __syncthreads();
     for (int i = tid; i < heads * D; i += NT) {
         const int h = i / D, ch = i - h * D;
         float mn = -INFINITY;
 #pragma unroll
-        for (int w = 0; w <= NT / 32; ++w)
+        for (int w = 0; w < NT / 32 + PRE; ++w)
             if (w < count) mn = fmaxf(mn, sml[w][h][0]);
         float sum = 0.f, x = 0.f;
 #pragma unroll
-        for (int w = 0; w <= NT / 32; ++w) {
+        for (int w = 0; w < NT / 32 + PRE; ++w) {
             if (w == count) break;
             const float mw = sml[w][h][0], fw = mw == -INFINITY ? 0.f : ex2((mw - mn) * c);
             sum += fw * sml[w][h][1];
@@ -171,7 +174,7 @@ __device__ __forceinline__ void finish(float (&so)[NT / 32 + 1][HEADS][P], float
     if (!parts.cluster) {
         if (parts.splits == 1 && __syncthreads_or(odd))
             for (int h = tid >> 5; h < heads; h += NT / 32)
-                mend_step_row<E, D>(a, n, h0 + h, f, [&] {
+                mend_step_row<E, D, PRE>(a, n, h0 + h, f, [&] {
                     float mn;
                     return whole(h, mn);
                 });
@@ -210,16 +213,20 @@ __device__ __forceinline__ void finish(float (&so)[NT / 32 + 1][HEADS][P], float
     if (again)
         for (int h = tid >> 5; h < heads; h += NT / 32)
             if (h * D / NT % parts.splits == split)  // a row that was written here
-                mend_step_row<E, D>(a, n, h0 + h, f, [&] { return sml[1][h][1]; });
+                mend_step_row<E, D, PRE>(a, n, h0 + h, f, [&] { return sml[1][h][1]; });
 }
 
-template <int D, int GC>
-__global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts, ScoreFactor f) {
+// With one head the compiler is told how many CTAs an SM to leave registers for: four,
+// which the plan counts on (33 sequences with window 1024, 8 heads: 21.8 us, 24.9 with
+// five), and five behind a prefix, whose kernel's last CTAs they stand beside (33 behind
+// 1501: 20.6 us, 31.7 with four).
+template <int D, int GC, bool PRE>
+__global__ void __launch_bounds__(NT, GC == 1 ? (PRE ? 5 : 4) : 0) step_simt_kernel(StepArgs a, Parts parts, ScoreFactor f) {
     constexpr int LANES = D / 8;            // lanes of a key
     constexpr int GROUPS = NT / LANES;      // keys in flight
     constexpr int U = 4;                    // keys of a group per pass
-    __shared__ __align__(16) float so[NT / 32 + 1][GC][D];
-    __shared__ float sml[NT / 32 + 1][GC][2];
+    __shared__ __align__(16) float so[NT / 32 + PRE][GC][D];
+    __shared__ float sml[NT / 32 + PRE][GC][2];
     const int tid = threadIdx.x, warp = tid >> 5;
     const int G = a.Hq / a.Hk, gq = (G + GC - 1) / GC;
     int id = blockIdx.x;
@@ -232,7 +239,7 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts, 
     const int h0 = hk * G + gi * GC, heads = min(GC, G - gi * GC);
     if (len < 0 || len > a.max_len) {
         if (len > 0 && tid == 0 && split == 0 && gi == 0 && hk == 0) atomicOr(&g_step_error, kAttnIndex);
-        if (a.pre) wait_for_previous();
+        if (PRE) wait_for_previous();
         if (a.fill && split == 0) zero_rows<float, D>(a, n, h0, heads);
         return;
     }
@@ -240,7 +247,7 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts, 
     const int seen = s.s1 + s.hi - s.lo;
     const int c0 = split * parts.chunk;
     if (c0 >= seen && split > 0 && !parts.cluster) {  // the join knows how many chunks there are
-        if (a.pre) wait_for_previous();
+        if (PRE) wait_for_previous();
         return;
     }
     const int c1 = min(seen, c0 + parts.chunk);
@@ -260,9 +267,9 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts, 
     const int lanes0 = (tid & 31) / LANES * LANES;
     const unsigned mask = LANES == 32 ? 0xffffffffu : ((1u << LANES) - 1) << lanes0;
     bool bad = false;
-    if (a.pre) wait_for_previous();
-    if (a.pre && split == 0)
-        load_prefix<D>(a, (size_t)n * a.Hq + h0, heads, f.c, so[NT / 32], sml[NT / 32]);
+    if (PRE) wait_for_previous();
+    if constexpr (PRE)
+        if (split == 0) load_prefix<D>(a, (size_t)n * a.Hq + h0, heads, f.c, so[NT / 32], sml[NT / 32]);
     for (int base = c0 + group; base < c1; base += GROUPS * U) {
         long long row[U];
         float x[U][8], y[U][8], sc[U][GC];  // keys, values: all on their way at once
@@ -343,7 +350,7 @@ __global__ void __launch_bounds__(NT) step_simt_kernel(StepArgs a, Parts parts, 
             if (lane == 0) sml[warp][g][0] = mn, sml[warp][g][1] = l[g];
         }
     }
-    finish<float, D, GC, D>(so, sml, heads, n, h0, split, f, a, parts);
+    finish<float, D, PRE, GC, D>(so, sml, heads, n, h0, split, f, a, parts);
 }
 
 // ------------------------------------------------------------------- bf16
@@ -389,8 +396,8 @@ __global__ void __launch_bounds__(NT, PRE && NH == 1 ? 4 : 1)
     constexpr int KC = D / 32;   // 32-channel pieces of a key: 16 bytes per lane and row
     constexpr int VW = D / 16;   // words of a value row per lane = 16-channel blocks of O^T
     constexpr int HEADS = 8 * NH;
-    __shared__ __align__(16) float so[NT / 32 + 1][HEADS][D + 8];
-    __shared__ float sml[NT / 32 + 1][HEADS][2];
+    __shared__ __align__(16) float so[NT / 32 + PRE][HEADS][D + 8];
+    __shared__ float sml[NT / 32 + PRE][HEADS][2];
     __shared__ __align__(16) long long rows[kMostTiles];  // first cache row of each tile, -1: a bad page
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int G = a.Hq / a.Hk, gq = (G + HEADS - 1) / HEADS;
@@ -509,7 +516,8 @@ __global__ void __launch_bounds__(NT, PRE && NH == 1 ? 4 : 1)
         load_v(first);
     }
     if (PRE) wait_for_previous();
-    if (PRE && split == 0) load_prefix<D>(a, (size_t)n * a.Hq + h0, heads, c, so[NT / 32], sml[NT / 32]);
+    if constexpr (PRE)
+        if (split == 0) load_prefix<D>(a, (size_t)n * a.Hq + h0, heads, c, so[NT / 32], sml[NT / 32]);
     for (int i = first; i < t1; i += NT / 32) {
         float sc[NH][4];
 #pragma unroll
@@ -593,7 +601,7 @@ __global__ void __launch_bounds__(NT, PRE && NH == 1 ? 4 : 1)
                 *reinterpret_cast<float2 *>(&so[warp][h][col]) = make_float2(acc[j][nh][e], acc[j][nh][e + 2]);
             }
         }
-    finish<__nv_bfloat16, D, HEADS, D + 8>(so, sml, heads, n, h0, split, f, a, parts);
+    finish<__nv_bfloat16, D, PRE, HEADS, D + 8>(so, sml, heads, n, h0, split, f, a, parts);
 }
 
 // One CTA of D threads per output row: the chunks' parts in order.
@@ -639,7 +647,7 @@ __global__ void __launch_bounds__(D) step_join_kernel(StepArgs a, Parts parts, S
     const float out = l == 0.f ? 0.f : x / l;
     static_cast<E *>(a.o)[(size_t)r * D + ch] = from_f<E>(out);
     if (__syncthreads_or(!isfinite(out)) && ch < 32)
-        mend_step_row<E, D>(a, n, r - n * a.Hq, factor, [&] { return l; });
+        mend_step_row<E, D, true>(a, n, r - n * a.Hq, factor, [&] { return l; });
 }
 
 Parts parts_of(const StepArgs &a, int d, const StepPlan &p, void *ws) {
@@ -664,9 +672,10 @@ cudaError_t launch_f32(const StepArgs &a, const Parts &parts, cudaStream_t strea
     const int gc = heads_of_cta(G, LR_DT_F32);
     const unsigned grid = (unsigned)(a.N * a.Hk * ((G + gc - 1) / gc) * parts.splits);
     const ScoreFactor f = score_factor(a.scale);
-    if (gc == 1) return launch_cut(&step_simt_kernel<D, 1>, grid, NT, parts.cluster ? parts.splits : 1, 0, a.pre > 0, stream, a, parts, f);
-    if (gc == 2) return launch_cut(&step_simt_kernel<D, 2>, grid, NT, parts.cluster ? parts.splits : 1, 0, a.pre > 0, stream, a, parts, f);
-    return launch_cut(&step_simt_kernel<D, 4>, grid, NT, parts.cluster ? parts.splits : 1, 0, a.pre > 0, stream, a, parts, f);
+    const int cluster = parts.cluster ? parts.splits : 1;
+    auto go = [&](auto *fn) { return launch_cut(fn, grid, NT, cluster, 0, a.pre > 0, stream, a, parts, f); };
+    if (a.pre) return gc == 1 ? go(&step_simt_kernel<D, 1, true>) : gc == 2 ? go(&step_simt_kernel<D, 2, true>) : go(&step_simt_kernel<D, 4, true>);
+    return gc == 1 ? go(&step_simt_kernel<D, 1, false>) : gc == 2 ? go(&step_simt_kernel<D, 2, false>) : go(&step_simt_kernel<D, 4, false>);
 }
 
 template <int D>
