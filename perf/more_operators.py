@@ -314,14 +314,14 @@ def run(s):
         s["o"].copy_(torch.where(live[:, None], o, s["o"].float()))
         return s["o"]
     N, Hk, page = case["N"], case["Hk"], case["page"]
+    table, lens = s["table"].long(), s["lens"].long()
+    most = table.shape[1] * page
     if op == "diff_step":
         if own:
             import gated_delta_rule_fwd_gb300 as lr
             return lr.lr_step_paged_diff(s["q"], s["k_cache"], s["v_cache"], s["table"], s["lens"], s["lam"],
                                          max_len=case["len_hi"], window=case["window"], sinks=case["sinks"],
                                          scale=scale, norm=case["norm"], norm_weight=s["weight"], eps=EPS)
-        table, lens = s["table"].long(), s["lens"].long()
-        most = table.shape[1] * page
         k, v = (c[table].transpose(1, 2).reshape(N, 2 * Hk, most, d).float() for c in (s["k_cache"], s["v_cache"]))
         j = torch.arange(most, device=k.device)
         seen = _visible(lens[:, None] - 1, j, case["window"], case["sinks"])[:, None, None]
@@ -332,8 +332,7 @@ def run(s):
         return lr.lr_step_paged_prefix(s["q"], s["k_cache"], s["v_cache"], s["prefix"], case["P"], s["table"],
                                        s["lens"], max_len=case["len_hi"], window=case["window"],
                                        sinks=case["sinks"], scale=scale)
-    table, lens = s["table"].long(), s["lens"].long()
-    most, Hq, P = table.shape[1] * page, case["Hq"], case["P"]
+    Hq, P = case["Hq"], case["P"]
     q = s["q"].float().view(N, Hk, Hq // Hk, d) * scale
     # the prefix once for all sequences, then every sequence's own keys
     pk, pv = (c[s["prefix"].long()].transpose(0, 1).reshape(Hk, -1, d)[:, :P].float() for c in (s["k_cache"], s["v_cache"]))
