@@ -10,12 +10,12 @@
 // buffer and the value products run at the same time.  The pipe gets them in the order
 // P V of tile i, S of tile i + 2, P V of tile i + 1: a softmax takes as long as the
 // products of a tile, so scores that wait behind the next value products hold up all
-// (185 -> 200 us).  Both CTAs multiply the same values, so each loads one head of them
-// for both (192 -> 187 us).  Two softmax threads share a row, 64 keys each; they
-// exchange the tile's maximum, so that both raise the one in use together.  At the end
-// a CTA takes over the rows' 128 channels of its half: the CTAs send each other the
-// other half of their output, scaled, through distributed shared memory (over queries
-// and keys, which are free from the last scores on), and the rows' sums of squares.
+// (185 -> 200 us).  Each CTA loads the values for itself.  Two softmax threads share a
+// row, 64 keys each; they exchange the tile's maximum, so that both raise the one in use
+// together.  At the end a CTA takes over the rows' 128 channels of its half: the CTAs
+// send each other the other half of their output, scaled, through distributed shared
+// memory (over queries and keys, which are free from the last scores on), and the rows'
+// sums of squares.
 //
 // What the weights' rounding left is multiplied for a quarter of the keys as in
 // diff_tc.cu; a row's non-finite values, padding and the rounding of the exponent's
@@ -87,23 +87,6 @@ static_assert(sizeof(Barriers) <= 448, "shared memory layout");
 constexpr uint32_t kS = 0, kO = 256;  // TMEM columns: two score buffers (P over them), then O
 constexpr uint32_t kSqBytes = 4 * 128 * 4;
 
-// An arrival on this mbarrier of both CTAs when the products issued so far are done.
-__device__ __forceinline__ void mma_commit_both(uint64_t *bar) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_u32(bar)),
-        "h"((uint16_t)3)
-        : "memory");
-}
-// tma_load_5d to the same place of both CTAs, counted on this mbarrier of each.
-__device__ __forceinline__ void tma_load_5d_both(void *dst, const void *map, int x, int y, int z, int w, int v,
-                                                 uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.5d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.multicast::cluster "
-        "[%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(v), "r"(smem_u32(bar)), "h"((uint16_t)3)
-        : "memory");
-}
 // Arrive (count 1) on the mbarrier at cluster address `bar`.
 __device__ __forceinline__ void arrive_remote(uint32_t bar) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
@@ -134,7 +117,7 @@ __global__ void __launch_bounds__(NT, 1)
         for (int s = 0; s < NV; ++s) {
             mbar_init(&bars->vfull[s], 1);
             mbar_init(&bars->pad[s], 1);
-            mbar_init(&bars->vempty[s], 2);  // both CTAs' products
+            mbar_init(&bars->vempty[s], 1);
         }
         for (int s = 0; s < 4; ++s) mbar_init(&bars->pair[s], 2);
         mbar_init(&bars->oempty, 8);
@@ -232,12 +215,10 @@ __global__ void __launch_bounds__(NT, 1)
         }
     } else if (warp == 10) {
         // ============================================================ values
-        // Both CTAs multiply the same values: each loads a head of them for both.  A slot
-        // is asked for again when both have used it, so its barriers' phases agree.
         uint32_t asked = 0, turn = 0, padded = 0, pad_turn = 0;  // a bit a slot: ever, phase of the last time
         int slot = 0;                                            // of the next half
         // one lane throughout: see above
-        auto ask = [&](int k0, int hv, int b, uint64_t *bar) {
+        auto ask = [&](int k0, int hv, int b, uint64_t *bar) {  // both heads' channels by one copy
             const uint32_t bit = 1u << slot;
             if (asked & bit) {
                 ok = wait_bar(&bars->vempty[slot], (turn >> slot) & 1);
@@ -246,11 +227,11 @@ __global__ void __launch_bounds__(NT, 1)
             }
             asked |= bit;
             mbar_expect_tx(&bar[slot], VHALF);
-            tma_load_5d_both(sm + SM_V + slot * VHALF + rank * (VHALF / 2), &tmv, 0, k0, 0, hv, b, &bar[slot]);
+            tma_load_5d(sm + SM_V + slot * VHALF, &tmv, 0, k0, 0, hv, b, &bar[slot]);
         };
         while (const DiffItem *px = take()) {
             const DiffItem &x = *px;
-            const int b = x.b, hv = 2 * x.hk + rank, kl = x.kl, jump = 2 * x.sink_tiles, lo = x.lo, all = 2 * x.n;
+            const int b = x.b, hv = 2 * x.hk, kl = x.kl, jump = 2 * x.sink_tiles, lo = x.lo, all = 2 * x.n;
             // halves that reach behind the last key, where padding follows, get zeros there: the
             // last ones (or some, behind sinks that end near it)
             int plain = kl < a.Tk && x.sink_tiles * kDiffKeys > kl ? 0 : all;
@@ -293,12 +274,11 @@ __global__ void __launch_bounds__(NT, 1)
             __syncwarp();
             give_back();
         }
-        // both CTAs' last copies and products
+        // never leave with copies into shared memory in flight
         if (lane == 0) {
             for (int s = 0; s < NV; ++s) {
                 if ((padded >> s & 1) && !wait_bar(&bars->pad[s], pad_turn >> s & 1)) ok = false;
                 if ((asked >> s & 1) && !wait_bar(&bars->vfull[s], turn >> s & 1)) ok = false;
-                if ((asked >> s & 1) && !wait_bar(&bars->vempty[s], turn >> s & 1)) ok = false;
             }
         }
     } else if (warp == 9) {
@@ -376,7 +356,7 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
                     for (int ks = 0; ks < 2 * kDiffRest; ++ks)
                         if (ks < steps) mma_bf16_ta(o, p + 32 + 8 * ks, mndesc_step(dv0, ks), id_o, 1);
-                    mma_commit_both(&bars->vempty[slot0]);
+                    mma_commit(&bars->vempty[slot0]);
                 }
                 __syncwarp();
                 ok = wait(&bars->vfull[slot1], done >> 1);
@@ -388,7 +368,7 @@ __global__ void __launch_bounds__(NT, 1)
                         if (ks < steps) mma_bf16_ta(o, p + 64 + 8 * (ks - 4), mndesc_step(dv1, ks - 4), id_o, 1);
                     tc_fence_before();
                     mbar_arrive(&bars->queued[u]);
-                    mma_commit_both(&bars->vempty[slot1]);
+                    mma_commit(&bars->vempty[slot1]);
                     mma_commit(&bars->vdone[u]);
                     if (it == n - 1) mma_commit(&bars->ofull);
                 }
@@ -661,7 +641,7 @@ cudaError_t launch_diff_wide_tc(const DiffArgs &a, cudaStream_t stream) {
     CUtensorMap mq, mk, mv;
     cudaError_t e = blocks_map(&mq, a.q, a.qs, a.B, 2 * a.H, a.Tq, D, BM, 1);
     if (e == cudaSuccess) e = blocks_map(&mk, a.k, a.ks, a.B, 2 * a.Hk, a.Tk, D, kDiffKeys, 1, true);
-    if (e == cudaSuccess) e = blocks_map(&mv, a.v, a.vs, a.B, 2 * a.Hk, a.Tk, D, 64, 1);
+    if (e == cudaSuccess) e = blocks_map(&mv, a.v, a.vs, a.B, 2 * a.Hk, a.Tk, D, 64, 2);
     if (e != cudaSuccess) return e;
     const DiffTcArgs g = diff_tc_args(a, D);
     auto *fn = diff_wide_kernel;
