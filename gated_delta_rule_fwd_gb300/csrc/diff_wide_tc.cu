@@ -79,7 +79,7 @@ static_assert(SM_ALLOC <= 227 * 1024, "shared memory of a CTA");
 struct Barriers {
     uint64_t qfull, qempty, kfull[2], kempty[2], vfull[NV], vempty[NV];
     uint64_t sfull[2], pready[2], vdone[2], ofull, oempty;
-    uint64_t ifull[2], iempty[2], pair[4], lfull, xfull, xempty, xdone, sqfull[2], pad[NV], fin[2], queued[2];
+    uint64_t ifull[2], iempty[2], pair[4], lfull, xfull, xempty, xdone, sqfull[2], pad[NV], fin[2];
     uint32_t tmem;
 };
 static_assert(sizeof(Barriers) <= 448, "shared memory layout");
@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(NT, 1)
     if (tid == 0) {
         for (uint64_t *bar : {&bars->qfull, &bars->qempty, &bars->ofull, &bars->xfull}) mbar_init(bar, 1);
         for (int s = 0; s < 2; ++s) {
-            for (uint64_t *bar : {&bars->queued[s], &bars->sfull[s], &bars->vdone[s], &bars->ifull[s], &bars->sqfull[s], &bars->fin[s]})
+            for (uint64_t *bar : {&bars->sfull[s], &bars->vdone[s], &bars->ifull[s], &bars->sqfull[s], &bars->fin[s]})
                 mbar_init(bar, 1);
             mbar_init(&bars->kfull[s], 2);  // a tile's two blocks
             mbar_init(&bars->kempty[s], 1);
@@ -297,9 +297,9 @@ __global__ void __launch_bounds__(NT, 1)
                 const uint32_t id = idesc_bf16_f32(BM, x.width(it)) | g.negate;
                 const int slot1 = slot == NK - 1 ? 0 : slot + 1;
                 ok = wait(&bars->kfull[u], done >> 1);
-                // the products of the buffer's weights are ahead on the pipe, which takes
-                // products in order (the fences on both sides hold it between the two warps)
-                if (ok && done >= 2) ok = wait(&bars->queued[u], (done >> 1) - 1);
+                // the products that read the buffer's weights are done: products of another
+                // shape and accumulator have no order among each other but by completion
+                if (ok && done >= 2) ok = wait(&bars->vdone[u], (done >> 1) - 1);
                 if (!ok) break;
                 tc_fence_after();
                 if (lead) {
@@ -310,7 +310,6 @@ __global__ void __launch_bounds__(NT, 1)
                         mma_bf16(tmem + kS + 128 * u, kdesc_step(dq, 128, ks), kdesc_step(ks < 4 ? dk0 : dk1, 128, ks & 3), id,
                                  ks > 0);
                     // the last tile's value products may follow
-                    tc_fence_before();
                     if (it > 0) mbar_arrive(&bars->pready[u ^ 1]);
                     if (it == n - 1) mbar_arrive(&bars->pready[u]);
                     mma_commit(&bars->sfull[u]);
@@ -366,8 +365,6 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
                     for (int ks = 4; ks < 8; ++ks)
                         if (ks < steps) mma_bf16_ta(o, p + 64 + 8 * (ks - 4), mndesc_step(dv1, ks - 4), id_o, 1);
-                    tc_fence_before();
-                    mbar_arrive(&bars->queued[u]);
                     mma_commit(&bars->vempty[slot1]);
                     mma_commit(&bars->vdone[u]);
                     if (it == n - 1) mma_commit(&bars->ofull);
