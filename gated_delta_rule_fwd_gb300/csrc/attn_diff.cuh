@@ -17,35 +17,127 @@ __device__ __forceinline__ float diff_rms(float squares, int d, float eps) {
     return squares > 0.f ? rsqrtf(squares * (0.5f / d) + eps) : (squares == 0.f ? 0.f : NAN);
 }
 
-// A row whose result is not finite, by one warp: both maps over all 2 d
-// channels from the definition (attn_rows.cuh).  q0, q1: the maps' rows;
-// keys(map, half, j, kj, vj): whether key j can be read, its row of k for the map
-// and of v for the half; fin0, fin1: whether the maps' sums of weights are
-// finite.  y[half][i]: the row's channel half d + lane + 32 i.
+// One map of a row that did not come out finite, by one warp, from what the row sees:
+// 32 keys at a time from the newest on, a lane a key for their scores, then all lanes
+// over the values, of which four keys are on their way at once.  A running mean, which no
+// large value can drive out of range; infinities and NaN are noted channel by channel and
+// stand for the channel in the end (attn_rows.cuh has the rules).  A score of NaN or +inf
+// makes the row NaN: false.  y[half][i]: channel half d + lane + 32 i, of the halves (bits)
+// that are asked for.
+template <typename E, int D, typename Keys>
+__device__ __forceinline__ bool mend_map(const E *q, int map, const Keys &keys, SeenKeys s, ScoreFactor f,
+                                         unsigned halves, float (&y)[2][D / 32]) {
+    constexpr int PL = D / 32, U = 4;
+    constexpr float kMost = 3.402823466e38f;
+    const int lane = threadIdx.x & 31;
+    unsigned found[2][PL];  // seen in a channel: 1 +inf, 2 -inf, 4 NaN
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int i = 0; i < PL; ++i) found[half][i] = 0, y[half][i] = 0.f;
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+    for (int j0 = s.hi - 1; j0 >= 0; j0 -= 32) {
+        if (j0 < s.lo && j0 >= s.s1) j0 = s.s1 - 1;
+        const int j = j0 - lane;
+        float x = -INFINITY;
+        const E *kj, *vj;
+        const bool on = j >= 0 && (j >= s.lo || j < s.s1) && keys(map, 0, j, kj, vj);
+        if (on) {
+            x = 0.f;
+#pragma unroll 4
+            for (int c = 0; c < D; c += 4) {
+                const float4 a = load4(q + c), b = load4(kj + c);
+                x += a.x * b.x + a.y * b.y + a.z * b.z + a.w * b.w;
+            }
+            x *= f.sign;
+        }
+        if (__any_sync(0xffffffffu, !(x < INFINITY))) return false;
+        float top = x;
+#pragma unroll
+        for (int w = 16; w; w >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, w));
+        top = fmaxf(top, m);
+        // a score of -inf weighs nothing
+        const float old = m == -INFINITY ? 0.f : l * ex2((m - top) * f.c), p = x == -INFINITY ? 0.f : ex2((x - top) * f.c);
+        m = top;
+        l = old + warp_sum(p);
+        const float keep = l > 0.f ? old / l : 0.f, take = l > 0.f ? p / l : 0.f;
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int i = 0; i < PL; ++i) y[half][i] *= keep;
+        const unsigned some = __ballot_sync(0xffffffffu, on);
+#pragma unroll 1
+        for (int b = 0; b < 32; b += U) {
+            float v[U][2][PL];
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    const bool read = (some >> (b + u) & 1u) && (halves >> half & 1u) && keys(map, half, j0 - b - u, kj, vj);
+#pragma unroll
+                    for (int i = 0; i < PL; ++i) v[u][half][i] = read ? to_f<E>(vj[lane + 32 * i]) : 0.f;
+                }
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+                const float w = __shfl_sync(0xffffffffu, take, b + u);
+#pragma unroll
+                for (int half = 0; half < 2; ++half)
+#pragma unroll
+                    for (int i = 0; i < PL; ++i) {
+                        const float z = v[u][half][i];
+                        if (!isfinite(z)) found[half][i] |= z > 0.f ? 1u : (z < 0.f ? 2u : 4u);
+                        // a mean of the type's largest values, but for its rounding
+                        y[half][i] = fminf(fmaxf(fmaf(w, z, y[half][i]), -kMost), kMost);
+                    }
+            }
+        }
+        bool open = false;  // a channel that more keys could still change
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+#pragma unroll
+            for (int i = 0; i < PL; ++i) open = open || ((halves >> half & 1u) && found[half][i] < 3u);
+        if (!__any_sync(0xffffffffu, open)) break;
+    }
+#pragma unroll
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int i = 0; i < PL; ++i)
+            if (found[half][i])
+                y[half][i] = found[half][i] == 1u ? INFINITY : (found[half][i] == 2u ? -INFINITY : NAN);
+    return true;
+}
+
+// A row whose difference is not finite, by one warp, from the definition.  q0, q1: the
+// maps' rows; keys(map, half, j, kj, vj): whether key j can be read, its row of k for the
+// map and of v for the half; halves: those of the value row (bits) that are wanted without
+// the norm.  y[half][i]: the row's channel half d + lane + 32 i.
 template <typename E, int D, typename Keys>
 __device__ __forceinline__ void mend_diff(const E *q0, const E *q1, const Keys &keys, float lambda, bool norm,
-                                          const float *weight, float eps, SeenKeys s, ScoreFactor f, bool fin0,
-                                          bool fin1, float (&y)[2][D / 32]) {
+                                          const float *weight, float eps, SeenKeys s, ScoreFactor f, unsigned halves,
+                                          float (&y)[2][D / 32]) {
     constexpr int PL = D / 32;
     const int lane = threadIdx.x & 31;
+    if (norm) halves = 3;
+    bool fine = true;
 #pragma unroll 1
-    for (int half = 0; half < 2; ++half)
-#pragma unroll 1
-        for (int map = 0; map < 2; ++map) {
-            float x[PL];
-            unsigned odd[PL];
+    for (int map = 0; map < 2 && fine; ++map) {
+        float x[2][PL];
+        fine = mend_map<E, D>(map ? q1 : q0, map, keys, s, f, halves, x);
 #pragma unroll
-            for (int i = 0; i < PL; ++i) odd[i] = 1, x[i] = 0.f;
-            mend_values<E, D>(
-                map ? q1 : q0, [&](int j, const E *&kj, const E *&vj) { return keys(map, half, j, kj, vj); }, x, odd,
-                s, f, map ? fin1 : fin0);
+        for (int half = 0; half < 2; ++half)
 #pragma unroll
-            for (int i = 0; i < PL; ++i) y[half][i] = map ? y[half][i] - lambda * x[i] : x[i];
-        }
-    if (!norm) return;
+            for (int i = 0; i < PL; ++i) y[half][i] = map ? y[half][i] - lambda * x[half][i] : x[half][i];
+    }
     float sum = 0.f;
 #pragma unroll
-    for (int i = 0; i < PL; ++i) sum += y[0][i] * y[0][i] + y[1][i] * y[1][i];
+    for (int half = 0; half < 2; ++half)
+#pragma unroll
+        for (int i = 0; i < PL; ++i) {
+            if (!fine) y[half][i] = NAN;
+            sum += y[half][i] * y[half][i];
+        }
+    if (!norm) return;
     const float r = diff_rms(warp_sum(sum), D, eps);
 #pragma unroll
     for (int half = 0; half < 2; ++half)

@@ -75,33 +75,69 @@ __device__ __forceinline__ void make_diff_item(const DiffTcArgs &g, int block, D
     x.all1 = x.sink_tiles + (end > 0 ? end / kDiffKeys : 0);
 }
 
-// One row by a warp, put right; this CTA and warpgroup write channels c0 ..
-// c0 + n - 1 of the pair's 2 D.
+// What follows the difference of a row, for the sum of its squares (`squares`; of the
+// thread's own values where there is no norm): NaN for a row that is to be put right.  Such
+// a row leaves as NaN in all of its channels, which marks it for mend_marked.
+__device__ __forceinline__ float diff_scale(bool norm, float squares, int d, float eps) {
+    return norm ? diff_rms(squares, d, eps) : (squares == squares ? 1.f : NAN);
+}
+// The squares' sum of N values: NaN where one of them is not finite.  Squares of finite
+// values may pass the range; the row is then divided by infinity, as the formula has it.
+template <int N>
+__device__ __forceinline__ float marked_squares(const float (&y)[N], float squares) {
+    if (squares < INFINITY) return squares;
+    float odd = 0.f;
+#pragma unroll
+    for (int i = 0; i < N; ++i) odd = fmaf(y[i], 0.f, odd);
+    return odd == 0.f ? INFINITY : NAN;
+}
+
+// Rows that the pieces of this CTA (or cluster), number `me` of `all`, left marked, by the
+// warp that wrote rows row0 .. row0 + 31 of each piece and channels c0 .. c0 + n - 1 of the
+// pair's 2 D.  It comes last, when no other warp waits for this one: a row takes two passes
+// over all its keys.
 template <int D>
-__device__ __forceinline__ void mend_pair_row(const DiffTcArgs &g, const DiffItem &x, int row, int c0, int n, bool fin0, bool fin1) {
+__device__ __forceinline__ void mend_marked(const DiffTcArgs &g, int me, int all, int row0, int c0, int n) {
     using E = __nv_bfloat16;
     const DiffArgs &a = g.a;
-    const int lane = threadIdx.x & 31;
-    const E *q = static_cast<const E *>(a.q) + x.b * a.qs.b + 2 * x.h * a.qs.h + (long long)(x.i0 + row) * a.qs.t;
-    const E *k = static_cast<const E *>(a.k) + x.b * a.ks.b + 2 * x.hk * a.ks.h;
-    const E *v = static_cast<const E *>(a.v) + x.b * a.vs.b + 2 * x.hk * a.vs.h;
-    E *o = static_cast<E *>(a.o) + x.b * a.os.b + 2 * x.h * a.os.h + (long long)(x.i0 + row) * a.os.t;
-    float y[2][D / 32];
-    mend_diff<E, D>(
-        q, q + a.qs.h,
-        [&](int map, int half, int j, const E *&kj, const E *&vj) {
-            kj = k + map * a.ks.h + j * a.ks.t, vj = v + half * a.vs.h + j * a.vs.t;
-            return true;
-        },
-        a.lambda[x.h], a.norm, a.weight, a.eps, seen_keys(x.p0 + row, x.kl, a.window, a.sinks),
-        score_factor(a.scale), fin0, fin1, y);
+    const int lane = threadIdx.x & 31, own = c0 / D;
+    __syncwarp();
+#pragma unroll 1
+    for (int i = 0;; ++i) {
+        const long long block = (long long)i * all + (i & 1 ? all - 1 - me : me);
+        if (block >= g.pieces) break;
+        bool bad = false;
+        DiffItem x;
+        make_diff_item(g, (int)block, x, &bad);
+        E *o = static_cast<E *>(a.o) + x.b * a.os.b + 2 * x.h * a.os.h + (long long)(x.i0 + row0) * a.os.t;
+        float mark = 0.f;
+        if (row0 + lane < x.rows) mark = to_f<E>(o[own * a.os.h + lane * a.os.t + c0 - own * D]);
+        unsigned again = __ballot_sync(0xffffffffu, mark != mark);
+        while (again) {
+            const int row = __ffs(again) - 1;
+            again &= again - 1;
+            const E *q = static_cast<const E *>(a.q) + x.b * a.qs.b + 2 * x.h * a.qs.h +
+                         (long long)(x.i0 + row0 + row) * a.qs.t;
+            const E *k = static_cast<const E *>(a.k) + x.b * a.ks.b + 2 * x.hk * a.ks.h;
+            const E *v = static_cast<const E *>(a.v) + x.b * a.vs.b + 2 * x.hk * a.vs.h;
+            float y[2][D / 32];
+            mend_diff<E, D>(
+                q, q + a.qs.h,
+                [&](int map, int half, int j, const E *&kj, const E *&vj) {
+                    kj = k + map * a.ks.h + j * a.ks.t, vj = v + half * a.vs.h + j * a.vs.t;
+                    return true;
+                },
+                a.lambda[x.h], a.norm, a.weight, a.eps, seen_keys(x.p0 + row0 + row, x.kl, a.window, a.sinks),
+                score_factor(a.scale), 1u << own, y);
 #pragma unroll
-    for (int half = 0; half < 2; ++half)
+            for (int half = 0; half < 2; ++half)
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) {
-            const int ch = half * D + lane + 32 * i;
-            if (ch >= c0 && ch < c0 + n) o[half * a.os.h + lane + 32 * i] = from_f<E>(y[half][i]);
+                for (int c = 0; c < D / 32; ++c) {
+                    const int ch = half * D + lane + 32 * c;
+                    if (ch >= c0 && ch < c0 + n) o[half * a.os.h + row * a.os.t + lane + 32 * c] = from_f<E>(y[half][c]);
+                }
         }
+    }
 }
 
 inline DiffTcArgs diff_tc_args(const DiffArgs &a, int d) {

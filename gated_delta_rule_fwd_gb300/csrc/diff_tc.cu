@@ -338,6 +338,7 @@ __global__ void __launch_bounds__(NT, 1)
         const int col = t * CH;     // the first of them in the outputs
         const int half = col / D, in_half = col - half * D;
         int seen = 0, used = 0;
+        bool marked = false;  // a row of the warp is to be put right
         while (const DiffItem *px = take()) {
             const DiffItem &x = *px;
             const int n = x.n, all0 = x.all0, all1 = x.all1;
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(NT, 1)
             tc_fence_before();
             __syncwarp();
             if (lane == 0) mbar_arrive(&bars->oempty);
-            float scale = 1.f;
+            squares = marked_squares(y, squares);
             if (a.norm) {
                 // the other channels' sum of this row, from the other warpgroup
                 float *sq = reinterpret_cast<float *>(sm + L::SQ) + slot * 256;
@@ -403,10 +404,10 @@ __global__ void __launch_bounds__(NT, 1)
                 if (lane == 0) mbar_arrive(&bars->sqready);
                 ok = __all_sync(0xffffffffu, wait_bar(&bars->sqready, used & 1));
                 if (!ok) break;
-                const float total = sq[row] + sq[128 + row];
-                scale = diff_rms(total, D, a.eps);
-                squares = total;
+                squares = sq[row] + sq[128 + row];
             }
+            const float scale = diff_scale(a.norm, squares, D, a.eps);
+            marked = marked || (row < x.rows && scale != scale);
             ++used;
             // Rows leave through the warp's shared memory, 32 channels at a time,
             // so that a store writes whole 64-byte pieces of eight rows.
@@ -438,18 +439,10 @@ __global__ void __launch_bounds__(NT, 1)
                     if (w0 + rr < rows) *reinterpret_cast<uint4 *>(o + 8 * i * a.os.t + c) = z;
                 }
             }
-            // a value that is not finite shows in the squares, and so do finite ones past
-            // 1.8e19: these rows are computed again as well
-            unsigned again = __ballot_sync(0xffffffffu, row < rows && !(squares < INFINITY));
-            __syncwarp();
-            while (again) {
-                const int src = __ffs(again) - 1;
-                again &= again - 1;
-                mend_pair_row<D>(g, x, w0 + src, col, CH, isfinite(__shfl_sync(0xffffffffu, l0, src)),
-                            isfinite(__shfl_sync(0xffffffffu, l1, src)));
-            }
             give_back();
         }
+        if (ok && __any_sync(0xffffffffu, marked))
+            mend_marked<D>(g, blockIdx.x, gridDim.x, 32 * (warp & 3), col, CH);
     }
 
     if (!ok) atomicOr(&g_diff_error, kAttnTimeout);

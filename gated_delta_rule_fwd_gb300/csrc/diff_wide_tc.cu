@@ -386,6 +386,7 @@ __global__ void __launch_bounds__(NT, 1)
         const float2 c2 = make_float2(g.c, g.c);
         float *maxima = reinterpret_cast<float *>(sm + SM_MAX);
         int seen = 0, used = 0;
+        bool marked = false;  // a row of the warp is to be put right
         while (const DiffItem *px = take()) {
             const DiffItem &x = *px;
             const int n = x.n, all0 = x.all0, all1 = x.all1;
@@ -556,7 +557,7 @@ __global__ void __launch_bounds__(NT, 1)
             float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int i = 0; i < 64; ++i) part[i & 3] = fmaf(y[i], y[i], part[i & 3]);
-            float squares = (part[0] + part[1]) + (part[2] + part[3]), scale = 1.f;
+            float squares = marked_squares(y, (part[0] + part[1]) + (part[2] + part[3]));
             if (a.norm) {
                 // the row's other channels: every warp sends its rows' sums to both CTAs,
                 // four a lane
@@ -576,8 +577,9 @@ __global__ void __launch_bounds__(NT, 1)
                 squares = (sq[row] + sq[128 + row]) + (sq[256 + row] + sq[384 + row]);
                 // the slot's next use is two pieces on (its sums may come before it is armed)
                 if (tid == 0) mbar_expect_tx(&bars->sqfull[slot], kSqBytes);
-                scale = diff_rms(squares, D, a.eps);
             }
+            const float scale = diff_scale(a.norm, squares, D, a.eps);
+            marked = marked || (row < x.rows && scale != scale);
             ++used;
             // Rows leave through the warp's shared memory, 16 channels at a time, so that a
             // store writes whole 32-byte sectors of 16 rows.
@@ -609,19 +611,10 @@ __global__ void __launch_bounds__(NT, 1)
                     if (w0 + rr < rows) *reinterpret_cast<uint4 *>(o + 16 * i * a.os.t + c) = z;
                 }
             }
-            // a value that is not finite shows in the squares, and so do finite ones past
-            // 1.8e19: these rows are computed again as well
-            unsigned again = __ballot_sync(0xffffffffu, row < rows && !(squares < INFINITY));
-            __syncwarp();
-            while (again) {
-                const int src = __ffs(again) - 1;
-                again &= again - 1;
-                // of the other map's sum nothing is known here
-                const bool fin = isfinite(__shfl_sync(0xffffffffu, l, src));
-                mend_pair_row<D>(g, x, w0 + src, 128 * rank + 64 * t, 64, rank == 0 && fin, rank == 1 && fin);
-            }
             give_back();
         }
+        if (ok && __any_sync(0xffffffffu, marked))
+            mend_marked<D>(g, blockIdx.x / 2, gridDim.x / 2, 32 * (warp & 3), 128 * rank + 64 * t, 64);
     }
 
     if (!ok) atomicOr(&g_diff_wide_error, kAttnTimeout);

@@ -73,7 +73,7 @@ __device__ __forceinline__ void finish_pair(const DiffStep &s, int n, int h, int
     const StepArgs &a = s.a;
     const int lane = threadIdx.x & 31;
     const float lambda = s.lambda[h];
-    float y[N], sums[2];
+    float y[N];
 #pragma unroll
     for (int map = 0; map < 2; ++map) {
         float top = -INFINITY, sum = 0.f, x[N];
@@ -101,7 +101,6 @@ __device__ __forceinline__ void finish_pair(const DiffStep &s, int n, int h, int
             }
             top = mn;
         }
-        sums[map] = sum;
         // no key, or only scores of -inf: zeros
         const float inv = sum == 0.f ? 0.f : (map ? -lambda : 1.f) / sum;
         // each product rounded, so that equal maps cancel exactly
@@ -112,14 +111,13 @@ __device__ __forceinline__ void finish_pair(const DiffStep &s, int n, int h, int
 #pragma unroll
     for (int c = 0; c < N; ++c) squares = fmaf(y[c], y[c], squares);
     squares = warp_sum(squares);
-    bool odd = s.norm && !(squares < INFINITY);
+    bool odd = false;
     const float r = s.norm ? diff_rms(squares, D, s.eps) : 1.f;
     E *o = static_cast<E *>(a.o) + ((size_t)n * a.Hq + h) * 2 * D + lane;
 #pragma unroll
     for (int c = 0; c < N; ++c) {
-        y[c] = y[c] * r * (s.norm && s.weight ? s.weight[lane + 32 * c] : 1.f);
         odd = odd || !isfinite(y[c]);
-        o[32 * c] = from_f<E>(y[c]);
+        o[32 * c] = from_f<E>(y[c] * r * (s.norm && s.weight ? s.weight[lane + 32 * c] : 1.f));
     }
     if (!__any_sync(0xffffffffu, odd)) return;
     // not finite: from the definition; keys of pages outside the pool are left out
@@ -137,8 +135,7 @@ __device__ __forceinline__ void finish_pair(const DiffStep &s, int n, int h, int
             vj = static_cast<const E *>(a.v) + (((head + half) << a.page_log2) + at) * D;
             return true;
         },
-        lambda, s.norm, s.weight, s.eps, seen_keys(len - 1, len, a.window, a.sinks), f, isfinite(sums[0]),
-        isfinite(sums[1]), z);
+        lambda, s.norm, s.weight, s.eps, seen_keys(len - 1, len, a.window, a.sinks), f, 3, z);
 #pragma unroll
     for (int half = 0; half < 2; ++half)
 #pragma unroll

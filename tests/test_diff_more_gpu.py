@@ -64,3 +64,118 @@ def test_diff_rows_of_many_tiles(dev, d, dtype):
     within(first, ref, bound)
     for _ in range(20):
         assert torch.equal(lr.lr_fwd_diff(*on, eps=EPS), first)
+
+
+LONG = 8192
+
+
+def _seconds(call):
+    import time
+    torch.cuda.synchronize()
+    t0 = time.time()
+    o = call()
+    torch.cuda.synchronize()
+    return o, time.time() - t0
+
+
+@widths
+@pytest.mark.parametrize("norm", [True, False], ids=["norm", "plain"])
+def test_diff_one_early_infinity_in_a_long_sequence(dev, norm, d):
+    """Every row but the first few sees an infinity in one channel, none has an end in
+    sight before its last key: all rows are written, in time, and no wait gives up.
+    Without the norm that channel is NaN where lambda is positive and the infinity where
+    it is negative, and the others are as without it; with the norm NaN in all channels
+    or in that one, with zeros beside it."""
+    H, T, last = 8, LONG, 200
+    q, k, v, _ = inputs(1, H, 4, T, T, d, BF16, seed=311)
+    lam = torch.where(torch.arange(H) % 2 == 0, 0.5, -0.5)
+    ref, bound, _ = oa.diff(np64(q[:, :4, -last:]), np64(k[:, :2]), np64(v[:, :2]), np64(lam[:2]), NW, 0, d ** -0.5,
+                            BITS[BF16], 8)
+    v[0, 1, 5, 7] = float("inf")  # the second half of the first two pairs' values
+    on = [t.to(dev) for t in (q, k, v, lam)]
+    o, seconds = _seconds(lambda: lr.lr_fwd_diff(*on, norm=norm, eps=EPS, o=torch.full_like(on[0], 7.0)))
+    assert lr.device_status() == LR_OK
+    assert seconds < 1.0
+    assert not (o[0, :, 5:] == 7).all(-1).any()
+    assert o[0, 4:].isfinite().all() and o[0, :4, :5].isfinite().all()
+    if norm:
+        assert o[0, :2, 5:].isnan().all() and o[0, 3, 5:, 7].isnan().all()
+        assert (o[0, 2, 5:] == 0).all() and (o[0, 3, 5:, :7] == 0).all() and (o[0, 3, 5:, 8:] == 0).all()
+        return
+    assert o[0, 1, 5:, 7].isnan().all() and (o[0, 3, 5:, 7] == float("inf")).all()
+    got = o[:, :4, -last:].clone()
+    got[:, 1::2, :, 7] = torch.from_numpy(ref[:, 1::2, :, 7]).to(dev)
+    bound[:, 1::2, :, 7] += 1.0
+    # rows that are computed again are rounded another way
+    within(got, ref, 2 * bound)
+
+
+@widths
+def test_diff_squares_past_the_range_stay_quick(dev, d):
+    """Finite values whose squares overflow: rows of zeros with the norm, without a
+    second computation of every row; without it they are as they are."""
+    T = LONG
+    q, k, v, lam = inputs(1, 8, 8, T, T, d, BF16, seed=321)
+    v.fill_(2.0 ** 70)
+    on = [t.to(dev) for t in (q, k, v, lam)]
+    usual = _seconds(lambda: lr.lr_fwd_diff(*[t.to(dev) for t in inputs(1, 8, 8, T, T, d, BF16, seed=321)]))[1]
+    o, seconds = _seconds(lambda: lr.lr_fwd_diff(*on, eps=EPS))
+    assert (o == 0).all()
+    assert seconds < usual + 0.02
+    o = np64(lr.lr_fwd_diff(*on, norm=False)) / 2.0 ** 70
+    want = 1 - np.repeat(np64(lam), 2)[None, :, None, None]
+    # the two means are off by the weights' rounding, 2^-8 each, and the result's
+    assert (np.abs(o - want) <= 2.0 ** -7 * 2).all()
+
+
+@types
+@widths
+def test_diff_rows_put_right_in_pieces_in_turn(dev, d, dtype):
+    """More pieces than run at once, ragged, with NaN and infinities in some of them: the
+    rows that see them, and no others."""
+    B, H, T = 3, 16, 700
+    q, k, v, lam = inputs(B, H, 4, T, T, d, dtype, seed=331)
+    lens = [700, 389, 130]
+    ref, bound, written = oa.diff(np64(q), np64(k), np64(v), np64(lam), 300, 2, d ** -0.5, BITS[dtype],
+                                  8 if dtype == BF16 else None, None, None, lens, lens)
+    nan, inf = float("nan"), float("inf")
+    v[0, 0, 600, 1], v[1, 3, 50, 2], v[1, 3, 60, 2], v[2, 7, 129, d - 1] = nan, inf, -inf, nan
+    ints = torch.tensor(lens, dtype=torch.int32, device=dev)
+    o = torch.full(q.shape, 7.0, dtype=dtype, device=dev)
+    lr.lr_fwd_diff(*(t.to(dev) for t in (q, k, v, lam)), window=300, sinks=2, norm=False, q_len=ints, k_len=ints, o=o)
+    got, rows = np64(o), np.arange(T)
+    for b, head, ch, sees in ((0, 0, 1, (rows >= 600)), (1, 1, 2, (rows >= 50) & (rows < 360)),
+                              (2, 1, d - 1, rows >= 129)):
+        pairs = {0: 0, 3: 1, 7: 3}[{0: 0, 1: 3, 2: 7}[b]]
+        for h in range(4 * pairs, 4 * pairs + 4):
+            at = sees & (rows < lens[b])
+            assert np.isnan(got[b, 2 * h + head, at, ch]).all()
+            got[b, 2 * h + head, at, ch] = ref[b, 2 * h + head, at, ch]
+    w = np.broadcast_to(written[:, None, :, None], ref.shape)
+    within(torch.from_numpy(got), np.where(w, ref, 7.0), np.where(w, 2 * bound, 0.0))
+
+
+@types
+@widths
+@pytest.mark.parametrize("max_len", [65536, 131072])
+def test_diff_step_beside_an_early_infinity(dev, max_len, d, dtype):
+    """One sequence of 65536 tokens whose fourth holds an infinity: its channel, and the
+    others as without it."""
+    L, page = 65536, 256
+    q = rnd(341, 1, 4, d, dtype=dtype)
+    kc, vc = (rnd(342 + i, L // page, 2, page, d, dtype=dtype) for i in range(2))
+    lam = torch.tensor([0.5, -0.5])
+    table = torch.zeros(1, max_len // page, dtype=torch.int32)
+    table[0, :L // page] = torch.arange(L // page)
+    ref, bound, _ = oa.diff_step(np64(q), np64(kc), np64(vc), table.numpy(), [L], np64(lam), NW, 0, d ** -0.5,
+                                 BITS[dtype], 8 if dtype == BF16 else None)
+    vc[0, 1, 3, 2] = float("inf")
+    on = [t.to(dev) for t in (q, kc, vc, table, torch.tensor([L], dtype=torch.int32), lam)]
+    o, seconds = _seconds(lambda: lr.lr_step_paged_diff(*on, max_len=max_len, norm=False))
+    assert seconds < 0.5
+    assert o[0, 1, 2].isnan() and o[0, 3, 2] == float("inf")
+    got = np64(o)
+    got[0, 1::2, 2] = ref[0, 1::2, 2]
+    within(torch.from_numpy(got), ref, 2 * bound)
+    normed = lr.lr_step_paged_diff(*on, max_len=max_len)
+    assert normed[0, :2].isnan().all() and normed[0, 3, 2].isnan() and (normed[0, 2] == 0).all()
