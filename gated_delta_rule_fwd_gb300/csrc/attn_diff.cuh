@@ -11,10 +11,12 @@
 
 namespace lr {
 
-// What follows the difference, for the squares' sum of a whole row (2 d
-// channels): a row of zeros stays one, with eps 0 too.
+// What follows the difference, for the squares' sum of a whole row (2 d channels).  A mean
+// that underflows counts as the smallest number there is: a row of zeros stays one, with
+// eps 0 too, and a row that is not zero stays finite.
 __device__ __forceinline__ float diff_rms(float squares, int d, float eps) {
-    return squares > 0.f ? rsqrtf(squares * (0.5f / d) + eps) : (squares == 0.f ? 0.f : NAN);
+    const float mean = squares * (0.5f / d) + eps;
+    return mean > 0.f ? rsqrtf(mean) : (mean == 0.f ? 0x1.6a09e6p74f : NAN);  // 2^74.5
 }
 
 // One map of a row that did not come out finite, by one warp, from what the row sees:

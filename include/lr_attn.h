@@ -190,10 +190,11 @@ lr_status lr_fwd_window(const void *q, lr_strides qs, const void *k, lr_strides 
  * (see above) lr_fwd_diff multiplies what it left for a quarter of the keys, so that
  * the error of a result is 1.4 times that of 32-bit weights although the maps'
  * common part goes; lr_step_paged_diff does so for all keys.  Equal maps cancel
- * exactly.  A row that sees no key, or whose y
- * is zero, is zeros.  Where a map's row is not finite (lr_fwd_window says when)
- * the formulas hold as fp32 arithmetic has them; a row whose squares sum to more
- * than fp32 holds is divided by infinity.
+ * exactly.  A row that sees no key, or whose y is zero, is zeros.  With eps 0, rows
+ * below 1e-19 lose digits, as their squares do; a mean that underflows counts as 2^-149.
+ * Where a map's row is not finite (lr_fwd_window says when) the formulas hold as fp32
+ * arithmetic has them; a row whose squares sum to more than fp32 holds is divided by
+ * infinity.
  */
 #define LR_DIFF_NORM 0x1u /* the root-mean-square norm over the pair's 2 d channels */
 #define LR_DIFF_FILL 0x2u /* lr_step_paged_diff: rows of unused slots are written as zeros */

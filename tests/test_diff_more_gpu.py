@@ -179,3 +179,31 @@ def test_diff_step_beside_an_early_infinity(dev, max_len, d, dtype):
     within(torch.from_numpy(got), ref, 2 * bound)
     normed = lr.lr_step_paged_diff(*on, max_len=max_len)
     assert normed[0, :2].isnan().all() and normed[0, 3, 2].isnan() and (normed[0, 2] == 0).all()
+
+
+@types
+@widths
+@pytest.mark.parametrize("top", [-58, -66, -73, -75, -110])
+def test_diff_squares_below_the_range(dev, top, d, dtype):
+    """Rows of one tiny channel, eps 0: their norm as long as the mean square is there
+    (of 2^-140 it has nine bits), else times 2^74.5, and never an infinity."""
+    q, k, v, _ = inputs(1, 2, 1, 5, 9, d, dtype, seed=351)
+    v.zero_()
+    v[0, 1, :, 4] = 2.0 ** top
+    lam = torch.zeros(2, device=dev)
+    args = [t.to(dev) for t in (q, k, v)]
+    table = torch.zeros(1, 1, dtype=torch.int32, device=dev)
+    pool = [torch.zeros(1, 2, 16, d, dtype=dtype, device=dev) for _ in range(2)]
+    for p, t in zip(pool, args[1:]):
+        p[0, :, :9] = t[0]
+    rows = lr.lr_fwd_diff(*args, lam, eps=0.0)[0, :, -1]
+    step = lr.lr_step_paged_diff(args[0][:, :, -1].contiguous(), *pool, table,
+                                 torch.tensor([9], dtype=torch.int32, device=dev), lam, eps=0.0)[0]
+    # 2 d channels of which one is not zero: sqrt(2 d)
+    x = (2 * d) ** 0.5 if top >= -66 else 2.0 ** (top + 74.5)
+    # the weights are off by up to 2^-8 each in bf16, the result by as much; the mean by 2^-10
+    for o in (rows, step):
+        o = np64(o)
+        assert (np.abs(o[1::2, 4] - x) <= x * (3 * 2.0 ** -8 if dtype == BF16 else 2.0 ** -10)).all()
+        o[1::2, 4] = 0
+        assert (o == 0).all()
