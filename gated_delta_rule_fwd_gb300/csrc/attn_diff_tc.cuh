@@ -12,7 +12,6 @@
 namespace lr {
 
 constexpr int kDiffRows = 128, kDiffKeys = 128;
-constexpr int kDiffRest = 1;  // of a tile's four 32-key pieces, those with the rest of P's rounding
 
 struct DiffTcArgs {
     DiffArgs a;

@@ -141,15 +141,13 @@ __device__ __forceinline__ uint32_t pack2_rest(float2 x, uint32_t &rest) {
 // maximum m in use where a score passes it by 2^8 (rescaling the sum l and the
 // output's DV columns at `to`), replaces the 128 scores at `ts` by bf16 weights
 // over their first 64 columns, handing them over in halves (ready0, ready1, one
-// arrival a warp), and adds the weights to l.  For the first 32 REST keys, columns
-// 64 on take what the weights' rounding left, as bf16 weights of their own, which
-// ready1 covers.  A weight is 2^(c s - b) with
-// b = c m rounded, so all of a row refer to the same b.  keep(i): which of the
-// columns 32 i .. 32 i + 31 the row sees; not asked where `whole`.
+// arrival a warp), and adds the weights to l.  A weight is 2^(c s - b) with b = c m
+// rounded, so all of a row refer to the same b.  keep(i): which of the columns 32 i ..
+// 32 i + 31 the row sees; not asked where `whole`.
 //
 // A tile at the edge of what the rows see gets -inf over the scores that a row
 // does not see, in tensor memory, so that one code serves all tiles.
-template <int DV, int REST, typename Keep>
+template <int DV, typename Keep>
 __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, bool whole, const Keep &keep,
                                              float &m, float &l, uint64_t *ready0, uint64_t *ready1) {
     const float2 c2 = make_float2(c, c);
@@ -214,15 +212,8 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, 
             e.y = ex2(e.y);
             sum[i & 3] = add2(sum[i & 3], e);
             r[i] = pack2(e.x, e.y);
-            if (ch < REST) s[ch][2 * i] = e.x, s[ch][2 * i + 1] = e.y;
         }
         tmem_st16(ts + 16 * ch, r);
-        if (ch > 1 && ch - 2 < REST) {
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                pack2_rest(make_float2(s[ch - 2][2 * i], s[ch - 2][2 * i + 1]), r[i]);
-            tmem_st16(ts + 64 + 16 * (ch - 2), r);
-        }
         if (ch & 1) {
             tmem_st_wait();
             tc_fence_before();

@@ -13,16 +13,17 @@
 // the difference is formed there in fp32 and rounded once: at the end each of
 // the two softmax warpgroups reads half of the channels of both outputs.
 //
-// The difference takes away what the maps have in common, but not the rounding of
-// their weights to bf16: against weights of 32 bits the error was 1.53 times as
-// large (lr_fwd_window: 1.35).  So a quarter of the keys, the first 32 of a tile,
-// multiply what that rounding left as well (1.39; 8192 causal tokens of 8 pairs, d
-// = 64: 155 -> 173 us; with half of them 1.27 and 196 us, with all 1.0 and 267 us).
+// A weight is rounded to bf16 for its product with the values, as in window_tc.cu, every
+// key's alike; the difference takes away what the maps have in common, but not these
+// roundings: against weights of 32 bits the error is 1.53 times as large (lr_fwd_window:
+// 1.35).  With what the rounding left as products of their own it is 1.0, for 1.7 times
+// the time.  (For the first quarter of a tile's keys alone, 1.39 on average: the worst
+// row was no better, and a key's weight depended on its place in the tile.)
 //
-// Measured: those 8192 tokens 165 us, 1249 TFLOP/s of visible products.  What bounds it is
-// a map's chain: its softmax of a tile (1420 cycles), its last products, its next scores
-// (2500 cycles a tile of both maps, whose products need 1792); scores further ahead find
-// no room in tensor memory.
+// Measured: 8192 causal tokens of 8 pairs, d = 64: 154 us, 1339 TFLOP/s of visible
+// products.  What bounds it is a map's chain: its softmax of a tile (1420 cycles), its
+// last products, its next scores, which the tensor pipe takes behind them: some 2300
+// cycles a tile of both maps, whose products need 1536.
 //
 // Tensor memory holds 2 x 128 columns of scores and 2 x 128 of output, so d is 32
 // or 64 here (diff_wide_tc.cu: 128).
@@ -283,13 +284,12 @@ __global__ void __launch_bounds__(NT, 1)
                 if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bars->vfull[done % NV], (done / NV) & 1));
                 const uint64_t dv = tile_desc_mn(v_s + (done % NV) * L::VTILE, 128, 0);
                 const int steps = width(it) >> 4;
-                auto product = [&](uint32_t p, int ks, bool add) {
+                auto values = [&](int ks) {
 #pragma unroll
                     for (int j = 0; j < NO; ++j)
-                        mma_bf16_ta(o_t + j * (DV / NO), p + 8 * ks, mndesc_step(dv, ks) + j * (16384u >> 4), id_o, add);
+                        mma_bf16_ta(o_t + j * (DV / NO), s_t + 8 * ks, mndesc_step(dv, ks) + j * (16384u >> 4), id_o,
+                                    ks > 0 || it > 0);
                 };
-                auto values = [&](int ks) { product(s_t, ks, ks > 0 || it > 0); };
-                auto rests = [&](int ks) { product(s_t + 64, ks, true); };
                 // the last piece's outputs have left
                 if (ok && it == 0 && used > 0)
                     ok = __all_sync(0xffffffffu, wait_bar(&bars->oempty, (used - 1) & 1));
@@ -311,9 +311,6 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
                     for (int ks = 4; ks < BN / 16; ++ks)
                         if (ks < steps) values(ks);
-#pragma unroll
-                    for (int ks = 0; ks < 2 * kDiffRest; ++ks)
-                        if (ks < steps) rests(ks);
                     mma_commit(&bars->vempty[done % NV]);
                     if (it + 1 < n) scores(it + 1, done + 1);
                     else mma_commit(&bars->ofull[t]);
@@ -360,7 +357,7 @@ __global__ void __launch_bounds__(NT, 1)
                     const int kc = k0 + 32 * ch;
                     return low_bits(end - kc) & (~low_bits(rlo - kc) | low_bits(a.sinks - kc));
                 };
-                softmax_tile<DV, kDiffRest>(ts, to, g.c, whole, keep, m, l, &bars->pready[t][0], &bars->pready[t][1]);
+                softmax_tile<DV>(ts, to, g.c, whole, keep, m, l, &bars->pready[t][0], &bars->pready[t][1]);
                 ++seen;
             }
             // the rounding of the exponent's base took the weights' range

@@ -17,9 +17,8 @@
 // memory (over queries and keys, which are free from the last scores on), and the rows'
 // sums of squares.
 //
-// What the weights' rounding left is multiplied for a quarter of the keys as in
-// diff_tc.cu; a row's non-finite values, padding and the rounding of the exponent's
-// base are dealt with as in window_tc.cu.
+// Weights are rounded as in diff_tc.cu; a row's non-finite values, padding and the rounding
+// of the exponent's base are dealt with as in window_tc.cu.
 //
 // Roles of the 384 threads: warps 0-3 softmax of a tile's first 64 keys and the first
 // half of the CTA's channels, warps 4-7 of the others, warp 8 issues the value
@@ -352,9 +351,6 @@ __global__ void __launch_bounds__(NT, 1)
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
                         if (ks < steps) mma_bf16_ta(o, p + 8 * ks, mndesc_step(dv0, ks), id_o, ks > 0 || it > 0);
-#pragma unroll
-                    for (int ks = 0; ks < 2 * kDiffRest; ++ks)
-                        if (ks < steps) mma_bf16_ta(o, p + 32 + 8 * ks, mndesc_step(dv0, ks), id_o, 1);
                     mma_commit(&bars->vempty[slot0]);
                 }
                 __syncwarp();
@@ -481,19 +477,8 @@ __global__ void __launch_bounds__(NT, 1)
                         e.y = ex2(e.y);
                         sum[i & 3] = add2(sum[i & 3], e);
                         r[i] = pack2(e.x, e.y);
-                        if (ch < kDiffRest) s[ch][2 * i] = e.x, s[ch][2 * i + 1] = e.y;
                     }
                     tmem_st16(ts + 16 * ch, r);
-                }
-                // what the rounding of the tile's first keys left
-                if (t == 0) {
-#pragma unroll
-                    for (int ch = 0; ch < kDiffRest; ++ch) {
-                        uint32_t r[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) pack2_rest(make_float2(s[ch][2 * i], s[ch][2 * i + 1]), r[i]);
-                        tmem_st16(ts + 32 + 16 * ch, r);
-                    }
                 }
                 tmem_st_wait();
                 tc_fence_before();

@@ -207,3 +207,24 @@ def test_diff_squares_below_the_range(dev, top, d, dtype):
         assert (np.abs(o[1::2, 4] - x) <= x * (3 * 2.0 ** -8 if dtype == BF16 else 2.0 ** -10)).all()
         o[1::2, 4] = 0
         assert (o == 0).all()
+
+
+@widths
+def test_diff_weights_count_the_same_anywhere_in_a_tile(dev, d):
+    """A row on two keys, one in each of two tiles of 128: the same bits for every place
+    of either, and right."""
+    B, T = 128, 256
+    q, k = torch.zeros(B, 2, 1, d), torch.zeros(B, 2, T, d)
+    q[:, 0, :, 0], q[:, 1, :, 0] = 1.0, 1.25
+    k[..., 0] = -1000.0
+    v = rnd(361, 1, 2, 2, d, dtype=BF16)
+    values = rnd(362, B, 2, T, d, dtype=BF16)
+    for b in range(B):
+        first, second = b, 128 + (37 * b + 11) % 128
+        k[b, :, first, 0], k[b, :, second, 0] = 0.0, -1.203125
+        values[b, :, first], values[b, :, second] = v[0, :, 0], v[0, :, 1]
+    lam = torch.tensor([0.5])
+    o = lr.lr_fwd_diff(*(t.to(BF16).to(dev) for t in (q, k, values)), lam.to(dev), scale=1.0, norm=False)
+    ref, bound, _ = oa.diff(np64(q[:1]), np64(k[:1]), np64(values[:1]), np64(lam), NW, 0, 1.0, BITS[BF16], 8)
+    within(o, np.broadcast_to(ref, o.shape), np.broadcast_to(bound, o.shape))
+    assert torch.equal(o, o[:1].expand_as(o))
