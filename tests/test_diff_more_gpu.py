@@ -228,3 +228,34 @@ def test_diff_weights_count_the_same_anywhere_in_a_tile(dev, d):
     ref, bound, _ = oa.diff(np64(q[:1]), np64(k[:1]), np64(values[:1]), np64(lam), NW, 0, 1.0, BITS[BF16], 8)
     within(o, np.broadcast_to(ref, o.shape), np.broadcast_to(bound, o.shape))
     assert torch.equal(o, o[:1].expand_as(o))
+
+
+@types
+@widths
+def test_diff_equal_maps_cancel(dev, d, dtype):
+    """The same map twice and lambda 1, over several tiles and pieces: zeros, whatever eps."""
+    q, k, v, _ = inputs(2, 3, 1, 300, 700, d, dtype, seed=371)
+    q[:, 1::2], k[:, 1::2] = q[:, 0::2], k[:, 0::2]
+    one = torch.ones(3, device=dev)
+    for norm, eps, window in ((False, 0.0, None), (True, 0.0, 90), (True, EPS, None)):
+        o = lr.lr_fwd_diff(*(t.to(dev) for t in (q, k, v)), one, norm=norm, eps=eps, window=window, sinks=3)
+        assert (o == 0).all()
+
+
+@types
+@widths
+@pytest.mark.parametrize("scale", [1.0, -1.0])
+@pytest.mark.parametrize("top", [2.0 ** 33, 2.0 ** 66, 2.0 ** 126], ids=str)
+def test_diff_scores_far_above_the_others(dev, top, scale, d, dtype):
+    """Scores of 1e10 and more, one a 64th part above the others in each map, in the
+    first and in the last tile: each map gives its value alone."""
+    Tq, Tk = 30, 300
+    q, k, v, lam = inputs(1, 1, 1, Tq, Tk, d, dtype, seed=381)
+    q.zero_(), k.zero_()
+    q[..., 0] = scale
+    k[..., 0] = torch.tensor(top * (1 - 2.0 ** -6))
+    k[0, 0, 250, 0] = k[0, 1, 17, 0] = top
+    o = lr.lr_fwd_diff(*(t.to(dev) for t in (q, k, v)), lam.to(dev), scale=scale, norm=False)
+    row = torch.cat((v[0, 0], v[0, 1]), -1).double()
+    want = (row[250] - float(lam[0]) * row[17]).view(2, 1, d).expand(2, Tq, d)
+    within(o[0], np64(want), np.abs(np64(want)) * 2.0 ** -BITS[dtype] + 2.0 ** -22)
