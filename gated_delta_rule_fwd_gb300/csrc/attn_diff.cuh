@@ -19,13 +19,45 @@ __device__ __forceinline__ float diff_rms(float squares, int d, float eps) {
     return mean > 0.f ? rsqrtf(mean) : (mean == 0.f ? 0x1.6a09e6p74f : NAN);  // 2^74.5
 }
 
+// N channels of a row in a row: one load.
+template <int N>
+__device__ __forceinline__ void load_run(const __nv_bfloat16 *p, float (&x)[N]) {
+    if constexpr (N == 1) {
+        x[0] = __bfloat162float(*p);
+    } else {
+        uint32_t w[N / 2];
+        if constexpr (N == 2) w[0] = *reinterpret_cast<const uint32_t *>(p);
+        else {
+            const uint2 u = *reinterpret_cast<const uint2 *>(p);
+            w[0] = u.x, w[1] = u.y;
+        }
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+            const float2 y = unpack2(w[i]);
+            x[2 * i] = y.x, x[2 * i + 1] = y.y;
+        }
+    }
+}
+template <int N>
+__device__ __forceinline__ void load_run(const float *p, float (&x)[N]) {
+    if constexpr (N == 1) {
+        x[0] = *p;
+    } else if constexpr (N == 2) {
+        const float2 u = *reinterpret_cast<const float2 *>(p);
+        x[0] = u.x, x[1] = u.y;
+    } else {
+        const float4 u = *reinterpret_cast<const float4 *>(p);
+        x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+    }
+}
+
 // One map of a row that did not come out finite, by one warp, from what the row sees:
 // 32 keys at a time from the newest on, a lane a key for their scores, then all lanes
 // over the values, of which four keys are on their way at once.  A running mean, which no
 // large value can drive out of range; infinities and NaN are noted channel by channel and
 // stand for the channel in the end (attn_rows.cuh has the rules).  A score of NaN or +inf
-// makes the row NaN: false.  y[half][i]: channel half d + lane + 32 i, of the halves (bits)
-// that are asked for.
+// makes the row NaN: false.  y[half][i]: channel half d + lane d / 32 + i, of the halves
+// (bits) that are asked for.
 template <typename E, int D, typename Keys>
 __device__ __forceinline__ bool mend_map(const E *q, int map, const Keys &keys, SeenKeys s, ScoreFactor f,
                                          unsigned halves, float (&y)[2][D / 32]) {
@@ -78,7 +110,8 @@ __device__ __forceinline__ bool mend_map(const E *q, int map, const Keys &keys, 
                 for (int half = 0; half < 2; ++half) {
                     const bool read = (some >> (b + u) & 1u) && (halves >> half & 1u) && keys(map, half, j0 - b - u, kj, vj);
 #pragma unroll
-                    for (int i = 0; i < PL; ++i) v[u][half][i] = read ? to_f<E>(vj[lane + 32 * i]) : 0.f;
+                    for (int i = 0; i < PL; ++i) v[u][half][i] = 0.f;
+                    if (read) load_run<PL>(vj + lane * PL, v[u][half]);
                 }
 #pragma unroll
             for (int u = 0; u < U; ++u) {
@@ -113,7 +146,7 @@ __device__ __forceinline__ bool mend_map(const E *q, int map, const Keys &keys, 
 // A row whose difference is not finite, by one warp, from the definition.  q0, q1: the
 // maps' rows; keys(map, half, j, kj, vj): whether key j can be read, its row of k for the
 // map and of v for the half; halves: those of the value row (bits) that are wanted without
-// the norm.  y[half][i]: the row's channel half d + lane + 32 i.
+// the norm.  y[half][i]: the row's channel half d + lane d / 32 + i.
 template <typename E, int D, typename Keys>
 __device__ __forceinline__ void mend_diff(const E *q0, const E *q1, const Keys &keys, float lambda, bool norm,
                                           const float *weight, float eps, SeenKeys s, ScoreFactor f, unsigned halves,
@@ -145,7 +178,7 @@ __device__ __forceinline__ void mend_diff(const E *q0, const E *q1, const Keys &
     for (int half = 0; half < 2; ++half)
 #pragma unroll
         for (int i = 0; i < PL; ++i)
-            y[half][i] = y[half][i] * r * (weight ? weight[half * D + lane + 32 * i] : 1.f);
+            y[half][i] = y[half][i] * r * (weight ? weight[half * D + lane * PL + i] : 1.f);
 }
 
 }  // namespace lr

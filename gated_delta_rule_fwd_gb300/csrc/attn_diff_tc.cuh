@@ -91,16 +91,25 @@ __device__ __forceinline__ float marked_squares(const float (&y)[N], float squar
     return odd == 0.f ? INFINITY : NAN;
 }
 
-// Rows that the pieces of this CTA (or cluster), number `me` of `all`, left marked, by the
-// warp that wrote rows row0 .. row0 + 31 of each piece and channels c0 .. c0 + n - 1 of the
-// pair's 2 D.  It comes last, when no other warp waits for this one: a row takes two passes
-// over all its keys.
+// Rows that the pieces of this CTA (or cluster), number `me` of `all`, left marked, put
+// right by its eight softmax warps.  It comes last, when no other warp waits for these in
+// a loop that gives up: a row takes two passes over its keys.  Warp w of warpgroup t wrote
+// rows 32 w .. 32 w + 31 of each piece, channels c0 + t n .. of n; here the warpgroups take
+// every other of these rows, with both their channels.  marked: the warp left such a row.
 template <int D>
-__device__ __forceinline__ void mend_marked(const DiffTcArgs &g, int me, int all, int row0, int c0, int n) {
+__device__ __forceinline__ void mend_marked(const DiffTcArgs &g, bool marked, int me, int all, int c0, int n) {
     using E = __nv_bfloat16;
+    constexpr int PL = D / 32;
     const DiffArgs &a = g.a;
-    const int lane = threadIdx.x & 31, own = c0 / D;
-    __syncwarp();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row0 = 32 * (warp & 3);
+    uint32_t some;  // of all eight, which are through with their pieces
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 256, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(some)
+        : "r"((uint32_t)marked)
+        : "memory");
+    if (!some) return;
 #pragma unroll 1
     for (int i = 0;; ++i) {
         const long long block = (long long)i * all + (i & 1 ? all - 1 - me : me);
@@ -109,17 +118,27 @@ __device__ __forceinline__ void mend_marked(const DiffTcArgs &g, int me, int all
         DiffItem x;
         make_diff_item(g, (int)block, x, &bad);
         E *o = static_cast<E *>(a.o) + x.b * a.os.b + 2 * x.h * a.os.h + (long long)(x.i0 + row0) * a.os.t;
-        float mark = 0.f;
-        if (row0 + lane < x.rows) mark = to_f<E>(o[own * a.os.h + lane * a.os.t + c0 - own * D]);
-        unsigned again = __ballot_sync(0xffffffffu, mark != mark);
-        while (again) {
-            const int row = __ffs(again) - 1;
-            again &= again - 1;
+        // a mark for either warpgroup's channels
+        bool odd[2] = {false, false};
+        if (row0 + lane < x.rows && (lane & 1) == warp >> 2)
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int ch = c0 + t * n;
+                const float mark = to_f<E>(o[ch / D * a.os.h + lane * a.os.t + ch % D]);
+                odd[t] = mark != mark;
+            }
+        const unsigned again[2] = {__ballot_sync(0xffffffffu, odd[0]), __ballot_sync(0xffffffffu, odd[1])};
+        unsigned rows = again[0] | again[1];
+#pragma unroll 1
+        while (rows) {
+            const int row = __ffs(rows) - 1;
+            rows &= rows - 1;
+            const bool put[2] = {(again[0] >> row & 1u) != 0, (again[1] >> row & 1u) != 0};
             const E *q = static_cast<const E *>(a.q) + x.b * a.qs.b + 2 * x.h * a.qs.h +
                          (long long)(x.i0 + row0 + row) * a.qs.t;
             const E *k = static_cast<const E *>(a.k) + x.b * a.ks.b + 2 * x.hk * a.ks.h;
             const E *v = static_cast<const E *>(a.v) + x.b * a.vs.b + 2 * x.hk * a.vs.h;
-            float y[2][D / 32];
+            float y[2][PL];
             mend_diff<E, D>(
                 q, q + a.qs.h,
                 [&](int map, int half, int j, const E *&kj, const E *&vj) {
@@ -127,13 +146,13 @@ __device__ __forceinline__ void mend_marked(const DiffTcArgs &g, int me, int all
                     return true;
                 },
                 a.lambda[x.h], a.norm, a.weight, a.eps, seen_keys(x.p0 + row0 + row, x.kl, a.window, a.sinks),
-                score_factor(a.scale), 1u << own, y);
+                score_factor(a.scale), (put[0] ? 1u << c0 / D : 0u) | (put[1] ? 1u << (c0 + n) / D : 0u), y);
 #pragma unroll
             for (int half = 0; half < 2; ++half)
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    const int ch = half * D + lane + 32 * c;
-                    if (ch >= c0 && ch < c0 + n) o[half * a.os.h + row * a.os.t + lane + 32 * c] = from_f<E>(y[half][c]);
+                for (int c = 0; c < PL; ++c) {
+                    const int in = lane * PL + c, ch = half * D + in - c0;  // of the CTA's 2 n
+                    if (ch >= 0 && ch < 2 * n && put[ch >= n]) o[half * a.os.h + row * a.os.t + in] = from_f<E>(y[half][c]);
                 }
         }
     }

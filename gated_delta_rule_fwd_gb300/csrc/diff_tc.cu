@@ -438,8 +438,7 @@ __global__ void __launch_bounds__(NT, 1)
             }
             give_back();
         }
-        if (ok && __any_sync(0xffffffffu, marked))
-            mend_marked<D>(g, blockIdx.x, gridDim.x, 32 * (warp & 3), col, CH);
+        mend_marked<D>(g, __any_sync(0xffffffffu, ok && marked), blockIdx.x, gridDim.x, 0, CH);
     }
 
     if (!ok) atomicOr(&g_diff_error, kAttnTimeout);

@@ -598,8 +598,7 @@ __global__ void __launch_bounds__(NT, 1)
             }
             give_back();
         }
-        if (ok && __any_sync(0xffffffffu, marked))
-            mend_marked<D>(g, blockIdx.x / 2, gridDim.x / 2, 32 * (warp & 3), 128 * rank + 64 * t, 64);
+        mend_marked<D>(g, __any_sync(0xffffffffu, ok && marked), blockIdx.x / 2, gridDim.x / 2, 128 * rank, 64);
     }
 
     if (!ok) atomicOr(&g_diff_wide_error, kAttnTimeout);

@@ -113,11 +113,11 @@ __device__ __forceinline__ void finish_pair(const DiffStep &s, int n, int h, int
     squares = warp_sum(squares);
     bool odd = false;
     const float r = s.norm ? diff_rms(squares, D, s.eps) : 1.f;
-    E *o = static_cast<E *>(a.o) + ((size_t)n * a.Hq + h) * 2 * D + lane;
+    E *o = static_cast<E *>(a.o) + ((size_t)n * a.Hq + h) * 2 * D;
 #pragma unroll
     for (int c = 0; c < N; ++c) {
         odd = odd || !isfinite(y[c]);
-        o[32 * c] = from_f<E>(y[c] * r * (s.norm && s.weight ? s.weight[lane + 32 * c] : 1.f));
+        o[lane + 32 * c] = from_f<E>(y[c] * r * (s.norm && s.weight ? s.weight[lane + 32 * c] : 1.f));
     }
     if (!__any_sync(0xffffffffu, odd)) return;
     // not finite: from the definition; keys of pages outside the pool are left out
@@ -139,7 +139,7 @@ __device__ __forceinline__ void finish_pair(const DiffStep &s, int n, int h, int
 #pragma unroll
     for (int half = 0; half < 2; ++half)
 #pragma unroll
-        for (int i = 0; i < D / 32; ++i) o[half * D + 32 * i] = from_f<E>(z[half][i]);
+        for (int i = 0; i < D / 32; ++i) o[half * D + lane * (D / 32) + i] = from_f<E>(z[half][i]);
 }
 
 // The end of a CTA: its warps' parts of each map, streams of them, are joined
