@@ -218,10 +218,11 @@ __device__ __forceinline__ void finish(float (&so)[NT / 32 + PRE][HEADS][P], flo
 
 // With one head the compiler is told how many CTAs an SM to leave registers for: four,
 // which the plan counts on (33 sequences with window 1024, 8 heads: 21.8 us, 24.9 with
-// five), and five behind a prefix, whose kernel's last CTAs they stand beside (33 behind
-// 1501: 20.6 us, 31.7 with four).
+// five).  Behind a prefix (us with four, with five; d = 128 but for the last): 64 sequences
+// of 100 to 1024 behind 4096 94, 103; 33 of up to 512 behind 1501, window 1024, 32, 35; 48
+// of up to 2048 behind 1024 87, 94; 16 of up to 4096 on 16 heads, d = 64, 57, 54.
 template <int D, int GC, bool PRE>
-__global__ void __launch_bounds__(NT, GC == 1 ? (PRE ? 5 : 4) : 0) step_simt_kernel(StepArgs a, Parts parts, ScoreFactor f) {
+__global__ void __launch_bounds__(NT, GC == 1 ? 4 : 0) step_simt_kernel(StepArgs a, Parts parts, ScoreFactor f) {
     constexpr int LANES = D / 8;            // lanes of a key
     constexpr int GROUPS = NT / LANES;      // keys in flight
     constexpr int U = 4;                    // keys of a group per pass
