@@ -358,23 +358,21 @@ __global__ void __launch_bounds__(NT, GC == 1 ? 4 : 0) step_simt_kernel(StepArgs
 
 // The sequence at place `place` when the longest comes first: its rank counted by the
 // thread that holds it.  room: kSorted ints and one of shared memory.
-constexpr int kSorted = 2 * NT;
+constexpr int kSorted = NT;
 __device__ __forceinline__ int by_length(const int *lens, int N, int place, int *room) {
-    for (int i = threadIdx.x; i < kSorted; i += NT) room[i] = i < N ? lens[i] : INT_MIN;
+    const int i = threadIdx.x, mine = i < N ? lens[i] : INT_MIN;
+    room[i] = mine;
     __syncthreads();
-    for (int i = threadIdx.x; i < N; i += NT) {
-        const int mine = room[i];
-        int rank = 0;
+    int rank = 0;
 #pragma unroll 8
-        for (int j = 0; j < (N + 3) / 4; ++j) {
-            const int4 x = reinterpret_cast<const int4 *>(room)[j];
-            rank += x.x > mine || (x.x == mine && 4 * j < i);
-            rank += x.y > mine || (x.y == mine && 4 * j + 1 < i);
-            rank += x.z > mine || (x.z == mine && 4 * j + 2 < i);
-            rank += x.w > mine || (x.w == mine && 4 * j + 3 < i);
-        }
-        if (rank == place) room[kSorted] = i;
+    for (int j = 0; j < (N + 3) / 4; ++j) {
+        const int4 x = reinterpret_cast<const int4 *>(room)[j];
+        rank += x.x > mine || (x.x == mine && 4 * j < i);
+        rank += x.y > mine || (x.y == mine && 4 * j + 1 < i);
+        rank += x.z > mine || (x.z == mine && 4 * j + 2 < i);
+        rank += x.w > mine || (x.w == mine && 4 * j + 3 < i);
     }
+    if (i < N && rank == place) room[kSorted] = i;
     __syncthreads();
     const int n = room[kSorted];
     __syncthreads();  // the room is used again
@@ -383,8 +381,10 @@ __device__ __forceinline__ int by_length(const int *lens, int N, int place, int 
 
 // NH: 8-head column blocks of the products.
 // PRE: behind a shared prefix.  Own tokens are short lists, so a CTA's start and its
-// longest sequence count: four CTAs to an SM and the longest first (128 sequences of 100
-// to 1024, 8 key heads: 57 -> 50 us; either alone changed nothing).
+// longest sequence count: four CTAs to an SM (us with and without that bound, 32 heads on
+// 8: 128 sequences of 100 to 1024 88, 94, of 900 to 1024 100, 107; 256 of up to 512 71, 74;
+// 128 of up to 8192 on 2 key heads 94, 103; but 64 of 100 to 1024 57, 53, and 32 43, 37)
+// and the longest first (launch_step_prefix).
 template <int D, int NH, bool PRE>
 __global__ void __launch_bounds__(NT, PRE && NH == 1 ? 4 : 1)
     step_mma_kernel(StepArgs a, Parts parts, ScoreFactor f) {
@@ -787,7 +787,10 @@ size_t prefix_workspace_bytes(int N, int Hq, int d, const PrefixPlan &p) {
 cudaError_t launch_step_prefix(StepArgs a, int d, lr_dtype dt, void *ws, cudaStream_t stream) {
     const PrefixPlan p = prefix_plan(a.N, a.Hq, a.Hk, d, a.plen, a.window, a.all_sinks, dt);
     a.pre = p.parts;
-    // more CTAs than run at once; beyond kSorted sequences the last ones hardly count
+    // Where more CTAs than run at once, and every thread of a CTA ranks one length (us with
+    // and without, 32 heads on 8: 128 of 100 to 1024 88, 96; 96 of up to 512 33, 37; 112 of
+    // 100 to 1024 65, 72; 128 of up to 4096 202, 196; two lengths a thread: 192 of 100 to
+    // 1024 103, 97; 256 of up to 512 89, 70).
     const int G = a.Hq / a.Hk, heads = heads_of_cta(G, dt);
     a.longest_first = dt == LR_DT_BF16 && a.N <= kSorted && (long long)a.N * a.Hk * ((G + heads - 1) / heads) > 4 * 152;
     if (p.parts) {
