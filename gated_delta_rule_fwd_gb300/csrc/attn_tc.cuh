@@ -141,13 +141,14 @@ __device__ __forceinline__ uint32_t pack2_rest(float2 x, uint32_t &rest) {
 // maximum m in use where a score passes it by 2^8 (rescaling the sum l and the
 // output's DV columns at `to`), replaces the 128 scores at `ts` by bf16 weights
 // over their first 64 columns, handing them over in halves (ready0, ready1, one
-// arrival a warp), and adds the weights to l.  A weight is 2^(c s - b) with b = c m
-// rounded, so all of a row refer to the same b.  keep(i): which of the columns 32 i ..
-// 32 i + 31 the row sees; not asked where `whole`.
+// arrival a warp), and adds the weights to l.  REST: the other 64 columns take what the
+// weights' rounding left, as bf16 weights of their own, handed over with their halves.  A
+// weight is 2^(c s - b) with b = c m rounded, so all of a row refer to the same b.
+// keep(i): which of the columns 32 i .. 32 i + 31 the row sees; not asked where `whole`.
 //
 // A tile at the edge of what the rows see gets -inf over the scores that a row
 // does not see, in tensor memory, so that one code serves all tiles.
-template <int DV, typename Keep>
+template <int DV, bool REST, typename Keep>
 __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, bool whole, const Keep &keep,
                                              float &m, float &l, uint64_t *ready0, uint64_t *ready1) {
     const float2 c2 = make_float2(c, c);
@@ -204,16 +205,17 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, float c, 
     for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.f, 0.f);
 #pragma unroll
     for (int ch = 0; ch < 4; ++ch) {
-        uint32_t r[16];
+        uint32_t r[16], rest[16];
 #pragma unroll
         for (int i = 0; i < 16; ++i) {
             float2 e = fma2(make_float2(s[ch][2 * i], s[ch][2 * i + 1]), c2, b2);
             e.x = ex2(e.x);
             e.y = ex2(e.y);
             sum[i & 3] = add2(sum[i & 3], e);
-            r[i] = pack2(e.x, e.y);
+            r[i] = REST ? pack2_rest(e, rest[i]) : pack2(e.x, e.y);
         }
         tmem_st16(ts + 16 * ch, r);
+        if (REST) tmem_st16(ts + 64 + 16 * ch, rest);
         if (ch & 1) {
             tmem_st_wait();
             tc_fence_before();

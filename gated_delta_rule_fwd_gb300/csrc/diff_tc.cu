@@ -13,17 +13,17 @@
 // the difference is formed there in fp32 and rounded once: at the end each of
 // the two softmax warpgroups reads half of the channels of both outputs.
 //
-// A weight is rounded to bf16 for its product with the values, as in window_tc.cu, every
-// key's alike; the difference takes away what the maps have in common, but not these
-// roundings: against weights of 32 bits the error is 1.53 times as large (lr_fwd_window:
-// 1.35).  With what the rounding left as products of their own it is 1.0, for 1.7 times
-// the time.  (For the first quarter of a tile's keys alone, 1.39 on average: the worst
-// row was no better, and a key's weight depended on its place in the tile.)
+// The difference takes away what the maps have in common, but not the rounding of their
+// weights to bf16, so what that rounding left is multiplied as well, as bf16 weights of its
+// own in the other half of the score tile: a weight counts with 16 bits, and the error of
+// a result is that of 32-bit weights (without the rest 1.53 times that; lr_fwd_window:
+// 1.35).  It costs twice the value products: 8192 causal tokens of 8 pairs, d = 64, 156 us
+// without, 206 with it; d = 32 148 and 208.
 //
-// Measured: 8192 causal tokens of 8 pairs, d = 64: 154 us, 1339 TFLOP/s of visible
-// products.  What bounds it is a map's chain: its softmax of a tile (1420 cycles), its
-// last products, its next scores, which the tensor pipe takes behind them: some 2300
-// cycles a tile of both maps, whose products need 1536.
+// Measured: those 206 us are 1000 TFLOP/s of visible products, 1670 of those formed.  What
+// bounds it is a map's chain, softmax of a tile, its last products, its next scores, which
+// the tensor pipe takes behind them: some 3000 cycles a tile of both maps, whose products
+// need 2560 (1536 at d = 32).
 //
 // Tensor memory holds 2 x 128 columns of scores and 2 x 128 of output, so d is 32
 // or 64 here (diff_wide_tc.cu: 128).
@@ -284,11 +284,14 @@ __global__ void __launch_bounds__(NT, 1)
                 if (ok) ok = __all_sync(0xffffffffu, wait_bar(&bars->vfull[done % NV], (done / NV) & 1));
                 const uint64_t dv = tile_desc_mn(v_s + (done % NV) * L::VTILE, 128, 0);
                 const int steps = width(it) >> 4;
+                // 16 keys: their weights, and what the weights' rounding left
                 auto values = [&](int ks) {
 #pragma unroll
-                    for (int j = 0; j < NO; ++j)
-                        mma_bf16_ta(o_t + j * (DV / NO), s_t + 8 * ks, mndesc_step(dv, ks) + j * (16384u >> 4), id_o,
-                                    ks > 0 || it > 0);
+                    for (int rest = 0; rest < 2; ++rest)
+#pragma unroll
+                        for (int j = 0; j < NO; ++j)
+                            mma_bf16_ta(o_t + j * (DV / NO), s_t + 64 * rest + 8 * ks,
+                                        mndesc_step(dv, ks) + j * (16384u >> 4), id_o, rest || ks > 0 || it > 0);
                 };
                 // the last piece's outputs have left
                 if (ok && it == 0 && used > 0)
@@ -357,7 +360,7 @@ __global__ void __launch_bounds__(NT, 1)
                     const int kc = k0 + 32 * ch;
                     return low_bits(end - kc) & (~low_bits(rlo - kc) | low_bits(a.sinks - kc));
                 };
-                softmax_tile<DV>(ts, to, g.c, whole, keep, m, l, &bars->pready[t][0], &bars->pready[t][1]);
+                softmax_tile<DV, true>(ts, to, g.c, whole, keep, m, l, &bars->pready[t][0], &bars->pready[t][1]);
                 ++seen;
             }
             // the rounding of the exponent's base took the weights' range

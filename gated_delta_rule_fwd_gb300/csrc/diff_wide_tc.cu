@@ -8,17 +8,18 @@
 //
 // Scores are formed once, a buffer ahead: their products, the softmax of the other
 // buffer and the value products run at the same time.  The pipe gets them in the order
-// P V of tile i, S of tile i + 2, P V of tile i + 1: a softmax takes as long as the
-// products of a tile, so scores that wait behind the next value products hold up all
-// (185 -> 200 us).  Each CTA loads the values for itself.  Two softmax threads share a
-// row, 64 keys each; they exchange the tile's maximum, so that both raise the one in use
-// together.  At the end a CTA takes over the rows' 128 channels of its half: the CTAs
-// send each other the other half of their output, scaled, through distributed shared
-// memory (over queries and keys, which are free from the last scores on), and the rows'
-// sums of squares.
+// P V of tile i, S of tile i + 2, P V of tile i + 1: scores that wait behind the next value
+// products hold up their softmax (an earlier version: 200 instead of 181 us).  Scores of
+// tile i + 2 overwrite the weights of tile i and wait until the products that read these
+// are done.  Each CTA loads the values for itself.  Two softmax threads share a row, 64
+// keys each; they exchange the tile's maximum, so that both raise the one in use together.
+// At the end a CTA takes over the rows' 128 channels of its half: the CTAs send each other
+// the other half of their output, scaled, through distributed shared memory (over queries
+// and keys, which are free from the last scores on), and the rows' sums of squares.
 //
-// Weights are rounded as in diff_tc.cu; a row's non-finite values, padding and the rounding
-// of the exponent's base are dealt with as in window_tc.cu.
+// Weights count with 16 bits as in diff_tc.cu (2 x 4096 causal tokens of 8 pairs: 171 us
+// without their rest, 218 with it); a row's non-finite values, padding and the rounding of
+// the exponent's base are dealt with as in window_tc.cu.
 //
 // Roles of the 384 threads: warps 0-3 softmax of a tile's first 64 keys and the first
 // half of the CTA's channels, warps 4-7 of the others, warp 8 issues the value
@@ -29,11 +30,10 @@
 // a tile by the whole warp took longer than the tile's products), hence one lane in
 // short loops, few barriers, whole boxes.  Every wait is bounded (lr_device_status).
 //
-// Measured: 2 x 4096 causal tokens of 8 pairs: 172 us, 1194 TFLOP/s of visible products
-// (16384 tokens: 1621).
-// A tile takes some 2000 cycles where its products need 1792; a piece costs 9000 to
-// 10000 more: its last products, the exchange (64 KB each way at some 32 bytes a
-// cycle), two rounds between the CTAs and the stores.
+// Measured: those 218 us are 945 TFLOP/s of visible products, 1575 of those formed (16384
+// tokens of 8 pairs: 1154 and 1923, all that the pipe gives).  Beside its tiles a piece
+// costs the wait for its last products, the exchange (64 KB each way at some 32 bytes a
+// cycle), two rounds between the CTAs and the stores: the share of that falls with length.
 #include <algorithm>
 
 #include "attn_diff_tc.cuh"
@@ -331,6 +331,11 @@ __global__ void __launch_bounds__(NT, 1)
         constexpr uint32_t id_o = idesc_bf16_f32_mn(BM, DV, false, true);
         const uint64_t dv = tile_desc_mn(smem_u32(sm + SM_V), 64, 0);
         const uint32_t o = tmem + kO;
+        // 16 keys: their weights, and what the weights' rounding left
+        auto values = [&](uint32_t p, uint64_t v, bool add) {
+            mma_bf16_ta(o, p, v, id_o, add);
+            mma_bf16_ta(o, p + 32, v, id_o, 1);
+        };
         int done = 0, used = 0;  // tiles and pieces multiplied
         while (const DiffItem *px = take()) {
             const DiffItem &x = *px;
@@ -350,7 +355,7 @@ __global__ void __launch_bounds__(NT, 1)
                 if (lead) {
 #pragma unroll
                     for (int ks = 0; ks < 4; ++ks)
-                        if (ks < steps) mma_bf16_ta(o, p + 8 * ks, mndesc_step(dv0, ks), id_o, ks > 0 || it > 0);
+                        if (ks < steps) values(p + 8 * ks, mndesc_step(dv0, ks), ks > 0 || it > 0);
                     mma_commit(&bars->vempty[slot0]);
                 }
                 __syncwarp();
@@ -360,7 +365,7 @@ __global__ void __launch_bounds__(NT, 1)
                 if (lead) {
 #pragma unroll
                     for (int ks = 4; ks < 8; ++ks)
-                        if (ks < steps) mma_bf16_ta(o, p + 64 + 8 * (ks - 4), mndesc_step(dv1, ks - 4), id_o, 1);
+                        if (ks < steps) values(p + 64 + 8 * (ks - 4), mndesc_step(dv1, ks - 4), true);
                     mma_commit(&bars->vempty[slot1]);
                     mma_commit(&bars->vdone[u]);
                     if (it == n - 1) mma_commit(&bars->ofull);
@@ -469,16 +474,17 @@ __global__ void __launch_bounds__(NT, 1)
                 for (int i = 0; i < 4; ++i) sum[i] = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int ch = 0; ch < 2; ++ch) {
-                    uint32_t r[16];
+                    uint32_t r[16], rest[16];
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         float2 e = fma2(make_float2(s[ch][2 * i], s[ch][2 * i + 1]), c2, b2);
                         e.x = ex2(e.x);
                         e.y = ex2(e.y);
                         sum[i & 3] = add2(sum[i & 3], e);
-                        r[i] = pack2(e.x, e.y);
+                        r[i] = pack2_rest(e, rest[i]);
                     }
                     tmem_st16(ts + 16 * ch, r);
+                    tmem_st16(ts + 32 + 16 * ch, rest);
                 }
                 tmem_st_wait();
                 tc_fence_before();

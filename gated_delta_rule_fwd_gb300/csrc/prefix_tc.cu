@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(NT, 1)
                     }
                 return see;
             };
-            softmax_tile<D>(ts, to, g.c, whole, keep, m, l, &bars->pready[t][0], &bars->pready[t][1]);
+            softmax_tile<D, false>(ts, to, g.c, whole, keep, m, l, &bars->pready[t][0], &bars->pready[t][1]);
         }
         // every product of both tiles has read its operands: their place is free
         for (int u = 0; u < active; ++u)

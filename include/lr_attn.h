@@ -186,11 +186,10 @@ lr_status lr_fwd_window(const void *q, lr_strides qs, const void *k, lr_strides 
  *
  * over the keys that row i sees, as for lr_fwd_window (window, sinks, lengths,
  * strides and what a masked row may hold are as there).  The difference, its
- * mean square and its norm are formed in fp32.  Of the weights' rounding to bf16
- * (see above) the difference keeps both maps' part: against 32-bit weights the
- * error of a result is 1.5 times as large.  lr_step_paged_diff, which waits for
- * the cache and not for its products, multiplies what that rounding left as well,
- * for every key, and has the error of 32-bit weights.  Equal maps cancel exactly.
+ * mean square and its norm are formed in fp32.  The difference takes away what the
+ * maps have in common, but not the rounding of their weights to bf16 (see above), so
+ * lr_fwd_diff and lr_step_paged_diff multiply what that rounding left as well: weights
+ * of 16 bits, and the error of 32-bit ones.  Equal maps cancel exactly.
  * A row that sees no key, or whose y is zero, is zeros.  With eps 0, rows below
  * 1e-19 lose digits, as their squares do; a mean that underflows counts as 2^-149.
  * Where a map's row is not finite (lr_fwd_window says when) the formulas hold as

@@ -259,3 +259,30 @@ def test_diff_scores_far_above_the_others(dev, top, scale, d, dtype):
     row = torch.cat((v[0, 0], v[0, 1]), -1).double()
     want = (row[250] - float(lam[0]) * row[17]).view(2, 1, d).expand(2, Tq, d)
     within(o[0], np64(want), np.abs(np64(want)) * 2.0 ** -BITS[dtype] + 2.0 ** -22)
+
+
+@types
+@widths
+def test_diff_weights_keep_sixteen_bits(dev, d, dtype):
+    """Maps that differ little and lambda 1, rows on few keys: what is left of the values
+    is small beside the weights' rounding to 8 bits, so only wider ones come within the bound."""
+    T = 150
+    q, k, v, _ = inputs(1, 2, 2, T, T, d, dtype, seed=391)
+    q[:, 1::2] = q[:, 0::2]
+    k[:, 1::2] = (k[:, 0::2].float() + 0.02 * rnd(392, 1, 2, T, d)).to(dtype)
+    lam = torch.ones(2)
+    ref, bound, _ = oa.diff(np64(q), np64(k), np64(v), np64(lam), 40, 2, d ** -0.5, BITS[dtype],
+                            16 if dtype == BF16 else None)
+    o = lr.lr_fwd_diff(*(t.to(dev) for t in (q, k, v, lam)), window=40, sinks=2, norm=False)
+    within(o, ref, bound)
+    # the step of the last token, its cache in pages of 16
+    pages = -(-T // 16)
+    pool = [torch.zeros(pages * 16, 4, d, dtype=dtype, device=dev) for _ in range(2)]
+    for p, t in zip(pool, (k, v)):
+        p[:T] = t[0].transpose(0, 1)
+    pool = [p.view(pages, 16, 4, d).transpose(1, 2).contiguous() for p in pool]
+    o = lr.lr_step_paged_diff(q[:, :, -1].contiguous().to(dev), *pool,
+                              torch.arange(pages, dtype=torch.int32, device=dev)[None],
+                              torch.tensor([T], dtype=torch.int32, device=dev), lam.to(dev), window=40, sinks=2,
+                              norm=False)
+    within(o, ref[:, :, -1], bound[:, :, -1])
