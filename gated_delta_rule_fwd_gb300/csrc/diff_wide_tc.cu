@@ -296,8 +296,8 @@ __global__ void __launch_bounds__(NT, 1)
                 const uint32_t id = idesc_bf16_f32(BM, x.width(it)) | g.negate;
                 const int slot1 = slot == NK - 1 ? 0 : slot + 1;
                 ok = wait(&bars->kfull[u], done >> 1);
-                // the products that read the buffer's weights are done: products of another
-                // shape and accumulator have no order among each other but by completion
+                // the products that read the buffer's weights are done: another warp issued
+                // them, and nothing but their completion orders them with these
                 if (ok && done >= 2) ok = wait(&bars->vdone[u], (done >> 1) - 1);
                 if (!ok) break;
                 tc_fence_after();
