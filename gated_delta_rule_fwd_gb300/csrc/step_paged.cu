@@ -22,7 +22,7 @@
 //
 // fp32 (step_simt_kernel): CUDA cores.  Every group of d / 8 lanes takes keys
 // of its own, with a running maximum and sum of its own (33 sequences with
-// window 1024, 139 MB: 24.2 us).  With up to two heads on a key head it reads
+// window 1024, 139 MB: 22.3 us).  With up to two heads on a key head it reads
 // the cache at the copy rate; more heads cost instructions, and more than four
 // are parts that read the cache again (32 sequences of 4096, 4 key heads, d =
 // 128, 537 MB: 81 us with 1 head on each, 84 with 2, 147 with 4, 205 with 8, 324
@@ -217,7 +217,7 @@ __device__ __forceinline__ void finish(float (&so)[NT / 32 + PRE][HEADS][P], flo
 }
 
 // With one head the compiler is told how many CTAs an SM to leave registers for: four,
-// which the plan counts on (33 sequences with window 1024, 8 heads: 21.8 us, 24.9 with
+// which the plan counts on (33 sequences with window 1024, 8 heads: 22.3 us, 24.9 with
 // five).  Behind a prefix (us with four, with five; d = 128 but for the last): 64 sequences
 // of 100 to 1024 behind 4096 94, 103; 33 of up to 512 behind 1501, window 1024, 32, 35; 48
 // of up to 2048 behind 1024 87, 94; 16 of up to 4096 on 16 heads, d = 64, 57, 54.
@@ -750,8 +750,8 @@ StepPlan step_plan(int N, int Hq, int Hk, int d, int max_len, int window, int si
     // CTAs that run at once: an SM holds the registers of three of the bf16
     // kernel at d = 128 (two with more than 8 heads; more at smaller widths,
     // where one wave matters less), of three in fp32 with four heads, else of
-    // four or five (33 sequences with window 1024: 26 us with 4, 39 with 3, 33
-    // with 6).
+    // four or five (33 sequences with window 1024, an earlier kernel: 26 us with 4,
+    // 39 with 3, 33 with 6).
     const int G = Hq / Hk, heads = heads_of_cta(G, dt);
     const int per_sm = dt == LR_DT_BF16 ? (heads == 8 ? 3 : 2) : (heads == 4 ? 3 : 4);
     const int *room = kClusterRoom[(dt == LR_DT_BF16 && d < 128 ? 4 : per_sm) - 1];
